@@ -1,0 +1,756 @@
+// pn_attn.cu -- attention of a step's queries over the 4-bit cache.
+//
+// For each query row (token, head): x_t = scale * q . k_t over the visible
+// cached tokens t, out = sum_t exp(x_t) v_t / sum_t exp(x_t), lse = ln sum_t
+// exp(x_t), with k_t, v_t the cache's exact values d (n - 8).
+//
+// One pass over the cache.  A row of K is multiplied as the whole numbers
+// n - 8 (exact in fp16) and each group's fp32 sum by its scale afterwards; the
+// scales of V go into the probabilities, so V's codes are whole numbers in
+// their product too.  The products run on mma.sync with the cache as the A
+// operand: S^T = K Q^T (16 tokens x 8 query rows), O^T += V^T P^T (16 values x
+// 8 query rows).  The 8 columns are the query heads that share the key/value
+// head and the step's tokens, so a decode step wastes few of them, and the
+// words of a record are stored in the order in which the fragments take them
+// (pn_kv.cuh): a code costs one LOP3 + one HFMA2 per pair and nothing else.
+//
+// Probabilities are rounded to fp16 once, after the scale of V is multiplied
+// in: p d with p = 2^(x' - m), x' = x log2 e.  The reference m of a row is the
+// running maximum of x' + log2 |d| (d the token's largest V scale) less 14, so
+// p |d| stays below 2^15 whatever the scales are and keeps its 11 bits down to
+// 2^-28 of the largest.  Sums, maxima and outputs are held in fp32.
+//
+// Work split: the units (request, key/value head, row group, 64-token tile)
+// of a call are numbered in that order and every thread block takes one
+// contiguous range of them, so the cache bytes are shared evenly whatever the
+// lengths are.  A producer warp streams the tiles through a ring of bulk
+// copies; each consumer warp takes every W-th tile with accumulators of its
+// own; warps are joined through shared memory at the end of a segment
+// (request, head, row group), and segments that cross block boundaries
+// through the workspace, by the last block to arrive, in block order: results
+// do not depend on timing.
+#include <cstdint>
+
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "pn_device.cuh"
+#include "pn_internal.h"
+#include "pn_kv.cuh"
+
+namespace pn {
+namespace {
+
+constexpr int kTile = 64;                      // tokens per unit
+constexpr int kTileRecords = kTile / kKvTokens;
+constexpr int kWarps = 7;                      // consumer warps; with the producer 8, so two blocks leave each thread 128 registers
+constexpr int kThreads = (kWarps + 1) * 32;
+constexpr int kMinUnits = 2;                   // fewest units per thread block
+constexpr int kSlotFloats = 2048 + 32;         // a partial result: rows x D values (2048 at most), then (reference, sum) per row
+constexpr int kCtasPerSm = 2;
+constexpr int kJoinPitch = 72;                 // floats per row of the join buffer: conflict-free for the fragments' stores
+constexpr uint32_t kStatusTimeout = 5;         // PN_ETIMEOUT
+constexpr uint64_t kDrainLimitNs = 200ull * 1000 * 1000;
+
+struct AttnParams {
+    AttnArgs a;
+    KvCache cache;
+    int group;                 // query heads per key/value head
+    float scale_log2;          // scale * log2 e
+    uint32_t* status;
+    uint32_t* counters;
+    float* partials;
+    uint64_t timeout_ns;
+    int stall;                 // testing aid: see pn_set_test_stall
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// 8x8 transpose of 16-bit elements across the warp (row lane / 4, columns 2 (lane % 4), + 1).
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
+    uint32_t r;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+__device__ bool wait_phase(uint32_t bar, uint32_t parity, uint64_t limit_ns, volatile uint32_t* abort) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const uint64_t t0 = globaltimer_ns();
+    for (;;) {
+        if (mbar_wait_suspend(bar, parity, 2000)) return true;
+        if (abort && *abort) return false;
+        if (globaltimer_ns() - t0 > limit_ns) return false;
+    }
+}
+
+__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" :: "n"(kWarps * 32) : "memory"); }
+
+// What a request asks of the cache.
+struct Request {
+    int n;                     // query tokens
+    int q0;                    // first of them
+    int pos0;                  // position of the first
+    int rows;                  // n * group
+    int len;
+    int lo_tile;               // first tile of the window
+    int sink_tiles;            // tiles before it that hold visible first tokens
+    int tiles;                 // units per (head, row group), at least 1
+    int row_groups;
+};
+
+template <int RT>
+__device__ __forceinline__ Request request_of(const AttnParams& P, int b) {
+    Request r;
+    const AttnArgs& a = P.a;
+    const int T = static_cast<int>(a.tokens);
+    r.q0 = min(max(a.starts[b], 0), T);
+    r.n = min(min(max(a.starts[b + 1], r.q0), T) - r.q0, a.max_queries);
+    const int64_t room = static_cast<int64_t>(a.max_pages) << P.cache.page_shift;
+    r.len = static_cast<int>(min(static_cast<int64_t>(max(a.lens[b], 0)), room));
+    r.pos0 = r.len - r.n;
+    r.rows = r.n * P.group;
+    const int lo = a.window ? max(r.pos0 - a.window + 1, 0) : 0;
+    r.lo_tile = lo / kTile;
+    r.sink_tiles = a.window ? min((a.sinks + kTile - 1) / kTile, r.lo_tile) : 0;
+    r.tiles = max((r.len + kTile - 1) / kTile - r.lo_tile + r.sink_tiles, 1);
+    r.row_groups = (r.rows + RT - 1) / RT;
+    return r;
+}
+
+template <int D>
+struct Shape {
+    static constexpr int kGroups = D / 64;             // groups of 64 values (one scale each)
+    static constexpr int kPlanes = kv_planes(D);
+    static constexpr int kPlaneGroups = kv_plane_groups(D);
+    static constexpr int kRecord = kv_record_bytes(D);
+    static constexpr int kStage = kTileRecords * kRecord;
+    static constexpr int kPlaneBytes = 256 * kPlaneGroups;     // 8 tokens of a plane
+    static constexpr int kStages = D == 256 ? 5 : D == 128 ? 9 : 16;
+};
+
+template <int D, int NT>
+struct Smem {
+    static constexpr int kRT = 8 * NT;
+    static constexpr int kRing = Shape<D>::kStages * Shape<D>::kStage;
+    static constexpr int kJoin = kRing;                                    // [warps][rows][kJoinPitch] floats
+    static constexpr int kMl = kJoin + kWarps * kRT * kJoinPitch * 4;      // [warps][rows] (reference, sum)
+    static constexpr int kFinal = kMl + kWarps * kRT * 8;                  // [rows] (reference, sum)
+    static constexpr int kBars = kFinal + kRT * 8;                         // full, empty
+    static constexpr int kValid = kBars + 2 * Shape<D>::kStages * 8;       // per stage: records that hold data
+    static constexpr int kMisc = kValid + Shape<D>::kStages * 4;           // abort, last-block flag
+    static constexpr int kScan = (kMisc + 8 + 7) / 8 * 8;                  // the warps' sums, then [batch + 1] prefix sums of units
+    static constexpr int kFixed = kScan + (kWarps + 1) * 8;
+    static int bytes(int batch) { return kFixed + (batch + 1) * 8; }
+};
+
+// The four scale-free codes of two tokens' words a, b: halves (token a, token b).
+// `odd` selects codes 1, 3, 5, 7.
+__device__ __forceinline__ uint32_t token_pair(uint32_t a, uint32_t b, bool odd) {
+    return __byte_perm(a, b, odd ? 0x7632 : 0x5410);
+}
+
+template <int N>
+__device__ __forceinline__ void load_scales(const uint8_t* p, float (&d)[N]) {
+    uint32_t w[(N + 1) / 2];
+    if constexpr (N == 1) w[0] = *reinterpret_cast<const uint16_t*>(p);
+    if constexpr (N == 2) w[0] = lds_u32(p);
+    if constexpr (N == 4) {
+        const uint2 v = lds_u64(p);
+        w[0] = v.x; w[1] = v.y;
+    }
+#pragma unroll
+    for (int i = 0; i < N; ++i) d[i] = half_bits_to_float(i & 1 ? w[i / 2] >> 16 : w[i / 2] & 0xFFFFu);
+}
+
+// Running state of a warp's share of a segment.  Lane (g, t) holds, for query
+// columns 8 nt + 2t + c, the reference and its part of the sum, and of O the
+// values 64 j + 8 g + 2 i (o[..][c]) and + 1 (o[..][2 + c]) for i = 0 .. 3.
+template <int D, int NT>
+struct State {
+    float ref[NT][2];
+    float sum[NT][2];
+    float o[NT][D / 16][4];
+};
+
+template <int D, int NT, bool kMasked>
+__device__ __forceinline__ void take_tile(const uint8_t* stage, int tok0, uint32_t valid, const uint2 (&q)[NT][D / 64][2][2],
+                                          const int (&pos)[NT][2], int window, int sinks, float scale, State<D, NT>& st) {
+    using S = Shape<D>;
+    constexpr int NG = S::kGroups, GP = S::kPlaneGroups, PL = S::kPlanes;
+    const int lane = threadIdx.x & 31, g = lane >> 2;
+    float x[kTileRecords][NT][4];
+    float e[kTileRecords][2];                  // log2 of the tokens' largest V scale
+    float top[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) top[n][0] = top[n][1] = -INFINITY;
+#pragma unroll
+    for (int r = 0; r < kTileRecords; ++r) {
+        const uint8_t* rec = stage + r * S::kRecord;
+        float dk0[NG], dk1[NG];
+        load_scales<NG>(rec + kv_k_scales(D) + g * 2 * NG, dk0);
+        load_scales<NG>(rec + kv_k_scales(D) + (g + 8) * 2 * NG, dk1);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) x[r][n][0] = x[r][n][1] = x[r][n][2] = x[r][n][3] = 0.0f;
+#pragma unroll
+        for (int pl = 0; pl < PL; ++pl) {
+            uint32_t w0[2 * GP], w1[2 * GP];   // the lane's words of tokens g and g + 8: [group][2]
+            const uint8_t* p0 = rec + pl * S::kPlaneBytes + lane * 8 * GP;
+            const uint8_t* p1 = p0 + PL * S::kPlaneBytes;
+            if constexpr (GP == 2) {
+                const uint4 u = lds_u128(p0), v = lds_u128(p1);
+                w0[0] = u.x; w0[1] = u.y; w0[2] = u.z; w0[3] = u.w;
+                w1[0] = v.x; w1[1] = v.y; w1[2] = v.z; w1[3] = v.w;
+            } else {
+                const uint2 u = lds_u64(p0), v = lds_u64(p1);
+                w0[0] = u.x; w0[1] = u.y;
+                w1[0] = v.x; w1[1] = v.y;
+            }
+#pragma unroll
+            for (int jj = 0; jj < GP; ++jj) {
+                const int j = pl * GP + jj;
+                float acc[NT][4];
+#pragma unroll
+                for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    const uint32_t a = w0[2 * jj + w], b = w1[2 * jj + w], as = a >> 8, bs = b >> 8;
+                    const uint32_t a0 = decode_pair<kPn4t, 0>(a, as), a1 = decode_pair<kPn4t, 0>(b, bs);
+                    const uint32_t a2 = decode_pair<kPn4t, 1>(a, as), a3 = decode_pair<kPn4t, 1>(b, bs);
+                    const uint32_t b0 = decode_pair<kPn4t, 2>(a, as), b1 = decode_pair<kPn4t, 2>(b, bs);
+                    const uint32_t b2 = decode_pair<kPn4t, 3>(a, as), b3 = decode_pair<kPn4t, 3>(b, bs);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        mma_16816(acc[n], a0, a1, a2, a3, q[n][j][w][0].x, q[n][j][w][0].y);
+                        mma_16816(acc[n], b0, b1, b2, b3, q[n][j][w][1].x, q[n][j][w][1].y);
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    x[r][n][0] = fmaf(dk0[j], acc[n][0], x[r][n][0]);
+                    x[r][n][1] = fmaf(dk0[j], acc[n][1], x[r][n][1]);
+                    x[r][n][2] = fmaf(dk1[j], acc[n][2], x[r][n][2]);
+                    x[r][n][3] = fmaf(dk1[j], acc[n][3], x[r][n][3]);
+                }
+            }
+        }
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+            float dv[NG], big = 5.9604645e-8f;      // 2^-24, the least scale: rows of V that are all zero count as it
+            load_scales<NG>(rec + kv_v_scales(D) + (g + 8 * hh) * 2 * NG, dv);
+#pragma unroll
+            for (int j = 0; j < NG; ++j) big = fmaxf(big, fabsf(dv[j]));
+            e[r][hh] = lg2(big);
+        }
+    }
+    // which of the lane's scores are seen: bit ((r * 2 + hh) * NT + n) * 2 + c
+    uint32_t seen = 0xFFFFFFFFu;
+    if constexpr (kMasked) {
+        seen = 0;
+#pragma unroll
+        for (int r = 0; r < kTileRecords; ++r)
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const int tok = tok0 + r * kKvTokens + hh * 8 + g;
+                        const bool s = ((valid >> r) & 1) && tok <= pos[n][c] && (tok > pos[n][c] - window || tok < sinks);
+                        seen |= static_cast<uint32_t>(s) << (((r * 2 + hh) * NT + n) * 2 + c);
+                    }
+    }
+    auto sees = [&](int r, int hh, int n, int c) { return !kMasked || ((seen >> (((r * 2 + hh) * NT + n) * 2 + c)) & 1u); };
+#pragma unroll
+    for (int r = 0; r < kTileRecords; ++r)
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const float y = fmaf(x[r][n][2 * hh + c], scale, e[r][hh]);
+                    top[n][c] = fmaxf(top[n][c], sees(r, hh, n, c) ? y : -INFINITY);
+                }
+    bool moved = false;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+#pragma unroll
+            for (int d = 4; d <= 16; d <<= 1) top[n][c] = fmaxf(top[n][c], __shfl_xor_sync(0xFFFFFFFFu, top[n][c], d));
+            top[n][c] -= 14.0f;
+            moved |= top[n][c] > st.ref[n][c];
+        }
+    if (__any_sync(0xFFFFFFFFu, moved)) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float f[2];
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const float to = fmaxf(top[n][c], st.ref[n][c]);
+                f[c] = st.ref[n][c] == -INFINITY ? 0.0f : ex2(st.ref[n][c] - to);
+                st.ref[n][c] = to;
+                st.sum[n][c] *= f[c];
+            }
+#pragma unroll
+            for (int m = 0; m < D / 16; ++m) {
+                st.o[n][m][0] *= f[0];
+                st.o[n][m][1] *= f[1];
+                st.o[n][m][2] *= f[0];
+                st.o[n][m][3] *= f[1];
+            }
+        }
+    }
+#pragma unroll
+    for (int r = 0; r < kTileRecords; ++r) {
+        const uint8_t* rec = stage + r * S::kRecord;
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const float p = ex2(fmaf(x[r][n][2 * hh + c], scale, -st.ref[n][c]));
+                    x[r][n][2 * hh + c] = sees(r, hh, n, c) ? p : 0.0f;
+                    st.sum[n][c] += x[r][n][2 * hh + c];
+                }
+        float dv[2][NG];
+        load_scales<NG>(rec + kv_v_scales(D) + g * 2 * NG, dv[0]);
+        load_scales<NG>(rec + kv_v_scales(D) + (g + 8) * 2 * NG, dv[1]);
+#pragma unroll
+        for (int pl = 0; pl < PL; ++pl) {
+            uint32_t w[2][2 * GP];             // [h][token of the pair][group]
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint8_t* p = rec + kv_v_codes(D) + (h * PL + pl) * S::kPlaneBytes + lane * 8 * GP;
+                if constexpr (GP == 2) {
+                    const uint4 u = lds_u128(p);
+                    w[h][0] = u.x; w[h][1] = u.y; w[h][2] = u.z; w[h][3] = u.w;
+                } else {
+                    const uint2 u = lds_u64(p);
+                    w[h][0] = u.x; w[h][1] = u.y;
+                }
+            }
+#pragma unroll
+            for (int jj = 0; jj < GP; ++jj) {
+                const int j = pl * GP + jj;
+                uint32_t b[NT][2];
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int hh = 0; hh < 2; ++hh) {
+                        // a hidden token's scale may be anything, NaN too: it is not multiplied
+                        float p0 = x[r][n][2 * hh] * dv[hh][j], p1 = x[r][n][2 * hh + 1] * dv[hh][j];
+                        if (kMasked) {
+                            p0 = sees(r, hh, n, 0) ? p0 : 0.0f;
+                            p1 = sees(r, hh, n, 1) ? p1 : 0.0f;
+                        }
+                        b[n][hh] = transpose_8x8(pack_half2(p0, p1));
+                    }
+                const uint32_t e0 = token_pair(w[0][jj], w[0][GP + jj], false), o0 = token_pair(w[0][jj], w[0][GP + jj], true);
+                const uint32_t e1 = token_pair(w[1][jj], w[1][GP + jj], false), o1 = token_pair(w[1][jj], w[1][GP + jj], true);
+                const uint32_t e0s = e0 >> 8, o0s = o0 >> 8, e1s = e1 >> 8, o1s = o1 >> 8;
+                static_for<4>([&](auto ic) {
+                    constexpr int I = decltype(ic)::value;
+                    const uint32_t a0 = decode_pair<kPn4t, I>(e0, e0s), a1 = decode_pair<kPn4t, I>(o0, o0s);
+                    const uint32_t a2 = decode_pair<kPn4t, I>(e1, e1s), a3 = decode_pair<kPn4t, I>(o1, o1s);
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) mma_16816(st.o[n][4 * j + I], a0, a1, a2, a3, b[n][0], b[n][1]);
+                });
+            }
+        }
+    }
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, NT == 1 && D <= 128 ? 2 : 1) attn_kernel(const __grid_constant__ AttnParams P) {
+    using S = Shape<D>;
+    using M = Smem<D, NT>;
+    constexpr int RT = 8 * NT, NG = S::kGroups, kStages = S::kStages;
+    extern __shared__ __align__(128) uint8_t smem[];
+    const uint32_t base = smem_addr(smem);
+    auto full = [&](int s) { return base + M::kBars + 8u * s; };
+    auto empty = [&](int s) { return base + M::kBars + 8u * (kStages + s); };
+    volatile uint32_t* valid = reinterpret_cast<volatile uint32_t*>(smem + M::kValid);
+    volatile uint32_t* abort = reinterpret_cast<volatile uint32_t*>(smem + M::kMisc);
+    volatile uint32_t* last_flag = abort + 1;
+    int64_t* warp_sums = reinterpret_cast<int64_t*>(smem + M::kScan);
+    int64_t* prefix = reinterpret_cast<int64_t*>(smem + M::kFixed);      // [batch + 1]
+    const AttnArgs& a = P.a;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int heads = P.cache.heads;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(full(s), 1);
+            mbar_init(empty(s), 1);
+        }
+        *abort = 0u;
+        fence_mbar_init();
+    }
+    // units before each request
+    {
+        const int each = (a.batch + kThreads - 1) / kThreads;
+        const int b0 = min(static_cast<int>(threadIdx.x) * each, a.batch), b1 = min(b0 + each, a.batch);
+        int64_t mine = 0;
+        for (int b = b0; b < b1; ++b) {
+            const Request r = request_of<RT>(P, b);
+            mine += static_cast<int64_t>(r.tiles) * r.row_groups * heads;
+        }
+        int64_t in = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t o = __shfl_up_sync(0xFFFFFFFFu, in, d);
+            if (lane >= d) in += o;
+        }
+        if (lane == 31) warp_sums[warp] = in;
+        __syncthreads();
+        int64_t at = in - mine;
+        for (int w = 0; w < warp; ++w) at += warp_sums[w];
+        for (int b = b0; b < b1; ++b) {
+            prefix[b] = at;
+            const Request r = request_of<RT>(P, b);
+            at += static_cast<int64_t>(r.tiles) * r.row_groups * heads;
+        }
+        if (threadIdx.x == kThreads - 1) prefix[a.batch] = at;
+        __syncthreads();
+    }
+    const int64_t total = prefix[a.batch];
+    const int64_t blocks = min(static_cast<int64_t>(gridDim.x), (total + kMinUnits - 1) / kMinUnits);
+    if (static_cast<int64_t>(blockIdx.x) >= blocks) return;              // nothing of this block is in flight
+    const int64_t u0 = total * blockIdx.x / blocks, u1 = total * (blockIdx.x + 1) / blocks;
+    auto request_at = [&](int64_t u) {                                   // the request that holds unit u
+        int lo = 0, hi = a.batch - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (prefix[mid] <= u) lo = mid;
+            else hi = mid - 1;
+        }
+        return lo;
+    };
+
+    if (warp == kWarps) {
+        // ------------------------------------------------------- producer --
+        int64_t issued = 0;
+        bool stop = false;
+        for (int64_t batch0 = u0; batch0 < u1 && !stop; batch0 += 32) {
+            // each lane prepares one unit: its cache pages
+            const int64_t u = batch0 + lane;
+            const uint8_t* src[kTileRecords] = {nullptr, nullptr, nullptr, nullptr};
+            int records = 0;
+            uint32_t have = 0;
+            if (u < u1) {
+                const int b = request_at(u);
+                const Request r = request_of<RT>(P, b);
+                const int64_t v = u - prefix[b];
+                const int idx = static_cast<int>(v % r.tiles);
+                const int h = static_cast<int>(v / (static_cast<int64_t>(r.tiles) * r.row_groups));
+                const int tile = idx < r.sink_tiles ? idx : r.lo_tile + idx - r.sink_tiles;
+                records = min(max((r.len - tile * kTile + kKvTokens - 1) / kKvTokens, 0), kTileRecords);
+#pragma unroll
+                for (int i = 0; i < kTileRecords; ++i) {
+                    if (i >= records) break;
+                    const int tok = tile * kTile + i * kKvTokens;
+                    const int page = a.table[static_cast<int64_t>(b) * a.table_stride + (tok >> P.cache.page_shift)];
+                    if (page < 0 || page >= P.cache.pages) continue;     // no such page: its tokens are not seen
+                    src[i] = P.cache.record((static_cast<int64_t>(page) << P.cache.page_shift) + (tok & (P.cache.page_size - 1)), h);
+                    have |= 1u << i;
+                }
+            }
+            const int count = static_cast<int>(min(static_cast<int64_t>(32), u1 - batch0));
+            for (int i = 0; i < count && !stop; ++i) {
+                const int64_t it = issued + i;
+                const int s = static_cast<int>(it % kStages);
+                if (lane == i) {
+                    if (it >= kStages && !wait_phase(empty(s), static_cast<uint32_t>(it / kStages - 1) & 1u, P.timeout_ns, abort)) {
+                        *abort = 1u;
+                        atomicCAS(P.status, 0u, kStatusTimeout);
+                        stop = true;
+                    } else {
+                        const uint32_t dst = base + s * S::kStage;
+                        valid[s] = have;
+                        mbar_arrive_expect_tx(full(s), __popc(have) * S::kRecord);
+                        // runs of records that follow each other in memory go in one copy
+                        // (testing aid: with stall the first unit's bytes are announced but
+                        // never copied; its wait can only time out)
+                        for (int k = P.stall && it == 0 ? kTileRecords : 0; k < kTileRecords;) {
+                            if (!((have >> k) & 1)) { ++k; continue; }
+                            int e = k + 1;
+                            while (e < kTileRecords && ((have >> e) & 1) && src[e] == src[k] + (e - k) * S::kRecord) ++e;
+                            bulk_g2s(dst + k * S::kRecord, src[k], (e - k) * S::kRecord, full(s));
+                            k = e;
+                        }
+                    }
+                }
+                stop = __shfl_sync(0xFFFFFFFFu, stop, i);
+                if (stop) { issued += i; break; }
+            }
+            if (!stop) issued += count;
+        }
+        // every copy lands before the block ends, also after an abort
+        if (lane == 0) {
+            for (int s = 0; s < kStages; ++s) {
+                if (issued <= s) continue;
+                const int64_t last = s + kStages * ((issued - 1 - s) / kStages);
+                if (P.stall && last == 0) continue;                      // never copied
+                wait_phase(full(s), static_cast<uint32_t>(last / kStages) & 1u, kDrainLimitNs, nullptr);
+            }
+        }
+        return;
+    }
+
+    // ---------------------------------------------------------- consumers --
+    const int g = lane >> 2, t = lane & 3;
+    float* join = reinterpret_cast<float*>(smem + M::kJoin);
+    float2* ml = reinterpret_cast<float2*>(smem + M::kMl);
+    float2* fin = reinterpret_cast<float2*>(smem + M::kFinal);
+    int64_t it0 = 0;
+    bool alive = true;
+    for (int64_t u = u0; u < u1;) {
+        const int b = request_at(u);
+        const Request r = request_of<RT>(P, b);
+        const int64_t v = u - prefix[b];
+        const int first = static_cast<int>(v % r.tiles);
+        const int64_t seg = v / r.tiles;
+        const int rg = static_cast<int>(seg % r.row_groups), h = static_cast<int>(seg / r.row_groups);
+        const int64_t seg_u0 = u - first;
+        const int count = static_cast<int>(min(static_cast<int64_t>(r.tiles - first), u1 - u));
+        const bool whole = count == r.tiles;
+        const int row0 = rg * RT;
+        const int active = min(count, kWarps);
+
+        State<D, NT> st;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            st.ref[n][0] = st.ref[n][1] = -INFINITY;
+            st.sum[n][0] = st.sum[n][1] = 0.0f;
+#pragma unroll
+            for (int m = 0; m < D / 16; ++m) st.o[n][m][0] = st.o[n][m][1] = st.o[n][m][2] = st.o[n][m][3] = 0.0f;
+        }
+        if (warp < active) {
+            uint2 q[NT][NG][2][2];
+            int pos[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const int row = min(row0 + 8 * n + g, r.rows - 1);
+                const int qi = row / P.group;
+                const __half* src = a.q + (r.q0 + qi) * a.q_stride + (h * P.group + row - qi * P.group) * D;
+#pragma unroll
+                for (int j = 0; j < NG; ++j)
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) {
+                        const uint4 f = *reinterpret_cast<const uint4*>(src + 64 * j + 16 * t + 8 * w);
+                        q[n][j][w][0] = make_uint2(f.x, f.y);
+                        q[n][j][w][1] = make_uint2(f.z, f.w);
+                    }
+#pragma unroll
+                for (int c = 0; c < 2; ++c) pos[n][c] = r.pos0 + min(row0 + 8 * n + 2 * t + c, r.rows - 1) / P.group;
+            }
+            const int pos_lo = r.pos0 + row0 / P.group;
+            const int pos_hi = r.pos0 + min(row0 + RT - 1, r.rows - 1) / P.group;
+            const int window = a.window ? a.window : INT32_MAX;
+            for (int k = warp; k < count; k += kWarps) {
+                const int64_t it = it0 + k;
+                const int s = static_cast<int>(it % kStages);
+                if (alive) {
+                    alive = wait_phase(full(s), static_cast<uint32_t>(it / kStages) & 1u, P.timeout_ns, abort);
+                    alive = __all_sync(0xFFFFFFFFu, alive);
+                    if (!alive && lane == 0) {
+                        *abort = 1u;
+                        atomicCAS(P.status, 0u, kStatusTimeout);
+                    }
+                }
+                if (!alive) continue;
+                const int idx = first + k;
+                const int tok0 = (idx < r.sink_tiles ? idx : r.lo_tile + idx - r.sink_tiles) * kTile;
+                const uint32_t have = valid[s];
+                const uint8_t* stage = smem + s * S::kStage;
+                if (tok0 > pos_hi) {
+                    // no row sees this tile
+                } else if (have == (1u << kTileRecords) - 1 && tok0 + kTile - 1 <= pos_lo && (tok0 > pos_hi - window || tok0 + kTile <= a.sinks)) {
+                    take_tile<D, NT, false>(stage, tok0, have, q, pos, window, a.sinks, P.scale_log2, st);
+                } else {
+                    take_tile<D, NT, true>(stage, tok0, have, q, pos, window, a.sinks, P.scale_log2, st);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(empty(s));
+            }
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int c = 0; c < 2; ++c)
+#pragma unroll
+                    for (int d = 4; d <= 16; d <<= 1) st.sum[n][c] += __shfl_xor_sync(0xFFFFFFFFu, st.sum[n][c], d);
+            if (g == 0) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) ml[warp * RT + 8 * n + 2 * t + c] = make_float2(st.ref[n][c], st.sum[n][c]);
+            }
+        }
+        consumers_sync();
+        // the rows' common reference and sum
+        if (threadIdx.x < RT) {
+            float m = -INFINITY, l = 0.0f;
+            for (int w = 0; w < active; ++w) m = fmaxf(m, ml[w * RT + threadIdx.x].x);
+            for (int w = 0; w < active; ++w) {
+                const float2 p = ml[w * RT + threadIdx.x];
+                l += p.x == -INFINITY ? 0.0f : ex2(p.x - m) * p.y;
+            }
+            fin[threadIdx.x] = make_float2(m, l);
+        }
+        if (warp < active) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float f[2];
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    float m = -INFINITY;
+                    for (int w = 0; w < active; ++w) m = fmaxf(m, ml[w * RT + 8 * n + 2 * t + c].x);
+                    f[c] = st.ref[n][c] == -INFINITY ? 0.0f : ex2(st.ref[n][c] - m);
+                }
+#pragma unroll
+                for (int m = 0; m < D / 16; ++m) {
+                    st.o[n][m][0] *= f[0];
+                    st.o[n][m][1] *= f[1];
+                    st.o[n][m][2] *= f[0];
+                    st.o[n][m][3] *= f[1];
+                }
+            }
+        }
+        // blocks that share the segment
+        const int64_t seg_u1 = seg_u0 + r.tiles;
+        auto block_of = [&](int64_t x) { return static_cast<int>(((x + 1) * blocks + total - 1) / total - 1); };
+        const int c_first = whole ? 0 : block_of(seg_u0), c_last = whole ? 0 : block_of(seg_u1 - 1);
+        float* slot = P.partials + static_cast<int64_t>(2 * blockIdx.x + (first == 0 ? 1 : 0)) * kSlotFloats;
+#pragma unroll
+        for (int j = 0; j < NG; ++j) {
+            if (warp < active) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        float* to = join + (warp * RT + 8 * n + 2 * t + c) * kJoinPitch + 8 * g;
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            *reinterpret_cast<float2*>(to + 2 * i) = make_float2(st.o[n][4 * j + i][c], st.o[n][4 * j + i][2 + c]);
+                    }
+            }
+            consumers_sync();
+            for (int i = threadIdx.x; i < RT * 32; i += kWarps * 32) {
+                const int row = i >> 5, d = (i & 31) * 2;
+                if (row0 + row < r.rows) {
+                    float2 o = make_float2(0.0f, 0.0f);
+                    for (int w = 0; w < active; ++w) {
+                        const float2 p = *reinterpret_cast<const float2*>(join + (w * RT + row) * kJoinPitch + d);
+                        o.x += p.x;
+                        o.y += p.y;
+                    }
+                    const float2 f = fin[row];
+                    if (whole) {
+                        const float inv = f.y == 0.0f ? 0.0f : 1.0f / f.y;
+                        const int qi = (row0 + row) / P.group;
+                        const int64_t at = (static_cast<int64_t>(r.q0 + qi) * a.heads + h * P.group + row0 + row - qi * P.group);
+                        *reinterpret_cast<__half2*>(a.out + at * D + 64 * j + d) = __floats2half2_rn(o.x * inv, o.y * inv);
+                        if (a.lse && j == 0 && d == 0)
+                            a.lse[at] = f.y == 0.0f ? -INFINITY : 0.6931471805599453f * (f.x + log2f(f.y));
+                    } else {
+                        *reinterpret_cast<float2*>(slot + row * D + 64 * j + d) = o;
+                        if (j == 0 && d == 0) *reinterpret_cast<float2*>(slot + 2048 + 2 * row) = f;
+                    }
+                }
+            }
+            consumers_sync();
+        }
+        if (!whole) {
+            __threadfence();
+            consumers_sync();
+            if (threadIdx.x == 0) {
+                const uint32_t n = static_cast<uint32_t>(c_last - c_first);
+                const uint32_t old = atomicAdd(&P.counters[c_first], 1u);
+                *last_flag = old == n;
+                if (old == n) P.counters[c_first] = 0u;
+            }
+            consumers_sync();
+            if (*last_flag) {
+                __threadfence();
+                const float* parts = P.partials;
+                auto part = [&](int c) { return parts + static_cast<int64_t>(2 * c + (c == c_first ? 1 : 0)) * kSlotFloats; };
+                for (int i = threadIdx.x; i < RT * (D / 2); i += kWarps * 32) {
+                    const int row = i / (D / 2), d = (i % (D / 2)) * 2;
+                    if (row0 + row >= r.rows) continue;
+                    float m = -INFINITY, l = 0.0f;
+#pragma unroll 4
+                    for (int c = c_first; c <= c_last; ++c) m = fmaxf(m, __ldcg(part(c) + 2048 + 2 * row));
+                    float2 o = make_float2(0.0f, 0.0f);
+#pragma unroll 4
+                    for (int c = c_first; c <= c_last; ++c) {
+                        const float* p = part(c);
+                        const float2 f = __ldcg(reinterpret_cast<const float2*>(p + 2048 + 2 * row));
+                        const float2 w = __ldcg(reinterpret_cast<const float2*>(p + row * D + d));
+                        const float s = f.x == -INFINITY ? 0.0f : ex2(f.x - m);
+                        l += s * f.y;
+                        o.x += s * w.x;
+                        o.y += s * w.y;
+                    }
+                    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                    const int qi = (row0 + row) / P.group;
+                    const int64_t at = (static_cast<int64_t>(r.q0 + qi) * a.heads + h * P.group + row0 + row - qi * P.group);
+                    *reinterpret_cast<__half2*>(a.out + at * D + d) = __floats2half2_rn(o.x * inv, o.y * inv);
+                    if (a.lse && d == 0) a.lse[at] = l == 0.0f ? -INFINITY : 0.6931471805599453f * (m + log2f(l));
+                }
+            }
+        }
+        it0 += count;
+        u += count;
+    }
+}
+
+template <int D, int NT>
+cudaError_t launch(const AttnParams& P, int num_sms, cudaStream_t s) {
+    static std::atomic<uint64_t> smem_set{0};
+    if (cudaError_t e = set_smem_limit_once(attn_kernel<D, NT>, 227 * 1024, smem_set); e != cudaSuccess) return e;
+    const int smem = Smem<D, NT>::bytes(P.a.batch);
+    if (smem > 227 * 1024) return cudaErrorInvalidValue;
+    const int grid = num_sms * (NT == 1 && D <= 128 ? kCtasPerSm : 1);
+    attn_kernel<D, NT><<<grid, kThreads, smem, s>>>(P);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+// Workspace: status word (256 bytes), one counter per thread block, two partial slots per thread block.
+size_t attn_workspace_bytes(int num_sms) {
+    const size_t ctas = static_cast<size_t>(num_sms) * kCtasPerSm;
+    return 256 + (ctas * 4 + 255) / 256 * 256 + 2 * ctas * kSlotFloats * 4;
+}
+
+cudaError_t launch_attention(const AttnArgs& a, const KvGeometry& g, void* workspace, int num_sms, uint64_t timeout_ns, int stall,
+                             cudaStream_t s) {
+    int shift = 0;
+    while ((1 << shift) < g.page_size) ++shift;
+    const size_t ctas = static_cast<size_t>(num_sms) * kCtasPerSm;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    AttnParams P{a, KvCache{g.data, g.pages, g.page_size, shift, g.heads, g.D}, a.heads / g.heads, a.scale * 1.4426950408889634f,
+                 reinterpret_cast<uint32_t*>(ws), reinterpret_cast<uint32_t*>(ws + 256),
+                 reinterpret_cast<float*>(ws + 256 + (ctas * 4 + 255) / 256 * 256), timeout_ns, stall};
+    // 8 or 16 query rows share the decoded codes
+    const bool wide = static_cast<int64_t>(a.max_queries) * P.group > 8;
+    if (g.D == 64) return wide ? launch<64, 2>(P, num_sms, s) : launch<64, 1>(P, num_sms, s);
+    if (g.D == 128) return wide ? launch<128, 2>(P, num_sms, s) : launch<128, 1>(P, num_sms, s);
+    return launch<256, 1>(P, num_sms, s);
+}
+
+}  // namespace pn

@@ -27,6 +27,14 @@ bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
     return pa < pb + nb && pb < pa + na;
 }
 
+// Pages of the 4-bit cache hold a power of two of tokens, whole records of 16.
+bool page_size_ok(int page_size) { return page_size >= 16 && page_size <= 1024 && (page_size & (page_size - 1)) == 0; }
+
+bool kv_shape_ok(int64_t pages, int page_size, int kv_heads, int head_dim) {
+    return pages >= 1 && pages <= INT32_MAX && page_size_ok(page_size) && kv_heads >= 1 && kv_heads <= 65536 &&
+           (head_dim == 64 || head_dim == 128 || head_dim == 256);
+}
+
 }  // namespace
 
 namespace pn {
@@ -528,6 +536,166 @@ pn_status pn_read_ranges(const void* const* ptrs, const size_t* bytes, int count
     pn_status st = device_info(&sms, &major);
     if (st != PN_OK) return st;
     const cudaError_t e = pn::launch_read_ranges(ptrs, bytes, count, sink, sms, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PN_OK : pn::cuda_error(e);
+}
+
+// ------------------------------------------------- 4-bit cache, serving step --
+
+size_t pn_kv_cache_bytes(int64_t pages, int page_size, int kv_heads, int head_dim) {
+    if (!kv_shape_ok(pages, page_size, kv_heads, head_dim)) return 0;
+    return static_cast<size_t>(pages) * kv_heads * (page_size / 16) * 17 * head_dim;
+}
+
+pn_status pn_kv_plan(const int32_t* lens, const int32_t* add, const int32_t* held, int batch, int32_t* table,
+                     int64_t table_stride, int max_pages, int32_t* free_pages, int64_t pages, const int64_t* ring,
+                     int page_size, int64_t capacity, int64_t* slots, int32_t* positions, int32_t* requests,
+                     int32_t* starts, int32_t* lens_out, int32_t* held_out, int64_t* ring_out, int32_t* refused,
+                     pn_stream stream) {
+    if (batch < 1 || batch > pn::kKvMaxBatch || max_pages < 1 || table_stride < max_pages || pages < 1 ||
+        pages > INT32_MAX || !page_size_ok(page_size) || capacity < 0 || capacity > INT32_MAX ||
+        static_cast<int64_t>(max_pages) * page_size > INT32_MAX)
+        return PN_EINVAL;
+    if (!lens || !add || !held || !table || !free_pages || !ring || !starts || !lens_out || !held_out || !ring_out ||
+        !refused || (capacity > 0 && (!slots || !positions || !requests)))
+        return PN_EINVAL;
+    for (const void* p : {static_cast<const void*>(lens), static_cast<const void*>(add), static_cast<const void*>(held),
+                          static_cast<const void*>(table), static_cast<const void*>(free_pages),
+                          static_cast<const void*>(positions), static_cast<const void*>(requests),
+                          static_cast<const void*>(starts), static_cast<const void*>(lens_out),
+                          static_cast<const void*>(held_out), static_cast<const void*>(refused)})
+        if (!aligned(p, 4)) return PN_EALIGN;
+    if (!aligned(ring, 8) || !aligned(ring_out, 8) || !aligned(slots, 8)) return PN_EALIGN;
+    // the blocks read the inputs while others write: no output may be an input or another output
+    const size_t nb = static_cast<size_t>(batch) * 4, nc = static_cast<size_t>(capacity);
+    const struct { const void* p; size_t n; } in[] = {{lens, nb}, {add, nb}, {held, nb}, {ring, 16}},
+        out[] = {{table, (static_cast<size_t>(batch - 1) * table_stride + max_pages) * 4},
+                 {free_pages, static_cast<size_t>(pages) * 4}, {slots, nc * 8}, {positions, nc * 4},
+                 {requests, nc * 4}, {starts, nb + 4}, {lens_out, nb}, {held_out, nb}, {ring_out, 16}, {refused, 4}};
+    for (size_t i = 0; i < sizeof(out) / sizeof(out[0]); ++i) {
+        for (const auto& q : in)
+            if (overlaps(out[i].p, out[i].n, q.p, q.n)) return PN_EINVAL;
+        for (size_t j = 0; j < i; ++j)
+            if (overlaps(out[i].p, out[i].n, out[j].p, out[j].n)) return PN_EINVAL;
+    }
+    int sms = 0, major = 0;
+    if (pn_status st = device_info(&sms, &major); st != PN_OK) return st;
+    const pn::KvPlanArgs a{lens, add, held, batch, table, table_stride, max_pages, free_pages, pages, ring, page_size,
+                           capacity, slots, positions, requests, starts, lens_out, held_out, ring_out, refused};
+    const cudaError_t e = pn::launch_kv_plan(a, sms, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PN_OK : pn::cuda_error(e);
+}
+
+pn_status pn_kv_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                       int64_t v_stride, int dtype, int64_t tokens, int heads, const float* q_weight,
+                       const float* k_weight, float eps, const float* cos, const float* sin, int64_t table_rows,
+                       int rotary, int interleaved, const int32_t* positions, const int64_t* slots, void* cache,
+                       int64_t pages, int page_size, int kv_heads, int head_dim, uint16_t* q_out, pn_stream stream) {
+    if (!kv_shape_ok(pages, page_size, kv_heads, head_dim)) return PN_EINVAL;
+    if (dtype != PN_DTYPE_F32 && dtype != PN_DTYPE_F16) return PN_EINVAL;
+    if (tokens < 0 || tokens > INT32_MAX || heads < 0 || heads > 65536) return PN_EINVAL;
+    if (rotary < 0 || rotary > head_dim || rotary % 2 || table_rows < 0 || !(eps >= 0.0f)) return PN_EINVAL;
+    if (tokens == 0) return PN_OK;
+    if (!k || !v || !slots || !cache || (heads > 0 && (!q || !q_out))) return PN_EINVAL;
+    if (rotary > 0 && (!cos || !sin || !positions)) return PN_EINVAL;
+    const int64_t kv_cols = static_cast<int64_t>(kv_heads) * head_dim, q_cols = static_cast<int64_t>(heads) * head_dim;
+    if (k_stride < kv_cols || v_stride < kv_cols || (heads > 0 && q_stride < q_cols)) return PN_EINVAL;
+    const uintptr_t size = dtype == PN_DTYPE_F32 ? 4 : 2;
+    if (!aligned(q, size) || !aligned(k, size) || !aligned(v, size) || !aligned(q_weight, 4) || !aligned(k_weight, 4) ||
+        !aligned(cos, 4) || !aligned(sin, 4) || !aligned(positions, 4) || !aligned(slots, 8) || !aligned(cache, 16) ||
+        !aligned(q_out, 16))
+        return PN_EALIGN;
+    const size_t cache_bytes = pn_kv_cache_bytes(pages, page_size, kv_heads, head_dim);
+    const struct { const void* p; size_t n; } in[] = {
+        {q, heads > 0 ? ((tokens - 1) * q_stride + q_cols) * size : 0}, {k, ((tokens - 1) * k_stride + kv_cols) * size},
+        {v, ((tokens - 1) * v_stride + kv_cols) * size}};
+    for (const auto& i : in)
+        if (i.n && (overlaps(i.p, i.n, cache, cache_bytes) || (heads > 0 && overlaps(i.p, i.n, q_out, tokens * q_cols * 2))))
+            return PN_EINVAL;
+    int sms = 0, major = 0;
+    if (pn_status st = device_info(&sms, &major); st != PN_OK) return st;
+    const pn::KvAppendArgs a{q, k, v, q_stride, k_stride, v_stride, dtype == PN_DTYPE_F16, tokens, heads, q_weight,
+                             k_weight, eps, cos, sin, rotary / 2, table_rows, interleaved != 0, positions, slots,
+                             reinterpret_cast<__half*>(q_out)};
+    const pn::KvGeometry g{static_cast<uint8_t*>(cache), pages, page_size, kv_heads, head_dim};
+    const cudaError_t e = pn::launch_kv_append(a, g, sms, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PN_OK : pn::cuda_error(e);
+}
+
+pn_status pn_kv_read(const void* cache, int64_t pages, int page_size, int kv_heads, int head_dim,
+                     const int64_t* slots, int64_t tokens, float* k, float* v, pn_stream stream) {
+    if (!kv_shape_ok(pages, page_size, kv_heads, head_dim) || tokens < 0 || tokens > INT32_MAX) return PN_EINVAL;
+    if (tokens == 0) return PN_OK;
+    if (!cache || !slots || !k || !v) return PN_EINVAL;
+    if (!aligned(cache, 16) || !aligned(slots, 8) || !aligned(k, 16) || !aligned(v, 16)) return PN_EALIGN;
+    const size_t n = static_cast<size_t>(tokens) * kv_heads * head_dim * 4;
+    const size_t bytes = pn_kv_cache_bytes(pages, page_size, kv_heads, head_dim);
+    if (overlaps(k, n, v, n) || overlaps(k, n, cache, bytes) || overlaps(v, n, cache, bytes)) return PN_EINVAL;
+    int sms = 0, major = 0;
+    if (pn_status st = device_info(&sms, &major); st != PN_OK) return st;
+    const pn::KvGeometry g{static_cast<uint8_t*>(const_cast<void*>(cache)), pages, page_size, kv_heads, head_dim};
+    const cudaError_t e = pn::launch_kv_read(g, slots, tokens, k, v, sms, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PN_OK : pn::cuda_error(e);
+}
+
+size_t pn_attention_workspace_bytes(void) {
+    int sms = 0, major = 0;
+    return device_info(&sms, &major) == PN_OK ? pn::attn_workspace_bytes(sms) : 0;
+}
+
+pn_status pn_attention(const uint16_t* q, int64_t q_stride, int64_t tokens, int heads, const void* cache,
+                       int64_t pages, int page_size, int kv_heads, int head_dim, const int32_t* table,
+                       int64_t table_stride, int max_pages, const int32_t* lens, const int32_t* starts, int batch,
+                       int max_queries, float scale, int window, int sinks, uint16_t* out, float* lse,
+                       void* workspace, size_t workspace_bytes, pn_stream stream) {
+    if (!kv_shape_ok(pages, page_size, kv_heads, head_dim)) return PN_EINVAL;
+    if (tokens < 0 || tokens > INT32_MAX || heads < 1 || heads > 65536 || heads % kv_heads) return PN_EINVAL;
+    if (batch < 1 || batch > pn::kKvMaxBatch || max_queries < 1 || max_pages < 1 || table_stride < max_pages ||
+        window < 0 || sinks < 0 || !(scale - scale == 0.0f))
+        return PN_EINVAL;
+    if (static_cast<int64_t>(max_pages) * page_size > INT32_MAX - 128 ||
+        static_cast<int64_t>(max_queries) * (heads / kv_heads) > INT32_MAX - 128)
+        return PN_EINVAL;
+    const int64_t cols = static_cast<int64_t>(heads) * head_dim;
+    if (q_stride < cols) return PN_EINVAL;
+    if (tokens == 0) return PN_OK;
+    if (!q || !cache || !table || !lens || !starts || !out || !workspace) return PN_EINVAL;
+    if (!aligned(q, 16) || q_stride % 8 || !aligned(cache, 16) || !aligned(table, 4) || !aligned(lens, 4) ||
+        !aligned(starts, 4) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 256))
+        return PN_EALIGN;
+    const size_t nq = (static_cast<size_t>(tokens - 1) * q_stride + cols) * 2, no = static_cast<size_t>(tokens) * cols * 2;
+    if (overlaps(q, nq, out, no) || overlaps(cache, pn_kv_cache_bytes(pages, page_size, kv_heads, head_dim), out, no))
+        return PN_EINVAL;
+    int sms = 0, major = 0;
+    if (pn_status st = device_info(&sms, &major); st != PN_OK) return st;
+    if (major < 10) return PN_EUNSUPPORTED;
+    if (pn::attn_workspace_bytes(sms) > workspace_bytes) return PN_EINVAL;
+    const pn::AttnArgs a{reinterpret_cast<const __half*>(q), q_stride, tokens, heads, table, table_stride, max_pages,
+                         lens, starts, batch, max_queries, scale, window, sinks, reinterpret_cast<__half*>(out), lse};
+    const pn::KvGeometry g{static_cast<uint8_t*>(const_cast<void*>(cache)), pages, page_size, kv_heads, head_dim};
+    const cudaError_t e = pn::launch_attention(a, g, workspace, sms, g_timeout_ns.load(), g_test_stall.load(),
+                                               reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PN_OK : pn::cuda_error(e);
+}
+
+pn_status pn_verify(const int32_t* tokens, const float* target, int64_t target_stride, const float* draft,
+                    int64_t draft_stride, const float* uniforms, const int32_t* counts, int batch, int drafts,
+                    int vocab, int32_t* accepted, int32_t* out, pn_stream stream) {
+    if (batch < 0 || batch > (1 << 24) || drafts < 0 || drafts > PN_MAX_DRAFTS || vocab < 1 || vocab > PN_MAX_VOCAB)
+        return PN_EINVAL;
+    if (target_stride < vocab || (draft && draft_stride < vocab)) return PN_EINVAL;
+    if (batch == 0) return PN_OK;
+    if ((drafts > 0 && !tokens) || !target || !uniforms || !accepted || !out) return PN_EINVAL;
+    if (!aligned(tokens, 4) || !aligned(target, 4) || !aligned(draft, 4) || !aligned(uniforms, 4) ||
+        !aligned(counts, 4) || !aligned(accepted, 4) || !aligned(out, 4))
+        return PN_EALIGN;
+    const size_t nt = static_cast<size_t>(batch) * drafts * 4, no = nt + static_cast<size_t>(batch) * 4;
+    if (overlaps(tokens, nt, out, no) || overlaps(accepted, static_cast<size_t>(batch) * 4, out, no)) return PN_EINVAL;
+    int sms = 0, major = 0;
+    if (pn_status st = device_info(&sms, &major); st != PN_OK) return st;
+    if (major < 9) return PN_EUNSUPPORTED;
+    const pn::VerifyArgs a{tokens, target, target_stride, draft, draft_stride, uniforms, counts, batch, drafts, vocab,
+                           accepted, out};
+    const cudaError_t e = pn::launch_verify(a, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PN_OK : pn::cuda_error(e);
 }
 

@@ -3,6 +3,7 @@
 
 #include <atomic>
 #include <cstdint>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "../../include/pn.h"
@@ -176,6 +177,103 @@ size_t tc_partial_bytes(int num_sms);
 cudaError_t launch_gemv_ffma(const GemvTensor* t, int count, int M, uint32_t* status, int num_sms,
                              uint64_t timeout_ns, cudaStream_t s);
 int ffma_max_chunks();
+
+// ------------------------------------------------- 4-bit cache, serving step --
+
+struct KvGeometry {
+    uint8_t* data;
+    int64_t pages;
+    int page_size;
+    int heads;                 // key/value heads
+    int D;                     // 64, 128 or 256
+};
+
+struct KvPlanArgs {
+    const int32_t* lens;
+    const int32_t* add;
+    const int32_t* held;
+    int batch;
+    int32_t* table;
+    int64_t table_stride;
+    int max_pages;
+    int32_t* free_pages;
+    int64_t pages;             // entries of the ring
+    const int64_t* ring;
+    int page_size;
+    int64_t capacity;
+    int64_t* slots;
+    int32_t* positions;
+    int32_t* requests;
+    int32_t* starts;
+    int32_t* lens_out;
+    int32_t* held_out;
+    int64_t* ring_out;
+    int32_t* refused;
+};
+constexpr int kKvMaxBatch = 16384;     // requests of a plan or an attention call (their prefix sums stay in shared memory)
+cudaError_t launch_kv_plan(const KvPlanArgs& a, int num_sms, cudaStream_t s);
+
+struct KvAppendArgs {
+    const void* q;
+    const void* k;
+    const void* v;
+    int64_t q_stride, k_stride, v_stride;   // elements between tokens
+    bool f16;
+    int64_t tokens;
+    int heads;                 // query heads
+    const float* q_weight;
+    const float* k_weight;
+    float eps;
+    const float* cos;
+    const float* sin;
+    int half;                  // rotated pairs, 0 none
+    int64_t table_rows;        // rows of cos and sin
+    bool interleaved;
+    const int32_t* positions;
+    const int64_t* slots;
+    __half* q_out;
+};
+cudaError_t launch_kv_append(const KvAppendArgs& a, const KvGeometry& g, int num_sms, cudaStream_t s);
+cudaError_t launch_kv_read(const KvGeometry& g, const int64_t* slots, int64_t tokens, float* k, float* v, int num_sms,
+                           cudaStream_t s);
+
+struct AttnArgs {
+    const __half* q;
+    int64_t q_stride;          // elements between tokens
+    int64_t tokens;            // rows of q
+    int heads;                 // query heads
+    const int32_t* table;
+    int64_t table_stride;
+    int max_pages;
+    const int32_t* lens;
+    const int32_t* starts;
+    int batch;
+    int max_queries;
+    float scale;
+    int window;                // 0 none
+    int sinks;
+    __half* out;
+    float* lse;                // may be null
+};
+size_t attn_workspace_bytes(int num_sms);
+cudaError_t launch_attention(const AttnArgs& a, const KvGeometry& g, void* workspace, int num_sms, uint64_t timeout_ns, int stall,
+                             cudaStream_t s);
+
+struct VerifyArgs {
+    const int32_t* tokens;
+    const float* target;
+    int64_t target_stride;     // elements between rows
+    const float* draft;
+    int64_t draft_stride;
+    const float* uniforms;
+    const int32_t* counts;
+    int batch;
+    int drafts;
+    int vocab;
+    int32_t* accepted;
+    int32_t* out;
+};
+cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t s);
 
 // Host-side checks of a one-tensor GEMV, the same ones pn_gemv_ex makes before
 // it launches anything.  On PN_OK, *uses_workspace tells whether the call

@@ -324,6 +324,159 @@ pn_status pn_prefill(int type, const void* W, int64_t N, int64_t K, const uint16
                      pn_stream stream);
 
 /*
+ * ------------------------------------------------------------ 4-bit cache --
+ *
+ * A serving step between two GEMVs: pages and slots for its tokens
+ * (pn_kv_plan), norms and rotation of queries and keys with the write into a
+ * paged cache held in 4 bits (pn_kv_append), the step's queries against that
+ * cache (pn_attention), and the drafted tokens against the target's
+ * probabilities (pn_verify).  (The pages' engine keeps its cache in 4 bits and
+ * splits the cached tokens of a decode step over the GPU: tensorless docs,
+ * "What the fork adds".  They give no layout; the one here is this library's.)
+ *
+ * The cache: `pages` pages of page_size tokens (a power of two, 16 .. 1024)
+ * of kv_heads heads of head_dim values (64, 128 or 256), in all
+ * pn_kv_cache_bytes(...) bytes (0 for a shape outside these), 16-byte aligned:
+ *
+ *   uint8 [pages][kv_heads][page_size / 16][17 * head_dim]
+ *
+ * A record holds 16 consecutive tokens of one head: K codes (8 D bytes), K
+ * scales (D / 2), V codes (8 D), V scales (D / 2).  Values are pn4t's: groups
+ * of 64 with a signed fp16 scale d and codes n, value d * (n - 8), chosen by
+ * pn_pack's rule; eight codes to a 32-bit word as in a PN block.  With token r
+ * = 8 h + g of the record (h = 0, 1), group j = 2 plane + s (D = 64: plane =
+ * s = 0), word i of the group, the words lie in the order
+ *   K  [h][plane][g][i / 2][s][i % 2]
+ *   V  [h][plane][i][g / 2][g % 2][s]
+ * (s absent for D = 64), and the scales [token][group].  Bytes that no token
+ * was written to may hold anything.  A slot is page * page_size + place in the
+ * page (64 bits).
+ */
+size_t pn_kv_cache_bytes(int64_t pages, int page_size, int kv_heads, int head_dim);
+
+/*
+ * pn_kv_plan: one step's bookkeeping on the device.  For request b < batch
+ * (at most 16384): lens[b] tokens are cached, held[b] pages are its own (the
+ * first held[b] entries of row b of table: int32 [batch][table_stride], of
+ * which max_pages are used), and add[b] >= 0 tokens join it; add[b] < 0: the
+ * request is finished.  Free pages are a ring free_pages[pages] with
+ * ring = {head, tail}: entries head .. tail - 1, modulo pages, are free.
+ *   starts[b] (b <= batch): tokens of the step before request b.
+ *   Taking: request b needs max(ceil((lens + add) / page_size) - held, 0)
+ *   pages, taken from the ring's head in request order.  A request whose pages
+ *   pass max_pages, whose tokens end behind `capacity`, or whose need together
+ *   with those of the requests before it passes the free pages is refused: it
+ *   takes nothing, its length stays, its tokens get no slots.
+ *   Giving: a finished request's held pages go behind the ring's tail in
+ *   request order, its length and held become 0.  (A shorter lens with the same held, after
+ *   drafts were turned down, keeps the pages for the tokens to come.)
+ *   Token t < starts[batch] of request b: requests[t] = b, positions[t] =
+ *   lens[b] + t - starts[b], slots[t] = its place in the cache; -1 in the
+ *   latter two where b was refused, in all three for starts[batch] <= t <
+ *   capacity.
+ *   lens_out, held_out [batch], ring_out {head, tail}, refused[1] (how many):
+ *   the state after the step.
+ * Inputs stay as they are but for the new entries of table and free_pages, so
+ * a call repeated on them gives the same; no output may overlap an input or
+ * another output.  The ring's invariant (tail - head + all held pages at most
+ * `pages`) is the caller's; no access leaves the arrays without it.
+ */
+pn_status pn_kv_plan(const int32_t* lens, const int32_t* add, const int32_t* held, int batch, int32_t* table,
+                     int64_t table_stride, int max_pages, int32_t* free_pages, int64_t pages, const int64_t* ring,
+                     int page_size, int64_t capacity, int64_t* slots, int32_t* positions, int32_t* requests,
+                     int32_t* starts, int32_t* lens_out, int32_t* held_out, int64_t* ring_out, int32_t* refused,
+                     pn_stream stream);
+
+/*
+ * pn_kv_append: for each of `tokens` tokens with `heads` query heads and
+ * kv_heads key and value heads (q, k, v of `dtype`, rows of q_stride / k_stride
+ * / v_stride elements, heads contiguous in a row):
+ *   norm (where q_weight / k_weight, fp32 [head_dim], is given): y = x * (1 /
+ *   sqrt(mean(x^2) + eps)) * weight per head;
+ *   rotation (rotary > 0, even): with row positions[t] of cos and sin (fp32
+ *   [table_rows][rotary / 2]; a position outside the table leaves the row as
+ *   it is), the first `rotary` values as pairs (a, b) = (y[i], y[i + rotary/2])
+ *   or, interleaved, (y[2i], y[2i+1]) become (a c - b s, b c + a s);
+ *   q_out[t][heads][head_dim]: the queries rounded to fp16;
+ *   keys, and values as they are, by pn_pack's rule into slot slots[t]; a
+ *   token whose slot is negative or outside the cache writes no cache.
+ * The arithmetic is fp32 with every operation rounded by itself, in a fixed
+ * order, so the cache's bytes are reproducible bit for bit: squares are added
+ * pairwise, the upper half of the row to the lower until one is left, times
+ * 1 / head_dim; fp32 quotients and square roots are IEEE.  Inputs must be
+ * finite (else that head's codes are unspecified).  q_out and cache 16-byte
+ * aligned, other arrays to their element.  No two tokens of a call may share
+ * a slot.  heads = 0: keys and values alone.
+ */
+typedef enum { PN_DTYPE_F32 = 0, PN_DTYPE_F16 = 1 } pn_dtype;
+pn_status pn_kv_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                       int64_t v_stride, int dtype, int64_t tokens, int heads, const float* q_weight,
+                       const float* k_weight, float eps, const float* cos, const float* sin, int64_t table_rows,
+                       int rotary, int interleaved, const int32_t* positions, const int64_t* slots, void* cache,
+                       int64_t pages, int page_size, int kv_heads, int head_dim, uint16_t* q_out, pn_stream stream);
+
+/* pn_kv_read: the cached keys and values of `tokens` slots as fp32
+ * [tokens][kv_heads][head_dim], exact; zeros for a slot outside the cache.
+ * k and v 16-byte aligned. */
+pn_status pn_kv_read(const void* cache, int64_t pages, int page_size, int kv_heads, int head_dim,
+                     const int64_t* slots, int64_t tokens, float* k, float* v, pn_stream stream);
+
+/*
+ * pn_attention: for request b < batch (at most 16384) the query tokens
+ * starts[b] .. starts[b + 1] - 1 of q (fp16, rows of q_stride elements, heads
+ * contiguous; at most max_queries of them), the last of which sits at cached
+ * token lens[b] - 1; `heads` is a multiple of kv_heads, and query head h reads
+ * key/value head h / (heads / kv_heads).  A query at position p sees the
+ * cached tokens t <= p with, where window > 0, t > p - window or t < sinks.
+ *   x_t = scale * q . k_t;  lse = ln sum_t exp(x_t);
+ *   out = sum_t exp(x_t - lse) v_t
+ * A query that sees nothing gets out = 0 and lse = -inf.  Hidden tokens have
+ * no influence whatever their bytes hold, and neither have pages that the
+ * table gives outside the cache: their tokens are hidden.  Rows of out that
+ * belong to no request are not written.
+ * out fp16 [tokens][heads][head_dim], lse fp32 [tokens][heads] or NULL.
+ * Scores, sums and outputs are held in fp32; exp(x_t) times the scale of v_t
+ * is rounded to fp16 before it is multiplied by v_t's codes, so an output is
+ * within 2^-11 (sum_t p_t |v_t|) + 2^-11 |out| of the exact value, and a
+ * little more for the fp32 sums.  Deterministic.
+ * workspace: pn_attention_workspace_bytes() bytes, 256-byte aligned, zeroed
+ * once (pn_workspace_init); every completed call leaves its counters zeroed.
+ * pn_workspace_status reads its status word.  Calls that share a workspace
+ * must be ordered on one stream.  q, cache and out 16-byte aligned, q_stride a
+ * multiple of 8.
+ */
+size_t pn_attention_workspace_bytes(void);
+pn_status pn_attention(const uint16_t* q, int64_t q_stride, int64_t tokens, int heads, const void* cache,
+                       int64_t pages, int page_size, int kv_heads, int head_dim, const int32_t* table,
+                       int64_t table_stride, int max_pages, const int32_t* lens, const int32_t* starts, int batch,
+                       int max_queries, float scale, int window, int sinks, uint16_t* out, float* lse,
+                       void* workspace, size_t workspace_bytes, pn_stream stream);
+
+/*
+ * pn_verify: speculative verification.  For request b < batch with counts[b]
+ * (NULL: drafts) of at most `drafts` (0 .. PN_MAX_DRAFTS) drafted tokens
+ * tokens[b][i], target probabilities target[b][i] (fp32 rows of vocab values,
+ * row b * (drafts + 1) + i at target_stride elements), the draft model's
+ * draft[b][i] (row b * drafts + i; NULL: each draft was certain, q = 1 at its
+ * token) and random numbers uniforms[b][drafts + 1] in [0, 1):
+ *   draft i is accepted while uniforms[b][i] * q_i(token) < p_i(token)
+ *   (fp32; a token outside the vocabulary is turned down);
+ *   accepted[b] is the number n of them;
+ *   out[b][0 .. n - 1] the accepted tokens, out[b][n] one more, -1 behind it.
+ * The last token is the lowest index whose cumulated weight passes
+ * floor(uniforms[b][drafts] * total), the weights being those of row n: p
+ * after the last draft, max(p - q, 0) where draft n was turned down (p itself
+ * should that leave nothing), each limited to [0, 1] (NaN: 0) and rounded to a
+ * whole multiple of 2^-42, so that the token does not depend on the order of
+ * the sums.  -1 if the whole row weighs nothing.
+ */
+#define PN_MAX_DRAFTS 31
+#define PN_MAX_VOCAB (1 << 20)
+pn_status pn_verify(const int32_t* tokens, const float* target, int64_t target_stride, const float* draft,
+                    int64_t draft_stride, const float* uniforms, const int32_t* counts, int batch, int drafts,
+                    int vocab, int32_t* accepted, int32_t* out, pn_stream stream);
+
+/*
  * pn_read_ranges (diagnostic): the plain read-bandwidth ceiling a GEMV is
  * measured against.  Reads the first floor(bytes[i] / 16) * 16 bytes of each
  * of `count` (1 .. PN_MAX_LAYER) device ranges ptrs[i] once, with 16-byte
