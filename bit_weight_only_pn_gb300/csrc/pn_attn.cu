@@ -4,15 +4,24 @@
 // cached tokens t, out = sum_t exp(x_t) v_t / sum_t exp(x_t), lse = ln sum_t
 // exp(x_t), with k_t, v_t the cache's exact values d (n - 8).
 //
-// One pass over the cache.  A row of K is multiplied as the whole numbers
-// n - 8 (exact in fp16) and each group's fp32 sum by its scale afterwards; the
-// scales of V go into the probabilities, so V's codes are whole numbers in
-// their product too.  The products run on mma.sync with the cache as the A
-// operand: S^T = K Q^T (16 tokens x 8 query rows), O^T += V^T P^T (16 values x
-// 8 query rows).  The 8 columns are the query heads that share the key/value
-// head and the step's tokens, so a decode step wastes few of them, and the
-// words of a record are stored in the order in which the fragments take them
-// (pn_kv.cuh): a code costs one LOP3 + one HFMA2 per pair and nothing else.
+// One pass over the cache.  The codes enter the products as they are: four
+// bits masked out of a word are the fp16 number n 2^-24 (n 2^-20 for the upper
+// four of a byte), a subnormal, which the tensor cores multiply exactly.  So
+// two codes cost one LOP3 (and a shift for every other pair), no conversion.
+//   S: sum_d q_d (n_d - 8) = sum_d q_d n_d - 8 sum_d q_d: the second sum is
+//   taken once per row and group and is the accumulator's first value; each
+//   group's sum is multiplied by its scale in fp32.  The queries of a row are
+//   multiplied by a power of two so that the largest lies in [2^10, 2^11), and
+//   those that meet a lower four bits by 16 more.
+//   O: the scales of V go into the probabilities, and 8 is taken off the codes
+//   before the product (one HADD2 per pair, exact): with the 8 in the sums a
+//   sharp softmax over a token whose value is 0 would leave 2^-20 of its scale
+//   in place of the other tokens' share.
+// The products run on mma.sync with the cache as the A operand: S^T = K Q^T
+// (16 tokens x 8 query rows), O^T += V^T P^T (16 values x 8 query rows).  The
+// 8 columns are the query heads that share the key/value head and the step's
+// tokens, so a decode step wastes few of them, and the words of a record are
+// stored in the order in which the fragments take them (pn_kv.cuh).
 //
 // Probabilities are rounded to fp16 once, after the scale of V is multiplied
 // in: p d with p = 2^(x' - m), x' = x log2 e.  The reference m of a row is the
@@ -41,7 +50,7 @@
 namespace pn {
 namespace {
 
-constexpr int kTile = 64;                      // tokens per unit
+constexpr int kTile = 32;                      // tokens per unit
 constexpr int kTileRecords = kTile / kKvTokens;
 constexpr int kWarps = 7;                      // consumer warps; with the producer 8, so two blocks leave each thread 128 registers
 constexpr int kThreads = (kWarps + 1) * 32;
@@ -49,6 +58,8 @@ constexpr int kMinUnits = 2;                   // fewest units per thread block
 constexpr int kSlotFloats = 2048 + 32;         // a partial result: rows x D values (2048 at most), then (reference, sum) per row
 constexpr int kCtasPerSm = 2;
 constexpr int kJoinPitch = 72;                 // floats per row of the join buffer: conflict-free for the fragments' stores
+constexpr uint32_t kIssued = 1u << 8;          // marks beside a stage's records: its copy was started,
+constexpr uint32_t kOddTurn = 1u << 9;         // in an odd turn of the ring
 constexpr uint32_t kStatusTimeout = 5;         // PN_ETIMEOUT
 constexpr uint64_t kDrainLimitNs = 200ull * 1000 * 1000;
 
@@ -85,13 +96,17 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// Polls: a thread parked in mbarrier.try_wait notices a completed phase late.
 __device__ bool wait_phase(uint32_t bar, uint32_t parity, uint64_t limit_ns, volatile uint32_t* abort) {
-    if (mbar_try_wait(bar, parity)) return true;
-    const uint64_t t0 = globaltimer_ns();
+    uint64_t t0 = 0;
     for (;;) {
-        if (mbar_wait_suspend(bar, parity, 2000)) return true;
+#pragma unroll 1
+        for (int i = 0; i < 128; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
         if (abort && *abort) return false;
-        if (globaltimer_ns() - t0 > limit_ns) return false;
+        const uint64_t now = globaltimer_ns();
+        if (t0 == 0) t0 = now;
+        else if (now - t0 > limit_ns) return false;
     }
 }
 
@@ -129,6 +144,14 @@ __device__ __forceinline__ Request request_of(const AttnParams& P, int b) {
     return r;
 }
 
+// Unit v of a request: (head, row group, place among its tiles).
+__device__ __forceinline__ void locate(uint32_t v, const Request& r, int& h, int& rg, int& idx) {
+    const uint32_t seg = v / static_cast<uint32_t>(r.tiles);
+    idx = static_cast<int>(v - seg * r.tiles);
+    h = static_cast<int>(seg / static_cast<uint32_t>(r.row_groups));
+    rg = static_cast<int>(seg - h * r.row_groups);
+}
+
 template <int D>
 struct Shape {
     static constexpr int kGroups = D / 64;             // groups of 64 values (one scale each)
@@ -137,7 +160,9 @@ struct Shape {
     static constexpr int kRecord = kv_record_bytes(D);
     static constexpr int kStage = kTileRecords * kRecord;
     static constexpr int kPlaneBytes = 256 * kPlaneGroups;     // 8 tokens of a plane
-    static constexpr int kStages = D == 256 ? 5 : D == 128 ? 9 : 16;
+    // a multiple of kWarps, so that a stage is always read by the same warp
+    // (whose wait can then not mistake a phase for the one before last)
+    static constexpr int kStages = kWarps * (D == 256 ? 2 : D == 128 ? 3 : 4);
 };
 
 template <int D, int NT>
@@ -148,17 +173,41 @@ struct Smem {
     static constexpr int kMl = kJoin + kWarps * kRT * kJoinPitch * 4;      // [warps][rows] (reference, sum)
     static constexpr int kFinal = kMl + kWarps * kRT * 8;                  // [rows] (reference, sum)
     static constexpr int kBars = kFinal + kRT * 8;                         // full, empty
-    static constexpr int kValid = kBars + 2 * Shape<D>::kStages * 8;       // per stage: records that hold data
+    static constexpr int kValid = kBars + 2 * Shape<D>::kStages * 8;       // per stage: records that hold data, marks of its last copy
     static constexpr int kMisc = kValid + Shape<D>::kStages * 4;           // abort, last-block flag
-    static constexpr int kScan = (kMisc + 8 + 7) / 8 * 8;                  // the warps' sums, then [batch + 1] prefix sums of units
-    static constexpr int kFixed = kScan + (kWarps + 1) * 8;
-    static int bytes(int batch) { return kFixed + (batch + 1) * 8; }
+    static constexpr int kScan = kMisc + 8;                                // the warps' sums, then [batch + 1] prefix sums of units
+    static constexpr int kFixed = kScan + (kWarps + 1) * 4;
+    static int bytes(int batch) { return kFixed + (batch + 1) * 4; }
 };
 
-// The four scale-free codes of two tokens' words a, b: halves (token a, token b).
-// `odd` selects codes 1, 3, 5, 7.
+// Halves (code of token a, code of token b) of two tokens' words: the even
+// codes 0, 2, 4, 6 at bits 0, 4, 8, 12 of each half, or the odd ones.
 __device__ __forceinline__ uint32_t token_pair(uint32_t a, uint32_t b, bool odd) {
     return __byte_perm(a, b, odd ? 0x7632 : 0x5410);
+}
+
+// Pair I (0 .. 3) of four code pairs at bits 0, 4, 8, 12 of a word's halves, as
+// fp16 numbers: n 2^-24 for I even, n 2^-20 for I odd.  `shifted` = word >> 8.
+template <int I>
+__device__ __forceinline__ uint32_t raw_pair(uint32_t word, uint32_t shifted) {
+    return (I >= 2 ? shifted : word) & (I & 1 ? 0x00F000F0u : 0x000F000Fu);
+}
+
+// The same less 8: (n - 8) 2^-24 or (n - 8) 2^-20.
+template <int I>
+__device__ __forceinline__ uint32_t value_pair(uint32_t word, uint32_t shifted) {
+    uint32_t d;
+    asm("add.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(raw_pair<I>(word, shifted)), "r"(I & 1 ? 0x80808080u : 0x80088008u));
+    return d;
+}
+
+// D = C + A * B, m16n8k16, fp16 inputs, fp32 accumulate.
+__device__ __forceinline__ void mma_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1, float c0, float c1, float c2, float c3) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
 template <int N>
@@ -177,16 +226,38 @@ __device__ __forceinline__ void load_scales(const uint8_t* p, float (&d)[N]) {
 // Running state of a warp's share of a segment.  Lane (g, t) holds, for query
 // columns 8 nt + 2t + c, the reference and its part of the sum, and of O the
 // values 64 j + 8 g + 2 i (o[..][c]) and + 1 (o[..][2 + c]) for i = 0 .. 3.
+// o is in units of 2^-24 (i even) and 2^-20 (i odd).
 template <int D, int NT>
 struct State {
     float ref[NT][2];
     float sum[NT][2];
     float o[NT][D / 16][4];
+
+    __device__ __forceinline__ void scale_by(int n, float f0, float f1) {
+#pragma unroll
+        for (int m = 0; m < D / 16; ++m) {
+            o[n][m][0] *= f0;
+            o[n][m][1] *= f1;
+            o[n][m][2] *= f0;
+            o[n][m][3] *= f1;
+        }
+    }
+};
+
+// A row group's queries: lane (g, t) holds the B fragments of row 8 nt + g, and
+// for its columns' rows 8 nt + 2t + c what the products start from and the
+// factor from a product to the score times log2 e.
+template <int D, int NT>
+struct Queries {
+    uint2 q[NT][D / 64][2][2];                 // [group][word of the lane's pair][MMA]
+    float start[NT][D / 64][2];
+    float factor[NT][2];
+    int pos[NT][2];
 };
 
 template <int D, int NT, bool kMasked>
-__device__ __forceinline__ void take_tile(const uint8_t* stage, int tok0, uint32_t valid, const uint2 (&q)[NT][D / 64][2][2],
-                                          const int (&pos)[NT][2], int window, int sinks, float scale, State<D, NT>& st) {
+__device__ __forceinline__ void take_tile(const uint8_t* stage, int tok0, uint32_t valid, const Queries<D, NT>& Q, int window,
+                                          int sinks, State<D, NT>& st) {
     using S = Shape<D>;
     constexpr int NG = S::kGroups, GP = S::kPlaneGroups, PL = S::kPlanes;
     const int lane = threadIdx.x & 31, g = lane >> 2;
@@ -222,18 +293,17 @@ __device__ __forceinline__ void take_tile(const uint8_t* stage, int tok0, uint32
                 const int j = pl * GP + jj;
                 float acc[NT][4];
 #pragma unroll
-                for (int n = 0; n < NT; ++n) acc[n][0] = acc[n][1] = acc[n][2] = acc[n][3] = 0.0f;
-#pragma unroll
                 for (int w = 0; w < 2; ++w) {
                     const uint32_t a = w0[2 * jj + w], b = w1[2 * jj + w], as = a >> 8, bs = b >> 8;
-                    const uint32_t a0 = decode_pair<kPn4t, 0>(a, as), a1 = decode_pair<kPn4t, 0>(b, bs);
-                    const uint32_t a2 = decode_pair<kPn4t, 1>(a, as), a3 = decode_pair<kPn4t, 1>(b, bs);
-                    const uint32_t b0 = decode_pair<kPn4t, 2>(a, as), b1 = decode_pair<kPn4t, 2>(b, bs);
-                    const uint32_t b2 = decode_pair<kPn4t, 3>(a, as), b3 = decode_pair<kPn4t, 3>(b, bs);
+                    const uint32_t a0 = raw_pair<0>(a, as), a1 = raw_pair<0>(b, bs), a2 = raw_pair<1>(a, as), a3 = raw_pair<1>(b, bs);
+                    const uint32_t b0 = raw_pair<2>(a, as), b1 = raw_pair<2>(b, bs), b2 = raw_pair<3>(a, as), b3 = raw_pair<3>(b, bs);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        mma_16816(acc[n], a0, a1, a2, a3, q[n][j][w][0].x, q[n][j][w][0].y);
-                        mma_16816(acc[n], b0, b1, b2, b3, q[n][j][w][1].x, q[n][j][w][1].y);
+                        const float s0 = Q.start[n][j][0], s1 = Q.start[n][j][1];
+                        const uint2 u = Q.q[n][j][w][0], v = Q.q[n][j][w][1];
+                        if (w == 0) mma_from(acc[n], a0, a1, a2, a3, u.x, u.y, s0, s1, s0, s1);
+                        else mma_16816(acc[n], a0, a1, a2, a3, u.x, u.y);
+                        mma_16816(acc[n], b0, b1, b2, b3, v.x, v.y);
                     }
                 }
 #pragma unroll
@@ -267,7 +337,7 @@ __device__ __forceinline__ void take_tile(const uint8_t* stage, int tok0, uint32
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         const int tok = tok0 + r * kKvTokens + hh * 8 + g;
-                        const bool s = ((valid >> r) & 1) && tok <= pos[n][c] && (tok > pos[n][c] - window || tok < sinks);
+                        const bool s = ((valid >> r) & 1) && tok <= Q.pos[n][c] && (tok > Q.pos[n][c] - window || tok < sinks);
                         seen |= static_cast<uint32_t>(s) << (((r * 2 + hh) * NT + n) * 2 + c);
                     }
     }
@@ -280,7 +350,7 @@ __device__ __forceinline__ void take_tile(const uint8_t* stage, int tok0, uint32
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const float y = fmaf(x[r][n][2 * hh + c], scale, e[r][hh]);
+                    const float y = fmaf(x[r][n][2 * hh + c], Q.factor[n][c], e[r][hh]);
                     top[n][c] = fmaxf(top[n][c], sees(r, hh, n, c) ? y : -INFINITY);
                 }
     bool moved = false;
@@ -304,13 +374,7 @@ __device__ __forceinline__ void take_tile(const uint8_t* stage, int tok0, uint32
                 st.ref[n][c] = to;
                 st.sum[n][c] *= f[c];
             }
-#pragma unroll
-            for (int m = 0; m < D / 16; ++m) {
-                st.o[n][m][0] *= f[0];
-                st.o[n][m][1] *= f[1];
-                st.o[n][m][2] *= f[0];
-                st.o[n][m][3] *= f[1];
-            }
+            st.scale_by(n, f[0], f[1]);
         }
     }
 #pragma unroll
@@ -322,7 +386,7 @@ __device__ __forceinline__ void take_tile(const uint8_t* stage, int tok0, uint32
             for (int hh = 0; hh < 2; ++hh)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
-                    const float p = ex2(fmaf(x[r][n][2 * hh + c], scale, -st.ref[n][c]));
+                    const float p = ex2(fmaf(x[r][n][2 * hh + c], Q.factor[n][c], -st.ref[n][c]));
                     x[r][n][2 * hh + c] = sees(r, hh, n, c) ? p : 0.0f;
                     st.sum[n][c] += x[r][n][2 * hh + c];
                 }
@@ -364,8 +428,8 @@ __device__ __forceinline__ void take_tile(const uint8_t* stage, int tok0, uint32
                 const uint32_t e0s = e0 >> 8, o0s = o0 >> 8, e1s = e1 >> 8, o1s = o1 >> 8;
                 static_for<4>([&](auto ic) {
                     constexpr int I = decltype(ic)::value;
-                    const uint32_t a0 = decode_pair<kPn4t, I>(e0, e0s), a1 = decode_pair<kPn4t, I>(o0, o0s);
-                    const uint32_t a2 = decode_pair<kPn4t, I>(e1, e1s), a3 = decode_pair<kPn4t, I>(o1, o1s);
+                    const uint32_t a0 = value_pair<I>(e0, e0s), a1 = value_pair<I>(o0, o0s);
+                    const uint32_t a2 = value_pair<I>(e1, e1s), a3 = value_pair<I>(o1, o1s);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) mma_16816(st.o[n][4 * j + I], a0, a1, a2, a3, b[n][0], b[n][1]);
                 });
@@ -381,13 +445,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && D <= 128 ? 2 : 1) attn_ke
     constexpr int RT = 8 * NT, NG = S::kGroups, kStages = S::kStages;
     extern __shared__ __align__(128) uint8_t smem[];
     const uint32_t base = smem_addr(smem);
-    auto full = [&](int s) { return base + M::kBars + 8u * s; };
-    auto empty = [&](int s) { return base + M::kBars + 8u * (kStages + s); };
+    auto full = [&](uint32_t s) { return base + M::kBars + 8u * s; };
+    auto empty = [&](uint32_t s) { return base + M::kBars + 8u * (kStages + s); };
     volatile uint32_t* valid = reinterpret_cast<volatile uint32_t*>(smem + M::kValid);
     volatile uint32_t* abort = reinterpret_cast<volatile uint32_t*>(smem + M::kMisc);
     volatile uint32_t* last_flag = abort + 1;
-    int64_t* warp_sums = reinterpret_cast<int64_t*>(smem + M::kScan);
-    int64_t* prefix = reinterpret_cast<int64_t*>(smem + M::kFixed);      // [batch + 1]
+    uint32_t* warp_sums = reinterpret_cast<uint32_t*>(smem + M::kScan);
+    uint32_t* prefix = reinterpret_cast<uint32_t*>(smem + M::kFixed);    // [batch + 1]
     const AttnArgs& a = P.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int heads = P.cache.heads;
@@ -396,6 +460,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && D <= 128 ? 2 : 1) attn_ke
         for (int s = 0; s < kStages; ++s) {
             mbar_init(full(s), 1);
             mbar_init(empty(s), 1);
+            valid[s] = 0u;
         }
         *abort = 0u;
         fence_mbar_init();
@@ -404,34 +469,41 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && D <= 128 ? 2 : 1) attn_ke
     {
         const int each = (a.batch + kThreads - 1) / kThreads;
         const int b0 = min(static_cast<int>(threadIdx.x) * each, a.batch), b1 = min(b0 + each, a.batch);
-        int64_t mine = 0;
+        uint32_t mine = 0;
         for (int b = b0; b < b1; ++b) {
             const Request r = request_of<RT>(P, b);
-            mine += static_cast<int64_t>(r.tiles) * r.row_groups * heads;
+            mine += static_cast<uint32_t>(r.tiles) * r.row_groups * heads;
         }
-        int64_t in = mine;
+        uint32_t in = mine;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
-            const int64_t o = __shfl_up_sync(0xFFFFFFFFu, in, d);
+            const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, in, d);
             if (lane >= d) in += o;
         }
         if (lane == 31) warp_sums[warp] = in;
         __syncthreads();
-        int64_t at = in - mine;
+        uint32_t at = in - mine;
         for (int w = 0; w < warp; ++w) at += warp_sums[w];
         for (int b = b0; b < b1; ++b) {
             prefix[b] = at;
-            const Request r = request_of<RT>(P, b);
-            at += static_cast<int64_t>(r.tiles) * r.row_groups * heads;
+            if (b + 1 < b1) {
+                const Request r = request_of<RT>(P, b);
+                at += static_cast<uint32_t>(r.tiles) * r.row_groups * heads;
+            }
         }
-        if (threadIdx.x == kThreads - 1) prefix[a.batch] = at;
+        if (threadIdx.x == kThreads - 1) {
+            uint32_t all = 0;
+            for (int w = 0; w <= kWarps; ++w) all += warp_sums[w];
+            prefix[a.batch] = all;
+        }
         __syncthreads();
     }
-    const int64_t total = prefix[a.batch];
-    const int64_t blocks = min(static_cast<int64_t>(gridDim.x), (total + kMinUnits - 1) / kMinUnits);
-    if (static_cast<int64_t>(blockIdx.x) >= blocks) return;              // nothing of this block is in flight
-    const int64_t u0 = total * blockIdx.x / blocks, u1 = total * (blockIdx.x + 1) / blocks;
-    auto request_at = [&](int64_t u) {                                   // the request that holds unit u
+    const uint32_t total = prefix[a.batch];                              // below 2^32: checked on the host
+    const uint32_t blocks = min(gridDim.x, (total + kMinUnits - 1) / kMinUnits);
+    if (blockIdx.x >= blocks) return;                                    // nothing of this block is in flight
+    const uint32_t u0 = static_cast<uint32_t>(static_cast<uint64_t>(total) * blockIdx.x / blocks);
+    const uint32_t u1 = static_cast<uint32_t>(static_cast<uint64_t>(total) * (blockIdx.x + 1) / blocks);
+    auto request_at = [&](uint32_t u) {                                  // the request that holds unit u
         int lo = 0, hi = a.batch - 1;
         while (lo < hi) {
             const int mid = (lo + hi + 1) >> 1;
@@ -443,71 +515,89 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && D <= 128 ? 2 : 1) attn_ke
 
     if (warp == kWarps) {
         // ------------------------------------------------------- producer --
-        int64_t issued = 0;
-        bool stop = false;
-        for (int64_t batch0 = u0; batch0 < u1 && !stop; batch0 += 32) {
-            // each lane prepares one unit: its cache pages
-            const int64_t u = batch0 + lane;
-            const uint8_t* src[kTileRecords] = {nullptr, nullptr, nullptr, nullptr};
-            int records = 0;
-            uint32_t have = 0;
-            if (u < u1) {
-                const int b = request_at(u);
-                const Request r = request_of<RT>(P, b);
-                const int64_t v = u - prefix[b];
-                const int idx = static_cast<int>(v % r.tiles);
-                const int h = static_cast<int>(v / (static_cast<int64_t>(r.tiles) * r.row_groups));
-                const int tile = idx < r.sink_tiles ? idx : r.lo_tile + idx - r.sink_tiles;
-                records = min(max((r.len - tile * kTile + kKvTokens - 1) / kKvTokens, 0), kTileRecords);
+        // Each lane serves every kLanes-th unit: it looks up the next one's
+        // pages while it waits for the current one's stage.
+        constexpr int kLanes = kStages < 16 ? 8 : 16;
+        struct Copy {
+            const uint8_t* src[kTileRecords];  // records, or (pages that hold the whole tile) the first one alone
+            uint32_t have;                     // records that a page holds
+        };
+        const bool one_page = P.cache.page_size >= kTile;
+        auto prepare = [&](uint32_t n) {       // unit u0 + n
+            Copy c{};
+            if (n >= u1 - u0) return c;
+            const uint32_t u = u0 + n;
+            const int b = request_at(u);
+            const Request r = request_of<RT>(P, b);
+            int h, rg, idx;
+            locate(u - prefix[b], r, h, rg, idx);
+            const int tile = idx < r.sink_tiles ? idx : r.lo_tile + idx - r.sink_tiles;
+            const int records = min(max((r.len - tile * kTile + kKvTokens - 1) / kKvTokens, 0), kTileRecords);
+            const int32_t* row = a.table + static_cast<int64_t>(b) * a.table_stride;
 #pragma unroll
-                for (int i = 0; i < kTileRecords; ++i) {
-                    if (i >= records) break;
-                    const int tok = tile * kTile + i * kKvTokens;
-                    const int page = a.table[static_cast<int64_t>(b) * a.table_stride + (tok >> P.cache.page_shift)];
-                    if (page < 0 || page >= P.cache.pages) continue;     // no such page: its tokens are not seen
-                    src[i] = P.cache.record((static_cast<int64_t>(page) << P.cache.page_shift) + (tok & (P.cache.page_size - 1)), h);
-                    have |= 1u << i;
-                }
+            for (int i = 0; i < kTileRecords; ++i) {
+                if (i >= records || (i > 0 && one_page)) break;
+                const int tok = tile * kTile + i * kKvTokens;
+                const int page = row[tok >> P.cache.page_shift];
+                if (page < 0 || page >= P.cache.pages) continue;         // no such page: its tokens are not seen
+                c.src[i] = P.cache.record((static_cast<int64_t>(page) << P.cache.page_shift) + (tok & (P.cache.page_size - 1)), h);
+                c.have |= one_page ? (1u << records) - 1 : 1u << i;
             }
-            const int count = static_cast<int>(min(static_cast<int64_t>(32), u1 - batch0));
-            for (int i = 0; i < count && !stop; ++i) {
-                const int64_t it = issued + i;
-                const int s = static_cast<int>(it % kStages);
-                if (lane == i) {
-                    if (it >= kStages && !wait_phase(empty(s), static_cast<uint32_t>(it / kStages - 1) & 1u, P.timeout_ns, abort)) {
-                        *abort = 1u;
-                        atomicCAS(P.status, 0u, kStatusTimeout);
-                        stop = true;
-                    } else {
-                        const uint32_t dst = base + s * S::kStage;
-                        valid[s] = have;
-                        mbar_arrive_expect_tx(full(s), __popc(have) * S::kRecord);
-                        // runs of records that follow each other in memory go in one copy
-                        // (testing aid: with stall the first unit's bytes are announced but
-                        // never copied; its wait can only time out)
-                        for (int k = P.stall && it == 0 ? kTileRecords : 0; k < kTileRecords;) {
-                            if (!((have >> k) & 1)) { ++k; continue; }
-                            int e = k + 1;
-                            while (e < kTileRecords && ((have >> e) & 1) && src[e] == src[k] + (e - k) * S::kRecord) ++e;
-                            bulk_g2s(dst + k * S::kRecord, src[k], (e - k) * S::kRecord, full(s));
-                            k = e;
-                        }
+            return c;
+        };
+        const uint32_t count = u1 - u0;
+        uint32_t s = lane, turn = 0;           // the lane's stage, and how often the ring has gone round
+        bool ok = true;
+        Copy cur = prepare(lane);
+        // The lanes go on together: a wait tells a phase from the one before it,
+        // not from the one before that, so no lane may be a whole ring ahead of
+        // another (kLanes <= kStages keeps the stages of one pass apart).
+        for (uint32_t n = 0; n < count; n += kLanes) {
+            const bool mine = lane < kLanes && n + lane < count;
+            const Copy next = lane < kLanes ? prepare(n + lane + kLanes) : Copy{};
+            // each lane copies as soon as its own stage is free
+            bool done = !mine;
+            uint64_t t0 = 0;
+            for (uint32_t polls = 1;; ++polls) {
+                if (!done && (turn == 0 || mbar_try_wait(empty(s), (turn - 1) & 1u))) {
+                    const uint32_t dst = base + s * S::kStage;
+                    // (testing aid: with stall the first unit's bytes are announced but
+                    // never copied; its wait can only time out)
+                    const bool copied = !(P.stall && n + lane == 0);
+                    valid[s] = cur.have | (copied ? kIssued : 0u) | ((turn & 1u) ? kOddTurn : 0u);
+                    mbar_arrive_expect_tx(full(s), __popc(cur.have) * S::kRecord);
+                    if (copied && one_page) {
+                        if (cur.have) bulk_g2s(dst, cur.src[0], __popc(cur.have) * S::kRecord, full(s));
+                    } else if (copied) {
+#pragma unroll
+                        for (int i = 0; i < kTileRecords; ++i)
+                            if ((cur.have >> i) & 1) bulk_g2s(dst + i * S::kRecord, cur.src[i], S::kRecord, full(s));
                     }
+                    done = true;
                 }
-                stop = __shfl_sync(0xFFFFFFFFu, stop, i);
-                if (stop) { issued += i; break; }
+                if (__all_sync(0xFFFFFFFFu, done)) break;
+                if (polls % 256 == 0) {
+                    const uint64_t now = globaltimer_ns();
+                    if (t0 == 0) t0 = now;
+                    ok = !*abort && now - t0 <= P.timeout_ns;
+                    if (__any_sync(0xFFFFFFFFu, !ok)) break;
+                }
             }
-            if (!stop) issued += count;
-        }
-        // every copy lands before the block ends, also after an abort
-        if (lane == 0) {
-            for (int s = 0; s < kStages; ++s) {
-                if (issued <= s) continue;
-                const int64_t last = s + kStages * ((issued - 1 - s) / kStages);
-                if (P.stall && last == 0) continue;                      // never copied
-                wait_phase(full(s), static_cast<uint32_t>(last / kStages) & 1u, kDrainLimitNs, nullptr);
+            if (__any_sync(0xFFFFFFFFu, !ok)) {
+                if (lane == 0) {
+                    *abort = 1u;
+                    atomicCAS(P.status, 0u, kStatusTimeout);
+                }
+                break;
             }
+            cur = next;
+            s += kLanes;
+            if (s >= kStages) { s -= kStages; ++turn; }
         }
+        __syncwarp();
+        // the last copy into every stage lands before the block ends, also after an abort
+        if (lane < kStages && (valid[lane] & kIssued))
+            wait_phase(full(lane), valid[lane] & kOddTurn ? 1u : 0u, kDrainLimitNs, nullptr);
         return;
     }
 
@@ -516,20 +606,21 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && D <= 128 ? 2 : 1) attn_ke
     float* join = reinterpret_cast<float*>(smem + M::kJoin);
     float2* ml = reinterpret_cast<float2*>(smem + M::kMl);
     float2* fin = reinterpret_cast<float2*>(smem + M::kFinal);
-    int64_t it0 = 0;
+    uint32_t it0 = 0;
     bool alive = true;
-    for (int64_t u = u0; u < u1;) {
+    for (uint32_t u = u0; u < u1;) {
         const int b = request_at(u);
         const Request r = request_of<RT>(P, b);
-        const int64_t v = u - prefix[b];
-        const int first = static_cast<int>(v % r.tiles);
-        const int64_t seg = v / r.tiles;
-        const int rg = static_cast<int>(seg % r.row_groups), h = static_cast<int>(seg / r.row_groups);
-        const int64_t seg_u0 = u - first;
-        const int count = static_cast<int>(min(static_cast<int64_t>(r.tiles - first), u1 - u));
+        int h, rg, first;
+        locate(u - prefix[b], r, h, rg, first);
+        const uint32_t seg_u0 = u - first;
+        const int count = static_cast<int>(min(static_cast<uint32_t>(r.tiles - first), u1 - u));
         const bool whole = count == r.tiles;
         const int row0 = rg * RT;
+        // unit it of the block goes to warp it % kWarps; `part` numbers the
+        // warps that have some of the segment, from its first unit on
         const int active = min(count, kWarps);
+        const int part = static_cast<int>((warp + kWarps - it0 % kWarps) % kWarps);
 
         State<D, NT> st;
 #pragma unroll
@@ -539,33 +630,67 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && D <= 128 ? 2 : 1) attn_ke
 #pragma unroll
             for (int m = 0; m < D / 16; ++m) st.o[n][m][0] = st.o[n][m][1] = st.o[n][m][2] = st.o[n][m][3] = 0.0f;
         }
-        if (warp < active) {
-            uint2 q[NT][NG][2][2];
-            int pos[NT][2];
+        if (part < active) {
+            Queries<D, NT> Q;
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 const int row = min(row0 + 8 * n + g, r.rows - 1);
                 const int qi = row / P.group;
                 const __half* src = a.q + (r.q0 + qi) * a.q_stride + (h * P.group + row - qi * P.group) * D;
+                uint4 f[NG][2];
+                uint32_t top = 0;              // the row's largest |q|, as bits: both halves of a register at once
 #pragma unroll
                 for (int j = 0; j < NG; ++j)
 #pragma unroll
                     for (int w = 0; w < 2; ++w) {
-                        const uint4 f = *reinterpret_cast<const uint4*>(src + 64 * j + 16 * t + 8 * w);
-                        q[n][j][w][0] = make_uint2(f.x, f.y);
-                        q[n][j][w][1] = make_uint2(f.z, f.w);
-                    }
+                        f[j][w] = *reinterpret_cast<const uint4*>(src + 64 * j + 16 * t + 8 * w);
+                        const uint32_t v[4] = {f[j][w].x, f[j][w].y, f[j][w].z, f[j][w].w};
 #pragma unroll
-                for (int c = 0; c < 2; ++c) pos[n][c] = r.pos0 + min(row0 + 8 * n + 2 * t + c, r.rows - 1) / P.group;
+                        for (int i = 0; i < 4; ++i) top = __vmaxu2(top, v[i] & 0x7FFF7FFFu);
+                    }
+                top = max(top & 0xFFFFu, top >> 16);
+                top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+                top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+                const int e = 25 - static_cast<int>(max(top >> 10, 1u));         // the largest |q| 2^e lies in [2^10, 2^11)
+                const float up = __int_as_float((127 + e) << 23);
+                float sum[NG];
+#pragma unroll
+                for (int j = 0; j < NG; ++j) {
+                    sum[j] = 0.0f;
+#pragma unroll
+                    for (int w = 0; w < 2; ++w) {
+                        const uint32_t v[4] = {f[j][w].x, f[j][w].y, f[j][w].z, f[j][w].w};
+                        uint32_t to[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const float a0 = half_bits_to_float(v[i] & 0xFFFFu) * up, a1 = half_bits_to_float(v[i] >> 16) * up;
+                            sum[j] += a0 + a1;
+                            to[i] = i & 1 ? pack_half2(a0, a1) : pack_half2(16.0f * a0, 16.0f * a1);
+                        }
+                        Q.q[n][j][w][0] = make_uint2(to[0], to[1]);
+                        Q.q[n][j][w][1] = make_uint2(to[2], to[3]);
+                    }
+                    sum[j] += __shfl_xor_sync(0xFFFFFFFFu, sum[j], 1);
+                    sum[j] += __shfl_xor_sync(0xFFFFFFFFu, sum[j], 2);
+                }
+                const float back = P.scale_log2 * __int_as_float((127 + 20 - e) << 23);
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    // the columns' rows are those of lanes (2t + c, .)
+                    const int from = (2 * t + c) << 2;
+#pragma unroll
+                    for (int j = 0; j < NG; ++j) Q.start[n][j][c] = -0x1p-17f * __shfl_sync(0xFFFFFFFFu, sum[j], from);   // -8 * 2^-20
+                    Q.factor[n][c] = __shfl_sync(0xFFFFFFFFu, back, from);
+                    Q.pos[n][c] = r.pos0 + min(row0 + 8 * n + 2 * t + c, r.rows - 1) / P.group;
+                }
             }
             const int pos_lo = r.pos0 + row0 / P.group;
             const int pos_hi = r.pos0 + min(row0 + RT - 1, r.rows - 1) / P.group;
             const int window = a.window ? a.window : INT32_MAX;
-            for (int k = warp; k < count; k += kWarps) {
-                const int64_t it = it0 + k;
-                const int s = static_cast<int>(it % kStages);
+            for (int k = part; k < count; k += kWarps) {
+                const uint32_t it = it0 + k, s = it % kStages;
                 if (alive) {
-                    alive = wait_phase(full(s), static_cast<uint32_t>(it / kStages) & 1u, P.timeout_ns, abort);
+                    alive = wait_phase(full(s), (it / kStages) & 1u, P.timeout_ns, abort);
                     alive = __all_sync(0xFFFFFFFFu, alive);
                     if (!alive && lane == 0) {
                         *abort = 1u;
@@ -575,14 +700,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && D <= 128 ? 2 : 1) attn_ke
                 if (!alive) continue;
                 const int idx = first + k;
                 const int tok0 = (idx < r.sink_tiles ? idx : r.lo_tile + idx - r.sink_tiles) * kTile;
-                const uint32_t have = valid[s];
+                const uint32_t have = valid[s] & ((1u << kTileRecords) - 1);
                 const uint8_t* stage = smem + s * S::kStage;
                 if (tok0 > pos_hi) {
                     // no row sees this tile
                 } else if (have == (1u << kTileRecords) - 1 && tok0 + kTile - 1 <= pos_lo && (tok0 > pos_hi - window || tok0 + kTile <= a.sinks)) {
-                    take_tile<D, NT, false>(stage, tok0, have, q, pos, window, a.sinks, P.scale_log2, st);
+                    take_tile<D, NT, false>(stage, tok0, have, Q, window, a.sinks, st);
                 } else {
-                    take_tile<D, NT, true>(stage, tok0, have, q, pos, window, a.sinks, P.scale_log2, st);
+                    take_tile<D, NT, true>(stage, tok0, have, Q, window, a.sinks, st);
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(empty(s));
@@ -597,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && D <= 128 ? 2 : 1) attn_ke
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) ml[warp * RT + 8 * n + 2 * t + c] = make_float2(st.ref[n][c], st.sum[n][c]);
+                    for (int c = 0; c < 2; ++c) ml[part * RT + 8 * n + 2 * t + c] = make_float2(st.ref[n][c], st.sum[n][c]);
             }
         }
         consumers_sync();
@@ -611,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && D <= 128 ? 2 : 1) attn_ke
             }
             fin[threadIdx.x] = make_float2(m, l);
         }
-        if (warp < active) {
+        if (part < active) {
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 float f[2];
@@ -621,28 +746,28 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && D <= 128 ? 2 : 1) attn_ke
                     for (int w = 0; w < active; ++w) m = fmaxf(m, ml[w * RT + 8 * n + 2 * t + c].x);
                     f[c] = st.ref[n][c] == -INFINITY ? 0.0f : ex2(st.ref[n][c] - m);
                 }
+                st.scale_by(n, f[0], f[1]);
 #pragma unroll
-                for (int m = 0; m < D / 16; ++m) {
-                    st.o[n][m][0] *= f[0];
-                    st.o[n][m][1] *= f[1];
-                    st.o[n][m][2] *= f[0];
-                    st.o[n][m][3] *= f[1];
-                }
+                for (int m = 0; m < D / 16; ++m)
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+                        st.o[n][m][c] *= m & 1 ? 0x1p20f : 0x1p24f;
             }
         }
         // blocks that share the segment
-        const int64_t seg_u1 = seg_u0 + r.tiles;
-        auto block_of = [&](int64_t x) { return static_cast<int>(((x + 1) * blocks + total - 1) / total - 1); };
-        const int c_first = whole ? 0 : block_of(seg_u0), c_last = whole ? 0 : block_of(seg_u1 - 1);
+        auto block_of = [&](uint32_t x) {
+            return static_cast<int>(((static_cast<uint64_t>(x) + 1) * blocks + total - 1) / total - 1);
+        };
+        const int c_first = whole ? 0 : block_of(seg_u0), c_last = whole ? 0 : block_of(seg_u0 + r.tiles - 1);
         float* slot = P.partials + static_cast<int64_t>(2 * blockIdx.x + (first == 0 ? 1 : 0)) * kSlotFloats;
 #pragma unroll
         for (int j = 0; j < NG; ++j) {
-            if (warp < active) {
+            if (part < active) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        float* to = join + (warp * RT + 8 * n + 2 * t + c) * kJoinPitch + 8 * g;
+                        float* to = join + (part * RT + 8 * n + 2 * t + c) * kJoinPitch + 8 * g;
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
                             *reinterpret_cast<float2*>(to + 2 * i) = make_float2(st.o[n][4 * j + i][c], st.o[n][4 * j + i][2 + c]);
@@ -687,17 +812,17 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && D <= 128 ? 2 : 1) attn_ke
             if (*last_flag) {
                 __threadfence();
                 const float* parts = P.partials;
-                auto part = [&](int c) { return parts + static_cast<int64_t>(2 * c + (c == c_first ? 1 : 0)) * kSlotFloats; };
+                auto piece = [&](int c) { return parts + static_cast<int64_t>(2 * c + (c == c_first ? 1 : 0)) * kSlotFloats; };
                 for (int i = threadIdx.x; i < RT * (D / 2); i += kWarps * 32) {
                     const int row = i / (D / 2), d = (i % (D / 2)) * 2;
                     if (row0 + row >= r.rows) continue;
                     float m = -INFINITY, l = 0.0f;
 #pragma unroll 4
-                    for (int c = c_first; c <= c_last; ++c) m = fmaxf(m, __ldcg(part(c) + 2048 + 2 * row));
+                    for (int c = c_first; c <= c_last; ++c) m = fmaxf(m, __ldcg(piece(c) + 2048 + 2 * row));
                     float2 o = make_float2(0.0f, 0.0f);
 #pragma unroll 4
                     for (int c = c_first; c <= c_last; ++c) {
-                        const float* p = part(c);
+                        const float* p = piece(c);
                         const float2 f = __ldcg(reinterpret_cast<const float2*>(p + 2048 + 2 * row));
                         const float2 w = __ldcg(reinterpret_cast<const float2*>(p + row * D + d));
                         const float s = f.x == -INFINITY ? 0.0f : ex2(f.x - m);
@@ -747,6 +872,10 @@ cudaError_t launch_attention(const AttnArgs& a, const KvGeometry& g, void* works
                  reinterpret_cast<uint32_t*>(ws), reinterpret_cast<uint32_t*>(ws + 256),
                  reinterpret_cast<float*>(ws + 256 + (ctas * 4 + 255) / 256 * 256), timeout_ns, stall};
     // 8 or 16 query rows share the decoded codes
+    const int64_t rows = static_cast<int64_t>(a.max_queries) * P.group, per = g.D < 256 && rows > 8 ? 16 : 8;
+    const double units = static_cast<double>(a.batch) * g.heads * static_cast<double>((rows + per - 1) / per) *
+                         static_cast<double>((static_cast<int64_t>(a.max_pages) * g.page_size + kTile - 1) / kTile);
+    if (units >= 4294967296.0) return cudaErrorInvalidValue;
     const bool wide = static_cast<int64_t>(a.max_queries) * P.group > 8;
     if (g.D == 64) return wide ? launch<64, 2>(P, num_sms, s) : launch<64, 1>(P, num_sms, s);
     if (g.D == 128) return wide ? launch<128, 2>(P, num_sms, s) : launch<128, 1>(P, num_sms, s);
