@@ -29,15 +29,16 @@
 // p |d| stays below 2^15 whatever the scales are and keeps its 11 bits down to
 // 2^-28 of the largest.  Sums, maxima and outputs are held in fp32.
 //
-// Work split: the units (request, key/value head, row group, 64-token tile)
-// of a call are numbered in that order and every thread block takes one
-// contiguous range of them, so the cache bytes are shared evenly whatever the
-// lengths are.  A producer warp streams the tiles through a ring of bulk
-// copies; each consumer warp takes every W-th tile with accumulators of its
-// own; warps are joined through shared memory at the end of a segment
-// (request, head, row group), and segments that cross block boundaries
-// through the workspace, by the last block to arrive, in block order: results
-// do not depend on timing.
+// Work split: the units (request, key/value head, row group, 32-token tile) of
+// a call are numbered in that order and every consumer warp of the grid takes
+// one contiguous range of them, so the cache bytes are shared evenly whatever
+// the lengths are, and a warp keeps its accumulators for as long as a segment
+// (request, head, row group) lasts.  A producer warp fills each warp's own
+// ring of stages by bulk copies.  Segments that one warp has to itself go
+// straight to the output; the pieces of the others go through the workspace
+// (L2): a block joins its own warps' pieces when it is done, and the last
+// block to arrive joins those of several blocks, in unit order, so results do
+// not depend on timing.
 #include <cstdint>
 
 #include <cuda_fp16.h>
@@ -54,10 +55,7 @@ constexpr int kTile = 32;                      // tokens per unit
 constexpr int kTileRecords = kTile / kKvTokens;
 constexpr int kWarps = 7;                      // consumer warps; with the producer 8, so two blocks leave each thread 128 registers
 constexpr int kThreads = (kWarps + 1) * 32;
-constexpr int kMinUnits = 2;                   // fewest units per thread block
-constexpr int kSlotFloats = 2048 + 32;         // a partial result: rows x D values (2048 at most), then (reference, sum) per row
-constexpr int kCtasPerSm = 2;
-constexpr int kJoinPitch = 72;                 // floats per row of the join buffer: conflict-free for the fragments' stores
+constexpr int kCtasPerSm = 2;                  // where 128 registers suffice (8 rows, D <= 128), else 1
 constexpr uint32_t kIssued = 1u << 8;          // marks beside a stage's records: its copy was started,
 constexpr uint32_t kOddTurn = 1u << 9;         // in an odd turn of the ring
 constexpr uint32_t kStatusTimeout = 5;         // PN_ETIMEOUT
@@ -69,8 +67,9 @@ struct AttnParams {
     int group;                 // query heads per key/value head
     float scale_log2;          // scale * log2 e
     uint32_t* status;
-    uint32_t* counters;
-    float* partials;
+    uint32_t* counters;        // one per thread block
+    float* block_slots;        // two per thread block
+    float* warp_slots;         // two per consumer warp
     uint64_t timeout_ns;
     int stall;                 // testing aid: see pn_set_test_stall
 };
@@ -123,6 +122,8 @@ struct Request {
     int sink_tiles;            // tiles before it that hold visible first tokens
     int tiles;                 // units per (head, row group), at least 1
     int row_groups;
+    __device__ __forceinline__ uint32_t units(int heads) const { return static_cast<uint32_t>(tiles) * row_groups * heads; }
+    __device__ __forceinline__ int tile(int idx) const { return idx < sink_tiles ? idx : lo_tile + idx - sink_tiles; }
 };
 
 template <int RT>
@@ -160,25 +161,28 @@ struct Shape {
     static constexpr int kRecord = kv_record_bytes(D);
     static constexpr int kStage = kTileRecords * kRecord;
     static constexpr int kPlaneBytes = 256 * kPlaneGroups;     // 8 tokens of a plane
-    // a multiple of kWarps, so that a stage is always read by the same warp
-    // (whose wait can then not mistake a phase for the one before last)
-    static constexpr int kStages = kWarps * (D == 256 ? 2 : D == 128 ? 3 : 4);
+    static constexpr int kDepth = D == 256 ? 2 : D == 128 ? 3 : 4;      // stages per warp
+    static constexpr int kStages = kWarps * kDepth;
 };
 
 template <int D, int NT>
 struct Smem {
     static constexpr int kRT = 8 * NT;
     static constexpr int kRing = Shape<D>::kStages * Shape<D>::kStage;
-    static constexpr int kJoin = kRing;                                    // [warps][rows][kJoinPitch] floats
-    static constexpr int kMl = kJoin + kWarps * kRT * kJoinPitch * 4;      // [warps][rows] (reference, sum)
-    static constexpr int kFinal = kMl + kWarps * kRT * 8;                  // [rows] (reference, sum)
-    static constexpr int kBars = kFinal + kRT * 8;                         // full, empty
+    static constexpr int kFactors = kRing;                                 // [2 warps' pieces][rows] floats
+    static constexpr int kRuns = kFactors + 2 * kWarps * kRT * 4;          // see the block's join
+    static constexpr int kBars = kRuns + 4 * (2 * kWarps + 2) * 4;         // full, empty
     static constexpr int kValid = kBars + 2 * Shape<D>::kStages * 8;       // per stage: records that hold data, marks of its last copy
     static constexpr int kMisc = kValid + Shape<D>::kStages * 4;           // abort, last-block flag
     static constexpr int kScan = kMisc + 8;                                // the warps' sums, then [batch + 1] prefix sums of units
     static constexpr int kFixed = kScan + (kWarps + 1) * 4;
     static int bytes(int batch) { return kFixed + (batch + 1) * 4; }
+    static_assert(kBars % 8 == 0, "barriers are 8-byte aligned");
 };
+
+// Floats of a piece: rows x D values, then (reference, sum) per row.
+template <int D, int NT>
+constexpr int kPiece = 8 * NT * (D + 2);
 
 // Halves (code of token a, code of token b) of two tokens' words: the even
 // codes 0, 2, 4, 6 at bits 0, 4, 8, 12 of each half, or the odd ones.
@@ -233,6 +237,29 @@ struct State {
     float sum[NT][2];
     float o[NT][D / 16][4];
 
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            ref[n][0] = ref[n][1] = -INFINITY;
+            sum[n][0] = sum[n][1] = 0.0f;
+#pragma unroll
+            for (int m = 0; m < D / 16; ++m) o[n][m][0] = o[n][m][1] = o[n][m][2] = o[n][m][3] = 0.0f;
+        }
+    }
+    // the columns' whole sums, and o in units of 1
+    __device__ __forceinline__ void finish() {
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int c = 0; c < 2; ++c)
+#pragma unroll
+                for (int d = 4; d <= 16; d <<= 1) sum[n][c] += __shfl_xor_sync(0xFFFFFFFFu, sum[n][c], d);
+#pragma unroll
+            for (int m = 0; m < D / 16; ++m)
+#pragma unroll
+                for (int c = 0; c < 4; ++c) o[n][m][c] *= m & 1 ? 0x1p20f : 0x1p24f;
+        }
+    }
     __device__ __forceinline__ void scale_by(int n, float f0, float f1) {
 #pragma unroll
         for (int m = 0; m < D / 16; ++m) {
@@ -253,6 +280,62 @@ struct Queries {
     float start[NT][D / 64][2];
     float factor[NT][2];
     int pos[NT][2];
+
+    __device__ __forceinline__ void load(const AttnParams& P, const Request& r, int h, int row0) {
+        constexpr int NG = D / 64;
+        const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            const int row = min(row0 + 8 * n + g, r.rows - 1);
+            const int qi = row / P.group;
+            const __half* src = P.a.q + (r.q0 + qi) * P.a.q_stride + (h * P.group + row - qi * P.group) * D;
+            uint4 f[NG][2];
+            uint32_t top = 0;                  // the row's largest |q|, as bits: both halves of a register at once
+#pragma unroll
+            for (int j = 0; j < NG; ++j)
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    f[j][w] = *reinterpret_cast<const uint4*>(src + 64 * j + 16 * t + 8 * w);
+                    const uint32_t v[4] = {f[j][w].x, f[j][w].y, f[j][w].z, f[j][w].w};
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) top = __vmaxu2(top, v[i] & 0x7FFF7FFFu);
+                }
+            top = max(top & 0xFFFFu, top >> 16);
+            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+            top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+            const int e = 25 - static_cast<int>(max(top >> 10, 1u));             // the largest |q| 2^e lies in [2^10, 2^11)
+            const float up = __int_as_float((127 + e) << 23);
+            float sum[NG];
+#pragma unroll
+            for (int j = 0; j < NG; ++j) {
+                sum[j] = 0.0f;
+#pragma unroll
+                for (int w = 0; w < 2; ++w) {
+                    const uint32_t v[4] = {f[j][w].x, f[j][w].y, f[j][w].z, f[j][w].w};
+                    uint32_t to[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float a0 = half_bits_to_float(v[i] & 0xFFFFu) * up, a1 = half_bits_to_float(v[i] >> 16) * up;
+                        sum[j] += a0 + a1;
+                        to[i] = i & 1 ? pack_half2(a0, a1) : pack_half2(16.0f * a0, 16.0f * a1);
+                    }
+                    q[n][j][w][0] = make_uint2(to[0], to[1]);
+                    q[n][j][w][1] = make_uint2(to[2], to[3]);
+                }
+                sum[j] += __shfl_xor_sync(0xFFFFFFFFu, sum[j], 1);
+                sum[j] += __shfl_xor_sync(0xFFFFFFFFu, sum[j], 2);
+            }
+            const float back = P.scale_log2 * __int_as_float((127 + 20 - e) << 23);
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int from = (2 * t + c) << 2;             // the columns' rows are those of lanes (2t + c, .)
+#pragma unroll
+                for (int j = 0; j < NG; ++j) start[n][j][c] = -0x1p-17f * __shfl_sync(0xFFFFFFFFu, sum[j], from);   // -8 * 2^-20
+                factor[n][c] = __shfl_sync(0xFFFFFFFFu, back, from);
+                pos[n][c] = r.pos0 + min(row0 + 8 * n + 2 * t + c, r.rows - 1) / P.group;
+            }
+        }
+    }
 };
 
 template <int D, int NT, bool kMasked>
@@ -438,11 +521,25 @@ __device__ __forceinline__ void take_tile(const uint8_t* stage, int tok0, uint32
     }
 }
 
+// Where row `row` of row group rg of (request, head h) goes: its index in
+// [token][head], or -1 behind the last row.
+template <int RT>
+__device__ __forceinline__ int64_t row_index(const AttnParams& P, const Request& r, int h, int rg, int row) {
+    const int i = rg * RT + row;
+    if (i >= r.rows) return -1;
+    const int qi = i / P.group;
+    return (static_cast<int64_t>(r.q0) + qi) * P.a.heads + h * P.group + i - qi * P.group;
+}
+
+__device__ __forceinline__ float log_sum(float ref, float sum) {
+    return sum == 0.0f ? -INFINITY : 0.6931471805599453f * (ref + log2f(sum));
+}
+
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 && D <= 128 ? 2 : 1) attn_kernel(const __grid_constant__ AttnParams P) {
+__global__ void __launch_bounds__(kThreads, NT == 1 && D <= 128 ? kCtasPerSm : 1) attn_kernel(const __grid_constant__ AttnParams P) {
     using S = Shape<D>;
     using M = Smem<D, NT>;
-    constexpr int RT = 8 * NT, NG = S::kGroups, kStages = S::kStages;
+    constexpr int RT = 8 * NT, NG = S::kGroups, kStages = S::kStages, kDepth = S::kDepth;
     extern __shared__ __align__(128) uint8_t smem[];
     const uint32_t base = smem_addr(smem);
     auto full = [&](uint32_t s) { return base + M::kBars + 8u * s; };
@@ -470,10 +567,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && D <= 128 ? 2 : 1) attn_ke
         const int each = (a.batch + kThreads - 1) / kThreads;
         const int b0 = min(static_cast<int>(threadIdx.x) * each, a.batch), b1 = min(b0 + each, a.batch);
         uint32_t mine = 0;
-        for (int b = b0; b < b1; ++b) {
-            const Request r = request_of<RT>(P, b);
-            mine += static_cast<uint32_t>(r.tiles) * r.row_groups * heads;
-        }
+        for (int b = b0; b < b1; ++b) mine += request_of<RT>(P, b).units(heads);
         uint32_t in = mine;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -486,10 +580,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && D <= 128 ? 2 : 1) attn_ke
         for (int w = 0; w < warp; ++w) at += warp_sums[w];
         for (int b = b0; b < b1; ++b) {
             prefix[b] = at;
-            if (b + 1 < b1) {
-                const Request r = request_of<RT>(P, b);
-                at += static_cast<uint32_t>(r.tiles) * r.row_groups * heads;
-            }
+            if (b + 1 < b1) at += request_of<RT>(P, b).units(heads);
         }
         if (threadIdx.x == kThreads - 1) {
             uint32_t all = 0;
@@ -499,10 +590,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && D <= 128 ? 2 : 1) attn_ke
         __syncthreads();
     }
     const uint32_t total = prefix[a.batch];                              // below 2^32: checked on the host
-    const uint32_t blocks = min(gridDim.x, (total + kMinUnits - 1) / kMinUnits);
+    const uint32_t blocks = min(gridDim.x, (total + kWarps - 1) / kWarps);
     if (blockIdx.x >= blocks) return;                                    // nothing of this block is in flight
-    const uint32_t u0 = static_cast<uint32_t>(static_cast<uint64_t>(total) * blockIdx.x / blocks);
-    const uint32_t u1 = static_cast<uint32_t>(static_cast<uint64_t>(total) * (blockIdx.x + 1) / blocks);
+    auto first_unit = [&](uint32_t w) {                                  // of consumer warp w of the grid
+        return static_cast<uint32_t>(static_cast<uint64_t>(total) * w / (blocks * kWarps));
+    };
     auto request_at = [&](uint32_t u) {                                  // the request that holds unit u
         int lo = 0, hi = a.batch - 1;
         while (lo < hi) {
@@ -515,371 +607,399 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && D <= 128 ? 2 : 1) attn_ke
 
     if (warp == kWarps) {
         // ------------------------------------------------------- producer --
-        // Each lane serves every kLanes-th unit: it looks up the next one's
-        // pages while it waits for the current one's stage.
-        constexpr int kLanes = kStages < 16 ? 8 : 16;
-        struct Copy {
-            const uint8_t* src[kTileRecords];  // records, or (pages that hold the whole tile) the first one alone
-            uint32_t have;                     // records that a page holds
-        };
-        const bool one_page = P.cache.page_size >= kTile;
-        auto prepare = [&](uint32_t n) {       // unit u0 + n
-            Copy c{};
-            if (n >= u1 - u0) return c;
-            const uint32_t u = u0 + n;
-            const int b = request_at(u);
-            const Request r = request_of<RT>(P, b);
-            int h, rg, idx;
-            locate(u - prefix[b], r, h, rg, idx);
-            const int tile = idx < r.sink_tiles ? idx : r.lo_tile + idx - r.sink_tiles;
-            const int records = min(max((r.len - tile * kTile + kKvTokens - 1) / kKvTokens, 0), kTileRecords);
-            const int32_t* row = a.table + static_cast<int64_t>(b) * a.table_stride;
+        // A lane to each stage: it copies every kDepth-th unit of the stage's
+        // warp and looks up the next one's pages while it waits.
+        if (lane < kStages) {
+            const uint32_t s = lane, mine = blockIdx.x * kWarps + lane / kDepth, place = lane % kDepth;
+            const uint32_t u0 = first_unit(mine), count = first_unit(mine + 1) - u0;
+            const bool one_page = P.cache.page_size >= kTile;
+            int b = 0, h = 0, rg = 0, idx = 0;
+            Request r{};
+            int tok0 = 0, records = 0, page[kTileRecords];
+            auto look = [&]() {                // the current unit's pages
+                const int tile = r.tile(idx);
+                tok0 = tile * kTile;
+                records = min(max((r.len - tok0 + kKvTokens - 1) / kKvTokens, 0), kTileRecords);
+                const int32_t* row = a.table + static_cast<int64_t>(b) * a.table_stride;
 #pragma unroll
-            for (int i = 0; i < kTileRecords; ++i) {
-                if (i >= records || (i > 0 && one_page)) break;
-                const int tok = tile * kTile + i * kKvTokens;
-                const int page = row[tok >> P.cache.page_shift];
-                if (page < 0 || page >= P.cache.pages) continue;         // no such page: its tokens are not seen
-                c.src[i] = P.cache.record((static_cast<int64_t>(page) << P.cache.page_shift) + (tok & (P.cache.page_size - 1)), h);
-                c.have |= one_page ? (1u << records) - 1 : 1u << i;
+                for (int i = 0; i < kTileRecords; ++i)
+                    page[i] = i < records && (i == 0 || !one_page) ? row[(tok0 + i * kKvTokens) >> P.cache.page_shift] : -1;
+            };
+            uint32_t n = place;
+            if (n < count) {
+                b = request_at(u0 + n);
+                r = request_of<RT>(P, b);
+                locate(u0 + n - prefix[b], r, h, rg, idx);
+                look();
             }
-            return c;
-        };
-        const uint32_t count = u1 - u0;
-        uint32_t s = lane, turn = 0;           // the lane's stage, and how often the ring has gone round
-        bool ok = true;
-        Copy cur = prepare(lane);
-        // The lanes go on together: a wait tells a phase from the one before it,
-        // not from the one before that, so no lane may be a whole ring ahead of
-        // another (kLanes <= kStages keeps the stages of one pass apart).
-        for (uint32_t n = 0; n < count; n += kLanes) {
-            const bool mine = lane < kLanes && n + lane < count;
-            const Copy next = lane < kLanes ? prepare(n + lane + kLanes) : Copy{};
-            // each lane copies as soon as its own stage is free
-            bool done = !mine;
+            uint32_t turn = 0;
             uint64_t t0 = 0;
-            for (uint32_t polls = 1;; ++polls) {
-                if (!done && (turn == 0 || mbar_try_wait(empty(s), (turn - 1) & 1u))) {
-                    const uint32_t dst = base + s * S::kStage;
-                    // (testing aid: with stall the first unit's bytes are announced but
-                    // never copied; its wait can only time out)
-                    const bool copied = !(P.stall && n + lane == 0);
-                    valid[s] = cur.have | (copied ? kIssued : 0u) | ((turn & 1u) ? kOddTurn : 0u);
-                    mbar_arrive_expect_tx(full(s), __popc(cur.have) * S::kRecord);
-                    if (copied && one_page) {
-                        if (cur.have) bulk_g2s(dst, cur.src[0], __popc(cur.have) * S::kRecord, full(s));
-                    } else if (copied) {
-#pragma unroll
-                        for (int i = 0; i < kTileRecords; ++i)
-                            if ((cur.have >> i) & 1) bulk_g2s(dst + i * S::kRecord, cur.src[i], S::kRecord, full(s));
+            for (uint32_t polls = 0; n < count; ++polls) {
+                if (turn > 0 && !mbar_try_wait(empty(s), (turn - 1) & 1u)) {
+                    if (polls % 256 == 255) {
+                        const uint64_t now = globaltimer_ns();
+                        if (t0 == 0) t0 = now;
+                        if (*abort || now - t0 > P.timeout_ns) {
+                            *abort = 1u;
+                            atomicCAS(P.status, 0u, kStatusTimeout);
+                            break;
+                        }
                     }
-                    done = true;
+                    continue;
                 }
-                if (__all_sync(0xFFFFFFFFu, done)) break;
-                if (polls % 256 == 0) {
-                    const uint64_t now = globaltimer_ns();
-                    if (t0 == 0) t0 = now;
-                    ok = !*abort && now - t0 <= P.timeout_ns;
-                    if (__any_sync(0xFFFFFFFFu, !ok)) break;
+                // pages outside the cache: their tokens are not seen
+                uint32_t have = 0;
+#pragma unroll
+                for (int i = 0; i < kTileRecords; ++i)
+                    if (page[i] >= 0 && page[i] < P.cache.pages) have |= one_page ? (1u << records) - 1 : 1u << i;
+                // (testing aid: with stall the first unit's bytes are announced but
+                // never copied; its wait can only time out)
+                const bool copied = !(P.stall && lane == 0 && n == 0);
+                const uint32_t dst = base + s * S::kStage;
+                valid[s] = have | (copied ? kIssued : 0u) | ((turn & 1u) ? kOddTurn : 0u);
+                mbar_arrive_expect_tx(full(s), __popc(have) * S::kRecord);
+                if (copied) {
+#pragma unroll
+                    for (int i = 0; i < kTileRecords; ++i) {
+                        if (!((have >> i) & 1) || (i > 0 && one_page)) continue;
+                        const int tok = tok0 + i * kKvTokens;
+                        const uint8_t* src = P.cache.record((static_cast<int64_t>(page[i]) << P.cache.page_shift) + (tok & (P.cache.page_size - 1)), h);
+                        bulk_g2s(dst + i * S::kRecord, src, (one_page ? __popc(have) : 1) * S::kRecord, full(s));
+                    }
+                }
+                ++turn;
+                t0 = 0;
+                n += kDepth;
+                if (n < count) {
+                    idx += kDepth;
+                    while (idx >= r.tiles) {
+                        idx -= r.tiles;
+                        if (++rg < r.row_groups) continue;
+                        rg = 0;
+                        if (++h < heads) continue;
+                        h = 0;
+                        do r = request_of<RT>(P, ++b); while (r.rows == 0);   // a request with units follows: n < count
+                    }
+                    look();
                 }
             }
-            if (__any_sync(0xFFFFFFFFu, !ok)) {
-                if (lane == 0) {
-                    *abort = 1u;
-                    atomicCAS(P.status, 0u, kStatusTimeout);
-                }
-                break;
-            }
-            cur = next;
-            s += kLanes;
-            if (s >= kStages) { s -= kStages; ++turn; }
+            // the last copy into the stage lands before the block ends, also after an abort
+            if (valid[s] & kIssued) wait_phase(full(s), valid[s] & kOddTurn ? 1u : 0u, kDrainLimitNs, nullptr);
         }
-        __syncwarp();
-        // the last copy into every stage lands before the block ends, also after an abort
-        if (lane < kStages && (valid[lane] & kIssued))
-            wait_phase(full(lane), valid[lane] & kOddTurn ? 1u : 0u, kDrainLimitNs, nullptr);
         return;
     }
 
     // ---------------------------------------------------------- consumers --
     const int g = lane >> 2, t = lane & 3;
-    float* join = reinterpret_cast<float*>(smem + M::kJoin);
-    float2* ml = reinterpret_cast<float2*>(smem + M::kMl);
-    float2* fin = reinterpret_cast<float2*>(smem + M::kFinal);
-    uint32_t it0 = 0;
-    bool alive = true;
-    for (uint32_t u = u0; u < u1;) {
-        const int b = request_at(u);
-        const Request r = request_of<RT>(P, b);
-        int h, rg, first;
-        locate(u - prefix[b], r, h, rg, first);
-        const uint32_t seg_u0 = u - first;
-        const int count = static_cast<int>(min(static_cast<uint32_t>(r.tiles - first), u1 - u));
-        const bool whole = count == r.tiles;
-        const int row0 = rg * RT;
-        // unit it of the block goes to warp it % kWarps; `part` numbers the
-        // warps that have some of the segment, from its first unit on
-        const int active = min(count, kWarps);
-        const int part = static_cast<int>((warp + kWarps - it0 % kWarps) % kWarps);
-
-        State<D, NT> st;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            st.ref[n][0] = st.ref[n][1] = -INFINITY;
-            st.sum[n][0] = st.sum[n][1] = 0.0f;
-#pragma unroll
-            for (int m = 0; m < D / 16; ++m) st.o[n][m][0] = st.o[n][m][1] = st.o[n][m][2] = st.o[n][m][3] = 0.0f;
+    const uint32_t mine = blockIdx.x * kWarps + warp;
+    const uint32_t u0 = first_unit(mine), u1 = first_unit(mine + 1);
+    // a warp's pieces: [0] of a segment that began before it, [1] of one that goes on behind it;
+    // seg: the segment's first unit, or kNone
+    constexpr uint32_t kNone = 0xFFFFFFFFu;
+    uint32_t* piece_seg = reinterpret_cast<uint32_t*>(smem + M::kRuns);  // [warps][2]
+    if (lane < 2) piece_seg[2 * warp + lane] = kNone;
+    __syncwarp();
+    {
+        uint32_t stage = warp * kDepth, parity = 0;
+        bool alive = true;
+        int b = 0, h = 0, rg = 0, first = 0;
+        Request r{};
+        if (u0 < u1) {
+            b = request_at(u0);
+            r = request_of<RT>(P, b);
+            locate(u0 - prefix[b], r, h, rg, first);
         }
-        if (part < active) {
+        for (uint32_t u = u0; u < u1;) {
+            const int count = static_cast<int>(min(static_cast<uint32_t>(r.tiles - first), u1 - u));
+            const int row0 = rg * RT;
+            State<D, NT> st;
+            st.clear();
             Queries<D, NT> Q;
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                const int row = min(row0 + 8 * n + g, r.rows - 1);
-                const int qi = row / P.group;
-                const __half* src = a.q + (r.q0 + qi) * a.q_stride + (h * P.group + row - qi * P.group) * D;
-                uint4 f[NG][2];
-                uint32_t top = 0;              // the row's largest |q|, as bits: both halves of a register at once
-#pragma unroll
-                for (int j = 0; j < NG; ++j)
-#pragma unroll
-                    for (int w = 0; w < 2; ++w) {
-                        f[j][w] = *reinterpret_cast<const uint4*>(src + 64 * j + 16 * t + 8 * w);
-                        const uint32_t v[4] = {f[j][w].x, f[j][w].y, f[j][w].z, f[j][w].w};
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) top = __vmaxu2(top, v[i] & 0x7FFF7FFFu);
-                    }
-                top = max(top & 0xFFFFu, top >> 16);
-                top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-                top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-                const int e = 25 - static_cast<int>(max(top >> 10, 1u));         // the largest |q| 2^e lies in [2^10, 2^11)
-                const float up = __int_as_float((127 + e) << 23);
-                float sum[NG];
-#pragma unroll
-                for (int j = 0; j < NG; ++j) {
-                    sum[j] = 0.0f;
-#pragma unroll
-                    for (int w = 0; w < 2; ++w) {
-                        const uint32_t v[4] = {f[j][w].x, f[j][w].y, f[j][w].z, f[j][w].w};
-                        uint32_t to[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const float a0 = half_bits_to_float(v[i] & 0xFFFFu) * up, a1 = half_bits_to_float(v[i] >> 16) * up;
-                            sum[j] += a0 + a1;
-                            to[i] = i & 1 ? pack_half2(a0, a1) : pack_half2(16.0f * a0, 16.0f * a1);
-                        }
-                        Q.q[n][j][w][0] = make_uint2(to[0], to[1]);
-                        Q.q[n][j][w][1] = make_uint2(to[2], to[3]);
-                    }
-                    sum[j] += __shfl_xor_sync(0xFFFFFFFFu, sum[j], 1);
-                    sum[j] += __shfl_xor_sync(0xFFFFFFFFu, sum[j], 2);
-                }
-                const float back = P.scale_log2 * __int_as_float((127 + 20 - e) << 23);
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    // the columns' rows are those of lanes (2t + c, .)
-                    const int from = (2 * t + c) << 2;
-#pragma unroll
-                    for (int j = 0; j < NG; ++j) Q.start[n][j][c] = -0x1p-17f * __shfl_sync(0xFFFFFFFFu, sum[j], from);   // -8 * 2^-20
-                    Q.factor[n][c] = __shfl_sync(0xFFFFFFFFu, back, from);
-                    Q.pos[n][c] = r.pos0 + min(row0 + 8 * n + 2 * t + c, r.rows - 1) / P.group;
-                }
-            }
+            Q.load(P, r, h, row0);
             const int pos_lo = r.pos0 + row0 / P.group;
             const int pos_hi = r.pos0 + min(row0 + RT - 1, r.rows - 1) / P.group;
             const int window = a.window ? a.window : INT32_MAX;
-            for (int k = part; k < count; k += kWarps) {
-                const uint32_t it = it0 + k, s = it % kStages;
+            for (int k = 0; k < count; ++k) {
                 if (alive) {
-                    alive = wait_phase(full(s), (it / kStages) & 1u, P.timeout_ns, abort);
-                    alive = __all_sync(0xFFFFFFFFu, alive);
+                    alive = __all_sync(0xFFFFFFFFu, wait_phase(full(stage), parity, P.timeout_ns, abort));
                     if (!alive && lane == 0) {
                         *abort = 1u;
                         atomicCAS(P.status, 0u, kStatusTimeout);
                     }
                 }
-                if (!alive) continue;
-                const int idx = first + k;
-                const int tok0 = (idx < r.sink_tiles ? idx : r.lo_tile + idx - r.sink_tiles) * kTile;
-                const uint32_t have = valid[s] & ((1u << kTileRecords) - 1);
-                const uint8_t* stage = smem + s * S::kStage;
+                if (!alive) break;
+                const int tok0 = r.tile(first + k) * kTile;
+                const uint32_t have = valid[stage] & ((1u << kTileRecords) - 1);
+                const uint8_t* data = smem + stage * S::kStage;
                 if (tok0 > pos_hi) {
                     // no row sees this tile
                 } else if (have == (1u << kTileRecords) - 1 && tok0 + kTile - 1 <= pos_lo && (tok0 > pos_hi - window || tok0 + kTile <= a.sinks)) {
-                    take_tile<D, NT, false>(stage, tok0, have, Q, window, a.sinks, st);
+                    take_tile<D, NT, false>(data, tok0, have, Q, window, a.sinks, st);
                 } else {
-                    take_tile<D, NT, true>(stage, tok0, have, Q, window, a.sinks, st);
+                    take_tile<D, NT, true>(data, tok0, have, Q, window, a.sinks, st);
                 }
                 __syncwarp();
-                if (lane == 0) mbar_arrive(empty(s));
-            }
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int c = 0; c < 2; ++c)
-#pragma unroll
-                    for (int d = 4; d <= 16; d <<= 1) st.sum[n][c] += __shfl_xor_sync(0xFFFFFFFFu, st.sum[n][c], d);
-            if (g == 0) {
-#pragma unroll
-                for (int n = 0; n < NT; ++n)
-#pragma unroll
-                    for (int c = 0; c < 2; ++c) ml[part * RT + 8 * n + 2 * t + c] = make_float2(st.ref[n][c], st.sum[n][c]);
-            }
-        }
-        consumers_sync();
-        // the rows' common reference and sum
-        if (threadIdx.x < RT) {
-            float m = -INFINITY, l = 0.0f;
-            for (int w = 0; w < active; ++w) m = fmaxf(m, ml[w * RT + threadIdx.x].x);
-            for (int w = 0; w < active; ++w) {
-                const float2 p = ml[w * RT + threadIdx.x];
-                l += p.x == -INFINITY ? 0.0f : ex2(p.x - m) * p.y;
-            }
-            fin[threadIdx.x] = make_float2(m, l);
-        }
-        if (part < active) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                float f[2];
-#pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                    float m = -INFINITY;
-                    for (int w = 0; w < active; ++w) m = fmaxf(m, ml[w * RT + 8 * n + 2 * t + c].x);
-                    f[c] = st.ref[n][c] == -INFINITY ? 0.0f : ex2(st.ref[n][c] - m);
+                if (lane == 0) mbar_arrive(empty(stage));
+                if (++stage == (warp + 1) * kDepth) {
+                    stage = warp * kDepth;
+                    parity ^= 1u;
                 }
-                st.scale_by(n, f[0], f[1]);
-#pragma unroll
-                for (int m = 0; m < D / 16; ++m)
-#pragma unroll
-                    for (int c = 0; c < 4; ++c)
-                        st.o[n][m][c] *= m & 1 ? 0x1p20f : 0x1p24f;
             }
-        }
-        // blocks that share the segment
-        auto block_of = [&](uint32_t x) {
-            return static_cast<int>(((static_cast<uint64_t>(x) + 1) * blocks + total - 1) / total - 1);
-        };
-        const int c_first = whole ? 0 : block_of(seg_u0), c_last = whole ? 0 : block_of(seg_u0 + r.tiles - 1);
-        float* slot = P.partials + static_cast<int64_t>(2 * blockIdx.x + (first == 0 ? 1 : 0)) * kSlotFloats;
-#pragma unroll
-        for (int j = 0; j < NG; ++j) {
-            if (part < active) {
+            st.finish();
+            if (count == r.tiles) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        float* to = join + (part * RT + 8 * n + 2 * t + c) * kJoinPitch + 8 * g;
+                        const int64_t at = row_index<RT>(P, r, h, rg, 8 * n + 2 * t + c);
+                        if (at < 0) continue;
+                        const float inv = st.sum[n][c] == 0.0f ? 0.0f : 1.0f / st.sum[n][c];
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            *reinterpret_cast<float2*>(to + 2 * i) = make_float2(st.o[n][4 * j + i][c], st.o[n][4 * j + i][2 + c]);
+                        for (int j = 0; j < NG; ++j) {
+                            uint32_t w[4];
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) w[i] = pack_half2(st.o[n][4 * j + i][c] * inv, st.o[n][4 * j + i][2 + c] * inv);
+                            *reinterpret_cast<uint4*>(a.out + at * D + 64 * j + 8 * g) = make_uint4(w[0], w[1], w[2], w[3]);
+                        }
+                        if (a.lse && g == 0) a.lse[at] = log_sum(st.ref[n][c], st.sum[n][c]);
+                    }
+            } else {
+                const int kind = first == 0 ? 1 : 0;
+                float* slot = P.warp_slots + static_cast<int64_t>(2 * mine + kind) * kPiece<D, NT>;
+                if (lane == 0) piece_seg[2 * warp + kind] = u - first;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        const int row = 8 * n + 2 * t + c;
+#pragma unroll
+                        for (int j = 0; j < NG; ++j) {
+                            float4* to = reinterpret_cast<float4*>(slot + row * D + 64 * j + 8 * g);
+                            to[0] = make_float4(st.o[n][4 * j][c], st.o[n][4 * j][2 + c], st.o[n][4 * j + 1][c], st.o[n][4 * j + 1][2 + c]);
+                            to[1] = make_float4(st.o[n][4 * j + 2][c], st.o[n][4 * j + 2][2 + c], st.o[n][4 * j + 3][c], st.o[n][4 * j + 3][2 + c]);
+                        }
+                        if (g == 0) reinterpret_cast<float2*>(slot + RT * D)[row] = make_float2(st.ref[n][c], st.sum[n][c]);
                     }
             }
-            consumers_sync();
-            for (int i = threadIdx.x; i < RT * 32; i += kWarps * 32) {
-                const int row = i >> 5, d = (i & 31) * 2;
-                if (row0 + row < r.rows) {
-                    float2 o = make_float2(0.0f, 0.0f);
-                    for (int w = 0; w < active; ++w) {
-                        const float2 p = *reinterpret_cast<const float2*>(join + (w * RT + row) * kJoinPitch + d);
-                        o.x += p.x;
-                        o.y += p.y;
-                    }
-                    const float2 f = fin[row];
-                    if (whole) {
-                        const float inv = f.y == 0.0f ? 0.0f : 1.0f / f.y;
-                        const int qi = (row0 + row) / P.group;
-                        const int64_t at = (static_cast<int64_t>(r.q0 + qi) * a.heads + h * P.group + row0 + row - qi * P.group);
-                        *reinterpret_cast<__half2*>(a.out + at * D + 64 * j + d) = __floats2half2_rn(o.x * inv, o.y * inv);
-                        if (a.lse && j == 0 && d == 0)
-                            a.lse[at] = f.y == 0.0f ? -INFINITY : 0.6931471805599453f * (f.x + log2f(f.y));
-                    } else {
-                        *reinterpret_cast<float2*>(slot + row * D + 64 * j + d) = o;
-                        if (j == 0 && d == 0) *reinterpret_cast<float2*>(slot + 2048 + 2 * row) = f;
-                    }
-                }
-            }
-            consumers_sync();
-        }
-        if (!whole) {
-            __threadfence();
-            consumers_sync();
-            if (threadIdx.x == 0) {
-                const uint32_t n = static_cast<uint32_t>(c_last - c_first);
-                const uint32_t old = atomicAdd(&P.counters[c_first], 1u);
-                *last_flag = old == n;
-                if (old == n) P.counters[c_first] = 0u;
-            }
-            consumers_sync();
-            if (*last_flag) {
-                __threadfence();
-                const float* parts = P.partials;
-                auto piece = [&](int c) { return parts + static_cast<int64_t>(2 * c + (c == c_first ? 1 : 0)) * kSlotFloats; };
-                for (int i = threadIdx.x; i < RT * (D / 2); i += kWarps * 32) {
-                    const int row = i / (D / 2), d = (i % (D / 2)) * 2;
-                    if (row0 + row >= r.rows) continue;
-                    float m = -INFINITY, l = 0.0f;
-#pragma unroll 4
-                    for (int c = c_first; c <= c_last; ++c) m = fmaxf(m, __ldcg(piece(c) + 2048 + 2 * row));
-                    float2 o = make_float2(0.0f, 0.0f);
-#pragma unroll 4
-                    for (int c = c_first; c <= c_last; ++c) {
-                        const float* p = piece(c);
-                        const float2 f = __ldcg(reinterpret_cast<const float2*>(p + 2048 + 2 * row));
-                        const float2 w = __ldcg(reinterpret_cast<const float2*>(p + row * D + d));
-                        const float s = f.x == -INFINITY ? 0.0f : ex2(f.x - m);
-                        l += s * f.y;
-                        o.x += s * w.x;
-                        o.y += s * w.y;
-                    }
-                    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-                    const int qi = (row0 + row) / P.group;
-                    const int64_t at = (static_cast<int64_t>(r.q0 + qi) * a.heads + h * P.group + row0 + row - qi * P.group);
-                    *reinterpret_cast<__half2*>(a.out + at * D + d) = __floats2half2_rn(o.x * inv, o.y * inv);
-                    if (a.lse && d == 0) a.lse[at] = l == 0.0f ? -INFINITY : 0.6931471805599453f * (m + log2f(l));
+            u += count;
+            first = 0;
+            if (u < u1 && ++rg == r.row_groups) {
+                rg = 0;
+                if (++h == heads) {
+                    h = 0;
+                    do r = request_of<RT>(P, ++b); while (r.rows == 0);
                 }
             }
         }
-        it0 += count;
-        u += count;
+    }
+
+    // -------------------------------------------------- the block's join --
+    // Its pieces in unit order form runs of one segment each.
+    consumers_sync();
+    uint32_t* order = piece_seg + 2 * kWarps + 2;      // [pieces] piece numbers
+    uint32_t* run_of = order + 2 * kWarps + 2;         // [pieces] and, behind them, the number of pieces and of runs
+    uint32_t* run_at = run_of + 2 * kWarps + 2;        // [runs + 1] first piece of a run
+    float* factors = reinterpret_cast<float*>(smem + M::kFactors);       // [pieces][rows]
+    if (threadIdx.x == 0) {
+        int pieces = 0, runs = 0;
+        uint32_t seg = kNone;
+        for (int i = 0; i < 2 * kWarps; ++i) {
+            if (piece_seg[i] == kNone) continue;
+            if (piece_seg[i] != seg) run_at[runs++] = pieces;
+            seg = piece_seg[i];
+            order[pieces] = i;
+            run_of[pieces++] = runs - 1;
+        }
+        run_at[runs] = pieces;
+        run_of[2 * kWarps] = pieces;
+        run_of[2 * kWarps + 1] = runs;
+    }
+    consumers_sync();
+    const int runs = static_cast<int>(run_of[2 * kWarps + 1]);
+    if (runs == 0) return;
+    auto block_of = [&](uint32_t x) {                  // the block that holds unit x
+        return static_cast<uint32_t>(((static_cast<uint64_t>(x) + 1) * blocks + total - 1) / total - 1);
+    };
+    auto warp_slot = [&](int i) { return P.warp_slots + (static_cast<int64_t>(2 * blockIdx.x) * kWarps + order[i]) * kPiece<D, NT>; };
+    auto block_slot = [&](uint32_t c, bool begins) { return P.block_slots + (2 * static_cast<int64_t>(c) + begins) * kPiece<D, NT>; };
+    // A run's row: common reference and sum; each piece's factor to them.
+    // Whole segments get the output's factor; the others' (reference, sum) goes to the block's slot.
+    for (int i = threadIdx.x; i < runs * RT; i += kWarps * 32) {
+        const int run = i / RT, row = i % RT;
+        const int p0 = run_at[run], p1 = run_at[run + 1];
+        const uint32_t seg = piece_seg[order[p0]];
+        const int b = request_at(seg);
+        const Request r = request_of<RT>(P, b);
+        float m = -INFINITY, l = 0.0f;
+        for (int p = p0; p < p1; ++p) m = fmaxf(m, reinterpret_cast<const float2*>(warp_slot(p) + RT * D)[row].x);
+        for (int p = p0; p < p1; ++p) {
+            const float2 v = reinterpret_cast<const float2*>(warp_slot(p) + RT * D)[row];
+            const float f = v.x == -INFINITY ? 0.0f : ex2(v.x - m);
+            factors[p * RT + row] = f;
+            l += f * v.y;
+        }
+        const uint32_t c0 = block_of(seg), c1 = block_of(seg + r.tiles - 1);
+        if (c0 == c1) {
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            for (int p = p0; p < p1; ++p) factors[p * RT + row] *= inv;
+            int h, rg, idx;
+            locate(seg - prefix[b], r, h, rg, idx);
+            const int64_t at = row_index<RT>(P, r, h, rg, row);
+            if (a.lse && at >= 0) a.lse[at] = log_sum(m, l);
+        } else {
+            reinterpret_cast<float2*>(block_slot(blockIdx.x, c0 == blockIdx.x) + RT * D)[row] = make_float2(m, l);
+        }
+    }
+    consumers_sync();
+    for (int i = threadIdx.x; i < runs * (RT * D / 4); i += kWarps * 32) {
+        const int run = i / (RT * D / 4), e = (i % (RT * D / 4)) * 4, row = e / D, d = e % D;
+        const int p0 = run_at[run], p1 = run_at[run + 1];
+        const uint32_t seg = piece_seg[order[p0]];
+        const int b = request_at(seg);
+        const Request r = request_of<RT>(P, b);
+        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+        for (int p = p0; p < p1; ++p) {
+            const float f = factors[p * RT + row];
+            const float4 v = *reinterpret_cast<const float4*>(warp_slot(p) + e);
+            // a piece that saw nothing, or of weight zero, adds nothing
+            o.x = fmaf(f, v.x, o.x); o.y = fmaf(f, v.y, o.y); o.z = fmaf(f, v.z, o.z); o.w = fmaf(f, v.w, o.w);
+        }
+        const uint32_t c0 = block_of(seg), c1 = block_of(seg + r.tiles - 1);
+        if (c0 == c1) {
+            int h, rg, idx;
+            locate(seg - prefix[b], r, h, rg, idx);
+            const int64_t at = row_index<RT>(P, r, h, rg, row);
+            if (at >= 0) *reinterpret_cast<uint2*>(a.out + at * D + d) = make_uint2(pack_half2(o.x, o.y), pack_half2(o.z, o.w));
+        } else {
+            *reinterpret_cast<float4*>(block_slot(blockIdx.x, c0 == blockIdx.x) + e) = o;
+        }
+    }
+
+    // ------------------------------------------- segments of several blocks --
+    // The first and the last run may be pieces of such; the last block to
+    // arrive joins them, in block order.  No copy is in flight any more: the
+    // ring holds the parts' factors.
+    const uint32_t piece0 = piece_seg[order[0]], piece1 = piece_seg[order[run_at[runs] - 1]];
+    float* part_factors = reinterpret_cast<float*>(smem);                // [parts][rows], as many as fit
+    constexpr uint32_t kParts = M::kRing / (RT * 4);
+    for (int side = 0; side < 2; ++side) {
+        if (side == 1 && piece1 == piece0) break;
+        const uint32_t seg = side ? piece1 : piece0;
+        const int b = request_at(seg);
+        const Request r = request_of<RT>(P, b);
+        const uint32_t c0 = block_of(seg), c1 = block_of(seg + r.tiles - 1);
+        if (c0 == c1) continue;                                          // the same for every thread
+        __threadfence();
+        consumers_sync();
+        if (threadIdx.x == 0) {
+            const bool last = atomicAdd(&P.counters[c0], 1u) == c1 - c0;
+            if (last) P.counters[c0] = 0u;
+            *last_flag = last;
+        }
+        consumers_sync();
+        if (!*last_flag) continue;
+        __threadfence();
+        int h, rg, idx;
+        locate(seg - prefix[b], r, h, rg, idx);
+        const uint32_t parts = c1 - c0 + 1;                              // at most the grid, which fits the ring
+        for (int row = warp; row < RT; row += kWarps) {
+            float m = -INFINITY, l = 0.0f;
+            for (uint32_t p = lane; p < parts; p += 32)
+                m = fmaxf(m, __ldcg(reinterpret_cast<const float2*>(block_slot(c0 + p, p == 0) + RT * D) + row).x);
+#pragma unroll
+            for (int d = 16; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
+            for (uint32_t p = lane; p < parts; p += 32) {
+                const float2 v = __ldcg(reinterpret_cast<const float2*>(block_slot(c0 + p, p == 0) + RT * D) + row);
+                const float f = v.x == -INFINITY ? 0.0f : ex2(v.x - m);
+                if (p < kParts) part_factors[p * RT + row] = f;
+                l += f * v.y;
+            }
+#pragma unroll
+            for (int d = 16; d >= 1; d >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
+            __syncwarp();
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            for (uint32_t p = lane; p < parts; p += 32)
+                if (p < kParts) part_factors[p * RT + row] *= inv;
+            const int64_t at = row_index<RT>(P, r, h, rg, row);
+            if (a.lse && at >= 0 && lane == 0) a.lse[at] = log_sum(m, l);
+        }
+        consumers_sync();
+        for (int i = threadIdx.x; i < RT * D / 4; i += kWarps * 32) {
+            const int e = i * 4, row = e / D, d = e % D;
+            const int64_t at = row_index<RT>(P, r, h, rg, row);
+            if (at < 0) continue;
+            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 16
+            for (uint32_t p = 0; p < parts; ++p) {
+                const float f = part_factors[p * RT + row];
+                const float4 v = __ldcg(reinterpret_cast<const float4*>(block_slot(c0 + p, p == 0) + e));
+                o.x = fmaf(f, v.x, o.x); o.y = fmaf(f, v.y, o.y); o.z = fmaf(f, v.z, o.z); o.w = fmaf(f, v.w, o.w);
+            }
+            *reinterpret_cast<uint2*>(a.out + at * D + d) = make_uint2(pack_half2(o.x, o.y), pack_half2(o.z, o.w));
+        }
+        consumers_sync();                                                // the factors are written again
     }
 }
 
 template <int D, int NT>
-cudaError_t launch(const AttnParams& P, int num_sms, cudaStream_t s) {
+constexpr int kBlocksPerSm = NT == 1 && D <= 128 ? kCtasPerSm : 1;
+
+// Workspace: status word (256 bytes), one counter per thread block, two slots
+// per thread block and per consumer warp.
+constexpr size_t counter_bytes(size_t blocks) { return (blocks * 4 + 255) / 256 * 256; }
+template <int D, int NT>
+size_t workspace_bytes(int num_sms) {
+    const size_t blocks = static_cast<size_t>(num_sms) * kBlocksPerSm<D, NT>;
+    return 256 + counter_bytes(static_cast<size_t>(num_sms) * kCtasPerSm) + 2 * blocks * (1 + kWarps) * kPiece<D, NT> * 4;
+}
+
+template <int D, int NT>
+cudaError_t launch(AttnParams P, uint8_t* ws, int num_sms, cudaStream_t s) {
     static std::atomic<uint64_t> smem_set{0};
     if (cudaError_t e = set_smem_limit_once(attn_kernel<D, NT>, 227 * 1024, smem_set); e != cudaSuccess) return e;
     const int smem = Smem<D, NT>::bytes(P.a.batch);
     if (smem > 227 * 1024) return cudaErrorInvalidValue;
-    const int grid = num_sms * (NT == 1 && D <= 128 ? kCtasPerSm : 1);
+    int grid = num_sms * kBlocksPerSm<D, NT>;
+    constexpr int kMost = Smem<D, NT>::kRing / (8 * NT * 4);             // blocks whose factors fit the ring
+    if (grid > kMost) grid = kMost;
+    P.status = reinterpret_cast<uint32_t*>(ws);
+    P.counters = reinterpret_cast<uint32_t*>(ws + 256);
+    P.block_slots = reinterpret_cast<float*>(ws + 256 + counter_bytes(static_cast<size_t>(num_sms) * kCtasPerSm));
+    P.warp_slots = P.block_slots + 2 * static_cast<size_t>(grid) * kPiece<D, NT>;
     attn_kernel<D, NT><<<grid, kThreads, smem, s>>>(P);
     return cudaGetLastError();
 }
 
 }  // namespace
 
-// Workspace: status word (256 bytes), one counter per thread block, two partial slots per thread block.
 size_t attn_workspace_bytes(int num_sms) {
-    const size_t ctas = static_cast<size_t>(num_sms) * kCtasPerSm;
-    return 256 + (ctas * 4 + 255) / 256 * 256 + 2 * ctas * kSlotFloats * 4;
+    size_t most = 0;
+    for (size_t n : {workspace_bytes<64, 1>(num_sms), workspace_bytes<64, 2>(num_sms), workspace_bytes<128, 1>(num_sms),
+                     workspace_bytes<128, 2>(num_sms), workspace_bytes<256, 1>(num_sms)})
+        most = n > most ? n : most;
+    return most;
+}
+
+bool attn_fits(const AttnArgs& a, const KvGeometry& g) {
+    const int64_t rows = static_cast<int64_t>(a.max_queries) * (a.heads / g.heads), per = g.D < 256 && rows > 8 ? 16 : 8;
+    const double units = static_cast<double>(a.batch) * g.heads * static_cast<double>((rows + per - 1) / per) *
+                         static_cast<double>((static_cast<int64_t>(a.max_pages) * g.page_size + kTile - 1) / kTile);
+    return units < 4294967296.0;
 }
 
 cudaError_t launch_attention(const AttnArgs& a, const KvGeometry& g, void* workspace, int num_sms, uint64_t timeout_ns, int stall,
                              cudaStream_t s) {
     int shift = 0;
     while ((1 << shift) < g.page_size) ++shift;
-    const size_t ctas = static_cast<size_t>(num_sms) * kCtasPerSm;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     AttnParams P{a, KvCache{g.data, g.pages, g.page_size, shift, g.heads, g.D}, a.heads / g.heads, a.scale * 1.4426950408889634f,
-                 reinterpret_cast<uint32_t*>(ws), reinterpret_cast<uint32_t*>(ws + 256),
-                 reinterpret_cast<float*>(ws + 256 + (ctas * 4 + 255) / 256 * 256), timeout_ns, stall};
+                 nullptr, nullptr, nullptr, nullptr, timeout_ns, stall};
     // 8 or 16 query rows share the decoded codes
-    const int64_t rows = static_cast<int64_t>(a.max_queries) * P.group, per = g.D < 256 && rows > 8 ? 16 : 8;
-    const double units = static_cast<double>(a.batch) * g.heads * static_cast<double>((rows + per - 1) / per) *
-                         static_cast<double>((static_cast<int64_t>(a.max_pages) * g.page_size + kTile - 1) / kTile);
-    if (units >= 4294967296.0) return cudaErrorInvalidValue;
     const bool wide = static_cast<int64_t>(a.max_queries) * P.group > 8;
-    if (g.D == 64) return wide ? launch<64, 2>(P, num_sms, s) : launch<64, 1>(P, num_sms, s);
-    if (g.D == 128) return wide ? launch<128, 2>(P, num_sms, s) : launch<128, 1>(P, num_sms, s);
-    return launch<256, 1>(P, num_sms, s);
+    if (g.D == 64) return wide ? launch<64, 2>(P, ws, num_sms, s) : launch<64, 1>(P, ws, num_sms, s);
+    if (g.D == 128) return wide ? launch<128, 2>(P, ws, num_sms, s) : launch<128, 1>(P, ws, num_sms, s);
+    return launch<256, 1>(P, ws, num_sms, s);
 }
 
 }  // namespace pn

@@ -672,6 +672,7 @@ pn_status pn_attention(const uint16_t* q, int64_t q_stride, int64_t tokens, int 
     const pn::AttnArgs a{reinterpret_cast<const __half*>(q), q_stride, tokens, heads, table, table_stride, max_pages,
                          lens, starts, batch, max_queries, scale, window, sinks, reinterpret_cast<__half*>(out), lse};
     const pn::KvGeometry g{static_cast<uint8_t*>(const_cast<void*>(cache)), pages, page_size, kv_heads, head_dim};
+    if (!pn::attn_fits(a, g)) return PN_EUNSUPPORTED;
     const cudaError_t e = pn::launch_attention(a, g, workspace, sms, g_timeout_ns.load(), g_test_stall.load(),
                                                reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PN_OK : pn::cuda_error(e);
