@@ -204,249 +204,317 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams P) 
 
 // ----------------------------------------------------------------- append --
 //
-// One warp per head row.  Lane l owns the D / 32 consecutive values from
-// l * D / 32.  The arithmetic is fixed, every operation rounded by itself, so
-// codes are the same whatever computes them: squares added pairwise (the upper
-// half of the row to the lower, until one sum is left: lane exchanges 16 .. 1,
-// then within the lane), times 1 / D, plus eps, 1 / sqrt; x * that * weight;
-// rotation with separate products and sums; pn4t's rule per group of 64.
-// Bound by memory: each value is read once and written once.
+// D / 8 lanes to a head row, so a warp takes 32 / (D / 8) heads of a token at
+// once: lane l of a row owns values 4 l .. 4 l + 3 and D / 2 + 4 l .. + 3.
+// With that ownership the pairwise sum's first level, the rotation of whole
+// heads by halves and that of neighbours stay inside a lane, and a row's loads
+// are 16 bytes wide.  (A warp to a row with neighbouring values in a lane
+// exchanged each value at every level of the sum and its partner through
+// shared memory: 307 us for 8192 tokens of 48 + 16 heads of 128, bound by its
+// instructions.)  A warp stays with its token for several groups of heads, so
+// the rotation's row and the weights are read once.
+//
+// The arithmetic is fixed, every operation rounded by itself, so codes are the
+// same whatever computes them: squares added pairwise (the upper half of the
+// row to the lower, until one sum is left), times 1 / D, plus eps, 1 / sqrt;
+// x * that * weight; rotation with separate products and sums; pn4t's rule per
+// group of 64.  Bound by memory: each value is read once and written once.
 
-template <int E>
-__device__ __forceinline__ void load_row(const void* p, int64_t at, bool f16, bool wide, float (&x)[E]) {
+struct Quads {
+    float x[8];                                // values 4 l + i, then D / 2 + 4 l + i
+};
+
+__device__ __forceinline__ void load_quad(const void* p, int64_t at, bool f16, bool wide, float* x) {
     if (f16) {
         const __half* h = static_cast<const __half*>(p) + at;
         if (wide) {
-            uint32_t w[E / 2];
-            if constexpr (E == 2) w[0] = __ldcs(reinterpret_cast<const unsigned int*>(h));
-            if constexpr (E == 4) {
-                const uint2 v = __ldcs(reinterpret_cast<const uint2*>(h));
-                w[0] = v.x; w[1] = v.y;
-            }
-            if constexpr (E == 8) {
-                const uint4 v = __ldcs(reinterpret_cast<const uint4*>(h));
-                w[0] = v.x; w[1] = v.y; w[2] = v.z; w[3] = v.w;
-            }
-#pragma unroll
-            for (int i = 0; i < E / 2; ++i) {
-                x[2 * i] = half_bits_to_float(w[i] & 0xFFFFu);
-                x[2 * i + 1] = half_bits_to_float(w[i] >> 16);
-            }
+            const uint2 v = __ldcs(reinterpret_cast<const uint2*>(h));
+            x[0] = half_bits_to_float(v.x & 0xFFFFu);
+            x[1] = half_bits_to_float(v.x >> 16);
+            x[2] = half_bits_to_float(v.y & 0xFFFFu);
+            x[3] = half_bits_to_float(v.y >> 16);
         } else {
 #pragma unroll
-            for (int i = 0; i < E; ++i) x[i] = __half2float(h[i]);
+            for (int i = 0; i < 4; ++i) x[i] = __half2float(h[i]);
         }
     } else {
         const float* f = static_cast<const float*>(p) + at;
         if (wide) {
-            if constexpr (E == 2) {
-                const float2 v = __ldcs(reinterpret_cast<const float2*>(f));
-                x[0] = v.x; x[1] = v.y;
-            } else {
-#pragma unroll
-                for (int i = 0; i < E / 4; ++i) {
-                    const float4 v = __ldcs(reinterpret_cast<const float4*>(f) + i);
-                    x[4 * i] = v.x; x[4 * i + 1] = v.y; x[4 * i + 2] = v.z; x[4 * i + 3] = v.w;
-                }
-            }
+            const float4 v = __ldcs(reinterpret_cast<const float4*>(f));
+            x[0] = v.x; x[1] = v.y; x[2] = v.z; x[3] = v.w;
         } else {
 #pragma unroll
-            for (int i = 0; i < E; ++i) x[i] = f[i];
+            for (int i = 0; i < 4; ++i) x[i] = f[i];
         }
     }
 }
 
-template <int E>
-__device__ __forceinline__ void norm_row(float (&x)[E], const float* weight, float eps, int lane) {
-    float p[E];
+template <int D>
+__device__ __forceinline__ void norm_row(Quads& q, const float (&weight)[8], float eps) {
+    constexpr int L = D / 8;
+    float p[4];
 #pragma unroll
-    for (int i = 0; i < E; ++i) p[i] = __fmul_rn(x[i], x[i]);
+    for (int i = 0; i < 4; ++i) p[i] = __fadd_rn(__fmul_rn(q.x[i], q.x[i]), __fmul_rn(q.x[4 + i], q.x[4 + i]));
 #pragma unroll
-    for (int d = 16; d >= 1; d >>= 1)
+    for (int d = L / 2; d >= 1; d >>= 1)
 #pragma unroll
-        for (int i = 0; i < E; ++i) p[i] = __fadd_rn(p[i], __shfl_xor_sync(0xFFFFFFFFu, p[i], d));
+        for (int i = 0; i < 4; ++i) p[i] = __fadd_rn(p[i], __shfl_xor_sync(0xFFFFFFFFu, p[i], d));
+    const float sum = __fadd_rn(__fadd_rn(p[0], p[2]), __fadd_rn(p[1], p[3]));
+    const float inv = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fmul_rn(sum, 1.0f / D), eps)));
 #pragma unroll
-    for (int h = E / 2; h >= 1; h >>= 1)
-#pragma unroll
-        for (int i = 0; i < h; ++i) p[i] = __fadd_rn(p[i], p[i + h]);
-    const float inv = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fmul_rn(p[0], 1.0f / (32 * E)), eps)));
-#pragma unroll
-    for (int i = 0; i < E; ++i) x[i] = __fmul_rn(__fmul_rn(x[i], inv), weight[lane * E + i]);
+    for (int i = 0; i < 8; ++i) q.x[i] = __fmul_rn(__fmul_rn(q.x[i], inv), weight[i]);
 }
 
-// Rotates values 0 .. 2 half - 1 of the row; `row` is the warp's D floats of
-// shared memory (the partner of value i lies half values away).
-template <int E>
-__device__ __forceinline__ void rotate_row(float (&x)[E], const float* cos, const float* sin, int half, bool interleaved,
-                                           float* row, int lane) {
-    if (interleaved) {
+// How the rotation's pairs lie.
+enum { kTurnNone, kTurnHalves /* of the whole head: in a lane */, kTurnNeighbours, kTurnPart /* halves of a part */ };
+
+// What a lane needs of the row of cos and sin, for each of its values: the
+// pair's cos, and its sin with the sign of the value's product.
+struct Turn {
+    float c[8], s[8];
+};
+
+template <int D>
+__device__ __forceinline__ void load_turn(Turn& t, int kind, const float* cos, const float* sin, int half, int l) {
 #pragma unroll
-        for (int i = 0; i < E; i += 2) {
-            const int pair = (lane * E + i) >> 1;
-            if (pair < half) {
-                const float c = cos[pair], s = sin[pair], u = x[i], v = x[i + 1];
-                x[i] = __fsub_rn(__fmul_rn(u, c), __fmul_rn(v, s));
-                x[i + 1] = __fadd_rn(__fmul_rn(v, c), __fmul_rn(u, s));
-            }
+    for (int i = 0; i < 8; ++i) {
+        const int at = (i < 4 ? 0 : D / 2) + 4 * l + (i & 3);
+        int pair;
+        bool second;
+        if (kind == kTurnNeighbours) {
+            pair = at >> 1;
+            second = at & 1;
+        } else {
+            second = at >= half;
+            pair = second ? at - half : at;
         }
+        const bool turns = kind == kTurnNeighbours ? pair < half : at < 2 * half;
+        t.c[i] = turns ? cos[pair] : 1.0f;
+        t.s[i] = turns ? (second ? sin[pair] : -sin[pair]) : 0.0f;
+    }
+}
+
+// (a, b) -> (a c - b s, b c + a s), products and sums rounded one by one;
+// a c - b s = a c + b (-s) exactly so.  `row` is D floats of shared memory per
+// row (kTurnPart only).  Values outside the rotated part stay as they are.
+template <int D>
+__device__ __forceinline__ void rotate_row(Quads& q, const Turn& t, int kind, int half, float* row, int l) {
+    float partner[8];
+    if (kind == kTurnHalves) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) partner[i] = q.x[i ^ 4];
+    } else if (kind == kTurnNeighbours) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) partner[i] = q.x[i ^ 1];
     } else {
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < E; ++i) row[lane * E + i] = x[i];
+        for (int i = 0; i < 8; ++i) row[(i < 4 ? 0 : D / 2) + 4 * l + (i & 3)] = q.x[i];
         __syncwarp();
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-            const int at = lane * E + i;
-            if (at < half) x[i] = __fsub_rn(__fmul_rn(x[i], cos[at]), __fmul_rn(row[at + half], sin[at]));
-            else if (at < 2 * half) x[i] = __fadd_rn(__fmul_rn(x[i], cos[at - half]), __fmul_rn(row[at - half], sin[at - half]));
+        for (int i = 0; i < 8; ++i) {
+            const int at = (i < 4 ? 0 : D / 2) + 4 * l + (i & 3);
+            partner[i] = at < half ? row[at + half] : at < 2 * half ? row[at - half] : 0.0f;
         }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int at = (i < 4 ? 0 : D / 2) + 4 * l + (i & 3);
+        if (at < 2 * half) q.x[i] = __fadd_rn(__fmul_rn(q.x[i], t.c[i]), __fmul_rn(partner[i], t.s[i]));
     }
 }
 
-// pn4t's rule on the row's groups of 64 (2048 / D lanes each): d = fp16 of the
-// first largest-magnitude value / -8, codes clamp(rint(x / d), -8, 7) + 8.
-// Returns the group's scale bits; codes in n.
-template <int E>
-__device__ __forceinline__ uint32_t quantise_row(const float (&x)[E], int (&n)[E], int lane) {
-    constexpr int kLanes = 64 / E;             // lanes of a group
-    uint32_t top = 0;
+__device__ __forceinline__ float first_of_size(const float* x, uint32_t size) {
+    float v = x[3];
 #pragma unroll
-    for (int i = 0; i < E; ++i) top = max(top, __float_as_uint(x[i]) & 0x7FFFFFFFu);
-    uint32_t best = top;
-#pragma unroll
-    for (int d = kLanes / 2; d >= 1; d >>= 1) best = max(best, __shfl_xor_sync(0xFFFFFFFFu, best, d));
-    float v = 0.0f;                            // the lane's first value of that size
-#pragma unroll
-    for (int i = E - 1; i >= 0; --i)
-        if ((__float_as_uint(x[i]) & 0x7FFFFFFFu) == best) v = x[i];
-    const uint32_t has = __ballot_sync(0xFFFFFFFFu, top == best);
-    const uint32_t group = kLanes == 32 ? 0xFFFFFFFFu : ((1u << (kLanes & 31)) - 1u) << (lane / kLanes * kLanes);
-    v = __shfl_sync(0xFFFFFFFFu, v, __ffs(has & group) - 1);
-    const float q = fminf(fmaxf(__fmul_rn(v, -0.125f), -65504.0f), 65504.0f);
-    uint32_t bits = __half_as_ushort(__float2half_rn(q));
-    const bool zero = (bits & 0x7FFFu) == 0;
-    if (zero) bits = 0;
+    for (int i = 2; i >= 0; --i)
+        if ((__float_as_uint(x[i]) & 0x7FFFFFFFu) == size) v = x[i];
+    return v;
+}
+
+// The scale (fp16 bits) of a group whose first largest-magnitude value is v.
+__device__ __forceinline__ uint32_t scale_bits(float v) {
+    const uint32_t bits = __half_as_ushort(__float2half_rn(fminf(fmaxf(__fmul_rn(v, -0.125f), -65504.0f), 65504.0f)));
+    return (bits & 0x7FFFu) ? bits : 0u;
+}
+
+// Codes clamp(rint(x / d), -8, 7) + 8 of four values at places c0 .. c0 + 3 of a word.
+__device__ __forceinline__ uint32_t half_word(const float* x, uint32_t bits, int c0) {
     const float d = half_bits_to_float(bits);
+    uint32_t w = 0;
 #pragma unroll
-    for (int i = 0; i < E; ++i) {
-        const float r = zero ? 0.0f : fminf(fmaxf(rintf(__fdiv_rn(x[i], d)), -8.0f), 7.0f);
-        n[i] = static_cast<int>(r) + 8;
+    for (int i = 0; i < 4; ++i) {
+        const float r = bits ? fminf(fmaxf(rintf(__fdiv_rn(x[i], d)), -8.0f), 7.0f) : 0.0f;
+        const int c = c0 + i;
+        w |= static_cast<uint32_t>(static_cast<int>(r) + 8) << (16 * (c & 1) + 4 * (c >> 1));
     }
-    return bits;
+    return w;
+}
+
+// The lanes' 64-value groups by pn4t's rule.  D >= 128: a group is 16 lanes'
+// first or second four values; D = 64: eight lanes' both.
+template <int D>
+__device__ __forceinline__ void group_scales(const Quads& q, uint32_t (&bits)[2]) {
+    constexpr int kSpan = D == 64 ? 8 : 16;
+    const int lane = threadIdx.x & 31;
+    const uint32_t members = ((1u << kSpan) - 1u) << (lane / kSpan * kSpan);
+    uint32_t top[2], best[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        top[k] = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) top[k] = max(top[k], __float_as_uint(q.x[4 * k + i]) & 0x7FFFFFFFu);
+        best[k] = top[k];
+#pragma unroll
+        for (int d = kSpan / 2; d >= 1; d >>= 1) best[k] = max(best[k], __shfl_xor_sync(0xFFFFFFFFu, best[k], d));
+    }
+    if constexpr (D == 64) best[0] = best[1] = max(best[0], best[1]);
+    float v[2];
+    uint32_t has[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        has[k] = __ballot_sync(0xFFFFFFFFu, top[k] == best[k]) & members;
+        v[k] = __shfl_sync(0xFFFFFFFFu, first_of_size(q.x + 4 * k, best[k]), has[k] ? __ffs(has[k]) - 1 : lane);
+    }
+    if constexpr (D == 64) v[0] = v[1] = has[0] ? v[0] : v[1];     // values 0 .. 31 come first
+    bits[0] = scale_bits(v[0]);
+    bits[1] = scale_bits(v[1]);
 }
 
 struct AppendParams {
     KvAppendArgs a;
     KvCache cache;
-    int64_t rows;              // tokens * (heads + 2 kv heads)
+    int turn;                  // kTurn...
+    int q_sets, kv_sets;       // groups of heads (32 / (D / 8) each) per token, of q and of k or v
+    int sets;                  // groups that one warp takes, of one kind
+    int q_tasks, kv_tasks;     // warps per token, of q and of k or v
+    int64_t tasks;             // warps' worth of work
     bool wide_q, wide_k, wide_v;
 };
 
 constexpr int kAppendWarps = 8;
 
 template <int D>
-__global__ void __launch_bounds__(kAppendWarps * 32) append_kernel(const AppendParams P) {
-    constexpr int E = D / 32;
-    __shared__ float rows[kAppendWarps][D];
+__global__ void __launch_bounds__(kAppendWarps * 32, 3) append_kernel(const AppendParams P) {
+    constexpr int L = D / 8, kRows = 32 / L;   // lanes to a row, rows to a warp
+    __shared__ float rows[kAppendWarps][kRows * D];
     const KvAppendArgs& a = P.a;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int per = a.heads + 2 * P.cache.heads;
-    for (int64_t row = static_cast<int64_t>(blockIdx.x) * kAppendWarps + warp; row < P.rows;
-         row += static_cast<int64_t>(gridDim.x) * kAppendWarps) {
-        const int64_t t = row / per;
-        const int r = static_cast<int>(row - t * per);
-        const bool is_q = r < a.heads, is_v = r >= a.heads + P.cache.heads;
-        const int h = is_q ? r : is_v ? r - a.heads - P.cache.heads : r - a.heads;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % L, sub = lane / L;
+    const int per = P.q_tasks + 2 * P.kv_tasks;
+    for (int64_t task = static_cast<int64_t>(blockIdx.x) * kAppendWarps + warp; task < P.tasks;
+         task += static_cast<int64_t>(gridDim.x) * kAppendWarps) {
+        const int64_t t = task / per;
+        int kind = static_cast<int>(task - t * per);
+        const bool is_q = kind < P.q_tasks, is_v = kind >= P.q_tasks + P.kv_tasks;
+        if (!is_q) kind -= is_v ? P.q_tasks + P.kv_tasks : P.q_tasks;
         const int64_t slot = is_q ? 0 : a.slots[t];
-        if (!is_q && (slot < 0 || slot >= P.cache.slots())) continue;   // the whole warp
-        float x[E];
+        if (!is_q && (slot < 0 || slot >= P.cache.slots())) continue;      // the whole warp
+        const int heads = is_q ? a.heads : P.cache.heads;
+        const int set0 = kind * P.sets, set1 = min(set0 + P.sets, is_q ? P.q_sets : P.kv_sets);
         const void* src = is_q ? a.q : is_v ? a.v : a.k;
-        const int64_t stride = is_q ? a.q_stride : is_v ? a.v_stride : a.k_stride;
-        load_row<E>(src, t * stride + h * D + lane * E, a.f16, is_q ? P.wide_q : is_v ? P.wide_v : P.wide_k, x);
-        if (!is_v) {
-            const float* weight = is_q ? a.q_weight : a.k_weight;
-            if (weight) norm_row<E>(x, weight, a.eps, lane);
-            if (a.half) {
-                const int pos = a.positions[t];
-                if (pos >= 0 && pos < a.table_rows)
-                    rotate_row<E>(x, a.cos + static_cast<int64_t>(pos) * a.half, a.sin + static_cast<int64_t>(pos) * a.half, a.half,
-                                  a.interleaved, rows[warp], lane);
+        const bool wide = is_q ? P.wide_q : is_v ? P.wide_v : P.wide_k;
+        const int64_t base = t * (is_q ? a.q_stride : is_v ? a.v_stride : a.k_stride);
+        auto load = [&](Quads& q, int set) {
+            const int h = min(set * kRows + sub, heads - 1);               // rows past the last head repeat it
+            load_quad(src, base + h * D + 4 * l, a.f16, wide, q.x);
+            load_quad(src, base + h * D + D / 2 + 4 * l, a.f16, wide, q.x + 4);
+        };
+        Quads next;
+        load(next, set0);
+        const float* weight = is_v ? nullptr : is_q ? a.q_weight : a.k_weight;
+        float w[8];
+        if (weight) {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) w[i] = weight[(i < 4 ? 0 : D / 2) + 4 * l + (i & 3)];
+        }
+        int turn = is_v ? kTurnNone : P.turn;
+        Turn tn;
+        if (turn != kTurnNone) {
+            const int pos = a.positions[t];
+            if (pos < 0 || pos >= a.table_rows) turn = kTurnNone;
+            else load_turn<D>(tn, turn, a.cos + static_cast<int64_t>(pos) * a.half, a.sin + static_cast<int64_t>(pos) * a.half, a.half, l);
+        }
+        for (int set = set0; set < set1; ++set) {
+            Quads q = next;
+            if (set + 1 < set1) load(next, set + 1);
+            if (weight) norm_row<D>(q, w, a.eps);
+            if (turn != kTurnNone) rotate_row<D>(q, tn, turn, a.half, rows[warp] + sub * D, l);
+            const int h = set * kRows + sub;
+            if (is_q) {
+                if (h < heads) {
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const __half2 lo = __floats2half2_rn(q.x[4 * k], q.x[4 * k + 1]), hi = __floats2half2_rn(q.x[4 * k + 2], q.x[4 * k + 3]);
+                        *reinterpret_cast<uint2*>(a.q_out + (t * a.heads + h) * D + k * (D / 2) + 4 * l) =
+                            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+                    }
+                }
+                continue;
             }
-        }
-        if (is_q) {
-            __half2* out = reinterpret_cast<__half2*>(a.q_out + (t * a.heads + h) * D + lane * E);
-#pragma unroll
-            for (int i = 0; i < E / 2; ++i) out[i] = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
-            continue;
-        }
-        int n[E];
-        const uint32_t bits = quantise_row<E>(x, n, lane);
-        // code c of a word: half c & 1, bit 4 (c >> 1)
-        uint32_t w = 0;
-        const int c0 = (lane * E) & 7;
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-            const int c = c0 + i;
-            w |= static_cast<uint32_t>(n[i]) << (16 * (c & 1) + 4 * (c >> 1));
-        }
-#pragma unroll
-        for (int d = 1; d < 8 / E; d <<= 1) w |= __shfl_xor_sync(0xFFFFFFFFu, w, d);
-        uint8_t* rec = P.cache.record(slot, h);
-        const int tok = static_cast<int>(slot) & 15, j = lane * E / 64, i = (lane * E % 64) >> 3;
-        if (c0 == 0) {
-            const int off = is_v ? kv_v_word<D>(tok, j, i) : kv_k_word<D>(tok, j, i);
-            *reinterpret_cast<uint32_t*>(rec + off) = w;
-        }
-        if (lane * E % 64 == 0) {
-            const int off = (is_v ? kv_v_scales(D) : kv_k_scales(D)) + (tok * (D / 64) + j) * 2;
-            *reinterpret_cast<uint16_t*>(rec + off) = static_cast<uint16_t>(bits);
+            uint32_t bits[2];
+            group_scales<D>(q, bits);
+            // two lanes to a word: the even one puts the first half's together, the odd one the second's
+            const bool odd = l & 1;
+            const int c0 = odd ? 4 : 0;
+            const uint32_t w0 = half_word(q.x, bits[0], c0), w1 = half_word(q.x + 4, bits[1], c0);
+            const uint32_t word = (odd ? w1 : w0) | __shfl_xor_sync(0xFFFFFFFFu, odd ? w0 : w1, 1);
+            if (h < heads) {
+                uint8_t* rec = P.cache.record(slot, h);
+                const int tok = static_cast<int>(slot) & 15;
+                const int at = (odd ? D / 2 : 0) + 4 * (l & ~1), j = at / 64, i = (at % 64) / 8;
+                *reinterpret_cast<uint32_t*>(rec + (is_v ? kv_v_word<D>(tok, j, i) : kv_k_word<D>(tok, j, i))) = word;
+                if (D == 64 ? l == 0 : l % 16 == 0) {
+                    uint8_t* sc = rec + (is_v ? kv_v_scales(D) : kv_k_scales(D)) + tok * (D / 64) * 2;
+                    *reinterpret_cast<uint16_t*>(sc + 2 * (4 * l / 64)) = static_cast<uint16_t>(bits[0]);
+                    if (D > 64) *reinterpret_cast<uint16_t*>(sc + 2 * ((D / 2 + 4 * l) / 64)) = static_cast<uint16_t>(bits[1]);
+                }
+            }
         }
     }
 }
 
 // ------------------------------------------------------------------- read --
+//
+// A lane to a code word: eight values, two 16-byte stores.
 
 struct ReadParams {
     KvCache cache;
     const int64_t* slots;
-    int64_t rows;              // tokens * kv heads * 2
+    int64_t words;             // tokens * kv heads * D / 8
     float* k;
     float* v;
 };
 
 template <int D>
 __global__ void __launch_bounds__(256) read_kernel(const ReadParams P) {
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
-    for (int64_t row = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5); row < P.rows;
-         row += static_cast<int64_t>(gridDim.x) * 8) {
-        const int64_t th = row >> 1;
-        const bool is_v = row & 1;
+    constexpr int kWords = D / 8;
+    const int64_t stride = static_cast<int64_t>(gridDim.x) * 256;
+    for (int64_t n = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; n < P.words; n += stride) {
+        const int64_t th = n / kWords;
+        const int at = static_cast<int>(n % kWords), j = at / 8, i = at % 8;
         const int64_t t = th / P.cache.heads;
         const int h = static_cast<int>(th - t * P.cache.heads);
         const int64_t slot = P.slots[t];
-        float x[E];
-        if (slot < 0 || slot >= P.cache.slots()) {
-#pragma unroll
-            for (int i = 0; i < E; ++i) x[i] = 0.0f;
-        } else {
-            const uint8_t* rec = P.cache.record(slot, h);
-            const int tok = static_cast<int>(slot) & 15, j = lane * E / 64, i = (lane * E % 64) >> 3;
-            const uint32_t w = *reinterpret_cast<const uint32_t*>(rec + (is_v ? kv_v_word<D>(tok, j, i) : kv_k_word<D>(tok, j, i)));
-            const float d = lds_half_as_float(rec + (is_v ? kv_v_scales(D) : kv_k_scales(D)) + (tok * (D / 64) + j) * 2);
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                const int c = ((lane * E) & 7) + e;
-                x[e] = __fmul_rn(d, static_cast<float>(static_cast<int>((w >> (16 * (c & 1) + 4 * (c >> 1))) & 15u) - 8));
-            }
+        const bool real = slot >= 0 && slot < P.cache.slots();
+        const uint8_t* rec = P.cache.record(real ? slot : 0, h);
+        const int tok = static_cast<int>(slot) & 15;
+        uint32_t w[2] = {0, 0};
+        float d[2] = {0.0f, 0.0f};
+        if (real) {
+            w[0] = *reinterpret_cast<const uint32_t*>(rec + kv_k_word<D>(tok, j, i));
+            w[1] = *reinterpret_cast<const uint32_t*>(rec + kv_v_word<D>(tok, j, i));
+            d[0] = lds_half_as_float(rec + kv_k_scales(D) + (tok * (D / 64) + j) * 2);
+            d[1] = lds_half_as_float(rec + kv_v_scales(D) + (tok * (D / 64) + j) * 2);
         }
-        float* out = (is_v ? P.v : P.k) + th * D + lane * E;
-        if constexpr (E == 2) {
-            *reinterpret_cast<float2*>(out) = make_float2(x[0], x[1]);
-        } else {
 #pragma unroll
-            for (int i = 0; i < E / 4; ++i)
-                reinterpret_cast<float4*>(out)[i] = make_float4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+        for (int k = 0; k < 2; ++k) {
+            float x[8];
+#pragma unroll
+            for (int c = 0; c < 8; ++c)
+                x[c] = real ? __fmul_rn(d[k], static_cast<float>(static_cast<int>((w[k] >> (16 * (c & 1) + 4 * (c >> 1))) & 15u) - 8)) : 0.0f;
+            float4* out = reinterpret_cast<float4*>((k ? P.v : P.k) + th * D + at * 8);
+            __stcs(out, make_float4(x[0], x[1], x[2], x[3]));
+            __stcs(out + 1, make_float4(x[4], x[5], x[6], x[7]));
         }
     }
 }
@@ -476,8 +544,9 @@ cudaError_t launch_kv_plan(const KvPlanArgs& a, int num_sms, cudaStream_t s) {
     static std::atomic<uint64_t> smem_set{0};
     if (smem > 40 * 1024)
         if (cudaError_t e = set_smem_limit_once(plan_kernel, (2 * kKvMaxBatch + 1) * 4, smem_set); e != cudaSuccess) return e;
-    int64_t blocks = (a.capacity + threads * 4 - 1) / (threads * 4);
-    const int64_t by_request = (a.batch + 255) / 256;
+    // a token to a thread and, for the table, a request to a warp, as far as one wave of blocks goes
+    int64_t blocks = (a.capacity + threads - 1) / threads;
+    const int64_t by_request = (a.batch + threads / 32 - 1) / (threads / 32);
     blocks = blocks > by_request ? blocks : by_request;
     if (blocks > num_sms) blocks = num_sms;
     if (blocks < 1) blocks = 1;
@@ -486,14 +555,24 @@ cudaError_t launch_kv_plan(const KvPlanArgs& a, int num_sms, cudaStream_t s) {
 }
 
 cudaError_t launch_kv_append(const KvAppendArgs& a, const KvGeometry& g, int num_sms, cudaStream_t s) {
-    AppendParams P{a, cache_of(g), a.tokens * (a.heads + 2 * static_cast<int64_t>(g.heads)), false, false, false};
+    AppendParams P{a, cache_of(g)};
+    P.turn = a.half == 0 ? kTurnNone : a.interleaved ? kTurnNeighbours : a.half == g.D / 2 ? kTurnHalves : kTurnPart;
+    const int rows = 32 / (g.D / 8);
+    P.q_sets = (a.heads + rows - 1) / rows;
+    P.kv_sets = (g.heads + rows - 1) / rows;
+    // as many groups of heads to a warp as leave every SM its 32 warps, 8 at most
+    const int64_t all = a.tokens * (P.q_sets + 2 * static_cast<int64_t>(P.kv_sets));
+    P.sets = 1;
+    while (P.sets < 8 && all >= static_cast<int64_t>(num_sms) * 32 * P.sets * 2) P.sets *= 2;
+    P.q_tasks = (P.q_sets + P.sets - 1) / P.sets;
+    P.kv_tasks = (P.kv_sets + P.sets - 1) / P.sets;
+    P.tasks = a.tokens * (P.q_tasks + 2 * static_cast<int64_t>(P.kv_tasks));
     const int size = a.f16 ? 2 : 4;
-    const int bytes = g.D / 32 * size < 16 ? g.D / 32 * size : 16;
-    P.wide_q = rows_aligned(a.q, a.q_stride, size, bytes);
-    P.wide_k = rows_aligned(a.k, a.k_stride, size, bytes);
-    P.wide_v = rows_aligned(a.v, a.v_stride, size, bytes);
-    int64_t blocks = (P.rows + kAppendWarps - 1) / kAppendWarps;
-    if (blocks > static_cast<int64_t>(num_sms) * 8) blocks = static_cast<int64_t>(num_sms) * 8;
+    P.wide_q = rows_aligned(a.q, a.q_stride, size, 4 * size);
+    P.wide_k = rows_aligned(a.k, a.k_stride, size, 4 * size);
+    P.wide_v = rows_aligned(a.v, a.v_stride, size, 4 * size);
+    int64_t blocks = (P.tasks + kAppendWarps - 1) / kAppendWarps;
+    if (blocks > (1 << 30)) blocks = 1 << 30;
     const int grid = static_cast<int>(blocks);
     if (g.D == 64) append_kernel<64><<<grid, kAppendWarps * 32, 0, s>>>(P);
     else if (g.D == 128) append_kernel<128><<<grid, kAppendWarps * 32, 0, s>>>(P);
@@ -503,9 +582,9 @@ cudaError_t launch_kv_append(const KvAppendArgs& a, const KvGeometry& g, int num
 
 cudaError_t launch_kv_read(const KvGeometry& g, const int64_t* slots, int64_t tokens, float* k, float* v, int num_sms,
                            cudaStream_t s) {
-    ReadParams P{cache_of(g), slots, tokens * g.heads * 2, k, v};
-    int64_t blocks = (P.rows + 7) / 8;
-    if (blocks > static_cast<int64_t>(num_sms) * 8) blocks = static_cast<int64_t>(num_sms) * 8;
+    ReadParams P{cache_of(g), slots, tokens * g.heads * (g.D / 8), k, v};
+    int64_t blocks = (P.words + 255) / 256;
+    if (blocks > static_cast<int64_t>(num_sms) * 64) blocks = static_cast<int64_t>(num_sms) * 64;
     const int grid = static_cast<int>(blocks);
     if (g.D == 64) read_kernel<64><<<grid, 256, 0, s>>>(P);
     else if (g.D == 128) read_kernel<128><<<grid, 256, 0, s>>>(P);

@@ -10,8 +10,9 @@
 //
 // Bound by the read of that one row (two with q): a cluster of thread blocks
 // shares it.  Each warp sums a contiguous part; block sums meet through
-// distributed shared memory; the warp whose part holds the threshold walks it
-// once more (from L2) to the token.
+// distributed shared memory; in the warp whose part holds the threshold each
+// lane sums a contiguous 32nd of it once more (from L2), then the warp walks
+// the one 32nd that holds the token.
 #include <cooperative_groups.h>
 #include <cstdint>
 
@@ -24,7 +25,7 @@ namespace cg = cooperative_groups;
 namespace pn {
 namespace {
 
-constexpr int kVerifyThreads = 512;
+constexpr int kVerifyThreads = 256;             // four blocks to an SM: 64 requests of 8 blocks run at once
 constexpr int kVerifyWarps = kVerifyThreads / 32;
 constexpr int kVerifyCluster = 8;
 
@@ -45,13 +46,30 @@ __device__ __forceinline__ int64_t weight(const Row& r, int j) {
     return j == r.skip ? 0 : whole(p);
 }
 
+// The sum of weights j0 + lane * 4 .. of every 128th four; rows 16-byte aligned, j0 and j1 multiples of 4.
+__device__ __forceinline__ int64_t sum_fours(const Row& r, int j0, int j1, int lane) {
+    int64_t s = 0;
+#pragma unroll 4
+    for (int j = j0 + 4 * lane; j < j1; j += 128) {
+        const float4 p = __ldcg(reinterpret_cast<const float4*>(r.p + j));
+        if (r.q) {
+            const float4 q = __ldcg(reinterpret_cast<const float4*>(r.q + j));
+            s += whole(__fsub_rn(p.x, q.x)) + whole(__fsub_rn(p.y, q.y)) + whole(__fsub_rn(p.z, q.z)) + whole(__fsub_rn(p.w, q.w));
+        } else {
+            s += (j == r.skip ? 0 : whole(p.x)) + (j + 1 == r.skip ? 0 : whole(p.y)) + (j + 2 == r.skip ? 0 : whole(p.z)) +
+                 (j + 3 == r.skip ? 0 : whole(p.w));
+        }
+    }
+    return s;
+}
+
 __device__ __forceinline__ int64_t warp_sum(int64_t v) {
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
     return v;
 }
 
-__global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyArgs a) {
+__global__ void __launch_bounds__(kVerifyThreads, 4) verify_kernel(const VerifyArgs a) {
     cg::cluster_group cluster = cg::this_cluster();
     __shared__ int64_t sums[kVerifyWarps];
     __shared__ int64_t block_total[2];
@@ -94,8 +112,13 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyArgs
     const float u = a.uniforms[static_cast<int64_t>(b) * (K + 1) + K];
     for (int pass = 0; pass < 2; ++pass) {
         int64_t s = 0;
+        // fours where both rows lie for it (vocab a multiple of 4, so the parts are too)
+        if (V % 4 == 0 && ((reinterpret_cast<uintptr_t>(row.p) | reinterpret_cast<uintptr_t>(row.q)) & 15) == 0) {
+            s = sum_fours(row, j0, j1, lane);
+        } else {
 #pragma unroll 8
-        for (int j = j0 + lane; j < j1; j += 32) s += weight(row, j);
+            for (int j = j0 + lane; j < j1; j += 32) s += weight(row, j);
+        }
         s = warp_sum(s);
         if (lane == 0) sums[warp] = s;
         __syncthreads();
@@ -125,14 +148,25 @@ __global__ void __launch_bounds__(kVerifyThreads) verify_kernel(const VerifyArgs
         at = min(max(at, static_cast<int64_t>(0)), total - 1);
         for (int w = 0; w < warp; ++w) before += sums[w];
         if (at >= before && at < before + s) {     // this warp's part (s > 0) holds it
-            for (int j = j0; j < j1; j += 32) {
-                const int64_t w = j + lane < j1 ? weight(row, j + lane) : 0;
-                int64_t in = w;
+            auto scan = [&](int64_t v) {
 #pragma unroll
                 for (int d = 1; d < 32; d <<= 1) {
-                    const int64_t o = __shfl_up_sync(0xFFFFFFFFu, in, d);
-                    if (lane >= d) in += o;
+                    const int64_t o = __shfl_up_sync(0xFFFFFFFFu, v, d);
+                    if (lane >= d) v += o;
                 }
+                return v;
+            };
+            const int piece = (j1 - j0 + 31) / 32;
+            const int k0 = min(j0 + lane * piece, j1), k1 = min(k0 + piece, j1);
+            int64_t mine = 0;
+#pragma unroll 8
+            for (int j = k0; j < k1; ++j) mine += weight(row, j);
+            const int64_t upto = scan(mine);
+            const int owner = __ffs(__ballot_sync(0xFFFFFFFFu, before + upto > at)) - 1;
+            before += __shfl_sync(0xFFFFFFFFu, upto - mine, owner);
+            const int m0 = __shfl_sync(0xFFFFFFFFu, k0, owner), m1 = __shfl_sync(0xFFFFFFFFu, k1, owner);
+            for (int j = m0; j < m1; j += 32) {
+                const int64_t in = scan(j + lane < m1 ? weight(row, j + lane) : 0);
                 const uint32_t past = __ballot_sync(0xFFFFFFFFu, before + in > at);
                 if (past) {
                     if (lane == 0) out[accepted] = j + __ffs(past) - 1;
