@@ -224,6 +224,19 @@ struct Quads {
     float x[8];                                // values 4 l + i, then D / 2 + 4 l + i
 };
 
+// Two fp32 operations in one instruction.  No packed product may meet a packed
+// sum: the assembler joins the two (also where the product is written as an
+// fma of -0) and the product's own rounding is lost; products that are added
+// are scalar ones.
+__device__ __forceinline__ void mul2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmul.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d0), "=f"(d1) : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+__device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1, float b0, float b1) {
+    asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tadd.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d0), "=f"(d1) : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
+}
+
 __device__ __forceinline__ void load_quad(const void* p, int64_t at, bool f16, bool wide, float* x) {
     if (f16) {
         const __half* h = static_cast<const __half*>(p) + at;
@@ -252,17 +265,23 @@ __device__ __forceinline__ void load_quad(const void* p, int64_t at, bool f16, b
 template <int D>
 __device__ __forceinline__ void norm_row(Quads& q, const float (&weight)[8], float eps) {
     constexpr int L = D / 8;
-    float p[4];
+    float p[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) p[i] = __fadd_rn(__fmul_rn(q.x[i], q.x[i]), __fmul_rn(q.x[4 + i], q.x[4 + i]));
+    for (int i = 0; i < 8; ++i) p[i] = __fmul_rn(q.x[i], q.x[i]);
+#pragma unroll
+    for (int i = 0; i < 4; i += 2) add2(p[i], p[i + 1], p[i], p[i + 1], p[4 + i], p[5 + i]);
 #pragma unroll
     for (int d = L / 2; d >= 1; d >>= 1)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p[i] = __fadd_rn(p[i], __shfl_xor_sync(0xFFFFFFFFu, p[i], d));
+        for (int i = 0; i < 4; i += 2)
+            add2(p[i], p[i + 1], p[i], p[i + 1], __shfl_xor_sync(0xFFFFFFFFu, p[i], d), __shfl_xor_sync(0xFFFFFFFFu, p[i + 1], d));
     const float sum = __fadd_rn(__fadd_rn(p[0], p[2]), __fadd_rn(p[1], p[3]));
-    const float inv = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fmul_rn(sum, 1.0f / D), eps)));
+    const float inv = __frcp_rn(__fsqrt_rn(__fadd_rn(__fmul_rn(sum, 1.0f / D), eps)));   // correctly rounded, as 1 / x is
 #pragma unroll
-    for (int i = 0; i < 8; ++i) q.x[i] = __fmul_rn(__fmul_rn(q.x[i], inv), weight[i]);
+    for (int i = 0; i < 8; i += 2) {
+        mul2(q.x[i], q.x[i + 1], q.x[i], q.x[i + 1], inv, inv);
+        mul2(q.x[i], q.x[i + 1], q.x[i], q.x[i + 1], weight[i], weight[i + 1]);
+    }
 }
 
 // How the rotation's pairs lie.
@@ -274,21 +293,21 @@ struct Turn {
     float c[8], s[8];
 };
 
-template <int D>
-__device__ __forceinline__ void load_turn(Turn& t, int kind, const float* cos, const float* sin, int half, int l) {
+template <int D, int TURN>
+__device__ __forceinline__ void load_turn(Turn& t, const float* cos, const float* sin, int half, int l) {
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const int at = (i < 4 ? 0 : D / 2) + 4 * l + (i & 3);
         int pair;
         bool second;
-        if (kind == kTurnNeighbours) {
+        if (TURN == kTurnNeighbours) {
             pair = at >> 1;
             second = at & 1;
         } else {
             second = at >= half;
             pair = second ? at - half : at;
         }
-        const bool turns = kind == kTurnNeighbours ? pair < half : at < 2 * half;
+        const bool turns = TURN == kTurnNeighbours ? pair < half : at < 2 * half;
         t.c[i] = turns ? cos[pair] : 1.0f;
         t.s[i] = turns ? (second ? sin[pair] : -sin[pair]) : 0.0f;
     }
@@ -297,13 +316,13 @@ __device__ __forceinline__ void load_turn(Turn& t, int kind, const float* cos, c
 // (a, b) -> (a c - b s, b c + a s), products and sums rounded one by one;
 // a c - b s = a c + b (-s) exactly so.  `row` is D floats of shared memory per
 // row (kTurnPart only).  Values outside the rotated part stay as they are.
-template <int D>
-__device__ __forceinline__ void rotate_row(Quads& q, const Turn& t, int kind, int half, float* row, int l) {
+template <int D, int TURN>
+__device__ __forceinline__ void rotate_row(Quads& q, const Turn& t, int half, float* row, int l) {
     float partner[8];
-    if (kind == kTurnHalves) {
+    if (TURN == kTurnHalves) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) partner[i] = q.x[i ^ 4];
-    } else if (kind == kTurnNeighbours) {
+    } else if (TURN == kTurnNeighbours) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) partner[i] = q.x[i ^ 1];
     } else {
@@ -317,10 +336,14 @@ __device__ __forceinline__ void rotate_row(Quads& q, const Turn& t, int kind, in
             partner[i] = at < half ? row[at + half] : at < 2 * half ? row[at - half] : 0.0f;
         }
     }
+    // (a pair's two values turn or stay together: 2 half is even)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 8; i += 2) {
         const int at = (i < 4 ? 0 : D / 2) + 4 * l + (i & 3);
-        if (at < 2 * half) q.x[i] = __fadd_rn(__fmul_rn(q.x[i], t.c[i]), __fmul_rn(partner[i], t.s[i]));
+        if (TURN == kTurnHalves || at < 2 * half) {
+            add2(q.x[i], q.x[i + 1], __fmul_rn(q.x[i], t.c[i]), __fmul_rn(q.x[i + 1], t.c[i + 1]), __fmul_rn(partner[i], t.s[i]),
+                 __fmul_rn(partner[i + 1], t.s[i + 1]));
+        }
     }
 }
 
@@ -384,7 +407,6 @@ __device__ __forceinline__ void group_scales(const Quads& q, uint32_t (&bits)[2]
 struct AppendParams {
     KvAppendArgs a;
     KvCache cache;
-    int turn;                  // kTurn...
     int q_sets, kv_sets;       // groups of heads (32 / (D / 8) each) per token, of q and of k or v
     int sets;                  // groups that one warp takes, of one kind
     int q_tasks, kv_tasks;     // warps per token, of q and of k or v
@@ -394,10 +416,10 @@ struct AppendParams {
 
 constexpr int kAppendWarps = 8;
 
-template <int D>
+template <int D, bool F16, int TURN>
 __global__ void __launch_bounds__(kAppendWarps * 32, 3) append_kernel(const AppendParams P) {
     constexpr int L = D / 8, kRows = 32 / L;   // lanes to a row, rows to a warp
-    __shared__ float rows[kAppendWarps][kRows * D];
+    __shared__ float rows[TURN == kTurnPart ? kAppendWarps : 1][kRows * D];
     const KvAppendArgs& a = P.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % L, sub = lane / L;
     const int per = P.q_tasks + 2 * P.kv_tasks;
@@ -416,8 +438,8 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 3) append_kernel(const Appe
         const int64_t base = t * (is_q ? a.q_stride : is_v ? a.v_stride : a.k_stride);
         auto load = [&](Quads& q, int set) {
             const int h = min(set * kRows + sub, heads - 1);               // rows past the last head repeat it
-            load_quad(src, base + h * D + 4 * l, a.f16, wide, q.x);
-            load_quad(src, base + h * D + D / 2 + 4 * l, a.f16, wide, q.x + 4);
+            load_quad(src, base + h * D + 4 * l, F16, wide, q.x);
+            load_quad(src, base + h * D + D / 2 + 4 * l, F16, wide, q.x + 4);
         };
         Quads next;
         load(next, set0);
@@ -427,28 +449,29 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 3) append_kernel(const Appe
 #pragma unroll
             for (int i = 0; i < 8; ++i) w[i] = weight[(i < 4 ? 0 : D / 2) + 4 * l + (i & 3)];
         }
-        int turn = is_v ? kTurnNone : P.turn;
+        bool turns = TURN != kTurnNone && !is_v;
         Turn tn;
-        if (turn != kTurnNone) {
+        if (turns) {
             const int pos = a.positions[t];
-            if (pos < 0 || pos >= a.table_rows) turn = kTurnNone;
-            else load_turn<D>(tn, turn, a.cos + static_cast<int64_t>(pos) * a.half, a.sin + static_cast<int64_t>(pos) * a.half, a.half, l);
+            turns = pos >= 0 && pos < a.table_rows;
+            if (turns) load_turn<D, TURN>(tn, a.cos + static_cast<int64_t>(pos) * a.half, a.sin + static_cast<int64_t>(pos) * a.half, a.half, l);
         }
+        uint2* to = reinterpret_cast<uint2*>(a.q_out + (t * a.heads + set0 * kRows + sub) * D + 4 * l);
         for (int set = set0; set < set1; ++set) {
             Quads q = next;
             if (set + 1 < set1) load(next, set + 1);
             if (weight) norm_row<D>(q, w, a.eps);
-            if (turn != kTurnNone) rotate_row<D>(q, tn, turn, a.half, rows[warp] + sub * D, l);
+            if (turns) rotate_row<D, TURN>(q, tn, a.half, rows[TURN == kTurnPart ? warp : 0] + sub * D, l);
             const int h = set * kRows + sub;
             if (is_q) {
                 if (h < heads) {
 #pragma unroll
                     for (int k = 0; k < 2; ++k) {
                         const __half2 lo = __floats2half2_rn(q.x[4 * k], q.x[4 * k + 1]), hi = __floats2half2_rn(q.x[4 * k + 2], q.x[4 * k + 3]);
-                        *reinterpret_cast<uint2*>(a.q_out + (t * a.heads + h) * D + k * (D / 2) + 4 * l) =
-                            make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+                        to[k * (D / 8)] = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
                     }
                 }
+                to += kRows * (D / 4);
                 continue;
             }
             uint32_t bits[2];
@@ -519,6 +542,21 @@ __global__ void __launch_bounds__(256) read_kernel(const ReadParams P) {
     }
 }
 
+template <int D, bool F16>
+void append(const AppendParams& P, int turn, int grid, cudaStream_t s) {
+    const int threads = kAppendWarps * 32;
+    if (turn == kTurnNone) append_kernel<D, F16, kTurnNone><<<grid, threads, 0, s>>>(P);
+    else if (turn == kTurnHalves) append_kernel<D, F16, kTurnHalves><<<grid, threads, 0, s>>>(P);
+    else if (turn == kTurnNeighbours) append_kernel<D, F16, kTurnNeighbours><<<grid, threads, 0, s>>>(P);
+    else append_kernel<D, F16, kTurnPart><<<grid, threads, 0, s>>>(P);
+}
+
+template <int D>
+void append(const AppendParams& P, int turn, int grid, cudaStream_t s) {
+    if (P.a.f16) append<D, true>(P, turn, grid, s);
+    else append<D, false>(P, turn, grid, s);
+}
+
 int log2_of(int v) {
     int s = 0;
     while ((1 << s) < v) ++s;
@@ -556,7 +594,7 @@ cudaError_t launch_kv_plan(const KvPlanArgs& a, int num_sms, cudaStream_t s) {
 
 cudaError_t launch_kv_append(const KvAppendArgs& a, const KvGeometry& g, int num_sms, cudaStream_t s) {
     AppendParams P{a, cache_of(g)};
-    P.turn = a.half == 0 ? kTurnNone : a.interleaved ? kTurnNeighbours : a.half == g.D / 2 ? kTurnHalves : kTurnPart;
+    const int turn = a.half == 0 ? kTurnNone : a.interleaved ? kTurnNeighbours : a.half == g.D / 2 ? kTurnHalves : kTurnPart;
     const int rows = 32 / (g.D / 8);
     P.q_sets = (a.heads + rows - 1) / rows;
     P.kv_sets = (g.heads + rows - 1) / rows;
@@ -574,9 +612,9 @@ cudaError_t launch_kv_append(const KvAppendArgs& a, const KvGeometry& g, int num
     int64_t blocks = (P.tasks + kAppendWarps - 1) / kAppendWarps;
     if (blocks > (1 << 30)) blocks = 1 << 30;
     const int grid = static_cast<int>(blocks);
-    if (g.D == 64) append_kernel<64><<<grid, kAppendWarps * 32, 0, s>>>(P);
-    else if (g.D == 128) append_kernel<128><<<grid, kAppendWarps * 32, 0, s>>>(P);
-    else append_kernel<256><<<grid, kAppendWarps * 32, 0, s>>>(P);
+    if (g.D == 64) append<64>(P, turn, grid, s);
+    else if (g.D == 128) append<128>(P, turn, grid, s);
+    else append<256>(P, turn, grid, s);
     return cudaGetLastError();
 }
 

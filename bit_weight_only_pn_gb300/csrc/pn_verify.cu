@@ -46,11 +46,11 @@ __device__ __forceinline__ int64_t weight(const Row& r, int j) {
     return j == r.skip ? 0 : whole(p);
 }
 
-// The sum of weights j0 + lane * 4 .. of every 128th four; rows 16-byte aligned, j0 and j1 multiples of 4.
-__device__ __forceinline__ int64_t sum_fours(const Row& r, int j0, int j1, int lane) {
+// The sum of the weights j .. j + 3 for j = j0, j0 + step, ... below j1; rows 16-byte aligned, all multiples of 4.
+__device__ __forceinline__ int64_t sum_fours(const Row& r, int j0, int j1, int step) {
     int64_t s = 0;
 #pragma unroll 4
-    for (int j = j0 + 4 * lane; j < j1; j += 128) {
+    for (int j = j0; j < j1; j += step) {
         const float4 p = __ldcg(reinterpret_cast<const float4*>(r.p + j));
         if (r.q) {
             const float4 q = __ldcg(reinterpret_cast<const float4*>(r.q + j));
@@ -113,8 +113,9 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_kernel(const VerifyA
     for (int pass = 0; pass < 2; ++pass) {
         int64_t s = 0;
         // fours where both rows lie for it (vocab a multiple of 4, so the parts are too)
-        if (V % 4 == 0 && ((reinterpret_cast<uintptr_t>(row.p) | reinterpret_cast<uintptr_t>(row.q)) & 15) == 0) {
-            s = sum_fours(row, j0, j1, lane);
+        const bool fours = V % 4 == 0 && ((reinterpret_cast<uintptr_t>(row.p) | reinterpret_cast<uintptr_t>(row.q)) & 15) == 0;
+        if (fours) {
+            s = sum_fours(row, j0 + 4 * lane, j1, 128);
         } else {
 #pragma unroll 8
             for (int j = j0 + lane; j < j1; j += 32) s += weight(row, j);
@@ -156,11 +157,15 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_kernel(const VerifyA
                 }
                 return v;
             };
-            const int piece = (j1 - j0 + 31) / 32;
+            const int piece = (j1 - j0 + 127) / 128 * 4;
             const int k0 = min(j0 + lane * piece, j1), k1 = min(k0 + piece, j1);
             int64_t mine = 0;
+            if (fours) {
+                mine = sum_fours(row, k0, k1, 4);
+            } else {
 #pragma unroll 8
-            for (int j = k0; j < k1; ++j) mine += weight(row, j);
+                for (int j = k0; j < k1; ++j) mine += weight(row, j);
+            }
             const int64_t upto = scan(mine);
             const int owner = __ffs(__ballot_sync(0xFFFFFFFFu, before + upto > at)) - 1;
             before += __shfl_sync(0xFFFFFFFFu, upto - mine, owner);
