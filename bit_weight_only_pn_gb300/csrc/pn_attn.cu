@@ -69,7 +69,7 @@ struct AttnParams {
     uint32_t* status;
     uint32_t* counters;        // one per thread block
     float* block_slots;        // two per thread block
-    float* warp_slots;         // two per consumer warp
+    float* warp_slots;         // one per consumer warp
     uint64_t timeout_ns;
     int stall;                 // testing aid: see pn_set_test_stall
 };
@@ -161,28 +161,32 @@ struct Shape {
     static constexpr int kRecord = kv_record_bytes(D);
     static constexpr int kStage = kTileRecords * kRecord;
     static constexpr int kPlaneBytes = 256 * kPlaneGroups;     // 8 tokens of a plane
-    static constexpr int kDepth = D == 256 ? 2 : D == 128 ? 3 : 4;      // stages per warp
-    static constexpr int kStages = kWarps * kDepth;
-};
-
-template <int D, int NT>
-struct Smem {
-    static constexpr int kRT = 8 * NT;
-    static constexpr int kRing = Shape<D>::kStages * Shape<D>::kStage;
-    static constexpr int kFactors = kRing;                                 // [2 warps' pieces][rows] floats
-    static constexpr int kRuns = kFactors + 2 * kWarps * kRT * 4;          // see the block's join
-    static constexpr int kBars = kRuns + 4 * (2 * kWarps + 2) * 4;         // full, empty
-    static constexpr int kValid = kBars + 2 * Shape<D>::kStages * 8;       // per stage: records that hold data, marks of its last copy
-    static constexpr int kMisc = kValid + Shape<D>::kStages * 4;           // abort, last-block flag
-    static constexpr int kScan = kMisc + 8;                                // the warps' sums, then [batch + 1] prefix sums of units
-    static constexpr int kFixed = kScan + (kWarps + 1) * 4;
-    static int bytes(int batch) { return kFixed + (batch + 1) * 4; }
-    static_assert(kBars % 8 == 0, "barriers are 8-byte aligned");
 };
 
 // Floats of a piece: rows x D values, then (reference, sum) per row.
 template <int D, int NT>
 constexpr int kPiece = 8 * NT * (D + 2);
+
+template <int D, int NT>
+struct Smem {
+    static constexpr int kRT = 8 * NT;
+    static constexpr int kDepth = D == 256 ? 2 : D == 128 && NT == 1 ? 3 : 4;      // stages per warp
+    static constexpr int kStages = kWarps * kDepth;
+    static constexpr int kWarpRing = kDepth * Shape<D>::kStage;
+    static constexpr int kRing = kWarps * kWarpRing;
+    static constexpr int kRunsMost = kWarps + 1;                           // a warp's last piece goes on in the next one's first
+    static constexpr int kFactors = kRing;                                 // [2 warps' pieces][rows] floats
+    static constexpr int kRowOut = kFactors + 2 * kWarps * kRT * 4;        // [runs][rows] where a run's row goes
+    static constexpr int kRuns = kRowOut + kRunsMost * kRT * 8;            // see the block's join
+    static constexpr int kBars = kRuns + 4 * (2 * kWarps + 2) * 4;         // full, empty
+    static constexpr int kValid = kBars + 2 * kStages * 8;                 // per stage: records that hold data, marks of its last copy
+    static constexpr int kMisc = kValid + kStages * 4;                     // abort, last-block flags
+    static constexpr int kScan = kMisc + 12;                               // the warps' sums, then [batch + 1] prefix sums of units
+    static constexpr int kFixed = kScan + (kWarps + 1) * 4;
+    static int bytes(int batch) { return kFixed + (batch + 1) * 4; }
+    static_assert(kBars % 8 == 0 && kRowOut % 8 == 0, "barriers and row indexes are 8-byte aligned");
+    static_assert(2 * kPiece<D, NT> * 4 <= kWarpRing && kWarpRing % 16 == 0, "a warp's pieces fit its stages");
+};
 
 // Halves (code of token a, code of token b) of two tokens' words: the even
 // codes 0, 2, 4, 6 at bits 0, 4, 8, 12 of each half, or the odd ones.
@@ -539,14 +543,14 @@ template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, NT == 1 && D <= 128 ? kCtasPerSm : 1) attn_kernel(const __grid_constant__ AttnParams P) {
     using S = Shape<D>;
     using M = Smem<D, NT>;
-    constexpr int RT = 8 * NT, NG = S::kGroups, kStages = S::kStages, kDepth = S::kDepth;
+    constexpr int RT = 8 * NT, NG = S::kGroups, kStages = M::kStages, kDepth = M::kDepth;
     extern __shared__ __align__(128) uint8_t smem[];
     const uint32_t base = smem_addr(smem);
     auto full = [&](uint32_t s) { return base + M::kBars + 8u * s; };
     auto empty = [&](uint32_t s) { return base + M::kBars + 8u * (kStages + s); };
     volatile uint32_t* valid = reinterpret_cast<volatile uint32_t*>(smem + M::kValid);
     volatile uint32_t* abort = reinterpret_cast<volatile uint32_t*>(smem + M::kMisc);
-    volatile uint32_t* last_flag = abort + 1;
+    volatile uint32_t* last_flag = abort + 1;                            // [2]
     uint32_t* warp_sums = reinterpret_cast<uint32_t*>(smem + M::kScan);
     uint32_t* prefix = reinterpret_cast<uint32_t*>(smem + M::kFixed);    // [batch + 1]
     const AttnArgs& a = P.a;
@@ -700,8 +704,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && D <= 128 ? kCtasPerSm : 1
     if (lane < 2) piece_seg[2 * warp + lane] = kNone;
     __syncwarp();
     {
+        float* my_pieces = reinterpret_cast<float*>(smem + warp * M::kWarpRing);      // [2] pieces, once the stages are free
         uint32_t stage = warp * kDepth, parity = 0;
-        bool alive = true;
+        bool alive = true, waiting = false;
         int b = 0, h = 0, rg = 0, first = 0;
         Request r{};
         if (u0 < u1) {
@@ -765,7 +770,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && D <= 128 ? kCtasPerSm : 1
                     }
             } else {
                 const int kind = first == 0 ? 1 : 0;
-                float* slot = P.warp_slots + static_cast<int64_t>(2 * mine + kind) * kPiece<D, NT>;
+                // the warp's stages are free behind its last unit; an earlier piece waits in the workspace
+                const bool at_end = u + count == u1;
+                float* slot = at_end ? my_pieces + kind * kPiece<D, NT> : P.warp_slots + static_cast<int64_t>(mine) * kPiece<D, NT>;
+                waiting |= !at_end;
+                __syncwarp();
                 if (lane == 0) piece_seg[2 * warp + kind] = u - first;
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
@@ -790,6 +799,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && D <= 128 ? kCtasPerSm : 1
                     do r = request_of<RT>(P, ++b); while (r.rows == 0);
                 }
             }
+        }
+        if (waiting && alive) {                        // (after an abort copies may still be on their way into the stages)
+            __syncwarp();                              // the warp's own writes
+            const float4* from = reinterpret_cast<const float4*>(P.warp_slots + static_cast<int64_t>(mine) * kPiece<D, NT>);
+#pragma unroll 8
+            for (int i = lane; i < kPiece<D, NT> / 4; i += 32) reinterpret_cast<float4*>(my_pieces)[i] = from[i];
         }
     }
 
@@ -820,10 +835,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && D <= 128 ? kCtasPerSm : 1
     auto block_of = [&](uint32_t x) {                  // the block that holds unit x
         return static_cast<uint32_t>(((static_cast<uint64_t>(x) + 1) * blocks + total - 1) / total - 1);
     };
-    auto warp_slot = [&](int i) { return P.warp_slots + (static_cast<int64_t>(2 * blockIdx.x) * kWarps + order[i]) * kPiece<D, NT>; };
+    auto piece_at = [&](int i) {                       // i-th piece of the block
+        return reinterpret_cast<const float*>(smem + (order[i] >> 1) * M::kWarpRing) + (order[i] & 1) * kPiece<D, NT>;
+    };
     auto block_slot = [&](uint32_t c, bool begins) { return P.block_slots + (2 * static_cast<int64_t>(c) + begins) * kPiece<D, NT>; };
-    // A run's row: common reference and sum; each piece's factor to them.
-    // Whole segments get the output's factor; the others' (reference, sum) goes to the block's slot.
+    // A run's row: common reference and sum; each piece's factor to them, for
+    // whole segments to the output; the others' (reference, sum) goes to the
+    // block's slot.
+    int64_t* row_out = reinterpret_cast<int64_t*>(smem + M::kRowOut);    // [runs][rows]: output row, kToNone, kToSlot + begins
+    constexpr int64_t kToNone = -1, kToSlot = -3;
     for (int i = threadIdx.x; i < runs * RT; i += kWarps * 32) {
         const int run = i / RT, row = i % RT;
         const int p0 = run_at[run], p1 = run_at[run + 1];
@@ -831,9 +851,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && D <= 128 ? kCtasPerSm : 1
         const int b = request_at(seg);
         const Request r = request_of<RT>(P, b);
         float m = -INFINITY, l = 0.0f;
-        for (int p = p0; p < p1; ++p) m = fmaxf(m, reinterpret_cast<const float2*>(warp_slot(p) + RT * D)[row].x);
+        for (int p = p0; p < p1; ++p) m = fmaxf(m, reinterpret_cast<const float2*>(piece_at(p) + RT * D)[row].x);
         for (int p = p0; p < p1; ++p) {
-            const float2 v = reinterpret_cast<const float2*>(warp_slot(p) + RT * D)[row];
+            const float2 v = reinterpret_cast<const float2*>(piece_at(p) + RT * D)[row];
             const float f = v.x == -INFINITY ? 0.0f : ex2(v.x - m);
             factors[p * RT + row] = f;
             l += f * v.y;
@@ -846,112 +866,119 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && D <= 128 ? kCtasPerSm : 1
             locate(seg - prefix[b], r, h, rg, idx);
             const int64_t at = row_index<RT>(P, r, h, rg, row);
             if (a.lse && at >= 0) a.lse[at] = log_sum(m, l);
+            row_out[i] = at >= 0 ? at : kToNone;
         } else {
             reinterpret_cast<float2*>(block_slot(blockIdx.x, c0 == blockIdx.x) + RT * D)[row] = make_float2(m, l);
+            row_out[i] = kToSlot + (c0 == blockIdx.x);
         }
     }
     consumers_sync();
     for (int i = threadIdx.x; i < runs * (RT * D / 4); i += kWarps * 32) {
         const int run = i / (RT * D / 4), e = (i % (RT * D / 4)) * 4, row = e / D, d = e % D;
+        const int64_t at = row_out[run * RT + row];
+        if (at == kToNone) continue;
         const int p0 = run_at[run], p1 = run_at[run + 1];
-        const uint32_t seg = piece_seg[order[p0]];
-        const int b = request_at(seg);
-        const Request r = request_of<RT>(P, b);
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 4
         for (int p = p0; p < p1; ++p) {
             const float f = factors[p * RT + row];
-            const float4 v = *reinterpret_cast<const float4*>(warp_slot(p) + e);
-            // a piece that saw nothing, or of weight zero, adds nothing
+            const float4 v = *reinterpret_cast<const float4*>(piece_at(p) + e);
             o.x = fmaf(f, v.x, o.x); o.y = fmaf(f, v.y, o.y); o.z = fmaf(f, v.z, o.z); o.w = fmaf(f, v.w, o.w);
         }
-        const uint32_t c0 = block_of(seg), c1 = block_of(seg + r.tiles - 1);
-        if (c0 == c1) {
-            int h, rg, idx;
-            locate(seg - prefix[b], r, h, rg, idx);
-            const int64_t at = row_index<RT>(P, r, h, rg, row);
-            if (at >= 0) *reinterpret_cast<uint2*>(a.out + at * D + d) = make_uint2(pack_half2(o.x, o.y), pack_half2(o.z, o.w));
-        } else {
-            *reinterpret_cast<float4*>(block_slot(blockIdx.x, c0 == blockIdx.x) + e) = o;
-        }
+        if (at >= 0) *reinterpret_cast<uint2*>(a.out + at * D + d) = make_uint2(pack_half2(o.x, o.y), pack_half2(o.z, o.w));
+        else *reinterpret_cast<float4*>(block_slot(blockIdx.x, at != kToSlot) + e) = o;
     }
 
     // ------------------------------------------- segments of several blocks --
     // The first and the last run may be pieces of such; the last block to
-    // arrive joins them, in block order.  No copy is in flight any more: the
-    // ring holds the parts' factors.
-    const uint32_t piece0 = piece_seg[order[0]], piece1 = piece_seg[order[run_at[runs] - 1]];
-    float* part_factors = reinterpret_cast<float*>(smem);                // [parts][rows], as many as fit
-    constexpr uint32_t kParts = M::kRing / (RT * 4);
+    // arrive joins them, in block order.
+    const uint32_t seg_first = piece_seg[order[0]], seg_last = piece_seg[order[run_at[runs] - 1]];
+    consumers_sync();                                  // the block's slots are written, the pieces read
+    if (threadIdx.x < 2) {
+        const uint32_t seg = threadIdx.x ? seg_last : seg_first;
+        bool last = false;
+        if (threadIdx.x == 0 || seg_last != seg_first) {
+            const Request r = request_of<RT>(P, request_at(seg));
+            const uint32_t c0 = block_of(seg), c1 = block_of(seg + r.tiles - 1);
+            if (c0 != c1) {
+                __threadfence();
+                last = atomicAdd(&P.counters[c0], 1u) == c1 - c0;
+                __threadfence();
+                if (last) P.counters[c0] = 0u;
+            }
+        }
+        last_flag[threadIdx.x] = last;
+    }
+    consumers_sync();
+    // no copy is in flight and no piece is read any more: the ring holds the parts' factors
+    float* part_factors = reinterpret_cast<float*>(smem);                // [parts][rows]; the grid's fit (see launch)
+    float2* part_sums = reinterpret_cast<float2*>(smem + M::kRing / 2);  // [parts][rows]
     for (int side = 0; side < 2; ++side) {
-        if (side == 1 && piece1 == piece0) break;
-        const uint32_t seg = side ? piece1 : piece0;
+        if (!last_flag[side]) continue;
+        const uint32_t seg = side ? seg_last : seg_first;
         const int b = request_at(seg);
         const Request r = request_of<RT>(P, b);
         const uint32_t c0 = block_of(seg), c1 = block_of(seg + r.tiles - 1);
-        if (c0 == c1) continue;                                          // the same for every thread
-        __threadfence();
-        consumers_sync();
-        if (threadIdx.x == 0) {
-            const bool last = atomicAdd(&P.counters[c0], 1u) == c1 - c0;
-            if (last) P.counters[c0] = 0u;
-            *last_flag = last;
-        }
-        consumers_sync();
-        if (!*last_flag) continue;
-        __threadfence();
         int h, rg, idx;
         locate(seg - prefix[b], r, h, rg, idx);
-        const uint32_t parts = c1 - c0 + 1;                              // at most the grid, which fits the ring
+        const int parts = static_cast<int>(c1 - c0 + 1);
+        for (int i = threadIdx.x; i < parts * RT; i += kWarps * 32) {
+            const int p = i / RT, row = i % RT;
+            part_sums[i] = __ldcg(reinterpret_cast<const float2*>(block_slot(c0 + p, p == 0) + RT * D) + row);
+        }
+        consumers_sync();
         for (int row = warp; row < RT; row += kWarps) {
             float m = -INFINITY, l = 0.0f;
-            for (uint32_t p = lane; p < parts; p += 32)
-                m = fmaxf(m, __ldcg(reinterpret_cast<const float2*>(block_slot(c0 + p, p == 0) + RT * D) + row).x);
+            for (int p = lane; p < parts; p += 32) m = fmaxf(m, part_sums[p * RT + row].x);
 #pragma unroll
             for (int d = 16; d >= 1; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, d));
-            for (uint32_t p = lane; p < parts; p += 32) {
-                const float2 v = __ldcg(reinterpret_cast<const float2*>(block_slot(c0 + p, p == 0) + RT * D) + row);
-                const float f = v.x == -INFINITY ? 0.0f : ex2(v.x - m);
-                if (p < kParts) part_factors[p * RT + row] = f;
-                l += f * v.y;
+            for (int p = lane; p < parts; p += 32) {
+                const float2 v = part_sums[p * RT + row];
+                l += v.x == -INFINITY ? 0.0f : ex2(v.x - m) * v.y;
             }
 #pragma unroll
             for (int d = 16; d >= 1; d >>= 1) l += __shfl_xor_sync(0xFFFFFFFFu, l, d);
-            __syncwarp();
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-            for (uint32_t p = lane; p < parts; p += 32)
-                if (p < kParts) part_factors[p * RT + row] *= inv;
+            for (int p = lane; p < parts; p += 32) {
+                const float ref = part_sums[p * RT + row].x;
+                part_factors[p * RT + row] = ref == -INFINITY ? 0.0f : ex2(ref - m) * inv;
+            }
             const int64_t at = row_index<RT>(P, r, h, rg, row);
             if (a.lse && at >= 0 && lane == 0) a.lse[at] = log_sum(m, l);
         }
         consumers_sync();
-        for (int i = threadIdx.x; i < RT * D / 4; i += kWarps * 32) {
-            const int e = i * 4, row = e / D, d = e % D;
-            const int64_t at = row_index<RT>(P, r, h, rg, row);
-            if (at < 0) continue;
-            float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-#pragma unroll 16
-            for (uint32_t p = 0; p < parts; ++p) {
-                const float f = part_factors[p * RT + row];
-                const float4 v = __ldcg(reinterpret_cast<const float4*>(block_slot(c0 + p, p == 0) + e));
-                o.x = fmaf(f, v.x, o.x); o.y = fmaf(f, v.y, o.y); o.z = fmaf(f, v.z, o.z); o.w = fmaf(f, v.w, o.w);
+        constexpr int kElements = RT * D / 4;
+        for (int i = threadIdx.x; i < kElements; i += 2 * kWarps * 32) {
+            const int e0 = i * 4, e1 = min(i + kWarps * 32, kElements - 1) * 4;
+            float4 o0 = make_float4(0.0f, 0.0f, 0.0f, 0.0f), o1 = o0;
+            const float* f0 = part_factors + e0 / D;
+            const float* f1 = part_factors + e1 / D;
+#pragma unroll 8
+            for (int p = 0; p < parts; ++p) {
+                const float* from = block_slot(c0 + p, p == 0);
+                const float4 v0 = __ldcg(reinterpret_cast<const float4*>(from + e0)), v1 = __ldcg(reinterpret_cast<const float4*>(from + e1));
+                const float a0 = f0[p * RT], a1 = f1[p * RT];
+                o0.x = fmaf(a0, v0.x, o0.x); o0.y = fmaf(a0, v0.y, o0.y); o0.z = fmaf(a0, v0.z, o0.z); o0.w = fmaf(a0, v0.w, o0.w);
+                o1.x = fmaf(a1, v1.x, o1.x); o1.y = fmaf(a1, v1.y, o1.y); o1.z = fmaf(a1, v1.z, o1.z); o1.w = fmaf(a1, v1.w, o1.w);
             }
-            *reinterpret_cast<uint2*>(a.out + at * D + d) = make_uint2(pack_half2(o.x, o.y), pack_half2(o.z, o.w));
+            const int64_t at0 = row_index<RT>(P, r, h, rg, e0 / D), at1 = row_index<RT>(P, r, h, rg, e1 / D);
+            if (at0 >= 0) *reinterpret_cast<uint2*>(a.out + at0 * D + e0 % D) = make_uint2(pack_half2(o0.x, o0.y), pack_half2(o0.z, o0.w));
+            if (i + kWarps * 32 < kElements && at1 >= 0)
+                *reinterpret_cast<uint2*>(a.out + at1 * D + e1 % D) = make_uint2(pack_half2(o1.x, o1.y), pack_half2(o1.z, o1.w));
         }
-        consumers_sync();                                                // the factors are written again
+        consumers_sync();                              // the factors are written again
     }
 }
 
 template <int D, int NT>
 constexpr int kBlocksPerSm = NT == 1 && D <= 128 ? kCtasPerSm : 1;
 
-// Workspace: status word (256 bytes), one counter per thread block, two slots
-// per thread block and per consumer warp.
+// Workspace: status word (256 bytes), one counter and two slots per thread
+// block, one slot per consumer warp.
 constexpr size_t counter_bytes(size_t blocks) { return (blocks * 4 + 255) / 256 * 256; }
 template <int D, int NT>
 size_t workspace_bytes(int num_sms) {
     const size_t blocks = static_cast<size_t>(num_sms) * kBlocksPerSm<D, NT>;
-    return 256 + counter_bytes(static_cast<size_t>(num_sms) * kCtasPerSm) + 2 * blocks * (1 + kWarps) * kPiece<D, NT> * 4;
+    return 256 + counter_bytes(static_cast<size_t>(num_sms) * kCtasPerSm) + blocks * (2 + kWarps) * kPiece<D, NT> * 4;
 }
 
 template <int D, int NT>
@@ -961,7 +988,7 @@ cudaError_t launch(AttnParams P, uint8_t* ws, int num_sms, cudaStream_t s) {
     const int smem = Smem<D, NT>::bytes(P.a.batch);
     if (smem > 227 * 1024) return cudaErrorInvalidValue;
     int grid = num_sms * kBlocksPerSm<D, NT>;
-    constexpr int kMost = Smem<D, NT>::kRing / (8 * NT * 4);             // blocks whose factors fit the ring
+    constexpr int kMost = Smem<D, NT>::kRing / (2 * 8 * NT * 8);         // blocks whose references and sums fit half the ring
     if (grid > kMost) grid = kMost;
     P.status = reinterpret_cast<uint32_t*>(ws);
     P.counters = reinterpret_cast<uint32_t*>(ws + 256);

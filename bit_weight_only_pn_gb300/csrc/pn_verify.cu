@@ -10,9 +10,10 @@
 //
 // Bound by the read of that one row (two with q): a cluster of thread blocks
 // shares it.  Each warp sums a contiguous part; block sums meet through
-// distributed shared memory; in the warp whose part holds the threshold each
-// lane sums a contiguous 32nd of it once more (from L2), then the warp walks
-// the one 32nd that holds the token.
+// distributed shared memory; the block that holds the threshold splits the
+// warp's part that holds it over all its threads (a second read, from L2), and
+// the one thread whose few weights hold it walks them.  (With the part left to
+// its own warp that second read was a third of the time.)
 #include <cooperative_groups.h>
 #include <cstdint>
 
@@ -147,38 +148,36 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_kernel(const VerifyA
         }
         int64_t at = __double2ll_rd(static_cast<double>(u) * static_cast<double>(total));
         at = min(max(at, static_cast<int64_t>(0)), total - 1);
-        for (int w = 0; w < warp; ++w) before += sums[w];
-        if (at >= before && at < before + s) {     // this warp's part (s > 0) holds it
-            auto scan = [&](int64_t v) {
+        if (at < before || at >= before + block_total[pass]) break;      // another block's
+        int owner = 0;
+        while (at >= before + sums[owner]) before += sums[owner++];
+        const int o0 = min((rank * kVerifyWarps + owner) * each, V), o1 = min(o0 + each, V);
+        const int piece = (o1 - o0 + 4 * kVerifyThreads - 1) / (4 * kVerifyThreads) * 4;
+        const int k0 = min(o0 + static_cast<int>(threadIdx.x) * piece, o1), k1 = min(k0 + piece, o1);
+        int64_t mine = 0;
+        if (fours) {
+            mine = sum_fours(row, k0, k1, 4);
+        } else {
+            for (int j = k0; j < k1; ++j) mine += weight(row, j);
+        }
+        int64_t upto = mine;
 #pragma unroll
-                for (int d = 1; d < 32; d <<= 1) {
-                    const int64_t o = __shfl_up_sync(0xFFFFFFFFu, v, d);
-                    if (lane >= d) v += o;
-                }
-                return v;
-            };
-            const int piece = (j1 - j0 + 127) / 128 * 4;
-            const int k0 = min(j0 + lane * piece, j1), k1 = min(k0 + piece, j1);
-            int64_t mine = 0;
-            if (fours) {
-                mine = sum_fours(row, k0, k1, 4);
-            } else {
-#pragma unroll 8
-                for (int j = k0; j < k1; ++j) mine += weight(row, j);
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t o = __shfl_up_sync(0xFFFFFFFFu, upto, d);
+            if (lane >= d) upto += o;
+        }
+        __syncthreads();                           // everyone has read sums
+        if (lane == 31) sums[warp] = upto;
+        __syncthreads();
+        before += upto - mine;
+        for (int w = 0; w < warp; ++w) before += sums[w];
+        if (at >= before && at < before + mine) {
+            int j = k0;
+            for (; j < k1 - 1; ++j) {
+                before += weight(row, j);
+                if (before > at) break;
             }
-            const int64_t upto = scan(mine);
-            const int owner = __ffs(__ballot_sync(0xFFFFFFFFu, before + upto > at)) - 1;
-            before += __shfl_sync(0xFFFFFFFFu, upto - mine, owner);
-            const int m0 = __shfl_sync(0xFFFFFFFFu, k0, owner), m1 = __shfl_sync(0xFFFFFFFFu, k1, owner);
-            for (int j = m0; j < m1; j += 32) {
-                const int64_t in = scan(j + lane < m1 ? weight(row, j + lane) : 0);
-                const uint32_t past = __ballot_sync(0xFFFFFFFFu, before + in > at);
-                if (past) {
-                    if (lane == 0) out[accepted] = j + __ffs(past) - 1;
-                    break;
-                }
-                before += __shfl_sync(0xFFFFFFFFu, in, 31);
-            }
+            out[accepted] = j;
         }
         break;
     }
