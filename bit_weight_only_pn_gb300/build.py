@@ -18,9 +18,9 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIBRARY = os.path.join(HERE, "libpn_gb300.so")
-SOURCES = ["pn_attn.cu", "pn_capi.cu", "pn_codec.cu", "pn_gemv_ffma.cu", "pn_gemv_simt.cu", "pn_gemv_stream.cu", "pn_gemv_tc.cu",
+SOURCES = ["pn_attn.cu", "pn_attn_tc.cu", "pn_capi.cu", "pn_codec.cu", "pn_gemv_ffma.cu", "pn_gemv_simt.cu", "pn_gemv_stream.cu", "pn_gemv_tc.cu",
            "pn_gptq.cu", "pn_kv.cu", "pn_noalloc.cu", "pn_prefill.cu", "pn_probe.cu", "pn_rotate.cu", "pn_verify.cu"]
-HEADERS = ["pn_device.cuh", "pn_internal.h", "pn_kv.cuh"]
+HEADERS = ["pn_attn.cuh", "pn_device.cuh", "pn_internal.h", "pn_kv.cuh", "pn_tcgen05.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
               "-I", os.path.join(ROOT, "include")]

@@ -44,9 +44,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
-#include "pn_device.cuh"
-#include "pn_internal.h"
-#include "pn_kv.cuh"
+#include "pn_attn.cuh"
 
 namespace pn {
 namespace {
@@ -58,57 +56,12 @@ constexpr int kThreads = (kWarps + 1) * 32;
 constexpr int kCtasPerSm = 2;                  // where 128 registers suffice (8 rows, D <= 128), else 1
 constexpr uint32_t kIssued = 1u << 8;          // marks beside a stage's records: its copy was started,
 constexpr uint32_t kOddTurn = 1u << 9;         // in an odd turn of the ring
-constexpr uint32_t kStatusTimeout = 5;         // PN_ETIMEOUT
-constexpr uint64_t kDrainLimitNs = 200ull * 1000 * 1000;
-
-struct AttnParams {
-    AttnArgs a;
-    KvCache cache;
-    int group;                 // query heads per key/value head
-    float scale_log2;          // scale * log2 e
-    uint32_t* status;
-    uint32_t* counters;        // one per thread block
-    float* block_slots;        // two per thread block
-    float* warp_slots;         // one per consumer warp
-    uint64_t timeout_ns;
-    int stall;                 // testing aid: see pn_set_test_stall
-};
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-__device__ __forceinline__ float lg2(float x) {
-    float y;
-    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
 // 8x8 transpose of 16-bit elements across the warp (row lane / 4, columns 2 (lane % 4), + 1).
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
     uint32_t r;
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
 }
-__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
-
-// Polls: a thread parked in mbarrier.try_wait notices a completed phase late.
-__device__ bool wait_phase(uint32_t bar, uint32_t parity, uint64_t limit_ns, volatile uint32_t* abort) {
-    uint64_t t0 = 0;
-    for (;;) {
-#pragma unroll 1
-        for (int i = 0; i < 128; ++i)
-            if (mbar_try_wait(bar, parity)) return true;
-        if (abort && *abort) return false;
-        const uint64_t now = globaltimer_ns();
-        if (t0 == 0) t0 = now;
-        else if (now - t0 > limit_ns) return false;
-    }
-}
-
 __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" :: "n"(kWarps * 32) : "memory"); }
 
 // What a request asks of the cache.
@@ -535,10 +488,6 @@ __device__ __forceinline__ int64_t row_index(const AttnParams& P, const Request&
     return (static_cast<int64_t>(r.q0) + qi) * P.a.heads + h * P.group + i - qi * P.group;
 }
 
-__device__ __forceinline__ float log_sum(float ref, float sum) {
-    return sum == 0.0f ? -INFINITY : 0.6931471805599453f * (ref + log2f(sum));
-}
-
 template <int D, int NT>
 __global__ void __launch_bounds__(kThreads, NT == 1 && D <= 128 ? kCtasPerSm : 1) attn_kernel(const __grid_constant__ AttnParams P) {
     using S = Shape<D>;
@@ -645,7 +594,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && D <= 128 ? kCtasPerSm : 1
                         if (t0 == 0) t0 = now;
                         if (*abort || now - t0 > P.timeout_ns) {
                             *abort = 1u;
-                            atomicCAS(P.status, 0u, kStatusTimeout);
+                            atomicCAS(P.status, 0u, kAttnTimeout);
                             break;
                         }
                     }
@@ -688,7 +637,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && D <= 128 ? kCtasPerSm : 1
                 }
             }
             // the last copy into the stage lands before the block ends, also after an abort
-            if (valid[s] & kIssued) wait_phase(full(s), valid[s] & kOddTurn ? 1u : 0u, kDrainLimitNs, nullptr);
+            if (valid[s] & kIssued) wait_phase(full(s), valid[s] & kOddTurn ? 1u : 0u, kAttnDrainNs, nullptr);
         }
         return;
     }
@@ -729,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && D <= 128 ? kCtasPerSm : 1
                     alive = __all_sync(0xFFFFFFFFu, wait_phase(full(stage), parity, P.timeout_ns, abort));
                     if (!alive && lane == 0) {
                         *abort = 1u;
-                        atomicCAS(P.status, 0u, kStatusTimeout);
+                        atomicCAS(P.status, 0u, kAttnTimeout);
                     }
                 }
                 if (!alive) break;
@@ -974,11 +923,10 @@ constexpr int kBlocksPerSm = NT == 1 && D <= 128 ? kCtasPerSm : 1;
 
 // Workspace: status word (256 bytes), one counter and two slots per thread
 // block, one slot per consumer warp.
-constexpr size_t counter_bytes(size_t blocks) { return (blocks * 4 + 255) / 256 * 256; }
 template <int D, int NT>
 size_t workspace_bytes(int num_sms) {
     const size_t blocks = static_cast<size_t>(num_sms) * kBlocksPerSm<D, NT>;
-    return 256 + counter_bytes(static_cast<size_t>(num_sms) * kCtasPerSm) + blocks * (2 + kWarps) * kPiece<D, NT> * 4;
+    return 256 + attn_counter_bytes(num_sms) + blocks * (2 + kWarps) * kPiece<D, NT> * 4;
 }
 
 template <int D, int NT>
@@ -992,7 +940,7 @@ cudaError_t launch(AttnParams P, uint8_t* ws, int num_sms, cudaStream_t s) {
     if (grid > kMost) grid = kMost;
     P.status = reinterpret_cast<uint32_t*>(ws);
     P.counters = reinterpret_cast<uint32_t*>(ws + 256);
-    P.block_slots = reinterpret_cast<float*>(ws + 256 + counter_bytes(static_cast<size_t>(num_sms) * kCtasPerSm));
+    P.block_slots = reinterpret_cast<float*>(ws + 256 + attn_counter_bytes(num_sms));
     P.warp_slots = P.block_slots + 2 * static_cast<size_t>(grid) * kPiece<D, NT>;
     attn_kernel<D, NT><<<grid, kThreads, smem, s>>>(P);
     return cudaGetLastError();
@@ -1003,7 +951,7 @@ cudaError_t launch(AttnParams P, uint8_t* ws, int num_sms, cudaStream_t s) {
 size_t attn_workspace_bytes(int num_sms) {
     size_t most = 0;
     for (size_t n : {workspace_bytes<64, 1>(num_sms), workspace_bytes<64, 2>(num_sms), workspace_bytes<128, 1>(num_sms),
-                     workspace_bytes<128, 2>(num_sms), workspace_bytes<256, 1>(num_sms)})
+                     workspace_bytes<128, 2>(num_sms), workspace_bytes<256, 1>(num_sms), attn_tc_workspace_bytes(num_sms)})
         most = n > most ? n : most;
     return most;
 }
@@ -1022,6 +970,7 @@ cudaError_t launch_attention(const AttnArgs& a, const KvGeometry& g, void* works
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     AttnParams P{a, KvCache{g.data, g.pages, g.page_size, shift, g.heads, g.D}, a.heads / g.heads, a.scale * 1.4426950408889634f,
                  nullptr, nullptr, nullptr, nullptr, timeout_ns, stall};
+    if (attn_tc_takes(a, g)) return launch_attention_tc(P, ws, num_sms, s);
     // 8 or 16 query rows share the decoded codes
     const bool wide = static_cast<int64_t>(a.max_queries) * P.group > 8;
     if (g.D == 64) return wide ? launch<64, 2>(P, ws, num_sms, s) : launch<64, 1>(P, ws, num_sms, s);

@@ -1,0 +1,72 @@
+// pn_attn.cuh -- what the attention kernels share.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda_fp16.h>
+
+#include "pn_device.cuh"
+#include "pn_internal.h"
+#include "pn_kv.cuh"
+
+namespace pn {
+
+constexpr uint32_t kAttnTimeout = 5;         // PN_ETIMEOUT
+constexpr uint64_t kAttnDrainNs = 200ull * 1000 * 1000;
+
+struct AttnParams {
+    AttnArgs a;
+    KvCache cache;
+    int group;                 // query heads per key/value head
+    float scale_log2;          // scale * log2 e
+    uint32_t* status;
+    uint32_t* counters;        // one per thread block
+    float* block_slots;        // two per thread block
+    float* warp_slots;         // one per consumer warp
+    uint64_t timeout_ns;
+    int stall;                 // testing aid: see pn_set_test_stall
+};
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ float lg2(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Polls: a thread parked in mbarrier.try_wait notices a completed phase late.
+static __device__ bool wait_phase(uint32_t bar, uint32_t parity, uint64_t limit_ns, volatile uint32_t* abort) {
+    uint64_t t0 = 0;
+    for (;;) {
+#pragma unroll 1
+        for (int i = 0; i < 128; ++i)
+            if (mbar_try_wait(bar, parity)) return true;
+        if (abort && *abort) return false;
+        const uint64_t now = globaltimer_ns();
+        if (t0 == 0) t0 = now;
+        else if (now - t0 > limit_ns) return false;
+    }
+}
+
+__device__ __forceinline__ float log_sum(float ref, float sum) {
+    return sum == 0.0f ? -INFINITY : 0.6931471805599453f * (ref + log2f(sum));
+}
+
+// Bytes of the counters at the head of an attention workspace, behind the
+// status word's 256: one per thread block, two blocks to an SM at most.
+constexpr size_t attn_counter_bytes(int num_sms) { return (static_cast<size_t>(num_sms) * 2 * 4 + 255) / 256 * 256; }
+
+// The kernel for many query rows to a key/value head (pn_attn_tc.cu).
+bool attn_tc_takes(const AttnArgs& a, const KvGeometry& g);
+size_t attn_tc_workspace_bytes(int num_sms);
+cudaError_t launch_attention_tc(AttnParams P, uint8_t* ws, int num_sms, cudaStream_t s);
+
+}  // namespace pn

@@ -1,0 +1,740 @@
+// pn_attn_tc.cu -- attention over the 4-bit cache for many query rows to a
+// key/value head (prompts, long drafts): the same function as pn_attn.cu, on
+// the fifth-generation tensor cores.
+//
+// A segment is (request, row tile, key/value head): 128 rows, the query heads
+// that share the head times as many whole tokens as fit.  Its visible cached
+// tokens are taken 64 at a time.  In a thread block of 14 warps
+//   warp 12 copies records into a raw ring (bulk copies, a lane to a stage);
+//   warps 8-11 decode them into fp16 whole numbers n - 8, exact, K and V as
+//     [token][64 values] tiles with the 128-byte swizzle, and the scales as
+//     fp32; a tile's codes are decoded once for 128 rows;
+//   warp 13 issues the products: S_j = Q_j K_j^T for each group j of 64 values
+//     (fp32 in tensor memory, M = 128, N = 64), O_j += P_j V_j with P_j from
+//     tensor memory and V as its token-major tile;
+//   warps 0-3 and 4-7 take even and odd tiles, a row to a thread: x = sum_j
+//     d_j S_j, the online softmax, P_j = p d_j rounded once to fp16, written
+//     over S.  Each of the two keeps its own reference, sum and O, so one's
+//     softmax runs beside the other's products; they are joined at the end.
+// The scales of K and V never touch the operands, so scores and values are as
+// exact as in the kernel for few rows; P_j takes the place of one P because V's
+// scale differs by group.
+//
+// The reference of a row is its maximum of x + log2 of the tile's largest V
+// scale, less 7, and stays until that maximum lies 15 above it: p d < 2^15, and
+// O is hardly ever rescaled.
+//
+// Work split: as in pn_attn.cu, units (segment, tile) in order, a contiguous
+// range to each of one thread block per SM; what crosses block boundaries is
+// joined by the last block to arrive, in block order.
+#include <cstdint>
+
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "pn_attn.cuh"
+#include "pn_tcgen05.cuh"
+
+namespace pn {
+namespace {
+
+constexpr int kRows = 128;                     // MMA M
+constexpr int kTile = 64;                      // tokens per unit, MMA N of S
+constexpr int kTileRecords = kTile / kKvTokens;
+constexpr int kThreads = 14 * 32;
+constexpr int kSoftmaxThreads = 256;
+constexpr int kRawStages = 4;
+constexpr int kBufs = 4;                       // decoded tiles
+constexpr uint32_t kTmemCols = 512;            // S of both halves (P over it), O of both
+constexpr float kMargin = 7.0f, kSlack = 15.0f;
+constexpr uint32_t kIssued = 1u << 8, kOddTurn = 1u << 9;   // marks beside a raw stage's records
+
+// fp32 accumulators, fp16 operands, M = 128, N = 64; B K-major, or (bit 16) MN-major.
+constexpr uint32_t kDescS = (1u << 4) | (static_cast<uint32_t>(kTile >> 3) << 17) | (static_cast<uint32_t>(kRows >> 4) << 24);
+constexpr uint32_t kDescO = (1u << 4) | (1u << 16) | (8u << 17) | (static_cast<uint32_t>(kRows >> 4) << 24);
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %3, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %4, p;\n\t}"
+        :: "r"(d), "l"(a), "l"(b), "r"(static_cast<uint32_t>(accumulate)), "r"(desc) : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t desc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %3, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %4, p;\n\t}"
+        :: "r"(d), "r"(a), "l"(b), "r"(static_cast<uint32_t>(accumulate)), "r"(desc) : "memory");
+}
+// An MN-major tile of 64 values (128 bytes) by tokens with the 128-byte
+// swizzle: 8 tokens to an atom of 1024 bytes (stride byte offset); one atom
+// wide, so the leading byte offset is not used (set alike).
+__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t addr) {
+    return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(1024 >> 4) << 16) |
+           (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
+}
+
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 2, %0;" :: "n"(kSoftmaxThreads) : "memory"); }
+
+// A request, one of its row tiles, and walking over them.
+struct Walk {
+    int b, qt, h, idx;         // request, row tile, head, tile of the segment
+    int n, q0, pos0, len;      // the request's queries, their first row and position, cached tokens
+    int qtiles;
+    int t0, nt;                // the row tile's tokens
+    int pos_lo, pos_hi;
+    int lo_tile, sink_tiles, tiles;
+
+    __device__ __forceinline__ void request(const AttnParams& P, int per) {
+        const AttnArgs& a = P.a;
+        const int T = static_cast<int>(a.tokens);
+        q0 = min(max(a.starts[b], 0), T);
+        n = min(min(max(a.starts[b + 1], q0), T) - q0, a.max_queries);
+        const int64_t room = static_cast<int64_t>(a.max_pages) << P.cache.page_shift;
+        len = static_cast<int>(min(static_cast<int64_t>(max(a.lens[b], 0)), room));
+        pos0 = len - n;
+        qtiles = (n + per - 1) / per;
+    }
+    __device__ __forceinline__ void row_tile(const AttnParams& P, int per) {
+        t0 = qt * per;
+        nt = min(per, n - t0);
+        pos_lo = pos0 + t0;
+        pos_hi = pos_lo + nt - 1;
+        const int end_tile = (max(pos_hi + 1, 0) + kTile - 1) / kTile;
+        const int lo = P.a.window ? max(pos_lo - P.a.window + 1, 0) : 0;
+        lo_tile = lo / kTile;
+        sink_tiles = P.a.window ? min((P.a.sinks + kTile - 1) / kTile, lo_tile) : 0;
+        tiles = max(end_tile - lo_tile + sink_tiles, 1);
+    }
+    // units of the request
+    __device__ __forceinline__ uint32_t units(const AttnParams& P, int per) {
+        uint32_t u = 0;
+        for (qt = 0; qt < qtiles; ++qt) {
+            row_tile(P, per);
+            u += static_cast<uint32_t>(tiles);
+        }
+        return u * P.cache.heads;
+    }
+    __device__ __forceinline__ int first_token() const { return (idx < sink_tiles ? idx : lo_tile + idx - sink_tiles) * kTile; }
+    // the next segment; one follows
+    __device__ __forceinline__ void next(const AttnParams& P, int per) {
+        idx = 0;
+        if (++h < P.cache.heads) return;
+        h = 0;
+        if (++qt >= qtiles) {
+            qt = 0;
+            do {
+                ++b;
+                request(P, per);
+            } while (qtiles == 0);
+        }
+        row_tile(P, per);
+    }
+};
+
+template <int D>
+struct Smem {
+    static constexpr int kGroups = D / 64;
+    static constexpr int kQ = 0;                                           // [group][128 rows][128 bytes]
+    static constexpr int kKv = kQ + kGroups * kRows * 128;                 // [buffer][K, V][group][64 tokens][128 bytes]
+    static constexpr int kKvBytes = 2 * kGroups * kTile * 128;
+    static constexpr int kScales = kKv + kBufs * kKvBytes;                 // [buffer][64 tokens] (K scales, V scales) floats
+    static constexpr int kScaleBytes = kTile * 2 * kGroups * 4;
+    static constexpr int kRaw = kScales + kBufs * kScaleBytes;             // [stage][4 records]
+    static constexpr int kRawBytes = kTileRecords * kv_record_bytes(D);
+    static constexpr int kSums = kRaw + kRawStages * kRawBytes;            // [2][rows] (reference, sum)
+    static constexpr int kTop = kSums + 2 * kRows * 8;                     // [buffer][4] largest V scale of each record
+    static constexpr int kHave = kTop + kBufs * 16;                        // [buffer] records that a page holds
+    static constexpr int kValid = kHave + kBufs * 4;                       // [raw stage] the same, marks of its last copy
+    static constexpr int kBars = (kValid + kRawStages * 4 + 7) / 8 * 8;
+    static constexpr int kNumBars = 2 * kRawStages + 2 * kBufs + 1 + 6 + 1;
+    static constexpr int kMisc = kBars + kNumBars * 8;                     // TMEM base, abort, last-block flags
+    static constexpr int kScan = kMisc + 16;                               // [threads + 1] units before each thread's requests
+    static constexpr int kUsed = kScan + (kThreads + 1) * 4;
+    static constexpr int kBytes = kUsed + 1024;                            // slack to align to 1024 bytes
+    static_assert(kBytes <= 227 * 1024, "fits one SM's shared memory");
+    static_assert(kScales % 16 == 0 && kRaw % 16 == 0 && kSums % 16 == 0 && kTop % 16 == 0, "alignment");
+};
+
+// Floats of a piece: [D / 4][rows] fours, then (reference, sum) per row.
+template <int D>
+constexpr int kPiece = kRows * (D + 2);
+
+// Sixteen scores of a row: x = sum of the groups' products by their scales.
+template <int D>
+__device__ __forceinline__ void scores16(float* x, const uint32_t (&s0)[16], const uint32_t (&s1)[16], const float* sc) {
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        if constexpr (D == 128) {
+            const float4 d = *reinterpret_cast<const float4*>(sc + 4 * i);
+            x[i] = fmaf(d.y, __uint_as_float(s1[i]), d.x * __uint_as_float(s0[i]));
+        } else {
+            x[i] = sc[2 * i] * __uint_as_float(s0[i]);
+        }
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_constant__ AttnParams P) {
+    using M = Smem<D>;
+    constexpr int NG = M::kGroups;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_base = smem_addr(smem_raw), base = (raw_base + 1023u) & ~1023u;
+    uint8_t* smem = smem_raw + (base - raw_base);
+    uint32_t bar = base + M::kBars;
+    auto take = [&](int n) { const uint32_t b = bar; bar += 8u * n; return b; };
+    const uint32_t raw_full = take(kRawStages), raw_empty = take(kRawStages), kv_full = take(kBufs), kv_empty = take(kBufs);
+    const uint32_t q_full = take(1), s_full = take(2), p_ready = take(2), o_full = take(2), drain = take(1);
+    volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + M::kMisc);
+    volatile uint32_t* abort = misc + 1;
+    volatile uint32_t* last_flag = misc + 2;           // [2]
+    volatile uint32_t* valid = reinterpret_cast<volatile uint32_t*>(smem + M::kValid);
+    volatile uint32_t* have_of = reinterpret_cast<volatile uint32_t*>(smem + M::kHave);
+    uint32_t* scan = reinterpret_cast<uint32_t*>(smem + M::kScan);
+    const AttnArgs& a = P.a;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int heads = P.cache.heads, per = kRows / P.group;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kRawStages; ++s) {
+            mbar_init(raw_full + 8 * s, 1);
+            mbar_init(raw_empty + 8 * s, 4);
+            valid[s] = 0u;
+        }
+        for (int s = 0; s < kBufs; ++s) {
+            mbar_init(kv_full + 8 * s, 4);
+            mbar_init(kv_empty + 8 * s, 1);
+        }
+        mbar_init(q_full, kSoftmaxThreads / 32);
+        for (int w = 0; w < 2; ++w) {
+            mbar_init(s_full + 8 * w, 1);
+            mbar_init(p_ready + 8 * w, 4);
+            mbar_init(o_full + 8 * w, 1);
+        }
+        mbar_init(drain, 1);
+        *abort = 0u;
+        fence_mbar_init();
+    }
+    if (warp == 13) {
+        tmem_alloc(base + M::kMisc, kTmemCols);
+        tmem_relinquish();
+    }
+    // units before each thread's share of the requests
+    const int each = (a.batch + kThreads - 1) / kThreads;
+    {
+        uint32_t* warp_sums = reinterpret_cast<uint32_t*>(smem + M::kSums);
+        const int b0 = min(static_cast<int>(threadIdx.x) * each, a.batch), b1 = min(b0 + each, a.batch);
+        Walk w{};
+        uint32_t mine = 0;
+        for (w.b = b0; w.b < b1; ++w.b) {
+            w.request(P, per);
+            mine += w.units(P, per);
+        }
+        uint32_t in = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, in, d);
+            if (lane >= d) in += o;
+        }
+        if (lane == 31) warp_sums[warp] = in;
+        __syncthreads();
+        uint32_t at = in - mine;
+        for (int i = 0; i < warp; ++i) at += warp_sums[i];
+        scan[threadIdx.x] = at;
+        if (threadIdx.x == kThreads - 1) scan[kThreads] = at + mine;
+    }
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = misc[0];
+    const uint32_t total = scan[kThreads];             // below 2^32: checked on the host
+    const uint32_t blocks = min(gridDim.x, max(total, 1u));
+    const bool idle = blockIdx.x >= min(blocks, total);
+    const uint32_t u0 = idle ? 0 : static_cast<uint32_t>(static_cast<uint64_t>(total) * blockIdx.x / blocks);
+    const uint32_t u1 = idle ? 0 : static_cast<uint32_t>(static_cast<uint64_t>(total) * (blockIdx.x + 1) / blocks);
+    // the segment and tile of unit u
+    auto locate = [&](uint32_t u, Walk& w) {
+        int lo = 0, hi = kThreads - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (scan[mid] <= u) lo = mid;
+            else hi = mid - 1;
+        }
+        uint32_t at = scan[lo];
+        w.b = lo * each;
+        w.request(P, per);
+        for (w.qt = 0;; ++w.qt) {
+            while (w.qt >= w.qtiles) {
+                w.qt = 0;
+                ++w.b;
+                w.request(P, per);
+            }
+            w.row_tile(P, per);
+            const uint32_t units = static_cast<uint32_t>(w.tiles) * heads;
+            if (u < at + units) break;
+            at += units;
+        }
+        w.h = static_cast<int>((u - at) / static_cast<uint32_t>(w.tiles));
+        w.idx = static_cast<int>(u - at - static_cast<uint32_t>(w.h) * w.tiles);
+    };
+    auto give_up = [&]() {
+        *abort = 1u;
+        atomicCAS(P.status, 0u, kAttnTimeout);
+    };
+
+    if (warp == 12) {
+        // ------------------------------------------------------- producer --
+        const uint32_t count = u1 - u0;
+        if (lane < kRawStages && static_cast<uint32_t>(lane) < count) {
+            Walk w;
+            locate(u0 + lane, w);
+            uint32_t turn = 0;
+            for (uint32_t n = lane;;) {
+                const int tok0 = w.first_token();
+                const int records = min(max((w.len - tok0 + kKvTokens - 1) / kKvTokens, 0), kTileRecords);
+                const int32_t* row = a.table + static_cast<int64_t>(w.b) * a.table_stride;
+                int page[kTileRecords];
+#pragma unroll
+                for (int i = 0; i < kTileRecords; ++i) page[i] = i < records ? row[(tok0 + i * kKvTokens) >> P.cache.page_shift] : -1;
+                if (turn > 0 && !wait_phase(raw_empty + 8 * lane, (turn - 1) & 1u, P.timeout_ns, abort)) {
+                    give_up();
+                    break;
+                }
+                uint32_t have = 0;
+#pragma unroll
+                for (int i = 0; i < kTileRecords; ++i) have |= static_cast<uint32_t>(page[i] >= 0 && page[i] < P.cache.pages) << i;
+                // (testing aid: with stall the first unit's bytes are announced but
+                // never copied; its wait can only time out)
+                const bool copied = !(P.stall && n == 0);
+                valid[lane] = have | (copied ? kIssued : 0u) | ((turn & 1u) ? kOddTurn : 0u);
+                mbar_arrive_expect_tx(raw_full + 8 * lane, __popc(have) * kv_record_bytes(D));
+                if (copied) {
+                    const uint32_t dst = base + M::kRaw + lane * M::kRawBytes;
+#pragma unroll
+                    for (int i = 0; i < kTileRecords; ++i) {
+                        if (!((have >> i) & 1)) continue;
+                        const int tok = tok0 + i * kKvTokens;
+                        bulk_g2s(dst + i * kv_record_bytes(D),
+                                 P.cache.record((static_cast<int64_t>(page[i]) << P.cache.page_shift) + (tok & (P.cache.page_size - 1)), w.h),
+                                 kv_record_bytes(D), raw_full + 8 * lane);
+                    }
+                }
+                ++turn;
+                n += kRawStages;
+                if (n >= count) break;
+                int idx = w.idx + kRawStages;
+                while (idx >= w.tiles) {
+                    idx -= w.tiles;
+                    w.next(P, per);
+                }
+                w.idx = idx;
+            }
+            // the last copy into the stage lands before the block ends, also after an abort
+            if (valid[lane] & kIssued) wait_phase(raw_full + 8 * lane, valid[lane] & kOddTurn ? 1u : 0u, kAttnDrainNs, nullptr);
+        }
+        __syncwarp();
+    } else if (warp == 13) {
+        // ------------------------------------------------------ MMA issue --
+        if (lane == 0) {
+            bool ok = u0 < u1;
+            uint32_t it = 0, segs = 0, p_turn[2] = {0, 0};
+            Walk w;
+            if (ok) locate(u0, w);
+            auto products = [&](uint32_t i, uint32_t n) {          // S of unit n (i-th of the segment)
+                const uint32_t buf = n % kBufs, half = i & 1;
+                if (!wait_phase(kv_full + 8 * buf, (n / kBufs) & 1u, P.timeout_ns, abort)) return false;
+                tc_fence_after_sync();
+                const uint32_t k = base + M::kKv + buf * M::kKvBytes;
+#pragma unroll
+                for (int j = 0; j < NG; ++j)
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        mma_ss(tmem + half * 128 + 64 * j, smem_desc_sw128(base + M::kQ + j * (kRows * 128) + kk * 32),
+                               smem_desc_sw128(k + j * (kTile * 128) + kk * 32), kDescS, kk != 0);
+                mma_commit(s_full + 8 * half);
+                return true;
+            };
+            for (uint32_t u = u0; u < u1 && ok;) {
+                const uint32_t count = min(static_cast<uint32_t>(w.tiles - w.idx), u1 - u);
+                ok = wait_phase(q_full, segs & 1u, P.timeout_ns, abort);
+                tc_fence_after_sync();
+                if (ok) ok = products(0, it);
+                if (ok && count > 1) ok = products(1, it + 1);
+                for (uint32_t i = 0; i < count && ok; ++i) {
+                    const uint32_t half = i & 1, buf = (it + i) % kBufs;
+                    ok = wait_phase(p_ready + 8 * half, p_turn[half]++ & 1u, P.timeout_ns, abort);
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    const uint32_t v = base + M::kKv + buf * M::kKvBytes + NG * (kTile * 128);
+#pragma unroll
+                    for (int j = 0; j < NG; ++j)
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_ts(tmem + 256 + half * 128 + 64 * j, tmem + half * 128 + 32 * j + 8 * kk,
+                                   smem_desc_mn_sw128(v + j * (kTile * 128) + kk * 2048), kDescO, i > 1 || kk != 0);
+                    mma_commit(kv_empty + 8 * buf);
+                    if (i + 2 >= count) mma_commit(o_full + 8 * half);
+                    if (i + 2 < count) ok = products(i + 2, it + i + 2);
+                }
+                it += count;
+                ++segs;
+                u += count;
+                if (u < u1) w.next(P, per);
+            }
+            if (!ok && u0 < u1) give_up();
+            mma_commit(drain);                         // every product of this block finished (also after an abort)
+            wait_phase(drain, 0u, kAttnDrainNs, nullptr);
+        }
+        __syncwarp();
+    } else if (warp >= 8) {
+        // --------------------------------------------------------- decode --
+        const int rec = warp - 8;                      // of the tile
+        bool ok = true;
+        for (uint32_t n = 0; n < u1 - u0; ++n) {
+            const uint32_t s = n % kRawStages, buf = n % kBufs;
+            ok = wait_phase(raw_full + 8 * s, (n / kRawStages) & 1u, P.timeout_ns, abort);
+            if (ok && n >= kBufs) ok = wait_phase(kv_empty + 8 * buf, (n / kBufs - 1) & 1u, P.timeout_ns, abort);
+            if (!__all_sync(0xFFFFFFFFu, ok)) break;
+            const uint8_t* from = smem + M::kRaw + s * M::kRawBytes + rec * kv_record_bytes(D);
+            uint8_t* kt = smem + M::kKv + buf * M::kKvBytes;
+            uint8_t* vt = kt + NG * (kTile * 128);
+            const uint32_t have = valid[s];
+            const int g = lane >> 2, t = lane & 3;
+            // 16-byte chunk `i` of a token's row in a group's tile, swizzled
+            auto put = [&](uint8_t* tile, int token, int j, int i, uint32_t word) {
+                const uint32_t sh = word >> 8;
+                *reinterpret_cast<uint4*>(tile + j * (kTile * 128) + token * 128 + ((i ^ (token & 7)) << 4)) =
+                    make_uint4(decode_pair<kPn4t, 0>(word, sh), decode_pair<kPn4t, 1>(word, sh), decode_pair<kPn4t, 2>(word, sh),
+                               decode_pair<kPn4t, 3>(word, sh));
+            };
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if constexpr (NG == 2) {
+                    const uint4 kw = lds_u128(from + h * 512 + lane * 16), vw = lds_u128(from + kv_v_codes(D) + h * 512 + lane * 16);
+                    const int kt0 = rec * 16 + h * 8 + g, vt0 = rec * 16 + h * 8 + 2 * t;
+                    put(kt, kt0, 0, 2 * t, kw.x);
+                    put(kt, kt0, 0, 2 * t + 1, kw.y);
+                    put(kt, kt0, 1, 2 * t, kw.z);
+                    put(kt, kt0, 1, 2 * t + 1, kw.w);
+                    put(vt, vt0, 0, g, vw.x);
+                    put(vt, vt0, 1, g, vw.y);
+                    put(vt, vt0 + 1, 0, g, vw.z);
+                    put(vt, vt0 + 1, 1, g, vw.w);
+                } else {
+                    const uint2 kw = lds_u64(from + h * 256 + lane * 8), vw = lds_u64(from + kv_v_codes(D) + h * 256 + lane * 8);
+                    const int kt0 = rec * 16 + h * 8 + g, vt0 = rec * 16 + h * 8 + 2 * t;
+                    put(kt, kt0, 0, 2 * t, kw.x);
+                    put(kt, kt0, 0, 2 * t + 1, kw.y);
+                    put(vt, vt0, 0, g, vw.x);
+                    put(vt, vt0 + 1, 0, g, vw.y);
+                }
+            }
+            // scales: (K by scale * log2 e, V) of a token; none where no page holds the record
+            float top = 0.0f;
+            if (lane < 16) {
+                float* sc = reinterpret_cast<float*>(smem + M::kScales + buf * M::kScaleBytes) + (rec * 16 + lane) * 2 * NG;
+                const bool real = (have >> rec) & 1;
+#pragma unroll
+                for (int j = 0; j < NG; ++j) {
+                    const float dk = real ? lds_half_as_float(from + kv_k_scales(D) + (lane * NG + j) * 2) * P.scale_log2 : 0.0f;
+                    const float dv = real ? lds_half_as_float(from + kv_v_scales(D) + (lane * NG + j) * 2) : 0.0f;
+                    sc[j] = dk;
+                    sc[NG + j] = dv;
+                    top = fmaxf(top, fabsf(dv));
+                }
+            }
+#pragma unroll
+            for (int d = 8; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+            if (lane == 0) {
+                reinterpret_cast<float*>(smem + M::kTop)[buf * 4 + rec] = top;
+                if (rec == 0) have_of[buf] = have & 15u;
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(kv_full + 8 * buf);
+                mbar_arrive(raw_empty + 8 * s);
+            }
+        }
+        if (!ok) give_up();
+    } else {
+        // -------------------------------------------------------- softmax --
+        const int half = warp >> 2, row = threadIdx.x & 127;
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + half * 128 + lanes, to = tmem + 256 + half * 128 + lanes;
+        float2* sums = reinterpret_cast<float2*>(smem + M::kSums);         // [2][rows]
+        float2* slot_sums = nullptr;
+        auto block_slot = [&](uint32_t c, bool begins) { return P.block_slots + (2 * static_cast<int64_t>(c) + begins) * kPiece<D>; };
+        bool ok = true;
+        uint32_t it = 0, s_turn = 0, o_turn[2] = {0, 0};
+        uint32_t shared_seg[2] = {0xFFFFFFFFu, 0xFFFFFFFFu}, shared_tiles[2] = {0, 0};   // pieces of segments of other blocks too
+        Walk w;
+        if (u0 < u1) locate(u0, w);
+        for (uint32_t u = u0; u < u1;) {
+            const int first = w.idx;
+            const uint32_t count = min(static_cast<uint32_t>(w.tiles - first), u1 - u);
+            const int rows = w.nt * P.group;
+            // the row tile's queries, swizzled; rows past them are zero
+            for (int i = threadIdx.x; i < kRows * (D / 8); i += kSoftmaxThreads) {
+                const int r = i / (D / 8), c = i % (D / 8);
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (r < rows) {
+                    const int tq = r / P.group;
+                    v = *reinterpret_cast<const uint4*>(a.q + (static_cast<int64_t>(w.q0) + w.t0 + tq) * a.q_stride +
+                                                        (w.h * P.group + r - tq * P.group) * D + 8 * c);
+                }
+                *reinterpret_cast<uint4*>(smem + M::kQ + (c >> 3) * (kRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
+            }
+            fence_proxy_async_smem();
+            tc_fence_before_sync();                    // the last segment's O has been read
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full);
+            const int pos = w.pos_lo + min(row, max(rows - 1, 0)) / P.group;
+            const int window = a.window ? a.window : INT32_MAX;
+            float ref = -INFINITY, sum = 0.0f;
+            for (uint32_t i = half; i < count; i += 2) {
+                const uint32_t n = it + i, buf = n % kBufs;
+                if (ok) {
+                    ok = wait_phase(s_full + 8 * half, s_turn & 1u, P.timeout_ns, abort);
+                    if (ok) ok = wait_phase(kv_full + 8 * buf, (n / kBufs) & 1u, P.timeout_ns, abort);
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    if (!ok && lane == 0) give_up();
+                }
+                if (!ok) break;
+                ++s_turn;
+                tc_fence_after_sync();
+                w.idx = first + static_cast<int>(i);
+                const int tok0 = w.first_token();
+                const float* sc = reinterpret_cast<const float*>(smem + M::kScales + buf * M::kScaleBytes);
+                const float4 tops = *reinterpret_cast<const float4*>(smem + M::kTop + buf * 16);
+                const uint32_t have = have_of[buf];
+                const bool plain = have == 15u && tok0 + kTile - 1 <= w.pos_lo && (tok0 > w.pos_hi - window || tok0 + kTile <= a.sinks);
+                float x[kTile];
+                {
+                    uint32_t s0[2][16], s1[2][16];
+                    tmem_ld16(ts, s0[0]);
+                    if (NG == 2) tmem_ld16(ts + 64, s1[0]);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        tmem_wait_ld();
+                        if (c < 3) {
+                            tmem_ld16(ts + 16 * (c + 1), s0[(c + 1) & 1]);
+                            if (NG == 2) tmem_ld16(ts + 64 + 16 * (c + 1), s1[(c + 1) & 1]);
+                        }
+                        scores16<D>(x + 16 * c, s0[c & 1], s1[c & 1], sc + 16 * c * 2 * NG);
+                    }
+                }
+                uint64_t seen = ~0ull;
+                if (!plain) {
+                    seen = 0;
+#pragma unroll
+                    for (int c = 0; c < kTile; ++c) {
+                        const int tok = tok0 + c;
+                        const bool s = ((have >> (c >> 4)) & 1) && tok <= pos && (tok > pos - window || tok < a.sinks);
+                        seen |= static_cast<uint64_t>(s) << c;
+                        if (!s) x[c] = -INFINITY;
+                    }
+                }
+                float top = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < kTile; ++c) top = fmaxf(top, x[c]);
+                top += lg2(fminf(fmaxf(fmaxf(fmaxf(tops.x, tops.y), fmaxf(tops.z, tops.w)), 5.9604645e-8f), 65504.0f));
+                // the reference moves when it is passed by far
+                const bool move = top > ref + kSlack || (ref == -INFINITY && top > -INFINITY);
+                if (__any_sync(0xFFFFFFFFu, move)) {
+                    const float to_ref = move ? top - kMargin : ref;
+                    const float f = ref == -INFINITY ? 0.0f : ex2(ref - to_ref);
+                    ref = to_ref;
+                    sum *= f;
+                    if (i >= 2) {                      // O holds something
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(to + c, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                            tmem_st32(to + c, o);
+                        }
+                    }
+                }
+                const float base_ref = ref == -INFINITY ? 0.0f : ref;
+#pragma unroll
+                for (int c = 0; c < kTile; ++c) {
+                    x[c] = ex2(x[c] - base_ref);
+                    sum += x[c];
+                }
+#pragma unroll
+                for (int j = 0; j < NG; ++j) {
+                    uint32_t p[32];
+#pragma unroll
+                    for (int c = 0; c < kTile; c += 2) {
+                        float p0 = x[c] * sc[(c * 2 + 1) * NG + j], p1 = x[c + 1] * sc[(c * 2 + 3) * NG + j];
+                        if (!plain) {                  // a hidden token's scale may be anything, NaN too
+                            p0 = (seen >> c) & 1 ? p0 : 0.0f;
+                            p1 = (seen >> (c + 1)) & 1 ? p1 : 0.0f;
+                        }
+                        p[c / 2] = pack_half2(p0, p1);
+                    }
+                    tmem_st32(ts + 32 * j, p);
+                }
+                tmem_wait_st();
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_ready + 8 * half);
+            }
+            // ------------------------------------- join of the two halves --
+            sums[half * kRows + row] = make_float2(ref, sum);
+            const uint32_t halves = min(count, 2u);
+            for (uint32_t k = 0; k < halves && ok; ++k) ok = wait_phase(o_full + 8 * k, o_turn[k]++ & 1u, P.timeout_ns, abort);
+            ok = __all_sync(0xFFFFFFFFu, ok);
+            if (!ok && lane == 0) give_up();
+            tc_fence_after_sync();
+            softmax_sync();
+            const float2 e0 = sums[row], e1 = sums[kRows + row];
+            const float m = fmaxf(e0.x, e1.x);
+            const float f0 = e0.x == -INFINITY ? 0.0f : ex2(e0.x - m), f1 = e1.x == -INFINITY ? 0.0f : ex2(e1.x - m);
+            const float l = f0 * e0.y + f1 * e1.y;
+            const bool whole = count == static_cast<uint32_t>(w.tiles);
+            const int tq = row / P.group;
+            const int64_t at = row < rows ? (static_cast<int64_t>(w.q0) + w.t0 + tq) * a.heads + w.h * P.group + row - tq * P.group : -1;
+            float* slot = nullptr;
+            if (!whole) {
+                const int kind = first == 0;
+                slot = block_slot(blockIdx.x, kind);
+                slot_sums = reinterpret_cast<float2*>(slot + kRows * D);
+                shared_seg[kind] = u - first;
+                shared_tiles[kind] = w.tiles;
+                if (half == 0) slot_sums[row] = make_float2(m, l);
+            }
+            const float inv = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
+            const float g0 = f0 * inv, g1 = f1 * inv;
+            if (whole && half == 0 && a.lse && at >= 0) a.lse[at] = log_sum(m, l);
+            if (ok) {
+#pragma unroll 1
+                for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
+                    uint32_t o0[16], o1[16];
+                    tmem_ld16(tmem + 256 + lanes + c, o0);
+                    if (halves > 1) tmem_ld16(tmem + 384 + lanes + c, o1);
+                    tmem_wait_ld();
+                    float o[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        // a half that saw nothing of a row left nothing of it but may have no number there
+                        o[k] = g0 == 0.0f ? 0.0f : g0 * __uint_as_float(o0[k]);
+                        if (halves > 1 && g1 != 0.0f) o[k] = fmaf(g1, __uint_as_float(o1[k]), o[k]);
+                    }
+                    if (!whole) {
+#pragma unroll
+                        for (int k = 0; k < 16; k += 4)
+                            reinterpret_cast<float4*>(slot)[((c + k) / 4) * kRows + row] = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                    } else if (at >= 0) {
+                        uint4* out = reinterpret_cast<uint4*>(a.out + at * D + c);
+                        out[0] = make_uint4(pack_half2(o[0], o[1]), pack_half2(o[2], o[3]), pack_half2(o[4], o[5]), pack_half2(o[6], o[7]));
+                        out[1] = make_uint4(pack_half2(o[8], o[9]), pack_half2(o[10], o[11]), pack_half2(o[12], o[13]), pack_half2(o[14], o[15]));
+                    }
+                }
+            }
+            softmax_sync();                            // sums and Q are written again
+            it += count;
+            u += count;
+            if (u < u1) w.next(P, per);
+        }
+
+        // --------------------------------------- segments of several blocks --
+        if (u0 < u1) {
+            auto block_of = [&](uint32_t x) {          // the block that holds unit x
+                return static_cast<uint32_t>(((static_cast<uint64_t>(x) + 1) * blocks + total - 1) / total - 1);
+            };
+            if (threadIdx.x < 2) {
+                bool last = false;
+                const uint32_t seg = shared_seg[threadIdx.x];
+                if (seg != 0xFFFFFFFFu) {
+                    const uint32_t c0 = block_of(seg), c1 = block_of(seg + shared_tiles[threadIdx.x] - 1);
+                    __threadfence();
+                    last = atomicAdd(&P.counters[c0], 1u) == c1 - c0;
+                    __threadfence();
+                    if (last) P.counters[c0] = 0u;
+                }
+                last_flag[threadIdx.x] = last;
+            }
+            softmax_sync();
+            float* factors = reinterpret_cast<float*>(smem);               // [parts][rows]: no product reads Q or the tiles any more
+            for (int kind = 0; kind < 2; ++kind) {
+                if (!last_flag[kind]) continue;
+                const uint32_t seg = shared_seg[kind], c0 = block_of(seg), c1 = block_of(seg + shared_tiles[kind] - 1);
+                const int parts = static_cast<int>(c1 - c0 + 1);
+                locate(seg, w);
+                const int rows = w.nt * P.group, tq = row / P.group;
+                const int64_t at = row < rows ? (static_cast<int64_t>(w.q0) + w.t0 + tq) * a.heads + w.h * P.group + row - tq * P.group : -1;
+                if (half == 0) {
+                    auto part_sum = [&](int p) { return __ldcg(reinterpret_cast<const float2*>(block_slot(c0 + p, p == 0) + kRows * D) + row); };
+                    float m = -INFINITY, l = 0.0f;
+#pragma unroll 4
+                    for (int p = 0; p < parts; ++p) m = fmaxf(m, part_sum(p).x);
+#pragma unroll 4
+                    for (int p = 0; p < parts; ++p) {
+                        const float2 v = part_sum(p);
+                        const float f = v.x == -INFINITY ? 0.0f : ex2(v.x - m);
+                        factors[p * kRows + row] = f;
+                        l += f * v.y;
+                    }
+                    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                    for (int p = 0; p < parts; ++p) factors[p * kRows + row] *= inv;
+                    if (a.lse && at >= 0) a.lse[at] = log_sum(m, l);
+                }
+                softmax_sync();
+                if (at >= 0) {
+                    for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 4) {
+                        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 8
+                        for (int p = 0; p < parts; ++p) {
+                            const float f = factors[p * kRows + row];
+                            const float4 v = __ldcg(reinterpret_cast<const float4*>(block_slot(c0 + p, p == 0)) + (c / 4) * kRows + row);
+                            o.x = fmaf(f, v.x, o.x); o.y = fmaf(f, v.y, o.y); o.z = fmaf(f, v.z, o.z); o.w = fmaf(f, v.w, o.w);
+                        }
+                        *reinterpret_cast<uint2*>(a.out + at * D + c) = make_uint2(pack_half2(o.x, o.y), pack_half2(o.z, o.w));
+                    }
+                }
+                softmax_sync();                        // the factors are written again
+            }
+        }
+    }
+    // ------------------------------------------------------------ teardown --
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == 13) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, kTmemCols);
+    }
+}
+
+template <int D>
+cudaError_t launch(AttnParams P, uint8_t* ws, int num_sms, cudaStream_t s) {
+    static std::atomic<uint64_t> smem_set{0};
+    if (cudaError_t e = set_smem_limit_once(attn_tc_kernel<D>, Smem<D>::kBytes, smem_set); e != cudaSuccess) return e;
+    P.status = reinterpret_cast<uint32_t*>(ws);
+    P.counters = reinterpret_cast<uint32_t*>(ws + 256);
+    P.block_slots = reinterpret_cast<float*>(ws + 256 + attn_counter_bytes(num_sms));
+    constexpr int kMost = Smem<D>::kScales / (kRows * 4);                  // blocks whose factors fit the place of Q and the tiles
+    attn_tc_kernel<D><<<num_sms < kMost ? num_sms : kMost, kThreads, Smem<D>::kBytes, s>>>(P);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+bool attn_tc_takes(const AttnArgs& a, const KvGeometry& g) {
+    const int group = a.heads / g.heads;
+    return g.D <= 128 && group <= kRows && static_cast<int64_t>(a.max_queries) * group > 16;
+}
+
+size_t attn_tc_workspace_bytes(int num_sms) {
+    return 256 + attn_counter_bytes(num_sms) + 2 * static_cast<size_t>(num_sms) * kPiece<128> * 4;
+}
+
+cudaError_t launch_attention_tc(AttnParams P, uint8_t* ws, int num_sms, cudaStream_t s) {
+    return P.cache.D == 64 ? launch<64>(P, ws, num_sms, s) : launch<128>(P, ws, num_sms, s);
+}
+
+}  // namespace pn
