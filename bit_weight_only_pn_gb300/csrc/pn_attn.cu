@@ -586,13 +586,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && D <= 128 ? kCtasPerSm : 1
                 look();
             }
             uint32_t turn = 0;
-            uint64_t t0 = 0;
+            int64_t t0 = 0;
             for (uint32_t polls = 0; n < count; ++polls) {
                 if (turn > 0 && !mbar_try_wait(empty(s), (turn - 1) & 1u)) {
                     if (polls % 256 == 255) {
-                        const uint64_t now = globaltimer_ns();
+                        const int64_t now = clock64();
                         if (t0 == 0) t0 = now;
-                        if (*abort || now - t0 > P.timeout_ns) {
+                        if (*abort || now - t0 > cycles_of(P.timeout_ns)) {
                             *abort = 1u;
                             atomicCAS(P.status, 0u, kAttnTimeout);
                             break;

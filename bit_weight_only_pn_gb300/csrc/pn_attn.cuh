@@ -42,17 +42,23 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Polls: a thread parked in mbarrier.try_wait notices a completed phase late.
-static __device__ bool wait_phase(uint32_t bar, uint32_t parity, uint64_t limit_ns, volatile uint32_t* abort) {
-    uint64_t t0 = 0;
+// Nanoseconds in SM cycles, at the fastest clock: limits are at least as long as asked.
+__device__ __forceinline__ int64_t cycles_of(uint64_t ns) { return static_cast<int64_t>(ns) * 21 / 10; }
+
+// Polls: a thread parked in mbarrier.try_wait notices a completed phase late,
+// and so does one that reads the global timer in between (about a thousand
+// cycles); the limit goes by the SM's clock.
+// nap: nanoseconds between polls, for a wait that is in no hurry.
+static __device__ bool wait_phase(uint32_t bar, uint32_t parity, uint64_t limit_ns, volatile uint32_t* abort, uint32_t nap = 0) {
+    if (mbar_try_wait(bar, parity)) return true;
+    const int64_t end = clock64() + cycles_of(limit_ns);
     for (;;) {
 #pragma unroll 1
-        for (int i = 0; i < 128; ++i)
+        for (int i = 0; i < 32; ++i) {
+            if (nap) __nanosleep(nap);
             if (mbar_try_wait(bar, parity)) return true;
-        if (abort && *abort) return false;
-        const uint64_t now = globaltimer_ns();
-        if (t0 == 0) t0 = now;
-        else if (now - t0 > limit_ns) return false;
+        }
+        if ((abort && *abort) || clock64() > end) return false;
     }
 }
 

@@ -41,7 +41,11 @@ namespace {
 constexpr int kRows = 128;                     // MMA M
 constexpr int kTile = 64;                      // tokens per unit, MMA N of S
 constexpr int kTileRecords = kTile / kKvTokens;
-constexpr int kThreads = 14 * 32;
+constexpr int kThreads = 16 * 32;              // warps 14 and 15 fill the last warpgroup
+// Registers per thread after the split of the launch's 128: 256 x 176 + 256 x
+// 80 = 512 x 128.  A row's 64 scores stay in registers.
+constexpr int kSoftmaxRegs = 176, kOtherRegs = 80;
+static_assert(kSoftmaxRegs + kOtherRegs == 2 * 128, "the shares add up to the launch's registers");
 constexpr int kSoftmaxThreads = 256;
 constexpr int kRawStages = 4;
 constexpr int kBufs = 4;                       // decoded tiles
@@ -67,12 +71,13 @@ __device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint3
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %4, p;\n\t}"
         :: "r"(d), "r"(a), "l"(b), "r"(static_cast<uint32_t>(accumulate)), "r"(desc) : "memory");
 }
-// An MN-major tile of 64 values (128 bytes) by tokens with the 128-byte
-// swizzle: 8 tokens to an atom of 1024 bytes (stride byte offset); one atom
-// wide, so the leading byte offset is not used (set alike).
-__device__ __forceinline__ uint64_t smem_desc_mn_sw128(uint32_t addr) {
-    return static_cast<uint64_t>((addr >> 4) & 0x3FFFu) | (static_cast<uint64_t>(1024 >> 4) << 16) |
-           (static_cast<uint64_t>(1024 >> 4) << 32) | (static_cast<uint64_t>(1) << 46) | (static_cast<uint64_t>(2) << 61);
+// One lane of the converged warp: products issued under it keep their operands
+// in uniform registers (issued by a lone diverged lane they took 47 cycles each
+// where the tensor cores take 40).
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 2, %0;" :: "n"(kSoftmaxThreads) : "memory"); }
@@ -139,7 +144,7 @@ struct Smem {
     static constexpr int kQ = 0;                                           // [group][128 rows][128 bytes]
     static constexpr int kKv = kQ + kGroups * kRows * 128;                 // [buffer][K, V][group][64 tokens][128 bytes]
     static constexpr int kKvBytes = 2 * kGroups * kTile * 128;
-    static constexpr int kScales = kKv + kBufs * kKvBytes;                 // [buffer][64 tokens] (K scales, V scales) floats
+    static constexpr int kScales = kKv + kBufs * kKvBytes;                 // [buffer][K scales of each group, V scales][64 tokens] floats
     static constexpr int kScaleBytes = kTile * 2 * kGroups * 4;
     static constexpr int kRaw = kScales + kBufs * kScaleBytes;             // [stage][4 records]
     static constexpr int kRawBytes = kTileRecords * kv_record_bytes(D);
@@ -161,18 +166,173 @@ struct Smem {
 template <int D>
 constexpr int kPiece = kRows * (D + 2);
 
-// Sixteen scores of a row: x = sum of the groups' products by their scales.
-template <int D>
-__device__ __forceinline__ void scores16(float* x, const uint32_t (&s0)[16], const uint32_t (&s1)[16], const float* sc) {
+// Two fp32 numbers in a register pair, and operations on both at once.
+using Two = unsigned long long;
+__device__ __forceinline__ Two two(float a, float b) {
+    Two d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ Two two(uint32_t a, uint32_t b) {
+    Two d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ float2 apart(Two v) {
+    float2 d;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(v));
+    return d;
+}
+__device__ __forceinline__ Two mul2(Two a, Two b) {
+    Two d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ Two add2(Two a, Two b) {
+    Two d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+    Two d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// A row's state in one of the two halves.
+struct RowState {
+    float ref, sum;
+    int pos;
+};
+
+// One tile of a row: S from tensor memory at ts, P over it.  sc: the tile's
+// scales, [K by group, V by group][64 tokens]; big: log2 of the largest V
+// scale; filled: O (at to) holds something.
+template <int D, bool kMasked>
+__device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, const float* sc, float big, bool filled, int tok0, uint32_t have,
+                                             int window, int sinks, RowState& st) {
+    constexpr int NG = D / 64;
+    Two x[kTile / 2];
+    float top2[2] = {-INFINITY, -INFINITY};
+    {
+        uint32_t s[2][NG][16];
+        tmem_ld16(ts, s[0][0]);
+        if constexpr (NG == 2) tmem_ld16(ts + 64, s[0][NG - 1]);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        if constexpr (D == 128) {
-            const float4 d = *reinterpret_cast<const float4*>(sc + 4 * i);
-            x[i] = fmaf(d.y, __uint_as_float(s1[i]), d.x * __uint_as_float(s0[i]));
-        } else {
-            x[i] = sc[2 * i] * __uint_as_float(s0[i]);
+        for (int c = 0; c < 4; ++c) {
+            tmem_wait_ld();
+            if (c < 3) {
+                tmem_ld16(ts + 16 * (c + 1), s[(c + 1) & 1][0]);
+                if constexpr (NG == 2) tmem_ld16(ts + 64 + 16 * (c + 1), s[(c + 1) & 1][NG - 1]);
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {              // four tokens
+                const ulonglong2 d0 = *reinterpret_cast<const ulonglong2*>(sc + 16 * c + 4 * i);
+                Two a = mul2(d0.x, two(s[c & 1][0][4 * i], s[c & 1][0][4 * i + 1]));
+                Two b = mul2(d0.y, two(s[c & 1][0][4 * i + 2], s[c & 1][0][4 * i + 3]));
+                if constexpr (NG == 2) {
+                    const ulonglong2 d1 = *reinterpret_cast<const ulonglong2*>(sc + kTile + 16 * c + 4 * i);
+                    a = fma2(d1.x, two(s[c & 1][NG - 1][4 * i], s[c & 1][NG - 1][4 * i + 1]), a);
+                    b = fma2(d1.y, two(s[c & 1][NG - 1][4 * i + 2], s[c & 1][NG - 1][4 * i + 3]), b);
+                }
+                x[8 * c + 2 * i] = a;
+                x[8 * c + 2 * i + 1] = b;
+                if constexpr (!kMasked) {
+                    const float2 u = apart(a), v = apart(b);
+                    top2[0] = max3(top2[0], u.x, u.y);
+                    top2[1] = max3(top2[1], v.x, v.y);
+                }
+            }
         }
     }
+    uint32_t seen[2] = {~0u, ~0u};
+    if constexpr (kMasked) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            seen[k] = 0;
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+                const int tok = tok0 + 32 * k + c;
+                const bool s = ((have >> (2 * k + c / 16)) & 1u) && tok <= st.pos && (tok > st.pos - window || tok < sinks);
+                seen[k] |= static_cast<uint32_t>(s) << c;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kTile / 2; ++i) {
+            float2 v = apart(x[i]);
+            if (!((seen[i / 16] >> (2 * i % 32)) & 1u)) v.x = -INFINITY;
+            if (!((seen[i / 16] >> (2 * i % 32 + 1)) & 1u)) v.y = -INFINITY;
+            x[i] = two(v.x, v.y);
+        }
+    }
+    if constexpr (kMasked) {
+#pragma unroll
+        for (int i = 0; i < kTile / 2; ++i) {
+            const float2 v = apart(x[i]);
+            top2[i & 1] = max3(top2[i & 1], v.x, v.y);
+        }
+    }
+    const float top = fmaxf(top2[0], top2[1]) + big;
+    // the reference moves when it is passed by far
+    const bool move = top > st.ref + kSlack || (st.ref == -INFINITY && top > -INFINITY);
+    if (__any_sync(0xFFFFFFFFu, move)) {
+        const float ref = move ? top - kMargin : st.ref;
+        const float f = st.ref == -INFINITY ? 0.0f : ex2(st.ref - ref);
+        st.ref = ref;
+        st.sum *= f;
+        if (filled) {
+#pragma unroll 1
+            for (int c = 0; c < D; c += 16) {
+                uint32_t o[16];
+                tmem_ld16(to + c, o);
+                tmem_wait_ld();
+#pragma unroll
+                for (int k = 0; k < 16; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
+                tmem_st16(to + c, o);
+            }
+        }
+    }
+    const float less = st.ref == -INFINITY ? 0.0f : -st.ref;
+    const Two less2 = two(less, less);
+    Two sum[2] = {two(st.sum, 0.0f), two(0.0f, 0.0f)};
+    // exponentials and, beside them, the probabilities by group
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+        uint32_t p[NG][16];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {                  // four tokens
+            Two e[2];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const float2 v = apart(add2(x[16 * q + 2 * i + k], less2));
+                e[k] = two(ex2(v.x), ex2(v.y));
+                sum[k] = add2(sum[k], e[k]);
+            }
+#pragma unroll
+            for (int j = 0; j < NG; ++j) {
+                const ulonglong2 d = *reinterpret_cast<const ulonglong2*>(sc + (NG + j) * kTile + 32 * q + 4 * i);
+                float2 a = apart(mul2(d.x, e[0])), b = apart(mul2(d.y, e[1]));
+                if constexpr (kMasked) {               // a hidden token's scale may be anything, NaN too
+                    a.x = (seen[q] >> (4 * i)) & 1u ? a.x : 0.0f;
+                    a.y = (seen[q] >> (4 * i + 1)) & 1u ? a.y : 0.0f;
+                    b.x = (seen[q] >> (4 * i + 2)) & 1u ? b.x : 0.0f;
+                    b.y = (seen[q] >> (4 * i + 3)) & 1u ? b.y : 0.0f;
+                }
+                p[j][2 * i] = pack_half2(a.x, a.y);
+                p[j][2 * i + 1] = pack_half2(b.x, b.y);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < NG; ++j) tmem_st16(ts + 32 * j + 16 * q, p[j]);
+    }
+    const float2 both = apart(add2(sum[0], sum[1]));
+    st.sum = both.x + both.y;
 }
 
 template <int D>
@@ -283,23 +443,40 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         atomicCAS(P.status, 0u, kAttnTimeout);
     };
 
-    if (warp == 12) {
+    // one register count to a warpgroup, set where its roles part
+    if (warp >= 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kOtherRegs));
+        if (warp == 12) {
         // ------------------------------------------------------- producer --
         const uint32_t count = u1 - u0;
         if (lane < kRawStages && static_cast<uint32_t>(lane) < count) {
             Walk w;
             locate(u0 + lane, w);
-            uint32_t turn = 0;
-            for (uint32_t n = lane;;) {
-                const int tok0 = w.first_token();
+            int tok0 = 0, page[kTileRecords];
+            auto look = [&]() {                // the current unit's pages
+                tok0 = w.first_token();
                 const int records = min(max((w.len - tok0 + kKvTokens - 1) / kKvTokens, 0), kTileRecords);
                 const int32_t* row = a.table + static_cast<int64_t>(w.b) * a.table_stride;
-                int page[kTileRecords];
 #pragma unroll
                 for (int i = 0; i < kTileRecords; ++i) page[i] = i < records ? row[(tok0 + i * kKvTokens) >> P.cache.page_shift] : -1;
-                if (turn > 0 && !wait_phase(raw_empty + 8 * lane, (turn - 1) & 1u, P.timeout_ns, abort)) {
-                    give_up();
-                    break;
+            };
+            look();
+            uint32_t turn = 0, n = lane;
+            int64_t t0 = 0;
+            // Every lane polls its own stage and copies as soon as it is free: lanes
+            // that left a wait one by one would meet again behind it, and four
+            // stages be filled when the last of them is empty.
+            for (uint32_t polls = 0; n < count; ++polls) {
+                if (turn > 0 && !mbar_try_wait(raw_empty + 8 * lane, (turn - 1) & 1u)) {
+                    if (polls % 64 == 63) {
+                        const int64_t now = clock64();
+                        if (t0 == 0) t0 = now;
+                        if (*abort || now - t0 > cycles_of(P.timeout_ns)) {
+                            give_up();
+                            break;
+                        }
+                    }
+                    continue;
                 }
                 uint32_t have = 0;
 #pragma unroll
@@ -311,90 +488,124 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 mbar_arrive_expect_tx(raw_full + 8 * lane, __popc(have) * kv_record_bytes(D));
                 if (copied) {
                     const uint32_t dst = base + M::kRaw + lane * M::kRawBytes;
+                    if (P.cache.page_size >= kTile) {  // one page holds the tile: its records follow each other
+                        if (have)
+                            bulk_g2s(dst, P.cache.record((static_cast<int64_t>(page[0]) << P.cache.page_shift) + (tok0 & (P.cache.page_size - 1)), w.h),
+                                     __popc(have) * kv_record_bytes(D), raw_full + 8 * lane);
+                    } else {
 #pragma unroll
-                    for (int i = 0; i < kTileRecords; ++i) {
-                        if (!((have >> i) & 1)) continue;
-                        const int tok = tok0 + i * kKvTokens;
-                        bulk_g2s(dst + i * kv_record_bytes(D),
-                                 P.cache.record((static_cast<int64_t>(page[i]) << P.cache.page_shift) + (tok & (P.cache.page_size - 1)), w.h),
-                                 kv_record_bytes(D), raw_full + 8 * lane);
+                        for (int i = 0; i < kTileRecords; ++i) {
+                            if (!((have >> i) & 1)) continue;
+                            const int tok = tok0 + i * kKvTokens;
+                            bulk_g2s(dst + i * kv_record_bytes(D),
+                                     P.cache.record((static_cast<int64_t>(page[i]) << P.cache.page_shift) + (tok & (P.cache.page_size - 1)), w.h),
+                                     kv_record_bytes(D), raw_full + 8 * lane);
+                        }
                     }
                 }
                 ++turn;
+                t0 = 0;
                 n += kRawStages;
-                if (n >= count) break;
-                int idx = w.idx + kRawStages;
-                while (idx >= w.tiles) {
-                    idx -= w.tiles;
-                    w.next(P, per);
+                if (n < count) {
+                    int idx = w.idx + kRawStages;
+                    while (idx >= w.tiles) {
+                        idx -= w.tiles;
+                        w.next(P, per);
+                    }
+                    w.idx = idx;
+                    look();
                 }
-                w.idx = idx;
             }
             // the last copy into the stage lands before the block ends, also after an abort
             if (valid[lane] & kIssued) wait_phase(raw_full + 8 * lane, valid[lane] & kOddTurn ? 1u : 0u, kAttnDrainNs, nullptr);
         }
         __syncwarp();
-    } else if (warp == 13) {
+        } else if (warp == 13) {
         // ------------------------------------------------------ MMA issue --
-        if (lane == 0) {
+        if (elect_one()) {
             bool ok = u0 < u1;
-            uint32_t it = 0, segs = 0, p_turn[2] = {0, 0};
+            uint32_t segs = 0;
             Walk w;
             if (ok) locate(u0, w);
-            auto products = [&](uint32_t i, uint32_t n) {          // S of unit n (i-th of the segment)
-                const uint32_t buf = n % kBufs, half = i & 1;
-                if (!wait_phase(kv_full + 8 * buf, (n / kBufs) & 1u, P.timeout_ns, abort)) return false;
-                tc_fence_after_sync();
-                const uint32_t k = base + M::kKv + buf * M::kKvBytes;
+            auto wait = [&](uint32_t b, uint32_t parity) {
+                return mbar_try_wait(b, parity) || wait_phase(b, parity, P.timeout_ns, abort);
+            };
+            // Descriptors: the upper words are constants (stride byte offset 1024, version
+            // 1, 128-byte swizzle), the lower ones address and leading byte offset.  K
+            // and Q: rows of 128 bytes, K-major, 8 rows to 1024 bytes.  V the same
+            // bytes as an MN-major tile, 64 values by tokens, 8 tokens to 1024; one
+            // atom wide, so its leading offset is not used (set to 1024).
+            constexpr uint32_t kHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+            constexpr uint32_t kStep = M::kKvBytes >> 4;
+            auto desc = [](uint32_t low) { return (static_cast<uint64_t>(kHigh) << 32) | low; };
+            const uint32_t q_low = ((base + M::kQ) >> 4) | (1u << 16);
+            const uint32_t k_low0 = ((base + M::kKv) >> 4) | (1u << 16);
+            const uint32_t v_low0 = ((base + M::kKv + NG * (kTile * 128)) >> 4) | ((1024u >> 4) << 16);
+            auto scores = [&](uint32_t k, uint32_t d) {        // S = Q K^T of the tile at k
 #pragma unroll
                 for (int j = 0; j < NG; ++j)
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        mma_ss(tmem + half * 128 + 64 * j, smem_desc_sw128(base + M::kQ + j * (kRows * 128) + kk * 32),
-                               smem_desc_sw128(k + j * (kTile * 128) + kk * 32), kDescS, kk != 0);
-                mma_commit(s_full + 8 * half);
-                return true;
+                        mma_ss(d + 64 * j, desc(q_low + ((j * (kRows * 128) + kk * 32) >> 4)),
+                               desc(k + ((j * (kTile * 128) + kk * 32) >> 4)), kDescS, kk != 0);
             };
+            // the decoded tiles in turn: kb, kp the next S's buffer and parity; vb the next O's
+            uint32_t kb = 0, kp = 0, vb = 0, pp = 0;           // pp: bit h the parity of half h's next P
             for (uint32_t u = u0; u < u1 && ok;) {
                 const uint32_t count = min(static_cast<uint32_t>(w.tiles - w.idx), u1 - u);
-                ok = wait_phase(q_full, segs & 1u, P.timeout_ns, abort);
-                tc_fence_after_sync();
-                if (ok) ok = products(0, it);
-                if (ok && count > 1) ok = products(1, it + 1);
-                for (uint32_t i = 0; i < count && ok; ++i) {
-                    const uint32_t half = i & 1, buf = (it + i) % kBufs;
-                    ok = wait_phase(p_ready + 8 * half, p_turn[half]++ & 1u, P.timeout_ns, abort);
+                ok = wait(q_full, segs & 1u);
+                for (uint32_t i = 0; i < min(count, 2u) && ok; ++i) {
+                    ok = wait(kv_full + 8 * kb, kp);
                     if (!ok) break;
                     tc_fence_after_sync();
-                    const uint32_t v = base + M::kKv + buf * M::kKvBytes + NG * (kTile * 128);
+                    scores(k_low0 + kb * kStep, tmem + i * 128);
+                    mma_commit(s_full + 8 * i);
+                    if (++kb == kBufs) { kb = 0; kp ^= 1u; }
+                }
+                for (uint32_t i = 0; i < count && ok; ++i) {
+                    const uint32_t half = i & 1, t = tmem + half * 128, v = v_low0 + vb * kStep;
+                    ok = wait(p_ready + 8 * half, (pp >> half) & 1u);
+                    if (!ok) break;
+                    pp ^= 1u << half;
+                    tc_fence_after_sync();
 #pragma unroll
                     for (int j = 0; j < NG; ++j)
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            mma_ts(tmem + 256 + half * 128 + 64 * j, tmem + half * 128 + 32 * j + 8 * kk,
-                                   smem_desc_mn_sw128(v + j * (kTile * 128) + kk * 2048), kDescO, i > 1 || kk != 0);
-                    mma_commit(kv_empty + 8 * buf);
-                    if (i + 2 >= count) mma_commit(o_full + 8 * half);
-                    if (i + 2 < count) ok = products(i + 2, it + i + 2);
+                            mma_ts(t + 256 + 64 * j, t + 32 * j + 8 * kk, desc(v + ((j * (kTile * 128) + kk * 2048) >> 4)), kDescO,
+                                   i > 1 || kk != 0);
+                    if (i + 2 < count) {
+                        ok = wait(kv_full + 8 * kb, kp);
+                        if (!ok) break;
+                        tc_fence_after_sync();
+                        scores(k_low0 + kb * kStep, t);
+                        mma_commit(s_full + 8 * half);
+                        if (++kb == kBufs) { kb = 0; kp ^= 1u; }
+                    } else {
+                        mma_commit(o_full + 8 * half);
+                    }
+                    mma_commit(kv_empty + 8 * vb);
+                    if (++vb == kBufs) vb = 0;
                 }
-                it += count;
                 ++segs;
                 u += count;
                 if (u < u1) w.next(P, per);
             }
             if (!ok && u0 < u1) give_up();
-            mma_commit(drain);                         // every product of this block finished (also after an abort)
+            mma_commit(drain);                             // every product of this block finished (also after an abort)
             wait_phase(drain, 0u, kAttnDrainNs, nullptr);
         }
         __syncwarp();
+        }
     } else if (warp >= 8) {
         // --------------------------------------------------------- decode --
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kOtherRegs));
         const int rec = warp - 8;                      // of the tile
         bool ok = true;
         for (uint32_t n = 0; n < u1 - u0; ++n) {
             const uint32_t s = n % kRawStages, buf = n % kBufs;
-            ok = wait_phase(raw_full + 8 * s, (n / kRawStages) & 1u, P.timeout_ns, abort);
-            if (ok && n >= kBufs) ok = wait_phase(kv_empty + 8 * buf, (n / kBufs - 1) & 1u, P.timeout_ns, abort);
+            ok = wait_phase(raw_full + 8 * s, (n / kRawStages) & 1u, P.timeout_ns, abort, 40);
+            if (ok && n >= kBufs) ok = wait_phase(kv_empty + 8 * buf, (n / kBufs - 1) & 1u, P.timeout_ns, abort, 40);
             if (!__all_sync(0xFFFFFFFFu, ok)) break;
             const uint8_t* from = smem + M::kRaw + s * M::kRawBytes + rec * kv_record_bytes(D);
             uint8_t* kt = smem + M::kKv + buf * M::kKvBytes;
@@ -408,40 +619,48 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                     make_uint4(decode_pair<kPn4t, 0>(word, sh), decode_pair<kPn4t, 1>(word, sh), decode_pair<kPn4t, 2>(word, sh),
                                decode_pair<kPn4t, 3>(word, sh));
             };
+            // every load before the first store, which might be taken to alias
+            const bool real = (have >> rec) & 1;
+            float dk[NG], dv[NG];
+#pragma unroll
+            for (int j = 0; j < NG; ++j) {
+                dk[j] = lds_half_as_float(from + kv_k_scales(D) + ((lane & 15) * NG + j) * 2);
+                dv[j] = lds_half_as_float(from + kv_v_scales(D) + ((lane & 15) * NG + j) * 2);
+            }
+            uint32_t kw[2][2 * NG], vw[2][2 * NG];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
+                const uint8_t* p = from + h * 256 * NG + lane * 8 * NG;
                 if constexpr (NG == 2) {
-                    const uint4 kw = lds_u128(from + h * 512 + lane * 16), vw = lds_u128(from + kv_v_codes(D) + h * 512 + lane * 16);
-                    const int kt0 = rec * 16 + h * 8 + g, vt0 = rec * 16 + h * 8 + 2 * t;
-                    put(kt, kt0, 0, 2 * t, kw.x);
-                    put(kt, kt0, 0, 2 * t + 1, kw.y);
-                    put(kt, kt0, 1, 2 * t, kw.z);
-                    put(kt, kt0, 1, 2 * t + 1, kw.w);
-                    put(vt, vt0, 0, g, vw.x);
-                    put(vt, vt0, 1, g, vw.y);
-                    put(vt, vt0 + 1, 0, g, vw.z);
-                    put(vt, vt0 + 1, 1, g, vw.w);
+                    const uint4 k4 = lds_u128(p), v4 = lds_u128(p + kv_v_codes(D));
+                    kw[h][0] = k4.x; kw[h][1] = k4.y; kw[h][2] = k4.z; kw[h][3] = k4.w;
+                    vw[h][0] = v4.x; vw[h][1] = v4.y; vw[h][2] = v4.z; vw[h][3] = v4.w;
                 } else {
-                    const uint2 kw = lds_u64(from + h * 256 + lane * 8), vw = lds_u64(from + kv_v_codes(D) + h * 256 + lane * 8);
-                    const int kt0 = rec * 16 + h * 8 + g, vt0 = rec * 16 + h * 8 + 2 * t;
-                    put(kt, kt0, 0, 2 * t, kw.x);
-                    put(kt, kt0, 0, 2 * t + 1, kw.y);
-                    put(vt, vt0, 0, g, vw.x);
-                    put(vt, vt0 + 1, 0, g, vw.y);
+                    const uint2 k2 = lds_u64(p), v2 = lds_u64(p + kv_v_codes(D));
+                    kw[h][0] = k2.x; kw[h][1] = k2.y;
+                    vw[h][0] = v2.x; vw[h][1] = v2.y;
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int k0 = rec * 16 + h * 8 + g, v0 = rec * 16 + h * 8 + 2 * t;
+#pragma unroll
+                for (int j = 0; j < NG; ++j) {
+                    put(kt, k0, j, 2 * t, kw[h][2 * j]);
+                    put(kt, k0, j, 2 * t + 1, kw[h][2 * j + 1]);
+                    put(vt, v0, j, g, vw[h][j]);
+                    put(vt, v0 + 1, j, g, vw[h][NG + j]);
                 }
             }
             // scales: (K by scale * log2 e, V) of a token; none where no page holds the record
             float top = 0.0f;
             if (lane < 16) {
-                float* sc = reinterpret_cast<float*>(smem + M::kScales + buf * M::kScaleBytes) + (rec * 16 + lane) * 2 * NG;
-                const bool real = (have >> rec) & 1;
+                float* sc = reinterpret_cast<float*>(smem + M::kScales + buf * M::kScaleBytes) + rec * 16 + lane;
 #pragma unroll
                 for (int j = 0; j < NG; ++j) {
-                    const float dk = real ? lds_half_as_float(from + kv_k_scales(D) + (lane * NG + j) * 2) * P.scale_log2 : 0.0f;
-                    const float dv = real ? lds_half_as_float(from + kv_v_scales(D) + (lane * NG + j) * 2) : 0.0f;
-                    sc[j] = dk;
-                    sc[NG + j] = dv;
-                    top = fmaxf(top, fabsf(dv));
+                    sc[j * kTile] = real ? dk[j] * P.scale_log2 : 0.0f;
+                    sc[(NG + j) * kTile] = real ? dv[j] : 0.0f;
+                    top = real ? fmaxf(top, fabsf(dv[j])) : 0.0f;
                 }
             }
 #pragma unroll
@@ -460,6 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         if (!ok) give_up();
     } else {
         // -------------------------------------------------------- softmax --
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kSoftmaxRegs));
         const int half = warp >> 2, row = threadIdx.x & 127;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + half * 128 + lanes, to = tmem + 256 + half * 128 + lanes;
@@ -490,9 +710,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             tc_fence_before_sync();                    // the last segment's O has been read
             __syncwarp();
             if (lane == 0) mbar_arrive(q_full);
-            const int pos = w.pos_lo + min(row, max(rows - 1, 0)) / P.group;
+            RowState st{-INFINITY, 0.0f, w.pos_lo + min(row, max(rows - 1, 0)) / P.group};
             const int window = a.window ? a.window : INT32_MAX;
-            float ref = -INFINITY, sum = 0.0f;
             for (uint32_t i = half; i < count; i += 2) {
                 const uint32_t n = it + i, buf = n % kBufs;
                 if (ok) {
@@ -510,82 +729,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 const float4 tops = *reinterpret_cast<const float4*>(smem + M::kTop + buf * 16);
                 const uint32_t have = have_of[buf];
                 const bool plain = have == 15u && tok0 + kTile - 1 <= w.pos_lo && (tok0 > w.pos_hi - window || tok0 + kTile <= a.sinks);
-                float x[kTile];
-                {
-                    uint32_t s0[2][16], s1[2][16];
-                    tmem_ld16(ts, s0[0]);
-                    if (NG == 2) tmem_ld16(ts + 64, s1[0]);
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        tmem_wait_ld();
-                        if (c < 3) {
-                            tmem_ld16(ts + 16 * (c + 1), s0[(c + 1) & 1]);
-                            if (NG == 2) tmem_ld16(ts + 64 + 16 * (c + 1), s1[(c + 1) & 1]);
-                        }
-                        scores16<D>(x + 16 * c, s0[c & 1], s1[c & 1], sc + 16 * c * 2 * NG);
-                    }
-                }
-                uint64_t seen = ~0ull;
-                if (!plain) {
-                    seen = 0;
-#pragma unroll
-                    for (int c = 0; c < kTile; ++c) {
-                        const int tok = tok0 + c;
-                        const bool s = ((have >> (c >> 4)) & 1) && tok <= pos && (tok > pos - window || tok < a.sinks);
-                        seen |= static_cast<uint64_t>(s) << c;
-                        if (!s) x[c] = -INFINITY;
-                    }
-                }
-                float top = -INFINITY;
-#pragma unroll
-                for (int c = 0; c < kTile; ++c) top = fmaxf(top, x[c]);
-                top += lg2(fminf(fmaxf(fmaxf(fmaxf(tops.x, tops.y), fmaxf(tops.z, tops.w)), 5.9604645e-8f), 65504.0f));
-                // the reference moves when it is passed by far
-                const bool move = top > ref + kSlack || (ref == -INFINITY && top > -INFINITY);
-                if (__any_sync(0xFFFFFFFFu, move)) {
-                    const float to_ref = move ? top - kMargin : ref;
-                    const float f = ref == -INFINITY ? 0.0f : ex2(ref - to_ref);
-                    ref = to_ref;
-                    sum *= f;
-                    if (i >= 2) {                      // O holds something
-#pragma unroll 1
-                        for (int c = 0; c < D; c += 32) {
-                            uint32_t o[32];
-                            tmem_ld32(to + c, o);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) o[k] = __float_as_uint(__uint_as_float(o[k]) * f);
-                            tmem_st32(to + c, o);
-                        }
-                    }
-                }
-                const float base_ref = ref == -INFINITY ? 0.0f : ref;
-#pragma unroll
-                for (int c = 0; c < kTile; ++c) {
-                    x[c] = ex2(x[c] - base_ref);
-                    sum += x[c];
-                }
-#pragma unroll
-                for (int j = 0; j < NG; ++j) {
-                    uint32_t p[32];
-#pragma unroll
-                    for (int c = 0; c < kTile; c += 2) {
-                        float p0 = x[c] * sc[(c * 2 + 1) * NG + j], p1 = x[c + 1] * sc[(c * 2 + 3) * NG + j];
-                        if (!plain) {                  // a hidden token's scale may be anything, NaN too
-                            p0 = (seen >> c) & 1 ? p0 : 0.0f;
-                            p1 = (seen >> (c + 1)) & 1 ? p1 : 0.0f;
-                        }
-                        p[c / 2] = pack_half2(p0, p1);
-                    }
-                    tmem_st32(ts + 32 * j, p);
-                }
+                const float big = lg2(fminf(fmaxf(fmaxf(fmaxf(tops.x, tops.y), fmaxf(tops.z, tops.w)), 5.9604645e-8f), 65504.0f));
+                if (plain) softmax_tile<D, false>(ts, to, sc, big, i >= 2, tok0, have, window, a.sinks, st);
+                else softmax_tile<D, true>(ts, to, sc, big, i >= 2, tok0, have, window, a.sinks, st);
                 tmem_wait_st();
                 tc_fence_before_sync();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(p_ready + 8 * half);
             }
             // ------------------------------------- join of the two halves --
-            sums[half * kRows + row] = make_float2(ref, sum);
+            sums[half * kRows + row] = make_float2(st.ref, st.sum);
             const uint32_t halves = min(count, 2u);
             for (uint32_t k = 0; k < halves && ok; ++k) ok = wait_phase(o_full + 8 * k, o_turn[k]++ & 1u, P.timeout_ns, abort);
             ok = __all_sync(0xFFFFFFFFu, ok);
