@@ -4,18 +4,20 @@
 //
 // A segment is (request, row tile, key/value head): 128 rows, the query heads
 // that share the head times as many whole tokens as fit.  Its visible cached
-// tokens are taken 64 at a time.  In a thread block of 14 warps
-//   warp 12 copies records into a raw ring (bulk copies, a lane to a stage);
-//   warps 8-11 decode them into fp16 whole numbers n - 8, exact, K and V as
+// tokens are taken 64 at a time.  In a thread block of 16 warps
+//   warp 14 copies records into a raw ring (bulk copies, a lane to a stage);
+//   warps 8-13 decode them into fp16 whole numbers n - 8, exact, K and V as
 //     [token][64 values] tiles with the 128-byte swizzle, and the scales as
 //     fp32; a tile's codes are decoded once for 128 rows;
-//   warp 13 issues the products: S_j = Q_j K_j^T for each group j of 64 values
+//   warp 15 issues the products: S_j = Q_j K_j^T for each group j of 64 values
 //     (fp32 in tensor memory, M = 128, N = 64), O_j += P_j V_j with P_j from
 //     tensor memory and V as its token-major tile;
-//   warps 0-3 and 4-7 take even and odd tiles, a row to a thread: x = sum_j
-//     d_j S_j, the online softmax, P_j = p d_j rounded once to fp16, written
-//     over S.  Each of the two keeps its own reference, sum and O, so one's
-//     softmax runs beside the other's products; they are joined at the end.
+//   warps 0-7 take the tiles, half a tile's tokens of a row to a thread: x =
+//     sum_j d_j S_j, the online softmax, P_j = p d_j rounded once to fp16,
+//     written over the half's own columns of S.  The halves keep references,
+//     sums and O's of their own, so they never wait for each other, and are
+//     joined at the end of a segment.  S has two places, so one tile's scores
+//     are made while the other's probabilities are worked out.
 // The scales of K and V never touch the operands, so scores and values are as
 // exact as in the kernel for few rows; P_j takes the place of one P because V's
 // scale differs by group.
@@ -23,6 +25,11 @@
 // The reference of a row is its maximum of x + log2 of the tile's largest V
 // scale, less 7, and stays until that maximum lies 15 above it: p d < 2^15, and
 // O is hardly ever rescaled.
+//
+// What it is bound by: the 16 products of a tile take 640 cycles (S at N = 64
+// reads 6 KB of shared memory each, 48 cycles; O 32), its softmax about 900
+// instructions on each of the four schedulers, at roughly one every two cycles:
+// about 1900 cycles a tile.
 //
 // Work split: as in pn_attn.cu, units (segment, tile) in order, a contiguous
 // range to each of one thread block per SM; what crosses block boundaries is
@@ -41,15 +48,16 @@ namespace {
 constexpr int kRows = 128;                     // MMA M
 constexpr int kTile = 64;                      // tokens per unit, MMA N of S
 constexpr int kTileRecords = kTile / kKvTokens;
-constexpr int kThreads = 16 * 32;              // warps 14 and 15 fill the last warpgroup
-// Registers per thread after the split of the launch's 128: 256 x 176 + 256 x
-// 80 = 512 x 128.  A row's 64 scores stay in registers.
-constexpr int kSoftmaxRegs = 176, kOtherRegs = 80;
-static_assert(kSoftmaxRegs + kOtherRegs == 2 * 128, "the shares add up to the launch's registers");
+constexpr int kThreads = 16 * 32;              // 128 registers each
+constexpr int kHalf = kTile / 2;               // tokens of a softmax thread
+constexpr int kPlaces = 2;                     // of S in tensor memory, 128 columns each
+constexpr int kDecodeWarps = 6;
+constexpr int kPieces = 8;                     // 8 tokens each, what a decode warp takes at a time
 constexpr int kSoftmaxThreads = 256;
 constexpr int kRawStages = 4;
 constexpr int kBufs = 4;                       // decoded tiles
-constexpr uint32_t kTmemCols = 512;            // S of both halves (P over it), O of both
+constexpr uint32_t kTmemCols = 512;            // two places of S (P over it), O of either half
+constexpr uint32_t kTmemO = kPlaces * 128;
 constexpr float kMargin = 7.0f, kSlack = 15.0f;
 constexpr uint32_t kIssued = 1u << 8, kOddTurn = 1u << 9;   // marks beside a raw stage's records
 
@@ -81,7 +89,6 @@ __device__ __forceinline__ bool elect_one() {
 }
 
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 2, %0;" :: "n"(kSoftmaxThreads) : "memory"); }
-
 // A request, one of its row tiles, and walking over them.
 struct Walk {
     int b, qt, h, idx;         // request, row tile, head, tile of the segment
@@ -138,6 +145,34 @@ struct Walk {
     }
 };
 
+// The segment and tile of unit u; scan: units before each thread's `each` requests.
+__device__ __noinline__ Walk locate_unit(const AttnParams& P, int per, const uint32_t* scan, int each, uint32_t u) {
+    Walk w;
+    int lo = 0, hi = kThreads - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (scan[mid] <= u) lo = mid;
+        else hi = mid - 1;
+    }
+    uint32_t at = scan[lo];
+    w.b = lo * each;
+    w.request(P, per);
+    for (w.qt = 0;; ++w.qt) {
+        while (w.qt >= w.qtiles) {
+            w.qt = 0;
+            ++w.b;
+            w.request(P, per);
+        }
+        w.row_tile(P, per);
+        const uint32_t units = static_cast<uint32_t>(w.tiles) * P.cache.heads;
+        if (u < at + units) break;
+        at += units;
+    }
+    w.h = static_cast<int>((u - at) / static_cast<uint32_t>(w.tiles));
+    w.idx = static_cast<int>(u - at - static_cast<uint32_t>(w.h) * w.tiles);
+    return w;
+}
+
 template <int D>
 struct Smem {
     static constexpr int kGroups = D / 64;
@@ -149,16 +184,17 @@ struct Smem {
     static constexpr int kRaw = kScales + kBufs * kScaleBytes;             // [stage][4 records]
     static constexpr int kRawBytes = kTileRecords * kv_record_bytes(D);
     static constexpr int kSums = kRaw + kRawStages * kRawBytes;            // [2][rows] (reference, sum)
-    static constexpr int kTop = kSums + 2 * kRows * 8;                     // [buffer][4] largest V scale of each record
-    static constexpr int kHave = kTop + kBufs * 16;                        // [buffer] records that a page holds
+    static constexpr int kTop = kSums + 2 * kRows * 8;                     // [buffer][piece] largest V scale (bits)
+    static constexpr int kHave = kTop + kBufs * kPieces * 4;                        // [buffer] records that a page holds
     static constexpr int kValid = kHave + kBufs * 4;                       // [raw stage] the same, marks of its last copy
     static constexpr int kBars = (kValid + kRawStages * 4 + 7) / 8 * 8;
-    static constexpr int kNumBars = 2 * kRawStages + 2 * kBufs + 1 + 6 + 1;
+    static constexpr int kNumBars = 2 * kRawStages + 2 * kBufs + 1 + 3 * kPlaces + 1 + 1;
     static constexpr int kMisc = kBars + kNumBars * 8;                     // TMEM base, abort, last-block flags
     static constexpr int kScan = kMisc + 16;                               // [threads + 1] units before each thread's requests
     static constexpr int kUsed = kScan + (kThreads + 1) * 4;
     static constexpr int kBytes = kUsed + 1024;                            // slack to align to 1024 bytes
     static_assert(kBytes <= 227 * 1024, "fits one SM's shared memory");
+    static_assert(kPieces * 8 == kTile);
     static_assert(kScales % 16 == 0 && kRaw % 16 == 0 && kSums % 16 == 0 && kTop % 16 == 0, "alignment");
 };
 
@@ -205,80 +241,102 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
-// A row's state in one of the two halves.
-struct RowState {
-    float ref, sum;
-    int pos;
-};
-
-// One tile of a row: S from tensor memory at ts, P over it.  sc: the tile's
-// scales, [K by group, V by group][64 tokens]; big: log2 of the largest V
-// scale; filled: O (at to) holds something.
+// Half a tile's scores of a row, from tensor memory at ts.  sc: the tile's
+// scales from the half's first token on, [K by group, V by group][64 tokens].
+// Hidden tokens (bits of seen that are 0) score -inf.  Returns the largest.
 template <int D, bool kMasked>
-__device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, const float* sc, float big, bool filled, int tok0, uint32_t have,
-                                             int window, int sinks, RowState& st) {
+__device__ __forceinline__ float half_scores(Two (&x)[kHalf / 2], uint32_t ts, const float* sc, uint32_t seen) {
     constexpr int NG = D / 64;
-    Two x[kTile / 2];
-    float top2[2] = {-INFINITY, -INFINITY};
-    {
-        uint32_t s[2][NG][16];
-        tmem_ld16(ts, s[0][0]);
-        if constexpr (NG == 2) tmem_ld16(ts + 64, s[0][NG - 1]);
+    float top[2] = {-INFINITY, -INFINITY};
+    uint32_t s[2][NG][16];
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-            tmem_wait_ld();
-            if (c < 3) {
-                tmem_ld16(ts + 16 * (c + 1), s[(c + 1) & 1][0]);
-                if constexpr (NG == 2) tmem_ld16(ts + 64 + 16 * (c + 1), s[(c + 1) & 1][NG - 1]);
-            }
+    for (int c = 0; c < 2; ++c)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {              // four tokens
-                const ulonglong2 d0 = *reinterpret_cast<const ulonglong2*>(sc + 16 * c + 4 * i);
-                Two a = mul2(d0.x, two(s[c & 1][0][4 * i], s[c & 1][0][4 * i + 1]));
-                Two b = mul2(d0.y, two(s[c & 1][0][4 * i + 2], s[c & 1][0][4 * i + 3]));
-                if constexpr (NG == 2) {
-                    const ulonglong2 d1 = *reinterpret_cast<const ulonglong2*>(sc + kTile + 16 * c + 4 * i);
-                    a = fma2(d1.x, two(s[c & 1][NG - 1][4 * i], s[c & 1][NG - 1][4 * i + 1]), a);
-                    b = fma2(d1.y, two(s[c & 1][NG - 1][4 * i + 2], s[c & 1][NG - 1][4 * i + 3]), b);
-                }
-                x[8 * c + 2 * i] = a;
-                x[8 * c + 2 * i + 1] = b;
-                if constexpr (!kMasked) {
-                    const float2 u = apart(a), v = apart(b);
-                    top2[0] = max3(top2[0], u.x, u.y);
-                    top2[1] = max3(top2[1], v.x, v.y);
-                }
+        for (int j = 0; j < NG; ++j) tmem_ld16(ts + 64 * j + 16 * c, s[c][j]);
+    tmem_wait_ld();
+#pragma unroll
+    for (int c = 0; c < 2; ++c)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {                  // four tokens
+            const ulonglong2 d0 = *reinterpret_cast<const ulonglong2*>(sc + 16 * c + 4 * i);
+            Two a = mul2(d0.x, two(s[c][0][4 * i], s[c][0][4 * i + 1]));
+            Two b = mul2(d0.y, two(s[c][0][4 * i + 2], s[c][0][4 * i + 3]));
+            if constexpr (NG == 2) {
+                const ulonglong2 d1 = *reinterpret_cast<const ulonglong2*>(sc + kTile + 16 * c + 4 * i);
+                a = fma2(d1.x, two(s[c][NG - 1][4 * i], s[c][NG - 1][4 * i + 1]), a);
+                b = fma2(d1.y, two(s[c][NG - 1][4 * i + 2], s[c][NG - 1][4 * i + 3]), b);
             }
+            float2 u = apart(a), v = apart(b);
+            if constexpr (kMasked) {
+                const uint32_t m = seen >> (16 * c + 4 * i);
+                u.x = m & 1u ? u.x : -INFINITY;
+                u.y = m & 2u ? u.y : -INFINITY;
+                v.x = m & 4u ? v.x : -INFINITY;
+                v.y = m & 8u ? v.y : -INFINITY;
+                a = two(u.x, u.y);
+                b = two(v.x, v.y);
+            }
+            top[0] = max3(top[0], u.x, u.y);
+            top[1] = max3(top[1], v.x, v.y);
+            x[8 * c + 2 * i] = a;
+            x[8 * c + 2 * i + 1] = b;
         }
-    }
-    uint32_t seen[2] = {~0u, ~0u};
-    if constexpr (kMasked) {
+    return fmaxf(top[0], top[1]);
+}
+
+// The probabilities of the same tokens by group, to tensor memory at tp; their
+// sum (before V's scales) is added to sum.
+template <int D, bool kMasked>
+__device__ __forceinline__ void half_probabilities(const Two (&x)[kHalf / 2], uint32_t tp, const float* sc, uint32_t seen, float ref,
+                                                   float& sum) {
+    constexpr int NG = D / 64;
+    const float less = ref == -INFINITY ? 0.0f : -ref;
+    const Two less2 = two(less, less);
+    Two part[2] = {two(sum, 0.0f), two(0.0f, 0.0f)};
+    uint32_t p[NG][16];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {                      // four tokens
+        Two e[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            seen[k] = 0;
+            const float2 v = apart(add2(x[2 * i + k], less2));
+            e[k] = two(ex2(v.x), ex2(v.y));
+            part[k] = add2(part[k], e[k]);
+        }
 #pragma unroll
-            for (int c = 0; c < 32; ++c) {
-                const int tok = tok0 + 32 * k + c;
-                const bool s = ((have >> (2 * k + c / 16)) & 1u) && tok <= st.pos && (tok > st.pos - window || tok < sinks);
-                seen[k] |= static_cast<uint32_t>(s) << c;
+        for (int j = 0; j < NG; ++j) {
+            const ulonglong2 d = *reinterpret_cast<const ulonglong2*>(sc + (NG + j) * kTile + 4 * i);
+            float2 a = apart(mul2(d.x, e[0])), b = apart(mul2(d.y, e[1]));
+            if constexpr (kMasked) {                   // a hidden token's scale may be anything, NaN too
+                const uint32_t m = seen >> (4 * i);
+                a.x = m & 1u ? a.x : 0.0f;
+                a.y = m & 2u ? a.y : 0.0f;
+                b.x = m & 4u ? b.x : 0.0f;
+                b.y = m & 8u ? b.y : 0.0f;
             }
-        }
-#pragma unroll
-        for (int i = 0; i < kTile / 2; ++i) {
-            float2 v = apart(x[i]);
-            if (!((seen[i / 16] >> (2 * i % 32)) & 1u)) v.x = -INFINITY;
-            if (!((seen[i / 16] >> (2 * i % 32 + 1)) & 1u)) v.y = -INFINITY;
-            x[i] = two(v.x, v.y);
+            p[j][2 * i] = pack_half2(a.x, a.y);
+            p[j][2 * i + 1] = pack_half2(b.x, b.y);
         }
     }
-    if constexpr (kMasked) {
 #pragma unroll
-        for (int i = 0; i < kTile / 2; ++i) {
-            const float2 v = apart(x[i]);
-            top2[i & 1] = max3(top2[i & 1], v.x, v.y);
-        }
-    }
-    const float top = fmaxf(top2[0], top2[1]) + big;
+    for (int j = 0; j < NG; ++j) tmem_st16(tp + 16 * j, p[j]);
+    const float2 both = apart(add2(part[0], part[1]));
+    sum = both.x + both.y;
+}
+
+struct RowState {
+    float ref, sum;
+    bool ok;                   // no wait has run out
+};
+
+// Half a tile of a row: S at ts (P into the half's own columns of it), O of the
+// half at to.  before, parity: the barrier phase by which the last product into
+// O is done (0: O holds nothing yet).
+template <int D, bool kMasked>
+__device__ __forceinline__ RowState half_tile(RowState st, uint32_t ts, uint32_t to, const float* sc, float big, uint32_t seen,
+                                              uint32_t before, uint32_t parity, uint64_t limit_ns, volatile uint32_t* abort) {
+    Two x[kHalf / 2];
+    const float top = half_scores<D, kMasked>(x, ts, sc, seen) + big;
     // the reference moves when it is passed by far
     const bool move = top > st.ref + kSlack || (st.ref == -INFINITY && top > -INFINITY);
     if (__any_sync(0xFFFFFFFFu, move)) {
@@ -286,7 +344,9 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, const flo
         const float f = st.ref == -INFINITY ? 0.0f : ex2(st.ref - ref);
         st.ref = ref;
         st.sum *= f;
-        if (filled) {
+        if (before) {
+            if (st.ok) st.ok = __all_sync(0xFFFFFFFFu, wait_phase(before, parity, limit_ns, abort));
+            tc_fence_after_sync();
 #pragma unroll 1
             for (int c = 0; c < D; c += 16) {
                 uint32_t o[16];
@@ -298,41 +358,23 @@ __device__ __forceinline__ void softmax_tile(uint32_t ts, uint32_t to, const flo
             }
         }
     }
-    const float less = st.ref == -INFINITY ? 0.0f : -st.ref;
-    const Two less2 = two(less, less);
-    Two sum[2] = {two(st.sum, 0.0f), two(0.0f, 0.0f)};
-    // exponentials and, beside them, the probabilities by group
+    half_probabilities<D, kMasked>(x, ts, sc, seen, st.ref, st.sum);
+    return st;
+}
+
+// The same for tiles with hidden tokens, a call of its own: few tiles are, and
+// with its code beside the other's in the loop every tile took a fifth longer.
+template <int D>
+__device__ __noinline__ RowState half_tile_masked(RowState st, uint32_t ts, uint32_t to, const float* sc, float big, int tok, uint32_t have,
+                                                  int pos, int window, int sinks, uint32_t before, uint32_t parity, uint64_t limit_ns,
+                                                  volatile uint32_t* abort) {
+    uint32_t seen = 0;
 #pragma unroll
-    for (int q = 0; q < 2; ++q) {
-        uint32_t p[NG][16];
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {                  // four tokens
-            Two e[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const float2 v = apart(add2(x[16 * q + 2 * i + k], less2));
-                e[k] = two(ex2(v.x), ex2(v.y));
-                sum[k] = add2(sum[k], e[k]);
-            }
-#pragma unroll
-            for (int j = 0; j < NG; ++j) {
-                const ulonglong2 d = *reinterpret_cast<const ulonglong2*>(sc + (NG + j) * kTile + 32 * q + 4 * i);
-                float2 a = apart(mul2(d.x, e[0])), b = apart(mul2(d.y, e[1]));
-                if constexpr (kMasked) {               // a hidden token's scale may be anything, NaN too
-                    a.x = (seen[q] >> (4 * i)) & 1u ? a.x : 0.0f;
-                    a.y = (seen[q] >> (4 * i + 1)) & 1u ? a.y : 0.0f;
-                    b.x = (seen[q] >> (4 * i + 2)) & 1u ? b.x : 0.0f;
-                    b.y = (seen[q] >> (4 * i + 3)) & 1u ? b.y : 0.0f;
-                }
-                p[j][2 * i] = pack_half2(a.x, a.y);
-                p[j][2 * i + 1] = pack_half2(b.x, b.y);
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < NG; ++j) tmem_st16(ts + 32 * j + 16 * q, p[j]);
+    for (int c = 0; c < kHalf; ++c) {
+        const bool s = ((have >> (c / 16)) & 1u) && tok + c <= pos && (tok + c > pos - window || tok + c < sinks);
+        seen |= static_cast<uint32_t>(s) << c;
     }
-    const float2 both = apart(add2(sum[0], sum[1]));
-    st.sum = both.x + both.y;
+    return half_tile<D, true>(st, ts, to, sc, big, seen, before, parity, limit_ns, abort);
 }
 
 template <int D>
@@ -345,7 +387,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     uint32_t bar = base + M::kBars;
     auto take = [&](int n) { const uint32_t b = bar; bar += 8u * n; return b; };
     const uint32_t raw_full = take(kRawStages), raw_empty = take(kRawStages), kv_full = take(kBufs), kv_empty = take(kBufs);
-    const uint32_t q_full = take(1), s_full = take(2), p_ready = take(2), o_full = take(2), drain = take(1);
+    const uint32_t q_full = take(1), s_full = take(kPlaces), p_ready = take(2 * kPlaces), o_full = take(1), drain = take(1);
     volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + M::kMisc);
     volatile uint32_t* abort = misc + 1;
     volatile uint32_t* last_flag = misc + 2;           // [2]
@@ -354,29 +396,30 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     uint32_t* scan = reinterpret_cast<uint32_t*>(smem + M::kScan);
     const AttnArgs& a = P.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int heads = P.cache.heads, per = kRows / P.group;
+    const int per = kRows / P.group;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < kRawStages; ++s) {
             mbar_init(raw_full + 8 * s, 1);
-            mbar_init(raw_empty + 8 * s, 4);
+            mbar_init(raw_empty + 8 * s, kPieces);
             valid[s] = 0u;
         }
         for (int s = 0; s < kBufs; ++s) {
-            mbar_init(kv_full + 8 * s, 4);
+            mbar_init(kv_full + 8 * s, kPieces);
             mbar_init(kv_empty + 8 * s, 1);
         }
         mbar_init(q_full, kSoftmaxThreads / 32);
-        for (int w = 0; w < 2; ++w) {
+        for (int w = 0; w < kPlaces; ++w) {
             mbar_init(s_full + 8 * w, 1);
-            mbar_init(p_ready + 8 * w, 4);
-            mbar_init(o_full + 8 * w, 1);
+            mbar_init(p_ready + 16 * w, 4);                // of either half
+            mbar_init(p_ready + 16 * w + 8, 4);
         }
+        mbar_init(o_full, 1);
         mbar_init(drain, 1);
         *abort = 0u;
         fence_mbar_init();
     }
-    if (warp == 13) {
+    if (warp == 15) {
         tmem_alloc(base + M::kMisc, kTmemCols);
         tmem_relinquish();
     }
@@ -413,40 +456,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     const bool idle = blockIdx.x >= min(blocks, total);
     const uint32_t u0 = idle ? 0 : static_cast<uint32_t>(static_cast<uint64_t>(total) * blockIdx.x / blocks);
     const uint32_t u1 = idle ? 0 : static_cast<uint32_t>(static_cast<uint64_t>(total) * (blockIdx.x + 1) / blocks);
-    // the segment and tile of unit u
-    auto locate = [&](uint32_t u, Walk& w) {
-        int lo = 0, hi = kThreads - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (scan[mid] <= u) lo = mid;
-            else hi = mid - 1;
-        }
-        uint32_t at = scan[lo];
-        w.b = lo * each;
-        w.request(P, per);
-        for (w.qt = 0;; ++w.qt) {
-            while (w.qt >= w.qtiles) {
-                w.qt = 0;
-                ++w.b;
-                w.request(P, per);
-            }
-            w.row_tile(P, per);
-            const uint32_t units = static_cast<uint32_t>(w.tiles) * heads;
-            if (u < at + units) break;
-            at += units;
-        }
-        w.h = static_cast<int>((u - at) / static_cast<uint32_t>(w.tiles));
-        w.idx = static_cast<int>(u - at - static_cast<uint32_t>(w.h) * w.tiles);
-    };
+    auto locate = [&](uint32_t u, Walk& w) { w = locate_unit(P, per, scan, each, u); };
     auto give_up = [&]() {
         *abort = 1u;
         atomicCAS(P.status, 0u, kAttnTimeout);
     };
 
-    // one register count to a warpgroup, set where its roles part
-    if (warp >= 12) {
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kOtherRegs));
-        if (warp == 12) {
+    if (warp == 14) {
         // ------------------------------------------------------- producer --
         const uint32_t count = u1 - u0;
         if (lane < kRawStages && static_cast<uint32_t>(lane) < count) {
@@ -520,7 +536,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             if (valid[lane] & kIssued) wait_phase(raw_full + 8 * lane, valid[lane] & kOddTurn ? 1u : 0u, kAttnDrainNs, nullptr);
         }
         __syncwarp();
-        } else if (warp == 13) {
+    } else if (warp == 15) {
         // ------------------------------------------------------ MMA issue --
         if (elect_one()) {
             bool ok = u0 < u1;
@@ -549,43 +565,43 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                         mma_ss(d + 64 * j, desc(q_low + ((j * (kRows * 128) + kk * 32) >> 4)),
                                desc(k + ((j * (kTile * 128) + kk * 32) >> 4)), kDescS, kk != 0);
             };
-            // the decoded tiles in turn: kb, kp the next S's buffer and parity; vb the next O's
-            uint32_t kb = 0, kp = 0, vb = 0, pp = 0;           // pp: bit h the parity of half h's next P
+            // the decoded tiles in turn: kb, kp the next S's buffer and parity, kt its
+            // place; vb, vt, vp the next O's buffer, place of P and parity
+            uint32_t kb = 0, kp = 0, kt = 0, vb = 0, vt = 0, vp = 0;
+            auto next_scores = [&]() {
+                if (!wait(kv_full + 8 * kb, kp)) return false;
+                tc_fence_after_sync();
+                scores(k_low0 + kb * kStep, tmem + kt * 128);
+                mma_commit(s_full + 8 * kt);
+                if (++kb == kBufs) { kb = 0; kp ^= 1u; }
+                if (++kt == kPlaces) kt = 0;
+                return true;
+            };
             for (uint32_t u = u0; u < u1 && ok;) {
                 const uint32_t count = min(static_cast<uint32_t>(w.tiles - w.idx), u1 - u);
                 ok = wait(q_full, segs & 1u);
-                for (uint32_t i = 0; i < min(count, 2u) && ok; ++i) {
-                    ok = wait(kv_full + 8 * kb, kp);
-                    if (!ok) break;
-                    tc_fence_after_sync();
-                    scores(k_low0 + kb * kStep, tmem + i * 128);
-                    mma_commit(s_full + 8 * i);
-                    if (++kb == kBufs) { kb = 0; kp ^= 1u; }
-                }
+                tc_fence_after_sync();
+                for (uint32_t i = 0; i < min(count, static_cast<uint32_t>(kPlaces)) && ok; ++i) ok = next_scores();
                 for (uint32_t i = 0; i < count && ok; ++i) {
-                    const uint32_t half = i & 1, t = tmem + half * 128, v = v_low0 + vb * kStep;
-                    ok = wait(p_ready + 8 * half, (pp >> half) & 1u);
-                    if (!ok) break;
-                    pp ^= 1u << half;
-                    tc_fence_after_sync();
+                    const uint32_t t = tmem + vt * 128, v = v_low0 + vb * kStep;
 #pragma unroll
-                    for (int j = 0; j < NG; ++j)
-#pragma unroll
-                        for (int kk = 0; kk < 4; ++kk)
-                            mma_ts(t + 256 + 64 * j, t + 32 * j + 8 * kk, desc(v + ((j * (kTile * 128) + kk * 2048) >> 4)), kDescO,
-                                   i > 1 || kk != 0);
-                    if (i + 2 < count) {
-                        ok = wait(kv_full + 8 * kb, kp);
+                    for (int h = 0; h < 2; ++h) {
+                        ok = wait(p_ready + 16 * vt + 8 * h, vp);
                         if (!ok) break;
                         tc_fence_after_sync();
-                        scores(k_low0 + kb * kStep, t);
-                        mma_commit(s_full + 8 * half);
-                        if (++kb == kBufs) { kb = 0; kp ^= 1u; }
-                    } else {
-                        mma_commit(o_full + 8 * half);
+#pragma unroll
+                        for (int j = 0; j < NG; ++j)
+#pragma unroll
+                            for (int kk = 0; kk < 2; ++kk)
+                                mma_ts(tmem + kTmemO + 128 * h + 64 * j, t + kHalf * h + 16 * j + 8 * kk,
+                                       desc(v + ((j * (kTile * 128) + (2 * h + kk) * 2048) >> 4)), kDescO, i > 0 || kk != 0);
                     }
+                    if (!ok) break;
                     mma_commit(kv_empty + 8 * vb);
+                    if (i + 1 == count) mma_commit(o_full);
                     if (++vb == kBufs) vb = 0;
+                    if (++vt == kPlaces) { vt = 0; vp ^= 1u; }
+                    if (i + kPlaces < count) ok = next_scores();
                 }
                 ++segs;
                 u += count;
@@ -596,22 +612,22 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             wait_phase(drain, 0u, kAttnDrainNs, nullptr);
         }
         __syncwarp();
-        }
     } else if (warp >= 8) {
         // --------------------------------------------------------- decode --
-        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kOtherRegs));
-        const int rec = warp - 8;                      // of the tile
+        // the block's pieces of 8 tokens in turn: half h of record rec of unit n
+        const int g = lane >> 2, t = lane & 3;
         bool ok = true;
-        for (uint32_t n = 0; n < u1 - u0; ++n) {
+        for (uint32_t task = warp - 8; task / kPieces < u1 - u0; task += kDecodeWarps) {
+            const uint32_t n = task / kPieces, piece = task % kPieces;
+            const int rec = piece >> 1, h = piece & 1;
             const uint32_t s = n % kRawStages, buf = n % kBufs;
-            ok = wait_phase(raw_full + 8 * s, (n / kRawStages) & 1u, P.timeout_ns, abort, 40);
-            if (ok && n >= kBufs) ok = wait_phase(kv_empty + 8 * buf, (n / kBufs - 1) & 1u, P.timeout_ns, abort, 40);
+            ok = wait_phase(raw_full + 8 * s, (n / kRawStages) & 1u, P.timeout_ns, abort);
+            if (ok && n >= kBufs) ok = wait_phase(kv_empty + 8 * buf, (n / kBufs - 1) & 1u, P.timeout_ns, abort);
             if (!__all_sync(0xFFFFFFFFu, ok)) break;
             const uint8_t* from = smem + M::kRaw + s * M::kRawBytes + rec * kv_record_bytes(D);
             uint8_t* kt = smem + M::kKv + buf * M::kKvBytes;
             uint8_t* vt = kt + NG * (kTile * 128);
             const uint32_t have = valid[s];
-            const int g = lane >> 2, t = lane & 3;
             // 16-byte chunk `i` of a token's row in a group's tile, swizzled
             auto put = [&](uint8_t* tile, int token, int j, int i, uint32_t word) {
                 const uint32_t sh = word >> 8;
@@ -621,53 +637,37 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             };
             // every load before the first store, which might be taken to alias
             const bool real = (have >> rec) & 1;
-            float dk[NG], dv[NG];
-#pragma unroll
-            for (int j = 0; j < NG; ++j) {
-                dk[j] = lds_half_as_float(from + kv_k_scales(D) + ((lane & 15) * NG + j) * 2);
-                dv[j] = lds_half_as_float(from + kv_v_scales(D) + ((lane & 15) * NG + j) * 2);
-            }
-            uint32_t kw[2][2 * NG], vw[2][2 * NG];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
+            const int sj = lane >> 3, st = h * 8 + (lane & 7);             // lane's scale: kind and group sj, token st of the record
+            const float scale = sj < 2 * NG ? lds_half_as_float(from + (sj < NG ? kv_k_scales(D) : kv_v_scales(D)) + (st * NG + sj % NG) * 2) : 0.0f;
+            uint32_t kw[2 * NG], vw[2 * NG];
+            {
                 const uint8_t* p = from + h * 256 * NG + lane * 8 * NG;
                 if constexpr (NG == 2) {
                     const uint4 k4 = lds_u128(p), v4 = lds_u128(p + kv_v_codes(D));
-                    kw[h][0] = k4.x; kw[h][1] = k4.y; kw[h][2] = k4.z; kw[h][3] = k4.w;
-                    vw[h][0] = v4.x; vw[h][1] = v4.y; vw[h][2] = v4.z; vw[h][3] = v4.w;
+                    kw[0] = k4.x; kw[1] = k4.y; kw[2] = k4.z; kw[3] = k4.w;
+                    vw[0] = v4.x; vw[1] = v4.y; vw[2] = v4.z; vw[3] = v4.w;
                 } else {
                     const uint2 k2 = lds_u64(p), v2 = lds_u64(p + kv_v_codes(D));
-                    kw[h][0] = k2.x; kw[h][1] = k2.y;
-                    vw[h][0] = v2.x; vw[h][1] = v2.y;
+                    kw[0] = k2.x; kw[1] = k2.y;
+                    vw[0] = v2.x; vw[1] = v2.y;
                 }
             }
+            const int k0 = rec * 16 + h * 8 + g, v0 = rec * 16 + h * 8 + 2 * t;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int k0 = rec * 16 + h * 8 + g, v0 = rec * 16 + h * 8 + 2 * t;
-#pragma unroll
-                for (int j = 0; j < NG; ++j) {
-                    put(kt, k0, j, 2 * t, kw[h][2 * j]);
-                    put(kt, k0, j, 2 * t + 1, kw[h][2 * j + 1]);
-                    put(vt, v0, j, g, vw[h][j]);
-                    put(vt, v0 + 1, j, g, vw[h][NG + j]);
-                }
+            for (int j = 0; j < NG; ++j) {
+                put(kt, k0, j, 2 * t, kw[2 * j]);
+                put(kt, k0, j, 2 * t + 1, kw[2 * j + 1]);
+                put(vt, v0, j, g, vw[j]);
+                put(vt, v0 + 1, j, g, vw[NG + j]);
             }
-            // scales: (K by scale * log2 e, V) of a token; none where no page holds the record
-            float top = 0.0f;
-            if (lane < 16) {
-                float* sc = reinterpret_cast<float*>(smem + M::kScales + buf * M::kScaleBytes) + rec * 16 + lane;
-#pragma unroll
-                for (int j = 0; j < NG; ++j) {
-                    sc[j * kTile] = real ? dk[j] * P.scale_log2 : 0.0f;
-                    sc[(NG + j) * kTile] = real ? dv[j] : 0.0f;
-                    top = real ? fmaxf(top, fabsf(dv[j])) : 0.0f;
-                }
-            }
-#pragma unroll
-            for (int d = 8; d >= 1; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, d));
+            // scales: K by scale * log2 e, V; none where no page holds the record
+            float* sc = reinterpret_cast<float*>(smem + M::kScales + buf * M::kScaleBytes);
+            if (sj < 2 * NG) sc[sj * kTile + rec * 16 + st] = !real ? 0.0f : sj < NG ? scale * P.scale_log2 : scale;
+            const uint32_t top = real && sj >= NG && sj < 2 * NG ? __float_as_uint(fmaxf(fabsf(scale), 0.0f)) : 0u;   // (NaN: none)
+            const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, top);
             if (lane == 0) {
-                reinterpret_cast<float*>(smem + M::kTop)[buf * 4 + rec] = top;
-                if (rec == 0) have_of[buf] = have & 15u;
+                reinterpret_cast<uint32_t*>(smem + M::kTop)[buf * kPieces + piece] = most;
+                if (piece == 0) have_of[buf] = have & 15u;
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -679,120 +679,135 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         if (!ok) give_up();
     } else {
         // -------------------------------------------------------- softmax --
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kSoftmaxRegs));
         const int half = warp >> 2, row = threadIdx.x & 127;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const uint32_t ts = tmem + half * 128 + lanes, to = tmem + 256 + half * 128 + lanes;
-        float2* sums = reinterpret_cast<float2*>(smem + M::kSums);         // [2][rows]
-        float2* slot_sums = nullptr;
+        const uint32_t to_o = tmem + kTmemO + half * 128 + lanes;
+        float2* sums = reinterpret_cast<float2*>(smem + M::kSums);         // [2][rows] (reference, sum)
         auto block_slot = [&](uint32_t c, bool begins) { return P.block_slots + (2 * static_cast<int64_t>(c) + begins) * kPiece<D>; };
         bool ok = true;
-        uint32_t it = 0, s_turn = 0, o_turn[2] = {0, 0};
+        uint32_t segs = 0, n = 0, buf = 0, place = 0, s_turn = 0;         // n: units done; its buffer, its place of S and how often that went round
         uint32_t shared_seg[2] = {0xFFFFFFFFu, 0xFFFFFFFFu}, shared_tiles[2] = {0, 0};   // pieces of segments of other blocks too
+        // a row tile's queries, swizzled; rows past them are zero
+        auto load_queries = [&](const Walk& w) {
+            const int rows = w.nt * P.group;
+            constexpr int kEach = kRows * (D / 8) / kSoftmaxThreads;
+            uint4 v[kEach];
+#pragma unroll
+            for (int k = 0; k < kEach; ++k) {
+                const int i = threadIdx.x + k * kSoftmaxThreads, r = i / (D / 8), c = i % (D / 8);
+                v[k] = make_uint4(0, 0, 0, 0);
+                if (r < rows) {
+                    const int tq = r / P.group;
+                    v[k] = *reinterpret_cast<const uint4*>(a.q + (static_cast<int64_t>(w.q0) + w.t0 + tq) * a.q_stride +
+                                                           (w.h * P.group + r - tq * P.group) * D + 8 * c);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < kEach; ++k) {
+                const int i = threadIdx.x + k * kSoftmaxThreads, r = i / (D / 8), c = i % (D / 8);
+                *reinterpret_cast<uint4*>(smem + M::kQ + (c >> 3) * (kRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v[k];
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(q_full);
+        };
         Walk w;
-        if (u0 < u1) locate(u0, w);
+        if (u0 < u1) {
+            locate(u0, w);
+            load_queries(w);
+        }
         for (uint32_t u = u0; u < u1;) {
             const int first = w.idx;
             const uint32_t count = min(static_cast<uint32_t>(w.tiles - first), u1 - u);
             const int rows = w.nt * P.group;
-            // the row tile's queries, swizzled; rows past them are zero
-            for (int i = threadIdx.x; i < kRows * (D / 8); i += kSoftmaxThreads) {
-                const int r = i / (D / 8), c = i % (D / 8);
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (r < rows) {
-                    const int tq = r / P.group;
-                    v = *reinterpret_cast<const uint4*>(a.q + (static_cast<int64_t>(w.q0) + w.t0 + tq) * a.q_stride +
-                                                        (w.h * P.group + r - tq * P.group) * D + 8 * c);
-                }
-                *reinterpret_cast<uint4*>(smem + M::kQ + (c >> 3) * (kRows * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)) = v;
-            }
-            fence_proxy_async_smem();
-            tc_fence_before_sync();                    // the last segment's O has been read
-            __syncwarp();
-            if (lane == 0) mbar_arrive(q_full);
-            RowState st{-INFINITY, 0.0f, w.pos_lo + min(row, max(rows - 1, 0)) / P.group};
+            const int lo_tile = w.lo_tile, sink_tiles = w.sink_tiles, pos_lo = w.pos_lo, pos_hi = w.pos_hi;
+            const int pos = pos_lo + min(row, max(rows - 1, 0)) / P.group;
             const int window = a.window ? a.window : INT32_MAX;
-            for (uint32_t i = half; i < count; i += 2) {
-                const uint32_t n = it + i, buf = n % kBufs;
-                if (ok) {
-                    ok = wait_phase(s_full + 8 * half, s_turn & 1u, P.timeout_ns, abort);
-                    if (ok) ok = wait_phase(kv_full + 8 * buf, (n / kBufs) & 1u, P.timeout_ns, abort);
-                    ok = __all_sync(0xFFFFFFFFu, ok);
-                    if (!ok && lane == 0) give_up();
+            RowState st{-INFINITY, 0.0f, ok};
+            for (uint32_t i = 0; i < count; ++i) {
+                if (st.ok) {
+                    st.ok = wait_phase(s_full + 8 * place, s_turn & 1u, P.timeout_ns, abort) &&
+                            wait_phase(kv_full + 8 * buf, (n / kBufs) & 1u, P.timeout_ns, abort);
+                    st.ok = __all_sync(0xFFFFFFFFu, st.ok);
                 }
-                if (!ok) break;
-                ++s_turn;
                 tc_fence_after_sync();
-                w.idx = first + static_cast<int>(i);
-                const int tok0 = w.first_token();
-                const float* sc = reinterpret_cast<const float*>(smem + M::kScales + buf * M::kScaleBytes);
-                const float4 tops = *reinterpret_cast<const float4*>(smem + M::kTop + buf * 16);
+                const int idx = first + static_cast<int>(i), tok0 = (idx < sink_tiles ? idx : lo_tile + idx - sink_tiles) * kTile;
+                const uint32_t ts = tmem + place * 128 + lanes;
+                const float* sc = reinterpret_cast<const float*>(smem + M::kScales + buf * M::kScaleBytes) + half * kHalf;
+                const uint4 t0 = *reinterpret_cast<const uint4*>(smem + M::kTop + buf * kPieces * 4);
+                const uint4 t1 = *reinterpret_cast<const uint4*>(smem + M::kTop + buf * kPieces * 4 + 16);
+                const float most = __uint_as_float(max(max(max(t0.x, t0.y), max(t0.z, t0.w)), max(max(t1.x, t1.y), max(t1.z, t1.w))));
+                const float big = lg2(fminf(fmaxf(most, 5.9604645e-8f), 65504.0f));
                 const uint32_t have = have_of[buf];
-                const bool plain = have == 15u && tok0 + kTile - 1 <= w.pos_lo && (tok0 > w.pos_hi - window || tok0 + kTile <= a.sinks);
-                const float big = lg2(fminf(fmaxf(fmaxf(fmaxf(tops.x, tops.y), fmaxf(tops.z, tops.w)), 5.9604645e-8f), 65504.0f));
-                if (plain) softmax_tile<D, false>(ts, to, sc, big, i >= 2, tok0, have, window, a.sinks, st);
-                else softmax_tile<D, true>(ts, to, sc, big, i >= 2, tok0, have, window, a.sinks, st);
+                const bool plain = have == 15u && tok0 + kTile - 1 <= pos_lo && (tok0 > pos_hi - window || tok0 + kTile <= a.sinks);
+                const uint32_t before = i > 0 ? kv_empty + 8 * ((buf + kBufs - 1) % kBufs) : 0u, parity = ((n - 1) / kBufs) & 1u;
+                if (plain)
+                    st = half_tile<D, false>(st, ts + half * kHalf, to_o, sc, big, ~0u, before, parity, P.timeout_ns, abort);
+                else
+                    st = half_tile_masked<D>(st, ts + half * kHalf, to_o, sc, big, tok0 + half * kHalf, have >> (2 * half), pos, window,
+                                             a.sinks, before, parity, P.timeout_ns, abort);
                 tmem_wait_st();
                 tc_fence_before_sync();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(p_ready + 8 * half);
+                if (lane == 0) mbar_arrive(p_ready + 16 * place + 8 * half);
+                ++n;
+                if (++buf == kBufs) buf = 0;
+                if (++place == kPlaces) { place = 0; ++s_turn; }
             }
-            // ------------------------------------- join of the two halves --
+            ok = st.ok;
+            // every score of the segment is there, so Q may be replaced
+            const Walk done = w;
+            if (u + count < u1) {
+                w.next(P, per);
+                load_queries(w);
+            }
             sums[half * kRows + row] = make_float2(st.ref, st.sum);
-            const uint32_t halves = min(count, 2u);
-            for (uint32_t k = 0; k < halves && ok; ++k) ok = wait_phase(o_full + 8 * k, o_turn[k]++ & 1u, P.timeout_ns, abort);
-            ok = __all_sync(0xFFFFFFFFu, ok);
-            if (!ok && lane == 0) give_up();
+            if (ok) ok = wait_phase(o_full, segs & 1u, P.timeout_ns, abort);
+            if (!ok) give_up();
+            ++segs;
             tc_fence_after_sync();
             softmax_sync();
+            // the halves' common reference and sum
             const float2 e0 = sums[row], e1 = sums[kRows + row];
             const float m = fmaxf(e0.x, e1.x);
             const float f0 = e0.x == -INFINITY ? 0.0f : ex2(e0.x - m), f1 = e1.x == -INFINITY ? 0.0f : ex2(e1.x - m);
             const float l = f0 * e0.y + f1 * e1.y;
-            const bool whole = count == static_cast<uint32_t>(w.tiles);
+            const bool whole = count == static_cast<uint32_t>(done.tiles);
             const int tq = row / P.group;
-            const int64_t at = row < rows ? (static_cast<int64_t>(w.q0) + w.t0 + tq) * a.heads + w.h * P.group + row - tq * P.group : -1;
+            const int64_t at = row < rows ? (static_cast<int64_t>(done.q0) + done.t0 + tq) * a.heads + done.h * P.group + row - tq * P.group : -1;
             float* slot = nullptr;
             if (!whole) {
                 const int kind = first == 0;
                 slot = block_slot(blockIdx.x, kind);
-                slot_sums = reinterpret_cast<float2*>(slot + kRows * D);
                 shared_seg[kind] = u - first;
-                shared_tiles[kind] = w.tiles;
-                if (half == 0) slot_sums[row] = make_float2(m, l);
+                shared_tiles[kind] = done.tiles;
+                if (half == 0) reinterpret_cast<float2*>(slot + kRows * D)[row] = make_float2(m, l);
             }
             const float inv = whole ? (l == 0.0f ? 0.0f : 1.0f / l) : 1.0f;
             const float g0 = f0 * inv, g1 = f1 * inv;
             if (whole && half == 0 && a.lse && at >= 0) a.lse[at] = log_sum(m, l);
-            if (ok) {
-#pragma unroll 1
-                for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
-                    uint32_t o0[16], o1[16];
-                    tmem_ld16(tmem + 256 + lanes + c, o0);
-                    if (halves > 1) tmem_ld16(tmem + 384 + lanes + c, o1);
-                    tmem_wait_ld();
-                    float o[16];
+#pragma unroll 2
+            for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
+                uint32_t o0[16], o1[16];
+                tmem_ld16(tmem + kTmemO + lanes + c, o0);
+                tmem_ld16(tmem + kTmemO + 128 + lanes + c, o1);
+                tmem_wait_ld();
+                float o[16];
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        // a half that saw nothing of a row left nothing of it but may have no number there
-                        o[k] = g0 == 0.0f ? 0.0f : g0 * __uint_as_float(o0[k]);
-                        if (halves > 1 && g1 != 0.0f) o[k] = fmaf(g1, __uint_as_float(o1[k]), o[k]);
-                    }
-                    if (!whole) {
+                for (int k = 0; k < 16; ++k) o[k] = fmaf(g1, __uint_as_float(o1[k]), g0 * __uint_as_float(o0[k]));
+                if (!whole) {
 #pragma unroll
-                        for (int k = 0; k < 16; k += 4)
-                            reinterpret_cast<float4*>(slot)[((c + k) / 4) * kRows + row] = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
-                    } else if (at >= 0) {
-                        uint4* out = reinterpret_cast<uint4*>(a.out + at * D + c);
-                        out[0] = make_uint4(pack_half2(o[0], o[1]), pack_half2(o[2], o[3]), pack_half2(o[4], o[5]), pack_half2(o[6], o[7]));
-                        out[1] = make_uint4(pack_half2(o[8], o[9]), pack_half2(o[10], o[11]), pack_half2(o[12], o[13]), pack_half2(o[14], o[15]));
-                    }
+                    for (int k = 0; k < 16; k += 4)
+                        reinterpret_cast<float4*>(slot)[((c + k) / 4) * kRows + row] = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                } else if (at >= 0) {
+                    uint4* out = reinterpret_cast<uint4*>(a.out + at * D + c);
+                    out[0] = make_uint4(pack_half2(o[0], o[1]), pack_half2(o[2], o[3]), pack_half2(o[4], o[5]), pack_half2(o[6], o[7]));
+                    out[1] = make_uint4(pack_half2(o[8], o[9]), pack_half2(o[10], o[11]), pack_half2(o[12], o[13]), pack_half2(o[14], o[15]));
                 }
             }
-            softmax_sync();                            // sums and Q are written again
-            it += count;
+            tc_fence_before_sync();                    // O has been read before the next segment's first P is told
+            softmax_sync();                            // sums are written again
             u += count;
-            if (u < u1) w.next(P, per);
         }
 
         // --------------------------------------- segments of several blocks --
@@ -857,7 +872,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     // ------------------------------------------------------------ teardown --
     tc_fence_before_sync();
     __syncthreads();
-    if (warp == 13) {
+    if (warp == 15) {
         tc_fence_after_sync();
         tmem_dealloc(tmem, kTmemCols);
     }
@@ -877,9 +892,13 @@ cudaError_t launch(AttnParams P, uint8_t* ws, int num_sms, cudaStream_t s) {
 
 }  // namespace
 
+// From 49 query rows to a key/value head on.  24 requests of 4096 cached tokens,
+// 8 heads of 128: 32 rows 122 us here, 89 us in the kernel for few rows (16 at a
+// time); 48 rows 122 and 121 us; 64 rows 124 and 152 us.  (One request of 8192,
+// 64 rows: 48 and 36 us; two, 100 rows: 66 and 60 us.)
 bool attn_tc_takes(const AttnArgs& a, const KvGeometry& g) {
     const int group = a.heads / g.heads;
-    return g.D <= 128 && group <= kRows && static_cast<int64_t>(a.max_queries) * group > 16;
+    return g.D <= 128 && group <= kRows && static_cast<int64_t>(a.max_queries) * group > 48;
 }
 
 size_t attn_tc_workspace_bytes(int num_sms) {
