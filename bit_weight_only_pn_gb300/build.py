@@ -2,8 +2,10 @@
 
 Each translation unit in ``csrc/`` is compiled for sm_103a in parallel, then
 linked into one shared library with the CUDA runtime linked statically, so the
-library loads without any other CUDA shared object.  Objects go to
-``bit_weight_only_pn_gb300/_build/``.  Rebuilds only what is out of date.
+library loads without any other CUDA shared object.  The Python entry of the
+serving-step calls (``_step.so``, plain C++ against PyTorch's headers) is built
+beside it.  Objects go to ``bit_weight_only_pn_gb300/_build/``.  Rebuilds only
+what is out of date.
 """
 from __future__ import annotations
 
@@ -12,12 +14,14 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 BUILD = os.path.join(HERE, "_build")
 LIBRARY = os.path.join(HERE, "libpn_gb300.so")
+BINDING = os.path.join(HERE, "_step.so")
 SOURCES = ["pn_attn.cu", "pn_attn_tc.cu", "pn_capi.cu", "pn_codec.cu", "pn_gemv_ffma.cu", "pn_gemv_simt.cu", "pn_gemv_stream.cu", "pn_gemv_tc.cu",
            "pn_gptq.cu", "pn_kv.cu", "pn_noalloc.cu", "pn_prefill.cu", "pn_probe.cu", "pn_rotate.cu", "pn_verify.cu"]
 HEADERS = ["pn_attn.cuh", "pn_device.cuh", "pn_internal.h", "pn_kv.cuh", "pn_tcgen05.cuh"]
@@ -52,10 +56,49 @@ def _compile(src: str, extra=()) -> str:
     return obj
 
 
+def _run(cmd, what: str) -> None:
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{res.stdout}\n{res.stderr}")
+
+
+def _torch():
+    """PyTorch's include folders, library folder, version and C++ ABI flag."""
+    import torch
+    root = os.path.dirname(torch.__file__)
+    include = os.path.join(root, "include")
+    return ([include, os.path.join(include, "torch", "csrc", "api", "include")], os.path.join(root, "lib"),
+            torch.__version__, int(torch._C._GLIBCXX_USE_CXX11_ABI))
+
+
+def _compile_binding() -> str:
+    src = os.path.join(CSRC, "pn_step_binding.cpp")
+    include, _, version, abi = _torch()
+    # one object per PyTorch: its headers are part of it
+    obj = os.path.join(BUILD, f"pn_step_binding-{version}.o")
+    if _newer(obj, [src, os.path.join(ROOT, "include", "pn.h")]):
+        cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
+        _run(["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={abi}",
+              *(f"-I{d}" for d in [*include, cuda, sysconfig.get_paths()["include"]]), "-c", src, "-o", obj],
+             "g++ for pn_step_binding.cpp")
+    return obj
+
+
+def _link_binding(obj: str) -> None:
+    if _newer(BINDING, [obj, LIBRARY]):
+        tmp = BINDING + ".tmp"
+        _run(["g++", "-shared", "-o", tmp, obj, f"-L{HERE}", "-l:" + os.path.basename(LIBRARY), f"-L{_torch()[1]}",
+              "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"],
+             "link of the Python entry")
+        os.replace(tmp, BINDING)
+
+
 def build(verbose: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as pool:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as pool:
+        binding = pool.submit(_compile_binding)
         objs = list(pool.map(_compile, SOURCES))
+        binding = binding.result()
     if _newer(LIBRARY, objs):
         tmp = LIBRARY + ".tmp"
         cmd = [nvcc(), *ARCH, "-shared", "-o", tmp, *objs]
@@ -63,6 +106,7 @@ def build(verbose: bool = False) -> str:
         if res.returncode != 0:
             raise RuntimeError(f"link failed:\n{res.stdout}\n{res.stderr}")
         os.replace(tmp, LIBRARY)
+    _link_binding(binding)
     if verbose:
         print(LIBRARY)
     return LIBRARY

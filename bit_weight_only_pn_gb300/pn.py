@@ -412,37 +412,34 @@ def prefill(pn_type: int, W: torch.Tensor, K: int, x: torch.Tensor, y: torch.Ten
 
 # ------------------------------------------------- 4-bit cache, serving step --
 
-def _empty(shape, dtype, device, stream) -> torch.Tensor:
-    """An output, taken from the memory of the stream that will write it."""
+_step_module = None
+
+
+def _step():
+    """The compiled entry of these calls (csrc/pn_step_binding.cpp): checks,
+    outputs and the C call in one go."""
+    global _step_module
+    if _step_module is None:
+        lib()                                        # a missing library is reported by its own name
+        try:
+            from bit_weight_only_pn_gb300 import _step as module
+        except ImportError as e:
+            raise RuntimeError("the Python entry of the serving-step calls is not built; run "
+                               "`python -m bit_weight_only_pn_gb300.build`") from e
+        _step_module = module
+    return _step_module
+
+
+def _call(stream, function, what: str, *args):
+    """function(*args) on `stream` (None: the current one), whose memory the outputs are taken from."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=device)
-
-
-def _rows(t: torch.Tensor, name: str, dtypes, heads: int | None, dim: int) -> None:
-    """[tokens][heads][dim] whose heads are contiguous within a token."""
-    if not isinstance(t, torch.Tensor) or not t.is_cuda:
-        raise TypeError(f"{name} must be a CUDA tensor")
-    if t.dtype not in dtypes:
-        raise TypeError(f"{name} must be {' or '.join(map(str, dtypes))}, got {t.dtype}")
-    if t.dim() != 3 or t.shape[2] != dim or (heads is not None and t.shape[1] != heads):
-        raise ValueError(f"{name} must be [tokens][heads][{dim}], got {tuple(t.shape)}")
-    if t.numel() and (t.stride(2) != 1 or (t.stride(1) != dim and t.shape[1] > 1)):
-        raise ValueError(f"{name}'s heads must be contiguous within a token")
-
-
-def _row_stride(t: torch.Tensor) -> int:
-    """Elements between tokens (a lone token's stride may say anything)."""
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1] * t.shape[2]
-
-
-def _cache_shape(cache: torch.Tensor):
-    """(pages, page_size, kv_heads, head_dim) of a cache tensor (see kv_cache)."""
-    _require(cache, torch.uint8, "cache")
-    if cache.dim() != 4 or cache.shape[3] % 17:
-        raise ValueError("cache must be uint8 [pages][kv_heads][page_size / 16][17 * head_dim]")
-    return cache.shape[0], cache.shape[2] * 16, cache.shape[1], cache.shape[3] // 17
+        r = function(*args)
+    else:
+        with torch.cuda.stream(stream):
+            r = function(*args)
+    if r[0]:
+        _check(r[0], what)
+    return r
 
 
 def kv_cache(pages: int, page_size: int, kv_heads: int, head_dim: int, device=None) -> torch.Tensor:
@@ -473,37 +470,8 @@ def kv_plan(lens: torch.Tensor, add: torch.Tensor, held: torch.Tensor, table: to
     [batch][pages per request] (new entries are written), free int32 [pages],
     ring int64 [2].  `out` is an earlier result to write into (its lens, held
     and ring must not be this call's inputs)."""
-    for t, name in ((lens, "lens"), (add, "add"), (held, "held"), (free, "free")):
-        _require(t, torch.int32, name)
-    _require(ring, torch.int64, "ring")
-    B = lens.numel()
-    if not isinstance(table, torch.Tensor) or not table.is_cuda or table.dtype != torch.int32:
-        raise TypeError("table must be a CUDA int32 tensor")
-    if table.dim() != 2 or table.shape[0] != B or (table.shape[1] > 1 and table.stride(1) != 1):
-        raise ValueError("table must be [batch][pages per request] with contiguous rows")
-    if add.numel() != B or held.numel() != B or ring.numel() != 2:
-        raise ValueError("lens, add and held must have one entry per request and ring two")
-    T = int(capacity)
-    if out is None:
-        if T < 0:
-            raise ValueError("capacity must not be negative")
-        wide = _empty(T + 2, torch.int64, lens.device, stream).split([T, 2])
-        narrow = _empty(2 * T + 3 * B + 2, torch.int32, lens.device, stream).split([T, T, B + 1, B, B, 1])
-        out = KvPlan(wide[0], narrow[0], narrow[1], narrow[2], narrow[3], narrow[4], wide[1], narrow[5])
-    else:
-        for name, n in (("slots", T), ("positions", T), ("requests", T), ("starts", B + 1), ("lens", B), ("held", B),
-                        ("ring", 2), ("refused", 1)):
-            t = getattr(out, name)
-            _require(t, torch.int64 if name in ("slots", "ring") else torch.int32, f"out.{name}")
-            if t.numel() != n:
-                raise ValueError(f"out.{name} must have {n} entries")
-    stride = table.stride(0) if B > 1 else table.shape[1]
-    _check(lib().pn_kv_plan(lens.data_ptr(), add.data_ptr(), held.data_ptr(), B, table.data_ptr(), stride,
-                            table.shape[1], free.data_ptr(), free.numel(), ring.data_ptr(), page_size, T,
-                            out.slots.data_ptr(), out.positions.data_ptr(), out.requests.data_ptr(),
-                            out.starts.data_ptr(), out.lens.data_ptr(), out.held.data_ptr(), out.ring.data_ptr(),
-                            out.refused.data_ptr(), _stream(stream)), "pn_kv_plan")
-    return out
+    return KvPlan(*_call(stream, _step().kv_plan, "pn_kv_plan", lens, add, held, table, free, ring, page_size, capacity,
+                         out)[1:])
 
 
 def kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, cache: torch.Tensor, slots: torch.Tensor,
@@ -516,65 +484,14 @@ def kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, cache: t
     slots int64 [tokens]; positions int32 [tokens] choose the rows of cos and
     sin, fp32 [positions][rotated pairs] (None: no rotation).  Returns the
     queries as fp16 [tokens][heads][D]."""
-    pages, page_size, kv_heads, D = _cache_shape(cache)
-    kinds = (torch.float32, torch.float16)
-    _rows(k, "k", kinds, kv_heads, D)
-    _rows(v, "v", (k.dtype,), kv_heads, D)
-    T = k.shape[0]
-    heads = 0
-    if q is not None:
-        _rows(q, "q", (k.dtype,), None, D)
-        heads = q.shape[1]
-    if v.shape[0] != T or (q is not None and q.shape[0] != T):
-        raise ValueError("q, k and v must have the same tokens")
-    _require(slots, torch.int64, "slots")
-    if slots.numel() != T:
-        raise ValueError("slots must have one entry per token")
-    pairs = rows = 0
-    if cos is not None or sin is not None:
-        for t, name in ((cos, "cos"), (sin, "sin")):
-            _require(t, torch.float32, name)
-        if cos.dim() != 2 or cos.shape != sin.shape:
-            raise ValueError("cos and sin must be [positions][rotated pairs]")
-        _require(positions, torch.int32, "positions")
-        if positions.numel() != T:
-            raise ValueError("positions must have one entry per token")
-        rows, pairs = cos.shape
-    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        if t is not None:
-            _require(t, torch.float32, name)
-            if t.numel() != D:
-                raise ValueError(f"{name} must have {D} entries")
-    if q is not None:
-        if q_out is None:
-            q_out = _empty((T, heads, D), torch.float16, q.device, stream)
-        else:
-            _require(q_out, torch.float16, "q_out")
-            if q_out.numel() != T * heads * D:
-                raise ValueError("q_out must be [tokens][heads][D]")
-    _check(lib().pn_kv_append(_ptr(q), 0 if q is None else _row_stride(q), k.data_ptr(), _row_stride(k), v.data_ptr(),
-                              _row_stride(v), 0 if k.dtype == torch.float32 else 1, T, heads, _ptr(q_weight),
-                              _ptr(k_weight), eps, _ptr(cos), _ptr(sin), rows, 2 * pairs, interleaved,
-                              None if pairs == 0 else positions.data_ptr(), slots.data_ptr(), cache.data_ptr(), pages,
-                              page_size, kv_heads, D, None if q is None else q_out.data_ptr(), _stream(stream)),
-           "pn_kv_append")
-    return q_out if q is not None else None
+    return _call(stream, _step().kv_append, "pn_kv_append", q, k, v, cache, slots, positions, cos, sin, q_weight,
+                 k_weight, eps, interleaved, q_out)[1]
 
 
 def kv_read(cache: torch.Tensor, slots: torch.Tensor, out=None, stream=None):
     """The cached keys and values of `slots` (int64), exactly: two fp32
     [tokens][kv_heads][D] tensors (`out`, if given)."""
-    pages, page_size, kv_heads, D = _cache_shape(cache)
-    _require(slots, torch.int64, "slots")
-    T = slots.numel()
-    k, v = out if out is not None else (_empty((T, kv_heads, D), torch.float32, cache.device, stream) for _ in range(2))
-    for t in (k, v):
-        _require(t, torch.float32, "out")
-        if t.numel() != T * kv_heads * D:
-            raise ValueError("out must be two tensors [tokens][kv_heads][D]")
-    _check(lib().pn_kv_read(cache.data_ptr(), pages, page_size, kv_heads, D, slots.data_ptr(), T, k.data_ptr(),
-                            v.data_ptr(), _stream(stream)), "pn_kv_read")
-    return k, v
+    return _call(stream, _step().kv_read, "pn_kv_read", cache, slots, *(out if out is not None else (None, None)))[1:]
 
 
 class AttentionWorkspace:
@@ -608,37 +525,11 @@ def attention(q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, lens: t
     queries.  window > 0: a query sees the last `window` tokens up to its own
     and the first `sinks`.  Returns out fp16 [tokens][heads][D], with
     return_lse (or a given lse) also fp32 [tokens][heads]."""
-    pages, page_size, kv_heads, D = _cache_shape(cache)
-    _rows(q, "q", (torch.float16,), None, D)
-    T, heads = q.shape[0], q.shape[1]
-    _require(lens, torch.int32, "lens")
-    _require(starts, torch.int32, "starts")
-    B = lens.numel()
-    if not isinstance(table, torch.Tensor) or not table.is_cuda or table.dtype != torch.int32:
-        raise TypeError("table must be a CUDA int32 tensor")
-    if table.dim() != 2 or table.shape[0] != B or (table.shape[1] > 1 and table.stride(1) != 1):
-        raise ValueError("table must be [batch][pages per request] with contiguous rows")
-    if starts.numel() != B + 1:
-        raise ValueError("starts must have one entry more than lens")
-    if out is None:
-        out = _empty((T, heads, D), torch.float16, q.device, stream)
-    else:
-        _require(out, torch.float16, "out")
-        if out.numel() != T * heads * D:
-            raise ValueError("out must be [tokens][heads][D]")
-    if lse is not None:
-        _require(lse, torch.float32, "lse")
-        if lse.numel() != T * heads:
-            raise ValueError("lse must be [tokens][heads]")
-    elif return_lse:
-        lse = _empty((T, heads), torch.float32, q.device, stream)
     if workspace is None:
-        with torch.cuda.stream(stream):          # zeroed, used and freed in the order of the stream that runs the call
+        with torch.cuda.stream(stream):              # zeroed, used and freed in the order of the stream that runs the call
             workspace = AttentionWorkspace(q.device)
-    _check(lib().pn_attention(q.data_ptr(), _row_stride(q), T, heads, cache.data_ptr(), pages, page_size, kv_heads, D,
-                              table.data_ptr(), table.stride(0) if B > 1 else table.shape[1], table.shape[1],
-                              lens.data_ptr(), starts.data_ptr(), B, max_queries, scale, window, sinks, out.data_ptr(),
-                              _ptr(lse), workspace.ptr, workspace.nbytes, _stream(stream)), "pn_attention")
+    _, out, lse = _call(stream, _step().attention, "pn_attention", q, cache, table, lens, starts, max_queries, scale,
+                        window, sinks, out, lse, return_lse, workspace.ptr, workspace.nbytes)
     return out if lse is None else (out, lse)
 
 
@@ -650,34 +541,7 @@ def verify(tokens: torch.Tensor, target: torch.Tensor, draft: torch.Tensor | Non
     and the draft model's [batch][drafts][vocab] (None: certain drafts), with
     uniforms fp32 [batch][drafts + 1] in [0, 1).  Returns (accepted int32
     [batch], tokens int32 [batch][drafts + 1]: the accepted ones, one more, -1)."""
-    _require(tokens, torch.int32, "tokens")
-    _require(target, torch.float32, "target")
-    _require(uniforms, torch.float32, "uniforms")
-    if tokens.dim() != 2 or target.dim() != 3:
-        raise ValueError("tokens must be [batch][drafts] and target [batch][drafts + 1][vocab]")
-    B, K = tokens.shape
-    V = target.shape[2]
-    if target.shape[0] != B or target.shape[1] != K + 1 or uniforms.numel() != B * (K + 1):
-        raise ValueError("target and uniforms must have one row more than there are drafts")
-    if draft is not None:
-        _require(draft, torch.float32, "draft")
-        if draft.shape != (B, K, V):
-            raise ValueError("draft must be [batch][drafts][vocab]")
-    if counts is not None:
-        _require(counts, torch.int32, "counts")
-        if counts.numel() != B:
-            raise ValueError("counts must have one entry per request")
-    if accepted is None:
-        accepted = _empty((B,), torch.int32, target.device, stream)
-    if out is None:
-        out = _empty((B, K + 1), torch.int32, target.device, stream)
-    _require(accepted, torch.int32, "accepted")
-    _require(out, torch.int32, "out")
-    if accepted.numel() != B or out.numel() != B * (K + 1):
-        raise ValueError("accepted must be [batch] and out [batch][drafts + 1]")
-    _check(lib().pn_verify(tokens.data_ptr(), target.data_ptr(), V, _ptr(draft), V, uniforms.data_ptr(), _ptr(counts),
-                           B, K, V, accepted.data_ptr(), out.data_ptr(), _stream(stream)), "pn_verify")
-    return accepted, out
+    return _call(stream, _step().verify, "pn_verify", tokens, target, draft, uniforms, counts, accepted, out)[1:]
 
 
 def read_ranges(tensors, sink: torch.Tensor, stream=None) -> torch.Tensor:
