@@ -33,12 +33,18 @@
 // a call are numbered in that order and every consumer warp of the grid takes
 // one contiguous range of them, so the cache bytes are shared evenly whatever
 // the lengths are, and a warp keeps its accumulators for as long as a segment
-// (request, head, row group) lasts.  A producer warp fills each warp's own
-// ring of stages by bulk copies.  Segments that one warp has to itself go
-// straight to the output; the pieces of the others go through the workspace
-// (L2): a block joins its own warps' pieces when it is done, and the last
-// block to arrive joins those of several blocks, in unit order, so results do
+// (request, head, row group) lasts.  A segment counts one unit more than it has
+// tiles: to start one costs a warp about what a tile does.  A producer warp
+// fills each warp's own ring of stages by bulk copies.  Segments that one warp
+// has to itself go straight to the output; the pieces of the others are joined
+// in shared memory when the block is done, and those of several blocks through
+// the workspace (L2) by the last block to arrive, in unit order, so results do
 // not depend on timing.
+//
+// One block of 15 consumer warps to an SM.  The schedulers serve older warps
+// first: of two blocks of 7 the first was done 10 us of 50 before the second,
+// and half the SM idled since.  So a warp that is kLead tiles ahead of the
+// block's last one waits for it.
 #include <cstdint>
 
 #include <cuda_fp16.h>
@@ -51,9 +57,8 @@ namespace {
 
 constexpr int kTile = 32;                      // tokens per unit
 constexpr int kTileRecords = kTile / kKvTokens;
-constexpr int kWarps = 7;                      // consumer warps; with the producer 8, so two blocks leave each thread 128 registers
-constexpr int kThreads = (kWarps + 1) * 32;
-constexpr int kCtasPerSm = 2;                  // where 128 registers suffice (8 rows, D <= 128), else 1
+constexpr uint32_t kSegmentUnits = 1;          // of a segment beside its tiles
+constexpr int kLead = 6;                       // tiles that a warp may be ahead of its block's last one
 constexpr uint32_t kIssued = 1u << 8;          // marks beside a stage's records: its copy was started,
 constexpr uint32_t kOddTurn = 1u << 9;         // in an odd turn of the ring
 // 8x8 transpose of 16-bit elements across the warp (row lane / 4, columns 2 (lane % 4), + 1).
@@ -62,7 +67,8 @@ __device__ __forceinline__ uint32_t transpose_8x8(uint32_t v) {
     asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
     return r;
 }
-__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" :: "n"(kWarps * 32) : "memory"); }
+template <int W>
+__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" :: "n"(W * 32) : "memory"); }
 
 // What a request asks of the cache.
 struct Request {
@@ -75,7 +81,7 @@ struct Request {
     int sink_tiles;            // tiles before it that hold visible first tokens
     int tiles;                 // units per (head, row group), at least 1
     int row_groups;
-    __device__ __forceinline__ uint32_t units(int heads) const { return static_cast<uint32_t>(tiles) * row_groups * heads; }
+    __device__ __forceinline__ uint32_t units(int heads) const { return (static_cast<uint32_t>(tiles) + kSegmentUnits) * row_groups * heads; }
     __device__ __forceinline__ int tile(int idx) const { return idx < sink_tiles ? idx : lo_tile + idx - sink_tiles; }
 };
 
@@ -98,12 +104,23 @@ __device__ __forceinline__ Request request_of(const AttnParams& P, int b) {
     return r;
 }
 
-// Unit v of a request: (head, row group, place among its tiles).
+// Unit v of a request: (head, row group, place among its tiles; negative: one
+// of the units before them).
 __device__ __forceinline__ void locate(uint32_t v, const Request& r, int& h, int& rg, int& idx) {
-    const uint32_t seg = v / static_cast<uint32_t>(r.tiles);
-    idx = static_cast<int>(v - seg * r.tiles);
+    const uint32_t each = static_cast<uint32_t>(r.tiles) + kSegmentUnits, seg = v / each;
+    idx = static_cast<int>(v - seg * each) - static_cast<int>(kSegmentUnits);
     h = static_cast<int>(seg / static_cast<uint32_t>(r.row_groups));
     rg = static_cast<int>(seg - h * r.row_groups);
+}
+
+// The segment after (r, b, h, rg), which there is.
+template <int RT>
+__device__ __forceinline__ void next_segment(const AttnParams& P, Request& r, int& b, int& h, int& rg) {
+    if (++rg < r.row_groups) return;
+    rg = 0;
+    if (++h < P.cache.heads) return;
+    h = 0;
+    do r = request_of<RT>(P, ++b); while (r.rows == 0);
 }
 
 template <int D>
@@ -123,23 +140,37 @@ constexpr int kPiece = 8 * NT * (D + 2);
 template <int D, int NT>
 struct Smem {
     static constexpr int kRT = 8 * NT;
+    // consumer warps; with the producer 16 at 128 registers where these suffice (8 rows, D <= 128), else 8
+    static constexpr int kWarps = NT == 1 && D <= 128 ? 15 : 7;
+    static constexpr int kThreads = (kWarps + 1) * 32;
     static constexpr int kDepth = D == 256 ? 2 : D == 128 && NT == 1 ? 3 : 4;      // stages per warp
-    static constexpr int kStages = kWarps * kDepth;
     static constexpr int kWarpRing = kDepth * Shape<D>::kStage;
     static constexpr int kRing = kWarps * kWarpRing;
+    static constexpr int kPieces = 2 * kWarps;                             // pieces of segments: two to a warp
     static constexpr int kRunsMost = kWarps + 1;                           // a warp's last piece goes on in the next one's first
-    static constexpr int kFactors = kRing;                                 // [2 warps' pieces][rows] floats
-    static constexpr int kRowOut = kFactors + 2 * kWarps * kRT * 4;        // [runs][rows] where a run's row goes
-    static constexpr int kRuns = kRowOut + kRunsMost * kRT * 8;            // see the block's join
-    static constexpr int kBars = kRuns + 4 * (2 * kWarps + 2) * 4;         // full, empty
-    static constexpr int kValid = kBars + 2 * kStages * 8;                 // per stage: records that hold data, marks of its last copy
-    static constexpr int kMisc = kValid + kStages * 4;                     // abort, last-block flags
+    static constexpr int kFactors = kRing;                                 // [pieces][rows] floats
+    static constexpr int kRowOut = kFactors + kPieces * kRT * 4;           // [runs][rows] where a run's row goes
+    static constexpr int kPieceOf = kRowOut + kRunsMost * kRT * 8;         // [pieces] PieceInfo
+    static constexpr int kRuns = kPieceOf + kPieces * 24;                  // order [pieces], run starts [runs + 1], number of runs
+    static constexpr int kBars = kRuns + (kPieces + kRunsMost + 2 + 1) / 2 * 8;    // full, empty
+    static constexpr int kValid = kBars + 2 * kWarps * kDepth * 8;         // per stage: records that hold data, marks of its last copy
+    static constexpr int kProgress = kValid + kWarps * kDepth * 4;         // [warps] tiles done
+    static constexpr int kMisc = kProgress + kWarps * 4;                   // abort, last-block flags
     static constexpr int kScan = kMisc + 12;                               // the warps' sums, then [batch + 1] prefix sums of units
     static constexpr int kFixed = kScan + (kWarps + 1) * 4;
     static int bytes(int batch) { return kFixed + (batch + 1) * 4; }
-    static_assert(kBars % 8 == 0 && kRowOut % 8 == 0, "barriers and row indexes are 8-byte aligned");
-    static_assert(2 * kPiece<D, NT> * 4 <= kWarpRing && kWarpRing % 16 == 0, "a warp's pieces fit its stages");
+    static_assert(kBars % 8 == 0 && kRowOut % 8 == 0 && kPieceOf % 4 == 0, "alignment");
+    static_assert(2 * kPiece<D, NT> * 4 <= 2 * Shape<D>::kStage || 2 * kPiece<D, NT> * 4 <= kWarpRing, "a warp's pieces fit its stages");
+    static_assert(kPieces <= 32, "a lane to a piece");
 };
+
+// A piece of a segment: the segment's first unit with a tile (kNone: no piece),
+// its tiles, and whose it is.
+struct PieceInfo {
+    uint32_t seg;
+    int tiles, q0, rows, h, rg;
+};
+constexpr uint32_t kNone = 0xFFFFFFFFu;
 
 // Halves (code of token a, code of token b) of two tokens' words: the even
 // codes 0, 2, 4, 6 at bits 0, 4, 8, 12 of each half, or the odd ones.
@@ -481,43 +512,45 @@ __device__ __forceinline__ void take_tile(const uint8_t* stage, int tok0, uint32
 // Where row `row` of row group rg of (request, head h) goes: its index in
 // [token][head], or -1 behind the last row.
 template <int RT>
-__device__ __forceinline__ int64_t row_index(const AttnParams& P, const Request& r, int h, int rg, int row) {
+__device__ __forceinline__ int64_t row_index(const AttnParams& P, int q0, int rows, int h, int rg, int row) {
     const int i = rg * RT + row;
-    if (i >= r.rows) return -1;
+    if (i >= rows) return -1;
     const int qi = i / P.group;
-    return (static_cast<int64_t>(r.q0) + qi) * P.a.heads + h * P.group + i - qi * P.group;
+    return (static_cast<int64_t>(q0) + qi) * P.a.heads + h * P.group + i - qi * P.group;
 }
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 && D <= 128 ? kCtasPerSm : 1) attn_kernel(const __grid_constant__ AttnParams P) {
+__global__ void __launch_bounds__(Smem<D, NT>::kThreads, 1) attn_kernel(const __grid_constant__ AttnParams P) {
     using S = Shape<D>;
     using M = Smem<D, NT>;
-    constexpr int RT = 8 * NT, NG = S::kGroups, kStages = M::kStages, kDepth = M::kDepth;
+    constexpr int RT = 8 * NT, NG = S::kGroups, W = M::kWarps;
     extern __shared__ __align__(128) uint8_t smem[];
-    const uint32_t base = smem_addr(smem);
-    auto full = [&](uint32_t s) { return base + M::kBars + 8u * s; };
-    auto empty = [&](uint32_t s) { return base + M::kBars + 8u * (kStages + s); };
-    volatile uint32_t* valid = reinterpret_cast<volatile uint32_t*>(smem + M::kValid);
-    volatile uint32_t* abort = reinterpret_cast<volatile uint32_t*>(smem + M::kMisc);
+    const int depth = P.depth, warp_ring = depth * S::kStage;
+    uint8_t* behind = smem - P.early;          // with fewer stages what follows them lies that much earlier
+    const uint32_t base = smem_addr(smem), bars = base - P.early + M::kBars;
+    auto full = [&](uint32_t s) { return bars + 8u * s; };
+    auto empty = [&](uint32_t s) { return bars + 8u * (W * M::kDepth + s); };
+    volatile uint32_t* valid = reinterpret_cast<volatile uint32_t*>(behind + M::kValid);
+    volatile uint32_t* progress = reinterpret_cast<volatile uint32_t*>(behind + M::kProgress);
+    volatile uint32_t* abort = reinterpret_cast<volatile uint32_t*>(behind + M::kMisc);
     volatile uint32_t* last_flag = abort + 1;                            // [2]
-    uint32_t* warp_sums = reinterpret_cast<uint32_t*>(smem + M::kScan);
-    uint32_t* prefix = reinterpret_cast<uint32_t*>(smem + M::kFixed);    // [batch + 1]
+    uint32_t* warp_sums = reinterpret_cast<uint32_t*>(behind + M::kScan);
+    uint32_t* prefix = reinterpret_cast<uint32_t*>(behind + M::kFixed);    // [batch + 1]
     const AttnArgs& a = P.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int heads = P.cache.heads;
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
-            mbar_init(full(s), 1);
-            mbar_init(empty(s), 1);
-            valid[s] = 0u;
-        }
-        *abort = 0u;
+    if (static_cast<int>(threadIdx.x) < W * depth) {
+        mbar_init(full(threadIdx.x), 1);
+        mbar_init(empty(threadIdx.x), 1);
+        valid[threadIdx.x] = 0u;
+        if (threadIdx.x < W) progress[threadIdx.x] = 0u;
+        if (threadIdx.x == 0) *abort = 0u;
         fence_mbar_init();
     }
     // units before each request
     {
-        const int each = (a.batch + kThreads - 1) / kThreads;
+        const int each = (a.batch + M::kThreads - 1) / M::kThreads;
         const int b0 = min(static_cast<int>(threadIdx.x) * each, a.batch), b1 = min(b0 + each, a.batch);
         uint32_t mine = 0;
         for (int b = b0; b < b1; ++b) mine += request_of<RT>(P, b).units(heads);
@@ -535,18 +568,25 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && D <= 128 ? kCtasPerSm : 1
             prefix[b] = at;
             if (b + 1 < b1) at += request_of<RT>(P, b).units(heads);
         }
-        if (threadIdx.x == kThreads - 1) {
+        if (threadIdx.x == M::kThreads - 1) {
             uint32_t all = 0;
-            for (int w = 0; w <= kWarps; ++w) all += warp_sums[w];
+            for (int w = 0; w <= W; ++w) all += warp_sums[w];
             prefix[a.batch] = all;
         }
         __syncthreads();
     }
     const uint32_t total = prefix[a.batch];                              // below 2^32: checked on the host
-    const uint32_t blocks = min(gridDim.x, (total + kWarps - 1) / kWarps);
+    uint32_t blocks = min(gridDim.x, (total + W - 1) / W);
+    // One request with short segments: a block to a segment, so that nothing is
+    // joined over blocks (that takes longer than four tiles to a warp do).
+    if (a.batch == 1 && total > 0) {
+        const Request r = request_of<RT>(P, 0);
+        const uint32_t segments = static_cast<uint32_t>(r.row_groups) * heads;
+        if (r.tiles <= 4 * W && segments <= gridDim.x) blocks = segments;
+    }
     if (blockIdx.x >= blocks) return;                                    // nothing of this block is in flight
     auto first_unit = [&](uint32_t w) {                                  // of consumer warp w of the grid
-        return static_cast<uint32_t>(static_cast<uint64_t>(total) * w / (blocks * kWarps));
+        return static_cast<uint32_t>(static_cast<uint64_t>(total) * w / (blocks * W));
     };
     auto request_at = [&](uint32_t u) {                                  // the request that holds unit u
         int lo = 0, hi = a.batch - 1;
@@ -557,14 +597,26 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && D <= 128 ? kCtasPerSm : 1
         }
         return lo;
     };
+    // A warp's range u .. u1 - 1 from its first unit with a tile on: request,
+    // head, row group and tile of u.
+    auto begin = [&](uint32_t& u, uint32_t u1, Request& r, int& b, int& h, int& rg, int& idx) {
+        if (u >= u1) return;
+        b = request_at(u);
+        r = request_of<RT>(P, b);
+        locate(u - prefix[b], r, h, rg, idx);
+        if (idx < 0) {
+            u += static_cast<uint32_t>(-idx);
+            idx = 0;
+        }
+    };
 
-    if (warp == kWarps) {
+    if (warp == W) {
         // ------------------------------------------------------- producer --
-        // A lane to each stage: it copies every kDepth-th unit of the stage's
-        // warp and looks up the next one's pages while it waits.
-        if (lane < kStages) {
-            const uint32_t s = lane, mine = blockIdx.x * kWarps + lane / kDepth, place = lane % kDepth;
-            const uint32_t u0 = first_unit(mine), count = first_unit(mine + 1) - u0;
+        // A lane to each consumer warp: it copies the warp's units into its
+        // stages in turn and looks up the next one's pages while it waits.
+        if (lane < W) {
+            const uint32_t mine = blockIdx.x * W + lane, u1 = first_unit(mine + 1), s0 = lane * depth;
+            uint32_t u = first_unit(mine);
             const bool one_page = P.cache.page_size >= kTile;
             int b = 0, h = 0, rg = 0, idx = 0;
             Request r{};
@@ -578,17 +630,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && D <= 128 ? kCtasPerSm : 1
                 for (int i = 0; i < kTileRecords; ++i)
                     page[i] = i < records && (i == 0 || !one_page) ? row[(tok0 + i * kKvTokens) >> P.cache.page_shift] : -1;
             };
-            uint32_t n = place;
-            if (n < count) {
-                b = request_at(u0 + n);
-                r = request_of<RT>(P, b);
-                locate(u0 + n - prefix[b], r, h, rg, idx);
-                look();
-            }
-            uint32_t turn = 0;
+            begin(u, u1, r, b, h, rg, idx);
+            if (u < u1) look();
+            uint32_t s = 0, turn = 0;
             int64_t t0 = 0;
-            for (uint32_t polls = 0; n < count; ++polls) {
-                if (turn > 0 && !mbar_try_wait(empty(s), (turn - 1) & 1u)) {
+            bool first = true;
+            for (uint32_t polls = 0; u < u1; ++polls) {
+                if (turn > 0 && !mbar_try_wait(empty(s0 + s), (turn - 1) & 1u)) {
                     if (polls % 256 == 255) {
                         const int64_t now = clock64();
                         if (t0 == 0) t0 = now;
@@ -605,65 +653,59 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && D <= 128 ? kCtasPerSm : 1
 #pragma unroll
                 for (int i = 0; i < kTileRecords; ++i)
                     if (page[i] >= 0 && page[i] < P.cache.pages) have |= one_page ? (1u << records) - 1 : 1u << i;
-                // (testing aid: with stall the first unit's bytes are announced but
-                // never copied; its wait can only time out)
-                const bool copied = !(P.stall && lane == 0 && n == 0);
-                const uint32_t dst = base + s * S::kStage;
-                valid[s] = have | (copied ? kIssued : 0u) | ((turn & 1u) ? kOddTurn : 0u);
-                mbar_arrive_expect_tx(full(s), __popc(have) * S::kRecord);
+                // (testing aid: with stall each warp's first bytes are announced but never
+                // copied; its wait can only time out)
+                const bool copied = !(P.stall && first);
+                first = false;
+                const uint32_t dst = base + lane * warp_ring + s * S::kStage;
+                valid[s0 + s] = have | (copied ? kIssued : 0u) | ((turn & 1u) ? kOddTurn : 0u);
+                mbar_arrive_expect_tx(full(s0 + s), __popc(have) * S::kRecord);
                 if (copied) {
 #pragma unroll
                     for (int i = 0; i < kTileRecords; ++i) {
                         if (!((have >> i) & 1) || (i > 0 && one_page)) continue;
                         const int tok = tok0 + i * kKvTokens;
                         const uint8_t* src = P.cache.record((static_cast<int64_t>(page[i]) << P.cache.page_shift) + (tok & (P.cache.page_size - 1)), h);
-                        bulk_g2s(dst + i * S::kRecord, src, (one_page ? __popc(have) : 1) * S::kRecord, full(s));
+                        bulk_g2s(dst + i * S::kRecord, src, (one_page ? __popc(have) : 1) * S::kRecord, full(s0 + s));
                     }
                 }
-                ++turn;
+                if (++s == static_cast<uint32_t>(depth)) {
+                    s = 0;
+                    ++turn;
+                }
                 t0 = 0;
-                n += kDepth;
-                if (n < count) {
-                    idx += kDepth;
-                    while (idx >= r.tiles) {
-                        idx -= r.tiles;
-                        if (++rg < r.row_groups) continue;
-                        rg = 0;
-                        if (++h < heads) continue;
-                        h = 0;
-                        do r = request_of<RT>(P, ++b); while (r.rows == 0);   // a request with units follows: n < count
-                    }
-                    look();
+                ++u;
+                if (++idx == r.tiles) {
+                    idx = 0;
+                    u += kSegmentUnits;
+                    if (u < u1) next_segment<RT>(P, r, b, h, rg);
                 }
+                if (u < u1) look();
             }
-            // the last copy into the stage lands before the block ends, also after an abort
-            if (valid[s] & kIssued) wait_phase(full(s), valid[s] & kOddTurn ? 1u : 0u, kAttnDrainNs, nullptr);
+            // the last copies into the stages land before the block ends, also after an abort
+            for (int i = 0; i < depth; ++i)
+                if (valid[s0 + i] & kIssued) wait_phase(full(s0 + i), valid[s0 + i] & kOddTurn ? 1u : 0u, kAttnDrainNs, nullptr);
         }
         return;
     }
 
     // ---------------------------------------------------------- consumers --
     const int g = lane >> 2, t = lane & 3;
-    const uint32_t mine = blockIdx.x * kWarps + warp;
-    const uint32_t u0 = first_unit(mine), u1 = first_unit(mine + 1);
-    // a warp's pieces: [0] of a segment that began before it, [1] of one that goes on behind it;
-    // seg: the segment's first unit, or kNone
-    constexpr uint32_t kNone = 0xFFFFFFFFu;
-    uint32_t* piece_seg = reinterpret_cast<uint32_t*>(smem + M::kRuns);  // [warps][2]
-    if (lane < 2) piece_seg[2 * warp + lane] = kNone;
+    const uint32_t mine = blockIdx.x * W + warp;
+    const uint32_t u1 = first_unit(mine + 1);
+    // a warp's pieces: [0] of a segment that began before it, [1] of one that goes on behind it
+    PieceInfo* pieces = reinterpret_cast<PieceInfo*>(behind + M::kPieceOf);
+    if (lane < 2) pieces[2 * warp + lane].seg = kNone;
     __syncwarp();
     {
-        float* my_pieces = reinterpret_cast<float*>(smem + warp * M::kWarpRing);      // [2] pieces, once the stages are free
-        uint32_t stage = warp * kDepth, parity = 0;
+        float* my_pieces = reinterpret_cast<float*>(smem + warp * warp_ring);         // [2] pieces, once the stages are free
+        uint32_t stage = warp * depth, parity = 0, done = 0;
         bool alive = true, waiting = false;
         int b = 0, h = 0, rg = 0, first = 0;
         Request r{};
-        if (u0 < u1) {
-            b = request_at(u0);
-            r = request_of<RT>(P, b);
-            locate(u0 - prefix[b], r, h, rg, first);
-        }
-        for (uint32_t u = u0; u < u1;) {
+        uint32_t u = first_unit(mine);
+        begin(u, u1, r, b, h, rg, first);
+        while (u < u1) {
             const int count = static_cast<int>(min(static_cast<uint32_t>(r.tiles - first), u1 - u));
             const int row0 = rg * RT;
             State<D, NT> st;
@@ -694,18 +736,29 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && D <= 128 ? kCtasPerSm : 1
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(empty(stage));
-                if (++stage == (warp + 1) * kDepth) {
-                    stage = warp * kDepth;
+                if (++stage == (warp + 1) * static_cast<uint32_t>(depth)) {
+                    stage = warp * depth;
                     parity ^= 1u;
+                }
+                // not too far ahead of the block's last warp (it goes on by itself, so this ends;
+                // bounded all the same)
+                if (++done % 4 == 0) {
+                    if (lane == 0) progress[warp] = done;
+                    for (int tries = 0; tries < 4096; ++tries) {
+                        const uint32_t last = __reduce_min_sync(0xFFFFFFFFu, progress[lane < W ? lane : warp]);
+                        if (done <= last + kLead || *abort) break;
+                        __nanosleep(200);
+                    }
                 }
             }
             st.finish();
-            if (count == r.tiles) {
+            const bool cut = first + count < r.tiles;
+            if (first == 0 && !cut) {
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
-                        const int64_t at = row_index<RT>(P, r, h, rg, 8 * n + 2 * t + c);
+                        const int64_t at = row_index<RT>(P, r.q0, r.rows, h, rg, 8 * n + 2 * t + c);
                         if (at < 0) continue;
                         const float inv = st.sum[n][c] == 0.0f ? 0.0f : 1.0f / st.sum[n][c];
 #pragma unroll
@@ -720,11 +773,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && D <= 128 ? kCtasPerSm : 1
             } else {
                 const int kind = first == 0 ? 1 : 0;
                 // the warp's stages are free behind its last unit; an earlier piece waits in the workspace
-                const bool at_end = u + count == u1;
+                const bool at_end = cut || u + count + kSegmentUnits >= u1;
                 float* slot = at_end ? my_pieces + kind * kPiece<D, NT> : P.warp_slots + static_cast<int64_t>(mine) * kPiece<D, NT>;
                 waiting |= !at_end;
                 __syncwarp();
-                if (lane == 0) piece_seg[2 * warp + kind] = u - first;
+                if (lane == 0) pieces[2 * warp + kind] = PieceInfo{u - first, r.tiles, r.q0, r.rows, h, rg};
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -741,14 +794,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && D <= 128 ? kCtasPerSm : 1
             }
             u += count;
             first = 0;
-            if (u < u1 && ++rg == r.row_groups) {
-                rg = 0;
-                if (++h == heads) {
-                    h = 0;
-                    do r = request_of<RT>(P, ++b); while (r.rows == 0);
-                }
+            if (!cut) {
+                u += kSegmentUnits;
+                if (u < u1) next_segment<RT>(P, r, b, h, rg);
             }
         }
+        if (lane == 0) progress[warp] = kNone;
         if (waiting && alive) {                        // (after an abort copies may still be on their way into the stages)
             __syncwarp();                              // the warp's own writes
             const float4* from = reinterpret_cast<const float4*>(P.warp_slots + static_cast<int64_t>(mine) * kPiece<D, NT>);
@@ -759,46 +810,42 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && D <= 128 ? kCtasPerSm : 1
 
     // -------------------------------------------------- the block's join --
     // Its pieces in unit order form runs of one segment each.
-    consumers_sync();
-    uint32_t* order = piece_seg + 2 * kWarps + 2;      // [pieces] piece numbers
-    uint32_t* run_of = order + 2 * kWarps + 2;         // [pieces] and, behind them, the number of pieces and of runs
-    uint32_t* run_at = run_of + 2 * kWarps + 2;        // [runs + 1] first piece of a run
-    float* factors = reinterpret_cast<float*>(smem + M::kFactors);       // [pieces][rows]
-    if (threadIdx.x == 0) {
-        int pieces = 0, runs = 0;
-        uint32_t seg = kNone;
-        for (int i = 0; i < 2 * kWarps; ++i) {
-            if (piece_seg[i] == kNone) continue;
-            if (piece_seg[i] != seg) run_at[runs++] = pieces;
-            seg = piece_seg[i];
-            order[pieces] = i;
-            run_of[pieces++] = runs - 1;
+    consumers_sync<W>();
+    uint32_t* order = reinterpret_cast<uint32_t*>(behind + M::kRuns);      // [pieces] piece numbers
+    uint32_t* run_at = order + M::kPieces;                               // [runs + 1] first piece of a run, then the number of runs
+    float* factors = reinterpret_cast<float*>(behind + M::kFactors);       // [pieces][rows]
+    if (warp == 0) {
+        const uint32_t seg = lane < M::kPieces ? pieces[lane].seg : kNone, lower = (1u << lane) - 1u;
+        const uint32_t have = __ballot_sync(0xFFFFFFFFu, seg != kNone);
+        const uint32_t before = __shfl_sync(0xFFFFFFFFu, seg, have & lower ? 31 - __clz(have & lower) : lane);
+        const bool starts = seg != kNone && (!(have & lower) || before != seg);
+        const uint32_t start = __ballot_sync(0xFFFFFFFFu, starts);
+        if (seg != kNone) order[__popc(have & lower)] = lane;
+        if (starts) run_at[__popc(start & lower)] = __popc(have & lower);
+        if (lane == 0) {
+            run_at[__popc(start)] = __popc(have);
+            run_at[M::kRunsMost + 1] = __popc(start);
         }
-        run_at[runs] = pieces;
-        run_of[2 * kWarps] = pieces;
-        run_of[2 * kWarps + 1] = runs;
     }
-    consumers_sync();
-    const int runs = static_cast<int>(run_of[2 * kWarps + 1]);
+    consumers_sync<W>();
+    const int runs = static_cast<int>(run_at[M::kRunsMost + 1]);
     if (runs == 0) return;
-    auto block_of = [&](uint32_t x) {                  // the block that holds unit x
-        return static_cast<uint32_t>(((static_cast<uint64_t>(x) + 1) * blocks + total - 1) / total - 1);
-    };
+    // a segment is the block's alone if all its tiles are
+    const uint32_t b_u0 = first_unit(blockIdx.x * W), b_u1 = first_unit((blockIdx.x + 1) * W);
+    auto inside = [&](const PieceInfo& i) { return i.seg >= b_u0 && i.seg + i.tiles <= b_u1; };
     auto piece_at = [&](int i) {                       // i-th piece of the block
-        return reinterpret_cast<const float*>(smem + (order[i] >> 1) * M::kWarpRing) + (order[i] & 1) * kPiece<D, NT>;
+        return reinterpret_cast<const float*>(smem + (order[i] >> 1) * warp_ring) + (order[i] & 1) * kPiece<D, NT>;
     };
     auto block_slot = [&](uint32_t c, bool begins) { return P.block_slots + (2 * static_cast<int64_t>(c) + begins) * kPiece<D, NT>; };
     // A run's row: common reference and sum; each piece's factor to them, for
     // whole segments to the output; the others' (reference, sum) goes to the
     // block's slot.
-    int64_t* row_out = reinterpret_cast<int64_t*>(smem + M::kRowOut);    // [runs][rows]: output row, kToNone, kToSlot + begins
+    int64_t* row_out = reinterpret_cast<int64_t*>(behind + M::kRowOut);    // [runs][rows]: output row, kToNone, kToSlot + begins
     constexpr int64_t kToNone = -1, kToSlot = -3;
-    for (int i = threadIdx.x; i < runs * RT; i += kWarps * 32) {
+    for (int i = threadIdx.x; i < runs * RT; i += W * 32) {
         const int run = i / RT, row = i % RT;
         const int p0 = run_at[run], p1 = run_at[run + 1];
-        const uint32_t seg = piece_seg[order[p0]];
-        const int b = request_at(seg);
-        const Request r = request_of<RT>(P, b);
+        const PieceInfo info = pieces[order[p0]];
         float m = -INFINITY, l = 0.0f;
         for (int p = p0; p < p1; ++p) m = fmaxf(m, reinterpret_cast<const float2*>(piece_at(p) + RT * D)[row].x);
         for (int p = p0; p < p1; ++p) {
@@ -807,22 +854,20 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && D <= 128 ? kCtasPerSm : 1
             factors[p * RT + row] = f;
             l += f * v.y;
         }
-        const uint32_t c0 = block_of(seg), c1 = block_of(seg + r.tiles - 1);
-        if (c0 == c1) {
+        if (inside(info)) {
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
             for (int p = p0; p < p1; ++p) factors[p * RT + row] *= inv;
-            int h, rg, idx;
-            locate(seg - prefix[b], r, h, rg, idx);
-            const int64_t at = row_index<RT>(P, r, h, rg, row);
+            const int64_t at = row_index<RT>(P, info.q0, info.rows, info.h, info.rg, row);
             if (a.lse && at >= 0) a.lse[at] = log_sum(m, l);
             row_out[i] = at >= 0 ? at : kToNone;
         } else {
-            reinterpret_cast<float2*>(block_slot(blockIdx.x, c0 == blockIdx.x) + RT * D)[row] = make_float2(m, l);
-            row_out[i] = kToSlot + (c0 == blockIdx.x);
+            const bool begins = info.seg >= b_u0;
+            reinterpret_cast<float2*>(block_slot(blockIdx.x, begins) + RT * D)[row] = make_float2(m, l);
+            row_out[i] = kToSlot + begins;
         }
     }
-    consumers_sync();
-    for (int i = threadIdx.x; i < runs * (RT * D / 4); i += kWarps * 32) {
+    consumers_sync<W>();
+    for (int i = threadIdx.x; i < runs * (RT * D / 4); i += W * 32) {
         const int run = i / (RT * D / 4), e = (i % (RT * D / 4)) * 4, row = e / D, d = e % D;
         const int64_t at = row_out[run * RT + row];
         if (at == kToNone) continue;
@@ -840,42 +885,43 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && D <= 128 ? kCtasPerSm : 1
     // ------------------------------------------- segments of several blocks --
     // The first and the last run may be pieces of such; the last block to
     // arrive joins them, in block order.
-    const uint32_t seg_first = piece_seg[order[0]], seg_last = piece_seg[order[run_at[runs] - 1]];
-    consumers_sync();                                  // the block's slots are written, the pieces read
+    const PieceInfo side_of[2] = {pieces[order[0]], pieces[order[run_at[runs] - 1]]};
+    const bool shared[2] = {!inside(side_of[0]), side_of[1].seg != side_of[0].seg && !inside(side_of[1])};
+    if (!shared[0] && !shared[1]) return;              // the same for every thread
+    auto block_of = [&](uint32_t x) {                  // the block that holds unit x
+        return static_cast<uint32_t>(((static_cast<uint64_t>(x) + 1) * blocks + total - 1) / total - 1);
+    };
+    consumers_sync<W>();                               // the block's slots are written, the pieces read
     if (threadIdx.x < 2) {
-        const uint32_t seg = threadIdx.x ? seg_last : seg_first;
+        const PieceInfo& info = side_of[threadIdx.x];
         bool last = false;
-        if (threadIdx.x == 0 || seg_last != seg_first) {
-            const Request r = request_of<RT>(P, request_at(seg));
-            const uint32_t c0 = block_of(seg), c1 = block_of(seg + r.tiles - 1);
-            if (c0 != c1) {
-                __threadfence();
-                last = atomicAdd(&P.counters[c0], 1u) == c1 - c0;
-                __threadfence();
-                if (last) P.counters[c0] = 0u;
-            }
+        if (shared[threadIdx.x]) {
+            const uint32_t c0 = block_of(info.seg), c1 = block_of(info.seg + info.tiles - 1);
+            uint32_t old;
+            asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(old) : "l"(P.counters + c0) : "memory");
+            last = old == c1 - c0;
+            if (last) P.counters[c0] = 0u;
         }
         last_flag[threadIdx.x] = last;
     }
-    consumers_sync();
-    // no copy is in flight and no piece is read any more: the ring holds the parts' factors
-    float* part_factors = reinterpret_cast<float*>(smem);                // [parts][rows]; the grid's fit (see launch)
-    float2* part_sums = reinterpret_cast<float2*>(smem + M::kRing / 2);  // [parts][rows]
+    consumers_sync<W>();
+    // Nothing is in flight into the ring and no piece is read any more: it holds
+    // the parts' references and sums, their factors, and each warp's sum of every
+    // W-th part.
+    float2* part_sums = reinterpret_cast<float2*>(smem);                 // [parts][rows]; the grid's fit (see launch)
     for (int side = 0; side < 2; ++side) {
         if (!last_flag[side]) continue;
-        const uint32_t seg = side ? seg_last : seg_first;
-        const int b = request_at(seg);
-        const Request r = request_of<RT>(P, b);
-        const uint32_t c0 = block_of(seg), c1 = block_of(seg + r.tiles - 1);
-        int h, rg, idx;
-        locate(seg - prefix[b], r, h, rg, idx);
+        const PieceInfo info = side_of[side];
+        const uint32_t c0 = block_of(info.seg), c1 = block_of(info.seg + info.tiles - 1);
         const int parts = static_cast<int>(c1 - c0 + 1);
-        for (int i = threadIdx.x; i < parts * RT; i += kWarps * 32) {
+        float* part_factors = reinterpret_cast<float*>(part_sums + parts * RT);      // [parts][rows]
+        float4* share = reinterpret_cast<float4*>(smem + (parts * RT * 12 + 15) / 16 * 16);   // [warps][RT * D / 4]
+        for (int i = threadIdx.x; i < parts * RT; i += W * 32) {
             const int p = i / RT, row = i % RT;
             part_sums[i] = __ldcg(reinterpret_cast<const float2*>(block_slot(c0 + p, p == 0) + RT * D) + row);
         }
-        consumers_sync();
-        for (int row = warp; row < RT; row += kWarps) {
+        consumers_sync<W>();
+        for (int row = warp; row < RT; row += W) {
             float m = -INFINITY, l = 0.0f;
             for (int p = lane; p < parts; p += 32) m = fmaxf(m, part_sums[p * RT + row].x);
 #pragma unroll
@@ -891,58 +937,76 @@ __global__ void __launch_bounds__(kThreads, NT == 1 && D <= 128 ? kCtasPerSm : 1
                 const float ref = part_sums[p * RT + row].x;
                 part_factors[p * RT + row] = ref == -INFINITY ? 0.0f : ex2(ref - m) * inv;
             }
-            const int64_t at = row_index<RT>(P, r, h, rg, row);
+            const int64_t at = row_index<RT>(P, info.q0, info.rows, info.h, info.rg, row);
             if (a.lse && at >= 0 && lane == 0) a.lse[at] = log_sum(m, l);
         }
-        consumers_sync();
-        constexpr int kElements = RT * D / 4;
-        for (int i = threadIdx.x; i < kElements; i += 2 * kWarps * 32) {
-            const int e0 = i * 4, e1 = min(i + kWarps * 32, kElements - 1) * 4;
-            float4 o0 = make_float4(0.0f, 0.0f, 0.0f, 0.0f), o1 = o0;
-            const float* f0 = part_factors + e0 / D;
-            const float* f1 = part_factors + e1 / D;
-#pragma unroll 8
-            for (int p = 0; p < parts; ++p) {
-                const float* from = block_slot(c0 + p, p == 0);
-                const float4 v0 = __ldcg(reinterpret_cast<const float4*>(from + e0)), v1 = __ldcg(reinterpret_cast<const float4*>(from + e1));
-                const float a0 = f0[p * RT], a1 = f1[p * RT];
-                o0.x = fmaf(a0, v0.x, o0.x); o0.y = fmaf(a0, v0.y, o0.y); o0.z = fmaf(a0, v0.z, o0.z); o0.w = fmaf(a0, v0.w, o0.w);
-                o1.x = fmaf(a1, v1.x, o1.x); o1.y = fmaf(a1, v1.y, o1.y); o1.z = fmaf(a1, v1.z, o1.z); o1.w = fmaf(a1, v1.w, o1.w);
+        consumers_sync<W>();
+        constexpr int kEach = RT * D / 128;            // fours of a lane
+        float4 o[kEach];
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) o[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int p = warp; p < parts; p += W) {
+            const float4* from = reinterpret_cast<const float4*>(block_slot(c0 + p, p == 0));
+            float4 v[kEach];
+#pragma unroll
+            for (int k = 0; k < kEach; ++k) v[k] = __ldcg(from + lane + 32 * k);
+#pragma unroll
+            for (int k = 0; k < kEach; ++k) {
+                const float f = part_factors[p * RT + (lane + 32 * k) * 4 / D];
+                o[k].x = fmaf(f, v[k].x, o[k].x); o[k].y = fmaf(f, v[k].y, o[k].y);
+                o[k].z = fmaf(f, v[k].z, o[k].z); o[k].w = fmaf(f, v[k].w, o[k].w);
             }
-            const int64_t at0 = row_index<RT>(P, r, h, rg, e0 / D), at1 = row_index<RT>(P, r, h, rg, e1 / D);
-            if (at0 >= 0) *reinterpret_cast<uint2*>(a.out + at0 * D + e0 % D) = make_uint2(pack_half2(o0.x, o0.y), pack_half2(o0.z, o0.w));
-            if (i + kWarps * 32 < kElements && at1 >= 0)
-                *reinterpret_cast<uint2*>(a.out + at1 * D + e1 % D) = make_uint2(pack_half2(o1.x, o1.y), pack_half2(o1.z, o1.w));
         }
-        consumers_sync();                              // the factors are written again
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) share[warp * (RT * D / 4) + lane + 32 * k] = o[k];
+        consumers_sync<W>();
+        for (int i = threadIdx.x; i < RT * D / 4; i += W * 32) {
+            const int row = i * 4 / D, d = i * 4 % D;
+            const int64_t at = row_index<RT>(P, info.q0, info.rows, info.h, info.rg, row);
+            if (at < 0) continue;
+            float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            for (int w = 0; w < min(W, parts); ++w) {
+                const float4 v = share[w * (RT * D / 4) + i];
+                s.x += v.x; s.y += v.y; s.z += v.z; s.w += v.w;
+            }
+            *reinterpret_cast<uint2*>(a.out + at * D + d) = make_uint2(pack_half2(s.x, s.y), pack_half2(s.z, s.w));
+        }
+        consumers_sync<W>();                           // the ring is written again
     }
 }
-
-template <int D, int NT>
-constexpr int kBlocksPerSm = NT == 1 && D <= 128 ? kCtasPerSm : 1;
 
 // Workspace: status word (256 bytes), one counter and two slots per thread
 // block, one slot per consumer warp.
 template <int D, int NT>
 size_t workspace_bytes(int num_sms) {
-    const size_t blocks = static_cast<size_t>(num_sms) * kBlocksPerSm<D, NT>;
-    return 256 + attn_counter_bytes(num_sms) + blocks * (2 + kWarps) * kPiece<D, NT> * 4;
+    return 256 + attn_counter_bytes(num_sms) + static_cast<size_t>(num_sms) * (2 + Smem<D, NT>::kWarps) * kPiece<D, NT> * 4;
 }
 
 template <int D, int NT>
 cudaError_t launch(AttnParams P, uint8_t* ws, int num_sms, cudaStream_t s) {
+    using M = Smem<D, NT>;
+    constexpr int kLimit = 227 * 1024;
     static std::atomic<uint64_t> smem_set{0};
-    if (cudaError_t e = set_smem_limit_once(attn_kernel<D, NT>, 227 * 1024, smem_set); e != cudaSuccess) return e;
-    const int smem = Smem<D, NT>::bytes(P.a.batch);
-    if (smem > 227 * 1024) return cudaErrorInvalidValue;
-    int grid = num_sms * kBlocksPerSm<D, NT>;
-    constexpr int kMost = Smem<D, NT>::kRing / (2 * 8 * NT * 8);         // blocks whose references and sums fit half the ring
-    if (grid > kMost) grid = kMost;
+    if (cudaError_t e = set_smem_limit_once(attn_kernel<D, NT>, kLimit, smem_set); e != cudaSuccess) return e;
+    const int smem = M::bytes(P.a.batch);
+    // a very large batch's prefix sums take the place of a stage per warp
+    P.depth = M::kDepth;
+    int shift = 0;
+    while (smem - shift > kLimit && P.depth > 2) {
+        --P.depth;
+        shift += M::kWarps * Shape<D>::kStage;
+    }
+    P.early = shift;
+    if (smem - shift > kLimit || 2 * kPiece<D, NT> * 4 > P.depth * Shape<D>::kStage) return cudaErrorInvalidValue;
+    // the last block to join keeps the parts' references, sums and factors and its warps' shares in the ring
+    int grid = num_sms;
+    const int room = M::kWarps * P.depth * Shape<D>::kStage - M::kWarps * M::kRT * D * 4 - 16;
+    if (grid > room / (M::kRT * 12)) grid = room / (M::kRT * 12);
     P.status = reinterpret_cast<uint32_t*>(ws);
     P.counters = reinterpret_cast<uint32_t*>(ws + 256);
     P.block_slots = reinterpret_cast<float*>(ws + 256 + attn_counter_bytes(num_sms));
     P.warp_slots = P.block_slots + 2 * static_cast<size_t>(grid) * kPiece<D, NT>;
-    attn_kernel<D, NT><<<grid, kThreads, smem, s>>>(P);
+    attn_kernel<D, NT><<<grid, M::kThreads, smem - shift, s>>>(P);
     return cudaGetLastError();
 }
 

@@ -25,6 +25,8 @@ struct AttnParams {
     float* warp_slots;         // one per consumer warp
     uint64_t timeout_ns;
     int stall;                 // testing aid: see pn_set_test_stall
+    int depth;                 // stages per warp (kernel for few rows), and by how much
+    int early;                 // shared memory behind them moves forward for it
 };
 
 __device__ __forceinline__ float ex2(float x) {
