@@ -47,21 +47,49 @@ __device__ __forceinline__ int64_t weight(const Row& r, int j) {
     return j == r.skip ? 0 : whole(p);
 }
 
+// Weights are summed without 64-bit conversions (a fifth of the time): with t =
+// 2^21 w, a = rint(t) by adding 1.5 2^23 and the rest t - a, which is exact, times
+// 2^21 rounded the same way, whole(w) = 2^21 a + rint(2^21 (t - a)) -- the first
+// part is even, so ties go as in one rounding -- and both parts of up to 512
+// weights add up in 32 bits.
+struct Sum {
+    uint32_t high = 0, low = 0;
+    __device__ __forceinline__ void add(float w) {
+        constexpr float kMagic = 12582912.0f;      // 1.5 2^23
+        const float t = __fmul_rn(fminf(fmaxf(w, 0.0f), 1.0f), 2097152.0f);   // (NaN: 0)
+        const float a = __fadd_rn(t, kMagic);
+        const float b = __fmaf_rn(__fsub_rn(t, __fsub_rn(a, kMagic)), 2097152.0f, kMagic);
+        high += __float_as_uint(a) - 0x4B400000u;
+        low += __float_as_uint(b) - 0x4B400000u;
+    }
+    __device__ __forceinline__ int64_t value() const {
+        return (static_cast<int64_t>(static_cast<int32_t>(high)) << 21) + static_cast<int32_t>(low);
+    }
+};
+
 // The sum of the weights j .. j + 3 for j = j0, j0 + step, ... below j1; rows 16-byte aligned, all multiples of 4.
 __device__ __forceinline__ int64_t sum_fours(const Row& r, int j0, int j1, int step) {
-    int64_t s = 0;
+    Sum s;
+    if (r.q) {
 #pragma unroll 4
-    for (int j = j0; j < j1; j += step) {
-        const float4 p = __ldcg(reinterpret_cast<const float4*>(r.p + j));
-        if (r.q) {
-            const float4 q = __ldcg(reinterpret_cast<const float4*>(r.q + j));
-            s += whole(__fsub_rn(p.x, q.x)) + whole(__fsub_rn(p.y, q.y)) + whole(__fsub_rn(p.z, q.z)) + whole(__fsub_rn(p.w, q.w));
-        } else {
-            s += (j == r.skip ? 0 : whole(p.x)) + (j + 1 == r.skip ? 0 : whole(p.y)) + (j + 2 == r.skip ? 0 : whole(p.z)) +
-                 (j + 3 == r.skip ? 0 : whole(p.w));
+        for (int j = j0; j < j1; j += step) {
+            const float4 p = __ldcg(reinterpret_cast<const float4*>(r.p + j)), q = __ldcg(reinterpret_cast<const float4*>(r.q + j));
+            s.add(__fsub_rn(p.x, q.x));
+            s.add(__fsub_rn(p.y, q.y));
+            s.add(__fsub_rn(p.z, q.z));
+            s.add(__fsub_rn(p.w, q.w));
+        }
+    } else {
+#pragma unroll 8
+        for (int j = j0; j < j1; j += step) {
+            const float4 p = __ldcg(reinterpret_cast<const float4*>(r.p + j));
+            s.add(j == r.skip ? 0.0f : p.x);
+            s.add(j + 1 == r.skip ? 0.0f : p.y);
+            s.add(j + 2 == r.skip ? 0.0f : p.z);
+            s.add(j + 3 == r.skip ? 0.0f : p.w);
         }
     }
-    return s;
+    return s.value();
 }
 
 __device__ __forceinline__ int64_t warp_sum(int64_t v) {
@@ -131,6 +159,7 @@ __global__ void __launch_bounds__(kVerifyThreads, 4) verify_kernel(const VerifyA
         }
         cluster.sync();
         int64_t before = 0, total = 0;
+#pragma unroll
         for (int r = 0; r < kVerifyCluster; ++r) {
             const int64_t t = *cluster.map_shared_rank(&block_total[pass], r);
             before += r < rank ? t : 0;
