@@ -204,15 +204,16 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams P) 
 
 // ----------------------------------------------------------------- append --
 //
-// D / 16 lanes to a head row, so a warp takes 32 / (D / 16) heads of a token at
-// once: lane l of a row owns the four values from 4 l on of each quarter of the
-// row.  With that ownership the pairwise sum's first two levels, the rotation
-// of whole heads by halves and that of neighbours stay inside a lane, and loads
-// are 16 bytes wide, four to a lane.  It is bound by its instructions before it
-// is by memory, so values per lane count: for 8192 tokens of 48 + 16 heads of
-// 128 in fp32, 307 us with 4 values to a lane, 97 us with 8.  A warp stays with
-// its token for several groups of heads, so the rotation's row and the weights
-// are read once.
+// D / 8 lanes to a head row, so a warp takes 32 / (D / 8) heads of a token at
+// once: lane l of a row owns values 4 l .. 4 l + 3 and D / 2 + 4 l .. + 3.
+// With that ownership the pairwise sum's first level, the rotation of whole
+// heads by halves and that of neighbours stay inside a lane, and a row's loads
+// are 16 bytes wide.  A warp stays with its token for several groups of heads,
+// so the rotation's row and the weights are read once.  For 8192 tokens of
+// 48 + 16 heads of 128 in fp32: 85 us, 4.4 TB/s.  It is bound by latency and by
+// its instructions before it is by memory: four values to a lane and a warp to
+// a row takes 307 us (its exchanges), sixteen to a lane 90 us (half the warps
+// to an SM), and rows fetched further ahead than the next change nothing.
 //
 // The arithmetic is fixed, every operation rounded by itself, so codes are the
 // same whatever computes them: squares added pairwise (the upper half of the
@@ -220,8 +221,8 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams P) 
 // x * that * weight; rotation with separate products and sums; pn4t's rule per
 // group of 64.
 
-struct Row {
-    float x[4][4];                             // [quarter][value 4 l + i of it]
+struct Quads {
+    float x[8];                                // values 4 l + i, then D / 2 + 4 l + i
 };
 
 // Two fp32 operations in one instruction.  No packed product may meet a packed
@@ -237,7 +238,7 @@ __device__ __forceinline__ void add2(float& d0, float& d1, float a0, float a1, f
         : "=f"(d0), "=f"(d1) : "f"(a0), "f"(a1), "f"(b0), "f"(b1));
 }
 
-__device__ __forceinline__ void load_quad(const void* p, int64_t at, bool f16, bool wide, float (&x)[4]) {
+__device__ __forceinline__ void load_quad(const void* p, int64_t at, bool f16, bool wide, float* x) {
     if (f16) {
         const __half* h = static_cast<const __half*>(p) + at;
         if (wide) {
@@ -263,101 +264,96 @@ __device__ __forceinline__ void load_quad(const void* p, int64_t at, bool f16, b
 }
 
 template <int D>
-__device__ __forceinline__ void norm_row(Row& r, const float (&weight)[4][4], float eps) {
-    constexpr int L = D / 16;
-    float p[4][4];
+__device__ __forceinline__ void norm_row(Quads& q, const float (&weight)[8], float eps) {
+    constexpr int L = D / 8;
+    float p[8];
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
+    for (int i = 0; i < 8; ++i) p[i] = __fmul_rn(q.x[i], q.x[i]);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p[k][i] = __fmul_rn(r.x[k][i], r.x[k][i]);
-#pragma unroll
-    for (int k = 2; k >= 1; k >>= 1)
-#pragma unroll
-        for (int j = 0; j < k; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; i += 2) add2(p[j][i], p[j][i + 1], p[j][i], p[j][i + 1], p[j + k][i], p[j + k][i + 1]);
+    for (int i = 0; i < 4; i += 2) add2(p[i], p[i + 1], p[i], p[i + 1], p[4 + i], p[5 + i]);
 #pragma unroll
     for (int d = L / 2; d >= 1; d >>= 1)
 #pragma unroll
         for (int i = 0; i < 4; i += 2)
-            add2(p[0][i], p[0][i + 1], p[0][i], p[0][i + 1], __shfl_xor_sync(0xFFFFFFFFu, p[0][i], d),
-                 __shfl_xor_sync(0xFFFFFFFFu, p[0][i + 1], d));
-    const float sum = __fadd_rn(__fadd_rn(p[0][0], p[0][2]), __fadd_rn(p[0][1], p[0][3]));
+            add2(p[i], p[i + 1], p[i], p[i + 1], __shfl_xor_sync(0xFFFFFFFFu, p[i], d), __shfl_xor_sync(0xFFFFFFFFu, p[i + 1], d));
+    const float sum = __fadd_rn(__fadd_rn(p[0], p[2]), __fadd_rn(p[1], p[3]));
     const float inv = __frcp_rn(__fsqrt_rn(__fadd_rn(__fmul_rn(sum, 1.0f / D), eps)));   // correctly rounded, as 1 / x is
 #pragma unroll
-    for (int k = 0; k < 4; ++k)
-#pragma unroll
-        for (int i = 0; i < 4; i += 2) {
-            mul2(r.x[k][i], r.x[k][i + 1], r.x[k][i], r.x[k][i + 1], inv, inv);
-            mul2(r.x[k][i], r.x[k][i + 1], r.x[k][i], r.x[k][i + 1], weight[k][i], weight[k][i + 1]);
-        }
+    for (int i = 0; i < 8; i += 2) {
+        mul2(q.x[i], q.x[i + 1], q.x[i], q.x[i + 1], inv, inv);
+        mul2(q.x[i], q.x[i + 1], q.x[i], q.x[i + 1], weight[i], weight[i + 1]);
+    }
 }
 
 // How the rotation's pairs lie.
 enum { kTurnNone, kTurnHalves /* of the whole head: in a lane */, kTurnNeighbours, kTurnPart /* halves of a part */ };
 
-// cos and sin of the lane's pairs.  kTurnHalves: of its values in the first two
-// quarters (their partners in the last two turn by the same); otherwise of each
-// value, cos 1 and sin 0 where it does not turn.
-template <int D, int TURN>
+// What a lane needs of the row of cos and sin, for each of its values: the
+// pair's cos, and its sin with the sign of the value's product.
 struct Turn {
-    static constexpr int kQuarters = TURN == kTurnHalves ? 2 : 4;
-    float c[kQuarters][4], s[kQuarters][4];
-
-    __device__ __forceinline__ void load(const float* cos, const float* sin, int half, int l) {
-#pragma unroll
-        for (int k = 0; k < kQuarters; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int at = k * (D / 4) + 4 * l + i;
-                const int pair = TURN == kTurnNeighbours ? at >> 1 : at >= half ? at - half : at;
-                const bool turns = TURN == kTurnHalves || at < 2 * half;
-                c[k][i] = turns ? cos[pair] : 1.0f;
-                s[k][i] = turns ? sin[pair] : 0.0f;
-            }
-    }
+    float c[8], s[8];
 };
 
-// (a, b) -> (a c - b s, b c + a s), products and sums rounded one by one.
-// `row` is D floats of shared memory per row (kTurnPart only).
 template <int D, int TURN>
-__device__ __forceinline__ void rotate_row(Row& r, const Turn<D, TURN>& t, int half, float* row, int l) {
-    if constexpr (TURN == kTurnHalves) {
+__device__ __forceinline__ void load_turn(Turn& t, const float* cos, const float* sin, int half, int l) {
 #pragma unroll
-        for (int k = 0; k < 2; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; i += 2) {
-                const float a0 = r.x[k][i], a1 = r.x[k][i + 1], b0 = r.x[k + 2][i], b1 = r.x[k + 2][i + 1];
-                const float c0 = t.c[k][i], c1 = t.c[k][i + 1], s0 = t.s[k][i], s1 = t.s[k][i + 1];
-                add2(r.x[k][i], r.x[k][i + 1], __fmul_rn(a0, c0), __fmul_rn(a1, c1), __fmul_rn(-b0, s0), __fmul_rn(-b1, s1));
-                add2(r.x[k + 2][i], r.x[k + 2][i + 1], __fmul_rn(b0, c0), __fmul_rn(b1, c1), __fmul_rn(a0, s0), __fmul_rn(a1, s1));
-            }
-    } else if constexpr (TURN == kTurnNeighbours) {
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; i += 2) {
-                if (k * (D / 4) + 4 * l + i >= 2 * half) continue;
-                const float a = r.x[k][i], b = r.x[k][i + 1], c = t.c[k][i], s = t.s[k][i];
-                r.x[k][i] = __fsub_rn(__fmul_rn(a, c), __fmul_rn(b, s));
-                r.x[k][i + 1] = __fadd_rn(__fmul_rn(b, c), __fmul_rn(a, s));
-            }
-    } else if constexpr (TURN == kTurnPart) {
-        __syncwarp();
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) row[k * (D / 4) + 4 * l + i] = r.x[k][i];
-        __syncwarp();
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int at = k * (D / 4) + 4 * l + i;
-                if (at < half) r.x[k][i] = __fsub_rn(__fmul_rn(r.x[k][i], t.c[k][i]), __fmul_rn(row[at + half], t.s[k][i]));
-                else if (at < 2 * half) r.x[k][i] = __fadd_rn(__fmul_rn(r.x[k][i], t.c[k][i]), __fmul_rn(row[at - half], t.s[k][i]));
-            }
+    for (int i = 0; i < 8; ++i) {
+        const int at = (i < 4 ? 0 : D / 2) + 4 * l + (i & 3);
+        int pair;
+        bool second;
+        if (TURN == kTurnNeighbours) {
+            pair = at >> 1;
+            second = at & 1;
+        } else {
+            second = at >= half;
+            pair = second ? at - half : at;
+        }
+        const bool turns = TURN == kTurnNeighbours ? pair < half : at < 2 * half;
+        t.c[i] = turns ? cos[pair] : 1.0f;
+        t.s[i] = turns ? (second ? sin[pair] : -sin[pair]) : 0.0f;
     }
+}
+
+// (a, b) -> (a c - b s, b c + a s), products and sums rounded one by one;
+// a c - b s = a c + b (-s) exactly so.  `row` is D floats of shared memory per
+// row (kTurnPart only).  Values outside the rotated part stay as they are.
+template <int D, int TURN>
+__device__ __forceinline__ void rotate_row(Quads& q, const Turn& t, int half, float* row, int l) {
+    float partner[8];
+    if (TURN == kTurnHalves) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) partner[i] = q.x[i ^ 4];
+    } else if (TURN == kTurnNeighbours) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) partner[i] = q.x[i ^ 1];
+    } else {
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) row[(i < 4 ? 0 : D / 2) + 4 * l + (i & 3)] = q.x[i];
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int at = (i < 4 ? 0 : D / 2) + 4 * l + (i & 3);
+            partner[i] = at < half ? row[at + half] : at < 2 * half ? row[at - half] : 0.0f;
+        }
+    }
+    // (a pair's two values turn or stay together: 2 half is even)
+#pragma unroll
+    for (int i = 0; i < 8; i += 2) {
+        const int at = (i < 4 ? 0 : D / 2) + 4 * l + (i & 3);
+        if (TURN == kTurnHalves || at < 2 * half) {
+            add2(q.x[i], q.x[i + 1], __fmul_rn(q.x[i], t.c[i]), __fmul_rn(q.x[i + 1], t.c[i + 1]), __fmul_rn(partner[i], t.s[i]),
+                 __fmul_rn(partner[i + 1], t.s[i + 1]));
+        }
+    }
+}
+
+__device__ __forceinline__ float first_of_size(const float* x, uint32_t size) {
+    float v = x[3];
+#pragma unroll
+    for (int i = 2; i >= 0; --i)
+        if ((__float_as_uint(x[i]) & 0x7FFFFFFFu) == size) v = x[i];
+    return v;
 }
 
 // The scale (fp16 bits) of a group whose first largest-magnitude value is v.
@@ -367,7 +363,7 @@ __device__ __forceinline__ uint32_t scale_bits(float v) {
 }
 
 // Codes clamp(rint(x / d), -8, 7) + 8 of four values at places c0 .. c0 + 3 of a word.
-__device__ __forceinline__ uint32_t half_word(const float (&x)[4], uint32_t bits, int c0) {
+__device__ __forceinline__ uint32_t half_word(const float* x, uint32_t bits, int c0) {
     const float d = half_bits_to_float(bits);
     uint32_t w = 0;
 #pragma unroll
@@ -379,58 +375,51 @@ __device__ __forceinline__ uint32_t half_word(const float (&x)[4], uint32_t bits
     return w;
 }
 
-// The scales of the row's groups of 64 by pn4t's rule: group j is quarters
-// 4 j / NG .. of the row's lanes, in the order of quarters, then lanes.
+// The lanes' 64-value groups by pn4t's rule.  D >= 128: a group is 16 lanes'
+// first or second four values; D = 64: eight lanes' both.
 template <int D>
-__device__ __forceinline__ void group_scales(const Row& r, uint32_t (&bits)[D / 64]) {
-    constexpr int L = D / 16, NG = D / 64, kQuarters = 4 / NG;
+__device__ __forceinline__ void group_scales(const Quads& q, uint32_t (&bits)[2]) {
+    constexpr int kSpan = D == 64 ? 8 : 16;
     const int lane = threadIdx.x & 31;
-    const uint32_t members = ((1u << L) - 1u) << (lane / L * L);
+    const uint32_t members = ((1u << kSpan) - 1u) << (lane / kSpan * kSpan);
+    uint32_t top[2], best[2];
 #pragma unroll
-    for (int j = 0; j < NG; ++j) {
-        uint32_t top[kQuarters], best = 0;
+    for (int k = 0; k < 2; ++k) {
+        top[k] = 0;
 #pragma unroll
-        for (int k = 0; k < kQuarters; ++k) {
-            top[k] = 0;
+        for (int i = 0; i < 4; ++i) top[k] = max(top[k], __float_as_uint(q.x[4 * k + i]) & 0x7FFFFFFFu);
+        best[k] = top[k];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) top[k] = max(top[k], __float_as_uint(r.x[kQuarters * j + k][i]) & 0x7FFFFFFFu);
-            best = max(best, top[k]);
-        }
-#pragma unroll
-        for (int d = L / 2; d >= 1; d >>= 1) best = max(best, __shfl_xor_sync(0xFFFFFFFFu, best, d));
-        // the first quarter that has it, in it the first lane, in it the first value
-        float v = 0.0f;
-        bool found = false;
-#pragma unroll
-        for (int k = 0; k < kQuarters; ++k) {
-            const uint32_t has = __ballot_sync(0xFFFFFFFFu, top[k] == best) & members;
-            float mine = r.x[kQuarters * j + k][3];
-#pragma unroll
-            for (int i = 2; i >= 0; --i)
-                if ((__float_as_uint(r.x[kQuarters * j + k][i]) & 0x7FFFFFFFu) == best) mine = r.x[kQuarters * j + k][i];
-            const float first = __shfl_sync(0xFFFFFFFFu, mine, has ? __ffs(has) - 1 : lane);
-            if (has && !found) v = first;
-            found |= has != 0;
-        }
-        bits[j] = scale_bits(v);
+        for (int d = kSpan / 2; d >= 1; d >>= 1) best[k] = max(best[k], __shfl_xor_sync(0xFFFFFFFFu, best[k], d));
     }
+    if constexpr (D == 64) best[0] = best[1] = max(best[0], best[1]);
+    float v[2];
+    uint32_t has[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+        has[k] = __ballot_sync(0xFFFFFFFFu, top[k] == best[k]) & members;
+        v[k] = __shfl_sync(0xFFFFFFFFu, first_of_size(q.x + 4 * k, best[k]), has[k] ? __ffs(has[k]) - 1 : lane);
+    }
+    if constexpr (D == 64) v[0] = v[1] = has[0] ? v[0] : v[1];     // values 0 .. 31 come first
+    bits[0] = scale_bits(v[0]);
+    bits[1] = scale_bits(v[1]);
 }
 
 struct AppendParams {
     KvAppendArgs a;
     KvCache cache;
-    int q_sets, kv_sets;       // groups of heads (32 / (D / 16) each) per token, of q and of k or v
+    int q_sets, kv_sets;       // groups of heads (32 / (D / 8) each) per token, of q and of k or v
     int sets;                  // groups that one warp takes, of one kind
     int q_tasks, kv_tasks;     // warps per token, of q and of k or v
     int64_t tasks;             // warps' worth of work
     bool wide_q, wide_k, wide_v;
 };
 
-constexpr int kAppendWarps = 8;
+constexpr int kAppendWarps = 8, kAppendBlocks = 4;                // of a block, of an SM
 
 template <int D, bool F16, int TURN>
-__global__ void __launch_bounds__(kAppendWarps * 32, 2) append_kernel(const AppendParams P) {
-    constexpr int L = D / 16, kRows = 32 / L, NG = D / 64;         // lanes to a row, rows to a warp
+__global__ void __launch_bounds__(kAppendWarps * 32, kAppendBlocks) append_kernel(const AppendParams P) {
+    constexpr int L = D / 8, kRows = 32 / L;   // lanes to a row, rows to a warp
     __shared__ float rows[TURN == kTurnPart ? kAppendWarps : 1][kRows * D];
     const KvAppendArgs& a = P.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, l = lane % L, sub = lane / L;
@@ -447,71 +436,61 @@ __global__ void __launch_bounds__(kAppendWarps * 32, 2) append_kernel(const Appe
         const int set0 = kind * P.sets, set1 = min(set0 + P.sets, is_q ? P.q_sets : P.kv_sets);
         const void* src = is_q ? a.q : is_v ? a.v : a.k;
         const bool wide = is_q ? P.wide_q : is_v ? P.wide_v : P.wide_k;
-        const int64_t base = t * (is_q ? a.q_stride : is_v ? a.v_stride : a.k_stride) + 4 * l;
-        auto load = [&](Row& r, int set) {
+        const int64_t base = t * (is_q ? a.q_stride : is_v ? a.v_stride : a.k_stride);
+        auto load = [&](Quads& q, int set) {
             const int h = min(set * kRows + sub, heads - 1);               // rows past the last head repeat it
-#pragma unroll
-            for (int k = 0; k < 4; ++k) load_quad(src, base + h * D + k * (D / 4), F16, wide, r.x[k]);
+            load_quad(src, base + h * D + 4 * l, F16, wide, q.x);
+            load_quad(src, base + h * D + D / 2 + 4 * l, F16, wide, q.x + 4);
         };
-        Row next;
+        Quads next;
         load(next, set0);
         const float* weight = is_v ? nullptr : is_q ? a.q_weight : a.k_weight;
-        float w[4][4];
+        float w[8];
         if (weight) {
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) w[k][i] = weight[k * (D / 4) + 4 * l + i];
+            for (int i = 0; i < 8; ++i) w[i] = weight[(i < 4 ? 0 : D / 2) + 4 * l + (i & 3)];
         }
         bool turns = TURN != kTurnNone && !is_v;
-        Turn<D, TURN> tn;
+        Turn tn;
         if (turns) {
             const int pos = a.positions[t];
             turns = pos >= 0 && pos < a.table_rows;
-            if (turns) tn.load(a.cos + static_cast<int64_t>(pos) * a.half, a.sin + static_cast<int64_t>(pos) * a.half, a.half, l);
+            if (turns) load_turn<D, TURN>(tn, a.cos + static_cast<int64_t>(pos) * a.half, a.sin + static_cast<int64_t>(pos) * a.half, a.half, l);
         }
         uint2* to = reinterpret_cast<uint2*>(a.q_out + (t * a.heads + set0 * kRows + sub) * D + 4 * l);
         for (int set = set0; set < set1; ++set) {
-            Row r = next;
+            Quads q = next;
             if (set + 1 < set1) load(next, set + 1);
-            if (weight) norm_row<D>(r, w, a.eps);
-            if (turns) rotate_row<D, TURN>(r, tn, a.half, rows[TURN == kTurnPart ? warp : 0] + sub * D, l);
+            if (weight) norm_row<D>(q, w, a.eps);
+            if (turns) rotate_row<D, TURN>(q, tn, a.half, rows[TURN == kTurnPart ? warp : 0] + sub * D, l);
             const int h = set * kRows + sub;
             if (is_q) {
                 if (h < heads) {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const __half2 lo = __floats2half2_rn(r.x[k][0], r.x[k][1]), hi = __floats2half2_rn(r.x[k][2], r.x[k][3]);
-                        to[k * (D / 16)] = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
+                    for (int k = 0; k < 2; ++k) {
+                        const __half2 lo = __floats2half2_rn(q.x[4 * k], q.x[4 * k + 1]), hi = __floats2half2_rn(q.x[4 * k + 2], q.x[4 * k + 3]);
+                        to[k * (D / 8)] = make_uint2(*reinterpret_cast<const uint32_t*>(&lo), *reinterpret_cast<const uint32_t*>(&hi));
                     }
                 }
                 to += kRows * (D / 4);
                 continue;
             }
-            uint32_t bits[NG];
-            group_scales<D>(r, bits);
-            // two lanes to a word: the even one puts those of the first two quarters together, the odd one the others'
+            uint32_t bits[2];
+            group_scales<D>(q, bits);
+            // two lanes to a word: the even one puts the first half's together, the odd one the second's
             const bool odd = l & 1;
             const int c0 = odd ? 4 : 0;
-            uint32_t part[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k) part[k] = half_word(r.x[k], bits[k * NG / 4], c0);
-            uint32_t word[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-                word[k] = (odd ? part[2 + k] : part[k]) | __shfl_xor_sync(0xFFFFFFFFu, odd ? part[k] : part[2 + k], 1);
+            const uint32_t w0 = half_word(q.x, bits[0], c0), w1 = half_word(q.x + 4, bits[1], c0);
+            const uint32_t word = (odd ? w1 : w0) | __shfl_xor_sync(0xFFFFFFFFu, odd ? w0 : w1, 1);
             if (h < heads) {
                 uint8_t* rec = P.cache.record(slot, h);
                 const int tok = static_cast<int>(slot) & 15;
-#pragma unroll
-                for (int k = 0; k < 2; ++k) {
-                    const int at = (odd ? 2 + k : k) * (D / 4) + 4 * (l & ~1), j = at / 64, i = (at % 64) / 8;
-                    *reinterpret_cast<uint32_t*>(rec + (is_v ? kv_v_word<D>(tok, j, i) : kv_k_word<D>(tok, j, i))) = word[k];
-                }
-                if (l == 0) {
-                    uint16_t* sc = reinterpret_cast<uint16_t*>(rec + (is_v ? kv_v_scales(D) : kv_k_scales(D)) + tok * NG * 2);
-#pragma unroll
-                    for (int j = 0; j < NG; ++j) sc[j] = static_cast<uint16_t>(bits[j]);
+                const int at = (odd ? D / 2 : 0) + 4 * (l & ~1), j = at / 64, i = (at % 64) / 8;
+                *reinterpret_cast<uint32_t*>(rec + (is_v ? kv_v_word<D>(tok, j, i) : kv_k_word<D>(tok, j, i))) = word;
+                if (D == 64 ? l == 0 : l % 16 == 0) {
+                    uint8_t* sc = rec + (is_v ? kv_v_scales(D) : kv_k_scales(D)) + tok * (D / 64) * 2;
+                    *reinterpret_cast<uint16_t*>(sc + 2 * (4 * l / 64)) = static_cast<uint16_t>(bits[0]);
+                    if (D > 64) *reinterpret_cast<uint16_t*>(sc + 2 * ((D / 2 + 4 * l) / 64)) = static_cast<uint16_t>(bits[1]);
                 }
             }
         }
@@ -617,10 +596,11 @@ cudaError_t launch_kv_plan(const KvPlanArgs& a, int num_sms, cudaStream_t s) {
 cudaError_t launch_kv_append(const KvAppendArgs& a, const KvGeometry& g, int num_sms, cudaStream_t s) {
     AppendParams P{a, cache_of(g)};
     const int turn = a.half == 0 ? kTurnNone : a.interleaved ? kTurnNeighbours : a.half == g.D / 2 ? kTurnHalves : kTurnPart;
-    const int rows = 32 / (g.D / 16);
+    const int rows = 32 / (g.D / 8);
     P.q_sets = (a.heads + rows - 1) / rows;
     P.kv_sets = (g.heads + rows - 1) / rows;
-    // as many groups of heads to a warp as leave every SM 32 warps' worth, 8 at most
+    // as many groups of heads to a warp as leave every SM its 32 warps, 8 at most: what a task reads first (its
+    // slot or position, the rotation's row, the weights) costs it about four groups' time (1 group: 186 us, 4: 121)
     const int64_t all = a.tokens * (P.q_sets + 2 * static_cast<int64_t>(P.kv_sets));
     P.sets = 1;
     while (P.sets < 8 && all >= static_cast<int64_t>(num_sms) * 32 * P.sets * 2) P.sets *= 2;
@@ -632,7 +612,9 @@ cudaError_t launch_kv_append(const KvAppendArgs& a, const KvGeometry& g, int num
     P.wide_k = rows_aligned(a.k, a.k_stride, size, 4 * size);
     P.wide_v = rows_aligned(a.v, a.v_stride, size, 4 * size);
     int64_t blocks = (P.tasks + kAppendWarps - 1) / kAppendWarps;
-    if (blocks > (1 << 30)) blocks = 1 << 30;
+    // warps that take the next task when they are through with one: 85 us for 8192 tokens of 48 + 16 heads of 128,
+    // where a block to every eight tasks (which waits for its longest) takes 89 us
+    if (blocks > static_cast<int64_t>(num_sms) * kAppendBlocks) blocks = static_cast<int64_t>(num_sms) * kAppendBlocks;
     const int grid = static_cast<int>(blocks);
     if (g.D == 64) append<64>(P, turn, grid, s);
     else if (g.D == 128) append<128>(P, turn, grid, s);

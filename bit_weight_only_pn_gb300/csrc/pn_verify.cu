@@ -47,7 +47,8 @@ __device__ __forceinline__ int64_t weight(const Row& r, int j) {
     return j == r.skip ? 0 : whole(p);
 }
 
-// Weights are summed without 64-bit conversions (a fifth of the time): with t =
+// Weights are summed without 64-bit conversions (a third of the time: 64 requests of
+// 151936 tokens 20 us, with them 30): with t =
 // 2^21 w, a = rint(t) by adding 1.5 2^23 and the rest t - a, which is exact, times
 // 2^21 rounded the same way, whole(w) = 2^21 a + rint(2^21 (t - a)) -- the first
 // part is even, so ties go as in one rounding -- and both parts of up to 512
