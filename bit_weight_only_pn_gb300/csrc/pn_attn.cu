@@ -140,8 +140,9 @@ constexpr int kPiece = 8 * NT * (D + 2);
 template <int D, int NT>
 struct Smem {
     static constexpr int kRT = 8 * NT;
-    // consumer warps; with the producer 16 at 128 registers where these suffice (8 rows, D <= 128), else 8
-    static constexpr int kWarps = NT == 1 && D <= 128 ? 15 : 7;
+    // consumer warps: with the producer 16 at 128 registers where these suffice (8 rows, D <= 128), 12 at 168 for 16 rows
+    // of D = 64 (24 requests of 4096 tokens, 8 heads: 35 us, with 8 warps 40), else 8 (12 do not make 16 rows of 128 faster)
+    static constexpr int kWarps = D == 256 ? 7 : NT == 1 ? 15 : D == 64 ? 11 : 7;
     static constexpr int kThreads = (kWarps + 1) * 32;
     static constexpr int kDepth = D == 256 ? 2 : D == 128 && NT == 1 ? 3 : 4;      // stages per warp
     static constexpr int kWarpRing = kDepth * Shape<D>::kStage;
@@ -1023,7 +1024,7 @@ size_t attn_workspace_bytes(int num_sms) {
 bool attn_fits(const AttnArgs& a, const KvGeometry& g) {
     const int64_t rows = static_cast<int64_t>(a.max_queries) * (a.heads / g.heads), per = g.D < 256 && rows > 8 ? 16 : 8;
     const double units = static_cast<double>(a.batch) * g.heads * static_cast<double>((rows + per - 1) / per) *
-                         static_cast<double>((static_cast<int64_t>(a.max_pages) * g.page_size + kTile - 1) / kTile);
+                         static_cast<double>((static_cast<int64_t>(a.max_pages) * g.page_size + kTile - 1) / kTile + kSegmentUnits);
     return units < 4294967296.0;
 }
 

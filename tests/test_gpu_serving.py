@@ -566,3 +566,63 @@ def test_verify_refusals(pn):
     assert e.value.status == 1
     a, o = pn.verify(t[:0], p[:0], None, u[:0])
     assert a.shape == (0,) and o.shape == (0, 4)
+
+
+# ------------------------------------------------- large batches, far addresses --
+@pytest.mark.parametrize("batch,D,queries", [(9001, 128, 1), (16384, 128, 1), (16384, 64, 12), (16384, 256, 1), (16384, 128, 60)])
+def test_attention_many_requests(pn, batch, D, queries):
+    """Batches whose prefix sums take shared memory from the stages: one request in eight has 1 to 3 tokens, the last `queries`."""
+    rng = np.random.default_rng(batch + D)
+    lens = rng.integers(1, 4, batch) * (rng.random(batch) < 0.125)
+    lens[-1] = 70
+    counts = [int(x > 0) for x in lens]
+    counts[-1] = queries
+    case = attention_case([int(x) for x in lens], counts, 2, 1, D, 16)
+    ws = pn.AttentionWorkspace()
+    check_attention(pn, case, queries, 1 / math.sqrt(D), workspace=ws)
+
+
+@pytest.mark.parametrize("D,queries", [(128, 1), (128, 8), (128, 70), (256, 3)])
+def test_far_pages(pn, D, queries):
+    """A cache of more than 2^32 bytes: what is written to its last pages reads back, and attends, as in a small one."""
+    kv, heads, page, tokens = 8, 16, 1024, 1500
+    page_bytes = kv * page // 16 * 17 * D
+    pages = (1 << 32) // page_bytes + 40
+    g = torch.Generator(device="cuda").manual_seed(D)
+    q, k, v = (torch.randn(tokens, h, D, device="cuda", generator=g) for h in (heads, kv, kv))
+    place = torch.arange(tokens, device="cuda")
+    near, far = pn.kv_cache(2, page, kv, D), pn.kv_cache(pages, page, kv, D)
+    q_near = pn.kv_append(q, k, v, near, place)
+    q_far = pn.kv_append(q, k, v, far, place + (pages - 2) * page)
+    assert torch.equal(q_near, q_far)
+    for a, b in zip(pn.kv_read(near, place), pn.kv_read(far, place + (pages - 2) * page)):
+        assert torch.equal(a, b)
+    assert not far[:pages - 2].any()
+    lens = torch.tensor([tokens], dtype=torch.int32, device="cuda")
+    starts = torch.tensor([0, queries], dtype=torch.int32, device="cuda")
+    tables = [torch.tensor([[p, p + 1]], dtype=torch.int32, device="cuda") for p in (0, pages - 2)]
+    got = [pn.attention(q_near[-queries:], c, t, lens, starts, queries, 0.1, return_lse=True) for c, t in zip((near, far), tables)]
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+def test_attention_too_many_units(pn):
+    """Shapes whose bound on the work passes 32 bits are refused before anything is launched."""
+    q, cache, table, lens, starts = (cuda(x) for x in attention_case([20], [1], 8, 8, 256, 16)[:5])
+    many = torch.zeros(16384, dtype=torch.int32, device="cuda")
+    table = torch.zeros(16384, 2, dtype=torch.int32, device="cuda")
+    with pytest.raises(pn.PnError) as e:             # 16384 requests, 8 heads, 2^14 groups of 8 rows: a unit and one more for each
+        pn.attention(q, cache, table, many, torch.zeros(16385, dtype=torch.int32, device="cuda"), 1 << 17, 0.1)
+    assert e.value.status == 3
+
+
+@pytest.mark.parametrize("vocab", [(1 << 20) - 3, 1 << 20])
+def test_verify_largest_vocabulary(pn, vocab):
+    """Weights of 1 and above in every place: the sums at their bound."""
+    target = np.full((2, 2, vocab), 1.0, np.float32)
+    target[1] = 2.0
+    target[1, :, ::3] = 0.7
+    tokens = np.array([[3], [vocab - 1]], np.int32)
+    uniforms = np.array([[0.5, 0.9999], [0.5, 0.31]], np.float32)
+    got = pn.verify(cuda(tokens), cuda(target), None, cuda(uniforms))
+    want = ref.verify(tokens, target, None, uniforms, None)
+    assert np.array_equal(got[0].cpu().numpy(), want[0]) and np.array_equal(got[1].cpu().numpy(), want[1])
