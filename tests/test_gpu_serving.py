@@ -275,6 +275,10 @@ def attention_case(lens, counts, heads, kv, D, page, seed=0, k_size=1.0, v_size=
     for b, n in enumerate(lens):
         own = order[at:at + held[b]]
         at += held[b]
+        if n == 0:
+            ks.append(np.zeros((0, kv, D)))
+            vs.append(np.zeros((0, kv, D)))
+            continue
         table[b, :held[b]] = own
         k = (k_size * rng.standard_normal((n, kv, D))).astype(np.float32)
         v = (v_size * rng.standard_normal((n, kv, D)) * 2.0 ** rng.integers(-2, 3, (n, 1, 1))).astype(np.float32)
