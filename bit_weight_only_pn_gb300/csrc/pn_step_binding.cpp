@@ -3,7 +3,7 @@
 //
 // A step makes these calls for every token, so what they cost on the host
 // counts: through ctypes and Python checks a plan with its eight outputs took
-// 42 us and a verification 17 us of host time on the GPU's Arm host, where the
+// 42 us and a verification 17 us of host time on an Arm host, where the
 // C calls themselves take 4 us (launch included).  pn.py keeps the signatures,
 // defaults and documentation; each function here takes their arguments by
 // position and returns (status, outputs...), status as in pn.h.
