@@ -10,7 +10,8 @@
 #include <Python.h>
 
 #include <ATen/core/Tensor.h>
-#include <ATen/ops/empty.h>
+#include <ATen/EmptyTensor.h>
+#include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/autograd/python_variable.h>
@@ -122,15 +123,18 @@ struct Cache {
     }
 };
 
-at::Tensor fresh(at::IntArrayRef size, at::ScalarType type, const at::Tensor& like) {
-    return at::empty(size, at::TensorOptions().dtype(type).device(like.device()));
+// A new tensor on the current device (the guard's), as at::empty makes it for a CUDA
+// device, without the dispatcher on the way.
+at::Tensor fresh(at::IntArrayRef size, at::ScalarType type) {
+    return at::detail::empty_generic(size, c10::cuda::CUDACachingAllocator::get(), c10::DispatchKeySet(c10::DispatchKey::CUDA), type, std::nullopt);
 }
 
-// `n` entries from `at` on of a one-dimensional tensor of ours: another tensor on
-// the same memory (an allocation takes more than a microsecond).
-at::Tensor part_of(const at::Tensor& t, int64_t at, int64_t n) {
-    auto impl = c10::make_intrusive<c10::TensorImpl>(c10::Storage(t.storage()), t.key_set(), t.dtype());
-    impl->set_storage_offset(at);
+// `n` entries from byte `at` on of a tensor of ours: another tensor on the same
+// memory (an allocation takes more than a microsecond).
+at::Tensor part_of(const at::Tensor& t, int64_t at, int64_t n, at::ScalarType type) {
+    const caffe2::TypeMeta meta = c10::scalarTypeToTypeMeta(type);
+    auto impl = c10::make_intrusive<c10::TensorImpl>(c10::Storage(t.storage()), t.key_set(), meta);
+    impl->set_storage_offset(at / static_cast<int64_t>(meta.itemsize()));
     impl->set_sizes_contiguous({n});
     return at::Tensor(std::move(impl));
 }
@@ -178,12 +182,9 @@ PyObject* kv_plan(PyObject* const* a) {
     PyObject* given[8];
     const bool have = a[8] != Py_None;
     if (have && (!PyTuple_Check(a[8]) || PyTuple_GET_SIZE(a[8]) != 8)) fail(PyExc_TypeError, "%s must be a KvPlan", "out");
-    at::Tensor wide, narrow;
-    int64_t wide_at = 0, narrow_at = 0;
-    if (!have) {
-        wide = fresh({T + 2}, at::kLong, lens);
-        narrow = fresh({2 * T + 3 * B + 2}, at::kInt, lens);
-    }
+    at::Tensor all;                            // 64-bit outputs first
+    int64_t wide_at = 0, narrow_at = (T + 2) * 8;
+    if (!have) all = fresh({narrow_at + (2 * T + 3 * B + 2) * 4}, at::kByte);
     for (int i = 0; i < 8; ++i) {
         const at::ScalarType type = i == 0 || i == 6 ? at::kLong : at::kInt;
         given[i] = have ? PyTuple_GET_ITEM(a[8], i) : Py_None;
@@ -192,8 +193,8 @@ PyObject* kv_plan(PyObject* const* a) {
             if (o[i].numel() != sizes[i]) fail(PyExc_ValueError, "%s has another size", names[i]);
         } else {
             int64_t& from = type == at::kLong ? wide_at : narrow_at;
-            o[i] = part_of(type == at::kLong ? wide : narrow, from, sizes[i]);
-            from += sizes[i];
+            o[i] = part_of(all, from, sizes[i], type);
+            from += sizes[i] * (type == at::kLong ? 8 : 4);
         }
     }
     const pn_status st = pn_kv_plan(data<int32_t>(&lens), data<int32_t>(&add), data<int32_t>(&held), static_cast<int>(B), data<int32_t>(&table),
@@ -238,7 +239,7 @@ PyObject* kv_append(PyObject* const* a) {
     at::Tensor out;
     if (q) {
         const at::Tensor* given = optional(a[12], at::kHalf, T * heads * c.dim, "q_out", "[tokens][heads][head_dim]");
-        out = given ? *given : fresh({T, heads, c.dim}, at::kHalf, k);
+        out = given ? *given : fresh({T, heads, c.dim}, at::kHalf);
     }
     const pn_status st = pn_kv_append(data<void>(q), q ? row_stride(*q) : 0, data<void>(&k), row_stride(k), data<void>(&v), row_stride(v),
                                       type == at::kFloat ? PN_DTYPE_F32 : PN_DTYPE_F16, T, static_cast<int>(heads), data<float>(qw),
@@ -256,8 +257,8 @@ PyObject* kv_read(PyObject* const* a) {
     const c10::cuda::CUDAGuard guard(slots.device());
     const at::Tensor* gk = optional(a[2], at::kFloat, n, "out", "two tensors [tokens][kv_heads][head_dim]");
     const at::Tensor* gv = optional(a[3], at::kFloat, n, "out", "two tensors [tokens][kv_heads][head_dim]");
-    const at::Tensor k = gk ? *gk : fresh({T, c.heads, c.dim}, at::kFloat, slots);
-    const at::Tensor v = gv ? *gv : fresh({T, c.heads, c.dim}, at::kFloat, slots);
+    const at::Tensor k = gk ? *gk : fresh({T, c.heads, c.dim}, at::kFloat);
+    const at::Tensor v = gv ? *gv : fresh({T, c.heads, c.dim}, at::kFloat);
     const pn_status st = pn_kv_read(c.t.data_ptr(), c.pages, c.page_size, c.heads, c.dim, data<int64_t>(&slots), T, data<float>(&k),
                                     data<float>(&v), stream_of(slots));
     return answer(st, {given_or(a[2], k), given_or(a[3], v)});
@@ -284,10 +285,10 @@ PyObject* attention(PyObject* const* a) {
     if (!workspace && PyErr_Occurred()) throw PythonError{};
     const int64_t bytes = whole(a[13]);
     const c10::cuda::CUDAGuard guard(q.device());
-    const at::Tensor out = given ? *given : fresh({T, heads, c.dim}, at::kHalf, q);
+    const at::Tensor out = given ? *given : fresh({T, heads, c.dim}, at::kHalf);
     at::Tensor made;
     if (!lse && want_lse) {
-        made = fresh({T, heads}, at::kFloat, q);
+        made = fresh({T, heads}, at::kFloat);
         lse = &made;
     }
     const pn_status st = pn_attention(data<uint16_t>(&q), row_stride(q), T, static_cast<int>(heads), c.t.data_ptr(), c.pages, c.page_size,
@@ -318,8 +319,8 @@ PyObject* verify(PyObject* const* a) {
     const at::Tensor* given_accepted = optional(a[5], at::kInt, B, "accepted", "[batch]");
     const at::Tensor* given_out = optional(a[6], at::kInt, B * (K + 1), "out", "[batch][drafts + 1]");
     const c10::cuda::CUDAGuard guard(target.device());
-    const at::Tensor accepted = given_accepted ? *given_accepted : fresh({B}, at::kInt, target);
-    const at::Tensor out = given_out ? *given_out : fresh({B, K + 1}, at::kInt, target);
+    const at::Tensor accepted = given_accepted ? *given_accepted : fresh({B}, at::kInt);
+    const at::Tensor out = given_out ? *given_out : fresh({B, K + 1}, at::kInt);
     const pn_status st = pn_verify(data<int32_t>(&tokens), data<float>(&target), V, data<float>(draft), V, data<float>(&uniforms),
                                    data<int32_t>(counts), static_cast<int>(B), static_cast<int>(K), static_cast<int>(V),
                                    data<int32_t>(&accepted), data<int32_t>(&out), stream_of(target));
