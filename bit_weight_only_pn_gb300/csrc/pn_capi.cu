@@ -552,7 +552,7 @@ pn_status pn_kv_plan(const int32_t* lens, const int32_t* add, const int32_t* hel
                      int32_t* starts, int32_t* lens_out, int32_t* held_out, int64_t* ring_out, int32_t* refused,
                      pn_stream stream) {
     if (batch < 1 || batch > pn::kKvMaxBatch || max_pages < 1 || table_stride < max_pages || pages < 1 ||
-        pages > INT32_MAX || !page_size_ok(page_size) || capacity < 0 || capacity > INT32_MAX ||
+        pages > INT32_MAX || !page_size_ok(page_size) || capacity < 0 || capacity > INT32_MAX - 16 ||
         static_cast<int64_t>(max_pages) * page_size > INT32_MAX)
         return PN_EINVAL;
     if (!lens || !add || !held || !table || !free_pages || !ring || !starts || !lens_out || !held_out || !ring_out ||

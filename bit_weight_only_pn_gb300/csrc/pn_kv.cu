@@ -19,49 +19,61 @@ namespace {
 // pages taken (a request that would pass the free pages takes none) and pages
 // given back.  Every block scans all requests by itself (a few KB from L2)
 // instead of waiting for another block, keeps the result in shared memory and
-// then fills its share of the maps and of the table; block 0 writes the
-// per-request outputs.  Nothing is read that any block writes: taken pages
-// come from the ring's [head, tail), given ones go behind its tail, table
-// entries are read below `held` and written from it on.
+// then fills its share of the maps, of the table and of the per-request outputs
+// (these by block 0 alone cost 2 us).  Nothing is read that any block writes:
+// taken pages come from the ring's [head, tail), given ones go behind its tail,
+// table entries are read below `held` and written from it on.
+//
+// 4096 requests, 160000 slots: 7.4 us; 8 requests 3.5 us.  Bound by the chain of
+// loads, scans and instructions that every block goes through (about 8000 cycles
+// of 14000) and by the slot maps' loads behind it.
 
 constexpr int kPlanThreads = 1024;
 
-struct Scan3 {
-    int64_t tok, need, back;
-};
-__device__ __forceinline__ Scan3 add3(const Scan3& a, const Scan3& b) {
-    return {a.tok + b.tok, a.need + b.need, a.back + b.back};
-}
-__device__ __forceinline__ Scan3 shfl_up3(const Scan3& v, int d) {
-    return {__shfl_up_sync(0xFFFFFFFFu, v.tok, d), __shfl_up_sync(0xFFFFFFFFu, v.need, d),
-            __shfl_up_sync(0xFFFFFFFFu, v.back, d)};
-}
+// Counts are 32 bits wide and stop at kMost (every block works through all
+// requests, and in 64 bits that arithmetic was half its time): what passes it
+// passes every capacity and every number of pages, which are below.
+constexpr uint32_t kMost = 0x7FFFFFF0u;
+__device__ __forceinline__ uint32_t sum_to_most(uint32_t a, uint32_t b) { return min(a + b, kMost); }
 
-// Exclusive prefix over the block's threads; *total gets the sum.  `part`
-// holds one entry per warp; the caller synchronises before part is reused.
-__device__ Scan3 block_scan(Scan3 v, Scan3* part, Scan3* total) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    Scan3 in = v;
+// Exclusive prefix over the block's threads of N counts; total gets the sums.
+// `part` holds N entries per warp; the caller synchronises before it is reused.
+template <int N>
+__device__ __forceinline__ void block_scan(uint32_t (&v)[N], uint32_t* part, uint32_t (&total)[N]) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    uint32_t in[N];
 #pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const Scan3 o = shfl_up3(in, d);
-        if (lane >= d) in = add3(in, o);
-    }
-    if (lane == 31) part[warp] = in;
+    for (int k = 0; k < N; ++k) in[k] = v[k];
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1)
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, in[k], d);
+            if (lane >= d) in[k] = sum_to_most(in[k], o);
+        }
+    if (lane == 31)
+#pragma unroll
+        for (int k = 0; k < N; ++k) part[k * 32 + warp] = in[k];
     __syncthreads();
     if (warp == 0) {
-        Scan3 w = lane < static_cast<int>(blockDim.x >> 5) ? part[lane] : Scan3{0, 0, 0};
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const Scan3 o = shfl_up3(w, d);
-            if (lane >= d) w = add3(w, o);
+        for (int k = 0; k < N; ++k) {
+            uint32_t w = lane < warps ? part[k * 32 + lane] : 0u;
+#pragma unroll
+            for (int d = 1; d < 32; d <<= 1) {
+                const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, w, d);
+                if (lane >= d) w = sum_to_most(w, o);
+            }
+            part[k * 32 + lane] = w;
         }
-        part[lane] = w;
     }
     __syncthreads();
-    *total = part[(blockDim.x >> 5) - 1];
-    const Scan3 ex = {in.tok - v.tok, in.need - v.need, in.back - v.back};
-    return warp ? add3(part[warp - 1], ex) : ex;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        total[k] = part[k * 32 + warps - 1];
+        const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, in[k], 1);
+        v[k] = sum_to_most(lane ? o : 0u, warp ? part[k * 32 + warp - 1] : 0u);
+    }
 }
 
 __device__ __forceinline__ int64_t wrap(int64_t i, int64_t n) {
@@ -75,9 +87,12 @@ struct PlanParams {
     int each;                  // requests per thread of the scan
 };
 
-__global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams P) {
+// KEEP: a thread's requests where they stay in registers (read once, all loads on
+// their way together), 0 where they are too many and are read in each pass.
+template <int KEEP>
+__global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const PlanParams P) {
     extern __shared__ int plan_smem[];
-    __shared__ Scan3 part[32];
+    __shared__ uint32_t part[2 * 32];
     const KvPlanArgs& a = P.a;
     int* starts = plan_smem;                   // [batch + 1]
     int* first = plan_smem + a.batch + 1;      // [batch]: >= 0 the request's first page of the ring, -1 refused, <= -2 given back
@@ -85,78 +100,86 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams P) 
     const int b0 = min(tid * P.each, a.batch), b1 = min(b0 + P.each, a.batch);
     // whatever the ring holds, no index leaves it
     const int64_t ring_head = a.ring[0], tail = a.ring[1];
-    const int64_t avail = min(max(tail - ring_head, static_cast<int64_t>(0)), a.pages);
-    const int64_t head = wrap(ring_head, a.pages);
-    auto free_page = [&](int64_t i) -> int32_t {          // i < avail <= pages
-        const int64_t at = head + i;
-        return a.free_pages[at >= a.pages ? at - a.pages : at];
+    const uint32_t avail = static_cast<uint32_t>(min(max(tail - ring_head, static_cast<int64_t>(0)), min(a.pages, static_cast<int64_t>(kMost - 1))));
+    const uint32_t pages = static_cast<uint32_t>(a.pages), head = static_cast<uint32_t>(wrap(ring_head, a.pages));
+    auto free_page = [&](uint32_t i) -> int32_t {         // i < avail <= pages
+        const uint32_t at = head + i;
+        return a.free_pages[at >= pages ? at - pages : at];
+    };
+    struct Item { int add, held, len; };
+    auto read = [&](int b) -> Item { return {a.add[b], min(max(a.held[b], 0), a.max_pages), max(a.lens[b], 0)}; };
+    Item kept[KEEP ? KEEP : 1];
+    if constexpr (KEEP > 0) {
+#pragma unroll
+        for (int i = 0; i < KEEP; ++i) kept[i] = b0 + i < b1 ? read(b0 + i) : Item{0, 0, 0};
+    }
+    auto each_request = [&](auto f) {
+        if constexpr (KEEP > 0) {
+#pragma unroll
+            for (int i = 0; i < KEEP; ++i)
+                if (b0 + i < b1) f(b0 + i, kept[i]);
+        } else {
+#pragma unroll 4
+            for (int b = b0; b < b1; ++b) f(b, read(b));
+        }
     };
 
     // tokens and pages given back
-    Scan3 mine{0, 0, 0}, total;
-    for (int b = b0; b < b1; ++b) {
-        const int add = a.add[b];
-        if (add < 0) mine.back += min(max(a.held[b], 0), a.max_pages);
-        else mine.tok += add;
-    }
-    const Scan3 at = block_scan(mine, part, &total);
-    const int64_t tokens = total.tok, given = total.back;
+    uint32_t mine[2] = {0, 0}, total[2];
+    each_request([&](int, const Item& q) {
+        mine[0] = sum_to_most(mine[0], max(q.add, 0));
+        mine[1] = sum_to_most(mine[1], q.add < 0 ? q.held : 0);
+    });
+    block_scan(mine, part, total);
+    const uint32_t tokens = total[0], given = total[1];
     __syncthreads();
     // pages taken by the requests that fit the table and the maps
-    auto need_of = [&](int b, int64_t end) -> int64_t {   // -1: does not fit
-        const int64_t want = (static_cast<int64_t>(max(a.lens[b], 0)) + a.add[b] + a.page_size - 1) >> P.shift;
-        if (want > a.max_pages || end > a.capacity) return -1;
-        return max(want - min(max(a.held[b], 0), a.max_pages), static_cast<int64_t>(0));
+    auto need_of = [&](const Item& q, uint32_t end) -> int {      // -1: does not fit
+        const uint32_t len = static_cast<uint32_t>(q.len) + static_cast<uint32_t>(q.add);
+        const uint32_t want = (len >> P.shift) + ((len & (a.page_size - 1)) != 0);
+        if (want > static_cast<uint32_t>(a.max_pages) || end > static_cast<uint32_t>(a.capacity)) return -1;
+        return max(static_cast<int>(want) - q.held, 0);
     };
-    Scan3 need{0, 0, 0};
-    int64_t tok = at.tok;
-    for (int b = b0; b < b1; ++b) {
-        if (a.add[b] < 0) continue;
-        tok += a.add[b];
-        need.need += max(need_of(b, tok), static_cast<int64_t>(0));
-    }
-    const Scan3 before = block_scan(need, part, &total);
-    tok = at.tok;
-    int64_t taken = before.need, back = at.back;
-    int refused = 0;
-    int64_t served_need = 0;
-    const bool writer = blockIdx.x == 0;
-    for (int b = b0; b < b1; ++b) {
-        const int add = a.add[b];
-        const int start = static_cast<int>(min(tok, static_cast<int64_t>(INT32_MAX)));
+    uint32_t need[1] = {0}, all_need[1];
+    uint32_t tok = mine[0];
+    each_request([&](int, const Item& q) {
+        if (q.add < 0) return;
+        tok = sum_to_most(tok, q.add);
+        need[0] = sum_to_most(need[0], max(need_of(q, tok), 0));
+    });
+    block_scan(need, part, all_need);
+    tok = mine[0];
+    uint32_t taken = need[0], back = mine[1];
+    uint32_t counts[2] = {0, 0};               // refused requests, pages that the others take
+    // every block knows all per-request outputs and writes those of a few of its threads
+    const bool writer = static_cast<uint32_t>(tid) * gridDim.x / blockDim.x == blockIdx.x;
+    each_request([&](int b, const Item& q) {
+        const int start = static_cast<int>(tok);
         starts[b] = start;
-        const int held = min(max(a.held[b], 0), a.max_pages), len = max(a.lens[b], 0);
         int lens_out = 0, held_out = 0;
-        if (add < 0) {
-            first[b] = static_cast<int>(-2 - back);
-            back += held;
+        if (q.add < 0) {
+            first[b] = -2 - static_cast<int>(back);
+            back = sum_to_most(back, q.held);
         } else {
-            tok += add;
-            const int64_t n = need_of(b, tok);
-            const bool ok = n == 0 || (n > 0 && taken + n <= avail);
+            tok = sum_to_most(tok, q.add);
+            const int n = need_of(q, tok);
+            const uint32_t upto = sum_to_most(taken, max(n, 0));
+            const bool ok = n == 0 || (n > 0 && upto <= avail);
             first[b] = ok ? static_cast<int>(taken) : -1;
-            taken += max(n, static_cast<int64_t>(0));
-            served_need += ok ? n : 0;
-            refused += !ok;
-            lens_out = ok ? len + add : len;
-            held_out = held + (ok ? static_cast<int>(n) : 0);
+            taken = upto;
+            counts[0] += !ok;
+            counts[1] += ok ? n : 0;
+            lens_out = ok ? q.len + q.add : q.len;
+            held_out = q.held + (ok ? n : 0);
         }
         if (writer) {
             a.starts[b] = start;
             a.lens_out[b] = lens_out;
             a.held_out[b] = held_out;
         }
-    }
+    });
+    if (tid == 0) starts[a.batch] = static_cast<int>(tokens);
     __syncthreads();                           // part is free again; starts and first are complete
-    if (tid == 0) starts[a.batch] = static_cast<int>(min(tokens, static_cast<int64_t>(INT32_MAX)));
-    const Scan3 unused = block_scan(Scan3{refused, served_need, 0}, part, &total);
-    (void)unused;
-    if (writer && tid == 0) {
-        a.starts[a.batch] = starts[a.batch];
-        a.ring_out[0] = ring_head + total.need;
-        a.ring_out[1] = tail + given;
-        a.refused[0] = static_cast<int>(total.tok);
-    }
 
     // table entries and returned pages: one warp per request
     const int warps = blockDim.x >> 5;
@@ -167,38 +190,63 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams P) 
         int32_t* row = a.table + static_cast<int64_t>(b) * a.table_stride;
         if (f >= 0) {
             const int64_t want = (static_cast<int64_t>(max(a.lens[b], 0)) + a.add[b] + a.page_size - 1) >> P.shift;
-            for (int64_t i = held + (tid & 31); i < want; i += 32) row[i] = free_page(f + i - held);
+            for (int64_t i = held + (tid & 31); i < want; i += 32) row[i] = free_page(static_cast<uint32_t>(f + i - held));
         } else {
             const int64_t to = tail + (-2 - static_cast<int64_t>(f));
             for (int i = tid & 31; i < held; i += 32) a.free_pages[wrap(to + i, a.pages)] = row[i];
         }
     }
 
-    // slot maps: the request of a token by binary search in starts
-    const int64_t stride = static_cast<int64_t>(gridDim.x) * blockDim.x;
-    for (int64_t t = static_cast<int64_t>(blockIdx.x) * blockDim.x + tid; t < a.capacity; t += stride) {
+    // Slot maps.  A warp has 32 tokens in a row: it finds the last request whose
+    // start is at most the first token's (those that add nothing share the next
+    // one's) with a lane to a probe, and from there each lane its own.
+    const uint32_t capacity = static_cast<uint32_t>(a.capacity), stride = gridDim.x * blockDim.x;
+    for (uint32_t t0 = blockIdx.x * blockDim.x + (tid & ~31); t0 < capacity; t0 += stride) {
+        const uint32_t t = t0 + (tid & 31);
+        int req = -1, pos = -1;
         int64_t slot = -1;
-        int pos = -1, req = -1;
-        if (t < tokens) {
-            int lo = 0, hi = a.batch - 1;      // the last request whose start is <= t (those that add nothing share the next one's)
-            while (lo < hi) {
-                const int mid = (lo + hi + 1) >> 1;
-                if (starts[mid] <= t) lo = mid;
-                else hi = mid - 1;
+        if (t0 < tokens) {                     // (the whole warp)
+            int lo = 0;                        // starts[lo] <= t0; none that is has an index of lo + span or above
+            for (int span = a.batch; span > 1;) {
+                const int step = (span + 31) / 32, at = lo + (tid & 31) * step;
+                const uint32_t below = __ballot_sync(0xFFFFFFFFu, at < a.batch && at < lo + span && static_cast<uint32_t>(starts[min(at, a.batch)]) <= t0);
+                const int k = 31 - __clz(below);
+                span = min(step, lo + span - (lo + k * step));
+                lo += k * step;
             }
-            req = lo;
-            if (first[lo] >= 0) {
-                pos = max(a.lens[lo], 0) + static_cast<int>(t - starts[lo]);
-                const int held = min(max(a.held[lo], 0), a.max_pages);
-                const int pg = pos >> P.shift;
-                const int32_t page = pg < held ? a.table[lo * a.table_stride + pg]
-                                               : free_page(static_cast<int64_t>(first[lo]) + pg - held);
-                slot = (static_cast<int64_t>(page) << P.shift) + (pos & (a.page_size - 1));
+            int up = 1;                        // doubling steps, then halving ones
+            while (lo + up < a.batch && static_cast<uint32_t>(starts[lo + up]) <= t) {
+                lo += up;
+                up *= 2;
+            }
+            for (; up >= 1; up /= 2)
+                if (lo + up < a.batch && static_cast<uint32_t>(starts[lo + up]) <= t) lo += up;
+            if (t < tokens) {
+                req = lo;
+                const int f = first[lo];
+                if (f >= 0) {
+                    pos = max(a.lens[lo], 0) + static_cast<int>(t - starts[lo]);
+                    const int held = min(max(a.held[lo], 0), a.max_pages), pg = pos >> P.shift;
+                    const int32_t page = pg < held ? a.table[lo * a.table_stride + pg] : free_page(static_cast<uint32_t>(f + pg - held));
+                    slot = (static_cast<int64_t>(page) << P.shift) + (pos & (a.page_size - 1));
+                }
             }
         }
-        a.slots[t] = slot;
-        a.positions[t] = pos;
-        a.requests[t] = req;
+        if (t < capacity) {
+            a.slots[t] = slot;
+            a.positions[t] = pos;
+            a.requests[t] = req;
+        }
+    }
+    // the first block's totals, which no other needs
+    if (blockIdx.x != 0) return;
+    __syncthreads();
+    block_scan(counts, part, total);
+    if (tid == 0) {
+        a.starts[a.batch] = starts[a.batch];
+        a.ring_out[0] = ring_head + total[1];
+        a.ring_out[1] = tail + given;
+        a.refused[0] = static_cast<int>(total[0]);
     }
 }
 
@@ -580,17 +628,23 @@ cudaError_t launch_kv_plan(const KvPlanArgs& a, int num_sms, cudaStream_t s) {
     const int threads = a.batch <= 256 && a.capacity <= 1024 ? 256 : kPlanThreads;
     P.each = (a.batch + threads - 1) / threads;
     const int smem = (2 * a.batch + 1) * 4;
-    static std::atomic<uint64_t> smem_set{0};
-    if (smem > 40 * 1024)
-        if (cudaError_t e = set_smem_limit_once(plan_kernel, (2 * kKvMaxBatch + 1) * 4, smem_set); e != cudaSuccess) return e;
     // a token to a thread and, for the table, a request to a warp, as far as one wave of blocks goes
     int64_t blocks = (a.capacity + threads - 1) / threads;
     const int64_t by_request = (a.batch + threads / 32 - 1) / (threads / 32);
     blocks = blocks > by_request ? blocks : by_request;
     if (blocks > num_sms) blocks = num_sms;
     if (blocks < 1) blocks = 1;
-    plan_kernel<<<static_cast<int>(blocks), threads, smem, s>>>(P);
-    return cudaGetLastError();
+    auto run = [&](auto keep) {
+        constexpr int kKeep = decltype(keep)::value;
+        static std::atomic<uint64_t> smem_set{0};
+        if (smem > 40 * 1024)
+            if (cudaError_t e = set_smem_limit_once(plan_kernel<kKeep>, (2 * kKvMaxBatch + 1) * 4, smem_set); e != cudaSuccess) return e;
+        plan_kernel<kKeep><<<static_cast<int>(blocks), threads, smem, s>>>(P);
+        return cudaGetLastError();
+    };
+    if (P.each == 1) return run(std::integral_constant<int, 1>{});
+    if (P.each <= 4) return run(std::integral_constant<int, 4>{});
+    return run(std::integral_constant<int, 0>{});
 }
 
 cudaError_t launch_kv_append(const KvAppendArgs& a, const KvGeometry& g, int num_sms, cudaStream_t s) {

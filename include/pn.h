@@ -356,12 +356,13 @@ size_t pn_kv_cache_bytes(int64_t pages, int page_size, int kv_heads, int head_di
 
 /*
  * pn_kv_plan: one step's bookkeeping on the device.  For request b < batch
- * (at most 16384): lens[b] tokens are cached, held[b] pages are its own (the
+ * (at most 16384; capacity at most 2^31 - 17): lens[b] tokens are cached, held[b] pages are its own (the
  * first held[b] entries of row b of table: int32 [batch][table_stride], of
  * which max_pages are used), and add[b] >= 0 tokens join it; add[b] < 0: the
  * request is finished.  Free pages are a ring free_pages[pages] with
  * ring = {head, tail}: entries head .. tail - 1, modulo pages, are free.
- *   starts[b] (b <= batch): tokens of the step before request b.
+ *   starts[b] (b <= batch): tokens of the step before request b (2^31 - 16
+ *   where there are more).
  *   Taking: request b needs max(ceil((lens + add) / page_size) - held, 0)
  *   pages, taken from the ring's head in request order.  A request whose pages
  *   pass max_pages, whose tokens end behind `capacity`, or whose need together

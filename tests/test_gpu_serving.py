@@ -630,3 +630,19 @@ def test_verify_largest_vocabulary(pn, vocab):
     got = pn.verify(cuda(tokens), cuda(target), None, cuda(uniforms))
     want = ref.verify(tokens, target, None, uniforms, None)
     assert np.array_equal(got[0].cpu().numpy(), want[0]) and np.array_equal(got[1].cpu().numpy(), want[1])
+
+
+def test_plan_counts_past_32_bits(pn):
+    """Tokens whose sum passes 2^31 and 2^32 are refused, those before them served."""
+    big = (1 << 31) - 1
+    lens = torch.tensor([3, big, 0, big, 1], dtype=torch.int32, device="cuda")
+    add = torch.tensor([5, big, big, big, 7], dtype=torch.int32, device="cuda")
+    held = torch.tensor([1, 0, 0, 0, 1], dtype=torch.int32, device="cuda")
+    table = torch.full((5, 4), 9, dtype=torch.int32, device="cuda")
+    free, ring = torch.arange(10, dtype=torch.int32, device="cuda"), torch.tensor([(1 << 40) + 2, (1 << 40) + 8], device="cuda")
+    p = pn.kv_plan(lens, add, held, table, free, ring, 16, 40)
+    assert p.starts.tolist() == [0, 5] + [(1 << 31) - 16] * 4
+    assert p.lens.tolist() == [8, big, 0, big, 1] and p.held.tolist() == [1, 0, 0, 0, 1]
+    assert p.refused.tolist() == [4] and p.ring.tolist() == ring.tolist()
+    assert p.slots.tolist() == [9 * 16 + 3 + i for i in range(5)] + [-1] * 35
+    assert p.requests.tolist() == [0] * 5 + [1] * 35 and p.positions.tolist() == [3, 4, 5, 6, 7] + [-1] * 35
