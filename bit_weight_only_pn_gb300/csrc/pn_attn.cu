@@ -843,21 +843,36 @@ __global__ void __launch_bounds__(Smem<D, NT>::kThreads, 1) attn_kernel(const __
     // block's slot.
     int64_t* row_out = reinterpret_cast<int64_t*>(behind + M::kRowOut);    // [runs][rows]: output row, kToNone, kToSlot + begins
     constexpr int64_t kToNone = -1, kToSlot = -3;
-    for (int i = threadIdx.x; i < runs * RT; i += W * 32) {
-        const int run = i / RT, row = i % RT;
-        const int p0 = run_at[run], p1 = run_at[run + 1];
-        const PieceInfo info = pieces[order[p0]];
+    // Four lanes to a row, each with every fourth piece: a run has one of each warp at most.
+    static_assert(W <= 16, "pieces of a run");
+    for (int i = threadIdx.x / 4; i < runs * RT; i += W * 8) {
+        const int run = i / RT, row = i % RT, p0 = run_at[run] + lane % 4, p1 = run_at[run + 1];
+        const PieceInfo info = pieces[order[run_at[run]]];
+        float2 v[4];
         float m = -INFINITY, l = 0.0f;
-        for (int p = p0; p < p1; ++p) m = fmaxf(m, reinterpret_cast<const float2*>(piece_at(p) + RT * D)[row].x);
-        for (int p = p0; p < p1; ++p) {
-            const float2 v = reinterpret_cast<const float2*>(piece_at(p) + RT * D)[row];
-            const float f = v.x == -INFINITY ? 0.0f : ex2(v.x - m);
-            factors[p * RT + row] = f;
-            l += f * v.y;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            v[k] = p0 + 4 * k < p1 ? reinterpret_cast<const float2*>(piece_at(p0 + 4 * k) + RT * D)[row] : make_float2(-INFINITY, 0.0f);
+            m = fmaxf(m, v[k].x);
         }
-        if (inside(info)) {
-            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-            for (int p = p0; p < p1; ++p) factors[p * RT + row] *= inv;
+        const uint32_t four = 0xFu << (lane & 28);
+        m = fmaxf(m, __shfl_xor_sync(four, m, 1));
+        m = fmaxf(m, __shfl_xor_sync(four, m, 2));
+        float f[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            f[k] = v[k].x == -INFINITY ? 0.0f : ex2(v[k].x - m);
+            l += f[k] * v[k].y;
+        }
+        l += __shfl_xor_sync(four, l, 1);
+        l += __shfl_xor_sync(four, l, 2);
+        const bool whole = inside(info);
+        const float inv = !whole ? 1.0f : l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (p0 + 4 * k < p1) factors[(p0 + 4 * k) * RT + row] = f[k] * inv;
+        if (lane % 4) continue;
+        if (whole) {
             const int64_t at = row_index<RT>(P, info.q0, info.rows, info.h, info.rg, row);
             if (a.lse && at >= 0) a.lse[at] = log_sum(m, l);
             row_out[i] = at >= 0 ? at : kToNone;
@@ -874,6 +889,7 @@ __global__ void __launch_bounds__(Smem<D, NT>::kThreads, 1) attn_kernel(const __
         if (at == kToNone) continue;
         const int p0 = run_at[run], p1 = run_at[run + 1];
         float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
         for (int p = p0; p < p1; ++p) {
             const float f = factors[p * RT + row];
             const float4 v = *reinterpret_cast<const float4*>(piece_at(p) + e);
