@@ -52,9 +52,9 @@ constexpr int kThreads = 16 * 32;              // 128 registers each
 constexpr int kHalf = kTile / 2;               // tokens of a softmax thread
 constexpr int kPlaces = 2;                     // of S in tensor memory, 128 columns each
 constexpr int kDecodeWarps = 6;
-constexpr int kPieces = 8;                     // 8 tokens each, what a decode warp takes at a time
 constexpr int kSoftmaxThreads = 256;
 constexpr int kRawStages = 4;
+constexpr uint32_t kNap = 100;                 // nanoseconds between polls of the warps that work ahead: polling took a third of all instructions
 constexpr int kBufs = 4;                       // decoded tiles
 constexpr uint32_t kTmemCols = 512;            // two places of S (P over it), O of either half
 constexpr uint32_t kTmemO = kPlaces * 128;
@@ -184,8 +184,8 @@ struct Smem {
     static constexpr int kRaw = kScales + kBufs * kScaleBytes;             // [stage][4 records]
     static constexpr int kRawBytes = kTileRecords * kv_record_bytes(D);
     static constexpr int kSums = kRaw + kRawStages * kRawBytes;            // [2][rows] (reference, sum)
-    static constexpr int kTop = kSums + 2 * kRows * 8;                     // [buffer][piece] largest V scale (bits)
-    static constexpr int kHave = kTop + kBufs * kPieces * 4;                        // [buffer] records that a page holds
+    static constexpr int kTop = kSums + 2 * kRows * 8;                     // [buffer][record] largest V scale (bits)
+    static constexpr int kHave = kTop + kBufs * kTileRecords * 4;                    // [buffer] records that a page holds
     static constexpr int kValid = kHave + kBufs * 4;                       // [raw stage] the same, marks of its last copy
     static constexpr int kBars = (kValid + kRawStages * 4 + 7) / 8 * 8;
     static constexpr int kNumBars = 2 * kRawStages + 2 * kBufs + 1 + 3 * kPlaces + 1 + 1;
@@ -194,7 +194,6 @@ struct Smem {
     static constexpr int kUsed = kScan + (kThreads + 1) * 4;
     static constexpr int kBytes = kUsed + 1024;                            // slack to align to 1024 bytes
     static_assert(kBytes <= 227 * 1024, "fits one SM's shared memory");
-    static_assert(kPieces * 8 == kTile);
     static_assert(kScales % 16 == 0 && kRaw % 16 == 0 && kSums % 16 == 0 && kTop % 16 == 0, "alignment");
 };
 
@@ -401,11 +400,11 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     if (threadIdx.x == 0) {
         for (int s = 0; s < kRawStages; ++s) {
             mbar_init(raw_full + 8 * s, 1);
-            mbar_init(raw_empty + 8 * s, kPieces);
+            mbar_init(raw_empty + 8 * s, kTileRecords);
             valid[s] = 0u;
         }
         for (int s = 0; s < kBufs; ++s) {
-            mbar_init(kv_full + 8 * s, kPieces);
+            mbar_init(kv_full + 8 * s, kTileRecords);
             mbar_init(kv_empty + 8 * s, 1);
         }
         mbar_init(q_full, kSoftmaxThreads / 32);
@@ -492,6 +491,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                             break;
                         }
                     }
+                    __nanosleep(kNap);
                     continue;
                 }
                 uint32_t have = 0;
@@ -614,15 +614,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         __syncwarp();
     } else if (warp >= 8) {
         // --------------------------------------------------------- decode --
-        // the block's pieces of 8 tokens in turn: half h of record rec of unit n
+        // the block's records in turn, both halves of 8 tokens at once
         const int g = lane >> 2, t = lane & 3;
+        const int sj = lane >> 3, scale_at = (sj < NG ? kv_k_scales(D) : kv_v_scales(D)) + ((lane & 7) * NG + sj % NG) * 2;
         bool ok = true;
-        for (uint32_t task = warp - 8; task / kPieces < u1 - u0; task += kDecodeWarps) {
-            const uint32_t n = task / kPieces, piece = task % kPieces;
-            const int rec = piece >> 1, h = piece & 1;
+        for (uint32_t task = warp - 8; task / kTileRecords < u1 - u0; task += kDecodeWarps) {
+            const uint32_t n = task / kTileRecords, rec = task % kTileRecords;
             const uint32_t s = n % kRawStages, buf = n % kBufs;
             ok = wait_phase(raw_full + 8 * s, (n / kRawStages) & 1u, P.timeout_ns, abort);
-            if (ok && n >= kBufs) ok = wait_phase(kv_empty + 8 * buf, (n / kBufs - 1) & 1u, P.timeout_ns, abort);
+            if (ok && n >= kBufs) ok = wait_phase(kv_empty + 8 * buf, (n / kBufs - 1) & 1u, P.timeout_ns, abort, kNap);
             if (!__all_sync(0xFFFFFFFFu, ok)) break;
             const uint8_t* from = smem + M::kRaw + s * M::kRawBytes + rec * kv_record_bytes(D);
             uint8_t* kt = smem + M::kKv + buf * M::kKvBytes;
@@ -637,37 +637,45 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             };
             // every load before the first store, which might be taken to alias
             const bool real = (have >> rec) & 1;
-            const int sj = lane >> 3, st = h * 8 + (lane & 7);             // lane's scale: kind and group sj, token st of the record
-            const float scale = sj < 2 * NG ? lds_half_as_float(from + (sj < NG ? kv_k_scales(D) : kv_v_scales(D)) + (st * NG + sj % NG) * 2) : 0.0f;
-            uint32_t kw[2 * NG], vw[2 * NG];
-            {
+            float scale[2] = {0.0f, 0.0f};     // the lane's scales: kind and group sj, tokens lane % 8 and 8 more
+            uint32_t kw[2][2 * NG], vw[2][2 * NG];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (sj < 2 * NG) scale[h] = lds_half_as_float(from + scale_at + h * 16 * NG);
                 const uint8_t* p = from + h * 256 * NG + lane * 8 * NG;
                 if constexpr (NG == 2) {
                     const uint4 k4 = lds_u128(p), v4 = lds_u128(p + kv_v_codes(D));
-                    kw[0] = k4.x; kw[1] = k4.y; kw[2] = k4.z; kw[3] = k4.w;
-                    vw[0] = v4.x; vw[1] = v4.y; vw[2] = v4.z; vw[3] = v4.w;
+                    kw[h][0] = k4.x; kw[h][1] = k4.y; kw[h][2] = k4.z; kw[h][3] = k4.w;
+                    vw[h][0] = v4.x; vw[h][1] = v4.y; vw[h][2] = v4.z; vw[h][3] = v4.w;
                 } else {
                     const uint2 k2 = lds_u64(p), v2 = lds_u64(p + kv_v_codes(D));
-                    kw[0] = k2.x; kw[1] = k2.y;
-                    vw[0] = v2.x; vw[1] = v2.y;
+                    kw[h][0] = k2.x; kw[h][1] = k2.y;
+                    vw[h][0] = v2.x; vw[h][1] = v2.y;
                 }
             }
-            const int k0 = rec * 16 + h * 8 + g, v0 = rec * 16 + h * 8 + 2 * t;
 #pragma unroll
-            for (int j = 0; j < NG; ++j) {
-                put(kt, k0, j, 2 * t, kw[2 * j]);
-                put(kt, k0, j, 2 * t + 1, kw[2 * j + 1]);
-                put(vt, v0, j, g, vw[j]);
-                put(vt, v0 + 1, j, g, vw[NG + j]);
+            for (int h = 0; h < 2; ++h) {
+                const int k0 = rec * 16 + h * 8 + g, v0 = rec * 16 + h * 8 + 2 * t;
+#pragma unroll
+                for (int j = 0; j < NG; ++j) {
+                    put(kt, k0, j, 2 * t, kw[h][2 * j]);
+                    put(kt, k0, j, 2 * t + 1, kw[h][2 * j + 1]);
+                    put(vt, v0, j, g, vw[h][j]);
+                    put(vt, v0 + 1, j, g, vw[h][NG + j]);
+                }
             }
             // scales: K by scale * log2 e, V; none where no page holds the record
-            float* sc = reinterpret_cast<float*>(smem + M::kScales + buf * M::kScaleBytes);
-            if (sj < 2 * NG) sc[sj * kTile + rec * 16 + st] = !real ? 0.0f : sj < NG ? scale * P.scale_log2 : scale;
-            const uint32_t top = real && sj >= NG && sj < 2 * NG ? __float_as_uint(fmaxf(fabsf(scale), 0.0f)) : 0u;   // (NaN: none)
+            float* sc = reinterpret_cast<float*>(smem + M::kScales + buf * M::kScaleBytes) + sj * kTile + rec * 16 + (lane & 7);
+            uint32_t top = 0u;                 // (NaN: none)
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (sj < 2 * NG) sc[8 * h] = !real ? 0.0f : sj < NG ? scale[h] * P.scale_log2 : scale[h];
+                if (real && sj >= NG) top = max(top, __float_as_uint(fmaxf(fabsf(scale[h]), 0.0f)));
+            }
             const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, top);
             if (lane == 0) {
-                reinterpret_cast<uint32_t*>(smem + M::kTop)[buf * kPieces + piece] = most;
-                if (piece == 0) have_of[buf] = have & 15u;
+                reinterpret_cast<uint32_t*>(smem + M::kTop)[buf * kTileRecords + rec] = most;
+                if (rec == 0) have_of[buf] = have & 15u;
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -724,36 +732,39 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             const int pos = pos_lo + min(row, max(rows - 1, 0)) / P.group;
             const int window = a.window ? a.window : INT32_MAX;
             RowState st{-INFINITY, 0.0f, ok};
+            uint32_t written = 0;              // barrier of the P whose stores are on their way; told when the next tile is looked at
+            auto tell = [&]() {
+                tmem_wait_st();
+                tc_fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(written);
+            };
             for (uint32_t i = 0; i < count; ++i) {
-                if (st.ok) {
-                    st.ok = wait_phase(s_full + 8 * place, s_turn & 1u, P.timeout_ns, abort) &&
-                            wait_phase(kv_full + 8 * buf, (n / kBufs) & 1u, P.timeout_ns, abort);
-                    st.ok = __all_sync(0xFFFFFFFFu, st.ok);
-                }
-                tc_fence_after_sync();
+                bool there = st.ok && wait_phase(kv_full + 8 * buf, (n / kBufs) & 1u, P.timeout_ns, abort);
                 const int idx = first + static_cast<int>(i), tok0 = (idx < sink_tiles ? idx : lo_tile + idx - sink_tiles) * kTile;
                 const uint32_t ts = tmem + place * 128 + lanes;
                 const float* sc = reinterpret_cast<const float*>(smem + M::kScales + buf * M::kScaleBytes) + half * kHalf;
-                const uint4 t0 = *reinterpret_cast<const uint4*>(smem + M::kTop + buf * kPieces * 4);
-                const uint4 t1 = *reinterpret_cast<const uint4*>(smem + M::kTop + buf * kPieces * 4 + 16);
-                const float most = __uint_as_float(max(max(max(t0.x, t0.y), max(t0.z, t0.w)), max(max(t1.x, t1.y), max(t1.z, t1.w))));
+                const uint4 tops = *reinterpret_cast<const uint4*>(smem + M::kTop + buf * kTileRecords * 4);
+                const float most = __uint_as_float(max(max(tops.x, tops.y), max(tops.z, tops.w)));
                 const float big = lg2(fminf(fmaxf(most, 5.9604645e-8f), 65504.0f));
                 const uint32_t have = have_of[buf];
                 const bool plain = have == 15u && tok0 + kTile - 1 <= pos_lo && (tok0 > pos_hi - window || tok0 + kTile <= a.sinks);
+                if (i > 0) tell();
+                there = there && wait_phase(s_full + 8 * place, s_turn & 1u, P.timeout_ns, abort);
+                st.ok = __all_sync(0xFFFFFFFFu, there);
+                tc_fence_after_sync();
                 const uint32_t before = i > 0 ? kv_empty + 8 * ((buf + kBufs - 1) % kBufs) : 0u, parity = ((n - 1) / kBufs) & 1u;
                 if (plain)
                     st = half_tile<D, false>(st, ts + half * kHalf, to_o, sc, big, ~0u, before, parity, P.timeout_ns, abort);
                 else
                     st = half_tile_masked<D>(st, ts + half * kHalf, to_o, sc, big, tok0 + half * kHalf, have >> (2 * half), pos, window,
                                              a.sinks, before, parity, P.timeout_ns, abort);
-                tmem_wait_st();
-                tc_fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(p_ready + 16 * place + 8 * half);
+                written = p_ready + 16 * place + 8 * half;
                 ++n;
                 if (++buf == kBufs) buf = 0;
                 if (++place == kPlaces) { place = 0; ++s_turn; }
             }
+            tell();
             ok = st.ok;
             // every score of the segment is there, so Q may be replaced
             const Walk done = w;
