@@ -46,23 +46,33 @@ namespace pn {
 namespace {
 
 constexpr int kRows = 128;                     // MMA M
-constexpr int kTile = 64;                      // tokens per unit, MMA N of S
-constexpr int kTileRecords = kTile / kKvTokens;
 constexpr int kThreads = 16 * 32;              // 128 registers each
-constexpr int kHalf = kTile / 2;               // tokens of a softmax thread
 constexpr int kPlaces = 2;                     // of S in tensor memory, 128 columns each
 constexpr int kDecodeWarps = 6;
 constexpr int kSoftmaxThreads = 256;
 constexpr int kRawStages = 4;
 constexpr uint32_t kNap = 100;                 // nanoseconds between polls of the warps that work ahead: polling took a third of all instructions
-constexpr int kBufs = 4;                       // decoded tiles
 constexpr uint32_t kTmemCols = 512;            // two places of S (P over it), O of either half
 constexpr uint32_t kTmemO = kPlaces * 128;
 constexpr float kMargin = 7.0f, kSlack = 15.0f;
 constexpr uint32_t kIssued = 1u << 8, kOddTurn = 1u << 9;   // marks beside a raw stage's records
 
-// fp32 accumulators, fp16 operands, M = 128, N = 64; B K-major, or (bit 16) MN-major.
-constexpr uint32_t kDescS = (1u << 4) | (static_cast<uint32_t>(kTile >> 3) << 17) | (static_cast<uint32_t>(kRows >> 4) << 24);
+// What differs by head size: tensor memory holds two places of S and the O's, so
+// heads of 256 have tiles of 32 tokens and one reference and O to a row, of which
+// two warps have 16 tokens each.
+template <int D>
+struct Shape {
+    static constexpr int kGroups = D / 64;
+    static constexpr int kTile = D == 256 ? 32 : 64;                       // tokens per unit, MMA N of S
+    static constexpr int kRecords = kTile / kKvTokens;
+    static constexpr int kPart = kTile / 2;                                // tokens of a softmax thread
+    static constexpr int kStates = D == 256 ? 1 : 2;                       // references and O's of a row
+    static constexpr int kBufs = D == 256 ? 3 : 4;                         // decoded tiles
+    static constexpr uint32_t kAll = (1u << kRecords) - 1;
+};
+
+// fp32 accumulators, fp16 operands, M = 128; S: N = a tile's tokens, B K-major; O: N = 64, B MN-major (bit 16).
+__host__ __device__ constexpr uint32_t desc_s(int tile) { return (1u << 4) | (static_cast<uint32_t>(tile >> 3) << 17) | (static_cast<uint32_t>(kRows >> 4) << 24); }
 constexpr uint32_t kDescO = (1u << 4) | (1u << 16) | (8u << 17) | (static_cast<uint32_t>(kRows >> 4) << 24);
 
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool accumulate) {
@@ -88,8 +98,21 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
+// The two warps that share rows (barriers 3 - 6, by quadrant): has either a reason?
+// Scores that either has loaded before may be written over behind it.
+__device__ __forceinline__ bool pair_any(int pair, bool v) {
+    uint32_t r;
+    tc_fence_before_sync();
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\tbarrier.cta.red.or.pred q, %1, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r) : "r"(3 + pair), "r"(static_cast<uint32_t>(v)) : "memory");
+    tc_fence_after_sync();
+    return r != 0;
+}
+__device__ __forceinline__ void pair_sync(int pair) { asm volatile("bar.sync %0, 64;" :: "r"(3 + pair) : "memory"); }
+
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 2, %0;" :: "n"(kSoftmaxThreads) : "memory"); }
 // A request, one of its row tiles, and walking over them.
+template <int kTile>
 struct Walk {
     int b, qt, h, idx;         // request, row tile, head, tile of the segment
     int n, q0, pos0, len;      // the request's queries, their first row and position, cached tokens
@@ -146,8 +169,9 @@ struct Walk {
 };
 
 // The segment and tile of unit u; scan: units before each thread's `each` requests.
-__device__ __noinline__ Walk locate_unit(const AttnParams& P, int per, const uint32_t* scan, int each, uint32_t u) {
-    Walk w;
+template <int kTile>
+__device__ __noinline__ Walk<kTile> locate_unit(const AttnParams& P, int per, const uint32_t* scan, int each, uint32_t u) {
+    Walk<kTile> w;
     int lo = 0, hi = kThreads - 1;
     while (lo < hi) {
         const int mid = (lo + hi + 1) >> 1;
@@ -174,18 +198,20 @@ __device__ __noinline__ Walk locate_unit(const AttnParams& P, int per, const uin
 }
 
 template <int D>
-struct Smem {
-    static constexpr int kGroups = D / 64;
+struct Smem : Shape<D> {
+    using S = Shape<D>;
+    static constexpr int kGroups = S::kGroups, kTile = S::kTile, kBufs = S::kBufs;
     static constexpr int kQ = 0;                                           // [group][128 rows][128 bytes]
     static constexpr int kKv = kQ + kGroups * kRows * 128;                 // [buffer][K, V][group][64 tokens][128 bytes]
     static constexpr int kKvBytes = 2 * kGroups * kTile * 128;
     static constexpr int kScales = kKv + kBufs * kKvBytes;                 // [buffer][K scales of each group, V scales][64 tokens] floats
     static constexpr int kScaleBytes = kTile * 2 * kGroups * 4;
     static constexpr int kRaw = kScales + kBufs * kScaleBytes;             // [stage][4 records]
-    static constexpr int kRawBytes = kTileRecords * kv_record_bytes(D);
+    static constexpr int kRawBytes = S::kRecords * kv_record_bytes(D);
     static constexpr int kSums = kRaw + kRawStages * kRawBytes;            // [2][rows] (reference, sum)
-    static constexpr int kTop = kSums + 2 * kRows * 8;                     // [buffer][record] largest V scale (bits)
-    static constexpr int kHave = kTop + kBufs * kTileRecords * 4;                    // [buffer] records that a page holds
+    static constexpr int kMax = kSums + 2 * kRows * 8;                     // [quadrant][2][32] maxima of warps that share rows
+    static constexpr int kTop = kMax + 4 * 2 * 32 * 4;                     // [buffer][record] largest V scale (bits)
+    static constexpr int kHave = kTop + kBufs * S::kRecords * 4;                    // [buffer] records that a page holds
     static constexpr int kValid = kHave + kBufs * 4;                       // [raw stage] the same, marks of its last copy
     static constexpr int kBars = (kValid + kRawStages * 4 + 7) / 8 * 8;
     static constexpr int kNumBars = 2 * kRawStages + 2 * kBufs + 1 + 3 * kPlaces + 1 + 1;
@@ -240,30 +266,33 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     return d;
 }
 
+// log2 of a scale's size, from fp16's least (which stands for zero too) to its largest.
+__device__ __forceinline__ float log2_scale(float v) { return lg2(fminf(fmaxf(v, 5.9604645e-8f), 65504.0f)); }
+
 // Half a tile's scores of a row, from tensor memory at ts.  sc: the tile's
-// scales from the half's first token on, [K by group, V by group][64 tokens].
-// Hidden tokens (bits of seen that are 0) score -inf.  Returns the largest.
+// scales from the half's first token on, [K by group, V by group][a tile's
+// tokens].  Hidden tokens (bits of seen that are 0) score -inf.  Returns the largest.
 template <int D, bool kMasked>
-__device__ __forceinline__ float half_scores(Two (&x)[kHalf / 2], uint32_t ts, const float* sc, uint32_t seen) {
-    constexpr int NG = D / 64;
+__device__ __forceinline__ float half_scores(Two (&x)[Shape<D>::kPart / 2], uint32_t ts, const float* sc, uint32_t seen) {
+    constexpr int NG = D / 64, kTile = Shape<D>::kTile, kWide = Shape<D>::kPart / 16;
     float top[2] = {-INFINITY, -INFINITY};
-    uint32_t s[2][NG][16];
+    uint32_t s[kWide][NG][16];
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
+    for (int c = 0; c < kWide; ++c)
 #pragma unroll
-        for (int j = 0; j < NG; ++j) tmem_ld16(ts + 64 * j + 16 * c, s[c][j]);
+        for (int j = 0; j < NG; ++j) tmem_ld16(ts + kTile * j + 16 * c, s[c][j]);
     tmem_wait_ld();
 #pragma unroll
-    for (int c = 0; c < 2; ++c)
+    for (int c = 0; c < kWide; ++c)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {                  // four tokens
-            const ulonglong2 d0 = *reinterpret_cast<const ulonglong2*>(sc + 16 * c + 4 * i);
-            Two a = mul2(d0.x, two(s[c][0][4 * i], s[c][0][4 * i + 1]));
-            Two b = mul2(d0.y, two(s[c][0][4 * i + 2], s[c][0][4 * i + 3]));
-            if constexpr (NG == 2) {
-                const ulonglong2 d1 = *reinterpret_cast<const ulonglong2*>(sc + kTile + 16 * c + 4 * i);
-                a = fma2(d1.x, two(s[c][NG - 1][4 * i], s[c][NG - 1][4 * i + 1]), a);
-                b = fma2(d1.y, two(s[c][NG - 1][4 * i + 2], s[c][NG - 1][4 * i + 3]), b);
+            Two a, b;
+#pragma unroll
+            for (int j = 0; j < NG; ++j) {
+                const ulonglong2 d = *reinterpret_cast<const ulonglong2*>(sc + j * kTile + 16 * c + 4 * i);
+                const Two s0 = two(s[c][j][4 * i], s[c][j][4 * i + 1]), s1 = two(s[c][j][4 * i + 2], s[c][j][4 * i + 3]);
+                a = j ? fma2(d.x, s0, a) : mul2(d.x, s0);
+                b = j ? fma2(d.y, s1, b) : mul2(d.y, s1);
             }
             float2 u = apart(a), v = apart(b);
             if constexpr (kMasked) {
@@ -283,18 +312,38 @@ __device__ __forceinline__ float half_scores(Two (&x)[kHalf / 2], uint32_t ts, c
     return fmaxf(top[0], top[1]);
 }
 
+// The largest score with the log2 of its token's largest V scale added: for tiles
+// with hidden tokens, whose scales may be anything and must not set a reference.
+template <int D>
+__device__ __forceinline__ float top_with_scale(const Two (&x)[Shape<D>::kPart / 2], const float* sc) {
+    constexpr int NG = D / 64, kTile = Shape<D>::kTile;
+    float top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < Shape<D>::kPart / 2; ++i) {
+        float2 most = make_float2(0.0f, 0.0f);         // (NaN: none)
+#pragma unroll
+        for (int j = 0; j < NG; ++j) {
+            const float2 d = *reinterpret_cast<const float2*>(sc + (NG + j) * kTile + 2 * i);
+            most = make_float2(fmaxf(most.x, fabsf(d.x)), fmaxf(most.y, fabsf(d.y)));
+        }
+        const float2 v = apart(x[i]);
+        top = max3(top, v.x + log2_scale(most.x), v.y + log2_scale(most.y));
+    }
+    return top;
+}
+
 // The probabilities of the same tokens by group, to tensor memory at tp; their
 // sum (before V's scales) is added to sum.
 template <int D, bool kMasked>
-__device__ __forceinline__ void half_probabilities(const Two (&x)[kHalf / 2], uint32_t tp, const float* sc, uint32_t seen, float ref,
+__device__ __forceinline__ void half_probabilities(const Two (&x)[Shape<D>::kPart / 2], uint32_t tp, const float* sc, uint32_t seen, float ref,
                                                    float& sum) {
-    constexpr int NG = D / 64;
+    constexpr int NG = D / 64, kTile = Shape<D>::kTile, kPart = Shape<D>::kPart;
     const float less = ref == -INFINITY ? 0.0f : -ref;
     const Two less2 = two(less, less);
     Two part[2] = {two(sum, 0.0f), two(0.0f, 0.0f)};
-    uint32_t p[NG][16];
+    uint32_t p[NG][kPart / 2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {                      // four tokens
+    for (int i = 0; i < kPart / 4; ++i) {              // four tokens
         Two e[2];
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
@@ -318,7 +367,10 @@ __device__ __forceinline__ void half_probabilities(const Two (&x)[kHalf / 2], ui
         }
     }
 #pragma unroll
-    for (int j = 0; j < NG; ++j) tmem_st16(tp + 16 * j, p[j]);
+    for (int j = 0; j < NG; ++j) {
+        if constexpr (kPart == 32) tmem_st16(tp + 16 * j, p[j]);
+        else tmem_st8(tp + 16 * j, p[j]);
+    }
     const float2 both = apart(add2(part[0], part[1]));
     sum = both.x + both.y;
 }
@@ -328,18 +380,27 @@ struct RowState {
     bool ok;                   // no wait has run out
 };
 
-// Half a tile of a row: S at ts (P into the half's own columns of it), O of the
-// half at to.  before, parity: the barrier phase by which the last product into
-// O is done (0: O holds nothing yet).
+// Half a tile of a row: S at ts, P to tp, O (of one state: the warp's share of it)
+// at to.  most: the pair's place for maxima.  before, parity: the barrier phase by
+// which the last product into O is done (0: O holds nothing yet).
 template <int D, bool kMasked>
-__device__ __forceinline__ RowState half_tile(RowState st, uint32_t ts, uint32_t to, const float* sc, float big, uint32_t seen,
-                                              uint32_t before, uint32_t parity, uint64_t limit_ns, volatile uint32_t* abort) {
-    Two x[kHalf / 2];
-    const float top = half_scores<D, kMasked>(x, ts, sc, seen) + big;
+__device__ __forceinline__ RowState half_tile(RowState st, uint32_t ts, uint32_t tp, uint32_t to, const float* sc, float big, uint32_t seen,
+                                              float* most, uint32_t before, uint32_t parity, uint64_t limit_ns, volatile uint32_t* abort) {
+    using S = Shape<D>;
+    Two x[S::kPart / 2];
+    float top = half_scores<D, kMasked>(x, ts, sc, seen);
+    if constexpr (kMasked) top = top_with_scale<D>(x, sc);
+    else top += big;
     // the reference moves when it is passed by far
-    const bool move = top > st.ref + kSlack || (st.ref == -INFINITY && top > -INFINITY);
-    if (__any_sync(0xFFFFFFFFu, move)) {
-        const float ref = move ? top - kMargin : st.ref;
+    auto far = [&]() { return top > st.ref + kSlack || (st.ref == -INFINITY && top > -INFINITY); };
+    const int lane = threadIdx.x & 31, half = (threadIdx.x >> 7) & 1, pair = (threadIdx.x >> 5) & 3;
+    if (S::kStates == 2 ? __any_sync(0xFFFFFFFFu, far()) : pair_any(pair, far())) {
+        if constexpr (S::kStates == 1) {
+            most[half * 32 + lane] = top;
+            pair_sync(pair);
+            top = fmaxf(top, most[(half ^ 1) * 32 + lane]);
+        }
+        const float ref = far() ? top - kMargin : st.ref;
         const float f = st.ref == -INFINITY ? 0.0f : ex2(st.ref - ref);
         st.ref = ref;
         st.sum *= f;
@@ -347,7 +408,7 @@ __device__ __forceinline__ RowState half_tile(RowState st, uint32_t ts, uint32_t
             if (st.ok) st.ok = __all_sync(0xFFFFFFFFu, wait_phase(before, parity, limit_ns, abort));
             tc_fence_after_sync();
 #pragma unroll 1
-            for (int c = 0; c < D; c += 16) {
+            for (int c = 0; c < D * S::kStates / 2; c += 16) {
                 uint32_t o[16];
                 tmem_ld16(to + c, o);
                 tmem_wait_ld();
@@ -357,29 +418,30 @@ __device__ __forceinline__ RowState half_tile(RowState st, uint32_t ts, uint32_t
             }
         }
     }
-    half_probabilities<D, kMasked>(x, ts, sc, seen, st.ref, st.sum);
+    half_probabilities<D, kMasked>(x, tp, sc, seen, st.ref, st.sum);
     return st;
 }
 
 // The same for tiles with hidden tokens, a call of its own: few tiles are, and
 // with its code beside the other's in the loop every tile took a fifth longer.
 template <int D>
-__device__ __noinline__ RowState half_tile_masked(RowState st, uint32_t ts, uint32_t to, const float* sc, float big, int tok, uint32_t have,
-                                                  int pos, int window, int sinks, uint32_t before, uint32_t parity, uint64_t limit_ns,
-                                                  volatile uint32_t* abort) {
+__device__ __noinline__ RowState half_tile_masked(RowState st, uint32_t ts, uint32_t tp, uint32_t to, const float* sc, float big, int tok,
+                                                  uint32_t have, int pos, int window, int sinks, float* most, uint32_t before,
+                                                  uint32_t parity, uint64_t limit_ns, volatile uint32_t* abort) {
     uint32_t seen = 0;
 #pragma unroll
-    for (int c = 0; c < kHalf; ++c) {
+    for (int c = 0; c < Shape<D>::kPart; ++c) {
         const bool s = ((have >> (c / 16)) & 1u) && tok + c <= pos && (tok + c > pos - window || tok + c < sinks);
         seen |= static_cast<uint32_t>(s) << c;
     }
-    return half_tile<D, true>(st, ts, to, sc, big, seen, before, parity, limit_ns, abort);
+    return half_tile<D, true>(st, ts, tp, to, sc, big, seen, most, before, parity, limit_ns, abort);
 }
 
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_constant__ AttnParams P) {
     using M = Smem<D>;
-    constexpr int NG = M::kGroups;
+    constexpr int NG = M::kGroups, kTile = M::kTile, kTileRecords = M::kRecords, kBufs = M::kBufs, kPart = M::kPart, kStates = M::kStates;
+    using Walk = Walk<kTile>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_base = smem_addr(smem_raw), base = (raw_base + 1023u) & ~1023u;
     uint8_t* smem = smem_raw + (base - raw_base);
@@ -410,8 +472,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         mbar_init(q_full, kSoftmaxThreads / 32);
         for (int w = 0; w < kPlaces; ++w) {
             mbar_init(s_full + 8 * w, 1);
-            mbar_init(p_ready + 16 * w, 4);                // of either half
-            mbar_init(p_ready + 16 * w + 8, 4);
+            mbar_init(p_ready + 16 * w, 8 / kStates);      // of either state
+            mbar_init(p_ready + 16 * w + 8, 8 / kStates);
         }
         mbar_init(o_full, 1);
         mbar_init(drain, 1);
@@ -455,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     const bool idle = blockIdx.x >= min(blocks, total);
     const uint32_t u0 = idle ? 0 : static_cast<uint32_t>(static_cast<uint64_t>(total) * blockIdx.x / blocks);
     const uint32_t u1 = idle ? 0 : static_cast<uint32_t>(static_cast<uint64_t>(total) * (blockIdx.x + 1) / blocks);
-    auto locate = [&](uint32_t u, Walk& w) { w = locate_unit(P, per, scan, each, u); };
+    auto locate = [&](uint32_t u, Walk& w) { w = locate_unit<kTile>(P, per, scan, each, u); };
     auto give_up = [&]() {
         *abort = 1u;
         atomicCAS(P.status, 0u, kAttnTimeout);
@@ -562,8 +624,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 for (int j = 0; j < NG; ++j)
 #pragma unroll
                     for (int kk = 0; kk < 4; ++kk)
-                        mma_ss(d + 64 * j, desc(q_low + ((j * (kRows * 128) + kk * 32) >> 4)),
-                               desc(k + ((j * (kTile * 128) + kk * 32) >> 4)), kDescS, kk != 0);
+                        mma_ss(d + kTile * j, desc(q_low + ((j * (kRows * 128) + kk * 32) >> 4)),
+                               desc(k + ((j * (kTile * 128) + kk * 32) >> 4)), desc_s(kTile), kk != 0);
             };
             // the decoded tiles in turn: kb, kp the next S's buffer and parity, kt its
             // place; vb, vt, vp the next O's buffer, place of P and parity
@@ -585,7 +647,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 for (uint32_t i = 0; i < count && ok; ++i) {
                     const uint32_t t = tmem + vt * 128, v = v_low0 + vb * kStep;
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
+                    for (int h = 0; h < kStates; ++h) {
                         ok = wait(p_ready + 16 * vt + 8 * h, vp);
                         if (!ok) break;
                         tc_fence_after_sync();
@@ -593,7 +655,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                         for (int j = 0; j < NG; ++j)
 #pragma unroll
                             for (int kk = 0; kk < 2; ++kk)
-                                mma_ts(tmem + kTmemO + 128 * h + 64 * j, t + kHalf * h + 16 * j + 8 * kk,
+                                mma_ts(tmem + kTmemO + 128 * h + 64 * j, t + 32 * h + 16 * j + 8 * kk,
                                        desc(v + ((j * (kTile * 128) + (2 * h + kk) * 2048) >> 4)), kDescO, i > 0 || kk != 0);
                     }
                     if (!ok) break;
@@ -616,7 +678,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         // --------------------------------------------------------- decode --
         // the block's records in turn, both halves of 8 tokens at once
         const int g = lane >> 2, t = lane & 3;
-        const int sj = lane >> 3, scale_at = (sj < NG ? kv_k_scales(D) : kv_v_scales(D)) + ((lane & 7) * NG + sj % NG) * 2;
+        constexpr int kKinds = (2 * NG + 3) / 4;           // kinds of scale (K, V by group) to a lane: lane / 8 and every fourth
         bool ok = true;
         for (uint32_t task = warp - 8; task / kTileRecords < u1 - u0; task += kDecodeWarps) {
             const uint32_t n = task / kTileRecords, rec = task % kTileRecords;
@@ -637,22 +699,33 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             };
             // every load before the first store, which might be taken to alias
             const bool real = (have >> rec) & 1;
-            float scale[2] = {0.0f, 0.0f};     // the lane's scales: kind and group sj, tokens lane % 8 and 8 more
+            float scale[2][kKinds];            // the lane's, of tokens lane % 8 and 8 more
             uint32_t kw[2][2 * NG], vw[2][2 * NG];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                if (sj < 2 * NG) scale[h] = lds_half_as_float(from + scale_at + h * 16 * NG);
-                const uint8_t* p = from + h * 256 * NG + lane * 8 * NG;
-                if constexpr (NG == 2) {
-                    const uint4 k4 = lds_u128(p), v4 = lds_u128(p + kv_v_codes(D));
-                    kw[h][0] = k4.x; kw[h][1] = k4.y; kw[h][2] = k4.z; kw[h][3] = k4.w;
-                    vw[h][0] = v4.x; vw[h][1] = v4.y; vw[h][2] = v4.z; vw[h][3] = v4.w;
+#pragma unroll
+                for (int q = 0; q < kKinds; ++q) {
+                    const int kind = (lane >> 3) + 4 * q;
+                    scale[h][q] = kind < 2 * NG ? lds_half_as_float(from + (kind < NG ? kv_k_scales(D) : kv_v_scales(D)) +
+                                                                    ((h * 8 + (lane & 7)) * NG + kind % NG) * 2) : 0.0f;
+                }
+                if constexpr (NG >= 2) {
+#pragma unroll
+                    for (int pl = 0; pl < NG / 2; ++pl) {
+                        const uint8_t* p = from + (h * (NG / 2) + pl) * 512 + lane * 16;
+                        const uint4 k4 = lds_u128(p), v4 = lds_u128(p + kv_v_codes(D));
+                        kw[h][4 * pl] = k4.x; kw[h][4 * pl + 1] = k4.y; kw[h][4 * pl + 2] = k4.z; kw[h][4 * pl + 3] = k4.w;
+                        vw[h][4 * pl] = v4.x; vw[h][4 * pl + 1] = v4.y; vw[h][4 * pl + 2] = v4.z; vw[h][4 * pl + 3] = v4.w;
+                    }
                 } else {
+                    const uint8_t* p = from + h * 256 + lane * 8;
                     const uint2 k2 = lds_u64(p), v2 = lds_u64(p + kv_v_codes(D));
                     kw[h][0] = k2.x; kw[h][1] = k2.y;
                     vw[h][0] = v2.x; vw[h][1] = v2.y;
                 }
             }
+            // words of K: (group, which of two); of V: (group's plane, token of two, group in the plane)
+            constexpr int GP = NG >= 2 ? 2 : 1;
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int k0 = rec * 16 + h * 8 + g, v0 = rec * 16 + h * 8 + 2 * t;
@@ -660,22 +733,25 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 for (int j = 0; j < NG; ++j) {
                     put(kt, k0, j, 2 * t, kw[h][2 * j]);
                     put(kt, k0, j, 2 * t + 1, kw[h][2 * j + 1]);
-                    put(vt, v0, j, g, vw[h][j]);
-                    put(vt, v0 + 1, j, g, vw[h][NG + j]);
+                    put(vt, v0, j, g, vw[h][j / GP * 2 * GP + j % GP]);
+                    put(vt, v0 + 1, j, g, vw[h][j / GP * 2 * GP + GP + j % GP]);
                 }
             }
             // scales: K by scale * log2 e, V; none where no page holds the record
-            float* sc = reinterpret_cast<float*>(smem + M::kScales + buf * M::kScaleBytes) + sj * kTile + rec * 16 + (lane & 7);
+            float* sc = reinterpret_cast<float*>(smem + M::kScales + buf * M::kScaleBytes) + rec * 16 + (lane & 7);
             uint32_t top = 0u;                 // (NaN: none)
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (sj < 2 * NG) sc[8 * h] = !real ? 0.0f : sj < NG ? scale[h] * P.scale_log2 : scale[h];
-                if (real && sj >= NG) top = max(top, __float_as_uint(fmaxf(fabsf(scale[h]), 0.0f)));
-            }
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int q = 0; q < kKinds; ++q) {
+                    const int kind = (lane >> 3) + 4 * q;
+                    if (kind < 2 * NG) sc[kind * kTile + 8 * h] = !real ? 0.0f : kind < NG ? scale[h][q] * P.scale_log2 : scale[h][q];
+                    if (real && kind >= NG) top = max(top, __float_as_uint(fmaxf(fabsf(scale[h][q]), 0.0f)));
+                }
             const uint32_t most = __reduce_max_sync(0xFFFFFFFFu, top);
             if (lane == 0) {
                 reinterpret_cast<uint32_t*>(smem + M::kTop)[buf * kTileRecords + rec] = most;
-                if (rec == 0) have_of[buf] = have & 15u;
+                if (rec == 0) have_of[buf] = have & M::kAll;
             }
             fence_proxy_async_smem();
             __syncwarp();
@@ -689,7 +765,8 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         // -------------------------------------------------------- softmax --
         const int half = warp >> 2, row = threadIdx.x & 127;
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        const uint32_t to_o = tmem + kTmemO + half * 128 + lanes;
+        float* pair_most = reinterpret_cast<float*>(smem + M::kMax) + (warp & 3) * 64;
+        const uint32_t to_o = tmem + kTmemO + half * 128 + lanes;              // the half's O, or its columns of the one O
         float2* sums = reinterpret_cast<float2*>(smem + M::kSums);         // [2][rows] (reference, sum)
         auto block_slot = [&](uint32_t c, bool begins) { return P.block_slots + (2 * static_cast<int64_t>(c) + begins) * kPiece<D>; };
         bool ok = true;
@@ -743,23 +820,31 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 bool there = st.ok && wait_phase(kv_full + 8 * buf, (n / kBufs) & 1u, P.timeout_ns, abort);
                 const int idx = first + static_cast<int>(i), tok0 = (idx < sink_tiles ? idx : lo_tile + idx - sink_tiles) * kTile;
                 const uint32_t ts = tmem + place * 128 + lanes;
-                const float* sc = reinterpret_cast<const float*>(smem + M::kScales + buf * M::kScaleBytes) + half * kHalf;
-                const uint4 tops = *reinterpret_cast<const uint4*>(smem + M::kTop + buf * kTileRecords * 4);
-                const float most = __uint_as_float(max(max(tops.x, tops.y), max(tops.z, tops.w)));
-                const float big = lg2(fminf(fmaxf(most, 5.9604645e-8f), 65504.0f));
+                const float* sc = reinterpret_cast<const float*>(smem + M::kScales + buf * M::kScaleBytes) + half * kPart;
+                const uint32_t* tops = reinterpret_cast<const uint32_t*>(smem + M::kTop) + buf * kTileRecords;
+                float most;
+                if constexpr (kTileRecords == 4) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(tops);
+                    most = __uint_as_float(max(max(v.x, v.y), max(v.z, v.w)));
+                } else {
+                    const uint2 v = *reinterpret_cast<const uint2*>(tops);
+                    most = __uint_as_float(max(v.x, v.y));
+                }
+                const float big = log2_scale(most);
                 const uint32_t have = have_of[buf];
-                const bool plain = have == 15u && tok0 + kTile - 1 <= pos_lo && (tok0 > pos_hi - window || tok0 + kTile <= a.sinks);
+                const bool plain = have == M::kAll && tok0 + kTile - 1 <= pos_lo && (tok0 > pos_hi - window || tok0 + kTile <= a.sinks);
                 if (i > 0) tell();
                 there = there && wait_phase(s_full + 8 * place, s_turn & 1u, P.timeout_ns, abort);
                 st.ok = __all_sync(0xFFFFFFFFu, there);
                 tc_fence_after_sync();
                 const uint32_t before = i > 0 ? kv_empty + 8 * ((buf + kBufs - 1) % kBufs) : 0u, parity = ((n - 1) / kBufs) & 1u;
+                const uint32_t tp = ts + half * (kStates == 2 ? 32 : 8);
                 if (plain)
-                    st = half_tile<D, false>(st, ts + half * kHalf, to_o, sc, big, ~0u, before, parity, P.timeout_ns, abort);
+                    st = half_tile<D, false>(st, ts + half * kPart, tp, to_o, sc, big, ~0u, pair_most, before, parity, P.timeout_ns, abort);
                 else
-                    st = half_tile_masked<D>(st, ts + half * kHalf, to_o, sc, big, tok0 + half * kHalf, have >> (2 * half), pos, window,
-                                             a.sinks, before, parity, P.timeout_ns, abort);
-                written = p_ready + 16 * place + 8 * half;
+                    st = half_tile_masked<D>(st, ts + half * kPart, tp, to_o, sc, big, tok0 + half * kPart, have >> (half * kPart / kKvTokens), pos,
+                                             window, a.sinks, pair_most, before, parity, P.timeout_ns, abort);
+                written = p_ready + 16 * place + (kStates == 2 ? 8 * half : 0);
                 ++n;
                 if (++buf == kBufs) buf = 0;
                 if (++place == kPlaces) { place = 0; ++s_turn; }
@@ -801,11 +886,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 16) {
                 uint32_t o0[16], o1[16];
                 tmem_ld16(tmem + kTmemO + lanes + c, o0);
-                tmem_ld16(tmem + kTmemO + 128 + lanes + c, o1);
+                if constexpr (kStates == 2) tmem_ld16(tmem + kTmemO + 128 + lanes + c, o1);
                 tmem_wait_ld();
                 float o[16];
 #pragma unroll
-                for (int k = 0; k < 16; ++k) o[k] = fmaf(g1, __uint_as_float(o1[k]), g0 * __uint_as_float(o0[k]));
+                for (int k = 0; k < 16; ++k) {
+                    o[k] = g0 * __uint_as_float(o0[k]);
+                    if constexpr (kStates == 2) o[k] = fmaf(g1, __uint_as_float(o1[k]), o[k]);
+                }
                 if (!whole) {
 #pragma unroll
                     for (int k = 0; k < 16; k += 4)
@@ -903,20 +991,33 @@ cudaError_t launch(AttnParams P, uint8_t* ws, int num_sms, cudaStream_t s) {
 
 }  // namespace
 
-// From 49 query rows to a key/value head on.  24 requests of 4096 cached tokens,
-// 8 heads of 128: 32 rows 122 us here, 89 us in the kernel for few rows (16 at a
-// time); 48 rows 122 and 121 us; 64 rows 124 and 152 us.  (One request of 8192,
-// 64 rows: 48 and 36 us; two, 100 rows: 66 and 60 us.)
+// By the rows and the row tiles of the call, as if every request had max_queries
+// queries: a row costs the kernel for few rows 3 units (16 or 8 rows at a time,
+// whatever their number), a tile of up to 128 rows costs this one 160, and with
+// few tiles it loses 4500 to the thread blocks that share a segment and the one
+// that joins their parts.  Microseconds there and here, 8192 cached tokens (*: 24
+// requests of 4096):
+//   heads of 128, 8 of them:  2048 rows in 16 tiles 62, 68; 4096 in 32: 103, 88;
+//     4096 in 64: 64, 70; 9216* in 192: 115, 122; 12288* in 192: 148, 124
+//   heads of 256, 4 of them:  1024 rows in 8 tiles 66, 140; 2048 in 16: 115, 118;
+//     6720* in 96: 184, 155; 49152 rows of a prompt in 392, 4096 tokens: 1143, 345
+//   heads of 64, 8 of them:  2048 rows in 16 tiles 40, 45; 4096 in 32: 61, 58;
+//     13440* in 192: 100, 86
 bool attn_tc_takes(const AttnArgs& a, const KvGeometry& g) {
     const int group = a.heads / g.heads;
-    return g.D <= 128 && group <= kRows && static_cast<int64_t>(a.max_queries) * group > 48;
+    if (group > kRows) return false;
+    const int per = kRows / group;
+    const double each = static_cast<double>(a.batch) * g.heads;
+    const double rows = each * a.max_queries * group, tiles = each * ((a.max_queries + per - 1) / per);
+    return 3.0 * rows - 160.0 * tiles > 4500.0;
 }
 
 size_t attn_tc_workspace_bytes(int num_sms) {
-    return 256 + attn_counter_bytes(num_sms) + 2 * static_cast<size_t>(num_sms) * kPiece<128> * 4;
+    return 256 + attn_counter_bytes(num_sms) + 2 * static_cast<size_t>(num_sms) * kPiece<256> * 4;
 }
 
 cudaError_t launch_attention_tc(AttnParams P, uint8_t* ws, int num_sms, cudaStream_t s) {
+    if (P.cache.D == 256) return launch<256>(P, ws, num_sms, s);
     return P.cache.D == 64 ? launch<64>(P, ws, num_sms, s) : launch<128>(P, ws, num_sms, s);
 }
 

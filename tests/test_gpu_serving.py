@@ -262,15 +262,15 @@ def test_append_refusals(pn):
 
 
 # ---------------------------------------------------------------- attention --
-def attention_case(lens, counts, heads, kv, D, page, seed=0, k_size=1.0, v_size=1.0, spare_rows=0):
-    """Cached tokens with known values; every byte that holds no token is 0xFF (NaN scales), and
+def attention_case(lens, counts, heads, kv, D, page, seed=0, k_size=1.0, v_size=1.0, spare_rows=0, fill=0xFF):
+    """Cached tokens with known values; every byte that holds no token is 0xFF (NaN scales; `fill`), and
     table entries behind a request's pages lie outside the cache."""
     rng = np.random.default_rng(seed + D + sum(lens))
     held = [-(-x // page) for x in lens]
     pages = sum(held) + 2
     order = rng.permutation(pages)
     table = np.full((len(lens), max(max(held), 1) + 1), 1 << 30, np.int32)
-    cache = np.full((pages, kv, page // 16, 17 * D), 0xFF, np.uint8)
+    cache = np.full((pages, kv, page // 16, 17 * D), fill, np.uint8)
     ks, vs, at = [], [], 0
     for b, n in enumerate(lens):
         own = order[at:at + held[b]]
@@ -646,3 +646,103 @@ def test_plan_counts_past_32_bits(pn):
     assert p.refused.tolist() == [4] and p.ring.tolist() == ring.tolist()
     assert p.slots.tolist() == [9 * 16 + 3 + i for i in range(5)] + [-1] * 35
     assert p.requests.tolist() == [0] * 5 + [1] * 35 and p.positions.tolist() == [3, 4, 5, 6, 7] + [-1] * 35
+
+
+# ------------------------------------------- many query rows (products on tcgen05) --
+MANY_ROWS = [
+    # lens, queries of each, heads, kv heads, D, page, window, sinks
+    ([401], [384], 8, 8, 64, 16, 0, 0), ([390], [384], 8, 8, 128, 64, 0, 0), ([385], [384], 8, 8, 256, 32, 0, 0),
+    ([130, 77, 500], [120, 77, 130], 48, 8, 128, 16, 0, 0), ([140, 333], [140, 100], 40, 8, 256, 128, 0, 0),
+    ([129, 300], [128, 200], 56, 8, 64, 64, 0, 0),
+    ([700], [400], 16, 8, 128, 32, 100, 5), ([640], [400], 16, 8, 256, 16, 33, 70), ([600, 90], [300, 90], 16, 8, 64, 16, 1, 1),
+    ([40] * 30 + [0, 3, 200], [40] * 30 + [0, 3, 40], 12, 3, 128, 16, 0, 0), ([33] * 40, [33] * 40, 8, 2, 256, 16, 20, 3),
+    ([2000], [390], 8, 8, 256, 64, 0, 0), ([3000], [390], 8, 8, 128, 16, 0, 0),
+]
+
+
+@pytest.mark.parametrize("lens,counts,heads,kv,D,page,window,sinks", MANY_ROWS)
+def test_attention_many_rows(pn, lens, counts, heads, kv, D, page, window, sinks):
+    case = attention_case(lens, counts, heads, kv, D, page)
+    ws = pn.AttentionWorkspace()
+    first = check_attention(pn, case, max(counts), 1 / math.sqrt(D), window, sinks, ws)
+    again = check_attention(pn, case, max(counts), 1 / math.sqrt(D), window, sinks, ws)
+    assert np.array_equal(first[0], again[0]) and np.array_equal(first[1], again[1])
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("k_size,v_size,scale", [(30.0, 1.0, 0.3), (1e-3, 1e-4, 0.1), (1.0, 3e4, -0.1), (2.0, 1e-7, 1.0), (1.0, 1.0, 0.0)])
+def test_attention_many_rows_sizes_of_values(pn, D, k_size, v_size, scale):
+    case = attention_case([150, 133], [128, 128], 24, 8, D, 16, 1, k_size, v_size)
+    check_attention(pn, case, 128, scale)
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attention_many_rows_hidden_bytes(pn, D):
+    """Lost pages hide their tokens; a last token's NaN and infinite scales reach its own query alone."""
+    B, L, n, page = 34, 100, 40, 16
+    q, cache, table, lens, starts, ks, vs = attention_case([L] * B, [n] * B, 4, 1, D, page)
+    for b in range(0, B, 3):
+        table[b, 1], table[b, 4] = -3, cache.shape[0]
+    run = lambda: pn.attention(cuda(q), cuda(cache), cuda(table), cuda(lens), cuda(starts), n, 0.1).cpu().numpy().astype(np.float64)
+    out = run()
+    for b in (0, 1, 33):
+        lost = [t for t in range(L) if t // page in (1, 4)] if b % 3 == 0 else []
+        for i in (0, 5, n - 1):
+            t = np.array([x for x in range(L - n + i + 1) if x not in lost])
+            for h in range(4):
+                x = 0.1 * ks[b][t, 0] @ q[starts[b] + i, h].astype(np.float64)
+                w = np.exp(x - x.max())
+                w /= w.sum()
+                want = w @ vs[b][t, 0]
+                limit = 2.0 ** -10 * (w @ np.abs(vs[b][t, 0])) + 2.0 ** -11 * np.abs(want) + 1e-6
+                assert np.all(np.abs(out[starts[b] + i, h] - want) <= limit)
+    NG = D // 64
+    for b in range(1, B, 3):
+        slot = int(table[b, (L - 1) // page]) * page + (L - 1) % page
+        rec, r = cache[slot // page, 0, slot % page // 16], slot % 16
+        for base, bits in ((8 * D, 0x7C00), (16 * D + D // 2, 0x7E00)):
+            rec[base + 2 * NG * r: base + 2 * NG * (r + 1)] = np.array([bits] * NG, np.uint16).view(np.uint8)
+    got = run()
+    last = np.zeros(len(q), bool)
+    last[starts[2::3] - 1] = True                     # the last queries of requests 1, 4, ...
+    assert np.array_equal(got[~last], out[~last])
+    assert all(np.isnan(got[i]).any() for i in np.flatnonzero(last))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_attention_many_rows_time_out(pn, D):
+    """A copy that never comes ends in the status word, and the workspace serves the next call."""
+    case = attention_case([400], [384], 8, 8, D, 16)
+    args = [cuda(x) for x in case[:5]]
+    ws = pn.AttentionWorkspace()
+    pn.set_wait_timeout_ns(20_000_000)
+    pn.set_test_stall(True)
+    try:
+        pn.attention(*args, 384, 0.1, workspace=ws)
+        assert ws.status() == 5
+    finally:
+        pn.set_test_stall(False)
+        pn.set_wait_timeout_ns(1_000_000_000)
+    check_attention(pn, case, 384, 0.1, workspace=ws)
+
+
+def test_attention_many_requests_and_rows(pn):
+    """16384 requests, most empty, the last with many rows: prefix sums of a large batch."""
+    lens = [0] * 16384
+    counts = [0] * 16384
+    for b, n in ((0, 3), (5000, 70), (16383, 200)):
+        lens[b], counts[b] = n + 10, n
+    check_attention(pn, attention_case(lens, counts, 4, 2, 128, 16), 200, 0.1, workspace=pn.AttentionWorkspace())
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("lens,counts,heads,kv", [([70, 3, 45], [1, 1, 1], 4, 2), ([70, 41, 29], [12, 3, 9], 4, 2), ([171, 141], [160, 140], 24, 8)])
+@pytest.mark.parametrize("v_size", [1.0, 1e-4])
+def test_attention_stale_bytes(pn, D, lens, counts, heads, kv, v_size):
+    """What bytes behind the last token hold (large finite scales, infinite ones, zeros) changes no bit."""
+    runs = []
+    for fill in (0x00, 0x7B, 0x7C, 0xFF):
+        case = attention_case(lens, counts, heads, kv, D, 64, 3, 1.0, v_size, fill=fill)
+        runs.append(check_attention(pn, case, max(counts), 0.1))
+    for r in runs[1:]:
+        assert np.array_equal(r[0], runs[0][0]) and np.array_equal(r[1], runs[0][1])
