@@ -4,32 +4,38 @@
 //
 // A segment is (request, row tile, key/value head): 128 rows, the query heads
 // that share the head times as many whole tokens as fit.  Its visible cached
-// tokens are taken 64 at a time.  In a thread block of 16 warps
+// tokens are taken 64 at a time (32 for heads of 256).  In a thread block of 16
+// warps
 //   warp 14 copies records into a raw ring (bulk copies, a lane to a stage);
 //   warps 8-13 decode them into fp16 whole numbers n - 8, exact, K and V as
 //     [token][64 values] tiles with the 128-byte swizzle, and the scales as
 //     fp32; a tile's codes are decoded once for 128 rows;
 //   warp 15 issues the products: S_j = Q_j K_j^T for each group j of 64 values
-//     (fp32 in tensor memory, M = 128, N = 64), O_j += P_j V_j with P_j from
-//     tensor memory and V as its token-major tile;
+//     (fp32 in tensor memory, M = 128, N = 64 or 32), O_j += P_j V_j with P_j
+//     from tensor memory and V as its token-major tile;
 //   warps 0-7 take the tiles, half a tile's tokens of a row to a thread: x =
 //     sum_j d_j S_j, the online softmax, P_j = p d_j rounded once to fp16,
-//     written over the half's own columns of S.  The halves keep references,
-//     sums and O's of their own, so they never wait for each other, and are
-//     joined at the end of a segment.  S has two places, so one tile's scores
-//     are made while the other's probabilities are worked out.
+//     written over S.  For heads of 64 and 128 the halves keep references, sums
+//     and O's of their own, so they never wait for each other, and are joined at
+//     the end of a segment; two O's of 256 columns do not fit tensor memory beside
+//     S, so there the two warps that share rows agree on a reference, by a vote
+//     per tile and maxima through shared memory when it moves.  S has two places,
+//     so one tile's scores are made while the other's probabilities are worked out.
 // The scales of K and V never touch the operands, so scores and values are as
 // exact as in the kernel for few rows; P_j takes the place of one P because V's
 // scale differs by group.
 //
 // The reference of a row is its maximum of x + log2 of the tile's largest V
-// scale, less 7, and stays until that maximum lies 15 above it: p d < 2^15, and
-// O is hardly ever rescaled.
+// scale (of each token's own where some are hidden), less 7, and stays until that
+// maximum lies 15 above it: p d < 2^15, and O is hardly ever rescaled.
 //
-// What it is bound by: the 16 products of a tile take 640 cycles (S at N = 64
-// reads 6 KB of shared memory each, 48 cycles; O 32), its softmax about 900
-// instructions on each of the four schedulers, at roughly one every two cycles:
-// about 1900 cycles a tile.
+// What it is bound by (heads of 128, 4096 queries over 8192 tokens, 32 heads: 691
+// us): a softmax warp's chain of 1900 cycles a tile, of which 490 are waits and
+// set-up, 1070 scores, exponentials and P, the rest stores and the segment's end;
+// the 16 products of a tile take 640 (S reads 6 KB of shared memory each, 48
+// cycles; O 32), and the decode warps wait three quarters of the time.  16
+// softmax warps of 16 tokens took 774 us: what a warp does once a tile is then
+// done twice as often.
 //
 // Work split: as in pn_attn.cu, units (segment, tile) in order, a contiguous
 // range to each of one thread block per SM; what crosses block boundaries is

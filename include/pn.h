@@ -439,7 +439,10 @@ pn_status pn_kv_read(const void* cache, int64_t pages, int page_size, int kv_hea
  * Scores, sums and outputs are held in fp32; exp(x_t) times the scale of v_t
  * is rounded to fp16 before it is multiplied by v_t's codes, so an output is
  * within 2^-11 (sum_t p_t |v_t|) + 2^-11 |out| of the exact value, and a
- * little more for the fp32 sums.  Deterministic.
+ * little more for the fp32 sums and, where V's scales differ by powers of ten,
+ * for products far below the largest (2^-29 max |v| to a token).  Deterministic.
+ * Which kernel runs, and with it the last bits, goes by batch, max_queries, the
+ * heads and head_dim alone.
  * workspace: pn_attention_workspace_bytes() bytes, 256-byte aligned, zeroed
  * once (pn_workspace_init); every completed call leaves its counters zeroed.
  * pn_workspace_status reads its status word.  Calls that share a workspace
