@@ -38,8 +38,11 @@
 // done twice as often.
 //
 // Work split: as in pn_attn.cu, units (segment, tile) in order, a contiguous
-// range to each of one thread block per SM; what crosses block boundaries is
-// joined by the last block to arrive, in block order.
+// range to each of one thread block per SM (of fewer where the joins would cost
+// more than they save); what crosses block boundaries is joined by the last block
+// to arrive, in block order, by all its warps: 16 loads of 16 bytes on their way
+// in every thread (with half the warps and 8 loads, 512 rows in 8192 tokens took
+// 88 us, now 60).
 #include <cstdint>
 
 #include <cuda_fp16.h>
@@ -221,8 +224,8 @@ struct Smem : Shape<D> {
     static constexpr int kValid = kHave + kBufs * 4;                       // [raw stage] the same, marks of its last copy
     static constexpr int kBars = (kValid + kRawStages * 4 + 7) / 8 * 8;
     static constexpr int kNumBars = 2 * kRawStages + 2 * kBufs + 1 + 3 * kPlaces + 1 + 1;
-    static constexpr int kMisc = kBars + kNumBars * 8;                     // TMEM base, abort, last-block flags
-    static constexpr int kScan = kMisc + 16;                               // [threads + 1] units before each thread's requests
+    static constexpr int kMisc = kBars + kNumBars * 8;                     // TMEM base, abort, last-block flags, shared segments
+    static constexpr int kScan = kMisc + 32;                               // [threads + 1] units before each thread's requests
     static constexpr int kUsed = kScan + (kThreads + 1) * 4;
     static constexpr int kBytes = kUsed + 1024;                            // slack to align to 1024 bytes
     static_assert(kBytes <= 227 * 1024, "fits one SM's shared memory");
@@ -458,6 +461,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + M::kMisc);
     volatile uint32_t* abort = misc + 1;
     volatile uint32_t* last_flag = misc + 2;           // [2]
+    volatile uint32_t* shared = misc + 4;              // [2] first units of segments of other blocks too, [2] their tiles
     volatile uint32_t* valid = reinterpret_cast<volatile uint32_t*>(smem + M::kValid);
     volatile uint32_t* have_of = reinterpret_cast<volatile uint32_t*>(smem + M::kHave);
     uint32_t* scan = reinterpret_cast<uint32_t*>(smem + M::kScan);
@@ -492,14 +496,16 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     }
     // units before each thread's share of the requests
     const int each = (a.batch + kThreads - 1) / kThreads;
+    uint32_t segments = 0;
     {
         uint32_t* warp_sums = reinterpret_cast<uint32_t*>(smem + M::kSums);
         const int b0 = min(static_cast<int>(threadIdx.x) * each, a.batch), b1 = min(b0 + each, a.batch);
         Walk w{};
-        uint32_t mine = 0;
+        uint32_t mine = 0, segs = 0;
         for (w.b = b0; w.b < b1; ++w.b) {
             w.request(P, per);
             mine += w.units(P, per);
+            segs += static_cast<uint32_t>(w.qtiles) * P.cache.heads;
         }
         uint32_t in = mine;
 #pragma unroll
@@ -507,10 +513,15 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, in, d);
             if (lane >= d) in += o;
         }
-        if (lane == 31) warp_sums[warp] = in;
+        segs = __reduce_add_sync(0xFFFFFFFFu, segs);
+        if (lane == 31) {
+            warp_sums[warp] = in;
+            warp_sums[kThreads / 32 + warp] = segs;
+        }
         __syncthreads();
         uint32_t at = in - mine;
         for (int i = 0; i < warp; ++i) at += warp_sums[i];
+        for (int i = 0; i < kThreads / 32; ++i) segments += warp_sums[kThreads / 32 + i];
         scan[threadIdx.x] = at;
         if (threadIdx.x == kThreads - 1) scan[kThreads] = at + mine;
     }
@@ -519,11 +530,17 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
     tc_fence_after_sync();
     const uint32_t tmem = misc[0];
     const uint32_t total = scan[kThreads];             // below 2^32: checked on the host
-    const uint32_t blocks = min(gridDim.x, max(total, 1u));
+    // A block shares a segment of T tiles for no less than sqrt(T D / 256) of them:
+    // a tile takes about a microsecond, and so does the join of a part for every 256
+    // values of a head, which one block does for all parts.
+    const float tiles = static_cast<float>(total) / static_cast<float>(max(segments, 1u));
+    const uint32_t least = max(static_cast<uint32_t>(sqrtf(tiles * (D / 256.0f))), 1u);
+    const uint32_t blocks = min(gridDim.x, max(total / least, 1u));
     const bool idle = blockIdx.x >= min(blocks, total);
     const uint32_t u0 = idle ? 0 : static_cast<uint32_t>(static_cast<uint64_t>(total) * blockIdx.x / blocks);
     const uint32_t u1 = idle ? 0 : static_cast<uint32_t>(static_cast<uint64_t>(total) * (blockIdx.x + 1) / blocks);
     auto locate = [&](uint32_t u, Walk& w) { w = locate_unit<kTile>(P, per, scan, each, u); };
+    auto block_slot = [&](uint32_t c, bool begins) { return P.block_slots + (2 * static_cast<int64_t>(c) + begins) * kPiece<D>; };
     auto give_up = [&]() {
         *abort = 1u;
         atomicCAS(P.status, 0u, kAttnTimeout);
@@ -774,7 +791,6 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         float* pair_most = reinterpret_cast<float*>(smem + M::kMax) + (warp & 3) * 64;
         const uint32_t to_o = tmem + kTmemO + half * 128 + lanes;              // the half's O, or its columns of the one O
         float2* sums = reinterpret_cast<float2*>(smem + M::kSums);         // [2][rows] (reference, sum)
-        auto block_slot = [&](uint32_t c, bool begins) { return P.block_slots + (2 * static_cast<int64_t>(c) + begins) * kPiece<D>; };
         bool ok = true;
         uint32_t segs = 0, n = 0, buf = 0, place = 0, s_turn = 0;         // n: units done; its buffer, its place of S and how often that went round
         uint32_t shared_seg[2] = {0xFFFFFFFFu, 0xFFFFFFFFu}, shared_tiles[2] = {0, 0};   // pieces of segments of other blocks too
@@ -901,9 +917,10 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                     if constexpr (kStates == 2) o[k] = fmaf(g1, __uint_as_float(o1[k]), o[k]);
                 }
                 if (!whole) {
+                    if (row < rows)
 #pragma unroll
-                    for (int k = 0; k < 16; k += 4)
-                        reinterpret_cast<float4*>(slot)[((c + k) / 4) * kRows + row] = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
+                        for (int k = 0; k < 16; k += 4)
+                            reinterpret_cast<float4*>(slot)[((c + k) / 4) * kRows + row] = make_float4(o[k], o[k + 1], o[k + 2], o[k + 3]);
                 } else if (at >= 0) {
                     uint4* out = reinterpret_cast<uint4*>(a.out + at * D + c);
                     out[0] = make_uint4(pack_half2(o[0], o[1]), pack_half2(o[2], o[3]), pack_half2(o[4], o[5]), pack_half2(o[6], o[7]));
@@ -915,63 +932,91 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
             u += count;
         }
 
-        // --------------------------------------- segments of several blocks --
-        if (u0 < u1) {
-            auto block_of = [&](uint32_t x) {          // the block that holds unit x
-                return static_cast<uint32_t>(((static_cast<uint64_t>(x) + 1) * blocks + total - 1) / total - 1);
-            };
-            if (threadIdx.x < 2) {
-                bool last = false;
-                const uint32_t seg = shared_seg[threadIdx.x];
-                if (seg != 0xFFFFFFFFu) {
-                    const uint32_t c0 = block_of(seg), c1 = block_of(seg + shared_tiles[threadIdx.x] - 1);
-                    __threadfence();
-                    last = atomicAdd(&P.counters[c0], 1u) == c1 - c0;
-                    __threadfence();
-                    if (last) P.counters[c0] = 0u;
-                }
-                last_flag[threadIdx.x] = last;
+        if (threadIdx.x < 2) {
+            shared[threadIdx.x] = shared_seg[threadIdx.x];
+            shared[2 + threadIdx.x] = shared_tiles[threadIdx.x];
+        }
+    }
+
+    // ------------------------------------------- segments of several blocks --
+    // Their joins by all warps: every role is through, no product or copy is on its way.
+    tc_fence_before_sync();
+    __syncthreads();
+    if (u0 < u1) {
+        auto block_of = [&](uint32_t x) {              // the block that holds unit x
+            return static_cast<uint32_t>(((static_cast<uint64_t>(x) + 1) * blocks + total - 1) / total - 1);
+        };
+        if (threadIdx.x < 2) {
+            bool last = false;
+            const uint32_t seg = shared[threadIdx.x];
+            if (seg != 0xFFFFFFFFu) {
+                const uint32_t c0 = block_of(seg), c1 = block_of(seg + shared[2 + threadIdx.x] - 1);
+                __threadfence();
+                last = atomicAdd(&P.counters[c0], 1u) == c1 - c0;
+                __threadfence();
+                if (last) P.counters[c0] = 0u;
             }
-            softmax_sync();
-            float* factors = reinterpret_cast<float*>(smem);               // [parts][rows]: no product reads Q or the tiles any more
-            for (int kind = 0; kind < 2; ++kind) {
-                if (!last_flag[kind]) continue;
-                const uint32_t seg = shared_seg[kind], c0 = block_of(seg), c1 = block_of(seg + shared_tiles[kind] - 1);
-                const int parts = static_cast<int>(c1 - c0 + 1);
-                locate(seg, w);
-                const int rows = w.nt * P.group, tq = row / P.group;
-                const int64_t at = row < rows ? (static_cast<int64_t>(w.q0) + w.t0 + tq) * a.heads + w.h * P.group + row - tq * P.group : -1;
-                if (half == 0) {
-                    auto part_sum = [&](int p) { return __ldcg(reinterpret_cast<const float2*>(block_slot(c0 + p, p == 0) + kRows * D) + row); };
-                    float m = -INFINITY, l = 0.0f;
-#pragma unroll 4
-                    for (int p = 0; p < parts; ++p) m = fmaxf(m, part_sum(p).x);
-#pragma unroll 4
-                    for (int p = 0; p < parts; ++p) {
-                        const float2 v = part_sum(p);
-                        const float f = v.x == -INFINITY ? 0.0f : ex2(v.x - m);
-                        factors[p * kRows + row] = f;
-                        l += f * v.y;
-                    }
-                    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-                    for (int p = 0; p < parts; ++p) factors[p * kRows + row] *= inv;
-                    if (a.lse && at >= 0) a.lse[at] = log_sum(m, l);
-                }
-                softmax_sync();
-                if (at >= 0) {
-                    for (int c = half * (D / 2); c < (half + 1) * (D / 2); c += 4) {
-                        float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            last_flag[threadIdx.x] = last;
+        }
+        __syncthreads();
+        const int row = threadIdx.x & (kRows - 1), quarter = threadIdx.x / kRows;
+        float* quarters = reinterpret_cast<float*>(smem);                  // [4][rows]; no product reads Q or the tiles any more
+        float* factors = quarters + 4 * kRows;                             // [parts][rows]
+        for (int kind = 0; kind < 2; ++kind) {
+            if (!last_flag[kind]) continue;
+            const uint32_t seg = shared[kind], c0 = block_of(seg), c1 = block_of(seg + shared[2 + kind] - 1);
+            const int parts = static_cast<int>(c1 - c0 + 1);
+            Walk w;
+            locate(seg, w);
+            const int rows = w.nt * P.group, tq = row / P.group;
+            const int64_t at = row < rows ? (static_cast<int64_t>(w.q0) + w.t0 + tq) * a.heads + w.h * P.group + row - tq * P.group : -1;
+            auto part = [&](int p) { return block_slot(c0 + p, p == 0); };
+            auto part_sum = [&](int p) { return __ldcg(reinterpret_cast<const float2*>(part(p) + kRows * D) + row); };
+            float m = -INFINITY, l = 0.0f;
 #pragma unroll 8
-                        for (int p = 0; p < parts; ++p) {
-                            const float f = factors[p * kRows + row];
-                            const float4 v = __ldcg(reinterpret_cast<const float4*>(block_slot(c0 + p, p == 0)) + (c / 4) * kRows + row);
-                            o.x = fmaf(f, v.x, o.x); o.y = fmaf(f, v.y, o.y); o.z = fmaf(f, v.z, o.z); o.w = fmaf(f, v.w, o.w);
-                        }
-                        *reinterpret_cast<uint2*>(a.out + at * D + c) = make_uint2(pack_half2(o.x, o.y), pack_half2(o.z, o.w));
-                    }
-                }
-                softmax_sync();                        // the factors are written again
+            for (int p = quarter; p < parts; p += 4) m = fmaxf(m, part_sum(p).x);
+            quarters[threadIdx.x] = m;
+            __syncthreads();
+            m = fmaxf(fmaxf(quarters[row], quarters[kRows + row]), fmaxf(quarters[2 * kRows + row], quarters[3 * kRows + row]));
+            __syncthreads();
+#pragma unroll 8
+            for (int p = quarter; p < parts; p += 4) {
+                const float2 v = part_sum(p);
+                const float f = v.x == -INFINITY ? 0.0f : ex2(v.x - m);
+                factors[p * kRows + row] = f;
+                l += f * v.y;
             }
+            quarters[threadIdx.x] = l;
+            __syncthreads();
+            l = (quarters[row] + quarters[kRows + row]) + (quarters[2 * kRows + row] + quarters[3 * kRows + row]);
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            if (quarter == 0 && a.lse && at >= 0) a.lse[at] = log_sum(m, l);
+            if (at >= 0) {
+                constexpr int kFours = D / 16 < 8 ? D / 16 : 8;            // at a time, of two parts: 16 loads on their way
+                for (int c = quarter * (D / 4); c < (quarter + 1) * (D / 4); c += 4 * kFours) {
+                    float4 o[kFours];
+#pragma unroll
+                    for (int k = 0; k < kFours; ++k) o[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 2
+                    for (int p = 0; p < parts; ++p) {
+                        const float4* from = reinterpret_cast<const float4*>(part(p)) + (c / 4) * kRows + row;
+                        float4 v[kFours];
+#pragma unroll
+                        for (int k = 0; k < kFours; ++k) v[k] = __ldcg(from + k * kRows);
+                        const float f = factors[p * kRows + row];
+#pragma unroll
+                        for (int k = 0; k < kFours; ++k) {
+                            o[k].x = fmaf(f, v[k].x, o[k].x); o[k].y = fmaf(f, v[k].y, o[k].y);
+                            o[k].z = fmaf(f, v[k].z, o[k].z); o[k].w = fmaf(f, v[k].w, o[k].w);
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < kFours; ++k)
+                        *reinterpret_cast<uint2*>(a.out + at * D + c + 4 * k) = make_uint2(pack_half2(o[k].x * inv, o[k].y * inv),
+                                                                                           pack_half2(o[k].z * inv, o[k].w * inv));
+                }
+            }
+            __syncthreads();                           // the factors are written again
         }
     }
     // ------------------------------------------------------------ teardown --
@@ -990,7 +1035,7 @@ cudaError_t launch(AttnParams P, uint8_t* ws, int num_sms, cudaStream_t s) {
     P.status = reinterpret_cast<uint32_t*>(ws);
     P.counters = reinterpret_cast<uint32_t*>(ws + 256);
     P.block_slots = reinterpret_cast<float*>(ws + 256 + attn_counter_bytes(num_sms));
-    constexpr int kMost = Smem<D>::kScales / (kRows * 4);                  // blocks whose factors fit the place of Q and the tiles
+    constexpr int kMost = (Smem<D>::kScales - 4 * kRows * 4) / (kRows * 4);                  // blocks whose factors fit the place of Q and the tiles
     attn_tc_kernel<D><<<num_sms < kMost ? num_sms : kMost, kThreads, Smem<D>::kBytes, s>>>(P);
     return cudaGetLastError();
 }
@@ -998,24 +1043,24 @@ cudaError_t launch(AttnParams P, uint8_t* ws, int num_sms, cudaStream_t s) {
 }  // namespace
 
 // By the rows and the row tiles of the call, as if every request had max_queries
-// queries: a row costs the kernel for few rows 3 units (16 or 8 rows at a time,
-// whatever their number), a tile of up to 128 rows costs this one 160, and with
-// few tiles it loses 4500 to the thread blocks that share a segment and the one
-// that joins their parts.  Microseconds there and here, 8192 cached tokens (*: 24
-// requests of 4096):
-//   heads of 128, 8 of them:  2048 rows in 16 tiles 62, 68; 4096 in 32: 103, 88;
-//     4096 in 64: 64, 70; 9216* in 192: 115, 122; 12288* in 192: 148, 124
-//   heads of 256, 4 of them:  1024 rows in 8 tiles 66, 140; 2048 in 16: 115, 118;
-//     6720* in 96: 184, 155; 49152 rows of a prompt in 392, 4096 tokens: 1143, 345
-//   heads of 64, 8 of them:  2048 rows in 16 tiles 40, 45; 4096 in 32: 61, 58;
-//     13440* in 192: 100, 86
+// queries: a tile of up to 128 rows costs this kernel what 62, 37 or 41 rows
+// (heads of 64, 128, 256) cost the one for few rows, which takes them 16 or, of
+// 256, 8 at a time, and with few tiles it loses what 1200, 600 or 1300 rows cost
+// to the joins of segments that several blocks share.  Microseconds there, here:
+//   8 heads of 64.  24 requests of 4096 cached tokens: 32 rows 52, 82; 64: 84, 83;
+//     70: 100, 84.  One of 8192: 128 rows 28, 29; 512: 61, 46
+//   8 heads of 128.  24 of 4096: 32 rows 85, 103; 40: 115, 105; 64: 148, 107.  One
+//     of 8192: 64 rows 31, 31; 256: 62, 54; 512: 103, 60.  One of 1024, 128 rows: 23, 25
+//   4 heads of 256.  24 of 4096: 32 rows 93, 111; 48: 129, 113; 70: 184, 117.  One
+//     of 8192: 256 rows 66, 87; 512: 115, 88.  One of 1024, 256 rows: 27, 58
 bool attn_tc_takes(const AttnArgs& a, const KvGeometry& g) {
     const int group = a.heads / g.heads;
     if (group > kRows) return false;
-    const int per = kRows / group;
-    const double each = static_cast<double>(a.batch) * g.heads;
-    const double rows = each * a.max_queries * group, tiles = each * ((a.max_queries + per - 1) / per);
-    return 3.0 * rows - 160.0 * tiles > 4500.0;
+    const int per = kRows / group, at_once = g.D == 256 ? 8 : 16;
+    const int64_t rows = (static_cast<int64_t>(a.max_queries) * group + at_once - 1) / at_once * at_once;
+    const int64_t tiles = (static_cast<int64_t>(a.max_queries) + per - 1) / per;
+    const int64_t tile_cost = g.D == 64 ? 62 : g.D == 128 ? 37 : 41, joins = g.D == 64 ? 1200 : g.D == 128 ? 600 : 1300;
+    return static_cast<double>(a.batch) * g.heads * static_cast<double>(rows - tile_cost * tiles) > static_cast<double>(joins);
 }
 
 size_t attn_tc_workspace_bytes(int num_sms) {
