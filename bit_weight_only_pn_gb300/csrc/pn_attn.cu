@@ -96,7 +96,7 @@ __device__ __forceinline__ Request request_of(const AttnParams& P, int b) {
     r.len = static_cast<int>(min(static_cast<int64_t>(max(a.lens[b], 0)), room));
     r.pos0 = r.len - r.n;
     r.rows = r.n * P.group;
-    const int lo = a.window ? max(r.pos0 - a.window + 1, 0) : 0;
+    const int lo = a.window ? window_first(r.pos0, a.window) : 0;
     r.lo_tile = lo / kTile;
     r.sink_tiles = a.window ? min((a.sinks + kTile - 1) / kTile, r.lo_tile) : 0;
     r.tiles = max((r.len + kTile - 1) / kTile - r.lo_tile + r.sink_tiles, 1);
@@ -400,6 +400,11 @@ __device__ __forceinline__ void take_tile(const uint8_t* stage, int tok0, uint32
     uint32_t seen = 0xFFFFFFFFu;
     if constexpr (kMasked) {
         seen = 0;
+        int from[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int c = 0; c < 2; ++c) from[n][c] = window_first(Q.pos[n][c], window);
 #pragma unroll
         for (int r = 0; r < kTileRecords; ++r)
 #pragma unroll
@@ -409,7 +414,7 @@ __device__ __forceinline__ void take_tile(const uint8_t* stage, int tok0, uint32
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         const int tok = tok0 + r * kKvTokens + hh * 8 + g;
-                        const bool s = ((valid >> r) & 1) && tok <= Q.pos[n][c] && (tok > Q.pos[n][c] - window || tok < sinks);
+                        const bool s = ((valid >> r) & 1) && tok <= Q.pos[n][c] && (tok >= from[n][c] || tok < sinks);
                         seen |= static_cast<uint32_t>(s) << (((r * 2 + hh) * NT + n) * 2 + c);
                     }
     }
@@ -730,7 +735,7 @@ __global__ void __launch_bounds__(Smem<D, NT>::kThreads, 1) attn_kernel(const __
                 const uint8_t* data = smem + stage * S::kStage;
                 if (tok0 > pos_hi) {
                     // no row sees this tile
-                } else if (have == (1u << kTileRecords) - 1 && tok0 + kTile - 1 <= pos_lo && (tok0 > pos_hi - window || tok0 + kTile <= a.sinks)) {
+                } else if (have == (1u << kTileRecords) - 1 && tok0 + kTile - 1 <= pos_lo && (tok0 >= window_first(pos_hi, window) || tok0 + kTile <= a.sinks)) {
                     take_tile<D, NT, false>(data, tok0, have, Q, window, a.sinks, st);
                 } else {
                     take_tile<D, NT, true>(data, tok0, have, Q, window, a.sinks, st);

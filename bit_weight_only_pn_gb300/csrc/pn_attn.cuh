@@ -64,6 +64,10 @@ static __device__ bool wait_phase(uint32_t bar, uint32_t parity, uint64_t limit_
     }
 }
 
+// The first cached token in the window (at least 1) of a query at `pos`, which is
+// negative for a query before the cache; pos - window may pass 32 bits.
+__device__ __forceinline__ int window_first(int pos, int window) { return pos >= window ? pos - window + 1 : 0; }
+
 __device__ __forceinline__ float log_sum(float ref, float sum) {
     return sum == 0.0f ? -INFINITY : 0.6931471805599453f * (ref + log2f(sum));
 }

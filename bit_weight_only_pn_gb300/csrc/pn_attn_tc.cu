@@ -146,7 +146,7 @@ struct Walk {
         pos_lo = pos0 + t0;
         pos_hi = pos_lo + nt - 1;
         const int end_tile = (max(pos_hi + 1, 0) + kTile - 1) / kTile;
-        const int lo = P.a.window ? max(pos_lo - P.a.window + 1, 0) : 0;
+        const int lo = P.a.window ? window_first(pos_lo, P.a.window) : 0;
         lo_tile = lo / kTile;
         sink_tiles = P.a.window ? min((P.a.sinks + kTile - 1) / kTile, lo_tile) : 0;
         tiles = max(end_tile - lo_tile + sink_tiles, 1);
@@ -437,10 +437,11 @@ template <int D>
 __device__ __noinline__ RowState half_tile_masked(RowState st, uint32_t ts, uint32_t tp, uint32_t to, const float* sc, float big, int tok,
                                                   uint32_t have, int pos, int window, int sinks, float* most, uint32_t before,
                                                   uint32_t parity, uint64_t limit_ns, volatile uint32_t* abort) {
+    const int from = window_first(pos, window);
     uint32_t seen = 0;
 #pragma unroll
     for (int c = 0; c < Shape<D>::kPart; ++c) {
-        const bool s = ((have >> (c / 16)) & 1u) && tok + c <= pos && (tok + c > pos - window || tok + c < sinks);
+        const bool s = ((have >> (c / 16)) & 1u) && tok + c <= pos && (tok + c >= from || tok + c < sinks);
         seen |= static_cast<uint32_t>(s) << c;
     }
     return half_tile<D, true>(st, ts, tp, to, sc, big, seen, most, before, parity, limit_ns, abort);
@@ -854,7 +855,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 }
                 const float big = log2_scale(most);
                 const uint32_t have = have_of[buf];
-                const bool plain = have == M::kAll && tok0 + kTile - 1 <= pos_lo && (tok0 > pos_hi - window || tok0 + kTile <= a.sinks);
+                const bool plain = have == M::kAll && tok0 + kTile - 1 <= pos_lo && (tok0 >= window_first(pos_hi, window) || tok0 + kTile <= a.sinks);
                 if (i > 0) tell();
                 there = there && wait_phase(s_full + 8 * place, s_turn & 1u, P.timeout_ns, abort);
                 st.ok = __all_sync(0xFFFFFFFFu, there);

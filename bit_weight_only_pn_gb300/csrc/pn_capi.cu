@@ -669,8 +669,12 @@ pn_status pn_attention(const uint16_t* q, int64_t q_stride, int64_t tokens, int 
     if (pn_status st = device_info(&sms, &major); st != PN_OK) return st;
     if (major < 10) return PN_EUNSUPPORTED;
     if (pn::attn_workspace_bytes(sms) > workspace_bytes) return PN_EINVAL;
+    // no request has more cached tokens than its row of the table has room for: a window of as many hides nothing, and
+    // no more first tokens are there (with both below 2^31 - 128 no index of a tile passes 32 bits)
+    const int room = max_pages * page_size;
     const pn::AttnArgs a{reinterpret_cast<const __half*>(q), q_stride, tokens, heads, table, table_stride, max_pages,
-                         lens, starts, batch, max_queries, scale, window, sinks, reinterpret_cast<__half*>(out), lse};
+                         lens, starts, batch, max_queries, scale, window < room ? window : 0, sinks < room ? sinks : room,
+                         reinterpret_cast<__half*>(out), lse};
     const pn::KvGeometry g{static_cast<uint8_t*>(const_cast<void*>(cache)), pages, page_size, kv_heads, head_dim};
     if (!pn::attn_fits(a, g)) return PN_EUNSUPPORTED;
     const cudaError_t e = pn::launch_attention(a, g, workspace, sms, g_timeout_ns.load(), g_test_stall.load(),

@@ -746,3 +746,28 @@ def test_attention_stale_bytes(pn, D, lens, counts, heads, kv, v_size):
         runs.append(check_attention(pn, case, max(counts), 0.1))
     for r in runs[1:]:
         assert np.array_equal(r[0], runs[0][0]) and np.array_equal(r[1], runs[0][1])
+
+
+# ------------------------------------------------ windows and first tokens near 2^31 --
+MOST = (1 << 31) - 1
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("lens,counts,heads,kv", [([500, 40, 3], [1, 3, 1], 4, 2), ([500, 40], [9, 3], 4, 2), ([390, 140], [384, 130], 8, 8)])
+@pytest.mark.parametrize("window,sinks", [(100, MOST), (10000, MOST), (1, MOST - 40), (130, MOST - 100), (MOST, 0), (MOST - 7, MOST - 12)])
+def test_attention_all_first_tokens(pn, D, lens, counts, heads, kv, window, sinks):
+    """As many first tokens as can be asked for, or such a window, hide nothing."""
+    case = attention_case(lens, counts, heads, kv, D, 16)
+    got = check_attention(pn, case, max(counts), 0.1, window, sinks, pn.AttentionWorkspace())
+    plain = check_attention(pn, case, max(counts), 0.1)
+    if window >= 10000:                               # more than the table has room for: the same call, so the same bits
+        assert np.array_equal(got[0], plain[0]) and np.array_equal(got[1], plain[1])
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("lens,counts,heads,kv", [([2, 9, 1], [5, 16, 1], 4, 2), ([100, 2, 250], [384, 30, 384], 8, 8)])
+@pytest.mark.parametrize("window,sinks", [(MOST, 0), (MOST - 3, MOST), (5, MOST), (MOST, MOST), (90, 3)])
+def test_attention_more_queries_than_tokens_and_windows(pn, D, lens, counts, heads, kv, window, sinks):
+    """Queries before the cache see nothing, those behind them what their window and the first tokens hold."""
+    case = attention_case(lens, counts, heads, kv, D, 16)
+    check_attention(pn, case, max(counts), 0.1, window, sinks, pn.AttentionWorkspace())
