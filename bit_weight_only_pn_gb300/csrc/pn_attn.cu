@@ -559,12 +559,12 @@ __global__ void __launch_bounds__(Smem<D, NT>::kThreads, 1) attn_kernel(const __
         const int each = (a.batch + M::kThreads - 1) / M::kThreads;
         const int b0 = min(static_cast<int>(threadIdx.x) * each, a.batch), b1 = min(b0 + each, a.batch);
         uint32_t mine = 0;
-        for (int b = b0; b < b1; ++b) mine += request_of<RT>(P, b).units(heads);
+        for (int b = b0; b < b1; ++b) mine = add_units(mine, request_of<RT>(P, b).units(heads));
         uint32_t in = mine;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, in, d);
-            if (lane >= d) in += o;
+            if (lane >= d) in = add_units(in, o);
         }
         if (lane == 31) warp_sums[warp] = in;
         __syncthreads();
@@ -576,12 +576,16 @@ __global__ void __launch_bounds__(Smem<D, NT>::kThreads, 1) attn_kernel(const __
         }
         if (threadIdx.x == M::kThreads - 1) {
             uint32_t all = 0;
-            for (int w = 0; w <= W; ++w) all += warp_sums[w];
+            for (int w = 0; w <= W; ++w) all = add_units(all, warp_sums[w]);
             prefix[a.batch] = all;
         }
         __syncthreads();
     }
-    const uint32_t total = prefix[a.batch];                              // below 2^32: checked on the host
+    uint32_t total = prefix[a.batch];
+    if (total == kTooManyUnits) {                                        // starts out of order: nothing is written
+        if (threadIdx.x == 0 && blockIdx.x == 0) atomicCAS(P.status, 0u, kAttnInvalid);
+        total = 0;
+    }
     uint32_t blocks = min(gridDim.x, (total + W - 1) / W);
     // One request with short segments: a block to a segment, so that nothing is
     // joined over blocks (that takes longer than four tiles to a warp do).
@@ -1042,11 +1046,22 @@ size_t attn_workspace_bytes(int num_sms) {
     return most;
 }
 
+// Two limits.  Row groups as the arguments alone allow for them, every request
+// with max_queries queries, below 2^31, whichever kernel runs.  And the chosen
+// kernel's units below 2^32 - 1, where the requests' queries together are no more
+// than `tokens`: n queries are at most n / per + 1 row groups (tiles), so a long
+// prompt beside many single tokens counts as what it is.  (With max_queries for
+// every request there too, 64 requests with one chunk of 8192 queries of 64 + 8
+// heads and tables for 131072 tokens would not fit, by a factor of 2.)
 bool attn_fits(const AttnArgs& a, const KvGeometry& g) {
-    const int64_t rows = static_cast<int64_t>(a.max_queries) * (a.heads / g.heads), per = g.D < 256 && rows > 8 ? 16 : 8;
-    const double units = static_cast<double>(a.batch) * g.heads * static_cast<double>((rows + per - 1) / per) *
-                         static_cast<double>((static_cast<int64_t>(a.max_pages) * g.page_size + kTile - 1) / kTile + kSegmentUnits);
-    return units < 4294967296.0;
+    const int group = a.heads / g.heads;
+    const int64_t rows = static_cast<int64_t>(a.max_queries) * group, per = g.D < 256 && rows > 8 ? 16 : 8;
+    const double batch = a.batch, allowed = batch * static_cast<double>((rows + per - 1) / per);
+    if (allowed * g.heads >= 2147483648.0) return false;
+    if (attn_tc_takes(a, g)) return attn_tc_units(a, g) < 4294967295.0;
+    const double there = static_cast<double>(a.tokens) * group / static_cast<double>(per) + batch;
+    const int64_t tiles = (static_cast<int64_t>(a.max_pages) * g.page_size + kTile - 1) / kTile + kSegmentUnits;
+    return (allowed < there ? allowed : there) * g.heads * static_cast<double>(tiles) < 4294967295.0;
 }
 
 cudaError_t launch_attention(const AttnArgs& a, const KvGeometry& g, void* workspace, int num_sms, uint64_t timeout_ns, int stall,

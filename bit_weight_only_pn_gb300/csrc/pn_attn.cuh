@@ -11,6 +11,7 @@
 
 namespace pn {
 
+constexpr uint32_t kAttnInvalid = 1;         // PN_EINVAL
 constexpr uint32_t kAttnTimeout = 5;         // PN_ETIMEOUT
 constexpr uint64_t kAttnDrainNs = 200ull * 1000 * 1000;
 
@@ -43,6 +44,11 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
 }
+
+// Sums of units that stop at 2^32 - 1, which no call reaches whose starts are in
+// order (the host sees to that); where they are not, the kernels stop there.
+constexpr uint32_t kTooManyUnits = 0xFFFFFFFFu;
+__device__ __forceinline__ uint32_t add_units(uint32_t a, uint32_t b) { return a + b < a ? kTooManyUnits : a + b; }
 
 // Nanoseconds in SM cycles, at the fastest clock: limits are at least as long as asked.
 __device__ __forceinline__ int64_t cycles_of(uint64_t ns) { return static_cast<int64_t>(ns) * 21 / 10; }
@@ -78,6 +84,7 @@ constexpr size_t attn_counter_bytes(int num_sms) { return (static_cast<size_t>(n
 
 // The kernel for many query rows to a key/value head (pn_attn_tc.cu).
 bool attn_tc_takes(const AttnArgs& a, const KvGeometry& g);
+double attn_tc_units(const AttnArgs& a, const KvGeometry& g);            // at most
 size_t attn_tc_workspace_bytes(int num_sms);
 cudaError_t launch_attention_tc(AttnParams P, uint8_t* ws, int num_sms, cudaStream_t s);
 

@@ -505,14 +505,14 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         uint32_t mine = 0, segs = 0;
         for (w.b = b0; w.b < b1; ++w.b) {
             w.request(P, per);
-            mine += w.units(P, per);
+            mine = add_units(mine, w.units(P, per));
             segs += static_cast<uint32_t>(w.qtiles) * P.cache.heads;
         }
         uint32_t in = mine;
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, in, d);
-            if (lane >= d) in += o;
+            if (lane >= d) in = add_units(in, o);
         }
         segs = __reduce_add_sync(0xFFFFFFFFu, segs);
         if (lane == 31) {
@@ -521,16 +521,20 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         }
         __syncthreads();
         uint32_t at = in - mine;
-        for (int i = 0; i < warp; ++i) at += warp_sums[i];
+        for (int i = 0; i < warp; ++i) at = add_units(at, warp_sums[i]);
         for (int i = 0; i < kThreads / 32; ++i) segments += warp_sums[kThreads / 32 + i];
         scan[threadIdx.x] = at;
-        if (threadIdx.x == kThreads - 1) scan[kThreads] = at + mine;
+        if (threadIdx.x == kThreads - 1) scan[kThreads] = add_units(at, mine);
     }
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = misc[0];
-    const uint32_t total = scan[kThreads];             // below 2^32: checked on the host
+    uint32_t total = scan[kThreads];
+    if (total == kTooManyUnits) {                      // starts out of order: nothing is written
+        if (threadIdx.x == 0 && blockIdx.x == 0) atomicCAS(P.status, 0u, kAttnInvalid);
+        total = 0;
+    }
     // A block shares a segment of T tiles for no less than sqrt(T D / 256) of them:
     // a tile takes about a microsecond, and so does the join of a part for every 256
     // values of a head, which one block does for all parts.
@@ -1062,6 +1066,15 @@ bool attn_tc_takes(const AttnArgs& a, const KvGeometry& g) {
     const int64_t tiles = (static_cast<int64_t>(a.max_queries) + per - 1) / per;
     const int64_t tile_cost = g.D == 64 ? 62 : g.D == 128 ? 37 : 41, joins = g.D == 64 ? 1200 : g.D == 128 ? 600 : 1300;
     return static_cast<double>(a.batch) * g.heads * static_cast<double>(rows - tile_cost * tiles) > static_cast<double>(joins);
+}
+
+double attn_tc_units(const AttnArgs& a, const KvGeometry& g) {
+    const int per = kRows / (a.heads / g.heads), tile = g.D == 256 ? Shape<256>::kTile : Shape<128>::kTile;
+    static_assert(Shape<64>::kTile == Shape<128>::kTile, "a tile's tokens");
+    const double allowed = static_cast<double>(a.batch) * static_cast<double>((static_cast<int64_t>(a.max_queries) + per - 1) / per);
+    const double there = static_cast<double>(a.tokens) / per + a.batch;
+    const int64_t tiles = (static_cast<int64_t>(a.max_pages) * g.page_size + tile - 1) / tile;
+    return (allowed < there ? allowed : there) * g.heads * static_cast<double>(tiles);
 }
 
 size_t attn_tc_workspace_bytes(int num_sms) {

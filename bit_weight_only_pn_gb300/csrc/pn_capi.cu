@@ -279,7 +279,7 @@ pn_status pn_workspace_status(void* workspace, size_t workspace_bytes, pn_stream
     if (e != cudaSuccess) return pn::cuda_error(e);
     if (word == 0) return PN_OK;
     if (cudaError_t e2 = cudaMemset(workspace, 0, workspace_bytes); e2 != cudaSuccess) return pn::cuda_error(e2);
-    return word == PN_ETIMEOUT ? PN_ETIMEOUT : PN_ECUDA;
+    return word == PN_ETIMEOUT || word == PN_EINVAL ? static_cast<pn_status>(word) : PN_ECUDA;
 }
 
 }  // extern "C"
@@ -665,10 +665,6 @@ pn_status pn_attention(const uint16_t* q, int64_t q_stride, int64_t tokens, int 
     const size_t nq = (static_cast<size_t>(tokens - 1) * q_stride + cols) * 2, no = static_cast<size_t>(tokens) * cols * 2;
     if (overlaps(q, nq, out, no) || overlaps(cache, pn_kv_cache_bytes(pages, page_size, kv_heads, head_dim), out, no))
         return PN_EINVAL;
-    int sms = 0, major = 0;
-    if (pn_status st = device_info(&sms, &major); st != PN_OK) return st;
-    if (major < 10) return PN_EUNSUPPORTED;
-    if (pn::attn_workspace_bytes(sms) > workspace_bytes) return PN_EINVAL;
     // no request has more cached tokens than its row of the table has room for: a window of as many hides nothing, and
     // no more first tokens are there (with both below 2^31 - 128 no index of a tile passes 32 bits)
     const int room = max_pages * page_size;
@@ -677,6 +673,10 @@ pn_status pn_attention(const uint16_t* q, int64_t q_stride, int64_t tokens, int 
                          reinterpret_cast<__half*>(out), lse};
     const pn::KvGeometry g{static_cast<uint8_t*>(const_cast<void*>(cache)), pages, page_size, kv_heads, head_dim};
     if (!pn::attn_fits(a, g)) return PN_EUNSUPPORTED;
+    int sms = 0, major = 0;
+    if (pn_status st = device_info(&sms, &major); st != PN_OK) return st;
+    if (major < 10) return PN_EUNSUPPORTED;
+    if (pn::attn_workspace_bytes(sms) > workspace_bytes) return PN_EINVAL;
     const cudaError_t e = pn::launch_attention(a, g, workspace, sms, g_timeout_ns.load(), g_test_stall.load(),
                                                reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PN_OK : pn::cuda_error(e);

@@ -256,7 +256,7 @@ struct AttnArgs {
     float* lse;                // may be null
 };
 size_t attn_workspace_bytes(int num_sms);
-// Whether the call's units can be numbered in 32 bits.
+// Whether the call's rows and units can be numbered in 32 bits (see there).
 bool attn_fits(const AttnArgs& a, const KvGeometry& g);
 cudaError_t launch_attention(const AttnArgs& a, const KvGeometry& g, void* workspace, int num_sms, uint64_t timeout_ns, int stall,
                              cudaStream_t s);

@@ -134,8 +134,9 @@ pn_status pn_unpack(int type, const void* W, int64_t N, int64_t K, float* w, pn_
  * pn_workspace_init: zero a workspace (required once before first use; every
  * call that completes leaves it zeroed again).
  * pn_workspace_status: synchronise `stream`, read and clear the device status
- * word of the workspace; returns PN_OK or the device-side error (PN_ETIMEOUT),
- * and re-zeroes the whole workspace after an error.
+ * word of the workspace; returns PN_OK or the device-side error (PN_ETIMEOUT,
+ * of pn_attention also PN_EINVAL), and re-zeroes the whole workspace after an
+ * error.
  * Workspace pointers must be 256-byte aligned.
  */
 size_t pn_workspace_bytes(int64_t total_rows);
@@ -443,6 +444,14 @@ pn_status pn_kv_read(const void* cache, int64_t pages, int page_size, int kv_hea
  * for products far below the largest (2^-29 max |v| to a token).  Deterministic.
  * Which kernel runs, and with it the last bits, goes by batch, max_queries, the
  * heads and head_dim alone.
+ * The work is numbered in 32 bits.  With group = heads / kv_heads and rows taken
+ * 16 at a time (8 where max_queries * group <= 8 or head_dim is 256), PN_EUNSUPPORTED
+ * if batch * kv_heads * ceil(max_queries * group / 16) reaches 2^31, or if kv_heads *
+ * min(that many row groups, tokens * group / 16 + batch) * (max_pages * page_size /
+ * 32 + 1) reaches 2^32 (where the kernel for many rows runs: by whole query tokens
+ * that fit 128 rows, 64 cached tokens at a time, 32 for head_dim 256).  The second
+ * limit takes starts to be in order; where they are not and the work passes it,
+ * nothing is written and the status word says PN_EINVAL.
  * workspace: pn_attention_workspace_bytes() bytes, 256-byte aligned, zeroed
  * once (pn_workspace_init); every completed call leaves its counters zeroed.
  * pn_workspace_status reads its status word.  Calls that share a workspace

@@ -771,3 +771,42 @@ def test_attention_more_queries_than_tokens_and_windows(pn, D, lens, counts, hea
     """Queries before the cache see nothing, those behind them what their window and the first tokens hold."""
     case = attention_case(lens, counts, heads, kv, D, 16)
     check_attention(pn, case, max(counts), 0.1, window, sinks, pn.AttentionWorkspace())
+
+
+# ----------------------------------- one long prompt among many requests, long tables --
+MIXED = [
+    # lens, queries of each, max_queries, heads, kv heads, D, page, columns of the table
+    ([90] + [7, 33, 64, 1] * 15 + [200, 16, 3], [40] + [1] * 63, 8192, 64, 8, 128, 16, 8192),
+    ([300] + [20, 45, 1] * 85, [260] + [1] * 255, 2048, 64, 8, 128, 64, 2048),
+    ([70] + [5, 17] * 40, [33] + [1] * 80, 8192, 64, 8, 256, 16, 8192), ([70] + [5, 17] * 40, [33] + [1] * 80, 8192, 64, 8, 64, 16, 8192),
+    ([0] * 16000 + [30, 9, 77] + [0] * 381, [0] * 16000 + [1, 1, 48] + [0] * 381, 48, 8, 8, 64, 1024, 512),
+]
+
+
+@pytest.mark.parametrize("lens,counts,most,heads,kv,D,page,columns", MIXED)
+def test_attention_long_tables(pn, lens, counts, most, heads, kv, D, page, columns):
+    """The bound on the work goes by the queries that there are, not by max_queries for every request."""
+    q, cache, table, lens, starts, ks, vs = attention_case(lens, counts, heads, kv, D, page)
+    wide = np.full((len(lens), columns), 1 << 30, np.int32)
+    wide[:, :table.shape[1]] = table
+    check_attention(pn, (q, cache, wide, lens, starts, ks, vs), most, 1 / math.sqrt(D), workspace=pn.AttentionWorkspace())
+
+
+@pytest.mark.parametrize("D,queries,kv", [(256, 32, 8), (128, 8192, 8)])
+def test_attention_starts_out_of_order(pn, D, queries, kv):
+    """Starts that go up and down make more work than any in order; past 32 bits the call ends at once, and says so."""
+    B, page, columns = 16384, 1024, 512
+    # 8192 requests x 8 heads x 4 groups of 8 rows x (16383 + 1) units = 2^32; 8192 x 8 x 64 tiles of 128 rows x 8192 of 64 tokens = 2^35
+    length = page * columns - (32 if D == 256 else 0)
+    starts = torch.zeros(B + 1, dtype=torch.int32, device="cuda")
+    starts[1::2] = queries
+    lens = torch.full((B,), length, dtype=torch.int32, device="cuda")
+    table = torch.full((B, columns), -1, dtype=torch.int32, device="cuda")
+    cache, ws = pn.kv_cache(1, page, kv, D), pn.AttentionWorkspace()
+    q = torch.ones(queries, kv, D, dtype=torch.float16, device="cuda")
+    out = torch.full_like(q, 7.0)
+    pn.attention(q, cache, table, lens, starts, queries, 0.1, out=out, workspace=ws)
+    assert ws.status() == 1
+    assert torch.all(out == 7.0)
+    case = attention_case([40, 9], [3, 1], 4, 2, 64, 16)
+    check_attention(pn, case, 3, 0.1, workspace=ws)

@@ -126,3 +126,14 @@ def test_wrappers_refuse_cpu_tensors():
     cpu = torch.zeros(2, dtype=torch.int32)
     with pytest.raises((TypeError, ValueError)):
         pn.kv_plan(cpu, cpu, cpu, torch.zeros(2, 2, dtype=torch.int32), cpu, torch.zeros(2, dtype=torch.int64), 16, 2)
+
+
+def test_attention_work_past_32_bits(lib):
+    """Refused on the host: row groups as max_queries allows for, and units by the queries there are."""
+    base = {**ATTENTION, "kv_heads": 8, "q_stride": 512, "batch": 16384}
+    for change in (dict(max_queries=1 << 17), dict(max_queries=1 << 18, head_dim=64),
+                   dict(batch=4, tokens=1 << 20, max_queries=1 << 20, max_pages=1 << 26, table_stride=1 << 26),
+                   dict(batch=16384, tokens=1 << 20, max_queries=64, max_pages=1 << 16, table_stride=1 << 16)):
+        args = {**base, **change}
+        assert list(args) == list(ATTENTION)
+        assert lib.pn_attention(*args.values()) == 3, change
