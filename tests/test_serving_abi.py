@@ -133,7 +133,7 @@ def test_attention_work_past_32_bits(lib):
     base = {**ATTENTION, "kv_heads": 8, "q_stride": 512, "batch": 16384}
     for change in (dict(max_queries=1 << 17), dict(max_queries=1 << 18, head_dim=64),
                    dict(batch=4, tokens=1 << 20, max_queries=1 << 20, max_pages=1 << 26, table_stride=1 << 26),
-                   dict(batch=16384, tokens=1 << 20, max_queries=64, max_pages=1 << 16, table_stride=1 << 16)):
+                   dict(tokens=1 << 20, max_queries=64, max_pages=1 << 18, table_stride=1 << 18)):   # 2^14 x 8 x 2^16
         args = {**base, **change}
         assert list(args) == list(ATTENTION)
         assert lib.pn_attention(*args.values()) == 3, change
