@@ -131,7 +131,7 @@ def test_wrappers_refuse_cpu_tensors():
 def test_attention_work_past_32_bits(lib):
     """Refused on the host: row groups as max_queries allows for, and units by the queries there are."""
     base = {**ATTENTION, "kv_heads": 8, "q_stride": 512, "batch": 16384}
-    for change in (dict(max_queries=1 << 17), dict(max_queries=1 << 18, head_dim=64),
+    for change in (dict(max_queries=1 << 18), dict(max_queries=1 << 17, head_dim=256, q_stride=2048),   # 2^14 x 8 x 2^14 row groups
                    dict(batch=4, tokens=1 << 20, max_queries=1 << 20, max_pages=1 << 26, table_stride=1 << 26),
                    dict(tokens=1 << 20, max_queries=64, max_pages=1 << 18, table_stride=1 << 18)):   # 2^14 x 8 x 2^16
         args = {**base, **change}
