@@ -27,6 +27,23 @@ bool overlaps(const void* a, size_t na, const void* b, size_t nb) {
     return pa < pb + nb && pb < pa + na;
 }
 
+struct Range {
+    const void* p;
+    size_t n;                  // bytes
+};
+// Whether an output shares memory with an input or with another output.  (Blocks read the inputs while others write.)
+template <size_t O, size_t I>
+bool shared(const Range (&out)[O], const Range (&in)[I]) {
+    auto meet = [](const Range& a, const Range& b) { return a.p && b.p && a.n && b.n && overlaps(a.p, a.n, b.p, b.n); };
+    for (size_t o = 0; o < O; ++o) {
+        for (const Range& i : in)
+            if (meet(out[o], i)) return true;
+        for (size_t j = 0; j < o; ++j)
+            if (meet(out[o], out[j])) return true;
+    }
+    return false;
+}
+
 // Pages of the 4-bit cache hold a power of two of tokens, whole records of 16.
 bool page_size_ok(int page_size) { return page_size >= 16 && page_size <= 1024 && (page_size & (page_size - 1)) == 0; }
 
@@ -565,18 +582,12 @@ pn_status pn_kv_plan(const int32_t* lens, const int32_t* add, const int32_t* hel
                           static_cast<const void*>(held_out), static_cast<const void*>(refused)})
         if (!aligned(p, 4)) return PN_EALIGN;
     if (!aligned(ring, 8) || !aligned(ring_out, 8) || !aligned(slots, 8)) return PN_EALIGN;
-    // the blocks read the inputs while others write: no output may be an input or another output
     const size_t nb = static_cast<size_t>(batch) * 4, nc = static_cast<size_t>(capacity);
-    const struct { const void* p; size_t n; } in[] = {{lens, nb}, {add, nb}, {held, nb}, {ring, 16}},
+    const Range in[] = {{lens, nb}, {add, nb}, {held, nb}, {ring, 16}},
         out[] = {{table, (static_cast<size_t>(batch - 1) * table_stride + max_pages) * 4},
                  {free_pages, static_cast<size_t>(pages) * 4}, {slots, nc * 8}, {positions, nc * 4},
                  {requests, nc * 4}, {starts, nb + 4}, {lens_out, nb}, {held_out, nb}, {ring_out, 16}, {refused, 4}};
-    for (size_t i = 0; i < sizeof(out) / sizeof(out[0]); ++i) {
-        for (const auto& q : in)
-            if (overlaps(out[i].p, out[i].n, q.p, q.n)) return PN_EINVAL;
-        for (size_t j = 0; j < i; ++j)
-            if (overlaps(out[i].p, out[i].n, out[j].p, out[j].n)) return PN_EINVAL;
-    }
+    if (shared(out, in)) return PN_EINVAL;
     int sms = 0, major = 0;
     if (pn_status st = device_info(&sms, &major); st != PN_OK) return st;
     const pn::KvPlanArgs a{lens, add, held, batch, table, table_stride, max_pages, free_pages, pages, ring, page_size,
@@ -605,12 +616,13 @@ pn_status pn_kv_append(const void* q, int64_t q_stride, const void* k, int64_t k
         !aligned(q_out, 16))
         return PN_EALIGN;
     const size_t cache_bytes = pn_kv_cache_bytes(pages, page_size, kv_heads, head_dim);
-    const struct { const void* p; size_t n; } in[] = {
-        {q, heads > 0 ? ((tokens - 1) * q_stride + q_cols) * size : 0}, {k, ((tokens - 1) * k_stride + kv_cols) * size},
-        {v, ((tokens - 1) * v_stride + kv_cols) * size}};
-    for (const auto& i : in)
-        if (i.n && (overlaps(i.p, i.n, cache, cache_bytes) || (heads > 0 && overlaps(i.p, i.n, q_out, tokens * q_cols * 2))))
-            return PN_EINVAL;
+    const size_t nt = static_cast<size_t>(tokens), turn = rotary > 0 ? static_cast<size_t>(table_rows) * (rotary / 2) * 4 : 0,
+                 row = static_cast<size_t>(head_dim) * 4;
+    const Range in[] = {{q, heads > 0 ? ((tokens - 1) * q_stride + q_cols) * size : 0}, {k, ((tokens - 1) * k_stride + kv_cols) * size},
+                        {v, ((tokens - 1) * v_stride + kv_cols) * size}, {q_weight, row}, {k_weight, row}, {cos, turn}, {sin, turn},
+                        {positions, rotary > 0 ? nt * 4 : 0}, {slots, nt * 8}},
+                out[] = {{cache, cache_bytes}, {q_out, nt * q_cols * 2}};
+    if (shared(out, in)) return PN_EINVAL;
     int sms = 0, major = 0;
     if (pn_status st = device_info(&sms, &major); st != PN_OK) return st;
     const pn::KvAppendArgs a{q, k, v, q_stride, k_stride, v_stride, dtype == PN_DTYPE_F16, tokens, heads, q_weight,
@@ -629,7 +641,8 @@ pn_status pn_kv_read(const void* cache, int64_t pages, int page_size, int kv_hea
     if (!aligned(cache, 16) || !aligned(slots, 8) || !aligned(k, 16) || !aligned(v, 16)) return PN_EALIGN;
     const size_t n = static_cast<size_t>(tokens) * kv_heads * head_dim * 4;
     const size_t bytes = pn_kv_cache_bytes(pages, page_size, kv_heads, head_dim);
-    if (overlaps(k, n, v, n) || overlaps(k, n, cache, bytes) || overlaps(v, n, cache, bytes)) return PN_EINVAL;
+    const Range in[] = {{cache, bytes}, {slots, static_cast<size_t>(tokens) * 8}}, out[] = {{k, n}, {v, n}};
+    if (shared(out, in)) return PN_EINVAL;
     int sms = 0, major = 0;
     if (pn_status st = device_info(&sms, &major); st != PN_OK) return st;
     const pn::KvGeometry g{static_cast<uint8_t*>(const_cast<void*>(cache)), pages, page_size, kv_heads, head_dim};
@@ -662,9 +675,11 @@ pn_status pn_attention(const uint16_t* q, int64_t q_stride, int64_t tokens, int 
     if (!aligned(q, 16) || q_stride % 8 || !aligned(cache, 16) || !aligned(table, 4) || !aligned(lens, 4) ||
         !aligned(starts, 4) || !aligned(out, 16) || !aligned(lse, 4) || !aligned(workspace, 256))
         return PN_EALIGN;
-    const size_t nq = (static_cast<size_t>(tokens - 1) * q_stride + cols) * 2, no = static_cast<size_t>(tokens) * cols * 2;
-    if (overlaps(q, nq, out, no) || overlaps(cache, pn_kv_cache_bytes(pages, page_size, kv_heads, head_dim), out, no))
-        return PN_EINVAL;
+    const size_t nt = static_cast<size_t>(tokens), nb = static_cast<size_t>(batch) * 4;
+    const Range ins[] = {{q, ((nt - 1) * q_stride + cols) * 2}, {cache, pn_kv_cache_bytes(pages, page_size, kv_heads, head_dim)},
+                         {table, (static_cast<size_t>(batch - 1) * table_stride + max_pages) * 4}, {lens, nb}, {starts, nb + 4}},
+                outs[] = {{out, nt * cols * 2}, {lse, nt * heads * 4}, {workspace, workspace_bytes}};
+    if (shared(outs, ins)) return PN_EINVAL;
     // no request has more cached tokens than its row of the table has room for: a window of as many hides nothing, and
     // no more first tokens are there (with both below 2^31 - 128 no index of a tile passes 32 bits)
     const int room = max_pages * page_size;
@@ -693,8 +708,12 @@ pn_status pn_verify(const int32_t* tokens, const float* target, int64_t target_s
     if (!aligned(tokens, 4) || !aligned(target, 4) || !aligned(draft, 4) || !aligned(uniforms, 4) ||
         !aligned(counts, 4) || !aligned(accepted, 4) || !aligned(out, 4))
         return PN_EALIGN;
-    const size_t nt = static_cast<size_t>(batch) * drafts * 4, no = nt + static_cast<size_t>(batch) * 4;
-    if (overlaps(tokens, nt, out, no) || overlaps(accepted, static_cast<size_t>(batch) * 4, out, no)) return PN_EINVAL;
+    const size_t nb = static_cast<size_t>(batch) * 4, nt = nb * drafts, row = static_cast<size_t>(vocab) * 4;
+    const Range ins[] = {{tokens, nt}, {target, (static_cast<size_t>(batch) * (drafts + 1) - 1) * target_stride * 4 + row},
+                         {draft, drafts > 0 ? (static_cast<size_t>(batch) * drafts - 1) * draft_stride * 4 + row : 0},
+                         {uniforms, nt + nb}, {counts, nb}},
+                outs[] = {{accepted, nb}, {out, nt + nb}};
+    if (shared(outs, ins)) return PN_EINVAL;
     int sms = 0, major = 0;
     if (pn_status st = device_info(&sms, &major); st != PN_OK) return st;
     if (major < 9) return PN_EUNSUPPORTED;

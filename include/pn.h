@@ -408,7 +408,8 @@ pn_status pn_kv_plan(const int32_t* lens, const int32_t* add, const int32_t* hel
  * 1 / head_dim; fp32 quotients and square roots are IEEE.  Inputs must be
  * finite (else that head's codes are unspecified).  q_out and cache 16-byte
  * aligned, other arrays to their element.  No two tokens of a call may share
- * a slot.  heads = 0: keys and values alone.
+ * a slot.  heads = 0: keys and values alone.  q_out and cache share no memory
+ * with each other or an input (PN_EINVAL).
  */
 typedef enum { PN_DTYPE_F32 = 0, PN_DTYPE_F16 = 1 } pn_dtype;
 pn_status pn_kv_append(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
@@ -419,7 +420,7 @@ pn_status pn_kv_append(const void* q, int64_t q_stride, const void* k, int64_t k
 
 /* pn_kv_read: the cached keys and values of `tokens` slots as fp32
  * [tokens][kv_heads][head_dim], exact; zeros for a slot outside the cache.
- * k and v 16-byte aligned. */
+ * k and v 16-byte aligned, sharing no memory with each other or an input. */
 pn_status pn_kv_read(const void* cache, int64_t pages, int page_size, int kv_heads, int head_dim,
                      const int64_t* slots, int64_t tokens, float* k, float* v, pn_stream stream);
 
@@ -456,7 +457,8 @@ pn_status pn_kv_read(const void* cache, int64_t pages, int page_size, int kv_hea
  * once (pn_workspace_init); every completed call leaves its counters zeroed.
  * pn_workspace_status reads its status word.  Calls that share a workspace
  * must be ordered on one stream.  q, cache and out 16-byte aligned, q_stride a
- * multiple of 8.
+ * multiple of 8; out, lse and workspace share no memory with each other or an
+ * input.
  */
 size_t pn_attention_workspace_bytes(void);
 pn_status pn_attention(const uint16_t* q, int64_t q_stride, int64_t tokens, int heads, const void* cache,
@@ -481,7 +483,8 @@ pn_status pn_attention(const uint16_t* q, int64_t q_stride, int64_t tokens, int 
  * after the last draft, max(p - q, 0) where draft n was turned down (p itself
  * should that leave nothing), each limited to [0, 1] (NaN: 0) and rounded to a
  * whole multiple of 2^-42, so that the token does not depend on the order of
- * the sums.  -1 if the whole row weighs nothing.
+ * the sums.  -1 if the whole row weighs nothing.  accepted and out share no
+ * memory with each other or an input (counts among them).
  */
 #define PN_MAX_DRAFTS 31
 #define PN_MAX_VOCAB (1 << 20)

@@ -133,7 +133,25 @@ def test_attention_work_past_32_bits(lib):
     base = {**ATTENTION, "kv_heads": 8, "q_stride": 512, "batch": 16384}
     for change in (dict(max_queries=1 << 18), dict(max_queries=1 << 17, head_dim=256, q_stride=2048),   # 2^14 x 8 x 2^14 row groups
                    dict(batch=4, tokens=1 << 20, max_queries=1 << 20, max_pages=1 << 26, table_stride=1 << 26),
-                   dict(tokens=1 << 20, max_queries=64, max_pages=1 << 18, table_stride=1 << 18)):   # 2^14 x 8 x 2^16
+                   dict(tokens=1 << 20, max_queries=64, max_pages=1 << 18, table_stride=1 << 18, table=at(100))):   # 2^14 x 8 x 2^16
         args = {**base, **change}
         assert list(args) == list(ATTENTION)
         assert lib.pn_attention(*args.values()) == 3, change
+
+
+SHARED = [
+    ("pn_kv_append", APPEND, [dict(q_out=at(9) + 64), dict(q_out=at(3)), dict(q_out=at(4)), dict(q_out=at(5)), dict(q_out=at(6)), dict(q_out=at(7)),
+                              dict(q_out=at(8)), dict(cache=at(8)), dict(cache=at(5)), dict(cache=at(3)), dict(q_out=at(1) + 256), dict(cache=at(2))]),
+    ("pn_kv_read", READ, [dict(k=at(1)), dict(v=at(1)), dict(v=at(2) + 512)]),
+    ("pn_attention", ATTENTION, [dict(out=at(2)), dict(out=at(3)), dict(out=at(4)), dict(out=at(7) + 4096), dict(lse=at(0)), dict(lse=at(1) + 4),
+                                 dict(lse=at(2)), dict(lse=at(3)), dict(lse=at(4) + 8), dict(lse=at(5) + 32), dict(lse=at(7)), dict(workspace=at(0)),
+                                 dict(workspace=at(3)), dict(workspace=at(1))]),
+    ("pn_verify", VERIFY, [dict(accepted=at(4)), dict(accepted=at(0)), dict(accepted=at(3) + 4), dict(accepted=at(1)), dict(accepted=at(2) + 2396),
+                           dict(out=at(1) + 3196), dict(out=at(2)), dict(out=at(3)), dict(out=at(4) + 4), dict(counts=at(5) + 4)]),
+]
+
+
+@pytest.mark.parametrize("name,good,changes", SHARED, ids=[r[0] for r in SHARED])
+def test_outputs_share_no_memory(lib, name, good, changes):
+    for change in changes:
+        assert getattr(lib, name)(*{**good, **change}.values()) == PN_EINVAL, change
