@@ -400,11 +400,6 @@ __device__ __forceinline__ void take_tile(const uint8_t* stage, int tok0, uint32
     uint32_t seen = 0xFFFFFFFFu;
     if constexpr (kMasked) {
         seen = 0;
-        int from[NT][2];
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int c = 0; c < 2; ++c) from[n][c] = window_first(Q.pos[n][c], window);
 #pragma unroll
         for (int r = 0; r < kTileRecords; ++r)
 #pragma unroll
@@ -414,7 +409,7 @@ __device__ __forceinline__ void take_tile(const uint8_t* stage, int tok0, uint32
 #pragma unroll
                     for (int c = 0; c < 2; ++c) {
                         const int tok = tok0 + r * kKvTokens + hh * 8 + g;
-                        const bool s = ((valid >> r) & 1) && tok <= Q.pos[n][c] && (tok >= from[n][c] || tok < sinks);
+                        const bool s = ((valid >> r) & 1) && tok <= Q.pos[n][c] && (tok > Q.pos[n][c] - window || tok < sinks);
                         seen |= static_cast<uint32_t>(s) << (((r * 2 + hh) * NT + n) * 2 + c);
                     }
     }
@@ -577,15 +572,11 @@ __global__ void __launch_bounds__(Smem<D, NT>::kThreads, 1) attn_kernel(const __
         if (threadIdx.x == M::kThreads - 1) {
             uint32_t all = 0;
             for (int w = 0; w <= W; ++w) all = add_units(all, warp_sums[w]);
-            prefix[a.batch] = all;
+            prefix[a.batch] = all_units(P, all);
         }
         __syncthreads();
     }
-    uint32_t total = prefix[a.batch];
-    if (total == kTooManyUnits) {                                        // starts out of order: nothing is written
-        if (threadIdx.x == 0 && blockIdx.x == 0) atomicCAS(P.status, 0u, kAttnInvalid);
-        total = 0;
-    }
+    const uint32_t total = prefix[a.batch];
     uint32_t blocks = min(gridDim.x, (total + W - 1) / W);
     // One request with short segments: a block to a segment, so that nothing is
     // joined over blocks (that takes longer than four tiles to a warp do).
@@ -739,7 +730,7 @@ __global__ void __launch_bounds__(Smem<D, NT>::kThreads, 1) attn_kernel(const __
                 const uint8_t* data = smem + stage * S::kStage;
                 if (tok0 > pos_hi) {
                     // no row sees this tile
-                } else if (have == (1u << kTileRecords) - 1 && tok0 + kTile - 1 <= pos_lo && (tok0 >= window_first(pos_hi, window) || tok0 + kTile <= a.sinks)) {
+                } else if (have == (1u << kTileRecords) - 1 && tok0 + kTile - 1 <= pos_lo && (tok0 > pos_hi - window || tok0 + kTile <= a.sinks)) {
                     take_tile<D, NT, false>(data, tok0, have, Q, window, a.sinks, st);
                 } else {
                     take_tile<D, NT, true>(data, tok0, have, Q, window, a.sinks, st);

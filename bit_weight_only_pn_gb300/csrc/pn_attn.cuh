@@ -46,9 +46,14 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
 }
 
 // Sums of units that stop at 2^32 - 1, which no call reaches whose starts are in
-// order (the host sees to that); where they are not, the kernels stop there.
+// order (the host sees to that).  One that does has no units: nothing is written.
 constexpr uint32_t kTooManyUnits = 0xFFFFFFFFu;
 __device__ __forceinline__ uint32_t add_units(uint32_t a, uint32_t b) { return a + b < a ? kTooManyUnits : a + b; }
+__device__ __forceinline__ uint32_t all_units(const AttnParams& P, uint32_t all) {
+    if (all != kTooManyUnits) return all;
+    atomicCAS(P.status, 0u, kAttnInvalid);
+    return 0u;
+}
 
 // Nanoseconds in SM cycles, at the fastest clock: limits are at least as long as asked.
 __device__ __forceinline__ int64_t cycles_of(uint64_t ns) { return static_cast<int64_t>(ns) * 21 / 10; }

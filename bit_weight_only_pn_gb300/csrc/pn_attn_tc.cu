@@ -437,11 +437,10 @@ template <int D>
 __device__ __noinline__ RowState half_tile_masked(RowState st, uint32_t ts, uint32_t tp, uint32_t to, const float* sc, float big, int tok,
                                                   uint32_t have, int pos, int window, int sinks, float* most, uint32_t before,
                                                   uint32_t parity, uint64_t limit_ns, volatile uint32_t* abort) {
-    const int from = window_first(pos, window);
     uint32_t seen = 0;
 #pragma unroll
     for (int c = 0; c < Shape<D>::kPart; ++c) {
-        const bool s = ((have >> (c / 16)) & 1u) && tok + c <= pos && (tok + c >= from || tok + c < sinks);
+        const bool s = ((have >> (c / 16)) & 1u) && tok + c <= pos && (tok + c > pos - window || tok + c < sinks);
         seen |= static_cast<uint32_t>(s) << c;
     }
     return half_tile<D, true>(st, ts, tp, to, sc, big, seen, most, before, parity, limit_ns, abort);
@@ -524,17 +523,13 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
         for (int i = 0; i < warp; ++i) at = add_units(at, warp_sums[i]);
         for (int i = 0; i < kThreads / 32; ++i) segments += warp_sums[kThreads / 32 + i];
         scan[threadIdx.x] = at;
-        if (threadIdx.x == kThreads - 1) scan[kThreads] = add_units(at, mine);
+        if (threadIdx.x == kThreads - 1) scan[kThreads] = all_units(P, add_units(at, mine));
     }
     tc_fence_before_sync();
     __syncthreads();
     tc_fence_after_sync();
     const uint32_t tmem = misc[0];
-    uint32_t total = scan[kThreads];
-    if (total == kTooManyUnits) {                      // starts out of order: nothing is written
-        if (threadIdx.x == 0 && blockIdx.x == 0) atomicCAS(P.status, 0u, kAttnInvalid);
-        total = 0;
-    }
+    const uint32_t total = scan[kThreads];
     // A block shares a segment of T tiles for no less than sqrt(T D / 256) of them:
     // a tile takes about a microsecond, and so does the join of a part for every 256
     // values of a head, which one block does for all parts.
@@ -859,7 +854,7 @@ __global__ void __launch_bounds__(kThreads, 1) attn_tc_kernel(const __grid_const
                 }
                 const float big = log2_scale(most);
                 const uint32_t have = have_of[buf];
-                const bool plain = have == M::kAll && tok0 + kTile - 1 <= pos_lo && (tok0 >= window_first(pos_hi, window) || tok0 + kTile <= a.sinks);
+                const bool plain = have == M::kAll && tok0 + kTile - 1 <= pos_lo && (tok0 > pos_hi - window || tok0 + kTile <= a.sinks);
                 if (i > 0) tell();
                 there = there && wait_phase(s_full + 8 * place, s_turn & 1u, P.timeout_ns, abort);
                 st.ok = __all_sync(0xFFFFFFFFu, there);
