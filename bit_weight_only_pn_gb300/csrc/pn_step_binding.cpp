@@ -41,24 +41,39 @@ const char* type_name(at::ScalarType t) {
     }
 }
 
-const at::Tensor& cuda_tensor(PyObject* o, const char* name) {
+// The device of a call's tensors: the first one's, and the others have to be there too.
+struct Device {
+    int index = -1;
+    const char* of = "";
+    void take(const at::Tensor& t, const char* name) {
+        if (index < 0) {
+            index = t.get_device();
+            of = name;
+        } else if (t.get_device() != index) {
+            fail(PyExc_ValueError, "%s must be on the device of %s", name, of);
+        }
+    }
+};
+
+const at::Tensor& cuda_tensor(Device& on, PyObject* o, const char* name) {
     if (!THPVariable_Check(o)) fail(PyExc_TypeError, "%s must be a CUDA tensor", name);
     const at::Tensor& t = THPVariable_Unpack(o);
     if (!t.is_cuda()) fail(PyExc_TypeError, "%s must be a CUDA tensor", name);
+    on.take(t, name);
     return t;
 }
 
-const at::Tensor& dense(PyObject* o, at::ScalarType type, const char* name) {
-    const at::Tensor& t = cuda_tensor(o, name);
+const at::Tensor& dense(Device& on, PyObject* o, at::ScalarType type, const char* name) {
+    const at::Tensor& t = cuda_tensor(on, o, name);
     if (t.scalar_type() != type) fail(PyExc_TypeError, "%s must be %s", name, type_name(type));
     if (!t.is_contiguous()) fail(PyExc_ValueError, "%s must be contiguous", name);
     return t;
 }
 
 // None, or a dense tensor of n entries.
-const at::Tensor* optional(PyObject* o, at::ScalarType type, int64_t n, const char* name, const char* shape) {
+const at::Tensor* optional(Device& on, PyObject* o, at::ScalarType type, int64_t n, const char* name, const char* shape) {
     if (o == Py_None) return nullptr;
-    const at::Tensor& t = dense(o, type, name);
+    const at::Tensor& t = dense(on, o, type, name);
     if (t.numel() != n) fail(PyExc_ValueError, "%s must be %s", name, shape);
     return &t;
 }
@@ -85,8 +100,8 @@ float real(PyObject* o) {
 }
 
 // int32 rows of a page table.
-const at::Tensor& page_table(PyObject* o, int64_t batch) {
-    const at::Tensor& t = cuda_tensor(o, "table");
+const at::Tensor& page_table(Device& on, PyObject* o, int64_t batch) {
+    const at::Tensor& t = cuda_tensor(on, o, "table");
     if (t.scalar_type() != at::kInt) fail(PyExc_TypeError, "%s must be a CUDA int32 tensor", "table");
     if (t.dim() != 2 || t.size(0) != batch || (t.size(1) > 1 && t.stride(1) != 1))
         fail(PyExc_ValueError, "%s must be [batch][pages per request] with contiguous rows", "table");
@@ -96,8 +111,8 @@ const at::Tensor& page_table(PyObject* o, int64_t batch) {
 int64_t table_stride(const at::Tensor& t) { return t.size(0) > 1 ? t.stride(0) : t.size(1); }
 
 // [tokens][heads][dim] whose heads are contiguous within a token.
-const at::Tensor& rows(PyObject* o, const char* name, at::ScalarType a, at::ScalarType b, int64_t heads, int64_t dim) {
-    const at::Tensor& t = cuda_tensor(o, name);
+const at::Tensor& rows(Device& on, PyObject* o, const char* name, at::ScalarType a, at::ScalarType b, int64_t heads, int64_t dim) {
+    const at::Tensor& t = cuda_tensor(on, o, name);
     if (t.scalar_type() != a && t.scalar_type() != b)
         fail(PyExc_TypeError, a == b ? "%s must be %s" : "%s must be torch.float32 or torch.float16", name, type_name(a));
     if (t.dim() != 3 || t.size(2) != dim || (heads >= 0 && t.size(1) != heads))
@@ -113,7 +128,7 @@ struct Cache {
     const at::Tensor& t;
     int64_t pages;
     int page_size, heads, dim;
-    explicit Cache(PyObject* o) : t(dense(o, at::kByte, "cache")) {
+    Cache(Device& on, PyObject* o) : t(dense(on, o, at::kByte, "cache")) {
         if (t.dim() != 4 || t.size(3) % 17 || t.size(1) > 65536 || t.size(2) > 65536 || t.size(3) > 65536)
             fail(PyExc_ValueError, "%s must be uint8 [pages][kv_heads][page_size / 16][17 * head_dim]", "cache");
         pages = t.size(0);
@@ -162,39 +177,41 @@ PyObject* given_or(PyObject* given, const at::Tensor& made) {
 
 // lens, add, held, table, free, ring, page_size, capacity, out (None or the eight tensors)
 PyObject* kv_plan(PyObject* const* a) {
-    const at::Tensor& lens = dense(a[0], at::kInt, "lens");
-    const at::Tensor& add = dense(a[1], at::kInt, "add");
-    const at::Tensor& held = dense(a[2], at::kInt, "held");
-    const at::Tensor& free = dense(a[4], at::kInt, "free");
-    const at::Tensor& ring = dense(a[5], at::kLong, "ring");
+    Device on;
+    const at::Tensor& lens = dense(on, a[0], at::kInt, "lens");
+    const at::Tensor& add = dense(on, a[1], at::kInt, "add");
+    const at::Tensor& held = dense(on, a[2], at::kInt, "held");
+    const at::Tensor& free = dense(on, a[4], at::kInt, "free");
+    const at::Tensor& ring = dense(on, a[5], at::kLong, "ring");
     const int64_t B = lens.numel();
-    const at::Tensor& table = page_table(a[3], B);
+    const at::Tensor& table = page_table(on, a[3], B);
     if (add.numel() != B || held.numel() != B || ring.numel() != 2)
         fail(PyExc_ValueError, "%s, add and held must have one entry per request and ring two", "lens");
     const int page_size = number(a[6], "page_size");
     const int64_t T = whole(a[7]);
     if (T < 0) fail(PyExc_ValueError, "%s must not be negative", "capacity");
     if (B > INT32_MAX) fail(PyExc_ValueError, "%s has too many entries", "lens");
-    const c10::cuda::CUDAGuard guard(lens.device());
     static const char* const names[8] = {"out.slots", "out.positions", "out.requests", "out.starts", "out.lens", "out.held", "out.ring", "out.refused"};
     const int64_t sizes[8] = {T, T, T, B + 1, B, B, 2, 1};
     at::Tensor o[8];
     PyObject* given[8];
     const bool have = a[8] != Py_None;
     if (have && (!PyTuple_Check(a[8]) || PyTuple_GET_SIZE(a[8]) != 8)) fail(PyExc_TypeError, "%s must be a KvPlan", "out");
-    at::Tensor all;                            // 64-bit outputs first
-    int64_t wide_at = 0, narrow_at = (T + 2) * 8;
-    if (!have) all = fresh({narrow_at + (2 * T + 3 * B + 2) * 4}, at::kByte);
+    auto type_of = [](int i) { return i == 0 || i == 6 ? at::kLong : at::kInt; };
     for (int i = 0; i < 8; ++i) {
-        const at::ScalarType type = i == 0 || i == 6 ? at::kLong : at::kInt;
         given[i] = have ? PyTuple_GET_ITEM(a[8], i) : Py_None;
-        if (have) {
-            o[i] = dense(given[i], type, names[i]);
-            if (o[i].numel() != sizes[i]) fail(PyExc_ValueError, "%s has another size", names[i]);
-        } else {
-            int64_t& from = type == at::kLong ? wide_at : narrow_at;
-            o[i] = part_of(all, from, sizes[i], type);
-            from += sizes[i] * (type == at::kLong ? 8 : 4);
+        if (!have) continue;
+        o[i] = dense(on, given[i], type_of(i), names[i]);
+        if (o[i].numel() != sizes[i]) fail(PyExc_ValueError, "%s has another size", names[i]);
+    }
+    const c10::cuda::CUDAGuard guard(lens.device());
+    if (!have) {
+        int64_t wide_at = 0, narrow_at = (T + 2) * 8;      // 64-bit outputs first
+        const at::Tensor all = fresh({narrow_at + (2 * T + 3 * B + 2) * 4}, at::kByte);
+        for (int i = 0; i < 8; ++i) {
+            int64_t& from = type_of(i) == at::kLong ? wide_at : narrow_at;
+            o[i] = part_of(all, from, sizes[i], type_of(i));
+            from += sizes[i] * (type_of(i) == at::kLong ? 8 : 4);
         }
     }
     const pn_status st = pn_kv_plan(data<int32_t>(&lens), data<int32_t>(&add), data<int32_t>(&held), static_cast<int>(B), data<int32_t>(&table),
@@ -208,39 +225,38 @@ PyObject* kv_plan(PyObject* const* a) {
 
 // q, k, v, cache, slots, positions, cos, sin, q_weight, k_weight, eps, interleaved, q_out
 PyObject* kv_append(PyObject* const* a) {
-    const Cache c(a[3]);
-    const at::Tensor& k = rows(a[1], "k", at::kFloat, at::kHalf, c.heads, c.dim);
+    Device on;
+    const Cache c(on, a[3]);
+    const at::Tensor& k = rows(on, a[1], "k", at::kFloat, at::kHalf, c.heads, c.dim);
     const at::ScalarType type = k.scalar_type();
-    const at::Tensor& v = rows(a[2], "v", type, type, c.heads, c.dim);
-    const at::Tensor* q = a[0] == Py_None ? nullptr : &rows(a[0], "q", type, type, -1, c.dim);
+    const at::Tensor& v = rows(on, a[2], "v", type, type, c.heads, c.dim);
+    const at::Tensor* q = a[0] == Py_None ? nullptr : &rows(on, a[0], "q", type, type, -1, c.dim);
     const int64_t T = k.size(0), heads = q ? q->size(1) : 0;
     if (v.size(0) != T || (q && q->size(0) != T)) fail(PyExc_ValueError, "%s, k and v must have the same tokens", "q");
     if (heads > INT32_MAX) fail(PyExc_ValueError, "%s has too many heads", "q");
-    const at::Tensor* slots = optional(a[4], at::kLong, T, "slots", "one entry per token");
+    const at::Tensor* slots = optional(on, a[4], at::kLong, T, "slots", "one entry per token");
     if (!slots) fail(PyExc_TypeError, "%s must be a CUDA tensor", "slots");
     const at::Tensor *cos = nullptr, *sin = nullptr, *positions = nullptr;
     int64_t pairs = 0, table_rows = 0;
     if (a[6] != Py_None || a[7] != Py_None) {
-        cos = &dense(a[6], at::kFloat, "cos");
-        sin = &dense(a[7], at::kFloat, "sin");
+        cos = &dense(on, a[6], at::kFloat, "cos");
+        sin = &dense(on, a[7], at::kFloat, "sin");
         if (cos->dim() != 2 || cos->sizes() != sin->sizes()) fail(PyExc_ValueError, "%s and sin must be [positions][rotated pairs]", "cos");
         table_rows = cos->size(0);
         pairs = cos->size(1);
-        positions = optional(a[5], at::kInt, T, "positions", "one entry per token");
+        positions = optional(on, a[5], at::kInt, T, "positions", "one entry per token");
         if (!positions) fail(PyExc_TypeError, "%s must be a CUDA tensor", "positions");
         if (pairs > 65536) fail(PyExc_ValueError, "%s has too many columns", "cos");
     }
-    const at::Tensor* qw = optional(a[8], at::kFloat, c.dim, "q_weight", "[head_dim]");
-    const at::Tensor* kw = optional(a[9], at::kFloat, c.dim, "k_weight", "[head_dim]");
+    const at::Tensor* qw = optional(on, a[8], at::kFloat, c.dim, "q_weight", "[head_dim]");
+    const at::Tensor* kw = optional(on, a[9], at::kFloat, c.dim, "k_weight", "[head_dim]");
     const float eps = real(a[10]);
     const int interleaved = PyObject_IsTrue(a[11]);
     if (interleaved < 0) throw PythonError{};
+    const at::Tensor* given = q ? optional(on, a[12], at::kHalf, T * heads * c.dim, "q_out", "[tokens][heads][head_dim]") : nullptr;
     const c10::cuda::CUDAGuard guard(k.device());
     at::Tensor out;
-    if (q) {
-        const at::Tensor* given = optional(a[12], at::kHalf, T * heads * c.dim, "q_out", "[tokens][heads][head_dim]");
-        out = given ? *given : fresh({T, heads, c.dim}, at::kHalf);
-    }
+    if (q) out = given ? *given : fresh({T, heads, c.dim}, at::kHalf);
     const pn_status st = pn_kv_append(data<void>(q), q ? row_stride(*q) : 0, data<void>(&k), row_stride(k), data<void>(&v), row_stride(v),
                                       type == at::kFloat ? PN_DTYPE_F32 : PN_DTYPE_F16, T, static_cast<int>(heads), data<float>(qw),
                                       data<float>(kw), eps, data<float>(cos), data<float>(sin), table_rows, static_cast<int>(2 * pairs),
@@ -251,12 +267,13 @@ PyObject* kv_append(PyObject* const* a) {
 
 // cache, slots, k, v (None, None: new ones)
 PyObject* kv_read(PyObject* const* a) {
-    const Cache c(a[0]);
-    const at::Tensor& slots = dense(a[1], at::kLong, "slots");
+    Device on;
+    const Cache c(on, a[0]);
+    const at::Tensor& slots = dense(on, a[1], at::kLong, "slots");
     const int64_t T = slots.numel(), n = T * c.heads * c.dim;
+    const at::Tensor* gk = optional(on, a[2], at::kFloat, n, "out", "two tensors [tokens][kv_heads][head_dim]");
+    const at::Tensor* gv = optional(on, a[3], at::kFloat, n, "out", "two tensors [tokens][kv_heads][head_dim]");
     const c10::cuda::CUDAGuard guard(slots.device());
-    const at::Tensor* gk = optional(a[2], at::kFloat, n, "out", "two tensors [tokens][kv_heads][head_dim]");
-    const at::Tensor* gv = optional(a[3], at::kFloat, n, "out", "two tensors [tokens][kv_heads][head_dim]");
     const at::Tensor k = gk ? *gk : fresh({T, c.heads, c.dim}, at::kFloat);
     const at::Tensor v = gv ? *gv : fresh({T, c.heads, c.dim}, at::kFloat);
     const pn_status st = pn_kv_read(c.t.data_ptr(), c.pages, c.page_size, c.heads, c.dim, data<int64_t>(&slots), T, data<float>(&k),
@@ -264,26 +281,25 @@ PyObject* kv_read(PyObject* const* a) {
     return answer(st, {given_or(a[2], k), given_or(a[3], v)});
 }
 
-// q, cache, table, lens, starts, max_queries, scale, window, sinks, out, lse, return_lse, workspace pointer, its bytes
+// q, cache, table, lens, starts, max_queries, scale, window, sinks, out, lse, return_lse, workspace
 PyObject* attention(PyObject* const* a) {
-    const Cache c(a[1]);
-    const at::Tensor& q = rows(a[0], "q", at::kHalf, at::kHalf, -1, c.dim);
+    Device on;
+    const Cache c(on, a[1]);
+    const at::Tensor& q = rows(on, a[0], "q", at::kHalf, at::kHalf, -1, c.dim);
     const int64_t T = q.size(0), heads = q.size(1);
-    const at::Tensor& lens = dense(a[3], at::kInt, "lens");
-    const at::Tensor& starts = dense(a[4], at::kInt, "starts");
+    const at::Tensor& lens = dense(on, a[3], at::kInt, "lens");
+    const at::Tensor& starts = dense(on, a[4], at::kInt, "starts");
     const int64_t B = lens.numel();
-    const at::Tensor& table = page_table(a[2], B);
+    const at::Tensor& table = page_table(on, a[2], B);
     if (starts.numel() != B + 1) fail(PyExc_ValueError, "%s must have one entry more than lens", "starts");
     if (B > INT32_MAX || heads > INT32_MAX) fail(PyExc_ValueError, "%s has too many entries", "lens or q");
     const int max_queries = number(a[5], "max_queries"), window = number(a[7], "window"), sinks = number(a[8], "sinks");
     const float scale = real(a[6]);
-    const at::Tensor* given = optional(a[9], at::kHalf, T * heads * c.dim, "out", "[tokens][heads][head_dim]");
-    const at::Tensor* lse = optional(a[10], at::kFloat, T * heads, "lse", "[tokens][heads]");
+    const at::Tensor* given = optional(on, a[9], at::kHalf, T * heads * c.dim, "out", "[tokens][heads][head_dim]");
+    const at::Tensor* lse = optional(on, a[10], at::kFloat, T * heads, "lse", "[tokens][heads]");
     const int want_lse = PyObject_IsTrue(a[11]);
     if (want_lse < 0) throw PythonError{};
-    void* workspace = PyLong_AsVoidPtr(a[12]);
-    if (!workspace && PyErr_Occurred()) throw PythonError{};
-    const int64_t bytes = whole(a[13]);
+    const at::Tensor& workspace = dense(on, a[12], at::kByte, "workspace");
     const c10::cuda::CUDAGuard guard(q.device());
     const at::Tensor out = given ? *given : fresh({T, heads, c.dim}, at::kHalf);
     at::Tensor made;
@@ -294,15 +310,16 @@ PyObject* attention(PyObject* const* a) {
     const pn_status st = pn_attention(data<uint16_t>(&q), row_stride(q), T, static_cast<int>(heads), c.t.data_ptr(), c.pages, c.page_size,
                                       c.heads, c.dim, data<int32_t>(&table), table_stride(table), static_cast<int>(table.size(1)),
                                       data<int32_t>(&lens), data<int32_t>(&starts), static_cast<int>(B), max_queries, scale, window, sinks,
-                                      data<uint16_t>(&out), data<float>(lse), workspace, static_cast<size_t>(bytes), stream_of(q));
+                                      data<uint16_t>(&out), data<float>(lse), workspace.data_ptr(), static_cast<size_t>(workspace.numel()), stream_of(q));
     return answer(st, {given_or(a[9], out), lse ? given_or(a[10], *lse) : nullptr});
 }
 
 // tokens, target, draft, uniforms, counts, accepted, out
 PyObject* verify(PyObject* const* a) {
-    const at::Tensor& tokens = dense(a[0], at::kInt, "tokens");
-    const at::Tensor& target = dense(a[1], at::kFloat, "target");
-    const at::Tensor& uniforms = dense(a[3], at::kFloat, "uniforms");
+    Device on;
+    const at::Tensor& tokens = dense(on, a[0], at::kInt, "tokens");
+    const at::Tensor& target = dense(on, a[1], at::kFloat, "target");
+    const at::Tensor& uniforms = dense(on, a[3], at::kFloat, "uniforms");
     if (tokens.dim() != 2 || target.dim() != 3)
         fail(PyExc_ValueError, "%s must be [batch][drafts] and target [batch][drafts + 1][vocab]", "tokens");
     const int64_t B = tokens.size(0), K = tokens.size(1), V = target.size(2);
@@ -310,14 +327,14 @@ PyObject* verify(PyObject* const* a) {
         fail(PyExc_ValueError, "%s and uniforms must have one row more than there are drafts", "target");
     const at::Tensor* draft = nullptr;
     if (a[2] != Py_None) {
-        draft = &dense(a[2], at::kFloat, "draft");
+        draft = &dense(on, a[2], at::kFloat, "draft");
         if (draft->dim() != 3 || draft->size(0) != B || draft->size(1) != K || draft->size(2) != V)
             fail(PyExc_ValueError, "%s must be [batch][drafts][vocab]", "draft");
     }
     if (B > INT32_MAX || K > INT32_MAX || V > INT32_MAX) fail(PyExc_ValueError, "%s is too large", "target");
-    const at::Tensor* counts = optional(a[4], at::kInt, B, "counts", "one entry per request");
-    const at::Tensor* given_accepted = optional(a[5], at::kInt, B, "accepted", "[batch]");
-    const at::Tensor* given_out = optional(a[6], at::kInt, B * (K + 1), "out", "[batch][drafts + 1]");
+    const at::Tensor* counts = optional(on, a[4], at::kInt, B, "counts", "one entry per request");
+    const at::Tensor* given_accepted = optional(on, a[5], at::kInt, B, "accepted", "[batch]");
+    const at::Tensor* given_out = optional(on, a[6], at::kInt, B * (K + 1), "out", "[batch][drafts + 1]");
     const c10::cuda::CUDAGuard guard(target.device());
     const at::Tensor accepted = given_accepted ? *given_accepted : fresh({B}, at::kInt);
     const at::Tensor out = given_out ? *given_out : fresh({B, K + 1}, at::kInt);
@@ -351,7 +368,7 @@ PyMethodDef method(const char* name) {
 }
 
 PyMethodDef g_methods[] = {method<kv_plan, 9>("kv_plan"), method<kv_append, 13>("kv_append"), method<kv_read, 4>("kv_read"),
-                           method<attention, 14>("attention"), method<verify, 7>("verify"), {nullptr, nullptr, 0, nullptr}};
+                           method<attention, 13>("attention"), method<verify, 7>("verify"), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_step", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

@@ -529,7 +529,7 @@ def attention(q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, lens: t
         with torch.cuda.stream(stream):              # zeroed, used and freed in the order of the stream that runs the call
             workspace = AttentionWorkspace(q.device)
     _, out, lse = _call(stream, _step().attention, "pn_attention", q, cache, table, lens, starts, max_queries, scale,
-                        window, sinks, out, lse, return_lse, workspace.ptr, workspace.nbytes)
+                        window, sinks, out, lse, return_lse, workspace.buffer)
     return out if lse is None else (out, lse)
 
 

@@ -155,3 +155,37 @@ SHARED = [
 def test_outputs_share_no_memory(lib, name, good, changes):
     for change in changes:
         assert getattr(lib, name)(*{**good, **change}.values()) == PN_EINVAL, change
+
+
+def test_wrappers_refuse_tensors_of_two_devices(lib):
+    """Tensors without memory that stand for two GPUs': every argument of every call is looked at before anything else is done."""
+    import types
+
+    import torch
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    from bit_weight_only_pn_gb300 import pn
+    i32, i64, f32, f16, u8 = torch.int32, torch.int64, torch.float32, torch.float16, torch.uint8
+    mode = FakeTensorMode()
+
+    def make(shape, dtype, device):
+        with mode:
+            return torch.empty(shape, dtype=dtype, device=f"cuda:{device}")
+
+    plan_out = [((4,), i64), ((4,), i32), ((4,), i32), ((3,), i32), ((2,), i32), ((2,), i32), ((2,), i64), ((1,), i32)]
+    plan_args = [((2,), i32)] * 3 + [((2, 3), i32), ((9,), i32), ((2,), i64)]
+    cache, token = ((4, 2, 1, 17 * 64), u8), ((3, 2, 64), f32)
+    calls = {
+        "plan": (plan_args, lambda t: pn.kv_plan(*t, 16, 4)),
+        "plan into": (plan_args + plan_out, lambda t: pn.kv_plan(*t[:6], 16, 4, out=pn.KvPlan(*t[6:]))),
+        "append": ([token, token, token, cache, ((3,), i64), ((3,), i32), ((5, 32), f32), ((5, 32), f32), ((64,), f32), ((64,), f32), ((3, 2, 64), f16)],
+                   lambda t: pn.kv_append(*t[:10], q_out=t[10])),
+        "read": ([cache, ((3,), i64), token, token], lambda t: pn.kv_read(t[0], t[1], out=(t[2], t[3]))),
+        "attention": ([((3, 4, 64), f16), cache, ((2, 3), i32), ((2,), i32), ((3,), i32), ((3, 4, 64), f16), ((3, 4), f32), ((1 << 20,), u8)],
+                      lambda t: pn.attention(*t[:5], 2, 0.1, out=t[5], lse=t[6], workspace=types.SimpleNamespace(buffer=t[7]))),
+        "verify": ([((2, 3), i32), ((2, 4, 10), f32), ((2, 3, 10), f32), ((2, 4), f32), ((2,), i32), ((2,), i32), ((2, 4), i32)],
+                   lambda t: pn.verify(*t[:4], counts=t[4], accepted=t[5], out=t[6])),
+    }
+    for name, (shapes, call) in calls.items():
+        for other in range(len(shapes)):
+            with pytest.raises(ValueError, match="must be on the device of"):
+                call([make(s, d, int(i == other)) for i, (s, d) in enumerate(shapes)])
