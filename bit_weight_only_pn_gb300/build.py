@@ -71,11 +71,17 @@ def _torch():
             torch.__version__, int(torch._C._GLIBCXX_USE_CXX11_ABI))
 
 
+def _binding_key() -> str:
+    """What the Python entry is built against: PyTorch, its C++ ABI, the Python and machine."""
+    _, _, version, abi = _torch()
+    return f"{version}-cxx11abi{abi}-{sysconfig.get_config_var('SOABI')}"
+
+
 def _compile_binding() -> str:
     src = os.path.join(CSRC, "pn_step_binding.cpp")
-    include, _, version, abi = _torch()
-    # one object per PyTorch: its headers are part of it
-    obj = os.path.join(BUILD, f"pn_step_binding-{version}.o")
+    include, _, _, abi = _torch()
+    # one object per PyTorch and Python: their headers are part of it
+    obj = os.path.join(BUILD, f"pn_step_binding-{_binding_key()}.o")
     if _newer(obj, [src, os.path.join(ROOT, "include", "pn.h")]):
         cuda = os.path.join(os.path.dirname(os.path.dirname(os.path.realpath(nvcc()))), "include")
         _run(["g++", "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", f"-D_GLIBCXX_USE_CXX11_ABI={abi}",
@@ -85,12 +91,22 @@ def _compile_binding() -> str:
 
 
 def _link_binding(obj: str) -> None:
-    if _newer(BINDING, [obj, LIBRARY]):
+    # what the entry that lies there was built against, which its age does not tell
+    record = os.path.join(BUILD, "step_binding_key.txt")
+    have = None
+    if os.path.exists(record):
+        with open(record) as f:
+            have = f.read()
+    if have != _binding_key() or _newer(BINDING, [obj, LIBRARY]):
+        if have is not None:
+            os.remove(record)
         tmp = BINDING + ".tmp"
         _run(["g++", "-shared", "-o", tmp, obj, f"-L{HERE}", "-l:" + os.path.basename(LIBRARY), f"-L{_torch()[1]}",
               "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN"],
              "link of the Python entry")
         os.replace(tmp, BINDING)
+        with open(record, "w") as f:
+            f.write(_binding_key())
 
 
 def build(verbose: bool = False) -> str:
