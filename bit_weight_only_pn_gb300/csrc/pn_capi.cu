@@ -47,9 +47,11 @@ bool shared(const Range (&out)[O], const Range (&in)[I]) {
 // Pages of the 4-bit cache hold a power of two of tokens, whole records of 16.
 bool page_size_ok(int page_size) { return page_size >= 16 && page_size <= 1024 && (page_size & (page_size - 1)) == 0; }
 
+// A cache's shape, of at most 2^63 - 1 bytes.
 bool kv_shape_ok(int64_t pages, int page_size, int kv_heads, int head_dim) {
     return pages >= 1 && pages <= INT32_MAX && page_size_ok(page_size) && kv_heads >= 1 && kv_heads <= 65536 &&
-           (head_dim == 64 || head_dim == 128 || head_dim == 256);
+           (head_dim == 64 || head_dim == 128 || head_dim == 256) &&
+           pages * kv_heads * (page_size / 16) <= INT64_MAX / (17 * head_dim);
 }
 
 }  // namespace

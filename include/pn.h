@@ -337,7 +337,8 @@ pn_status pn_prefill(int type, const void* W, int64_t N, int64_t K, const uint16
  *
  * The cache: `pages` pages of page_size tokens (a power of two, 16 .. 1024)
  * of kv_heads heads of head_dim values (64, 128 or 256), in all
- * pn_kv_cache_bytes(...) bytes (0 for a shape outside these), 16-byte aligned:
+ * pn_kv_cache_bytes(...) bytes (0 for a shape outside these, with more than
+ * 2^31 - 1 pages or 65536 heads, or past 2^63 - 1 bytes), 16-byte aligned:
  *
  *   uint8 [pages][kv_heads][page_size / 16][17 * head_dim]
  *

@@ -189,3 +189,18 @@ def test_wrappers_refuse_tensors_of_two_devices(lib):
         for other in range(len(shapes)):
             with pytest.raises(ValueError, match="must be on the device of"):
                 call([make(s, d, int(i == other)) for i, (s, d) in enumerate(shapes)])
+
+
+def test_cache_bytes_past_63_bits(lib):
+    """Shapes whose bytes do not fit are refused, not taken modulo 2^64."""
+    f, most = lib.pn_kv_cache_bytes, (1 << 31) - 1
+    per_page = 65536 * 64 * 17 * 256
+    pages = ((1 << 63) - 1) // per_page
+    assert f(pages, 1024, 65536, 256) == pages * per_page
+    for shape in ((pages + 1, 1024, 65536, 256), (most, 1024, 65536, 256), (most, 1024, 65536, 64), (1 << 30, 1024, 65536, 128)):
+        exact = shape[0] * shape[2] * (shape[1] // 16) * 17 * shape[3]
+        assert f(*shape) == (exact if exact < 1 << 63 else 0)
+        if exact >= 1 << 63:
+            change = dict(zip(("pages", "page_size", "kv_heads", "head_dim"), shape))
+            for name, good in (("pn_kv_append", APPEND), ("pn_kv_read", READ), ("pn_attention", ATTENTION)):
+                assert getattr(lib, name)(*{**good, **change}.values()) == PN_EINVAL
