@@ -495,15 +495,20 @@ def kv_read(cache: torch.Tensor, slots: torch.Tensor, out=None, stream=None):
 
 
 class AttentionWorkspace:
-    """Zeroed device scratch for attention calls on one device (see pn_attention)."""
+    """Zeroed device scratch for attention calls on one device (see pn_attention).
+    Ready on return, whichever stream the calls run on: the constructor waits for
+    its zeros (but not under graph capture, nor with wait=False, where the first
+    call has to follow on the current stream)."""
 
-    def __init__(self, device=None):
+    def __init__(self, device=None, wait: bool = True):
         self.device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
         with torch.cuda.device(self.device):
             self.nbytes = int(lib().pn_attention_workspace_bytes())
             if self.nbytes == 0:
                 raise PnError(4, "pn_attention_workspace_bytes")
             self.buffer = torch.zeros(self.nbytes, dtype=torch.uint8, device=self.device)
+            if wait and not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream().synchronize()
 
     @property
     def ptr(self) -> int:
@@ -527,7 +532,7 @@ def attention(q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, lens: t
     return_lse (or a given lse) also fp32 [tokens][heads]."""
     if workspace is None:
         with torch.cuda.stream(stream):              # zeroed, used and freed in the order of the stream that runs the call
-            workspace = AttentionWorkspace(q.device)
+            workspace = AttentionWorkspace(q.device, wait=False)
     _, out, lse = _call(stream, _step().attention, "pn_attention", q, cache, table, lens, starts, max_queries, scale,
                         window, sinks, out, lse, return_lse, workspace.buffer)
     return out if lse is None else (out, lse)

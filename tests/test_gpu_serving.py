@@ -810,3 +810,41 @@ def test_attention_starts_out_of_order(pn, D, queries, kv):
     assert torch.all(out == 7.0)
     case = attention_case([40, 9], [3, 1], 4, 2, 64, 16)
     check_attention(pn, case, 3, 0.1, workspace=ws)
+
+
+# ------------------------------------------------------------- workspace, memory --
+@pytest.mark.parametrize("counts", [[1], [200]])
+def test_attention_workspace_on_another_stream(pn, counts):
+    """A workspace made while the current stream is busy serves a call on another one at once: its zeros are there."""
+    case = attention_case([3000], counts, 8, 8, 128, 16)
+    q, cache, table, lens, starts = (cuda(x) for x in case[:5])
+    plain, plain_lse = pn.attention(q, cache, table, lens, starts, counts[0], 0.1, return_lse=True)
+    used = torch.full((pn.AttentionWorkspace().nbytes,), 0xFF, dtype=torch.uint8, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    del used                                          # the next allocation of this size finds these bytes
+    torch.cuda._sleep(100_000_000)
+    ws = pn.AttentionWorkspace()
+    assert torch.cuda.current_stream().query()
+    out, lse = pn.attention(q, cache, table, lens, starts, counts[0], 0.1, return_lse=True, workspace=ws, stream=side)
+    side.synchronize()
+    assert torch.equal(out, plain) and torch.equal(lse, plain_lse) and ws.status() == 0
+
+
+def test_attention_in_a_graph_without_a_workspace(pn):
+    """Captured with a workspace of its own: nothing waits, and every replay gives the call's output."""
+    case = attention_case([700, 90], [3, 2], 4, 2, 128, 16)
+    q, cache, table, lens, starts = (cuda(x) for x in case[:5])
+    plain = pn.attention(q, cache, table, lens, starts, 3, 0.1)
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        out = pn.attention(q, cache, table, lens, starts, 3, 0.1)
+        ws = pn.AttentionWorkspace()
+        again = pn.attention(q, cache, table, lens, starts, 3, 0.1, workspace=ws)
+    for _ in range(2):
+        out.zero_()
+        again.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, plain) and torch.equal(again, plain)
