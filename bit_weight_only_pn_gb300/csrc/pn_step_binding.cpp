@@ -14,6 +14,7 @@
 #include <c10/cuda/CUDACachingAllocator.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
+#include <c10/util/Exception.h>
 #include <torch/csrc/autograd/python_variable.h>
 
 #include <exception>
@@ -344,6 +345,16 @@ PyObject* verify(PyObject* const* a) {
     return answer(st, {given_or(a[5], accepted), given_or(a[6], out)});
 }
 
+// A shortage of device memory, as PyTorch's own calls raise it.
+void raise_out_of_memory(const char* what) {
+    PyObject* torch = PyImport_ImportModule("torch");
+    PyObject* type = torch ? PyObject_GetAttrString(torch, "OutOfMemoryError") : nullptr;
+    Py_XDECREF(torch);
+    if (!type) return;                         // (that error stands)
+    PyErr_SetString(type, what);
+    Py_DECREF(type);
+}
+
 // No C++ exception leaves an entry.
 template <PyObject* (*F)(PyObject* const*), Py_ssize_t N>
 PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
@@ -354,6 +365,8 @@ PyObject* entry(PyObject*, PyObject* const* args, Py_ssize_t n) {
     try {
         return F(args);
     } catch (const PythonError&) {
+    } catch (const c10::OutOfMemoryError& e) {
+        if (!PyErr_Occurred()) raise_out_of_memory(e.what_without_backtrace());
     } catch (const std::exception& e) {
         if (!PyErr_Occurred()) PyErr_SetString(PyExc_RuntimeError, e.what());
     } catch (...) {

@@ -848,3 +848,11 @@ def test_attention_in_a_graph_without_a_workspace(pn):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, plain) and torch.equal(again, plain)
+
+
+def test_out_of_memory_is_pytorchs(pn):
+    """Outputs past the device's memory (2 x 550 GB) end in the error that PyTorch's own calls raise, and the call works afterwards."""
+    cache, slots = pn.kv_cache(1, 16, 65536, 256), torch.zeros(8192, dtype=torch.int64, device="cuda")
+    with pytest.raises(torch.OutOfMemoryError):
+        pn.kv_read(cache, slots)
+    assert pn.kv_read(cache, slots[:1])[0].shape == (1, 65536, 256)
