@@ -856,3 +856,56 @@ def test_out_of_memory_is_pytorchs(pn):
     with pytest.raises(torch.OutOfMemoryError):
         pn.kv_read(cache, slots)
     assert pn.kv_read(cache, slots[:1])[0].shape == (1, 65536, 256)
+
+
+# ------------------------------------------------- V scales that differ within a tile --
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("counts,heads,kv,rounding", [([3, 2], 4, 2, 2.0 ** -35), ([128, 128], 24, 8, 2.0 ** -32)])
+@pytest.mark.parametrize("spread", [1.0, 1e3, 1e6])
+@pytest.mark.parametrize("away", [1.0, 4.0])
+def test_attention_scales_within_a_tile(pn, D, counts, heads, kv, rounding, spread, away):
+    """Every 37th token has values `spread` times the others' and keys that point away from all queries.
+
+    The tolerance is the one at the head of this file but for p_t d_t below fp16's normal numbers, which
+    are rounded to 2^-25 each, times |n - 8| <= 8, over the sum of the weights.  For few rows the reference
+    keeps the largest p_t d_t at 2^13 or more, so the sum is at least 2^13 over the largest V scale: 2^-35
+    of it to a token.  For many rows the reference lies 7 below the largest score plus the largest scale of
+    its tile or, in later tiles, lower; so the largest weight, and with it the sum, is at least 2^7 over the
+    largest scale: 2^-29 of that, which is 2^-32 of the largest value (eight steps of its scale)."""
+    rng = np.random.default_rng(D + int(away))
+    page, lens = 32, [400, 333]
+    held = [-(-n // page) for n in lens]
+    order = rng.permutation(sum(held))
+    table = np.full((2, max(held)), 1 << 30, np.int32)
+    cache = np.full((sum(held), kv, page // 16, 17 * D), 0xFF, np.uint8)
+    side = rng.choice([-1.0, 1.0], (kv, D))
+    ks, vs, at = [], [], 0
+    for b, n in enumerate(lens):
+        own = order[at:at + held[b]]
+        at += held[b]
+        table[b, :held[b]] = own
+        k = (0.5 * rng.standard_normal((n, kv, D))).astype(np.float32)
+        v = (1e-2 * rng.standard_normal((n, kv, D))).astype(np.float32)
+        k[5::37] = -away * side
+        v[5::37] *= spread
+        kn, kd = ref.quantise(k)
+        vn, vd = ref.quantise(v)
+        ref.write_tokens(cache, [own[t // page] * page + t % page for t in range(n)], kn, kd, vn, vd)
+        ks.append(ref.dequantise(kn, kd))
+        vs.append(ref.dequantise(vn, vd))
+    q = (side[:, None] + 0.3 * rng.standard_normal((sum(counts), kv, heads // kv, D))).reshape(-1, heads, D).astype(np.float16)
+    starts = np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)
+    scale = 1 / math.sqrt(D)
+    ws = pn.AttentionWorkspace()
+    out, lse = pn.attention(cuda(q), cuda(cache), cuda(table), cuda(np.array(lens, np.int32)), cuda(starts), max(counts), scale,
+                            return_lse=True, workspace=ws)
+    assert ws.status() == 0
+    out, lse = out.cpu().numpy().astype(np.float64), lse.cpu().numpy().astype(np.float64)
+    for b, L in enumerate(lens):
+        rows = slice(starts[b], starts[b + 1])
+        want, want_lse, size, reach = ref.attention(q[rows].astype(np.float64), ks[b], vs[b], scale, 0, 0)
+        e = 2.0 ** -19 * reach + 2.0 ** -22 * (1.5 * np.maximum(reach, 10) + 14) + 2.0 ** -21 + L * 2.0 ** -24
+        limit = (2.0 ** -11 + 2 * e)[..., None] * size + L * rounding * np.abs(vs[b]).max() + 2.0 ** -11 * np.abs(want) + 2.0 ** -25
+        far = np.abs(out[rows] - want) > limit
+        assert not far.any(), f"request {b}: {(np.abs(out[rows] - want) / limit).max()} of the limit"
+        assert np.all(np.abs(lse[rows] - want_lse) <= 2 * e + 2.0 ** -22 * np.abs(want_lse)), f"request {b}"
