@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(kPlanThreads, 1) plan_kernel(const PlanParams 
 // heads by halves and that of neighbours stay inside a lane, and a row's loads
 // are 16 bytes wide.  A warp stays with its token for several groups of heads,
 // so the rotation's row and the weights are read once.  For 8192 tokens of
-// 48 + 16 heads of 128 in fp32: 85 us, 4.4 TB/s.  It is bound by latency and by
+// 48 + 16 heads of 128 in fp32: 85 us, 4.5 TB/s (in fp16 105 us).  It is bound by latency and by
 // its instructions before it is by memory: four values to a lane and a warp to
 // a row takes 307 us (its exchanges), sixteen to a lane 90 us (half the warps
 // to an SM), and rows fetched further ahead than the next change nothing.

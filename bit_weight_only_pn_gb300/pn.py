@@ -452,7 +452,9 @@ def kv_cache(pages: int, page_size: int, kv_heads: int, head_dim: int, device=No
 
 
 class KvPlan(NamedTuple):
-    """A step's bookkeeping (see pn_kv_plan)."""
+    """A step's bookkeeping (see pn_kv_plan).  Unless given as `out`, the eight share
+    one allocation, which lasts as long as any of them: clone what is to outlive
+    the slot maps (16 bytes a slot)."""
     slots: torch.Tensor         # int64 [capacity]: where each token goes in the cache, -1 nowhere
     positions: torch.Tensor     # int32 [capacity]: its position in its request, -1 none
     requests: torch.Tensor      # int32 [capacity]: its request, -1 behind the step's tokens
@@ -529,7 +531,8 @@ def attention(q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, lens: t
     included), starts int32 [batch + 1]; no request has more than max_queries
     queries.  window > 0: a query sees the last `window` tokens up to its own
     and the first `sinks`.  Returns out fp16 [tokens][heads][D], with
-    return_lse (or a given lse) also fp32 [tokens][heads]."""
+    return_lse (or a given lse) also fp32 [tokens][heads].  Without a workspace
+    the call allocates and zeroes one (about 40 MB): a program keeps its own."""
     if workspace is None:
         with torch.cuda.stream(stream):              # zeroed, used and freed in the order of the stream that runs the call
             workspace = AttentionWorkspace(q.device, wait=False)

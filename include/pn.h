@@ -431,7 +431,8 @@ pn_status pn_kv_read(const void* cache, int64_t pages, int page_size, int kv_hea
  * contiguous; at most max_queries of them), the last of which sits at cached
  * token lens[b] - 1; `heads` is a multiple of kv_heads, and query head h reads
  * key/value head h / (heads / kv_heads).  A query at position p sees the
- * cached tokens t <= p with, where window > 0, t > p - window or t < sinks.
+ * cached tokens t <= p with, where window > 0, t > p - window or t < sinks (any
+ * number from 0 on; a length past max_pages * page_size counts as that).
  *   x_t = scale * q . k_t;  lse = ln sum_t exp(x_t);
  *   out = sum_t exp(x_t - lse) v_t
  * A query that sees nothing gets out = 0 and lse = -inf.  Hidden tokens have
@@ -443,9 +444,13 @@ pn_status pn_kv_read(const void* cache, int64_t pages, int page_size, int kv_hea
  * is rounded to fp16 before it is multiplied by v_t's codes, so an output is
  * within 2^-11 (sum_t p_t |v_t|) + 2^-11 |out| of the exact value, and a
  * little more for the fp32 sums and, where V's scales differ by powers of ten,
- * for products far below the largest (2^-29 max |v| to a token).  Deterministic.
- * Which kernel runs, and with it the last bits, goes by batch, max_queries, the
- * heads and head_dim alone.
+ * for products far below the largest (2^-32 max |v| to a token where many rows
+ * share a head, 2^-35 where few do).  Deterministic: a call repeated on a GPU of
+ * the same kind gives the same bits.  Which kernel runs goes by batch,
+ * max_queries, the heads and head_dim alone; the last bits also go by where the
+ * work is cut and joined again, that is by every request's length and queries,
+ * the window, the first tokens and the number of SMs.  So a request's last bits
+ * can differ with the requests beside it.
  * The work is numbered in 32 bits.  With group = heads / kv_heads and rows taken
  * 16 at a time (8 where max_queries * group <= 8 or head_dim is 256), PN_EUNSUPPORTED
  * if batch * kv_heads * ceil(max_queries * group / 16) reaches 2^31, or if kv_heads *
