@@ -1,4 +1,5 @@
-// pn_attn.cuh -- what the attention kernels share.
+// pn_attn.cuh -- what the attention kernels share, with that of the weight cached
+// tokens gather.
 #pragma once
 
 #include <cstdint>
@@ -43,6 +44,22 @@ __device__ __forceinline__ float lg2(float x) {
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Pair I (0 .. 3) of four code pairs at bits 0, 4, 8, 12 of a word's halves, as
+// fp16 numbers: n 2^-24 for I even, n 2^-20 for I odd.  `shifted` = word >> 8.
+template <int I>
+__device__ __forceinline__ uint32_t raw_pair(uint32_t word, uint32_t shifted) {
+    return (I >= 2 ? shifted : word) & (I & 1 ? 0x00F000F0u : 0x000F000Fu);
+}
+
+// D = C + A * B, m16n8k16, fp16 inputs, fp32 accumulate.
+__device__ __forceinline__ void mma_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1, float c0, float c1, float c2, float c3) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 "
+        "{%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %11, %12, %13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c0), "f"(c1), "f"(c2), "f"(c3));
 }
 
 // Sums of units that stop at 2^32 - 1, which no call reaches whose starts are in

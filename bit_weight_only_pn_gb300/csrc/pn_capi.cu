@@ -44,6 +44,9 @@ bool shared(const Range (&out)[O], const Range (&in)[I]) {
     return false;
 }
 
+// Elements between rows of `cols`: byte offsets of up to 2^31 rows stay below 2^63.
+bool stride_ok(int64_t stride, int64_t cols) { return stride >= cols && stride <= (int64_t{1} << 29); }
+
 // Pages of the 4-bit cache hold a power of two of tokens, whole records of 16.
 bool page_size_ok(int page_size) { return page_size >= 16 && page_size <= 1024 && (page_size & (page_size - 1)) == 0; }
 
@@ -722,6 +725,141 @@ pn_status pn_verify(const int32_t* tokens, const float* target, int64_t target_s
     const pn::VerifyArgs a{tokens, target, target_stride, draft, draft_stride, uniforms, counts, batch, drafts, vocab,
                            accepted, out};
     const cudaError_t e = pn::launch_verify(a, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PN_OK : pn::cuda_error(e);
+}
+
+pn_status pn_logprobs(const void* logits, int64_t stride, int dtype, int64_t rows, int vocab, float scale,
+                      const int32_t* tokens, int count, float* logprobs, float* entropy, int top,
+                      int32_t* top_tokens, float* top_logprobs, pn_stream stream) {
+    if (dtype != PN_DTYPE_F32 && dtype != PN_DTYPE_F16) return PN_EINVAL;
+    if (rows < 0 || rows > INT32_MAX || vocab < 1 || vocab > PN_MAX_VOCAB || count < 0 || count > PN_MAX_VOCAB || top < 0 ||
+        top > PN_MAX_TOP || !(scale >= 0x1p-64f && scale <= 0x1p64f) || !stride_ok(stride, vocab))
+        return PN_EINVAL;
+    if (rows == 0) return PN_OK;
+    if (!logits || (count > 0 && (!tokens || !logprobs)) || (top > 0 && (!top_tokens || !top_logprobs))) return PN_EINVAL;
+    const size_t size = dtype == PN_DTYPE_F32 ? 4 : 2, nr = static_cast<size_t>(rows) * 4;
+    if (!aligned(logits, size) || !aligned(tokens, 4) || !aligned(logprobs, 4) || !aligned(entropy, 4) || !aligned(top_tokens, 4) ||
+        !aligned(top_logprobs, 4))
+        return PN_EALIGN;
+    const Range ins[] = {{logits, ((rows - 1) * stride + vocab) * size}, {tokens, nr * count}},
+                outs[] = {{logprobs, nr * count}, {entropy, nr}, {top_tokens, nr * top}, {top_logprobs, nr * top}};
+    if (shared(outs, ins)) return PN_EINVAL;
+    int sms = 0, major = 0;
+    if (pn_status st = device_info(&sms, &major); st != PN_OK) return st;
+    if (major < 9) return PN_EUNSUPPORTED;
+    const pn::LogprobsArgs a{logits, stride, dtype == PN_DTYPE_F16, rows, vocab, scale, tokens, count, logprobs, entropy, top,
+                             top_tokens, top_logprobs};
+    const cudaError_t e = pn::launch_logprobs(a, sms, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PN_OK : pn::cuda_error(e);
+}
+
+pn_status pn_norm(const void* y, int64_t y_stride, int y_dtype, const void* residual, int64_t residual_stride,
+                  int residual_dtype, const float* gate, int64_t gate_stride, float scale, int64_t tokens, int hidden,
+                  int post, const float* post_weight, const float* post_bias, int pre, const float* pre_weight,
+                  const float* pre_bias, float eps, void* residual_out, int64_t out_stride, uint16_t* x,
+                  pn_stream stream) {
+    for (int d : {y_dtype, residual_dtype})
+        if (d != PN_DTYPE_F32 && d != PN_DTYPE_F16) return PN_EINVAL;
+    for (int k : {post, pre})
+        if (k != PN_NORM_NONE && k != PN_NORM_RMS && k != PN_NORM_LAYER) return PN_EINVAL;
+    if (tokens < 0 || tokens > INT32_MAX || hidden < 1 || hidden > PN_MAX_HIDDEN || !(eps >= 0.0f) || !(scale - scale == 0.0f)) return PN_EINVAL;
+    if ((post == PN_NORM_NONE && (post_weight || post_bias)) || (pre == PN_NORM_NONE && (pre_weight || pre_bias))) return PN_EINVAL;
+    if ((y && !stride_ok(y_stride, hidden)) || (residual && !stride_ok(residual_stride, hidden)) ||
+        (gate && gate_stride != 0 && !stride_ok(gate_stride, hidden)) || (residual_out && !stride_ok(out_stride, hidden)))
+        return PN_EINVAL;
+    if (tokens == 0) return PN_OK;
+    if ((!y && !residual) || (!residual_out && !x)) return PN_EINVAL;
+    // what nothing would be done with
+    if ((!y && (gate || post != PN_NORM_NONE)) || (!x && pre != PN_NORM_NONE)) return PN_EINVAL;
+    const size_t ys = y_dtype == PN_DTYPE_F32 ? 4 : 2, rs = residual_dtype == PN_DTYPE_F32 ? 4 : 2;
+    if (!aligned(y, ys) || !aligned(residual, rs) || !aligned(residual_out, rs) || !aligned(gate, 4) || !aligned(post_weight, 4) ||
+        !aligned(post_bias, 4) || !aligned(pre_weight, 4) || !aligned(pre_bias, 4) || !aligned(x, 2))
+        return PN_EALIGN;
+    const bool in_place = residual_out && residual_out == residual && out_stride == residual_stride;
+    const size_t row = static_cast<size_t>(hidden) * 4;
+    auto rows_of = [&](int64_t stride, size_t size) { return ((tokens - 1) * stride + hidden) * size; };
+    const Range ins[] = {{y, rows_of(y_stride, ys)}, {in_place ? nullptr : residual, rows_of(residual_stride, rs)},
+                         {gate, rows_of(gate_stride, 4)}, {post_weight, row}, {post_bias, row}, {pre_weight, row}, {pre_bias, row}},
+                outs[] = {{residual_out, rows_of(out_stride, rs)}, {x, static_cast<size_t>(tokens) * hidden * 2}};
+    if (shared(outs, ins)) return PN_EINVAL;
+    int sms = 0, major = 0;
+    if (pn_status st = device_info(&sms, &major); st != PN_OK) return st;
+    const pn::NormArgs a{y, y_stride, y_dtype == PN_DTYPE_F16, residual, residual_stride, residual_dtype == PN_DTYPE_F16, gate, gate_stride,
+                         scale, tokens, hidden, post, post_weight, post_bias, pre, pre_weight, pre_bias, eps, residual_out, out_stride,
+                         residual_dtype == PN_DTYPE_F16, reinterpret_cast<__half*>(x)};
+    const cudaError_t e = pn::launch_norm(a, sms, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PN_OK : pn::cuda_error(e);
+}
+
+pn_status pn_kv_weigh(const uint16_t* q, int64_t q_stride, int64_t tokens, int heads, const void* cache,
+                      int64_t pages, int page_size, int kv_heads, int head_dim, const int32_t* table,
+                      int64_t table_stride, int max_pages, const int32_t* lens, const int32_t* starts, int batch,
+                      int max_queries, const float* lse, float scale, int window, int sinks, const float* weights,
+                      float decay, float* out, pn_stream stream) {
+    if (!kv_shape_ok(pages, page_size, kv_heads, head_dim)) return PN_EINVAL;
+    if (tokens < 0 || tokens > INT32_MAX || heads < 1 || heads > 65536 || heads % kv_heads) return PN_EINVAL;
+    if (batch < 1 || batch > pn::kKvMaxBatch || max_queries < 1 || max_pages < 1 || table_stride < max_pages || window < 0 || sinks < 0 ||
+        !(scale - scale == 0.0f) || !(decay >= 0.0f && decay <= 1.0f))
+        return PN_EINVAL;
+    if (static_cast<int64_t>(max_pages) * page_size > INT32_MAX - 1024 ||
+        static_cast<int64_t>(max_queries) * (heads / kv_heads) > INT32_MAX - 128)
+        return PN_EINVAL;
+    const int64_t cols = static_cast<int64_t>(heads) * head_dim;
+    if (!stride_ok(q_stride, cols)) return PN_EINVAL;
+    if (tokens == 0) return PN_OK;
+    if (!q || !cache || !table || !lens || !starts || !lse || !out) return PN_EINVAL;
+    if (!aligned(q, 16) || q_stride % 8 || !aligned(cache, 16) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(starts, 4) ||
+        !aligned(lse, 4) || !aligned(weights, 4) || !aligned(out, 4))
+        return PN_EALIGN;
+    const size_t nt = static_cast<size_t>(tokens), nb = static_cast<size_t>(batch) * 4, nw = static_cast<size_t>(pages) * kv_heads * page_size * 4;
+    const Range ins[] = {{q, ((nt - 1) * q_stride + cols) * 2}, {cache, pn_kv_cache_bytes(pages, page_size, kv_heads, head_dim)},
+                         {table, (static_cast<size_t>(batch - 1) * table_stride + max_pages) * 4}, {lens, nb}, {starts, nb + 4},
+                         {lse, nt * heads * 4}, {weights == out ? nullptr : weights, nw}},
+                outs[] = {{out, nw}};
+    if (shared(outs, ins)) return PN_EINVAL;
+    int sms = 0, major = 0;
+    if (pn_status st = device_info(&sms, &major); st != PN_OK) return st;
+    if (major < 10) return PN_EUNSUPPORTED;
+    const int room = max_pages * page_size;            // as in pn_attention
+    const pn::WeighArgs a{reinterpret_cast<const __half*>(q), q_stride, tokens, heads, table, table_stride, max_pages, lens, starts, batch,
+                          max_queries, lse, scale, window < room ? window : 0, sinks < room ? sinks : room, weights, decay, out};
+    const pn::KvGeometry g{static_cast<uint8_t*>(const_cast<void*>(cache)), pages, page_size, kv_heads, head_dim};
+    const cudaError_t e = pn::launch_weigh(a, g, sms, reinterpret_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? PN_OK : pn::cuda_error(e);
+}
+
+pn_status pn_kv_evict(void* cache, int64_t pages, int page_size, int kv_heads, int head_dim, float* weights,
+                      const int32_t* table, int64_t table_stride, int max_pages, const int32_t* lens,
+                      const int32_t* held, int batch, int limit, int budget, int sinks, int recent,
+                      int32_t* free_pages, int64_t ring_pages, const int64_t* ring, int32_t* table_out,
+                      int64_t out_stride, int32_t* lens_out, int32_t* held_out, int64_t* ring_out, int32_t* kept,
+                      int32_t* refused, pn_stream stream) {
+    if (!kv_shape_ok(pages, page_size, kv_heads, head_dim)) return PN_EINVAL;
+    if (batch < 1 || batch > pn::kKvMaxBatch || max_pages < 1 || table_stride < max_pages || out_stride < max_pages || ring_pages < 1 ||
+        ring_pages > INT32_MAX || budget < 1 || budget > limit || budget > PN_MAX_BUDGET || sinks < 0 || recent < 0 ||
+        static_cast<int64_t>(sinks) + recent > budget)
+        return PN_EINVAL;
+    if (static_cast<int64_t>(max_pages) * page_size > INT32_MAX - 1024) return PN_EINVAL;
+    // (blocks are numbered in 31 bits)
+    if (static_cast<int64_t>(batch) * kv_heads >= INT32_MAX) return PN_EUNSUPPORTED;
+    if (!cache || !weights || !table || !lens || !held || !free_pages || !ring || !table_out || !lens_out || !held_out || !ring_out || !kept || !refused)
+        return PN_EINVAL;
+    for (const void* p : {static_cast<const void*>(weights), static_cast<const void*>(table), static_cast<const void*>(lens), static_cast<const void*>(held),
+                          static_cast<const void*>(free_pages), static_cast<const void*>(table_out), static_cast<const void*>(lens_out),
+                          static_cast<const void*>(held_out), static_cast<const void*>(kept), static_cast<const void*>(refused)})
+        if (!aligned(p, 4)) return PN_EALIGN;
+    if (!aligned(cache, 16) || !aligned(ring, 8) || !aligned(ring_out, 8)) return PN_EALIGN;
+    const size_t nb = static_cast<size_t>(batch) * 4;
+    auto rows_of = [&](int64_t stride) { return (static_cast<size_t>(batch - 1) * stride + max_pages) * 4; };
+    const Range in[] = {{table, rows_of(table_stride)}, {lens, nb}, {held, nb}, {ring, 16}},
+        out[] = {{cache, pn_kv_cache_bytes(pages, page_size, kv_heads, head_dim)}, {weights, static_cast<size_t>(pages) * kv_heads * page_size * 4},
+                 {free_pages, static_cast<size_t>(ring_pages) * 4}, {table_out, rows_of(out_stride)}, {lens_out, nb}, {held_out, nb}, {ring_out, 16},
+                 {kept, nb * kv_heads * budget}, {refused, 4}};
+    if (shared(out, in)) return PN_EINVAL;
+    const pn::EvictArgs a{weights, table, table_stride, max_pages, lens, held, batch, limit, budget, sinks, recent, free_pages, ring_pages, ring,
+                          table_out, out_stride, lens_out, held_out, ring_out, kept, refused};
+    const pn::KvGeometry g{static_cast<uint8_t*>(cache), pages, page_size, kv_heads, head_dim};
+    const cudaError_t e = pn::launch_evict(a, g, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PN_OK : pn::cuda_error(e);
 }
 

@@ -1,0 +1,343 @@
+// pn_evict.cu -- requests past a limit keep a budget of tokens.
+//
+// For each key/value head by itself: the first `sinks` tokens, the last `recent`,
+// and of those between them the ones with the largest weights, the lower position
+// first where weights are equal.  They go in their order into pages from the
+// ring's head; the request's old pages go behind its tail.  Nothing that any block
+// reads is written (new pages were free, the table is written to another one), so a
+// call can be repeated and no block waits for another.
+//
+// Two launches.  select: a block to a request and head finds the kept positions.
+// Weights as whole numbers in their order, found by three histograms of 11, 11 and
+// 10 bits, from the top: each fixes a digit of the last kept weight.  Then every warp
+// counts in its share what lies above that weight and what equals it, and writes the
+// positions behind those of the warps before.  move: a warp to a record of 16 new
+// tokens gathers their codes, scales and weights.
+#include <cstdint>
+
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "pn_device.cuh"
+#include "pn_internal.h"
+#include "pn_kv.cuh"
+
+namespace pn {
+namespace {
+
+constexpr int kSelectThreads = 512;
+constexpr int kSelectWarps = kSelectThreads / 32;
+constexpr int kBins = 2048;
+constexpr int kMostKeys = 48 * 1024;           // of a block, kept in shared memory
+constexpr int kMoveThreads = 256;
+constexpr int kMoveRecords = kMoveThreads / 32 * 2;    // of a block
+
+struct Params {
+    EvictArgs a;
+    KvCache cache;
+    int each;                  // pages of a request that was cut back
+    int keys;                  // places for keys in shared memory
+};
+
+__device__ __forceinline__ int64_t wrap(int64_t i, int64_t n) {
+    const int64_t r = i % n;
+    return r < 0 ? r + n : r;
+}
+
+__device__ __forceinline__ int length_of(const Params& P, int b) {
+    return static_cast<int>(min(static_cast<int64_t>(max(P.a.lens[b], 0)), static_cast<int64_t>(P.a.max_pages) << P.cache.page_shift));
+}
+__device__ __forceinline__ int held_of(const Params& P, int b) { return min(max(P.a.held[b], 0), P.a.max_pages); }
+
+// Requests that the free pages are enough for.
+__device__ __forceinline__ int64_t most_served(const Params& P) {
+    const int64_t avail = min(max(P.a.ring[1] - P.a.ring[0], static_cast<int64_t>(0)), P.a.pages);
+    return avail / P.each;
+}
+
+// The sum of v over the block's threads, in all of them; `part` a number per warp, free again behind it.
+template <int kWarps, typename T>
+__device__ __forceinline__ T block_sum(T v, T* part) {
+#pragma unroll
+    for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = 0;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) v += part[w];
+    __syncthreads();
+    return v;
+}
+
+// What does not belong to one request: the ring and how many were refused.
+__device__ void totals(const Params& P, int64_t* part) {
+    const EvictArgs& a = P.a;
+    const int64_t room = most_served(P);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int64_t over = 0, given = 0;               // requests past the limit so far, pages that come back
+    for (int b0 = 0; b0 < a.batch; b0 += kSelectThreads) {
+        const int b = b0 + static_cast<int>(threadIdx.x);
+        const bool past = b < a.batch && length_of(P, b) > a.limit;
+        const uint32_t in = __ballot_sync(0xFFFFFFFFu, past);
+        if (lane == 0) part[warp] = __popc(in);
+        __syncthreads();
+        int64_t turn = over + __popc(in & ((1u << lane) - 1u));
+        for (int w = 0; w < kSelectWarps; ++w) {
+            turn += w < warp ? part[w] : 0;
+            over += part[w];
+        }
+        __syncthreads();
+        given += past && turn < room ? held_of(P, b) : 0;
+    }
+    given = block_sum<kSelectWarps>(given, part);
+    if (threadIdx.x != 0) return;
+    const int64_t served = min(over, room);
+    a.ring_out[0] = a.ring[0] + served * P.each;
+    a.ring_out[1] = a.ring[1] + given;
+    a.refused[0] = static_cast<int>(over - served);
+}
+
+// The order of weights as that of whole numbers; NaN lowest.
+__device__ __forceinline__ uint32_t key_of(float w) {
+    const uint32_t u = __float_as_uint(w + 0.0f);      // -0 is 0
+    return w == w ? (u & 0x80000000u ? ~u : u | 0x80000000u) : 0u;
+}
+
+__global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_constant__ Params P) {
+    extern __shared__ uint32_t keys[];         // [P.keys]
+    __shared__ uint32_t bins[kBins];
+    __shared__ int64_t part[kSelectWarps];
+    __shared__ uint32_t warp_above[kSelectWarps], warp_equal[kSelectWarps];
+    __shared__ uint32_t found[2];              // a digit, and how many of it are to be kept
+    const EvictArgs& a = P.a;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, heads = P.cache.heads;
+    if (blockIdx.x == static_cast<unsigned>(a.batch) * heads) {
+        totals(P, part);
+        return;
+    }
+    const int b = static_cast<int>(blockIdx.x) / heads, h = static_cast<int>(blockIdx.x) % heads;
+    const int len = length_of(P, b);
+    int32_t* kept = a.kept + static_cast<int64_t>(blockIdx.x) * a.budget;
+    const int32_t* row = a.table + static_cast<int64_t>(b) * a.table_stride;
+    bool served = len > a.limit;
+    int64_t turn = 0, behind = 0;              // requests past the limit before this one, and the pages that they give back
+    if (served) {
+        for (int o = threadIdx.x; o < b; o += kSelectThreads)
+            if (length_of(P, o) > a.limit) {
+                ++turn;
+                behind += held_of(P, o);
+            }
+        turn = block_sum<kSelectWarps>(turn, part);
+        behind = block_sum<kSelectWarps>(behind, part);
+        served = turn < most_served(P);
+    }
+    if (h == 0) {
+        const int held = held_of(P, b);
+        int32_t* out = a.table_out + static_cast<int64_t>(b) * a.out_stride;
+        for (int i = threadIdx.x; i < a.max_pages; i += kSelectThreads)
+            out[i] = !served ? row[i] : i < P.each ? a.free_pages[wrap(a.ring[0] + turn * P.each + i, a.pages)] : -1;
+        if (served)
+            for (int i = threadIdx.x; i < held; i += kSelectThreads) a.free_pages[wrap(a.ring[1] + behind + i, a.pages)] = row[i];
+        if (threadIdx.x == 0) {
+            a.lens_out[b] = served ? a.budget : a.lens[b];
+            a.held_out[b] = served ? P.each : a.held[b];
+        }
+    }
+    if (!served) {
+        for (int i = threadIdx.x; i < a.budget; i += kSelectThreads) kept[i] = -1;
+        return;
+    }
+    for (int i = threadIdx.x; i < a.sinks; i += kSelectThreads) kept[i] = i;
+    for (int i = threadIdx.x; i < a.recent; i += kSelectThreads) kept[a.budget - a.recent + i] = len - a.recent + i;
+    const int count = len - a.sinks - a.recent, need = a.budget - a.sinks - a.recent;      // count > need
+    if (need == 0) return;
+    auto weight_key = [&](int i) -> uint32_t {         // of position sinks + i
+        const int tok = a.sinks + i, page = row[tok >> P.cache.page_shift];
+        if (page < 0 || page >= P.cache.pages) return 0u;
+        return key_of(__ldcg(a.weights + ((static_cast<int64_t>(page) * heads + h) << P.cache.page_shift) + (tok & (P.cache.page_size - 1))));
+    };
+    const bool inside = count <= P.keys;
+    if (inside)
+#pragma unroll 8
+        for (int i = threadIdx.x; i < count; i += kSelectThreads) keys[i] = weight_key(i);
+    auto key = [&](int i) { return inside ? keys[i] : weight_key(i); };
+    // the smallest kept key, digit by digit, and how many of those equal to it are kept
+    uint32_t least = 0, fixed = 0, left = static_cast<uint32_t>(need);
+    for (int pass = 0; pass < 3; ++pass) {
+        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, width = pass == 2 ? 10 : 11;
+        const uint32_t digits = (1u << width) - 1u;
+        for (int i = threadIdx.x; i < kBins; i += kSelectThreads) bins[i] = 0;
+        __syncthreads();
+#pragma unroll 4
+        for (int i = threadIdx.x; i < count; i += kSelectThreads) {
+            const uint32_t k = key(i);
+            if ((k & fixed) == least) atomicAdd(&bins[(k >> shift) & digits], 1u);
+        }
+        __syncthreads();
+        // from the largest digit down: a thread has four
+        constexpr int kEach = kBins / kSelectThreads;
+        const int top = kBins - 1 - static_cast<int>(threadIdx.x) * kEach;
+        uint32_t n[kEach], mine = 0;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) mine += n[i] = bins[top - i];
+        uint32_t in = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, in, d);
+            if (lane >= d) in += o;
+        }
+        if (lane == 31) warp_above[warp] = in;
+        __syncthreads();
+        uint32_t above = in - mine;
+        for (int w = 0; w < warp; ++w) above += warp_above[w];
+        if (above < left && left <= above + mine) {    // one thread's
+            int i = 0;
+            while (left > above + n[i]) above += n[i++];
+            found[0] = static_cast<uint32_t>(top - i);
+            found[1] = left - above;
+        }
+        __syncthreads();
+        least |= found[0] << shift;
+        fixed |= digits << shift;
+        left = found[1];
+    }
+    // a contiguous share to each warp
+    const int share = (count + kSelectWarps * 32 - 1) / (kSelectWarps * 32) * 32;
+    const int i0 = min(warp * share, count), i1 = min(i0 + share, count);
+    uint32_t above = 0, equal = 0;
+    for (int i = i0 + lane; i < i1; i += 32) {
+        const uint32_t k = key(i);
+        above += k > least;
+        equal += k == least;
+    }
+    above = __reduce_add_sync(0xFFFFFFFFu, above);
+    equal = __reduce_add_sync(0xFFFFFFFFu, equal);
+    __syncthreads();
+    if (lane == 0) {
+        warp_above[warp] = above;
+        warp_equal[warp] = equal;
+    }
+    __syncthreads();
+    above = equal = 0;
+    for (int w = 0; w < warp; ++w) {
+        above += warp_above[w];
+        equal += warp_equal[w];
+    }
+    const uint32_t lower = (1u << lane) - 1u;
+    for (int i = i0; i < i1; i += 32) {
+        const uint32_t k = i + lane < i1 ? key(i + lane) : 0u;
+        const uint32_t up = __ballot_sync(0xFFFFFFFFu, i + lane < i1 && k > least), same = __ballot_sync(0xFFFFFFFFu, i + lane < i1 && k == least);
+        const uint32_t before = equal + __popc(same & lower);
+        if (((up >> lane) & 1u) || (((same >> lane) & 1u) && before < left))
+            kept[a.sinks + above + __popc(up & lower) + min(before, left)] = a.sinks + i + lane;
+        above += __popc(up);
+        equal += __popc(same);
+    }
+}
+
+// Bytes of kv_record_bytes(D) / 16 that a token has in a record lie in pieces: of K
+// codes a run for each half and plane, of V codes one for each word, two scales.
+template <int D>
+__global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constant__ Params P) {
+    constexpr int NG = D / 64, GP = kv_plane_groups(D), PL = kv_planes(D);
+    using KBits = typename std::conditional<GP == 2, uint4, uint2>::type;      // a lane's bytes of a token's K codes
+    using VBits = typename std::conditional<GP == 2, uint2, uint32_t>::type;   // a word of V codes for each group of a plane
+    using DBits = typename std::conditional<NG == 4, uint2, typename std::conditional<NG == 2, uint32_t, uint16_t>::type>::type;
+    const EvictArgs& a = P.a;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, heads = P.cache.heads;
+    const int b = static_cast<int>(blockIdx.x) / heads, h = static_cast<int>(blockIdx.x) % heads;
+    const int32_t* kept = a.kept + static_cast<int64_t>(blockIdx.x) * a.budget;
+    if (kept[0] < 0) return;                   // left as it was
+    const int32_t* from_row = a.table + static_cast<int64_t>(b) * a.table_stride;
+    const int32_t* to_row = a.table_out + static_cast<int64_t>(b) * a.out_stride;
+    const int records = (a.budget + kKvTokens - 1) / kKvTokens;
+    const int rec0 = static_cast<int>(blockIdx.y) * kMoveRecords, rec1 = min(rec0 + kMoveRecords, records);
+    for (int rec = rec0 + warp; rec < rec1; rec += kMoveThreads / 32) {
+        const int to_tok = rec * kKvTokens, to_page = to_row[to_tok >> P.cache.page_shift];
+        if (to_page < 0 || to_page >= P.cache.pages) continue;
+        const int64_t to_slot = (static_cast<int64_t>(to_page) << P.cache.page_shift) + (to_tok & (P.cache.page_size - 1));
+        uint8_t* to = P.cache.record(to_slot, h);
+        const int have = min(a.budget - to_tok, kKvTokens);    // tokens of the record
+        // lane i (and i + 16): where the record's token i comes from
+        const uint8_t* from = nullptr;
+        int place = 0;
+        float weight = 0.0f;
+        if ((lane & 15) < have) {
+            const int tok = kept[to_tok + (lane & 15)], page = from_row[tok >> P.cache.page_shift];
+            if (page >= 0 && page < P.cache.pages) {
+                const int in_page = tok & (P.cache.page_size - 1);
+                from = P.cache.record((static_cast<int64_t>(page) << P.cache.page_shift) + in_page, h);
+                place = in_page & 15;
+                weight = a.weights[((static_cast<int64_t>(page) * heads + h) << P.cache.page_shift) + in_page];
+            }
+        }
+        auto source = [&](int token, int& r) {
+            r = __shfl_sync(0xFFFFFFFFu, place, token);
+            return reinterpret_cast<const uint8_t*>(__shfl_sync(0xFFFFFFFFu, reinterpret_cast<unsigned long long>(from), token));
+        };
+        // (reads of a plane whose D differs are compiled away; a token of no page becomes zeros)
+        KBits kb[2][PL];
+        VBits vb[2][PL][2];
+        DBits db{};
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+            int r;
+            const uint8_t* s = source(hh * 8 + (lane >> 2), r);
+#pragma unroll
+            for (int pl = 0; pl < PL; ++pl) {
+                kb[hh][pl] = KBits{};
+                if (s) kb[hh][pl] = *reinterpret_cast<const KBits*>(s + (((r >> 3) * PL + pl) * 32 + (r & 7) * 4 + (lane & 3)) * sizeof(KBits));
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {      // words lane / 4 of tokens 2 (lane % 4), + 1
+                s = source(hh * 8 + 2 * (lane & 3) + i, r);
+#pragma unroll
+                for (int pl = 0; pl < PL; ++pl) {
+                    vb[hh][pl][i] = VBits{};
+                    if (s) vb[hh][pl][i] = *reinterpret_cast<const VBits*>(s + kv_v_codes(D) + (((r >> 3) * PL + pl) * 64 + (lane >> 2) * 8 + (r & 7)) * sizeof(VBits));
+                }
+            }
+        }
+        if (from) db = *reinterpret_cast<const DBits*>(from + (lane < 16 ? kv_k_scales(D) : kv_v_scales(D)) + place * sizeof(DBits));
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh)
+#pragma unroll
+            for (int pl = 0; pl < PL; ++pl) {
+                if (hh * 8 + (lane >> 2) < have) *reinterpret_cast<KBits*>(to + ((hh * PL + pl) * 32 + lane) * sizeof(KBits)) = kb[hh][pl];
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (hh * 8 + 2 * (lane & 3) + i < have)
+                        *reinterpret_cast<VBits*>(to + kv_v_codes(D) + ((hh * PL + pl) * 64 + 2 * lane + i) * sizeof(VBits)) = vb[hh][pl][i];
+            }
+        if ((lane & 15) < have) {
+            *reinterpret_cast<DBits*>(to + (lane < 16 ? kv_k_scales(D) : kv_v_scales(D)) + (lane & 15) * sizeof(DBits)) = db;
+            if (lane < 16)
+                a.weights[((static_cast<int64_t>(to_page) * heads + h) << P.cache.page_shift) + (to_tok & (P.cache.page_size - 1)) + lane] = weight;
+        }
+    }
+}
+
+template <int D>
+cudaError_t move(const Params& P, cudaStream_t s) {
+    const int records = (P.a.budget + kKvTokens - 1) / kKvTokens;
+    move_kernel<D><<<dim3(static_cast<unsigned>(P.a.batch) * P.cache.heads, (records + kMoveRecords - 1) / kMoveRecords), kMoveThreads, 0, s>>>(P);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_evict(const EvictArgs& a, const KvGeometry& g, cudaStream_t s) {
+    int shift = 0;
+    while ((1 << shift) < g.page_size) ++shift;
+    const int64_t room = static_cast<int64_t>(a.max_pages) * g.page_size;
+    const Params P{a, KvCache{g.data, g.pages, g.page_size, shift, g.heads, g.D}, (a.budget + g.page_size - 1) / g.page_size,
+                   static_cast<int>(room < kMostKeys ? room : kMostKeys)};
+    static std::atomic<uint64_t> smem_set{0};
+    if (cudaError_t e = set_smem_limit_once(select_kernel, kMostKeys * 4, smem_set); e != cudaSuccess) return e;
+    select_kernel<<<static_cast<unsigned>(a.batch) * g.heads + 1, kSelectThreads, P.keys * 4, s>>>(P);
+    if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
+    if (g.D == 64) return move<64>(P, s);
+    return g.D == 128 ? move<128>(P, s) : move<256>(P, s);
+}
+
+}  // namespace pn

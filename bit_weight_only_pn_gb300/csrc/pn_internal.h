@@ -277,6 +277,96 @@ struct VerifyArgs {
 };
 cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t s);
 
+struct NormArgs {
+    const void* y;             // may be null
+    int64_t y_stride;          // elements between rows, as the others
+    bool y_f16;
+    const void* residual;      // may be null
+    int64_t residual_stride;
+    bool residual_f16;
+    const float* gate;         // may be null
+    int64_t gate_stride;       // 0: one row for all tokens
+    float scale;
+    int64_t tokens;
+    int hidden;
+    int post;                  // pn_norm_kind
+    const float* post_weight;
+    const float* post_bias;
+    int pre;
+    const float* pre_weight;
+    const float* pre_bias;
+    float eps;
+    void* residual_out;        // may be null
+    int64_t out_stride;
+    bool out_f16;
+    __half* x;                 // may be null
+};
+cudaError_t launch_norm(const NormArgs& a, int num_sms, cudaStream_t s);
+
+struct LogprobsArgs {
+    const void* logits;
+    int64_t stride;            // elements between rows
+    bool f16;
+    int64_t rows;
+    int vocab;
+    float scale;
+    const int32_t* tokens;     // [rows][count]
+    int count;
+    float* logprobs;           // [rows][count]
+    float* entropy;            // may be null
+    int top;
+    int32_t* top_tokens;
+    float* top_logprobs;
+};
+cudaError_t launch_logprobs(const LogprobsArgs& a, int num_sms, cudaStream_t s);
+
+struct WeighArgs {
+    const __half* q;
+    int64_t q_stride;          // elements between tokens
+    int64_t tokens;            // rows of q
+    int heads;                 // query heads
+    const int32_t* table;
+    int64_t table_stride;
+    int max_pages;
+    const int32_t* lens;
+    const int32_t* starts;
+    int batch;
+    int max_queries;
+    const float* lse;
+    float scale;
+    int window;                // 0 none
+    int sinks;
+    const float* weights;      // may be null
+    float decay;
+    float* out;
+};
+cudaError_t launch_weigh(const WeighArgs& a, const KvGeometry& g, int num_sms, cudaStream_t s);
+
+struct EvictArgs {
+    float* weights;
+    const int32_t* table;
+    int64_t table_stride;
+    int max_pages;
+    const int32_t* lens;
+    const int32_t* held;
+    int batch;
+    int limit;
+    int budget;
+    int sinks;
+    int recent;
+    int32_t* free_pages;
+    int64_t pages;             // entries of the ring
+    const int64_t* ring;
+    int32_t* table_out;
+    int64_t out_stride;
+    int32_t* lens_out;
+    int32_t* held_out;
+    int64_t* ring_out;
+    int32_t* kept;
+    int32_t* refused;
+};
+cudaError_t launch_evict(const EvictArgs& a, const KvGeometry& g, cudaStream_t s);
+
 // Host-side checks of a one-tensor GEMV, the same ones pn_gemv_ex makes before
 // it launches anything.  On PN_OK, *uses_workspace tells whether the call
 // would launch a tensor-core kernel (which reads and writes the workspace; the

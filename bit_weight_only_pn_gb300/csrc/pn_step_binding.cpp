@@ -345,6 +345,183 @@ PyObject* verify(PyObject* const* a) {
     return answer(st, {given_or(a[5], accepted), given_or(a[6], out)});
 }
 
+// [rows][cols] fp32 or fp16 whose rows are contiguous.
+const at::Tensor& matrix(Device& on, PyObject* o, const char* name) {
+    const at::Tensor& t = cuda_tensor(on, o, name);
+    if (t.scalar_type() != at::kFloat && t.scalar_type() != at::kHalf) fail(PyExc_TypeError, "%s must be torch.float32 or torch.float16", name);
+    if (t.dim() != 2) fail(PyExc_ValueError, "%s must have two dimensions", name);
+    if (t.numel() > 0 && t.size(1) > 1 && t.stride(1) != 1) fail(PyExc_ValueError, "%s's rows must be contiguous", name);
+    if (t.size(1) > INT32_MAX) fail(PyExc_ValueError, "%s has too many columns", name);
+    return t;
+}
+int64_t matrix_stride(const at::Tensor& t) { return t.size(0) > 1 ? t.stride(0) : t.size(1); }
+int dtype_of(const at::Tensor& t) { return t.scalar_type() == at::kFloat ? PN_DTYPE_F32 : PN_DTYPE_F16; }
+
+// logits, tokens (None: none), top, scale, entropy (bool)
+PyObject* logprobs(PyObject* const* a) {
+    Device on;
+    const at::Tensor& logits = matrix(on, a[0], "logits");
+    const int64_t R = logits.size(0), V = logits.size(1);
+    int64_t count = 0;
+    const at::Tensor* tokens = nullptr;
+    bool flat = false;                         // one token to a row, without a dimension of its own
+    if (a[1] != Py_None) {
+        tokens = &dense(on, a[1], at::kInt, "tokens");
+        flat = tokens->dim() == 1;
+        if ((!flat && tokens->dim() != 2) || tokens->size(0) != R) fail(PyExc_ValueError, "%s must be [rows] or [rows][count]", "tokens");
+        count = flat ? 1 : tokens->size(1);
+        if (count > INT32_MAX) fail(PyExc_ValueError, "%s has too many columns", "tokens");
+    }
+    const int top = number(a[2], "top");
+    if (top < 0 || top > PN_MAX_TOP) fail(PyExc_ValueError, "%s must be from 0 to 32", "top");
+    const float scale = real(a[3]);
+    const int want_entropy = PyObject_IsTrue(a[4]);
+    if (want_entropy < 0) throw PythonError{};
+    const c10::cuda::CUDAGuard guard(logits.device());
+    at::Tensor given, entropy, top_tokens, top_logprobs;
+    if (tokens) given = flat ? fresh({R}, at::kFloat) : fresh({R, count}, at::kFloat);
+    if (want_entropy) entropy = fresh({R}, at::kFloat);
+    if (top) {
+        top_tokens = fresh({R, top}, at::kInt);
+        top_logprobs = fresh({R, top}, at::kFloat);
+    }
+    const pn_status st = pn_logprobs(logits.data_ptr(), matrix_stride(logits), dtype_of(logits), R, static_cast<int>(V), scale, data<int32_t>(tokens),
+                                     static_cast<int>(count), tokens ? data<float>(&given) : nullptr, want_entropy ? data<float>(&entropy) : nullptr, top,
+                                     top ? data<int32_t>(&top_tokens) : nullptr, top ? data<float>(&top_logprobs) : nullptr, stream_of(logits));
+    return answer(st, {tokens ? THPVariable_Wrap(given) : nullptr, want_entropy ? THPVariable_Wrap(entropy) : nullptr,
+                       top ? THPVariable_Wrap(top_tokens) : nullptr, top ? THPVariable_Wrap(top_logprobs) : nullptr});
+}
+
+// y, residual, gate, scale, post, post_weight, post_bias, pre, pre_weight, pre_bias, eps, residual_out, x, want_residual, want_x
+PyObject* norm(PyObject* const* a) {
+    Device on;
+    const at::Tensor* y = a[0] == Py_None ? nullptr : &matrix(on, a[0], "y");
+    const at::Tensor* residual = a[1] == Py_None ? nullptr : &matrix(on, a[1], "residual");
+    const at::Tensor* one = y ? y : residual;
+    if (!one) fail(PyExc_TypeError, "%s or residual must be given", "y");
+    if (y && residual && y->sizes() != residual->sizes()) fail(PyExc_ValueError, "%s and residual must have the same shape", "y");
+    const int64_t T = one->size(0), N = one->size(1);
+    const at::Tensor* gate = nullptr;
+    int64_t gate_stride = 0;
+    if (a[2] != Py_None) {
+        gate = &cuda_tensor(on, a[2], "gate");
+        if (gate->scalar_type() != at::kFloat) fail(PyExc_TypeError, "%s must be torch.float32", "gate");
+        const bool rows = gate->dim() == 2;
+        if ((!rows && gate->dim() != 1) || gate->size(rows) != N || (rows && gate->size(0) != T && gate->size(0) != 1))
+            fail(PyExc_ValueError, "%s must be [hidden] or [tokens][hidden]", "gate");
+        if (N > 1 && gate->stride(rows) != 1) fail(PyExc_ValueError, "%s's rows must be contiguous", "gate");
+        gate_stride = rows && gate->size(0) > 1 ? gate->stride(0) : 0;
+    }
+    const float scale = real(a[3]);
+    const int post = number(a[4], "post"), pre = number(a[7], "pre");
+    const at::Tensor* post_weight = optional(on, a[5], at::kFloat, N, "post_weight", "[hidden]");
+    const at::Tensor* post_bias = optional(on, a[6], at::kFloat, N, "post_bias", "[hidden]");
+    const at::Tensor* pre_weight = optional(on, a[8], at::kFloat, N, "pre_weight", "[hidden]");
+    const at::Tensor* pre_bias = optional(on, a[9], at::kFloat, N, "pre_bias", "[hidden]");
+    const float eps = real(a[10]);
+    const at::Tensor* out = nullptr;
+    if (a[11] != Py_None) {
+        out = &matrix(on, a[11], "residual_out");
+        if (out->size(0) != T || out->size(1) != N) fail(PyExc_ValueError, "%s must have the inputs' shape", "residual_out");
+        if (residual && out->scalar_type() != residual->scalar_type()) fail(PyExc_TypeError, "%s must have residual's type", "residual_out");
+    }
+    const at::Tensor* given_x = optional(on, a[12], at::kHalf, T * N, "x", "[tokens][hidden]");
+    const int want_residual = out ? 1 : PyObject_IsTrue(a[13]), want_x = given_x ? 1 : PyObject_IsTrue(a[14]);
+    if (want_residual < 0 || want_x < 0) throw PythonError{};
+    const c10::cuda::CUDAGuard guard(one->device());
+    const at::ScalarType type = residual ? residual->scalar_type() : out ? out->scalar_type() : at::kFloat;
+    at::Tensor made, x;
+    if (out) made = *out;
+    else if (want_residual) made = fresh({T, N}, type);
+    if (want_x) x = given_x ? *given_x : fresh({T, N}, at::kHalf);
+    const pn_status st = pn_norm(data<void>(y), y ? matrix_stride(*y) : 0, y ? dtype_of(*y) : PN_DTYPE_F32, data<void>(residual),
+                                 residual ? matrix_stride(*residual) : 0, type == at::kFloat ? PN_DTYPE_F32 : PN_DTYPE_F16, data<float>(gate), gate_stride,
+                                 scale, T, static_cast<int>(N), post, data<float>(post_weight), data<float>(post_bias), pre, data<float>(pre_weight),
+                                 data<float>(pre_bias), eps, want_residual ? made.data_ptr() : nullptr, want_residual ? matrix_stride(made) : 0,
+                                 want_x ? data<uint16_t>(&x) : nullptr, stream_of(*one));
+    return answer(st, {want_residual ? given_or(a[11], made) : nullptr, want_x ? given_or(a[12], x) : nullptr});
+}
+
+// fp32 [pages][kv_heads][page_size]
+const at::Tensor& cache_weights(Device& on, PyObject* o, const Cache& c, const char* name) {
+    const at::Tensor& t = dense(on, o, at::kFloat, name);
+    if (t.dim() != 3 || t.size(0) != c.pages || t.size(1) != c.heads || t.size(2) != c.page_size)
+        fail(PyExc_ValueError, "%s must be [pages][kv_heads][page_size] of the cache", name);
+    return t;
+}
+
+// q, cache, table, lens, starts, max_queries, lse, scale, weights, decay, out (weights and out: one of them at least), window, sinks
+PyObject* kv_weigh(PyObject* const* a) {
+    Device on;
+    const Cache c(on, a[1]);
+    const at::Tensor& q = rows(on, a[0], "q", at::kHalf, at::kHalf, -1, c.dim);
+    const int64_t T = q.size(0), heads = q.size(1);
+    const at::Tensor& lens = dense(on, a[3], at::kInt, "lens");
+    const at::Tensor& starts = dense(on, a[4], at::kInt, "starts");
+    const int64_t B = lens.numel();
+    const at::Tensor& table = page_table(on, a[2], B);
+    if (starts.numel() != B + 1) fail(PyExc_ValueError, "%s must have one entry more than lens", "starts");
+    if (B > INT32_MAX || heads > INT32_MAX) fail(PyExc_ValueError, "%s has too many entries", "lens or q");
+    const int max_queries = number(a[5], "max_queries"), window = number(a[11], "window"), sinks = number(a[12], "sinks");
+    const at::Tensor* lse = optional(on, a[6], at::kFloat, T * heads, "lse", "[tokens][heads]");
+    if (!lse) fail(PyExc_TypeError, "%s must be a CUDA tensor", "lse");
+    const float scale = real(a[7]), decay = real(a[9]);
+    const at::Tensor* weights = a[8] == Py_None ? nullptr : &cache_weights(on, a[8], c, "weights");
+    const at::Tensor& out = cache_weights(on, a[10] == Py_None ? a[8] : a[10], c, "out");
+    const c10::cuda::CUDAGuard guard(q.device());
+    const pn_status st = pn_kv_weigh(data<uint16_t>(&q), row_stride(q), T, static_cast<int>(heads), c.t.data_ptr(), c.pages, c.page_size, c.heads, c.dim,
+                                     data<int32_t>(&table), table_stride(table), static_cast<int>(table.size(1)), data<int32_t>(&lens), data<int32_t>(&starts),
+                                     static_cast<int>(B), max_queries, data<float>(lse), scale, window, sinks, data<float>(weights), decay,
+                                     data<float>(&out), stream_of(q));
+    return answer(st, {given_or(a[10] == Py_None ? a[8] : a[10], out)});
+}
+
+// cache, weights, table, lens, held, free, ring, limit, budget, sinks, recent, out (None or the six tensors)
+PyObject* kv_evict(PyObject* const* a) {
+    Device on;
+    const Cache c(on, a[0]);
+    const at::Tensor& weights = cache_weights(on, a[1], c, "weights");
+    const at::Tensor& lens = dense(on, a[3], at::kInt, "lens");
+    const at::Tensor& held = dense(on, a[4], at::kInt, "held");
+    const at::Tensor& free = dense(on, a[5], at::kInt, "free");
+    const at::Tensor& ring = dense(on, a[6], at::kLong, "ring");
+    const int64_t B = lens.numel();
+    const at::Tensor& table = page_table(on, a[2], B);
+    if (held.numel() != B || ring.numel() != 2) fail(PyExc_ValueError, "%s must have one entry per request and ring two", "held");
+    if (B > INT32_MAX) fail(PyExc_ValueError, "%s has too many entries", "lens");
+    const int limit = number(a[7], "limit"), budget = number(a[8], "budget"), sinks = number(a[9], "sinks"), recent = number(a[10], "recent");
+    if (budget < 0 || budget > PN_MAX_BUDGET) fail(PyExc_ValueError, "%s is out of range", "budget");
+    static const char* const names[6] = {"out.table", "out.lens", "out.held", "out.ring", "out.kept", "out.refused"};
+    const int64_t sizes[6] = {B * table.size(1), B, B, 2, B * c.heads * budget, 1};
+    auto type_of = [](int i) { return i == 3 ? at::kLong : at::kInt; };
+    at::Tensor o[6];
+    PyObject* given[6];
+    const bool have = a[11] != Py_None;
+    if (have && (!PyTuple_Check(a[11]) || PyTuple_GET_SIZE(a[11]) != 6)) fail(PyExc_TypeError, "%s must be a KvEviction", "out");
+    for (int i = 0; i < 6; ++i) {
+        given[i] = have ? PyTuple_GET_ITEM(a[11], i) : Py_None;
+        if (!have) continue;
+        o[i] = dense(on, given[i], type_of(i), names[i]);
+        if (o[i].numel() != sizes[i]) fail(PyExc_ValueError, "%s has another size", names[i]);
+    }
+    const c10::cuda::CUDAGuard guard(lens.device());
+    if (!have) {
+        o[0] = fresh({B, table.size(1)}, at::kInt);
+        o[4] = fresh({B, c.heads, budget}, at::kInt);
+        const at::Tensor all = fresh({16 + (2 * B + 1) * 4}, at::kByte);       // the small ones share an allocation
+        o[3] = part_of(all, 0, 2, at::kLong);
+        o[1] = part_of(all, 16, B, at::kInt);
+        o[2] = part_of(all, 16 + 4 * B, B, at::kInt);
+        o[5] = part_of(all, 16 + 8 * B, 1, at::kInt);
+    }
+    const pn_status st = pn_kv_evict(c.t.data_ptr(), c.pages, c.page_size, c.heads, c.dim, data<float>(&weights), data<int32_t>(&table), table_stride(table),
+                                     static_cast<int>(table.size(1)), data<int32_t>(&lens), data<int32_t>(&held), static_cast<int>(B), limit, budget, sinks,
+                                     recent, data<int32_t>(&free), free.numel(), data<int64_t>(&ring), data<int32_t>(&o[0]), table.size(1), data<int32_t>(&o[1]),
+                                     data<int32_t>(&o[2]), data<int64_t>(&o[3]), data<int32_t>(&o[4]), data<int32_t>(&o[5]), stream_of(lens));
+    return answer(st, {given_or(given[0], o[0]), given_or(given[1], o[1]), given_or(given[2], o[2]), given_or(given[3], o[3]), given_or(given[4], o[4]),
+                       given_or(given[5], o[5])});
+}
+
 // A shortage of device memory, as PyTorch's own calls raise it.
 void raise_out_of_memory(const char* what) {
     PyObject* torch = PyImport_ImportModule("torch");
@@ -381,7 +558,8 @@ PyMethodDef method(const char* name) {
 }
 
 PyMethodDef g_methods[] = {method<kv_plan, 9>("kv_plan"), method<kv_append, 13>("kv_append"), method<kv_read, 4>("kv_read"),
-                           method<attention, 13>("attention"), method<verify, 7>("verify"), {nullptr, nullptr, 0, nullptr}};
+                           method<attention, 13>("attention"), method<verify, 7>("verify"), method<logprobs, 5>("logprobs"),
+                           method<norm, 15>("norm"), method<kv_weigh, 13>("kv_weigh"), method<kv_evict, 12>("kv_evict"), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_step", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

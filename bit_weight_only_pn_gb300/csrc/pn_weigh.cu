@@ -1,0 +1,335 @@
+// pn_weigh.cu -- the attention weight that cached tokens gather.
+//
+// For a cached token t of a request and a key/value head: the sum, over the step's
+// queries and the query heads that share the head and see t, of exp(scale q . k_t -
+// lse), with each row's lse as attention gave it, and decay times what t had before
+// (nothing, for the step's own tokens).
+//
+// Only K is read.  The products are those of pn_attn.cu: codes as fp16 subnormals,
+// 16 tokens x 8 query rows to an mma.sync, 8 sum q taken off through the
+// accumulator's first value, queries scaled by powers of two.  There is no softmax
+// state, so tokens do not wait for each other: a warp has 32 of them, whose codes
+// stay in registers while the query rows go by, and each lane sums what its columns
+// give.  A token's sum is made by one warp in a fixed order; nothing is joined and
+// no result depends on timing.
+#include <cstdint>
+
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "pn_attn.cuh"
+
+namespace pn {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kTile = 32;                      // tokens of a warp
+constexpr int kUnit = kWarps * kTile;          // tokens of a block's unit of work
+constexpr int kChunk = 8 * kWarps;             // query rows made ready at a time, 8 by a warp
+
+struct Params {
+    WeighArgs a;
+    KvCache cache;
+    int group;                 // query heads per key/value head
+    float scale_log2;          // scale * log2 e
+};
+
+struct Request {
+    int n, q0, pos0, len, rows;
+    int units;                 // per head
+    __device__ __forceinline__ void read(const Params& P, int b) {
+        const WeighArgs& a = P.a;
+        const int T = static_cast<int>(a.tokens);
+        q0 = min(max(a.starts[b], 0), T);
+        n = min(min(max(a.starts[b + 1], q0), T) - q0, a.max_queries);
+        const int64_t room = static_cast<int64_t>(a.max_pages) << P.cache.page_shift;
+        len = static_cast<int>(min(static_cast<int64_t>(max(a.lens[b], 0)), room));
+        pos0 = len - n;
+        rows = n * P.group;
+        units = n > 0 ? (len + kUnit - 1) / kUnit : 0;
+    }
+};
+
+// Eight query rows ready for the products: B fragments by lane, and for each row
+// what the products start from, the factor to scores times log2 e, -lse log2 e
+// (-inf: a row that gives nothing) and its position.
+template <int D>
+struct Rows {
+    uint4 q[D / 64][2][32];
+    float start[D / 64][8];
+    float factor[8], less[8];
+    int pos[8];
+};
+
+template <int D>
+__device__ __forceinline__ void make_ready(const Params& P, const Request& r, int h, int row0, Rows<D>& to) {
+    constexpr int NG = D / 64;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int row = min(row0 + g, r.rows - 1), qi = row / P.group, head = h * P.group + row - qi * P.group;
+    const __half* src = P.a.q + (r.q0 + qi) * P.a.q_stride + head * D;
+    uint4 f[NG][2];
+    uint32_t top = 0;                          // the row's largest |q|, as bits
+#pragma unroll
+    for (int j = 0; j < NG; ++j)
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            f[j][w] = *reinterpret_cast<const uint4*>(src + 64 * j + 16 * t + 8 * w);
+            const uint32_t v[4] = {f[j][w].x, f[j][w].y, f[j][w].z, f[j][w].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) top = __vmaxu2(top, v[i] & 0x7FFF7FFFu);
+        }
+    top = max(top & 0xFFFFu, top >> 16);
+    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+    const int e = 25 - static_cast<int>(max(top >> 10, 1u));                 // the largest |q| 2^e lies in [2^10, 2^11)
+    const float up = __int_as_float((127 + e) << 23);
+#pragma unroll
+    for (int j = 0; j < NG; ++j) {
+        float sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            const uint32_t v[4] = {f[j][w].x, f[j][w].y, f[j][w].z, f[j][w].w};
+            uint32_t made[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float a0 = half_bits_to_float(v[i] & 0xFFFFu) * up, a1 = half_bits_to_float(v[i] >> 16) * up;
+                sum += a0 + a1;
+                made[i] = i & 1 ? pack_half2(a0, a1) : pack_half2(16.0f * a0, 16.0f * a1);
+            }
+            to.q[j][w][lane] = make_uint4(made[0], made[1], made[2], made[3]);
+        }
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
+        if (t == 0) to.start[j][g] = -0x1p-17f * sum;                        // -8 * 2^-20
+    }
+    if (t == 0) {
+        const bool real = row0 + g < r.rows;
+        const float lse = real ? P.a.lse[static_cast<int64_t>(r.q0 + qi) * P.a.heads + head] : -INFINITY;
+        to.factor[g] = real ? P.scale_log2 * __int_as_float((127 + 20 - e) << 23) : 0.0f;
+        to.less[g] = lse == -INFINITY ? -INFINITY : -1.4426950408889634f * lse;
+        to.pos[g] = r.pos0 + qi;
+    }
+}
+
+// A warp's tokens: codes of K (words of tokens g and g + 8 of each record) and scales.
+template <int D>
+struct Keys {
+    static constexpr int kWords = D / 64 * 2;  // of a token, to a lane
+    uint32_t w[2][2][kWords];
+    float d[2][2][D / 64];
+};
+
+template <int D>
+__device__ __forceinline__ void load_keys(const uint8_t* const (&record)[2], Keys<D>& k) {
+    constexpr int NG = D / 64, GP = kv_plane_groups(D), PL = kv_planes(D);
+    const int lane = threadIdx.x & 31, g = lane >> 2;
+#pragma unroll
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+#pragma unroll
+            for (int i = 0; i < Keys<D>::kWords; ++i) k.w[r][hh][i] = 0;
+#pragma unroll
+            for (int j = 0; j < NG; ++j) k.d[r][hh][j] = 0.0f;
+            if (!record[r]) continue;
+#pragma unroll
+            for (int pl = 0; pl < PL; ++pl) {
+                const uint8_t* p = record[r] + ((hh * PL + pl) * 32 + lane) * 8 * GP;
+                if constexpr (GP == 2) {
+                    const uint4 v = *reinterpret_cast<const uint4*>(p);
+                    k.w[r][hh][4 * pl] = v.x; k.w[r][hh][4 * pl + 1] = v.y; k.w[r][hh][4 * pl + 2] = v.z; k.w[r][hh][4 * pl + 3] = v.w;
+                } else {
+                    const uint2 v = *reinterpret_cast<const uint2*>(p);
+                    k.w[r][hh][0] = v.x; k.w[r][hh][1] = v.y;
+                }
+            }
+            const __half* d = reinterpret_cast<const __half*>(record[r] + kv_k_scales(D)) + (g + 8 * hh) * NG;
+#pragma unroll
+            for (int j = 0; j < NG; ++j) k.d[r][hh][j] = __half2float(d[j]);
+        }
+}
+
+// The products of the warp's 32 tokens with NT times eight rows, by group scaled and summed.
+template <int D, int NT>
+__device__ __forceinline__ void products(const Keys<D>& k, const Rows<D>* rows, float (&x)[2][NT][4]) {
+    constexpr int NG = D / 64;
+    const int lane = threadIdx.x & 31, t = lane & 3;
+#pragma unroll
+    for (int j = 0; j < NG; ++j) {
+        float acc[2][NT][4];
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            uint4 b[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) b[n] = rows[n].q[j][w][lane];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                // word 2t + w of group j of tokens g (a) and g + 8 (c)
+                const uint32_t a = k.w[r][0][2 * j + w], c = k.w[r][1][2 * j + w], as = a >> 8, cs = c >> 8;
+                const uint32_t a0 = raw_pair<0>(a, as), a1 = raw_pair<0>(c, cs), a2 = raw_pair<1>(a, as), a3 = raw_pair<1>(c, cs);
+                const uint32_t b0 = raw_pair<2>(a, as), b1 = raw_pair<2>(c, cs), b2 = raw_pair<3>(a, as), b3 = raw_pair<3>(c, cs);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    if (w == 0) {
+                        const float2 s = *reinterpret_cast<const float2*>(rows[n].start[j] + 2 * t);
+                        mma_from(acc[r][n], a0, a1, a2, a3, b[n].x, b[n].y, s.x, s.y, s.x, s.y);
+                    } else {
+                        mma_16816(acc[r][n], a0, a1, a2, a3, b[n].x, b[n].y);
+                    }
+                    mma_16816(acc[r][n], b0, b1, b2, b3, b[n].z, b[n].w);
+                }
+            }
+        }
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    x[r][n][i] = j ? fmaf(k.d[r][i >> 1][j], acc[r][n][i], x[r][n][i]) : k.d[r][i >> 1][j] * acc[r][n][i];
+    }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const __grid_constant__ Params P) {
+    constexpr int NT = D == 256 ? 1 : 2;       // row groups at a time, as registers allow
+    __shared__ Rows<D> ready[kWarps];
+    __shared__ uint64_t scan[kThreads + 1];
+    __shared__ uint64_t warp_sums[kWarps];
+    const WeighArgs& a = P.a;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const int heads = P.cache.heads, window = a.window ? a.window : INT32_MAX;
+    // units before each thread's requests
+    const int each = (a.batch + kThreads - 1) / kThreads;
+    {
+        const int b0 = min(static_cast<int>(threadIdx.x) * each, a.batch), b1 = min(b0 + each, a.batch);
+        uint64_t mine = 0;
+        for (int b = b0; b < b1; ++b) {
+            Request r;
+            r.read(P, b);
+            mine += static_cast<uint64_t>(r.units) * heads;
+        }
+        uint64_t in = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const uint64_t o = __shfl_up_sync(0xFFFFFFFFu, in, d);
+            if (lane >= d) in += o;
+        }
+        if (lane == 31) warp_sums[warp] = in;
+        __syncthreads();
+        uint64_t at = in - mine;
+        for (int w = 0; w < warp; ++w) at += warp_sums[w];
+        scan[threadIdx.x] = at;
+        if (threadIdx.x == kThreads - 1) scan[kThreads] = at + mine;
+        __syncthreads();
+    }
+    const uint64_t total = scan[kThreads];
+    for (uint64_t u = blockIdx.x; u < total; u += gridDim.x) {
+        int lo = 0, hi = kThreads - 1;
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) >> 1;
+            if (scan[mid] <= u) lo = mid;
+            else hi = mid - 1;
+        }
+        int b = lo * each;
+        uint64_t at = scan[lo];
+        Request r;
+        for (;; ++b) {
+            r.read(P, b);
+            const uint64_t units = static_cast<uint64_t>(r.units) * heads;
+            if (u < at + units) break;
+            at += units;
+        }
+        const int h = static_cast<int>((u - at) / r.units), first = static_cast<int>((u - at) % r.units) * kUnit;
+        const int tok0 = first + warp * kTile;
+        const uint8_t* record[2];
+        int64_t place[2];                      // of each record's weights
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int tok = tok0 + i * kKvTokens;
+            record[i] = nullptr;
+            place[i] = -1;
+            if (tok >= r.len) continue;
+            const int page = a.table[b * a.table_stride + (tok >> P.cache.page_shift)], in_page = tok & (P.cache.page_size - 1);
+            if (page < 0 || page >= P.cache.pages) continue;
+            record[i] = P.cache.record((static_cast<int64_t>(page) << P.cache.page_shift) + in_page, h);
+            place[i] = ((static_cast<int64_t>(page) * heads + h) << P.cache.page_shift) + in_page;
+        }
+        Keys<D> keys;
+        load_keys<D>(record, keys);
+        // lane (g, t) writes token 8 t + g of the tile
+        const int tok = tok0 + 8 * t + g;
+        const int64_t mine = t < 2 ? place[0] : place[1];
+        const bool writes = mine >= 0 && tok < r.len;
+        const int64_t to = mine + ((8 * t + g) & 15);
+        const float before = writes && a.weights && tok < r.pos0 ? a.decay * a.weights[to] : 0.0f;
+        float sum[2][2] = {};
+        // the queries that see any of the unit's tokens
+        const int last = min(first + kUnit, r.len) - 1;
+        const int i0 = max(first - r.pos0, 0);
+        int i1 = r.n;
+        if (a.window && first >= a.sinks) i1 = static_cast<int>(min(static_cast<int64_t>(i1), max(static_cast<int64_t>(last) + window - r.pos0, static_cast<int64_t>(0))));
+        const int row_end = i1 * P.group;
+        for (int row0 = i0 * P.group / 8 * 8; row0 < row_end; row0 += kChunk) {
+            __syncthreads();                   // the rows before have been read
+            if (row0 + 8 * warp < row_end) make_ready<D>(P, r, h, row0 + 8 * warp, ready[warp]);
+            __syncthreads();
+            const int groups = min((row_end - row0 + 7) / 8, kWarps);
+            for (int n0 = 0; n0 < groups; n0 += NT) {
+                const int from = row0 + 8 * n0, upto = min(from + 8 * min(NT, groups - n0), r.rows) - 1;
+                const int pos_lo = r.pos0 + from / P.group, pos_hi = r.pos0 + upto / P.group;
+                if (tok0 > pos_hi) continue;
+                float x[2][NT][4];
+                products<D, NT>(keys, ready + n0, x);
+                const bool plain = n0 + NT <= groups && record[0] && record[1] && tok0 + kTile - 1 <= pos_lo && (tok0 > pos_hi - window || tok0 + kTile <= a.sinks);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    if (n0 + n >= groups) break;
+                    const Rows<D>& rows = ready[n0 + n];
+                    const float2 f = *reinterpret_cast<const float2*>(rows.factor + 2 * t), l = *reinterpret_cast<const float2*>(rows.less + 2 * t);
+                    const int2 pos = *reinterpret_cast<const int2*>(rows.pos + 2 * t);
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+#pragma unroll
+                        for (int hh = 0; hh < 2; ++hh) {
+                            float p0 = ex2(fmaf(x[i][n][2 * hh], f.x, l.x)), p1 = ex2(fmaf(x[i][n][2 * hh + 1], f.y, l.y));
+                            if (!plain) {
+                                const int k = tok0 + i * kKvTokens + hh * 8 + g;
+                                p0 = k <= pos.x && (k > pos.x - window || k < a.sinks) ? p0 : 0.0f;
+                                p1 = k <= pos.y && (k > pos.y - window || k < a.sinks) ? p1 : 0.0f;
+                            }
+                            sum[i][hh] += p0 + p1;
+                        }
+                }
+            }
+        }
+        float all = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            float s = sum[i >> 1][i & 1];
+            s += __shfl_xor_sync(0xFFFFFFFFu, s, 1);
+            s += __shfl_xor_sync(0xFFFFFFFFu, s, 2);
+            if (t == i) all = s;
+        }
+        if (writes) a.out[to] = before + all;
+    }
+}
+
+template <int D>
+cudaError_t launch(const Params& P, int num_sms, cudaStream_t s) {
+    weigh_kernel<D><<<num_sms * 2, kThreads, 0, s>>>(P);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_weigh(const WeighArgs& a, const KvGeometry& g, int num_sms, cudaStream_t s) {
+    int shift = 0;
+    while ((1 << shift) < g.page_size) ++shift;
+    const Params P{a, KvCache{g.data, g.pages, g.page_size, shift, g.heads, g.D}, a.heads / g.heads, a.scale * 1.4426950408889634f};
+    if (g.D == 64) return launch<64>(P, num_sms, s);
+    return g.D == 128 ? launch<128>(P, num_sms, s) : launch<256>(P, num_sms, s);
+}
+
+}  // namespace pn

@@ -16,6 +16,7 @@ import torch
 PN3T = 124
 PN4T = 125
 ALGO_AUTO, ALGO_TENSOR_CORE, ALGO_CUDA_CORE, ALGO_CUDA_CORE_STAGED = 0, 1, 2, 3
+NORM_NONE, NORM_RMS, NORM_LAYER = 0, 1, 2
 MAX_M = 16
 MAX_LAYER = 8
 STATUS = {0: "PN_OK", 1: "PN_EINVAL", 2: "PN_EALIGN", 3: "PN_EUNSUPPORTED", 4: "PN_ECUDA",
@@ -111,6 +112,16 @@ def lib() -> ctypes.CDLL:
                                        i32, i32, vp, vp, vp, sz, vp]
             L.pn_verify.restype = i32
             L.pn_verify.argtypes = [vp, vp, i64, vp, i64, vp, vp, i32, i32, i32, vp, vp, vp]
+            L.pn_logprobs.restype = i32
+            L.pn_logprobs.argtypes = [vp, i64, i32, i64, i32, f32, vp, i32, vp, vp, i32, vp, vp, vp]
+            L.pn_norm.restype = i32
+            L.pn_norm.argtypes = [vp, i64, i32, vp, i64, i32, vp, i64, f32, i64, i32, i32, vp, vp, i32, vp, vp, f32, vp, i64, vp, vp]
+            L.pn_kv_weigh.restype = i32
+            L.pn_kv_weigh.argtypes = [vp, i64, i64, i32, vp, i64, i32, i32, i32, vp, i64, i32, vp, vp, i32, i32, vp, f32, i32, i32,
+                                      vp, f32, vp, vp]
+            L.pn_kv_evict.restype = i32
+            L.pn_kv_evict.argtypes = [vp, i64, i32, i32, i32, vp, vp, i64, i32, vp, vp, i32, i32, i32, i32, i32, vp, i64, vp, vp,
+                                      i64, vp, vp, vp, vp, vp, vp]
             L.pn_read_ranges.restype = i32
             L.pn_read_ranges.argtypes = [ctypes.POINTER(vp), ctypes.POINTER(sz), i32, vp, vp]
             L.pn_hadamard.restype = i32
@@ -550,6 +561,84 @@ def verify(tokens: torch.Tensor, target: torch.Tensor, draft: torch.Tensor | Non
     uniforms fp32 [batch][drafts + 1] in [0, 1).  Returns (accepted int32
     [batch], tokens int32 [batch][drafts + 1]: the accepted ones, one more, -1)."""
     return _call(stream, _step().verify, "pn_verify", tokens, target, draft, uniforms, counts, accepted, out)[1:]
+
+
+class LogProbs(NamedTuple):
+    """What pn.logprobs gives of rows of logits; None where it was not asked for."""
+    logprobs: torch.Tensor      # fp32 [rows] or [rows][count]: log probabilities of the given tokens
+    entropy: torch.Tensor       # fp32 [rows]
+    top_tokens: torch.Tensor    # int32 [rows][top], -1 where fewer have a probability
+    top_logprobs: torch.Tensor  # fp32 [rows][top]
+
+
+def logprobs(logits: torch.Tensor, tokens: torch.Tensor | None = None, top: int = 0, scale: float = 1.0, entropy: bool = True,
+             stream=None) -> LogProbs:
+    """Log probabilities of given tokens (int32 [rows] or [rows][count]), the
+    entropy and the `top` (at most 32) likeliest tokens of softmax(scale * logits),
+    logits fp32 or fp16 [rows][vocab], rows at any stride (see pn_logprobs).  One
+    read of the logits; ties go to the lowest token."""
+    return LogProbs(*_call(stream, _step().logprobs, "pn_logprobs", logits, tokens, top, scale, entropy)[1:])
+
+
+def norm(y: torch.Tensor | None, residual: torch.Tensor | None = None, gate: torch.Tensor | None = None, scale: float = 1.0,
+         post: int = NORM_NONE, post_weight: torch.Tensor | None = None, post_bias: torch.Tensor | None = None, pre: int = NORM_RMS,
+         pre_weight: torch.Tensor | None = None, pre_bias: torch.Tensor | None = None, eps: float = 1e-6,
+         residual_out: torch.Tensor | None = None, x: torch.Tensor | None = None, want_residual: bool | None = None, want_x: bool = True,
+         stream=None):
+    """A block's output into the residual stream and the next GEMV's input, in one
+    pass (see pn_norm): r' = residual + scale * gate * post(y), x = pre(r') as fp16.
+    y, residual [tokens][hidden] fp32 or fp16 at any row stride (one may be None);
+    gate fp32 [hidden] or [tokens][hidden]; post, pre NORM_NONE, NORM_RMS or
+    NORM_LAYER with fp32 weights and biases.  Returns (r' in residual's type, x);
+    residual_out may be `residual`.  want_residual: None stands for "if there is a y";
+    what is not wanted is None (and pre is then left out with x)."""
+    if want_residual is None:
+        want_residual = y is not None
+    if not want_x and x is None:
+        pre, pre_weight, pre_bias = NORM_NONE, None, None
+    return _call(stream, _step().norm, "pn_norm", y, residual, gate, scale, post, post_weight, post_bias, pre, pre_weight, pre_bias, eps,
+                 residual_out, x, want_residual, want_x)[1:]
+
+
+def kv_weights(cache: torch.Tensor) -> torch.Tensor:
+    """Zeroed weights for the tokens of a 4-bit cache: fp32 [pages][kv_heads][page_size]."""
+    return torch.zeros(cache.shape[0], cache.shape[1], cache.shape[2] * 16, device=cache.device)
+
+
+def kv_weigh(q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, starts: torch.Tensor, max_queries: int,
+             lse: torch.Tensor, scale: float, weights: torch.Tensor | None = None, decay: float = 1.0, out: torch.Tensor | None = None,
+             window: int = 0, sinks: int = 0, stream=None) -> torch.Tensor:
+    """The attention weight that each cached token gathered from a step's queries
+    (see pn_kv_weigh): arguments as of the attention call before it, and the lse
+    that it returned.  Added to decay times `weights` (the step's own tokens begin
+    at zero; None: all do) and written to `out` (None: into `weights`; both None:
+    new zeroed ones)."""
+    if weights is None and out is None:
+        with torch.cuda.stream(stream):              # zeroed in the order of the stream that runs the call
+            out = kv_weights(cache)
+    return _call(stream, _step().kv_weigh, "pn_kv_weigh", q, cache, table, lens, starts, max_queries, lse, scale, weights, decay, out, window, sinks)[1]
+
+
+class KvEviction(NamedTuple):
+    """The state after pn.kv_evict."""
+    table: torch.Tensor         # int32 [batch][pages per request]: pages of a request cut back, then -1; others as they were
+    lens: torch.Tensor          # int32 [batch]
+    held: torch.Tensor          # int32 [batch]
+    ring: torch.Tensor          # int64 [2]
+    kept: torch.Tensor          # int32 [batch][kv_heads][budget]: the positions kept, -1 for a request left alone
+    refused: torch.Tensor       # int32 [1]: requests past the limit that found no pages
+
+
+def kv_evict(cache: torch.Tensor, weights: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, held: torch.Tensor, free: torch.Tensor,
+             ring: torch.Tensor, limit: int, budget: int, sinks: int = 0, recent: int = 0, out: KvEviction | None = None,
+             stream=None) -> KvEviction:
+    """Requests with more than `limit` cached tokens keep `budget` of them, each head
+    its first `sinks`, its last `recent` and those of the largest weight between, in
+    pages from the free ring; their old pages are given back (see pn_kv_evict).  The
+    positions of later tokens go on from the old length: add lens - result.lens to
+    those that kv_plan gives from then on.  `out` is an earlier result to write into."""
+    return KvEviction(*_call(stream, _step().kv_evict, "pn_kv_evict", cache, weights, table, lens, held, free, ring, limit, budget, sinks, recent,
+                             out)[1:])
 
 
 def read_ranges(tensors, sink: torch.Tensor, stream=None) -> torch.Tensor:

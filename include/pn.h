@@ -499,6 +499,115 @@ pn_status pn_verify(const int32_t* tokens, const float* target, int64_t target_s
                     int vocab, int32_t* accepted, int32_t* out, pn_stream stream);
 
 /*
+ * pn_logprobs: for each of `rows` rows of logits (`dtype`, vocab values, rows at
+ * `stride` elements), with x = scale * logit and lse = ln sum exp(x) over the row
+ * (scale is one over the temperature, from 2^-64 to 2^64):
+ *   logprobs[r][i] = x(tokens[r][i]) - lse for `count` (>= 0) given tokens;
+ *   entropy[r] = -sum p ln p, p = exp(x - lse) (NULL: not wanted);
+ *   top_tokens[r][i], top_logprobs[r][i] for i < top (0 .. PN_MAX_TOP): the tokens
+ *   of the largest logits, the lowest first where logits are equal.
+ * NaN and logits of -1.7e38 or less have probability 0: their log probability is
+ * -inf, and they are no alternatives; so is a token outside the vocabulary.  Where
+ * fewer than `top` tokens are left, -1 and -inf follow.  A row that has none gets
+ * -inf and entropy 0.  A logit above 1.7e38 counts as 1.7e38.
+ * Sums are fp32; a log probability is within 2^-22 (ln vocab + 1) + 2^-23 |x - max x|
+ * of the exact value.  Deterministic.  logits to their element, other arrays 4-byte aligned; rows
+ * whose 16-byte lines begin elsewhere than the row cost no copy.  No output shares
+ * memory with an input or another output.
+ */
+#define PN_MAX_TOP 32
+pn_status pn_logprobs(const void* logits, int64_t stride, int dtype, int64_t rows, int vocab, float scale,
+                      const int32_t* tokens, int count, float* logprobs, float* entropy, int top,
+                      int32_t* top_tokens, float* top_logprobs, pn_stream stream);
+
+/*
+ * pn_norm: a block's output y into the residual stream r, and the next block's
+ * input x, for `tokens` rows of `hidden` (1 .. 32768) values:
+ *   z = post(y);  r' = r + scale * gate * z;  x = pre(r')
+ * y, residual (r) and residual_out (r') of y_dtype, residual_dtype (both r and r'),
+ * rows at their strides in elements; x fp16 [tokens][hidden], as pn_gemv takes it.
+ * gate: fp32 rows at gate_stride (0: one row for all tokens), NULL: 1.
+ * post, pre:
+ *   PN_NORM_NONE   the row as it is
+ *   PN_NORM_RMS    v / sqrt(mean(v^2) + eps) * weight + bias
+ *   PN_NORM_LAYER  the same of v - mean(v)
+ * weight, bias: fp32 [hidden], NULL: 1 and 0 (NULL where there is no norm).
+ * y NULL: r' = r.  residual NULL: r' = scale * gate * z.  residual_out NULL: r' is
+ * not stored.  x NULL: only r' is wanted.  One of the two inputs and one of the two
+ * outputs there has to be.  Arithmetic and sums are fp32, each result is rounded
+ * once, and x is made of r' as it was before that.  residual_out may be residual,
+ * with its stride; else no output shares memory with an input or the other output.
+ * Arrays to their element; where all rows begin at 16 bytes (fp16: 8) and hidden is
+ * a multiple of 4, four values are taken at a time.
+ */
+typedef enum { PN_NORM_NONE = 0, PN_NORM_RMS = 1, PN_NORM_LAYER = 2 } pn_norm_kind;
+#define PN_MAX_HIDDEN 32768
+pn_status pn_norm(const void* y, int64_t y_stride, int y_dtype, const void* residual, int64_t residual_stride,
+                  int residual_dtype, const float* gate, int64_t gate_stride, float scale, int64_t tokens, int hidden,
+                  int post, const float* post_weight, const float* post_bias, int pre, const float* pre_weight,
+                  const float* pre_bias, float eps, void* residual_out, int64_t out_stride, uint16_t* x,
+                  pn_stream stream);
+
+/*
+ * A cache that keeps what is looked at: pn_kv_weigh gathers, for each cached token
+ * and key/value head, the attention weight that queries gave it; pn_kv_evict cuts
+ * requests past a limit back to a budget of tokens by it.  Weights are fp32
+ * [pages][kv_heads][page_size], beside the cache: a token's place is its slot's.
+ *
+ * pn_kv_weigh: q, table, lens, starts, max_queries, scale, window and sinks as in a
+ * pn_attention call and lse as that call wrote it.  For every request with queries,
+ * head and cached token t < lens[b]:
+ *   out_t = before_t + sum over the queries and the heads of the group that see t of
+ *           exp(scale * q . k_t - lse)
+ *   before_t = decay * weights_t, and 0 for the step's own tokens (those of its
+ *           queries' positions on) or where weights is NULL
+ * (a row whose lse is -inf gives nothing).  Other entries of out, among them those of
+ * requests without queries, are not written.  out may be weights; else the
+ * two share no memory.  No other output is written, no workspace is needed.  Tokens
+ * on pages outside the cache are passed over.  Requests may share pages as long as
+ * nobody reads what they leave there: each writes its own sums.  Each sum is made in
+ * fp32 in one order: deterministic, and independent of what else is in the batch.
+ * Scores err as pn_attention's; a sum of n probabilities by n 2^-24 of it more.
+ * q and cache 16-byte aligned, q_stride a multiple of 8.
+ */
+pn_status pn_kv_weigh(const uint16_t* q, int64_t q_stride, int64_t tokens, int heads, const void* cache,
+                      int64_t pages, int page_size, int kv_heads, int head_dim, const int32_t* table,
+                      int64_t table_stride, int max_pages, const int32_t* lens, const int32_t* starts, int batch,
+                      int max_queries, const float* lse, float scale, int window, int sinks, const float* weights,
+                      float decay, float* out, pn_stream stream);
+
+/*
+ * pn_kv_evict: request b < batch (at most 16384) with lens[b] > limit keeps `budget`
+ * (1 .. limit, at most PN_MAX_BUDGET) tokens of every head: the first `sinks`, the last
+ * `recent` (sinks + recent <= budget), and of those between them the ones with the
+ * largest weights, the earlier where they are equal (NaN counts as the lowest).
+ * Heads keep tokens of their own.  They go in their order to the places 0 .. budget -
+ * 1 of pages n = ceil(budget / page_size) of which are taken from the free ring's
+ * head (ring and free_pages as in pn_kv_plan), with codes, scales and weights as they
+ * are; keys stay rotated by their first positions, so positions of tokens to come go
+ * on from the old length.  The held[b] old pages go behind the ring's tail, in
+ * request order.  Requests take pages in their order as long as there are n; the
+ * others are refused and stay as they are.
+ *   table_out [batch][out_stride], max_pages entries each: the table after the call
+ *   (of a request cut back: its n pages, then -1); lens_out, held_out, ring_out
+ *   {head, tail}: the state after it; refused[1]: how many did not fit;
+ *   kept [batch][kv_heads][budget]: the positions that a head kept, -1 throughout
+ *   for a request that was left alone.
+ * Inputs stay as they are but for free_pages' entries behind the tail and the cache
+ * and the weights of the pages taken, so a call repeated on them gives the same.
+ * Pages that several requests share may be read, but are given back by each that
+ * holds them: take them out of held first.  A kept token on a page outside the
+ * cache becomes zeros.  No output shares memory with an input or another output.
+ */
+#define PN_MAX_BUDGET (1 << 23)
+pn_status pn_kv_evict(void* cache, int64_t pages, int page_size, int kv_heads, int head_dim, float* weights,
+                      const int32_t* table, int64_t table_stride, int max_pages, const int32_t* lens,
+                      const int32_t* held, int batch, int limit, int budget, int sinks, int recent,
+                      int32_t* free_pages, int64_t ring_pages, const int64_t* ring, int32_t* table_out,
+                      int64_t out_stride, int32_t* lens_out, int32_t* held_out, int64_t* ring_out, int32_t* kept,
+                      int32_t* refused, pn_stream stream);
+
+/*
  * pn_read_ranges (diagnostic): the plain read-bandwidth ceiling a GEMV is
  * measured against.  Reads the first floor(bytes[i] / 16) * 16 bytes of each
  * of `count` (1 .. PN_MAX_LAYER) device ranges ptrs[i] once, with 16-byte
