@@ -33,11 +33,29 @@ struct Params {
     KvCache cache;
     int group;                 // query heads per key/value head
     float scale_log2;          // scale * log2 e
+    float scale_rest;          // what that left of it, relative to it
 };
+
+// A row's lse as the exponent's argument takes it.  exp2(x f - lse log2 e), with x f
+// and lse log2 e some tens, would carry the roundings of f and of lse log2 e in all
+// of the row's probabilities (2^-20 each).  So the argument gets a multiple of 2^-6,
+// which a sum with x f takes up without a rounding before its own, and what is left,
+// with f's rounding where x = lse, becomes a factor near 1 of the row's probabilities.
+struct LogSum {
+    float less, factor;
+};
+__device__ __forceinline__ LogSum log_sum_of(float lse, float scale_rest) {
+    if (lse == -INFINITY) return {-INFINITY, 0.0f};
+    constexpr float kLog2e = 1.44269502f, kLog2eRest = 1.92596299e-8f;       // log2 e in two parts
+    const float hi = lse * kLog2e, lo = fmaf(lse, kLog2e, -hi) + lse * kLog2eRest;
+    const float near = rintf(hi * 64.0f) * 0.015625f;
+    // 2^u for |u| a little above 2^-7, by its series
+    const float u = ((near - hi) - lo + hi * scale_rest) * 0.693147181f;
+    return {-near, fabsf(u) < 1.0f ? fmaf(u, fmaf(u, fmaf(u, fmaf(u, 0.0416666667f, 0.166666667f), 0.5f), 1.0f), 1.0f) : 1.0f};
+}
 
 struct Request {
     int n, q0, pos0, len, rows;
-    int units;                 // per head
     __device__ __forceinline__ void read(const Params& P, int b) {
         const WeighArgs& a = P.a;
         const int T = static_cast<int>(a.tokens);
@@ -47,27 +65,69 @@ struct Request {
         len = static_cast<int>(min(static_cast<int64_t>(max(a.lens[b], 0)), room));
         pos0 = len - n;
         rows = n * P.group;
-        units = n > 0 ? (len + kUnit - 1) / kUnit : 0;
     }
 };
 
-// Eight query rows ready for the products: B fragments by lane, and for each row
-// what the products start from, the factor to scores times log2 e, -lse log2 e
-// (-inf: a row that gives nothing) and its position.
-template <int D>
-struct Rows {
-    uint4 q[D / 64][2][32];
-    float start[D / 64][8];
-    float factor[8], less[8];
-    int pos[8];
-};
+// Units of a head's kTokens tokens that a request has: none without queries.
+template <int kTokens>
+__device__ __forceinline__ int units_of(const Request& r) { return r.n > 0 ? (r.len + kTokens - 1) / kTokens : 0; }
 
+// scan[i]: units of all heads before thread i's requests, of which it has as many as
+// is returned; scan[kThreads] all of them.
+template <int kTokens>
+__device__ __forceinline__ int scan_units(const Params& P, uint64_t* scan, uint64_t* warp_sums) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, each = (P.a.batch + kThreads - 1) / kThreads;
+    const int b0 = min(static_cast<int>(threadIdx.x) * each, P.a.batch), b1 = min(b0 + each, P.a.batch);
+    uint64_t mine = 0;
+    for (int b = b0; b < b1; ++b) {
+        Request r;
+        r.read(P, b);
+        mine += static_cast<uint64_t>(units_of<kTokens>(r)) * P.cache.heads;
+    }
+    uint64_t in = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const uint64_t o = __shfl_up_sync(0xFFFFFFFFu, in, d);
+        if (lane >= d) in += o;
+    }
+    if (lane == 31) warp_sums[warp] = in;
+    __syncthreads();
+    uint64_t at = in - mine;
+    for (int w = 0; w < warp; ++w) at += warp_sums[w];
+    scan[threadIdx.x] = at;
+    if (threadIdx.x == kThreads - 1) scan[kThreads] = at + mine;
+    __syncthreads();
+    return each;
+}
+
+// Unit u (there is one): its request, head and place among the head's units.
+template <int kTokens>
+__device__ __forceinline__ void locate(const Params& P, const uint64_t* scan, int each, uint64_t u, Request& r, int& b, int& h, int& unit) {
+    int lo = 0, hi = kThreads - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (scan[mid] <= u) lo = mid;
+        else hi = mid - 1;
+    }
+    b = lo * each;
+    u -= scan[lo];
+    for (;; ++b) {
+        r.read(P, b);
+        const uint64_t units = static_cast<uint64_t>(units_of<kTokens>(r)) * P.cache.heads;
+        if (u < units) break;
+        u -= units;
+    }
+    const uint64_t of_head = static_cast<uint64_t>(units_of<kTokens>(r));
+    h = static_cast<int>(u / of_head);
+    unit = static_cast<int>(u - h * of_head);
+}
+
+// Row g of eight as the lane's part of the products' B fragments, scaled by a power of
+// two, the sums that the products start from, and the factor back to q . k.
 template <int D>
-__device__ __forceinline__ void make_ready(const Params& P, const Request& r, int h, int row0, Rows<D>& to) {
+__device__ __forceinline__ float ready_fragments(const __half* src, uint4 (&q)[D / 64][2], float (&start)[D / 64]) {
     constexpr int NG = D / 64;
-    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const int row = min(row0 + g, r.rows - 1), qi = row / P.group, head = h * P.group + row - qi * P.group;
-    const __half* src = P.a.q + (r.q0 + qi) * P.a.q_stride + head * D;
+    const int t = threadIdx.x & 3;
     uint4 f[NG][2];
     uint32_t top = 0;                          // the row's largest |q|, as bits
 #pragma unroll
@@ -97,17 +157,64 @@ __device__ __forceinline__ void make_ready(const Params& P, const Request& r, in
                 sum += a0 + a1;
                 made[i] = i & 1 ? pack_half2(a0, a1) : pack_half2(16.0f * a0, 16.0f * a1);
             }
-            to.q[j][w][lane] = make_uint4(made[0], made[1], made[2], made[3]);
+            q[j][w] = make_uint4(made[0], made[1], made[2], made[3]);
         }
         sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
         sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
-        if (t == 0) to.start[j][g] = -0x1p-17f * sum;                        // -8 * 2^-20
+        start[j] = -0x1p-17f * sum;                                          // -8 * 2^-20
+    }
+    return __int_as_float((127 + 20 - e) << 23);
+}
+
+// The sums of tokens 8 (2 i + hh) + g over a warp's columns, and what the tokens had
+// before (of lane (g, t): token 8 t + g), to the weights of a tile whose records are at
+// slots `place` (-1: nowhere).
+__device__ __forceinline__ void write_sums(const Params& P, const float (&sum)[2][2], const int64_t (&place)[2], int h, int tok0, int len, float before) {
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    float all = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float s = sum[i >> 1][i & 1];
+        s += __shfl_xor_sync(0xFFFFFFFFu, s, 1);
+        s += __shfl_xor_sync(0xFFFFFFFFu, s, 2);
+        if (t == i) all = s;
+    }
+    const int64_t mine = t < 2 ? place[0] : place[1];
+    if (mine >= 0 && tok0 + 8 * t + g < len)
+        P.a.out[(((mine >> P.cache.page_shift) * P.cache.heads + h) << P.cache.page_shift) + (mine & (P.cache.page_size - 1)) + ((8 * t + g) & 15)] = before + all;
+}
+
+// Eight query rows ready for the products: B fragments by lane, and for each row
+// what the products start from, the factor to scores times log2 e, its LogSum
+// (-inf: a row that gives nothing) and its position.
+template <int D>
+struct Rows {
+    uint4 q[D / 64][2][32];
+    float start[D / 64][8];
+    float factor[8], less[8], share[8];
+    int pos[8];
+};
+
+template <int D>
+__device__ __forceinline__ void make_ready(const Params& P, const Request& r, int h, int row0, Rows<D>& to) {
+    constexpr int NG = D / 64;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const int row = min(row0 + g, r.rows - 1), qi = row / P.group, head = h * P.group + row - qi * P.group;
+    uint4 q[NG][2];
+    float start[NG];
+    const float up = ready_fragments<D>(P.a.q + (r.q0 + qi) * P.a.q_stride + head * D, q, start);
+#pragma unroll
+    for (int j = 0; j < NG; ++j) {
+        to.q[j][0][lane] = q[j][0];
+        to.q[j][1][lane] = q[j][1];
+        if (t == 0) to.start[j][g] = start[j];
     }
     if (t == 0) {
         const bool real = row0 + g < r.rows;
-        const float lse = real ? P.a.lse[static_cast<int64_t>(r.q0 + qi) * P.a.heads + head] : -INFINITY;
-        to.factor[g] = real ? P.scale_log2 * __int_as_float((127 + 20 - e) << 23) : 0.0f;
-        to.less[g] = lse == -INFINITY ? -INFINITY : -1.4426950408889634f * lse;
+        const LogSum l = log_sum_of(real ? P.a.lse[static_cast<int64_t>(r.q0 + qi) * P.a.heads + head] : -INFINITY, P.scale_rest);
+        to.factor[g] = real ? P.scale_log2 * up : 0.0f;
+        to.less[g] = l.less;
+        to.share[g] = l.factor;
         to.pos[g] = r.pos0 + qi;
     }
 }
@@ -200,70 +307,32 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const __grid_constan
     const WeighArgs& a = P.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int heads = P.cache.heads, window = a.window ? a.window : INT32_MAX;
-    // units before each thread's requests
-    const int each = (a.batch + kThreads - 1) / kThreads;
-    {
-        const int b0 = min(static_cast<int>(threadIdx.x) * each, a.batch), b1 = min(b0 + each, a.batch);
-        uint64_t mine = 0;
-        for (int b = b0; b < b1; ++b) {
-            Request r;
-            r.read(P, b);
-            mine += static_cast<uint64_t>(r.units) * heads;
-        }
-        uint64_t in = mine;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const uint64_t o = __shfl_up_sync(0xFFFFFFFFu, in, d);
-            if (lane >= d) in += o;
-        }
-        if (lane == 31) warp_sums[warp] = in;
-        __syncthreads();
-        uint64_t at = in - mine;
-        for (int w = 0; w < warp; ++w) at += warp_sums[w];
-        scan[threadIdx.x] = at;
-        if (threadIdx.x == kThreads - 1) scan[kThreads] = at + mine;
-        __syncthreads();
-    }
+    const int each = scan_units<kUnit>(P, scan, warp_sums);
     const uint64_t total = scan[kThreads];
     for (uint64_t u = blockIdx.x; u < total; u += gridDim.x) {
-        int lo = 0, hi = kThreads - 1;
-        while (lo < hi) {
-            const int mid = (lo + hi + 1) >> 1;
-            if (scan[mid] <= u) lo = mid;
-            else hi = mid - 1;
-        }
-        int b = lo * each;
-        uint64_t at = scan[lo];
         Request r;
-        for (;; ++b) {
-            r.read(P, b);
-            const uint64_t units = static_cast<uint64_t>(r.units) * heads;
-            if (u < at + units) break;
-            at += units;
-        }
-        const int h = static_cast<int>((u - at) / r.units), first = static_cast<int>((u - at) % r.units) * kUnit;
-        const int tok0 = first + warp * kTile;
+        int b, h, unit;
+        locate<kUnit>(P, scan, each, u, r, b, h, unit);
+        const int first = unit * kUnit, tok0 = first + warp * kTile;
         const uint8_t* record[2];
-        int64_t place[2];                      // of each record's weights
+        int64_t place[2];
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int tok = tok0 + i * kKvTokens;
             record[i] = nullptr;
             place[i] = -1;
             if (tok >= r.len) continue;
-            const int page = a.table[b * a.table_stride + (tok >> P.cache.page_shift)], in_page = tok & (P.cache.page_size - 1);
+            const int page = a.table[b * a.table_stride + (tok >> P.cache.page_shift)];
             if (page < 0 || page >= P.cache.pages) continue;
-            record[i] = P.cache.record((static_cast<int64_t>(page) << P.cache.page_shift) + in_page, h);
-            place[i] = ((static_cast<int64_t>(page) * heads + h) << P.cache.page_shift) + in_page;
+            place[i] = (static_cast<int64_t>(page) << P.cache.page_shift) + (tok & (P.cache.page_size - 1));
+            record[i] = P.cache.record(place[i], h);
         }
         Keys<D> keys;
         load_keys<D>(record, keys);
-        // lane (g, t) writes token 8 t + g of the tile
-        const int tok = tok0 + 8 * t + g;
-        const int64_t mine = t < 2 ? place[0] : place[1];
-        const bool writes = mine >= 0 && tok < r.len;
-        const int64_t to = mine + ((8 * t + g) & 15);
-        const float before = writes && a.weights && tok < r.pos0 ? a.decay * a.weights[to] : 0.0f;
+        const int64_t mine = t < 2 ? place[0] : place[1];      // of lane (g, t)'s token, 8 t + g
+        float before = 0.0f;
+        if (a.weights && mine >= 0 && tok0 + 8 * t + g < r.pos0)
+            before = a.decay * a.weights[(((mine >> P.cache.page_shift) * heads + h) << P.cache.page_shift) + (mine & (P.cache.page_size - 1)) + ((8 * t + g) & 15)];
         float sum[2][2] = {};
         // the queries that see any of the unit's tokens
         const int last = min(first + kUnit, r.len) - 1;
@@ -287,7 +356,8 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const __grid_constan
                 for (int n = 0; n < NT; ++n) {
                     if (n0 + n >= groups) break;
                     const Rows<D>& rows = ready[n0 + n];
-                    const float2 f = *reinterpret_cast<const float2*>(rows.factor + 2 * t), l = *reinterpret_cast<const float2*>(rows.less + 2 * t);
+                    const float2 f = *reinterpret_cast<const float2*>(rows.factor + 2 * t), l = *reinterpret_cast<const float2*>(rows.less + 2 * t),
+                                 e = *reinterpret_cast<const float2*>(rows.share + 2 * t);
                     const int2 pos = *reinterpret_cast<const int2*>(rows.pos + 2 * t);
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
@@ -299,26 +369,200 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const __grid_constan
                                 p0 = k <= pos.x && (k > pos.x - window || k < a.sinks) ? p0 : 0.0f;
                                 p1 = k <= pos.y && (k > pos.y - window || k < a.sinks) ? p1 : 0.0f;
                             }
-                            sum[i][hh] += p0 + p1;
+                            sum[i][hh] = fmaf(p1, e.y, fmaf(p0, e.x, sum[i][hh]));
                         }
                 }
             }
         }
-        float all = 0.0f;
+        write_sums(P, sum, place, h, tok0, r.len, before);
+    }
+}
+
+// ---------------------------------------------------- few rows to a head --
+//
+// Up to 8 NT query rows, ready in a warp's registers.  Every warp takes a contiguous
+// range of the call's tiles (request, head, 32 tokens) and works alone: the next
+// tile's codes, scales and weights are on their way while it multiplies, and the
+// pages of the one behind that are being looked up.
+
+template <int D>
+struct Tile {
+    uint32_t w[2][2][D / 32];                  // as Keys
+    uint32_t d[2][2][(D / 64 + 1) / 2];        // scales, two to a word
+    float before;
+};
+
+template <int D>
+__device__ __forceinline__ void load_tile(const Params& P, const int64_t (&place)[2], int h, bool seen, bool kept, Tile<D>& k) {
+    constexpr int NG = D / 64, GP = kv_plane_groups(D), PL = kv_planes(D);
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            float s = sum[i >> 1][i & 1];
-            s += __shfl_xor_sync(0xFFFFFFFFu, s, 1);
-            s += __shfl_xor_sync(0xFFFFFFFFu, s, 2);
-            if (t == i) all = s;
+    for (int r = 0; r < 2; ++r)
+#pragma unroll
+        for (int hh = 0; hh < 2; ++hh) {
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) k.w[r][hh][i] = 0;
+#pragma unroll
+            for (int i = 0; i < (NG + 1) / 2; ++i) k.d[r][hh][i] = 0;
+            if (place[r] < 0 || !seen) continue;
+            const uint8_t* record = P.cache.record(place[r], h);
+#pragma unroll
+            for (int pl = 0; pl < PL; ++pl) {
+                const uint8_t* p = record + ((hh * PL + pl) * 32 + lane) * 8 * GP;
+                if constexpr (GP == 2) {
+                    const uint4 v = __ldcs(reinterpret_cast<const uint4*>(p));
+                    k.w[r][hh][4 * pl] = v.x; k.w[r][hh][4 * pl + 1] = v.y; k.w[r][hh][4 * pl + 2] = v.z; k.w[r][hh][4 * pl + 3] = v.w;
+                } else {
+                    const uint2 v = __ldcs(reinterpret_cast<const uint2*>(p));
+                    k.w[r][hh][0] = v.x; k.w[r][hh][1] = v.y;
+                }
+            }
+            const uint8_t* d = record + kv_k_scales(D) + (g + 8 * hh) * NG * 2;
+            if constexpr (NG == 1) k.d[r][hh][0] = *reinterpret_cast<const uint16_t*>(d);
+            if constexpr (NG == 2) k.d[r][hh][0] = *reinterpret_cast<const uint32_t*>(d);
+            if constexpr (NG == 4) {
+                const uint2 v = *reinterpret_cast<const uint2*>(d);
+                k.d[r][hh][0] = v.x; k.d[r][hh][1] = v.y;
+            }
         }
-        if (writes) a.out[to] = before + all;
+    // lane (g, t) has token 8 t + g
+    const int64_t mine = t < 2 ? place[0] : place[1];
+    k.before = 0.0f;
+    if (kept && mine >= 0)
+        k.before = P.a.weights[(((mine >> P.cache.page_shift) * P.cache.heads + h) << P.cache.page_shift) + (mine & (P.cache.page_size - 1)) + ((8 * t + g) & 15)];
+}
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kThreads, D == 256 || NT == 2 ? 2 : D == 128 ? 2 : 3) weigh_few_kernel(const __grid_constant__ Params P) {
+    constexpr int NG = D / 64;
+    __shared__ uint64_t scan[kThreads + 1];
+    __shared__ uint64_t warp_sums[kWarps];
+    const WeighArgs& a = P.a;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
+    const int heads = P.cache.heads, window = a.window ? a.window : INT32_MAX;
+    const int each = scan_units<kTile>(P, scan, warp_sums);
+    const uint64_t total = scan[kThreads], warps = static_cast<uint64_t>(gridDim.x) * kWarps, w = static_cast<uint64_t>(blockIdx.x) * kWarps + warp;
+    uint64_t u = total / warps * w + min(w, total % warps);
+    const uint64_t u1 = u + total / warps + (w < total % warps);
+    if (u >= u1) return;
+    Request r;
+    int b, h, first;
+    locate<kTile>(P, scan, each, u, r, b, h, first);
+    while (u < u1) {
+        const int tiles = units_of<kTile>(r), last = static_cast<int>(min(static_cast<uint64_t>(tiles - first), u1 - u)) + first;
+        const int32_t* row = a.table + static_cast<int64_t>(b) * a.table_stride;
+        // slots of a tile's two records, -1 where there is none
+        auto look = [&](int tile, int64_t (&place)[2]) {
+            const int tok0 = tile * kTile;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int tok = tok0 + i * kKvTokens;
+                place[i] = -1;
+                if (tile >= last || tok >= r.len) continue;
+                const int page = row[tok >> P.cache.page_shift];
+                if (page >= 0 && page < P.cache.pages) place[i] = (static_cast<int64_t>(page) << P.cache.page_shift) + (tok & (P.cache.page_size - 1));
+            }
+        };
+        const int pos_hi = r.pos0 + r.n - 1;
+        auto seen = [&](int tile) { return !a.window || tile * kTile < a.sinks || tile * kTile + kTile - 1 > r.pos0 - window; };
+        auto kept = [&](int tile) { return a.weights && tile * kTile + 8 * t + g < r.pos0; };
+        int64_t here[2], next[2];
+        look(first, here);
+        look(first + 1, next);
+        Tile<D> k;
+        load_tile<D>(P, here, h, seen(first), kept(first), k);
+        // the rows: B fragments, and for the lane's columns what the products start from and so on
+        uint4 q[NT][NG][2];
+        float start[NT][NG][2], factor[NT][2], less[NT][2], share[NT][2];
+        int pos[NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float sum[NG];
+            const int mine = min(8 * n + g, r.rows - 1), qi = mine / P.group, head = h * P.group + mine - qi * P.group;
+            const float up = ready_fragments<D>(a.q + (r.q0 + qi) * a.q_stride + head * D, q[n], sum);
+            const bool real = 8 * n + g < r.rows;
+            const LogSum l = log_sum_of(real ? a.lse[static_cast<int64_t>(r.q0 + qi) * a.heads + head] : -INFINITY, P.scale_rest);
+            const float f = real ? P.scale_log2 * up : 0.0f;
+#pragma unroll
+            for (int c = 0; c < 2; ++c) {
+                const int from = (2 * t + c) << 2;             // the columns' rows are those of lanes (2t + c, .)
+#pragma unroll
+                for (int j = 0; j < NG; ++j) start[n][j][c] = __shfl_sync(0xFFFFFFFFu, sum[j], from);
+                factor[n][c] = __shfl_sync(0xFFFFFFFFu, f, from);
+                less[n][c] = __shfl_sync(0xFFFFFFFFu, l.less, from);
+                share[n][c] = __shfl_sync(0xFFFFFFFFu, l.factor, from);
+                pos[n][c] = r.pos0 + __shfl_sync(0xFFFFFFFFu, qi, from);
+            }
+        }
+        for (int tile = first; tile < last; ++tile) {
+            const int64_t place[2] = {here[0], here[1]};
+            const Tile<D> cur = k;
+            here[0] = next[0]; here[1] = next[1];
+            if (tile + 1 < last) load_tile<D>(P, here, h, seen(tile + 1), kept(tile + 1), k);
+            look(tile + 2, next);
+            const int tok0 = tile * kTile;
+            float sum[2][2] = {};
+            if (seen(tile) && tok0 <= pos_hi) {
+                const bool plain = place[0] >= 0 && place[1] >= 0 && tok0 + kTile - 1 <= r.pos0 && (tok0 > pos_hi - window || tok0 + kTile <= a.sinks);
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float x[NT][4];
+#pragma unroll
+                    for (int j = 0; j < NG; ++j) {
+                        float acc[NT][4];
+#pragma unroll
+                        for (int v = 0; v < 2; ++v) {
+                            const uint32_t a0w = cur.w[i][0][2 * j + v], c0w = cur.w[i][1][2 * j + v], as = a0w >> 8, cs = c0w >> 8;
+                            const uint32_t a0 = raw_pair<0>(a0w, as), a1 = raw_pair<0>(c0w, cs), a2 = raw_pair<1>(a0w, as), a3 = raw_pair<1>(c0w, cs);
+                            const uint32_t b0 = raw_pair<2>(a0w, as), b1 = raw_pair<2>(c0w, cs), b2 = raw_pair<3>(a0w, as), b3 = raw_pair<3>(c0w, cs);
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) {
+                                if (v == 0) mma_from(acc[n], a0, a1, a2, a3, q[n][j][v].x, q[n][j][v].y, start[n][j][0], start[n][j][1], start[n][j][0], start[n][j][1]);
+                                else mma_16816(acc[n], a0, a1, a2, a3, q[n][j][v].x, q[n][j][v].y);
+                                mma_16816(acc[n], b0, b1, b2, b3, q[n][j][v].z, q[n][j][v].w);
+                            }
+                        }
+                        const float d0 = half_bits_to_float(j & 1 ? cur.d[i][0][j / 2] >> 16 : cur.d[i][0][j / 2] & 0xFFFFu);
+                        const float d1 = half_bits_to_float(j & 1 ? cur.d[i][1][j / 2] >> 16 : cur.d[i][1][j / 2] & 0xFFFFu);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n)
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const float d = e < 2 ? d0 : d1;
+                                x[n][e] = j ? fmaf(d, acc[n][e], x[n][e]) : d * acc[n][e];
+                            }
+                    }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            float p = ex2(fmaf(x[n][e], factor[n][e & 1], less[n][e & 1]));
+                            if (!plain) {
+                                const int tok = tok0 + i * kKvTokens + (e >> 1) * 8 + g;
+                                p = tok <= pos[n][e & 1] && (tok > pos[n][e & 1] - window || tok < a.sinks) ? p : 0.0f;
+                            }
+                            sum[i][e >> 1] = fmaf(p, share[n][e & 1], sum[i][e >> 1]);
+                        }
+                }
+            }
+            write_sums(P, sum, place, h, tok0, r.len, a.decay * cur.before);
+        }
+        u += static_cast<uint64_t>(last - first);
+        first = 0;
+        if (u >= u1) break;
+        if (++h == heads) {                    // the next request with tiles: there is one
+            h = 0;
+            do r.read(P, ++b); while (units_of<kTile>(r) == 0);
+        }
     }
 }
 
 template <int D>
 cudaError_t launch(const Params& P, int num_sms, cudaStream_t s) {
-    weigh_kernel<D><<<num_sms * 2, kThreads, 0, s>>>(P);
+    const int64_t rows = static_cast<int64_t>(P.a.max_queries) * P.group;
+    if (rows <= 8) weigh_few_kernel<D, 1><<<num_sms * (D == 64 ? 3 : 2), kThreads, 0, s>>>(P);
+    else if (D < 256 && rows <= 16) weigh_few_kernel<D, D == 256 ? 1 : 2><<<num_sms * 2, kThreads, 0, s>>>(P);
+    else weigh_kernel<D><<<num_sms * 2, kThreads, 0, s>>>(P);
     return cudaGetLastError();
 }
 
@@ -327,7 +571,9 @@ cudaError_t launch(const Params& P, int num_sms, cudaStream_t s) {
 cudaError_t launch_weigh(const WeighArgs& a, const KvGeometry& g, int num_sms, cudaStream_t s) {
     int shift = 0;
     while ((1 << shift) < g.page_size) ++shift;
-    const Params P{a, KvCache{g.data, g.pages, g.page_size, shift, g.heads, g.D}, a.heads / g.heads, a.scale * 1.4426950408889634f};
+    const double exact = static_cast<double>(a.scale) * 1.4426950408889634;
+    const float scale_log2 = static_cast<float>(exact), rest = exact != 0.0 ? static_cast<float>((exact - scale_log2) / exact) : 0.0f;
+    const Params P{a, KvCache{g.data, g.pages, g.page_size, shift, g.heads, g.D}, a.heads / g.heads, scale_log2, rest};
     if (g.D == 64) return launch<64>(P, num_sms, s);
     return g.D == 128 ? launch<128>(P, num_sms, s) : launch<256>(P, num_sms, s);
 }
