@@ -1,24 +1,26 @@
 // pn_logprobs.cu -- log probabilities of given tokens, entropy and the top
 // alternatives of rows of logits.
 //
-// With x = scale * logit, m the row's largest logit, d = logit - m and e =
-// exp(scale d):  S = sum e,  T = sum e d,
+// With m the row's largest logit, d = logit - m and e = exp(scale d):
+//   R = sum of e over all tokens but one of the largest, S = 1 + R, T = sum e d
 //   ln p(token) = scale d - ln S,   entropy = ln S - scale T / S
-// (both terms of the entropy are positive or zero, so nothing cancels).
+// R goes without the largest token's 1, so ln S = log1p(R) keeps its bits where one
+// token has nearly all of the probability; both terms of the entropy are positive or
+// zero, so nothing cancels.
 //
 // One pass over memory.  A cluster of 1 to 8 thread blocks has a row, each block a
-// contiguous part of it; a thread keeps a running m, S and T for 32 values at a
-// time, and the place of its largest.
+// contiguous part of it.  A warp takes 512 (fp16:
+// 1024) values at a time under one reference m, the next ones on their way;
+// only where one of them passes it (a few times in a row) are the sums moved and
+// the new largest value left out of R.
 //
-// Top k (at most 32): by the 64-bit number (order of the logit, ~index), so there
-// are no ties and the lowest index wins.  The k largest of a block's 256 thread
-// maxima bound the k-th largest of its part from below, the largest of the
-// cluster's bounds that of the row.  A value of the top k is at or above the bound,
-// and so is its thread's maximum: only the (at most k) threads of a block whose
-// maximum passes it have their values looked at again, from L2, by a warp each,
-// which collects in a sorted list, a lane to an entry, what passes; that is little
-// more than k values in all, and never more than 32 to a warp.  The first block
-// ranks them.
+// Top k (at most 32).  The k-th largest of a block's 256 thread maxima is a lower
+// bound of the k-th largest value of its part, the largest of the cluster's bounds one
+// of the row's.  Only threads whose maximum reaches the bound (k, and those that tie
+// with it) can hold one of the top k: their values are looked at again, from L2, by
+// their warp, which keeps the k first by the 64-bit number (order of the logit, ~index)
+// in a sorted list, a lane to an entry.  There are no ties in that order and the lowest
+// index wins.  The row's first block ranks what the lists hold.
 #include <cooperative_groups.h>
 #include <cstdint>
 
@@ -38,6 +40,7 @@ constexpr int kWarps = kThreads / 32;
 constexpr int kMostCluster = 8;
 constexpr int kMostEntries = kMostCluster * kWarps * 32;
 constexpr float kHuge = 1.7e38f;               // differences of numbers up to it are finite
+constexpr float kLeast = -1e30f;               // exponents' least (exp2 of it is 0, and 0 times it is)
 
 using Key = unsigned long long;
 
@@ -54,32 +57,65 @@ __device__ __forceinline__ float logit_of(Key k) {
     return __uint_as_float(u & 0x80000000u ? u & 0x7FFFFFFFu : ~u);
 }
 
-// NaN and -inf as -kHuge (they count where nothing else is there, and what they
-// gave is dropped when something is), +inf as kHuge.
-__device__ __forceinline__ float bounded(float x) { return fminf(fmaxf(x, -kHuge), kHuge); }
-
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
 
-// Sums relative to a largest value.
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+// Two fp32 numbers in a register pair, and operations on both at once.
+using Two = unsigned long long;
+__device__ __forceinline__ Two two(float a, float b) {
+    Two d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ float2 apart(Two v) {
+    float2 d;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(v));
+    return d;
+}
+__device__ __forceinline__ Two mul2(Two a, Two b) {
+    Two d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ Two add2(Two a, Two b) {
+    Two d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+    Two d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+// Sums relative to a largest logit m, whose own 1 is not in r (m = -kHuge: no token
+// yet); t is sum e y with y = scale log2 e (logit - m).
 struct Sums {
-    float m, s, t;
-    // to the larger reference `to`
-    __device__ __forceinline__ void move(float to, float scale_log2) {
-        const float by = m - to, f = exp2_fast(by * scale_log2);
-        t = f == 0.0f ? 0.0f : f * fmaf(s, by, t);
-        s *= f;
-        m = to;
+    float m, r, t;
+    __device__ __forceinline__ bool any() const { return m > -kHuge; }
+    // what `o`, with a smaller or the same m, adds
+    __device__ __forceinline__ void take(const Sums& o, float c) {
+        const float by = (o.m - m) * c, f = exp2_fast(by), s = o.r + (o.any() ? 1.0f : 0.0f);
+        r = fmaf(f, s, r);
+        t += f == 0.0f ? 0.0f : f * fmaf(s, by, o.t);
     }
-    __device__ __forceinline__ void join(Sums o, float scale_log2) {
-        const float to = fmaxf(m, o.m);
-        move(to, scale_log2);
-        o.move(to, scale_log2);
-        s += o.s;
-        t += o.t;
+    __device__ __forceinline__ void join(const Sums& o, float c) {
+        if (o.m > m) {
+            const Sums mine = *this;
+            *this = o;
+            take(mine, c);
+        } else {
+            take(o, c);
+        }
     }
 };
 
@@ -89,24 +125,112 @@ struct RowOf {
     static constexpr int kVec = 16 / sizeof(T);
     const T* p;                // aligned to 16 bytes, `skew` elements before the row
     int skew, vocab;
-    __device__ __forceinline__ void load(int v, float (&x)[kVec]) const {
+    // Vector v as it lies there; -inf in place of what is outside the row, which is not read.
+    __device__ __forceinline__ uint4 load(int v) const {
         const int at = v * kVec - skew;
-        if (at >= 0 && at + kVec <= vocab) {
-            if constexpr (kVec == 4) {
-                const float4 w = __ldcg(reinterpret_cast<const float4*>(p) + v);
-                x[0] = w.x; x[1] = w.y; x[2] = w.z; x[3] = w.w;
-            } else {
-                const uint4 w = __ldcg(reinterpret_cast<const uint4*>(p) + v);
-                const uint32_t u[4] = {w.x, w.y, w.z, w.w};
+        if (at >= 0 && at + kVec <= vocab) return __ldcg(reinterpret_cast<const uint4*>(p) + v);
+        return edge(p, at, v, vocab);
+    }
+    static __device__ __noinline__ uint4 edge(const T* p, int at, int v, int vocab) {
+        uint32_t w[4];
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    x[2 * i] = half_bits_to_float(u[i] & 0xFFFFu);
-                    x[2 * i + 1] = half_bits_to_float(u[i] >> 16);
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (kVec == 4) {
+                w[i] = at + i >= 0 && at + i < vocab ? reinterpret_cast<const uint32_t*>(p)[v * 4 + i] : 0xFF800000u;
+            } else {
+                const uint16_t* h = reinterpret_cast<const uint16_t*>(p) + v * 8 + 2 * i;
+                const uint32_t lo = at + 2 * i >= 0 && at + 2 * i < vocab ? h[0] : 0xFC00u, hi = at + 2 * i + 1 >= 0 && at + 2 * i + 1 < vocab ? h[1] : 0xFC00u;
+                w[i] = lo | hi << 16;
+            }
+        }
+        return make_uint4(w[0], w[1], w[2], w[3]);
+    }
+    static __device__ __forceinline__ uint4 nothing() {
+        constexpr uint32_t w = kVec == 4 ? 0xFF800000u : 0xFC00FC00u;
+        return make_uint4(w, w, w, w);
+    }
+    static __device__ __forceinline__ void values(const uint4& raw, float (&x)[kVec]) {
+        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if constexpr (kVec == 4) {
+                x[i] = __uint_as_float(w[i]);
+            } else {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w[i]));
+                x[2 * i] = f.x;
+                x[2 * i + 1] = f.y;
+            }
+        }
+    }
+    // -inf in place of the first value that is `high`.
+    template <int N>
+    static __device__ __forceinline__ void drop(uint4 (&raw)[N], float high) {
+        bool done = false;
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (kVec == 4) {
+                    const bool hit = !done && __uint_as_float(w[i]) == high;
+                    w[i] = hit ? 0xFF800000u : w[i];
+                    done |= hit;
+                } else {
+                    const bool lo = !done && half_bits_to_float(w[i] & 0xFFFFu) == high;
+                    w[i] = lo ? (w[i] & 0xFFFF0000u) | 0xFC00u : w[i];
+                    done |= lo;
+                    const bool hi = !done && half_bits_to_float(w[i] >> 16) == high;
+                    w[i] = hi ? (w[i] & 0xFFFFu) | 0xFC000000u : w[i];
+                    done |= hi;
                 }
             }
-        } else {                               // the row's ends: nothing outside it is read
+            raw[j] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+    }
+    // -inf in place of all values of kHuge and above (fp16: of infinity); how many there were.
+    template <int N>
+    static __device__ __forceinline__ float drop_huge(uint4 (&raw)[N]) {
+        float n = 0.0f;
 #pragma unroll
-            for (int i = 0; i < kVec; ++i) x[i] = at + i >= 0 && at + i < vocab ? static_cast<float>(p[v * kVec + i]) : -INFINITY;
+        for (int j = 0; j < N; ++j) {
+            uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (kVec == 4) {
+                    const bool hit = __uint_as_float(w[i]) >= kHuge;
+                    w[i] = hit ? 0xFF800000u : w[i];
+                    n += hit;
+                } else {
+                    const bool lo = (w[i] & 0xFFFFu) == 0x7C00u, hi = w[i] >> 16 == 0x7C00u;
+                    w[i] = lo ? (w[i] & 0xFFFF0000u) | 0xFC00u : w[i];
+                    w[i] = hi ? (w[i] & 0xFFFFu) | 0xFC000000u : w[i];
+                    n += lo + hi;
+                }
+            }
+            raw[j] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        return n;
+    }
+    // The largest of N vectors (-inf where all are NaN).
+    template <int N>
+    static __device__ __forceinline__ float largest(const uint4 (&raw)[N]) {
+        if constexpr (kVec == 4) {
+            float most = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                most = max3(most, __uint_as_float(raw[j].x), __uint_as_float(raw[j].y));
+                most = max3(most, __uint_as_float(raw[j].z), __uint_as_float(raw[j].w));
+            }
+            return most;
+        } else {
+            __half2 most = __half2half2(__ushort_as_half(0xFC00));
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const uint32_t w[4] = {raw[j].x, raw[j].y, raw[j].z, raw[j].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) most = __hmax2(most, *reinterpret_cast<const __half2*>(&w[i]));
+            }
+            return fmaxf(__low2float(most), __high2float(most));
         }
     }
 };
@@ -119,15 +243,21 @@ __device__ __forceinline__ Key insert(Key mine, Key add) {
     return lane < at ? mine : lane == at ? add : above;
 }
 
+// The order of floats that are no NaN as that of signed whole numbers, and back.
+__device__ __forceinline__ int order_of(float x) {
+    const int i = __float_as_int(x);
+    return i < 0 ? i ^ 0x7FFFFFFF : i;
+}
+__device__ __forceinline__ float float_of(int i) { return __int_as_float(i < 0 ? i ^ 0x7FFFFFFF : i); }
+
 template <typename T, bool kTop>
 __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArgs a) {
     using Row = RowOf<T>;
-    constexpr int kVec = Row::kVec, kUnroll = 32 / kVec;
+    constexpr int kVec = Row::kVec, kUnroll = 4;       // vectors of a thread at a time
     cg::cluster_group cluster = cg::this_cluster();
     __shared__ Sums warp_sums[kWarps], block_sums;
-    __shared__ Key lists[kTop ? kWarps * 32 : 1];      // the warps' thread maxima in order
-    __shared__ Key winners[32];                        // the largest thread maxima
-    __shared__ Key bound;                              // the k-th of them
+    __shared__ int lists[kTop ? kWarps * 32 : 1];      // the warps' thread maxima in order
+    __shared__ float bound;                            // the k-th of them
     __shared__ uint32_t entries;                       // (first block of a cluster)
     __shared__ Key entry[kTop ? kMostEntries : 1];
     const int parts = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
@@ -141,71 +271,80 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
     const int vectors = (row.skew + a.vocab + kVec - 1) / kVec;
     const int v0 = static_cast<int>(static_cast<int64_t>(vectors) * rank / parts), v1 = static_cast<int>(static_cast<int64_t>(vectors) * (rank + 1) / parts);
     const float c = a.scale * 1.4426950408889634f;
+    const Two c2 = two(c, c);
 
-    if (kTop && threadIdx.x < 32) {
-        winners[threadIdx.x] = 0;
-        if (threadIdx.x == 0) {
-            bound = 0;
-            entries = 0;
-        }
+    if (kTop && threadIdx.x == 0) {
+        bound = -INFINITY;
+        entries = 0;
     }
-    Sums mine{-kHuge, 0.0f, 0.0f};
-    float best = -INFINITY;
-    uint32_t best_at = 0;
-    for (int v = v0 + static_cast<int>(threadIdx.x); v < v1; v += kThreads * kUnroll) {
-        float x[kUnroll][kVec];
+    float m = -kHuge, best = -INFINITY;        // the warp's reference, the thread's maximum
+    Two r2 = two(0.0f, 0.0f), t2 = r2;
+    uint4 raw[kUnroll];
+    auto fetch = [&](int v) {
+#pragma unroll
+        for (int j = 0; j < kUnroll; ++j) raw[j] = v + lane + j * kThreads < v1 ? row.load(v + lane + j * kThreads) : Row::nothing();
+    };
+    fetch(v0 + warp * 32);
+    for (int v = v0 + warp * 32; v < v1; v += kThreads * kUnroll) {    // the same for the whole warp
+        uint4 now[kUnroll];
+#pragma unroll
+        for (int j = 0; j < kUnroll; ++j) now[j] = raw[j];
+        fetch(v + kThreads * kUnroll);         // the next ones are on their way meanwhile
+        const float most = Row::largest(now);
+        if (kTop) best = fmaxf(best, most);
+        const float high = float_of(__reduce_max_sync(0xFFFFFFFFu, order_of(most)));
+        if (high > m || high >= kHuge) {
+            const float to = fminf(fmaxf(high, m), kHuge), by = (m - to) * c, f = exp2_fast(by);
+            const float2 r1 = apart(r2), t1 = apart(t2);
+            const float sum = r1.x + r1.y + (lane == 0 && m > -kHuge ? 1.0f : 0.0f);
+            if (to > m) {
+                r2 = two(f * sum, 0.0f);
+                t2 = two(f == 0.0f ? 0.0f : f * fmaf(sum, by, t1.x + t1.y), 0.0f);
+                m = to;
+                // the first value of that size, of the first lane that has one, is left out
+                if (lane == __ffs(__ballot_sync(0xFFFFFFFFu, most == high)) - 1) Row::drop(now, high);
+            }
+            if (high >= kHuge) r2 = add2(r2, two(Row::drop_huge(now), 0.0f));      // each adds 1
+        }
+        const Two less = two(-m, -m);
 #pragma unroll
         for (int j = 0; j < kUnroll; ++j) {
-            if (v + j * kThreads < v1) row.load(v + j * kThreads, x[j]);
-            else
+            float x[kVec];
+            Row::values(now[j], x);
 #pragma unroll
-                for (int i = 0; i < kVec; ++i) x[j][i] = -INFINITY;
-        }
-        float most = x[0][0];
-#pragma unroll
-        for (int j = 0; j < kUnroll; ++j)
-#pragma unroll
-            for (int i = 0; i < kVec; ++i) most = fmaxf(most, x[j][i]);
-        if (kTop && most > best) {             // (NaN: fmaxf passes over it)
-            best = most;
-#pragma unroll
-            for (int j = kUnroll - 1; j >= 0; --j)
-#pragma unroll
-                for (int i = kVec - 1; i >= 0; --i)
-                    if (x[j][i] == most) best_at = static_cast<uint32_t>((v + j * kThreads) * kVec - row.skew + i);
-        }
-        most = bounded(most);
-        if (most > mine.m) mine.move(most, c);
-        const float less = -mine.m;
-        float s[2] = {0.0f, 0.0f}, t[2] = {0.0f, 0.0f};
-#pragma unroll
-        for (int j = 0; j < kUnroll; ++j)
-#pragma unroll
-            for (int i = 0; i < kVec; ++i) {
-                const float d = bounded(x[j][i]) + less, e = exp2_fast(d * c);
-                s[i & 1] += e;
-                t[i & 1] = fmaf(e, d, t[i & 1]);
+            for (int i = 0; i < kVec; i += 2) {
+                const float2 d = apart(mul2(add2(two(x[i], x[i + 1]), less), c2));
+                const float y0 = fmaxf(d.x, kLeast), y1 = fmaxf(d.y, kLeast);          // (NaN too)
+                const Two e = two(exp2_fast(y0), exp2_fast(y1));
+                r2 = add2(r2, e);
+                t2 = fma2(e, two(y0, y1), t2);
             }
-        mine.s += s[0] + s[1];
-        mine.t += t[0] + t[1];
+        }
     }
-    Sums all = mine;
+    float2 pair = apart(r2);
+    Sums all{m, pair.x + pair.y, 0.0f};
+    pair = apart(t2);
+    all.t = pair.x + pair.y;
 #pragma unroll
-    for (int d = 16; d >= 1; d >>= 1)
-        all.join(Sums{__shfl_xor_sync(0xFFFFFFFFu, all.m, d), __shfl_xor_sync(0xFFFFFFFFu, all.s, d), __shfl_xor_sync(0xFFFFFFFFu, all.t, d)}, c);
+    for (int d = 16; d >= 1; d >>= 1) {
+        all.r += __shfl_xor_sync(0xFFFFFFFFu, all.r, d);
+        all.t += __shfl_xor_sync(0xFFFFFFFFu, all.t, d);
+    }
     if (lane == 0) warp_sums[warp] = all;
-    Key key = 0;
+    int key = order_of(best);
     if constexpr (kTop) {
         // the warp's thread maxima in order, the largest in lane 0
-        key = key_of(best, best_at);
+        if (a.top == 1) {
+            key = __reduce_max_sync(0xFFFFFFFFu, key);
+        } else {
 #pragma unroll
-        for (int size = 2; size <= 32; size *= 2)
+            for (int size = 2; size <= 32; size *= 2)
 #pragma unroll
-            for (int d = size / 2; d >= 1; d /= 2) {
-                const Key o = __shfl_xor_sync(0xFFFFFFFFu, key, d);
-                const bool larger = ((lane & size) == 0 || size == 32) == ((lane & d) == 0);
-                key = larger == (key > o) ? key : o;
-            }
+                for (int d = size / 2; d >= 1; d /= 2) {
+                    const int o = __shfl_xor_sync(0xFFFFFFFFu, key, d);
+                    key = ((lane & size) == 0) == ((lane & d) == 0) ? max(key, o) : min(key, o);
+                }
+        }
         lists[warp * 32 + lane] = key;
     }
     __syncthreads();
@@ -215,33 +354,35 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
         block_sums = all;
     }
     if constexpr (kTop) {
-        // its place among the block's: how many of each other warp's list are larger
-        if (key != 0) {
+        // its place among the block's: how many of each other warp's list go before it (of equal ones, the lower warp's)
+        if (a.top == 1) {
+            if (threadIdx.x == 32) {
+                for (int w = 0; w < kWarps; ++w) key = max(key, lists[w * 32]);
+                bound = float_of(key);
+            }
+        } else if (lane < a.top) {
             int place = lane;
 #pragma unroll
             for (int o = 1; o < kWarps; ++o) {
-                const Key* list = lists + (warp + o) % kWarps * 32;
+                const int other = (warp + o) % kWarps, than = other < warp ? key - (key > INT32_MIN) : key;
+                const int* list = lists + other * 32;
                 int n = 0;
 #pragma unroll
-                for (int step = 16; step >= 1; step /= 2) n += list[n + step - 1] > key ? step : 0;
-                place += n + (n == 31 && list[31] > key);
+                for (int step = 16; step >= 1; step /= 2) n += list[n + step - 1] > than ? step : 0;
+                place += n + (n == 31 && list[31] > than);
             }
-            if (place < a.top) winners[place] = key;
-            if (place == a.top - 1) bound = key;
+            if (place == a.top - 1) bound = float_of(key);
         }
     }
     cluster.sync();
     // the row's sums, in the blocks' order, and its bound
-    Key least = 1;
+    float least = -kHuge;
     all = *cluster.map_shared_rank(&block_sums, 0);
     for (int o = 1; o < parts; ++o) all.join(*cluster.map_shared_rank(&block_sums, o), c);
-    const bool none = all.m == -kHuge;         // no token at all
-    const float log_sum = logf(all.s);
+    const bool none = !all.any();              // no token at all
+    const float log_sum = log1pf(all.r);
     if constexpr (kTop) {
-        for (int o = 0; o < parts; ++o) {
-            const Key b = *cluster.map_shared_rank(&bound, o);
-            least = b > least ? b : least;
-        }
+        for (int o = 0; o < parts; ++o) least = fmaxf(least, *cluster.map_shared_rank(&bound, o));
     }
     auto log_p = [&](float logit) {
         return none || !(logit > -kHuge) ? -INFINITY : fmaf(fminf(logit, kHuge) - all.m, a.scale, -log_sum);
@@ -251,27 +392,31 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
             const int token = a.tokens[r * a.count + i];
             a.logprobs[r * a.count + i] = token >= 0 && token < a.vocab ? log_p(static_cast<float>(begin[token])) : -INFINITY;
         }
-        if (threadIdx.x == 0 && a.entropy) a.entropy[r] = none ? 0.0f : fmaxf(fmaf(-a.scale, all.t / all.s, log_sum), 0.0f);
+        if (threadIdx.x == 0 && a.entropy) a.entropy[r] = none ? 0.0f : fmaxf(fmaf(-0.693147181f, all.t / (1.0f + all.r), log_sum), 0.0f);
     }
     if constexpr (kTop) {
-        // a winner to a warp: its thread's values that reach the bound
-        Key list = 0;
-        for (int w = warp; w < a.top; w += kWarps) {
-            const Key winner = winners[w];
-            if (winner < least) break;                 // so are those behind it
-            const int thread = ((static_cast<int>(index_of(winner)) + row.skew) / kVec - v0) % kThreads;
+        // the warp's threads that may hold some of the top k, one after the other
+        Key list = 0, floor = 0;               // floor: the list's k-th
+        for (uint32_t who = __ballot_sync(0xFFFFFFFFu, best >= least && best > -kHuge); who; who &= who - 1) {
+            const int thread = warp * 32 + __ffs(who) - 1;
             for (int first = v0 + thread; first < v1; first += 32 * kThreads) {
                 const int v = first + lane * kThreads;
+                const uint4 again[1] = {v < v1 ? row.load(v) : Row::nothing()};
+                if (!__any_sync(0xFFFFFFFFu, Row::largest(again) >= least)) continue;
                 float x[kVec];
-                if (v < v1) row.load(v, x);
+                Row::values(again[0], x);
 #pragma unroll
                 for (int i = 0; i < kVec; ++i) {
-                    const Key k = v < v1 ? key_of(x[i], static_cast<uint32_t>(v * kVec - row.skew + i)) : 0;
-                    for (uint32_t in = __ballot_sync(0xFFFFFFFFu, k >= least); in; in &= in - 1)
+                    const Key k = x[i] >= least ? key_of(x[i], static_cast<uint32_t>(v * kVec - row.skew + i)) : 0;
+                    for (uint32_t in = __ballot_sync(0xFFFFFFFFu, k > floor); in; in &= in - 1) {
                         list = insert(list, __shfl_sync(0xFFFFFFFFu, k, __ffs(in) - 1));
+                        floor = __shfl_sync(0xFFFFFFFFu, list, a.top - 1);
+                        in &= __ballot_sync(0xFFFFFFFFu, k > floor) | (in & -in);
+                    }
                 }
             }
         }
+        if (lane >= a.top) list = 0;
         uint32_t* counter = cluster.map_shared_rank(&entries, 0);
         Key* to = cluster.map_shared_rank(entry, 0);
         const int have = __popc(__ballot_sync(0xFFFFFFFFu, list != 0));
