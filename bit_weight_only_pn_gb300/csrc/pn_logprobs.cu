@@ -15,12 +15,13 @@
 // the new largest value left out of R.
 //
 // Top k (at most 32).  The k-th largest of a block's 256 thread maxima is a lower
-// bound of the k-th largest value of its part, the largest of the cluster's bounds one
-// of the row's.  Only threads whose maximum reaches the bound (k, and those that tie
+// bound of the k-th largest value of the row, and so is what all p blocks have (k / p)
+// of, rounded up; the best of them is taken.  Only threads whose maximum reaches the bound (k, and those that tie
 // with it) can hold one of the top k: their values are looked at again, from L2, by
-// their warp, which keeps the k first by the 64-bit number (order of the logit, ~index)
-// in a sorted list, a lane to an entry.  There are no ties in that order and the lowest
-// index wins.  The row's first block ranks what the lists hold.
+// their warp, and what reaches the bound goes to the row's first block, which ranks it
+// by the 64-bit number (order of the logit, ~index): there are no ties in that order
+// and the lowest index wins.  Where a block finds more than fits (a row of equal
+// values, say), each warp keeps the k first of it in a sorted list, a lane to an entry.
 #include <cooperative_groups.h>
 #include <cstdint>
 
@@ -38,7 +39,8 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMostCluster = 8;
-constexpr int kMostEntries = kMostCluster * kWarps * 32;
+constexpr int kMostFound = kWarps * 32;        // values of a block that may be in the top k
+constexpr int kMostEntries = kMostCluster * kMostFound;
 constexpr float kHuge = 1.7e38f;               // differences of numbers up to it are finite
 constexpr float kLeast = -1e30f;               // exponents' least (exp2 of it is 0, and 0 times it is)
 
@@ -118,6 +120,12 @@ struct Sums {
         }
     }
 };
+
+// Lane i's for i < n (a power of two up to 32; others' do not count), joined in a fixed order, in all lanes.
+__device__ __forceinline__ Sums join_lanes(Sums s, int n, float c) {
+    for (int d = 1; d < n; d *= 2) s.join(Sums{__shfl_xor_sync(0xFFFFFFFFu, s.m, d), __shfl_xor_sync(0xFFFFFFFFu, s.r, d), __shfl_xor_sync(0xFFFFFFFFu, s.t, d)}, c);
+    return Sums{__shfl_sync(0xFFFFFFFFu, s.m, 0), __shfl_sync(0xFFFFFFFFu, s.r, 0), __shfl_sync(0xFFFFFFFFu, s.t, 0)};
+}
 
 // 16 bytes of a row: value i of vector v is the row's element v * kVec - skew + i.
 template <typename T>
@@ -257,9 +265,10 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
     cg::cluster_group cluster = cg::this_cluster();
     __shared__ Sums warp_sums[kWarps], block_sums;
     __shared__ int lists[kTop ? kWarps * 32 : 1];      // the warps' thread maxima in order
-    __shared__ float bound;                            // the k-th of them
-    __shared__ uint32_t entries;                       // (first block of a cluster)
-    __shared__ Key entry[kTop ? kMostEntries : 1];
+    __shared__ float bound, share;                     // the k-th and the (k / parts)-th of them
+    __shared__ uint32_t found_count, entries, entry_base;
+    __shared__ Key found[kTop ? kMostFound : 1];       // the block's
+    __shared__ Key entry[kTop ? kMostEntries : 1];     // the row's (first block of a cluster)
     const int parts = static_cast<int>(cluster.num_blocks()), rank = static_cast<int>(cluster.block_rank());
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int64_t r = blockIdx.x / parts;
@@ -274,8 +283,8 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
     const Two c2 = two(c, c);
 
     if (kTop && threadIdx.x == 0) {
-        bound = -INFINITY;
-        entries = 0;
+        bound = share = -INFINITY;
+        found_count = entries = 0;
     }
     float m = -kHuge, best = -INFINITY;        // the warp's reference, the thread's maximum
     Two r2 = two(0.0f, 0.0f), t2 = r2;
@@ -348,17 +357,16 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
         lists[warp * 32 + lane] = key;
     }
     __syncthreads();
-    if (threadIdx.x == 0) {
-        all = warp_sums[0];
-        for (int w = 1; w < kWarps; ++w) all.join(warp_sums[w], c);
-        block_sums = all;
+    if (warp == 0) {
+        all = join_lanes(warp_sums[lane % kWarps], kWarps, c);
+        if (lane == 0) block_sums = all;
     }
     if constexpr (kTop) {
         // its place among the block's: how many of each other warp's list go before it (of equal ones, the lower warp's)
         if (a.top == 1) {
             if (threadIdx.x == 32) {
                 for (int w = 0; w < kWarps; ++w) key = max(key, lists[w * 32]);
-                bound = float_of(key);
+                bound = share = float_of(key);
             }
         } else if (lane < a.top) {
             int place = lane;
@@ -372,17 +380,19 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
                 place += n + (n == 31 && list[31] > than);
             }
             if (place == a.top - 1) bound = float_of(key);
+            if (place == (a.top - 1) / parts) share = float_of(key);
         }
     }
     cluster.sync();
     // the row's sums, in the blocks' order, and its bound
     float least = -kHuge;
-    all = *cluster.map_shared_rank(&block_sums, 0);
-    for (int o = 1; o < parts; ++o) all.join(*cluster.map_shared_rank(&block_sums, o), c);
+    all = join_lanes(*cluster.map_shared_rank(&block_sums, lane % parts), parts, c);
     const bool none = !all.any();              // no token at all
     const float log_sum = log1pf(all.r);
     if constexpr (kTop) {
-        for (int o = 0; o < parts; ++o) least = fmaxf(least, *cluster.map_shared_rank(&bound, o));
+        const int most = __reduce_max_sync(0xFFFFFFFFu, order_of(*cluster.map_shared_rank(&bound, lane % parts)));
+        const int all_have = __reduce_min_sync(0xFFFFFFFFu, order_of(*cluster.map_shared_rank(&share, lane % parts)));
+        least = fmaxf(least, float_of(max(most, all_have)));
     }
     auto log_p = [&](float logit) {
         return none || !(logit > -kHuge) ? -INFINITY : fmaf(fminf(logit, kHuge) - all.m, a.scale, -log_sum);
@@ -395,16 +405,52 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
         if (threadIdx.x == 0 && a.entropy) a.entropy[r] = none ? 0.0f : fmaxf(fmaf(-0.693147181f, all.t / (1.0f + all.r), log_sum), 0.0f);
     }
     if constexpr (kTop) {
-        // the warp's threads that may hold some of the top k, one after the other
-        Key list = 0, floor = 0;               // floor: the list's k-th
-        for (uint32_t who = __ballot_sync(0xFFFFFFFFu, best >= least && best > -kHuge); who; who &= who - 1) {
-            const int thread = warp * 32 + __ffs(who) - 1;
-            for (int first = v0 + thread; first < v1; first += 32 * kThreads) {
-                const int v = first + lane * kThreads;
-                const uint4 again[1] = {v < v1 ? row.load(v) : Row::nothing()};
-                if (!__any_sync(0xFFFFFFFFu, Row::largest(again) >= least)) continue;
+        // the warp's threads that may hold some of the top k: f(16 bytes of each lane, whose vector) of their values
+        auto look_again = [&](auto f) {
+            constexpr int kAtOnce = 4;         // threads whose loads are on their way together
+            for (uint32_t who = __ballot_sync(0xFFFFFFFFu, best >= least && best > -kHuge); who;) {
+                int first[kAtOnce];            // of their vectors
+#pragma unroll
+                for (int n = 0; n < kAtOnce; ++n) {
+                    first[n] = who ? v0 + warp * 32 + __ffs(who) - 1 + lane * kThreads : v1;
+                    who &= who - 1;
+                }
+                for (int go = 0; go < v1 - v0; go += 32 * kThreads) {
+                    uint4 raw[kAtOnce][1];
+#pragma unroll
+                    for (int n = 0; n < kAtOnce; ++n) raw[n][0] = first[n] + go < v1 ? row.load(first[n] + go) : Row::nothing();
+#pragma unroll
+                    for (int n = 0; n < kAtOnce; ++n) f(raw[n], first[n] + go);
+                }
+            }
+        };
+        look_again([&](const uint4 (&raw)[1], int v) {
+            if (!(Row::largest(raw) >= least)) return;
+            float x[kVec];
+            Row::values(raw[0], x);
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) {
+                const Key k = x[i] >= least ? key_of(x[i], static_cast<uint32_t>(v * kVec - row.skew + i)) : 0;
+                if (k == 0) continue;
+                const uint32_t at = atomicAdd(&found_count, 1u);
+                if (at < kMostFound) found[at] = k;
+            }
+        });
+        __syncthreads();
+        uint32_t* counter = cluster.map_shared_rank(&entries, 0);
+        Key* to = cluster.map_shared_rank(entry, 0);
+        const uint32_t count = found_count;
+        if (count <= kMostFound) {
+            if (threadIdx.x == 0) entry_base = count ? atomicAdd(counter, count) : 0;
+            __syncthreads();
+            if (threadIdx.x < count) to[entry_base + threadIdx.x] = found[threadIdx.x];
+        } else {
+            // many equal values or many large ones in one place: each warp keeps the k first in a sorted list
+            Key list = 0, floor = 0;           // floor: the list's k-th
+            look_again([&](const uint4 (&raw)[1], int v) {
+                if (!__any_sync(0xFFFFFFFFu, Row::largest(raw) >= least)) return;
                 float x[kVec];
-                Row::values(again[0], x);
+                Row::values(raw[0], x);
 #pragma unroll
                 for (int i = 0; i < kVec; ++i) {
                     const Key k = x[i] >= least ? key_of(x[i], static_cast<uint32_t>(v * kVec - row.skew + i)) : 0;
@@ -414,16 +460,14 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
                         in &= __ballot_sync(0xFFFFFFFFu, k > floor) | (in & -in);
                     }
                 }
-            }
+            });
+            if (lane >= a.top) list = 0;
+            const int have = __popc(__ballot_sync(0xFFFFFFFFu, list != 0));
+            uint32_t at = 0;
+            if (lane == 0 && have) at = atomicAdd(counter, static_cast<uint32_t>(have));
+            at = __shfl_sync(0xFFFFFFFFu, at, 0);
+            if (lane < have) to[at + lane] = list;
         }
-        if (lane >= a.top) list = 0;
-        uint32_t* counter = cluster.map_shared_rank(&entries, 0);
-        Key* to = cluster.map_shared_rank(entry, 0);
-        const int have = __popc(__ballot_sync(0xFFFFFFFFu, list != 0));
-        uint32_t at = 0;
-        if (lane == 0 && have) at = atomicAdd(counter, static_cast<uint32_t>(have));
-        at = __shfl_sync(0xFFFFFFFFu, at, 0);
-        if (lane < have) to[at + lane] = list;
         cluster.sync();
         if (rank != 0) return;
         const int n = static_cast<int>(entries);
