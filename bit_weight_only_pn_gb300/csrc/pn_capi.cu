@@ -786,7 +786,7 @@ pn_status pn_norm(const void* y, int64_t y_stride, int y_dtype, const void* resi
     if (pn_status st = device_info(&sms, &major); st != PN_OK) return st;
     const pn::NormArgs a{y, y_stride, y_dtype == PN_DTYPE_F16, residual, residual_stride, residual_dtype == PN_DTYPE_F16, gate, gate_stride,
                          scale, tokens, hidden, post, post_weight, post_bias, pre, pre_weight, pre_bias, eps, residual_out, out_stride,
-                         residual_dtype == PN_DTYPE_F16, reinterpret_cast<__half*>(x)};
+                         reinterpret_cast<__half*>(x)};
     const cudaError_t e = pn::launch_norm(a, sms, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PN_OK : pn::cuda_error(e);
 }

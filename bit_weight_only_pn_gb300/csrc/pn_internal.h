@@ -283,7 +283,7 @@ struct NormArgs {
     bool y_f16;
     const void* residual;      // may be null
     int64_t residual_stride;
-    bool residual_f16;
+    bool residual_f16;         // and residual_out
     const float* gate;         // may be null
     int64_t gate_stride;       // 0: one row for all tokens
     float scale;
@@ -298,7 +298,6 @@ struct NormArgs {
     float eps;
     void* residual_out;        // may be null
     int64_t out_stride;
-    bool out_f16;
     __half* x;                 // may be null
 };
 cudaError_t launch_norm(const NormArgs& a, int num_sms, cudaStream_t s);

@@ -23,42 +23,74 @@ namespace {
 
 constexpr int kWarpRowHidden = 1024;           // rows up to this size are a warp's
 constexpr int kWarpRowThreads = 128;
+constexpr unsigned kFewBlocks = 256;
 
-// V values of a row from element `at` on.  Every element belongs to one thread of
-// one block, which reads it before it writes it: r' may take the place of r.
-template <int V>
-__device__ __forceinline__ void load(const void* p, int64_t at, bool f16, float* v) {
-    if (f16) {
-        const __half* h = static_cast<const __half*>(p) + at;
-        if constexpr (V == 4) {
-            const uint2 w = __ldcs(reinterpret_cast<const uint2*>(h));
-            v[0] = half_bits_to_float(w.x & 0xFFFFu);
-            v[1] = half_bits_to_float(w.x >> 16);
-            v[2] = half_bits_to_float(w.y & 0xFFFFu);
-            v[3] = half_bits_to_float(w.y >> 16);
-        } else {
-            v[0] = __half2float(*h);
+// A thread has N groups of V values of a row: those of group k begin at place +
+// k * step, and lie wholly inside the row or outside, where they count as 0.  Loads of
+// a thread's groups stand together, without a branch between them (groups outside
+// the row read its last one): loaded and used one group after the other, each waited
+// for the one before, and 13 rows of 5003 took 12 us.
+template <int V, int N>
+struct Groups {
+    int place, step, hidden;
+    __device__ __forceinline__ int at(int k) const { return place + k * step; }
+    __device__ __forceinline__ bool inside(int k) const { return at(k) < hidden; }
+    // from row element 0 at p; every element is its thread's alone, which reads it before it
+    // writes it (r' may take the place of r)
+    template <bool kF16>
+    __device__ __forceinline__ void load(const void* p, float (&v)[N][V]) const {
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const int from = min(at(k), hidden - V);
+            if constexpr (kF16) {
+                const __half* h = static_cast<const __half*>(p) + from;
+                if constexpr (V == 4) {
+                    const uint2 w = __ldcs(reinterpret_cast<const uint2*>(h));
+                    const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&w.x)), b = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
+                    v[k][0] = a.x; v[k][1] = a.y; v[k][2] = b.x; v[k][3] = b.y;
+                } else {
+                    v[k][0] = __half2float(*h);
+                }
+            } else {
+                const float* f = static_cast<const float*>(p) + from;
+                if constexpr (V == 4) {
+                    const float4 w = __ldcs(reinterpret_cast<const float4*>(f));
+                    v[k][0] = w.x; v[k][1] = w.y; v[k][2] = w.z; v[k][3] = w.w;
+                } else {
+                    v[k][0] = *f;
+                }
+            }
         }
-    } else {
-        const float* f = static_cast<const float*>(p) + at;
-        if constexpr (V == 4) {
-            const float4 w = __ldcs(reinterpret_cast<const float4*>(f));
-            v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
-        } else {
-            v[0] = *f;
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[k][i] = inside(k) ? v[k][i] : 0.0f;
+    }
+    // v = f(v, a vector's values)
+    template <typename F>
+    __device__ __forceinline__ void with(const float* p, float (&v)[N][V], F f) const {
+        float w[N][V];
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            const float* from = p + min(at(k), hidden - V);
+            if constexpr (V == 4) {
+                const float4 u = *reinterpret_cast<const float4*>(from);
+                w[k][0] = u.x; w[k][1] = u.y; w[k][2] = u.z; w[k][3] = u.w;
+            } else {
+                w[k][0] = *from;
+            }
         }
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+#pragma unroll
+            for (int i = 0; i < V; ++i) v[k][i] = f(v[k][i], w[k][i]);
     }
-}
-
-template <int V>
-__device__ __forceinline__ void load_vector(const float* p, int at, float* v) {
-    if constexpr (V == 4) {
-        const float4 w = *reinterpret_cast<const float4*>(p + at);
-        v[0] = w.x; v[1] = w.y; v[2] = w.z; v[3] = w.w;
-    } else {
-        v[0] = p[at];
+    // what is read later comes nearer
+    __device__ __forceinline__ void prefetch(const void* p, int size) const {
+#pragma unroll
+        for (int k = 0; k < N; ++k) prefetch_l1(static_cast<const uint8_t*>(p) + static_cast<int64_t>(min(at(k), hidden - V)) * size);
     }
-}
+};
 
 template <int V>
 __device__ __forceinline__ void store_half(__half* p, int64_t at, const float* v) {
@@ -78,127 +110,146 @@ __device__ __forceinline__ void store(void* p, int64_t at, bool f16, const float
     else *f = v[0];
 }
 
-// Sum over the threads of a row (a warp or the block), the same bits in all of
-// them.  Every call of a row takes a place of its own in `part`.
-template <bool kWarpRow>
-__device__ __forceinline__ float row_sum(float v, float* part) {
+__device__ __forceinline__ float warp_sum(float v) {
 #pragma unroll
     for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
-    if constexpr (!kWarpRow) {
-        const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
-        if (lane == 0) part[threadIdx.x >> 5] = v;
-        __syncthreads();
-        v = lane < warps ? part[lane] : 0.0f;
-#pragma unroll
-        for (int d = 16; d >= 1; d >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, d);
-    }
     return v;
 }
 
-// A thread has N groups of V values: those of group k begin at (k * threads +
-// its place in the row) * V, and lie wholly inside the row or outside.
+// Number, mean and sum of squared differences from it, of values.
+struct Moments {
+    float n, mean, m2;
+};
+// The same over the lanes, in all of them: sums of n and of n mean give the common
+// mean, and what a lane's mean is off it adds n times its square.
+__device__ __forceinline__ Moments over_lanes(const Moments& m) {
+    const float n = warp_sum(m.n), mean = warp_sum(m.n * m.mean) / fmaxf(n, 1.0f), off = m.mean - mean;
+    return {n, mean, warp_sum(fmaf(m.n * off, off, m.m2))};
+}
+
+// A row's norm, with one barrier (none where the row is a warp's); `part` is its own
+// place in shared memory.
 template <int V, int N, bool kWarpRow>
-__device__ __forceinline__ void norm_row(float (&v)[N][V], int kind, const float* weight, const float* bias, float eps, int hidden,
-                                         int place, int step, float* part) {
-    const float each = 1.0f / static_cast<float>(hidden);
+__device__ __forceinline__ void norm_row(float (&v)[N][V], const Groups<V, N>& g, int kind, const float* weight, const float* bias, float eps, float* part) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    float mean = 0.0f, squares;
     if (kind == PN_NORM_LAYER) {
-        float sum = 0.0f;
+        // about the thread's own mean first: a large mean costs no bits
+        float n = 0.0f, sum = 0.0f;
+#pragma unroll
+        for (int k = 0; k < N; ++k) {
+            n += g.inside(k) ? static_cast<float>(V) : 0.0f;
+#pragma unroll
+            for (int i = 0; i < V; ++i) sum += v[k][i];
+        }
+        Moments m{n, sum / fmaxf(n, 1.0f), 0.0f};
+#pragma unroll
+        for (int k = 0; k < N; ++k)
+            if (g.inside(k))
+#pragma unroll
+                for (int i = 0; i < V; ++i) m.m2 = fmaf(v[k][i] - m.mean, v[k][i] - m.mean, m.m2);
+        m = over_lanes(m);
+        if constexpr (!kWarpRow) {
+            if (lane == 0) {
+                part[warp] = m.n;
+                part[32 + warp] = m.mean;
+                part[64 + warp] = m.m2;
+            }
+            __syncthreads();
+            m = over_lanes(lane < warps ? Moments{part[lane], part[32 + lane], part[64 + lane]} : Moments{0.0f, 0.0f, 0.0f});
+        }
+        mean = m.mean;
+        squares = m.m2;
+    } else {
+        squares = 0.0f;
 #pragma unroll
         for (int k = 0; k < N; ++k)
 #pragma unroll
-            for (int i = 0; i < V; ++i) sum += v[k][i];            // (values behind the row's end are 0)
-        const float mean = row_sum<kWarpRow>(sum, part) * each;
-#pragma unroll
-        for (int k = 0; k < N; ++k)
-            if (place + k * step < hidden)
-#pragma unroll
-                for (int i = 0; i < V; ++i) v[k][i] -= mean;
+            for (int i = 0; i < V; ++i) squares = fmaf(v[k][i], v[k][i], squares);
+        squares = warp_sum(squares);
+        if constexpr (!kWarpRow) {
+            if (lane == 0) part[warp] = squares;
+            __syncthreads();
+            squares = warp_sum(lane < warps ? part[lane] : 0.0f);
+        }
     }
-    float sum = 0.0f;
+    const float inv = 1.0f / sqrtf(squares * (1.0f / static_cast<float>(g.hidden)) + eps);
 #pragma unroll
     for (int k = 0; k < N; ++k)
 #pragma unroll
-        for (int i = 0; i < V; ++i) sum = fmaf(v[k][i], v[k][i], sum);
-    const float inv = 1.0f / sqrtf(row_sum<kWarpRow>(sum, part + 32) * each + eps);
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-        const int at = place + k * step;
-        if (at >= hidden) continue;
-        float w[V], b[V];
-        if (weight) load_vector<V>(weight, at, w);
-        if (bias) load_vector<V>(bias, at, b);
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            v[k][i] *= inv;
-            if (weight) v[k][i] *= w[i];
-            if (bias) v[k][i] += b[i];
-        }
-    }
+        for (int i = 0; i < V; ++i) v[k][i] = (v[k][i] - mean) * inv;
+    if (weight) g.with(weight, v, [](float x, float w) { return x * w; });
+    if (bias) g.with(bias, v, [](float x, float w) { return x + w; });
 }
 
-template <int V, int N, bool kWarpRow>
-__global__ void __launch_bounds__(kWarpRow ? kWarpRowThreads : 1024) norm_kernel(const NormArgs a) {
-    __shared__ float parts[kWarpRow ? 1 : 4 * 32];     // a place to each of a row's sums
-    const int threads = kWarpRow ? 32 : blockDim.x, place = (kWarpRow ? threadIdx.x & 31 : threadIdx.x) * V, step = threads * V;
+// A block's threads at most, and blocks to an SM at least, as the registers for N V values allow.
+template <int V, int N>
+constexpr int kMostThreads = N * V <= 8 ? 1024 : N * V == 16 ? (V == 4 ? 384 : 512) : 512;
+template <int V, int N>
+constexpr int kLeastBlocks = N * V <= 8 ? 1 : N * V == 16 ? (V == 4 ? 3 : 2) : N * V == 32 && V == 4 ? 2 : 1;
+
+template <int V, int N, bool kWarpRow, bool kYF16, bool kRF16>
+__global__ void __launch_bounds__(kWarpRow ? kWarpRowThreads : kMostThreads<V, N>, kWarpRow ? 1 : kLeastBlocks<V, N>) norm_kernel(const NormArgs a) {
+    __shared__ float parts[kWarpRow ? 1 : 2 * 96];     // a place to each of a row's norms
     const int64_t t = kWarpRow ? static_cast<int64_t>(blockIdx.x) * (kWarpRowThreads / 32) + (threadIdx.x >> 5) : blockIdx.x;
     if (t >= a.tokens) return;                         // (a whole warp, of rows that are warps')
+    const int threads = kWarpRow ? 32 : blockDim.x;
+    const Groups<V, N> g{static_cast<int>(kWarpRow ? threadIdx.x & 31 : threadIdx.x) * V, threads * V, a.hidden};
+    const uint8_t* y = static_cast<const uint8_t*>(a.y) + t * a.y_stride * (kYF16 ? 2 : 4);
+    const uint8_t* residual = static_cast<const uint8_t*>(a.residual) + t * a.residual_stride * (kRF16 ? 2 : 4);
+    const float* gate = a.gate + t * a.gate_stride;
     // r is on its way beside y, but where two rows do not fit a thread's registers
     constexpr bool kLate = N * V > 16;
-    float v[N][V], r[N][V];
-    auto load_residual = [&](int k) {
-        const int at = place + k * step;
-#pragma unroll
-        for (int i = 0; i < V; ++i) r[k][i] = 0.0f;
-        if (a.residual && at < a.hidden) load<V>(a.residual, t * a.residual_stride + at, a.residual_f16, r[k]);
-    };
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-        const int at = place + k * step;
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[k][i] = 0.0f;
-        if (a.y && at < a.hidden) load<V>(a.y, t * a.y_stride + at, a.y_f16, v[k]);
-        if (!kLate) load_residual(k);
+    float v[N][V] = {}, r[N][V] = {};
+    if (a.y) g.template load<kYF16>(y, v);
+    if (a.residual) {
+        if (kLate) g.prefetch(residual, kRF16 ? 2 : 4);
+        else g.template load<kRF16>(residual, r);
     }
-    if (a.post != PN_NORM_NONE) norm_row<V, N, kWarpRow>(v, a.post, a.post_weight, a.post_bias, a.eps, a.hidden, place, step, parts);
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-        const int at = place + k * step;
-        if (kLate) load_residual(k);
-        if (!a.y || at >= a.hidden) continue;
-        float g[V];
-        if (a.gate) load_vector<V>(a.gate + t * a.gate_stride, at, g);
-#pragma unroll
-        for (int i = 0; i < V; ++i) r[k][i] = fmaf(a.scale, a.gate ? v[k][i] * g[i] : v[k][i], r[k][i]);
+    if (a.gate && (a.gate_stride != 0 || gridDim.x <= kFewBlocks)) g.prefetch(gate, 4);
+    if (gridDim.x <= kFewBlocks) {             // (later rows find the vectors in L1)
+        if (a.post_weight) g.prefetch(a.post_weight, 4);
+        if (a.pre_weight) g.prefetch(a.pre_weight, 4);
     }
+    if (a.post != PN_NORM_NONE) norm_row<V, N, kWarpRow>(v, g, a.post, a.post_weight, a.post_bias, a.eps, parts);
+    if (kLate && a.residual) g.template load<kRF16>(residual, r);
+    if (a.gate) g.with(gate, v, [](float x, float w) { return x * w; });
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+#pragma unroll
+        for (int i = 0; i < V; ++i) r[k][i] = g.inside(k) && a.y ? fmaf(a.scale, v[k][i], r[k][i]) : r[k][i];
     if (a.residual_out)
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-            const int at = place + k * step;
-            if (at < a.hidden) store<V>(a.residual_out, t * a.out_stride + at, a.out_f16, r[k]);
-        }
+        for (int k = 0; k < N; ++k)
+            if (g.inside(k)) store<V>(a.residual_out, t * a.out_stride + g.at(k), kRF16, r[k]);
     if (!a.x) return;
-    if (a.pre != PN_NORM_NONE) norm_row<V, N, kWarpRow>(r, a.pre, a.pre_weight, a.pre_bias, a.eps, a.hidden, place, step, kWarpRow ? parts : parts + 64);
+    if (a.pre != PN_NORM_NONE) norm_row<V, N, kWarpRow>(r, g, a.pre, a.pre_weight, a.pre_bias, a.eps, kWarpRow ? parts : parts + 96);
 #pragma unroll
-    for (int k = 0; k < N; ++k) {
-        const int at = place + k * step;
-        if (at < a.hidden) store_half<V>(a.x, t * a.hidden + at, r[k]);
-    }
+    for (int k = 0; k < N; ++k)
+        if (g.inside(k)) store_half<V>(a.x, t * a.hidden + g.at(k), r[k]);
 }
 
-template <int V, int N, bool kWarpRow>
+static_assert(PN_MAX_HIDDEN <= 4 * 16 * kMostThreads<4, 16> && PN_MAX_HIDDEN <= 64 * kMostThreads<1, 64>, "the longest row fits");
+
+template <int V, int N, bool kWarpRow, bool kYF16, bool kRF16>
 cudaError_t launch(const NormArgs& a, cudaStream_t s) {
     const int groups = (a.hidden + V - 1) / V, threads = kWarpRow ? kWarpRowThreads : ((groups + N - 1) / N + 31) / 32 * 32;
     const int64_t blocks = kWarpRow ? (a.tokens + kWarpRowThreads / 32 - 1) / (kWarpRowThreads / 32) : a.tokens;
-    norm_kernel<V, N, kWarpRow><<<static_cast<unsigned>(blocks), threads, 0, s>>>(a);
+    norm_kernel<V, N, kWarpRow, kYF16, kRF16><<<static_cast<unsigned>(blocks), threads, 0, s>>>(a);
     return cudaGetLastError();
 }
+template <int V, int N, bool kWarpRow>
+cudaError_t launch(const NormArgs& a, cudaStream_t s) {
+    if (a.y_f16) return a.residual_f16 ? launch<V, N, kWarpRow, true, true>(a, s) : launch<V, N, kWarpRow, true, false>(a, s);
+    return a.residual_f16 ? launch<V, N, kWarpRow, false, true>(a, s) : launch<V, N, kWarpRow, false, false>(a, s);
+}
 
-// The least N of its list with which the block has at most 1024 threads (of rows that
-// are warps': a warp), but no less than `least`.
+// The least N of its list with which the block (of rows that are warps': a warp) has
+// threads enough, but no less than `least`.
 template <int V, bool kWarpRow, int N, int... More>
 cudaError_t choose(const NormArgs& a, int least, cudaStream_t s) {
     if constexpr (sizeof...(More) > 0) {
-        if (N < least || (a.hidden + V - 1) / V > N * (kWarpRow ? 32 : 1024)) return choose<V, kWarpRow, More...>(a, least, s);
+        if (N < least || (a.hidden + V - 1) / V > N * (kWarpRow ? 32 : kMostThreads<V, N>)) return choose<V, kWarpRow, More...>(a, least, s);
     }
     return launch<V, N, kWarpRow>(a, s);
 }
@@ -209,11 +260,11 @@ cudaError_t launch_norm(const NormArgs& a, int num_sms, cudaStream_t s) {
     // fours where every row lies for them
     auto fits = [](const void* p, uintptr_t bytes, int64_t stride) { return !p || (reinterpret_cast<uintptr_t>(p) % bytes == 0 && stride % 4 == 0); };
     const bool fours = a.hidden % 4 == 0 && fits(a.y, a.y_f16 ? 8 : 16, a.y_stride) && fits(a.residual, a.residual_f16 ? 8 : 16, a.residual_stride) &&
-                       fits(a.residual_out, a.out_f16 ? 8 : 16, a.out_stride) && fits(a.gate, 16, a.gate_stride) && fits(a.post_weight, 16, 0) &&
+                       fits(a.residual_out, a.residual_f16 ? 8 : 16, a.out_stride) && fits(a.gate, 16, a.gate_stride) && fits(a.post_weight, 16, 0) &&
                        fits(a.post_bias, 16, 0) && fits(a.pre_weight, 16, 0) && fits(a.pre_bias, 16, 0) && fits(a.x, 8, 0);
-    if (a.hidden <= kWarpRowHidden) return fours ? choose<4, true, 2, 4, 8>(a, 0, s) : choose<1, true, 8, 16, 32>(a, 0, s);
+    if (a.hidden <= kWarpRowHidden) return fours ? choose<4, true, 4, 8>(a, 0, s) : choose<1, true, 8, 32>(a, 0, s);
     const bool many = a.tokens > num_sms;
-    return fours ? choose<4, false, 1, 2, 4, 8>(a, many ? 4 : 0, s) : choose<1, false, 4, 8, 16, 32>(a, many ? 16 : 0, s);
+    return fours ? choose<4, false, 1, 2, 4, 8, 16>(a, many ? 4 : 0, s) : choose<1, false, 8, 16, 32, 64>(a, many ? 16 : 0, s);
 }
 
 }  // namespace pn
