@@ -24,8 +24,8 @@ LIBRARY = os.path.join(HERE, "libpn_gb300.so")
 BINDING = os.path.join(HERE, "_step.so")
 SOURCES = ["pn_attn.cu", "pn_attn_tc.cu", "pn_capi.cu", "pn_codec.cu", "pn_evict.cu", "pn_gemv_ffma.cu", "pn_gemv_simt.cu", "pn_gemv_stream.cu", "pn_gemv_tc.cu",
            "pn_gptq.cu", "pn_kv.cu", "pn_logprobs.cu", "pn_noalloc.cu", "pn_norm.cu", "pn_prefill.cu", "pn_probe.cu", "pn_rotate.cu", "pn_verify.cu",
-           "pn_weigh.cu"]
-HEADERS = ["pn_attn.cuh", "pn_device.cuh", "pn_internal.h", "pn_kv.cuh", "pn_tcgen05.cuh"]
+           "pn_weigh.cu", "pn_weigh_tc.cu"]
+HEADERS = ["pn_attn.cuh", "pn_device.cuh", "pn_internal.h", "pn_kv.cuh", "pn_tcgen05.cuh", "pn_weigh.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-Xcompiler", "-O2",
               "-I", os.path.join(ROOT, "include")]

@@ -17,110 +17,19 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
-#include "pn_attn.cuh"
+#include "pn_weigh.cuh"
 
 namespace pn {
 namespace {
+
+using Params = WeighParams;
+using Request = WeighRequest;
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kTile = 32;                      // tokens of a warp
 constexpr int kUnit = kWarps * kTile;          // tokens of a block's unit of work
 constexpr int kChunk = 8 * kWarps;             // query rows made ready at a time, 8 by a warp
-
-struct Params {
-    WeighArgs a;
-    KvCache cache;
-    int group;                 // query heads per key/value head
-    float scale_log2;          // scale * log2 e
-    float scale_rest;          // what that left of it, relative to it
-};
-
-// A row's lse as the exponent's argument takes it.  exp2(x f - lse log2 e), with x f
-// and lse log2 e some tens, would carry the roundings of f and of lse log2 e in all
-// of the row's probabilities (2^-20 each).  So the argument gets a multiple of 2^-6,
-// which a sum with x f takes up without a rounding before its own, and what is left,
-// with f's rounding where x = lse, becomes a factor near 1 of the row's probabilities.
-struct LogSum {
-    float less, factor;
-};
-__device__ __forceinline__ LogSum log_sum_of(float lse, float scale_rest) {
-    if (lse == -INFINITY) return {-INFINITY, 0.0f};
-    constexpr float kLog2e = 1.44269502f, kLog2eRest = 1.92596299e-8f;       // log2 e in two parts
-    const float hi = lse * kLog2e, lo = fmaf(lse, kLog2e, -hi) + lse * kLog2eRest;
-    const float near = rintf(hi * 64.0f) * 0.015625f;
-    // 2^u for |u| a little above 2^-7, by its series
-    const float u = ((near - hi) - lo + hi * scale_rest) * 0.693147181f;
-    return {-near, fabsf(u) < 1.0f ? fmaf(u, fmaf(u, fmaf(u, fmaf(u, 0.0416666667f, 0.166666667f), 0.5f), 1.0f), 1.0f) : 1.0f};
-}
-
-struct Request {
-    int n, q0, pos0, len, rows;
-    __device__ __forceinline__ void read(const Params& P, int b) {
-        const WeighArgs& a = P.a;
-        const int T = static_cast<int>(a.tokens);
-        q0 = min(max(a.starts[b], 0), T);
-        n = min(min(max(a.starts[b + 1], q0), T) - q0, a.max_queries);
-        const int64_t room = static_cast<int64_t>(a.max_pages) << P.cache.page_shift;
-        len = static_cast<int>(min(static_cast<int64_t>(max(a.lens[b], 0)), room));
-        pos0 = len - n;
-        rows = n * P.group;
-    }
-};
-
-// Units of a head's kTokens tokens that a request has: none without queries.
-template <int kTokens>
-__device__ __forceinline__ int units_of(const Request& r) { return r.n > 0 ? (r.len + kTokens - 1) / kTokens : 0; }
-
-// scan[i]: units of all heads before thread i's requests, of which it has as many as
-// is returned; scan[kThreads] all of them.
-template <int kTokens>
-__device__ __forceinline__ int scan_units(const Params& P, uint64_t* scan, uint64_t* warp_sums) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, each = (P.a.batch + kThreads - 1) / kThreads;
-    const int b0 = min(static_cast<int>(threadIdx.x) * each, P.a.batch), b1 = min(b0 + each, P.a.batch);
-    uint64_t mine = 0;
-    for (int b = b0; b < b1; ++b) {
-        Request r;
-        r.read(P, b);
-        mine += static_cast<uint64_t>(units_of<kTokens>(r)) * P.cache.heads;
-    }
-    uint64_t in = mine;
-#pragma unroll
-    for (int d = 1; d < 32; d <<= 1) {
-        const uint64_t o = __shfl_up_sync(0xFFFFFFFFu, in, d);
-        if (lane >= d) in += o;
-    }
-    if (lane == 31) warp_sums[warp] = in;
-    __syncthreads();
-    uint64_t at = in - mine;
-    for (int w = 0; w < warp; ++w) at += warp_sums[w];
-    scan[threadIdx.x] = at;
-    if (threadIdx.x == kThreads - 1) scan[kThreads] = at + mine;
-    __syncthreads();
-    return each;
-}
-
-// Unit u (there is one): its request, head and place among the head's units.
-template <int kTokens>
-__device__ __forceinline__ void locate(const Params& P, const uint64_t* scan, int each, uint64_t u, Request& r, int& b, int& h, int& unit) {
-    int lo = 0, hi = kThreads - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (scan[mid] <= u) lo = mid;
-        else hi = mid - 1;
-    }
-    b = lo * each;
-    u -= scan[lo];
-    for (;; ++b) {
-        r.read(P, b);
-        const uint64_t units = static_cast<uint64_t>(units_of<kTokens>(r)) * P.cache.heads;
-        if (u < units) break;
-        u -= units;
-    }
-    const uint64_t of_head = static_cast<uint64_t>(units_of<kTokens>(r));
-    h = static_cast<int>(u / of_head);
-    unit = static_cast<int>(u - h * of_head);
-}
 
 // Row g of eight as the lane's part of the products' B fragments, scaled by a power of
 // two, the sums that the products start from, and the factor back to q . k.
@@ -307,12 +216,12 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const __grid_constan
     const WeighArgs& a = P.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int heads = P.cache.heads, window = a.window ? a.window : INT32_MAX;
-    const int each = scan_units<kUnit>(P, scan, warp_sums);
+    const int each = scan_units<kUnit, kThreads>(P, scan, warp_sums);
     const uint64_t total = scan[kThreads];
     for (uint64_t u = blockIdx.x; u < total; u += gridDim.x) {
         Request r;
         int b, h, unit;
-        locate<kUnit>(P, scan, each, u, r, b, h, unit);
+        locate<kUnit, kThreads>(P, scan, each, u, r, b, h, unit);
         const int first = unit * kUnit, tok0 = first + warp * kTile;
         const uint8_t* record[2];
         int64_t place[2];
@@ -440,14 +349,14 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NT == 2 ? 2 : D == 128 ?
     const WeighArgs& a = P.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
     const int heads = P.cache.heads, window = a.window ? a.window : INT32_MAX;
-    const int each = scan_units<kTile>(P, scan, warp_sums);
+    const int each = scan_units<kTile, kThreads>(P, scan, warp_sums);
     const uint64_t total = scan[kThreads], warps = static_cast<uint64_t>(gridDim.x) * kWarps, w = static_cast<uint64_t>(blockIdx.x) * kWarps + warp;
     uint64_t u = total / warps * w + min(w, total % warps);
     const uint64_t u1 = u + total / warps + (w < total % warps);
     if (u >= u1) return;
     Request r;
     int b, h, first;
-    locate<kTile>(P, scan, each, u, r, b, h, first);
+    locate<kTile, kThreads>(P, scan, each, u, r, b, h, first);
     while (u < u1) {
         const int tiles = units_of<kTile>(r), last = static_cast<int>(min(static_cast<uint64_t>(tiles - first), u1 - u)) + first;
         const int32_t* row = a.table + static_cast<int64_t>(b) * a.table_stride;
@@ -568,12 +477,13 @@ cudaError_t launch(const Params& P, int num_sms, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_weigh(const WeighArgs& a, const KvGeometry& g, int num_sms, cudaStream_t s) {
+cudaError_t launch_weigh(const WeighArgs& a, const KvGeometry& g, int num_sms, uint64_t timeout_ns, int stall, cudaStream_t s) {
     int shift = 0;
     while ((1 << shift) < g.page_size) ++shift;
     const double exact = static_cast<double>(a.scale) * 1.4426950408889634;
     const float scale_log2 = static_cast<float>(exact), rest = exact != 0.0 ? static_cast<float>((exact - scale_log2) / exact) : 0.0f;
-    const Params P{a, KvCache{g.data, g.pages, g.page_size, shift, g.heads, g.D}, a.heads / g.heads, scale_log2, rest};
+    const Params P{a, KvCache{g.data, g.pages, g.page_size, shift, g.heads, g.D}, a.heads / g.heads, scale_log2, rest, timeout_ns, stall};
+    if (weigh_tc_takes(a, g)) return launch_weigh_tc(P, num_sms, s);
     if (g.D == 64) return launch<64>(P, num_sms, s);
     return g.D == 128 ? launch<128>(P, num_sms, s) : launch<256>(P, num_sms, s);
 }

@@ -1,0 +1,110 @@
+// pn_weigh.cuh -- what the kernels of the weight that cached tokens gather share.
+#pragma once
+
+#include <cstdint>
+
+#include "pn_attn.cuh"
+
+namespace pn {
+
+struct WeighParams {
+    WeighArgs a;
+    KvCache cache;
+    int group;                 // query heads per key/value head
+    float scale_log2;          // scale * log2 e
+    float scale_rest;          // what that left of it, relative to it
+    uint64_t timeout_ns;
+    int stall;                 // testing aid: see pn_set_test_stall
+};
+
+// A row's lse as the exponent's argument takes it.  exp2(x f - lse log2 e), with x f
+// and lse log2 e some tens, would carry the roundings of f and of lse log2 e in all
+// of the row's probabilities (2^-20 each).  So the argument gets a multiple of 2^-6,
+// which a sum with x f takes up without a rounding before its own, and what is left,
+// with f's rounding where x = lse, becomes a factor near 1 of the row's probabilities.
+struct LogSum {
+    float less, factor;
+};
+__device__ __forceinline__ LogSum log_sum_of(float lse, float scale_rest) {
+    if (lse == -INFINITY) return {-INFINITY, 0.0f};
+    constexpr float kLog2e = 1.44269502f, kLog2eRest = 1.92596299e-8f;       // log2 e in two parts
+    const float hi = lse * kLog2e, lo = fmaf(lse, kLog2e, -hi) + lse * kLog2eRest;
+    const float near = rintf(hi * 64.0f) * 0.015625f;
+    // 2^u for |u| a little above 2^-7, by its series
+    const float u = ((near - hi) - lo + hi * scale_rest) * 0.693147181f;
+    return {-near, fabsf(u) < 1.0f ? fmaf(u, fmaf(u, fmaf(u, fmaf(u, 0.0416666667f, 0.166666667f), 0.5f), 1.0f), 1.0f) : 1.0f};
+}
+
+struct WeighRequest {
+    int n, q0, pos0, len, rows;
+    __device__ __forceinline__ void read(const WeighParams& P, int b) {
+        const WeighArgs& a = P.a;
+        const int T = static_cast<int>(a.tokens);
+        q0 = min(max(a.starts[b], 0), T);
+        n = min(min(max(a.starts[b + 1], q0), T) - q0, a.max_queries);
+        const int64_t room = static_cast<int64_t>(a.max_pages) << P.cache.page_shift;
+        len = static_cast<int>(min(static_cast<int64_t>(max(a.lens[b], 0)), room));
+        pos0 = len - n;
+        rows = n * P.group;
+    }
+};
+
+// Units of a head's kTokens tokens that a request has: none without queries.
+template <int kTokens>
+__device__ __forceinline__ int units_of(const WeighRequest& r) { return r.n > 0 ? (r.len + kTokens - 1) / kTokens : 0; }
+
+// scan[i]: units of all heads before thread i's requests, of which it has as many as
+// is returned; scan[kThreads] all of them.
+template <int kTokens, int kThreads>
+__device__ __forceinline__ int scan_units(const WeighParams& P, uint64_t* scan, uint64_t* warp_sums) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, each = (P.a.batch + kThreads - 1) / kThreads;
+    const int b0 = min(static_cast<int>(threadIdx.x) * each, P.a.batch), b1 = min(b0 + each, P.a.batch);
+    uint64_t mine = 0;
+    for (int b = b0; b < b1; ++b) {
+        WeighRequest r;
+        r.read(P, b);
+        mine += static_cast<uint64_t>(units_of<kTokens>(r)) * P.cache.heads;
+    }
+    uint64_t in = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const uint64_t o = __shfl_up_sync(0xFFFFFFFFu, in, d);
+        if (lane >= d) in += o;
+    }
+    if (lane == 31) warp_sums[warp] = in;
+    __syncthreads();
+    uint64_t at = in - mine;
+    for (int w = 0; w < warp; ++w) at += warp_sums[w];
+    scan[threadIdx.x] = at;
+    if (threadIdx.x == kThreads - 1) scan[kThreads] = at + mine;
+    __syncthreads();
+    return each;
+}
+
+// Unit u (there is one): its request, head and place among the head's units.
+template <int kTokens, int kThreads>
+__device__ __forceinline__ void locate(const WeighParams& P, const uint64_t* scan, int each, uint64_t u, WeighRequest& r, int& b, int& h, int& unit) {
+    int lo = 0, hi = kThreads - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (scan[mid] <= u) lo = mid;
+        else hi = mid - 1;
+    }
+    b = lo * each;
+    u -= scan[lo];
+    for (;; ++b) {
+        r.read(P, b);
+        const uint64_t units = static_cast<uint64_t>(units_of<kTokens>(r)) * P.cache.heads;
+        if (u < units) break;
+        u -= units;
+    }
+    const uint64_t of_head = static_cast<uint64_t>(units_of<kTokens>(r));
+    h = static_cast<int>(u / of_head);
+    unit = static_cast<int>(u - h * of_head);
+}
+
+// The kernel for many query rows to a key/value head (pn_weigh_tc.cu).
+bool weigh_tc_takes(const WeighArgs& a, const KvGeometry& g);
+cudaError_t launch_weigh_tc(const WeighParams& P, int num_sms, cudaStream_t s);
+
+}  // namespace pn

@@ -1,0 +1,535 @@
+// pn_weigh_tc.cu -- the attention weight that cached tokens gather, for many query
+// rows to a key/value head (prompts): the same function as pn_weigh.cu, on the
+// fifth-generation tensor cores.
+//
+// A unit of work is (request, key/value head, 128 cached tokens).  The tokens are the
+// M of the products and the query rows their N, so that a token's probabilities lie
+// in one lane of tensor memory and are summed by one thread: nothing is exchanged
+// between lanes.  S_j = K_j Q_j^T for each group j of 64 values, with K's codes as
+// fp16 whole numbers n - 8 (exact) and the queries as they are; x = sum_j d_j S_j in
+// fp32, so scores are as exact as in the kernels for few rows.  In a block of 16 warps
+//   warps 8-11 decode the unit's codes into [token][64 values] tiles with the 128-byte
+//     swizzle, once for all rows, and the scales as fp32;
+//   warp 12 brings the query rows, a chunk at a time, by TMA: a box of 64 values, the
+//     heads of the group and as many tokens as fit (64 rows of 256 values, 128 of
+//     fewer); warp 13 makes their lse ready (LogSum) and their positions;
+//   warp 14 issues the products of a chunk into one of two places in tensor memory;
+//   warps 0-3 and 4-7 take the chunks in turn: scores, exponentials, sums.
+// A token's two sums (even and odd chunks of the unit) are added at the unit's end and
+// written; results depend on neither timing nor what else is in the batch.
+//
+// Every wait is bounded; a unit whose wait gave up gets NaN for its weights.
+#include <atomic>
+#include <cstdint>
+
+#include <cuda.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "pn_tcgen05.cuh"
+#include "pn_weigh.cuh"
+
+namespace pn {
+namespace {
+
+constexpr int kThreads = 16 * 32;
+constexpr int kUnit = 128;                     // tokens of a unit, MMA M
+constexpr int kPlaces = 2;                     // of S in tensor memory
+constexpr int kRowStages = 4;                  // of the rows' constants
+constexpr int kDecodeWarps = 4;
+
+struct Params {
+    CUtensorMap qmap;          // queries [tokens][heads][D]; box 64 values x group x per
+    WeighParams w;
+    int per;                   // tokens of a chunk
+};
+
+template <int D>
+struct Shape {
+    static constexpr int kGroups = D / 64;
+    static constexpr int kCols = D == 256 ? 64 : 128;          // rows of a chunk at most, MMA N
+    static constexpr int kABufs = D == 256 ? 1 : 2;            // decoded units
+    static constexpr int kQStages = D == 256 ? 4 : D == 128 ? 4 : 6;
+    static constexpr int kABytes = kGroups * kUnit * 128;
+    static constexpr int kQBytes = kGroups * kCols * 128;
+    static constexpr uint32_t kTmemCols = kPlaces * kGroups * kCols;       // 256 or 512
+    static constexpr int kA = 0;
+    static constexpr int kQ = kA + kABufs * kABytes;
+    static constexpr int kScales = kQ + kQStages * kQBytes;                // [buffer][group][token] floats
+    static constexpr int kRowData = kScales + kABufs * kGroups * kUnit * 4;    // [stage][less, share, pos][column]
+    static constexpr int kHalf = kRowData + kRowStages * 3 * kCols * 4;    // [2][token] the second sums
+    static constexpr int kScan = kHalf + 2 * kUnit * 4;                    // [threads + 1] units before each thread's requests
+    static constexpr int kWarpSums = kScan + (kThreads + 1) * 8;
+    static constexpr int kBars = kWarpSums + kThreads / 32 * 8;
+    static constexpr int kNumBars = 2 * kQStages + 3 * kABufs + 2 * kPlaces + 2 * kRowStages + 1;
+    static constexpr int kMisc = kBars + kNumBars * 8;                     // TMEM base, abort
+    static constexpr int kBytes = kMisc + 16 + 1024;                       // slack to align to 1024 bytes
+    static_assert(kBytes <= 227 * 1024, "fits one SM's shared memory");
+    static_assert(kQ % 1024 == 0 && kQBytes % 1024 == 0 && kScales % 16 == 0 && kBars % 8 == 0, "alignment");
+    static_assert(kTmemCols == 256 || kTmemCols == 512, "a size tensor memory is allocated in");
+};
+
+// fp32 accumulators, fp16 operands, both K-major, M = 128.
+__host__ __device__ constexpr uint32_t desc_of(int cols) { return (1u << 4) | (static_cast<uint32_t>(cols >> 3) << 17) | (static_cast<uint32_t>(kUnit >> 4) << 24); }
+
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t desc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %3, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %4, p;\n\t}"
+        :: "r"(d), "l"(a), "l"(b), "r"(static_cast<uint32_t>(accumulate)), "r"(desc) : "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int x, int y, int z, uint32_t bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
+        :: "r"(dst), "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
+}
+
+// Two fp32 numbers in a register pair, and operations on both at once.
+using Two = unsigned long long;
+__device__ __forceinline__ Two two(float a, float b) {
+    Two d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ Two two(uint32_t a, uint32_t b) {
+    Two d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "r"(a), "r"(b));
+    return d;
+}
+__device__ __forceinline__ float2 apart(Two v) {
+    float2 d;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(d.x), "=f"(d.y) : "l"(v));
+    return d;
+}
+__device__ __forceinline__ Two mul2(Two a, Two b) {
+    Two d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
+    Two d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+// A block's units, and the chunks of query rows that see any of a unit's tokens.
+struct Work {
+    uint64_t u, total;
+    WeighRequest r;
+    int b, h, tok0;
+    int c0, chunks;            // first chunk, how many
+    __device__ __forceinline__ bool any() const { return u < total; }
+    __device__ __forceinline__ void find(const Params& P, const uint64_t* scan, int each) {
+        if (u >= total) return;
+        int unit;
+        locate<kUnit, kThreads>(P.w, scan, each, u, r, b, h, unit);
+        tok0 = unit * kUnit;
+        const WeighArgs& a = P.w.a;
+        const int i0 = max(tok0 - r.pos0, 0), last = min(tok0 + kUnit, r.len) - 1;
+        int i1 = r.n;
+        if (a.window && tok0 >= a.sinks)
+            i1 = static_cast<int>(min(static_cast<int64_t>(i1), max(static_cast<int64_t>(last) + a.window - r.pos0, static_cast<int64_t>(0))));
+        c0 = i0 / P.per;
+        chunks = i0 < i1 ? (i1 + P.per - 1) / P.per - c0 : 0;
+    }
+    __device__ __forceinline__ void next(const Params& P, const uint64_t* scan, int each) {
+        u += gridDim.x;
+        find(P, scan, each);
+    }
+};
+
+// A place in a ring and how often it went round.
+template <int N>
+struct Ring {
+    uint32_t at = 0, turn = 0;
+    __device__ __forceinline__ void step() {
+        if (++at == N) {
+            at = 0;
+            ++turn;
+        }
+    }
+    __device__ __forceinline__ uint32_t full() const { return turn & 1u; }             // phase of the turn's filling
+    __device__ __forceinline__ uint32_t emptied() const { return (turn - 1u) & 1u; }   // of the emptying before it (turn > 0)
+};
+
+// A thread's share of a chunk: S of its token at ts, kCols columns by group.
+// Columns from `cols` (a multiple of 16) on are not looked at.
+template <int D, bool kMasked>
+__device__ __forceinline__ Two chunk_sum(Two sum, uint32_t ts, const Two (&d)[D / 64], float scale, const float* rows, int cols, int tok, int window, int sinks) {
+    constexpr int NG = D / 64, kCols = Shape<D>::kCols;
+    const Two f = two(scale, scale);
+#pragma unroll 1
+    for (int c = 0; c < cols; c += 16) {
+        uint32_t s[NG][16];
+#pragma unroll
+        for (int j = 0; j < NG; ++j) tmem_ld16(ts + kCols * j + c, s[j]);
+        tmem_wait_ld();
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+            const ulonglong2 less = *reinterpret_cast<const ulonglong2*>(rows + c + i), share = *reinterpret_cast<const ulonglong2*>(rows + kCols + c + i);
+            const Two l2[2] = {less.x, less.y}, g2[2] = {share.x, share.y};
+            int pos[4];
+            if constexpr (kMasked) {
+                const int4 v = *reinterpret_cast<const int4*>(rows + 2 * kCols + c + i);
+                pos[0] = v.x; pos[1] = v.y; pos[2] = v.z; pos[3] = v.w;
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                Two x = mul2(d[0], two(s[0][i + 2 * k], s[0][i + 2 * k + 1]));
+#pragma unroll
+                for (int j = 1; j < NG; ++j) x = fma2(d[j], two(s[j][i + 2 * k], s[j][i + 2 * k + 1]), x);
+                const float2 y = apart(fma2(x, f, l2[k]));
+                float p0 = ex2(y.x), p1 = ex2(y.y);
+                if constexpr (kMasked) {
+                    const int q0 = pos[2 * k], q1 = pos[2 * k + 1];
+                    p0 = tok <= q0 && (tok > q0 - window || tok < sinks) ? p0 : 0.0f;
+                    p1 = tok <= q1 && (tok > q1 - window || tok < sinks) ? p1 : 0.0f;
+                }
+                sum = fma2(two(p0, p1), g2[k], sum);
+            }
+        }
+    }
+    return sum;
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_constant__ Params P) {
+    using S = Shape<D>;
+    constexpr int NG = S::kGroups, kCols = S::kCols, kABufs = S::kABufs, kQStages = S::kQStages;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_base = smem_addr(smem_raw), base = (raw_base + 1023u) & ~1023u;
+    uint8_t* smem = smem_raw + (base - raw_base);
+    uint32_t bar = base + S::kBars;
+    auto take = [&](int n) { const uint32_t b = bar; bar += 8u * n; return b; };
+    const uint32_t q_full = take(kQStages), q_empty = take(kQStages), a_full = take(kABufs), a_empty = take(kABufs), d_empty = take(kABufs);
+    const uint32_t s_full = take(kPlaces), s_empty = take(kPlaces), rows_full = take(kRowStages), rows_empty = take(kRowStages), drain = take(1);
+    volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + S::kMisc);
+    volatile uint32_t* abort = misc + 1;
+    uint64_t* scan = reinterpret_cast<uint64_t*>(smem + S::kScan);
+    const WeighArgs& a = P.w.a;
+    const KvCache& cache = P.w.cache;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, group = P.w.group;
+    const uint64_t limit = P.w.timeout_ns;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kQStages; ++s) {
+            mbar_init(q_full + 8 * s, 1);
+            mbar_init(q_empty + 8 * s, 1);
+        }
+        for (int s = 0; s < kABufs; ++s) {
+            mbar_init(a_full + 8 * s, kDecodeWarps);
+            mbar_init(a_empty + 8 * s, 1);
+            mbar_init(d_empty + 8 * s, 8);
+        }
+        for (int s = 0; s < kPlaces; ++s) {
+            mbar_init(s_full + 8 * s, 1);
+            mbar_init(s_empty + 8 * s, 4);
+        }
+        for (int s = 0; s < kRowStages; ++s) {
+            mbar_init(rows_full + 8 * s, 1);
+            mbar_init(rows_empty + 8 * s, 4);
+        }
+        mbar_init(drain, 1);
+        *abort = 0u;
+        fence_mbar_init();
+    }
+    if (warp == 15) {
+        tmem_alloc(base + S::kMisc, S::kTmemCols);
+        tmem_relinquish();
+    }
+    // rows that no box fills stay zero: their products are finite
+    for (int i = threadIdx.x; i < kQStages * S::kQBytes / 16; i += kThreads) reinterpret_cast<uint4*>(smem + S::kQ)[i] = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+    const int each = scan_units<kUnit, kThreads>(P.w, scan, reinterpret_cast<uint64_t*>(smem + S::kWarpSums));
+    tc_fence_before_sync();
+    __syncthreads();
+    tc_fence_after_sync();
+    const uint32_t tmem = misc[0];
+    auto wait = [&](uint32_t b, uint32_t parity) { return mbar_try_wait(b, parity) || wait_phase(b, parity, limit, abort); };
+    Work w;
+    w.u = blockIdx.x;
+    w.total = scan[kThreads];
+    w.find(P, scan, each);
+
+    if (warp == 12) {
+        // ------------------------------------------------------- queries --
+        if (lane == 0) {
+            Ring<kQStages> q;
+            bool ok = true, stalled = false;
+            uint32_t issued = 0;
+            for (; ok && w.any(); w.next(P, scan, each))
+                for (int c = 0; c < w.chunks; ++c) {
+                    if (q.turn > 0 && !wait(q_empty + 8 * q.at, q.emptied())) {
+                        ok = false;
+                        break;
+                    }
+                    // (testing aid: with stall the first chunk's bytes are announced but never
+                    // copied; its wait can only time out)
+                    stalled |= P.w.stall != 0;
+                    const uint32_t dst = base + S::kQ + q.at * S::kQBytes, full = q_full + 8 * q.at;
+                    mbar_arrive_expect_tx(full, static_cast<uint32_t>(NG * P.per * group * 128));
+                    if (stalled) {
+                        ok = false;
+                        break;
+                    }
+#pragma unroll
+                    for (int j = 0; j < NG; ++j) tma_load_3d(dst + j * kCols * 128, &P.qmap, 64 * j, w.h * group, w.r.q0 + (w.c0 + c) * P.per, full);
+                    ++issued;
+                    q.step();
+                }
+            if (!ok && !stalled) *abort = 1u;
+            // the last copies into the stages land before the block ends, also after an abort
+            for (uint32_t s = 0; s < kQStages && s < issued; ++s) wait_phase(q_full + 8 * s, ((issued - 1 - s) / kQStages) & 1u, kAttnDrainNs, nullptr);
+        }
+        __syncwarp();
+    } else if (warp == 13) {
+        // ------------------------------------------------ the rows' constants --
+        Ring<kRowStages> s;
+        bool ok = true;
+        for (; ok && w.any(); w.next(P, scan, each))
+            for (int c = 0; c < w.chunks; ++c) {
+                if (s.turn > 0 && !__all_sync(0xFFFFFFFFu, wait(rows_empty + 8 * s.at, s.emptied()))) {
+                    ok = false;
+                    break;
+                }
+                float* to = reinterpret_cast<float*>(smem + S::kRowData) + s.at * 3 * kCols;
+#pragma unroll
+                for (int k = 0; k < kCols / 32; ++k) {
+                    const int row = lane + 32 * k, i = (w.c0 + c) * P.per + row / group;
+                    const bool real = row < P.per * group && i < w.r.n;
+                    const int64_t at = (static_cast<int64_t>(w.r.q0) + i) * a.heads + w.h * group + row % group;
+                    const LogSum l = log_sum_of(real ? a.lse[at] : -INFINITY, P.w.scale_rest);
+                    to[row] = l.less;
+                    to[kCols + row] = l.factor;
+                    reinterpret_cast<int*>(to)[2 * kCols + row] = real ? w.r.pos0 + i : INT32_MIN;
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(rows_full + 8 * s.at);
+                s.step();
+            }
+        if (!ok) *abort = 1u;
+    } else if (warp == 14) {
+        // ------------------------------------------------------ MMA issue --
+        if (elect_one()) {
+            Ring<kQStages> q;
+            Ring<kABufs> k;
+            Ring<kPlaces> t;
+            bool ok = true;
+            for (; ok && w.any(); w.next(P, scan, each)) {
+                ok = wait(a_full + 8 * k.at, k.full());
+                if (!ok) break;
+                for (int c = 0; c < w.chunks; ++c) {
+                    ok = (t.turn == 0 || wait(s_empty + 8 * t.at, t.emptied())) && wait(q_full + 8 * q.at, q.full());
+                    if (!ok) break;
+                    tc_fence_after_sync();
+                    const uint32_t ka = base + S::kA + k.at * S::kABytes, qa = base + S::kQ + q.at * S::kQBytes, d = tmem + t.at * (NG * kCols);
+#pragma unroll
+                    for (int j = 0; j < NG; ++j)
+#pragma unroll
+                        for (int kk = 0; kk < 4; ++kk)
+                            mma_ss(d + kCols * j, smem_desc_sw128(ka + j * (kUnit * 128) + kk * 32), smem_desc_sw128(qa + j * (kCols * 128) + kk * 32), desc_of(kCols), kk != 0);
+                    mma_commit(q_empty + 8 * q.at);
+                    mma_commit(s_full + 8 * t.at);
+                    q.step();
+                    t.step();
+                }
+                if (!ok) break;
+                mma_commit(a_empty + 8 * k.at);
+                k.step();
+            }
+            if (!ok) *abort = 1u;
+            mma_commit(drain);                 // every product of this block finished (also after an abort)
+            wait_phase(drain, 0u, kAttnDrainNs, nullptr);
+        }
+        __syncwarp();
+    } else if (warp >= 8 && warp < 8 + kDecodeWarps) {
+        // --------------------------------------------------------- decode --
+        constexpr int GP = kv_plane_groups(D), PL = kv_planes(D), kRecords = kUnit / kKvTokens / kDecodeWarps;
+        const int g = lane >> 2, t = lane & 3;
+        Ring<kABufs> k;
+        bool ok = true;
+        for (; w.any(); w.next(P, scan, each)) {
+            // the warp's records are read before the buffer is waited for
+            uint32_t kw[kRecords][2][D / 32];
+            float scale[kRecords][2];          // of tokens lane % 8 and 8 more, group lane / 8
+#pragma unroll
+            for (int i = 0; i < kRecords; ++i) {
+                const int tok = w.tok0 + ((warp - 8) + i * kDecodeWarps) * kKvTokens;
+                const uint8_t* record = nullptr;
+                if (tok < w.r.len) {
+                    const int page = a.table[w.b * a.table_stride + (tok >> cache.page_shift)];
+                    if (page >= 0 && page < cache.pages) record = cache.record((static_cast<int64_t>(page) << cache.page_shift) + (tok & (cache.page_size - 1)), w.h);
+                }
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+#pragma unroll
+                    for (int q = 0; q < D / 32; ++q) kw[i][hh][q] = 0x88888888u;        // (zero)
+                    scale[i][hh] = 0.0f;
+                    if (!record) continue;
+#pragma unroll
+                    for (int pl = 0; pl < PL; ++pl) {
+                        const uint8_t* p = record + ((hh * PL + pl) * 32 + lane) * 8 * GP;
+                        if constexpr (GP == 2) {
+                            const uint4 v = *reinterpret_cast<const uint4*>(p);
+                            kw[i][hh][4 * pl] = v.x; kw[i][hh][4 * pl + 1] = v.y; kw[i][hh][4 * pl + 2] = v.z; kw[i][hh][4 * pl + 3] = v.w;
+                        } else {
+                            const uint2 v = *reinterpret_cast<const uint2*>(p);
+                            kw[i][hh][0] = v.x; kw[i][hh][1] = v.y;
+                        }
+                    }
+                    if ((lane >> 3) < NG) scale[i][hh] = __half2float(*reinterpret_cast<const __half*>(record + kv_k_scales(D) + ((hh * 8 + (lane & 7)) * NG + (lane >> 3)) * 2));
+                }
+            }
+            if (k.turn > 0) ok = ok && wait(a_empty + 8 * k.at, k.emptied()) && wait(d_empty + 8 * k.at, k.emptied());
+            if (!__all_sync(0xFFFFFFFFu, ok)) break;
+            uint8_t* tile = smem + S::kA + k.at * S::kABytes;
+            float* d = reinterpret_cast<float*>(smem + S::kScales) + k.at * NG * kUnit;
+            auto put = [&](int token, int j, int i, uint32_t word) {   // 16-byte chunk `i` of a token's row in a group's tile
+                const uint32_t sh = word >> 8;
+                *reinterpret_cast<uint4*>(tile + j * (kUnit * 128) + token * 128 + ((i ^ (token & 7)) << 4)) =
+                    make_uint4(decode_pair<kPn4t, 0>(word, sh), decode_pair<kPn4t, 1>(word, sh), decode_pair<kPn4t, 2>(word, sh), decode_pair<kPn4t, 3>(word, sh));
+            };
+#pragma unroll
+            for (int i = 0; i < kRecords; ++i) {
+                const int first = ((warp - 8) + i * kDecodeWarps) * kKvTokens;
+#pragma unroll
+                for (int hh = 0; hh < 2; ++hh) {
+#pragma unroll
+                    for (int j = 0; j < NG; ++j) {
+                        put(first + hh * 8 + g, j, 2 * t, kw[i][hh][2 * j]);
+                        put(first + hh * 8 + g, j, 2 * t + 1, kw[i][hh][2 * j + 1]);
+                    }
+                    if ((lane >> 3) < NG) d[(lane >> 3) * kUnit + first + hh * 8 + (lane & 7)] = scale[i][hh];
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(a_full + 8 * k.at);
+            k.step();
+        }
+        if (!ok) *abort = 1u;
+    } else if (warp < 8) {
+        // ----------------------------------------------- scores and sums --
+        const int second = warp >> 2, token = threadIdx.x & (kUnit - 1);
+        const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
+        float* half = reinterpret_cast<float*>(smem + S::kHalf);
+        const int window = a.window ? a.window : INT32_MAX, cols = (P.per * group + 15) / 16 * 16;
+        Ring<kABufs> k;
+        Ring<kPlaces> t;
+        Ring<kRowStages> rows;
+        bool ok = true;
+        for (uint32_t n = 0; w.any(); w.next(P, scan, each), ++n) {
+            const int tok = w.tok0 + token;
+            // where the token's weight is, and what it was
+            int64_t to = -1;
+            float before = 0.0f;
+            if (tok < w.r.len) {
+                const int page = a.table[w.b * a.table_stride + (tok >> cache.page_shift)];
+                if (page >= 0 && page < cache.pages) to = ((static_cast<int64_t>(page) * cache.heads + w.h) << cache.page_shift) + (tok & (cache.page_size - 1));
+            }
+            if (second == 0 && to >= 0 && a.weights && tok < w.r.pos0) before = a.decay * a.weights[to];
+            ok = ok && __all_sync(0xFFFFFFFFu, wait(a_full + 8 * k.at, k.full()));
+            Two d[NG];
+#pragma unroll
+            for (int j = 0; j < NG; ++j) {
+                const float v = reinterpret_cast<const float*>(smem + S::kScales)[(k.at * NG + j) * kUnit + token];
+                d[j] = two(v, v);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(d_empty + 8 * k.at);
+            k.step();
+            Two sum = two(0.0f, 0.0f);
+            for (int c = 0; c < w.chunks; ++c) {
+                if (static_cast<int>(t.at) == second && ok) {
+                    ok = wait(rows_full + 8 * rows.at, rows.full()) && wait(s_full + 8 * t.at, t.full());
+                    ok = __all_sync(0xFFFFFFFFu, ok);
+                    tc_fence_after_sync();
+                    if (ok) {
+                        const int i0 = (w.c0 + c) * P.per, pos_lo = w.r.pos0 + i0, pos_hi = pos_lo + P.per - 1;
+                        const bool plain = i0 + P.per <= w.r.n && w.tok0 + kUnit - 1 <= pos_lo && (w.tok0 > pos_hi - window || w.tok0 + kUnit <= a.sinks);
+                        const float* data = reinterpret_cast<const float*>(smem + S::kRowData) + rows.at * 3 * kCols;
+                        const uint32_t ts = tmem + t.at * (NG * kCols) + lanes;
+                        if (plain) sum = chunk_sum<D, false>(sum, ts, d, P.w.scale_log2, data, cols, tok, window, a.sinks);
+                        else sum = chunk_sum<D, true>(sum, ts, d, P.w.scale_log2, data, cols, tok, window, a.sinks);
+                    }
+                    tc_fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) {
+                        mbar_arrive(s_empty + 8 * t.at);
+                        mbar_arrive(rows_empty + 8 * rows.at);
+                    }
+                }
+                t.step();
+                rows.step();
+            }
+            if (!ok) *abort = 1u;
+            const float2 both = apart(sum);
+            const float mine = ok ? both.x + both.y : __int_as_float(0x7FFFFFFF);
+            // the second warps' sums: two places in turn, so that one barrier a unit is enough
+            if (second) half[(n & 1) * kUnit + token] = mine;
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            if (!second && to >= 0) a.out[to] = before + (mine + half[(n & 1) * kUnit + token]);
+        }
+    }
+    // ------------------------------------------------------------ teardown --
+    tc_fence_before_sync();
+    __syncthreads();
+    if (warp == 15) {
+        tc_fence_after_sync();
+        tmem_dealloc(tmem, S::kTmemCols);
+    }
+}
+
+using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiledFn encode_tiled() {
+    static EncodeTiledFn fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult q{};
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess || q != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeTiledFn>(p);
+    }();
+    return fn;
+}
+
+template <int D>
+cudaError_t launch(const WeighParams& W, int num_sms, cudaStream_t s) {
+    using S = Shape<D>;
+    Params P{};
+    P.w = W;
+    P.per = S::kCols / W.group;
+    // queries as [tokens][heads][D], rows at q_stride; what lies behind the last token reads as zero
+    EncodeTiledFn fn = encode_tiled();
+    const cuuint64_t dims[3] = {D, static_cast<cuuint64_t>(W.a.heads), static_cast<cuuint64_t>(W.a.tokens)};
+    const cuuint64_t strides[2] = {D * 2, static_cast<cuuint64_t>(W.a.q_stride) * 2};
+    const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(W.group), static_cast<cuuint32_t>(P.per)}, element[3] = {1, 1, 1};
+    if (!fn || fn(&P.qmap, CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, const_cast<__half*>(W.a.q), dims, strides, box, element, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    static std::atomic<uint64_t> smem_set{0};
+    if (cudaError_t e = set_smem_limit_once(weigh_tc_kernel<D>, S::kBytes, smem_set); e != cudaSuccess) return e;
+    weigh_tc_kernel<D><<<num_sms, kThreads, S::kBytes, s>>>(P);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+bool weigh_tc_takes(const WeighArgs& a, const KvGeometry& g) {
+    const int group = a.heads / g.heads, cols = g.D == 256 ? Shape<256>::kCols : Shape<128>::kCols;
+    return group <= cols && static_cast<int64_t>(a.max_queries) * group >= 64;
+}
+
+cudaError_t launch_weigh_tc(const WeighParams& P, int num_sms, cudaStream_t s) {
+    if (P.cache.D == 64) return launch<64>(P, num_sms, s);
+    return P.cache.D == 128 ? launch<128>(P, num_sms, s) : launch<256>(P, num_sms, s);
+}
+
+}  // namespace pn

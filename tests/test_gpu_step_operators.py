@@ -358,7 +358,9 @@ WEIGHTS = [
     ([700], [1], 8, 2, 256, 32, 64, 70), ([900, 350], [8, 3], 12, 2, 128, 16, 130, 17), ([300], [5], 2, 1, 128, 16, 1, 1),
     ([70], [70], 4, 2, 128, 16, 0, 0), ([200, 150], [130, 150], 6, 2, 64, 32, 0, 0), ([290], [257], 5, 1, 256, 64, 0, 0),
     ([400], [300], 4, 1, 128, 16, 90, 5), ([333, 40, 129], [200, 40, 1], 8, 1, 128, 64, 0, 0), ([130], [130], 3, 3, 256, 128, 33, 70),
-    ([270], [270], 2, 2, 64, 16, 64, 0), ([600], [140], 8, 1, 128, 32, 0, 0),
+    ([270], [270], 2, 2, 64, 16, 64, 0), ([600], [140], 8, 1, 128, 32, 0, 0), ([300], [40], 5, 1, 128, 64, 0, 0), ([700, 0, 5, 257], [64, 0, 5, 200], 6, 2, 256, 16, 0, 0),
+    ([300, 128], [90, 127], 14, 2, 64, 16, 50, 9), ([200], [3], 130, 1, 128, 16, 0, 0), ([150], [4], 65, 1, 256, 16, 0, 0), ([129], [2], 128, 1, 128, 32, 0, 0),
+    ([1500, 40], [1, 33], 8, 1, 128, 64, 0, 0),
 ]
 
 
@@ -399,7 +401,7 @@ def test_weigh_sums_to_the_rows(pn):
     assert torch.all((total - 47 * 4).abs() <= 47 * 4 * 2.0 ** -14)
     for b in range(4):
         rows = slice(int(starts[b]), int(starts[b + 1]))
-        one = pn.kv_weigh(dev[0][rows], dev[1], dev[2][b:b + 1], dev[3][b:b + 1], cuda(starts[b:b + 2] - starts[b]), int(starts[b + 1] - starts[b]), lse[rows], 0.09)
+        one = pn.kv_weigh(dev[0][rows], dev[1], dev[2][b:b + 1], dev[3][b:b + 1], cuda(starts[b:b + 2] - starts[b]), 40, lse[rows], 0.09)
         pages = table[b, :-(-int(lens[b]) // 64)]
         assert torch.equal(one[pages], all_of[pages])
 
@@ -420,6 +422,24 @@ def test_weigh_long(pn):
     for h in range(kv):
         x = np.stack([0.05 * (kf[:, h] @ q[0, i].astype(np.float64)) - lse[0, i] for i in range(4 * h, 4 * h + 4)])
         assert np.abs(got[0, h] / np.exp(x).sum(0) - 1).max() <= 2.0 ** -15
+
+
+def test_weigh_wait_timeout(pn):
+    """A wait on the GPU that gives up leaves NaN in the weights, and the next call is right."""
+    case = weigh_case([300, 200], [80, 100], 4, 2, 128, 16)
+    q, cache, table, lens, starts, ks, vs, weights = case
+    dev = [cuda(a) for a in (q, cache, table, lens, starts)]
+    lse = torch.zeros(180, 4, device="cuda")
+    pn.set_wait_timeout_ns(20_000_000)
+    pn.set_test_stall(True)
+    try:
+        out = pn.kv_weigh(*dev, 100, lse, 0.1)
+        torch.cuda.synchronize()
+    finally:
+        pn.set_test_stall(False)
+        pn.set_wait_timeout_ns(1_000_000_000)
+    assert torch.isnan(out[table[0, :300 // 16]]).all()
+    check_weigh(pn, case, 100, 0.1)
 
 
 # -------------------------------------------------------------------- evict --
