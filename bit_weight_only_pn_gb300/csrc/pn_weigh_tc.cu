@@ -32,16 +32,19 @@
 namespace pn {
 namespace {
 
-constexpr int kThreads = 16 * 32;
+constexpr int kSumWarps = 16;                  // two places of S, two halves of the columns, four quarters of the tokens
+constexpr int kThreads = (kSumWarps + 8) * 32; // 80 registers each
 constexpr int kUnit = 128;                     // tokens of a unit, MMA M
 constexpr int kPlaces = 2;                     // of S in tensor memory
 constexpr int kRowStages = 4;                  // of the rows' constants
 constexpr int kDecodeWarps = 4;
+constexpr uint32_t kNap = 100;                 // nanoseconds between polls
 
 struct Params {
     CUtensorMap qmap;          // queries [tokens][heads][D]; box 64 values x group x per
     WeighParams w;
     int per;                   // tokens of a chunk
+    int split;                 // blocks to a unit, in a cluster: 1 or 2
 };
 
 template <int D>
@@ -57,11 +60,12 @@ struct Shape {
     static constexpr int kQ = kA + kABufs * kABytes;
     static constexpr int kScales = kQ + kQStages * kQBytes;                // [buffer][group][token] floats
     static constexpr int kRowData = kScales + kABufs * kGroups * kUnit * 4;    // [stage][less, share, pos][column]
-    static constexpr int kHalf = kRowData + kRowStages * 3 * kCols * 4;    // [2][token] the second sums
-    static constexpr int kScan = kHalf + 2 * kUnit * 4;                    // [threads + 1] units before each thread's requests
+    static constexpr int kParts = kRowData + kRowStages * 3 * kCols * 4;    // [2][4][token] parts of the sums
+    static constexpr int kOther = kParts + 2 * 4 * kUnit * 4;               // [2][token] sums of the cluster's second block (in the first)
+    static constexpr int kScan = kOther + 2 * kUnit * 4;                   // [threads + 1] units before each thread's requests
     static constexpr int kWarpSums = kScan + (kThreads + 1) * 8;
     static constexpr int kBars = kWarpSums + kThreads / 32 * 8;
-    static constexpr int kNumBars = 2 * kQStages + 3 * kABufs + 2 * kPlaces + 2 * kRowStages + 1;
+    static constexpr int kNumBars = 2 * kQStages + 3 * kABufs + 2 * kPlaces + 2 * kRowStages + 1 + 4;
     static constexpr int kMisc = kBars + kNumBars * 8;                     // TMEM base, abort
     static constexpr int kBytes = kMisc + 16 + 1024;                       // slack to align to 1024 bytes
     static_assert(kBytes <= 227 * 1024, "fits one SM's shared memory");
@@ -88,6 +92,29 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, int 
     asm volatile(
         "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];"
         :: "r"(dst), "l"(tmap), "r"(x), "r"(y), "r"(z), "r"(bar) : "memory");
+}
+
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+}
+// A float to, and an arrival at a barrier of, the same place of block `rank` of the cluster.
+__device__ __forceinline__ void store_to_block(uint32_t addr, uint32_t rank, float v) {
+    asm volatile("{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %0, %1;\n\tst.shared::cluster.f32 [r], %2;\n\t}" :: "r"(addr), "r"(rank), "f"(v) : "memory");
+}
+__device__ __forceinline__ void arrive_at_block(uint32_t bar, uint32_t rank) {
+    asm volatile("{\n\t.reg .b32 r;\n\tmapa.shared::cluster.u32 r, %0, %1;\n\tmbarrier.arrive.release.cluster.shared::cluster.b64 _, [r];\n\t}" :: "r"(bar), "r"(rank) : "memory");
+}
+// A wait for arrivals from another block, whose writes before them are then seen.
+__device__ __forceinline__ bool wait_cluster(uint32_t bar, uint32_t parity, uint64_t limit_ns, volatile uint32_t* abort) {
+    const int64_t end = clock64() + cycles_of(limit_ns);
+    for (;;) {
+        uint32_t done;
+        asm volatile("{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+                     : "=r"(done) : "r"(bar), "r"(parity) : "memory");
+        if (done) return true;
+        if (*abort || clock64() > end) return false;
+        __nanosleep(20);
+    }
 }
 
 // Two fp32 numbers in a register pair, and operations on both at once.
@@ -118,18 +145,30 @@ __device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
     return d;
 }
 
-// A block's units, and the chunks of query rows that see any of a unit's tokens.
+// A block's units, and the chunks of query rows that see any of a unit's tokens.  A
+// request's units are numbered tile by tile, all heads of a tile after each other: in
+// a prompt a tile costs no more than the one before.  Blocks take units in turns, in
+// every second one in reverse order, so the dear ones and the cheap ones of a prompt
+// are shared out evenly (in plain turns, head by head, the busiest SM had 1.5 times
+// the average: 4096 queries of 32 + 8 heads of 128 over 8192 tokens took 422 us).
 struct Work {
-    uint64_t u, total;
+    uint64_t total, turn;
     WeighRequest r;
     int b, h, tok0;
     int c0, chunks;            // first chunk, how many
-    __device__ __forceinline__ bool any() const { return u < total; }
+    uint32_t team, teams;      // blocks that share units, and which they are
+    __device__ __forceinline__ uint64_t unit() const { return turn * teams + (turn & 1u ? teams - 1 - team : team); }
+    __device__ __forceinline__ bool any() const { return unit() < total; }
     __device__ __forceinline__ void find(const Params& P, const uint64_t* scan, int each) {
+        const uint64_t u = unit();
         if (u >= total) return;
-        int unit;
-        locate<kUnit, kThreads>(P.w, scan, each, u, r, b, h, unit);
-        tok0 = unit * kUnit;
+        int of_head;
+        locate<kUnit, kThreads>(P.w, scan, each, u, r, b, h, of_head);
+        // (its number among the request's units, tile by tile)
+        const uint64_t index = static_cast<uint64_t>(h) * units_of<kUnit>(r) + of_head;
+        const uint64_t tile = index / static_cast<uint64_t>(P.w.cache.heads);
+        h = static_cast<int>(index - tile * P.w.cache.heads);
+        tok0 = static_cast<int>(tile) * kUnit;
         const WeighArgs& a = P.w.a;
         const int i0 = max(tok0 - r.pos0, 0), last = min(tok0 + kUnit, r.len) - 1;
         int i1 = r.n;
@@ -139,7 +178,7 @@ struct Work {
         chunks = i0 < i1 ? (i1 + P.per - 1) / P.per - c0 : 0;
     }
     __device__ __forceinline__ void next(const Params& P, const uint64_t* scan, int each) {
-        u += gridDim.x;
+        ++turn;
         find(P, scan, each);
     }
 };
@@ -159,19 +198,23 @@ struct Ring {
 };
 
 // A thread's share of a chunk: S of its token at ts, kCols columns by group.
-// Columns from `cols` (a multiple of 16) on are not looked at.
+// Columns c0 .. c1 - 1, multiples of 16, are its warp's.
 template <int D, bool kMasked>
-__device__ __forceinline__ Two chunk_sum(Two sum, uint32_t ts, const Two (&d)[D / 64], float scale, const float* rows, int cols, int tok, int window, int sinks) {
+__device__ __forceinline__ Two chunk_sum(Two sum, uint32_t ts, const Two (&d)[D / 64], float scale, const float* rows, int c0, int c1, int tok, int window, int sinks) {
     constexpr int NG = D / 64, kCols = Shape<D>::kCols;
     const Two f = two(scale, scale);
+    constexpr int kBlock = D == 256 ? 8 : 16;
 #pragma unroll 1
-    for (int c = 0; c < cols; c += 16) {
-        uint32_t s[NG][16];
+    for (int c = c0; c < c1; c += kBlock) {
+        uint32_t s[NG][kBlock];
 #pragma unroll
-        for (int j = 0; j < NG; ++j) tmem_ld16(ts + kCols * j + c, s[j]);
+        for (int j = 0; j < NG; ++j) {
+            if constexpr (kBlock == 16) tmem_ld16(ts + kCols * j + c, s[j]);
+            else tmem_ld8(ts + kCols * j + c, s[j]);
+        }
         tmem_wait_ld();
 #pragma unroll
-        for (int i = 0; i < 16; i += 4) {
+        for (int i = 0; i < kBlock; i += 4) {
             const ulonglong2 less = *reinterpret_cast<const ulonglong2*>(rows + c + i), share = *reinterpret_cast<const ulonglong2*>(rows + kCols + c + i);
             const Two l2[2] = {less.x, less.y}, g2[2] = {share.x, share.y};
             int pos[4];
@@ -209,6 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
     auto take = [&](int n) { const uint32_t b = bar; bar += 8u * n; return b; };
     const uint32_t q_full = take(kQStages), q_empty = take(kQStages), a_full = take(kABufs), a_empty = take(kABufs), d_empty = take(kABufs);
     const uint32_t s_full = take(kPlaces), s_empty = take(kPlaces), rows_full = take(kRowStages), rows_empty = take(kRowStages), drain = take(1);
+    const uint32_t x_full = take(2), x_empty = take(2);        // of the second block's sums: in the first block, in the second
     volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + S::kMisc);
     volatile uint32_t* abort = misc + 1;
     uint64_t* scan = reinterpret_cast<uint64_t*>(smem + S::kScan);
@@ -225,21 +269,25 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
         for (int s = 0; s < kABufs; ++s) {
             mbar_init(a_full + 8 * s, kDecodeWarps);
             mbar_init(a_empty + 8 * s, 1);
-            mbar_init(d_empty + 8 * s, 8);
+            mbar_init(d_empty + 8 * s, kSumWarps);
         }
         for (int s = 0; s < kPlaces; ++s) {
             mbar_init(s_full + 8 * s, 1);
-            mbar_init(s_empty + 8 * s, 4);
+            mbar_init(s_empty + 8 * s, kSumWarps / 2);
         }
         for (int s = 0; s < kRowStages; ++s) {
             mbar_init(rows_full + 8 * s, 1);
-            mbar_init(rows_empty + 8 * s, 4);
+            mbar_init(rows_empty + 8 * s, kSumWarps / 2);
         }
         mbar_init(drain, 1);
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(x_full + 8 * s, 4);
+            mbar_init(x_empty + 8 * s, 4);
+        }
         *abort = 0u;
         fence_mbar_init();
     }
-    if (warp == 15) {
+    if (warp == kThreads / 32 - 1) {
         tmem_alloc(base + S::kMisc, S::kTmemCols);
         tmem_relinquish();
     }
@@ -249,23 +297,28 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
     const int each = scan_units<kUnit, kThreads>(P.w, scan, reinterpret_cast<uint64_t*>(smem + S::kWarpSums));
     tc_fence_before_sync();
     __syncthreads();
+    if (P.split > 1) cluster_sync();           // both blocks' barriers are there
     tc_fence_after_sync();
     const uint32_t tmem = misc[0];
-    auto wait = [&](uint32_t b, uint32_t parity) { return mbar_try_wait(b, parity) || wait_phase(b, parity, limit, abort); };
+    // nap: of the warps that work ahead, whose polling would take the others' issue slots
+    auto wait = [&](uint32_t b, uint32_t parity, uint32_t nap = 0) { return mbar_try_wait(b, parity) || wait_phase(b, parity, limit, abort, nap); };
+    const int split = P.split, rank = static_cast<int>(blockIdx.x) % split;    // the block's chunks: rank, rank + split, ...
     Work w;
-    w.u = blockIdx.x;
+    w.turn = 0;
+    w.team = blockIdx.x / split;
+    w.teams = gridDim.x / split;
     w.total = scan[kThreads];
     w.find(P, scan, each);
 
-    if (warp == 12) {
+    if (warp == kSumWarps + 4) {
         // ------------------------------------------------------- queries --
         if (lane == 0) {
             Ring<kQStages> q;
             bool ok = true, stalled = false;
             uint32_t issued = 0;
             for (; ok && w.any(); w.next(P, scan, each))
-                for (int c = 0; c < w.chunks; ++c) {
-                    if (q.turn > 0 && !wait(q_empty + 8 * q.at, q.emptied())) {
+                for (int c = rank; c < w.chunks; c += split) {
+                    if (q.turn > 0 && !wait(q_empty + 8 * q.at, q.emptied(), kNap)) {
                         ok = false;
                         break;
                     }
@@ -288,23 +341,49 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
             for (uint32_t s = 0; s < kQStages && s < issued; ++s) wait_phase(q_full + 8 * s, ((issued - 1 - s) / kQStages) & 1u, kAttnDrainNs, nullptr);
         }
         __syncwarp();
-    } else if (warp == 13) {
+    } else if (warp == kSumWarps + 5 || warp == kSumWarps + 7) {
         // ------------------------------------------------ the rows' constants --
+        // (a load of lse waited for in every chunk took 3500 cycles a chunk, where its products take 800)
+        constexpr int kEach = kCols / 32;      // rows of a lane
         Ring<kRowStages> s;
+        int of_token[kEach], of_head[kEach];
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            of_token[k] = (lane + 32 * k) / group;
+            of_head[k] = lane + 32 * k - of_token[k] * group;
+        }
         bool ok = true;
-        for (; ok && w.any(); w.next(P, scan, each))
-            for (int c = 0; c < w.chunks; ++c) {
-                if (s.turn > 0 && !__all_sync(0xFFFFFFFFu, wait(rows_empty + 8 * s.at, s.emptied()))) {
+        for (; ok && w.any(); w.next(P, scan, each)) {
+            float lse[kEach];
+            auto fetch = [&](int c) {          // of the unit's chunk c; any of the request's where there is no such row
+#pragma unroll
+                for (int k = 0; k < kEach; ++k) {
+                    const int i = min((w.c0 + c) * P.per + of_token[k], w.r.n - 1);
+                    lse[k] = a.lse[(static_cast<int64_t>(w.r.q0) + i) * a.heads + w.h * group + of_head[k]];
+                }
+            };
+            // the two warps take the block's chunks in turn
+            const int mine = rank + (((s.at & 1u) != 0) != (warp == kSumWarps + 7) ? split : 0);
+            if (mine < w.chunks) fetch(mine);
+            for (int c = rank; c < w.chunks; c += split) {
+                if (((s.at & 1u) != 0) != (warp == kSumWarps + 7)) {
+                    s.step();
+                    continue;
+                }
+                float now[kEach];
+#pragma unroll
+                for (int k = 0; k < kEach; ++k) now[k] = lse[k];
+                if (c + 2 * split < w.chunks) fetch(c + 2 * split);
+                if (s.turn > 0 && !__all_sync(0xFFFFFFFFu, wait(rows_empty + 8 * s.at, s.emptied(), kNap))) {
                     ok = false;
                     break;
                 }
                 float* to = reinterpret_cast<float*>(smem + S::kRowData) + s.at * 3 * kCols;
 #pragma unroll
-                for (int k = 0; k < kCols / 32; ++k) {
-                    const int row = lane + 32 * k, i = (w.c0 + c) * P.per + row / group;
-                    const bool real = row < P.per * group && i < w.r.n;
-                    const int64_t at = (static_cast<int64_t>(w.r.q0) + i) * a.heads + w.h * group + row % group;
-                    const LogSum l = log_sum_of(real ? a.lse[at] : -INFINITY, P.w.scale_rest);
+                for (int k = 0; k < kEach; ++k) {
+                    const int row = lane + 32 * k, i = (w.c0 + c) * P.per + of_token[k];
+                    const bool real = of_token[k] < P.per && i < w.r.n;
+                    const LogSum l = log_sum_of(real ? now[k] : -INFINITY, P.w.scale_rest);
                     to[row] = l.less;
                     to[kCols + row] = l.factor;
                     reinterpret_cast<int*>(to)[2 * kCols + row] = real ? w.r.pos0 + i : INT32_MIN;
@@ -313,8 +392,9 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
                 if (lane == 0) mbar_arrive(rows_full + 8 * s.at);
                 s.step();
             }
+        }
         if (!ok) *abort = 1u;
-    } else if (warp == 14) {
+    } else if (warp == kSumWarps + 6) {
         // ------------------------------------------------------ MMA issue --
         if (elect_one()) {
             Ring<kQStages> q;
@@ -324,8 +404,8 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
             for (; ok && w.any(); w.next(P, scan, each)) {
                 ok = wait(a_full + 8 * k.at, k.full());
                 if (!ok) break;
-                for (int c = 0; c < w.chunks; ++c) {
-                    ok = (t.turn == 0 || wait(s_empty + 8 * t.at, t.emptied())) && wait(q_full + 8 * q.at, q.full());
+                for (int c = rank; c < w.chunks; c += split) {
+                    ok = (t.turn == 0 || wait(s_empty + 8 * t.at, t.emptied(), 20)) && wait(q_full + 8 * q.at, q.full(), 20);
                     if (!ok) break;
                     tc_fence_after_sync();
                     const uint32_t ka = base + S::kA + k.at * S::kABytes, qa = base + S::kQ + q.at * S::kQBytes, d = tmem + t.at * (NG * kCols);
@@ -348,7 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
             wait_phase(drain, 0u, kAttnDrainNs, nullptr);
         }
         __syncwarp();
-    } else if (warp >= 8 && warp < 8 + kDecodeWarps) {
+    } else if (warp >= kSumWarps && warp < kSumWarps + kDecodeWarps) {
         // --------------------------------------------------------- decode --
         constexpr int GP = kv_plane_groups(D), PL = kv_planes(D), kRecords = kUnit / kKvTokens / kDecodeWarps;
         const int g = lane >> 2, t = lane & 3;
@@ -360,7 +440,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
             float scale[kRecords][2];          // of tokens lane % 8 and 8 more, group lane / 8
 #pragma unroll
             for (int i = 0; i < kRecords; ++i) {
-                const int tok = w.tok0 + ((warp - 8) + i * kDecodeWarps) * kKvTokens;
+                const int tok = w.tok0 + ((warp - kSumWarps) + i * kDecodeWarps) * kKvTokens;
                 const uint8_t* record = nullptr;
                 if (tok < w.r.len) {
                     const int page = a.table[w.b * a.table_stride + (tok >> cache.page_shift)];
@@ -386,7 +466,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
                     if ((lane >> 3) < NG) scale[i][hh] = __half2float(*reinterpret_cast<const __half*>(record + kv_k_scales(D) + ((hh * 8 + (lane & 7)) * NG + (lane >> 3)) * 2));
                 }
             }
-            if (k.turn > 0) ok = ok && wait(a_empty + 8 * k.at, k.emptied()) && wait(d_empty + 8 * k.at, k.emptied());
+            if (k.turn > 0) ok = ok && wait(a_empty + 8 * k.at, k.emptied(), kNap) && wait(d_empty + 8 * k.at, k.emptied(), kNap);
             if (!__all_sync(0xFFFFFFFFu, ok)) break;
             uint8_t* tile = smem + S::kA + k.at * S::kABytes;
             float* d = reinterpret_cast<float*>(smem + S::kScales) + k.at * NG * kUnit;
@@ -397,7 +477,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
             };
 #pragma unroll
             for (int i = 0; i < kRecords; ++i) {
-                const int first = ((warp - 8) + i * kDecodeWarps) * kKvTokens;
+                const int first = ((warp - kSumWarps) + i * kDecodeWarps) * kKvTokens;
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh) {
 #pragma unroll
@@ -414,12 +494,13 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
             k.step();
         }
         if (!ok) *abort = 1u;
-    } else if (warp < 8) {
+    } else if (warp < kSumWarps) {
         // ----------------------------------------------- scores and sums --
-        const int second = warp >> 2, token = threadIdx.x & (kUnit - 1);
+        const int mine = warp >> 2, place = mine & 1, token = threadIdx.x & (kUnit - 1);
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
-        float* half = reinterpret_cast<float*>(smem + S::kHalf);
-        const int window = a.window ? a.window : INT32_MAX, cols = (P.per * group + 15) / 16 * 16;
+        float* parts = reinterpret_cast<float*>(smem + S::kParts);
+        const int window = a.window ? a.window : INT32_MAX, cols = (P.per * group + 15) / 16 * 16, cut = (cols / 2 + 15) / 16 * 16;
+        const int c0 = mine >> 1 ? cut : 0, c1 = mine >> 1 ? cols : cut;       // the warp's columns
         Ring<kABufs> k;
         Ring<kPlaces> t;
         Ring<kRowStages> rows;
@@ -433,7 +514,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
                 const int page = a.table[w.b * a.table_stride + (tok >> cache.page_shift)];
                 if (page >= 0 && page < cache.pages) to = ((static_cast<int64_t>(page) * cache.heads + w.h) << cache.page_shift) + (tok & (cache.page_size - 1));
             }
-            if (second == 0 && to >= 0 && a.weights && tok < w.r.pos0) before = a.decay * a.weights[to];
+            if (mine == 0 && to >= 0 && a.weights && tok < w.r.pos0) before = a.decay * a.weights[to];
             ok = ok && __all_sync(0xFFFFFFFFu, wait(a_full + 8 * k.at, k.full()));
             Two d[NG];
 #pragma unroll
@@ -445,9 +526,9 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
             if (lane == 0) mbar_arrive(d_empty + 8 * k.at);
             k.step();
             Two sum = two(0.0f, 0.0f);
-            for (int c = 0; c < w.chunks; ++c) {
-                if (static_cast<int>(t.at) == second && ok) {
-                    ok = wait(rows_full + 8 * rows.at, rows.full()) && wait(s_full + 8 * t.at, t.full());
+            for (int c = rank; c < w.chunks; c += split) {
+                if (static_cast<int>(t.at) == place && ok) {
+                    ok = wait(rows_full + 8 * rows.at, rows.full(), 20) && wait(s_full + 8 * t.at, t.full(), 20);
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     tc_fence_after_sync();
                     if (ok) {
@@ -455,8 +536,8 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
                         const bool plain = i0 + P.per <= w.r.n && w.tok0 + kUnit - 1 <= pos_lo && (w.tok0 > pos_hi - window || w.tok0 + kUnit <= a.sinks);
                         const float* data = reinterpret_cast<const float*>(smem + S::kRowData) + rows.at * 3 * kCols;
                         const uint32_t ts = tmem + t.at * (NG * kCols) + lanes;
-                        if (plain) sum = chunk_sum<D, false>(sum, ts, d, P.w.scale_log2, data, cols, tok, window, a.sinks);
-                        else sum = chunk_sum<D, true>(sum, ts, d, P.w.scale_log2, data, cols, tok, window, a.sinks);
+                        if (plain) sum = chunk_sum<D, false>(sum, ts, d, P.w.scale_log2, data, c0, c1, tok, window, a.sinks);
+                        else sum = chunk_sum<D, true>(sum, ts, d, P.w.scale_log2, data, c0, c1, tok, window, a.sinks);
                     }
                     tc_fence_before_sync();
                     __syncwarp();
@@ -470,20 +551,41 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
             }
             if (!ok) *abort = 1u;
             const float2 both = apart(sum);
-            const float mine = ok ? both.x + both.y : __int_as_float(0x7FFFFFFF);
-            // the second warps' sums: two places in turn, so that one barrier a unit is enough
-            if (second) half[(n & 1) * kUnit + token] = mine;
-            asm volatile("bar.sync 1, 256;" ::: "memory");
-            if (!second && to >= 0) a.out[to] = before + (mine + half[(n & 1) * kUnit + token]);
+            // a token's four sums: two places in turn, so that one barrier a unit is enough; the
+            // order does not depend on which place of S the unit's first chunk had
+            float* part = parts + (n & 1) * 4 * kUnit + token;
+            part[mine * kUnit] = ok ? both.x + both.y : __int_as_float(0x7FFFFFFF);
+            asm volatile("bar.sync 1, %0;" :: "n"(kSumWarps * 32) : "memory");
+            if (mine != 0) continue;
+            float all = (part[0] + part[2 * kUnit]) + (part[kUnit] + part[3 * kUnit]);
+            if (split > 1) {
+                // the second block's goes to the first, in two places in turn
+                const uint32_t at = n & 1u, turn = n >> 1;
+                const uint32_t slot = base + S::kOther + (at * kUnit + token) * 4;
+                if (rank == 1) {
+                    if (turn > 0 && ok) ok = __all_sync(0xFFFFFFFFu, wait_cluster(x_empty + 8 * at, (turn - 1) & 1u, limit, abort));
+                    store_to_block(slot, 0, ok ? all : __int_as_float(0x7FFFFFFF));
+                    __syncwarp();
+                    if (lane == 0) arrive_at_block(x_full + 8 * at, 0);
+                } else {
+                    if (ok) ok = __all_sync(0xFFFFFFFFu, wait_cluster(x_full + 8 * at, turn & 1u, limit, abort));
+                    all = ok ? all + *reinterpret_cast<const float*>(smem + S::kOther + (at * kUnit + token) * 4) : __int_as_float(0x7FFFFFFF);
+                    __syncwarp();
+                    if (lane == 0) arrive_at_block(x_empty + 8 * at, 1);
+                }
+                if (!ok) *abort = 1u;
+            }
+            if (rank == 0 && to >= 0) a.out[to] = before + all;
         }
     }
     // ------------------------------------------------------------ teardown --
     tc_fence_before_sync();
     __syncthreads();
-    if (warp == 15) {
+    if (warp == kThreads / 32 - 1) {
         tc_fence_after_sync();
         tmem_dealloc(tmem, S::kTmemCols);
     }
+    if (split > 1) cluster_sync();             // no block leaves while the other may still write to it
 }
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
@@ -516,8 +618,21 @@ cudaError_t launch(const WeighParams& W, int num_sms, cudaStream_t s) {
         return cudaErrorInvalidValue;
     static std::atomic<uint64_t> smem_set{0};
     if (cudaError_t e = set_smem_limit_once(weigh_tc_kernel<D>, S::kBytes, smem_set); e != cudaSuccess) return e;
-    weigh_tc_kernel<D><<<num_sms, kThreads, S::kBytes, s>>>(P);
-    return cudaGetLastError();
+    // two blocks to a unit where each has some chunks of it
+    const int64_t rows = static_cast<int64_t>(W.a.max_queries) * W.group;
+    P.split = rows >= 8 * S::kCols && num_sms > 1 ? 2 : 1;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(num_sms / P.split * P.split);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = S::kBytes;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = P.split;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, weigh_tc_kernel<D>, P);
 }
 
 }  // namespace
