@@ -33,7 +33,8 @@ namespace pn {
 namespace {
 
 constexpr int kSumWarps = 16;                  // two places of S, two halves of the columns, four quarters of the tokens
-constexpr int kThreads = (kSumWarps + 8) * 32; // 80 registers each
+constexpr int kThreads = (kSumWarps + 9) * 32; // 80 registers each
+constexpr int kList = 32;                      // units looked up at a time
 constexpr int kUnit = 128;                     // tokens of a unit, MMA M
 constexpr int kPlaces = 2;                     // of S in tensor memory
 constexpr int kRowStages = 4;                  // of the rows' constants
@@ -62,10 +63,11 @@ struct Shape {
     static constexpr int kRowData = kScales + kABufs * kGroups * kUnit * 4;    // [stage][less, share, pos][column]
     static constexpr int kParts = kRowData + kRowStages * 3 * kCols * 4;    // [2][4][token] parts of the sums
     static constexpr int kOther = kParts + 2 * 4 * kUnit * 4;               // [2][token] sums of the cluster's second block (in the first)
-    static constexpr int kScan = kOther + 2 * kUnit * 4;                   // [threads + 1] units before each thread's requests
+    static constexpr int kUnits = kOther + 2 * kUnit * 4;                  // [2][32] units
+    static constexpr int kScan = kUnits + 2 * kList * 80;                  // [threads + 1] units before each thread's requests
     static constexpr int kWarpSums = kScan + (kThreads + 1) * 8;
     static constexpr int kBars = kWarpSums + kThreads / 32 * 8;
-    static constexpr int kNumBars = 2 * kQStages + 3 * kABufs + 2 * kPlaces + 2 * kRowStages + 1 + 4;
+    static constexpr int kNumBars = 2 * kQStages + 3 * kABufs + 2 * kPlaces + 2 * kRowStages + 1 + 4 + 4;
     static constexpr int kMisc = kBars + kNumBars * 8;                     // TMEM base, abort
     static constexpr int kBytes = kMisc + 16 + 1024;                       // slack to align to 1024 bytes
     static_assert(kBytes <= 227 * 1024, "fits one SM's shared memory");
@@ -145,43 +147,51 @@ __device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
     return d;
 }
 
-// A block's units, and the chunks of query rows that see any of a unit's tokens.  A
-// request's units are numbered tile by tile, all heads of a tile after each other: in
-// a prompt a tile costs no more than the one before.  Blocks take units in turns, in
-// every second one in reverse order, so the dear ones and the cheap ones of a prompt
-// are shared out evenly (in plain turns, head by head, the busiest SM had 1.5 times
-// the average: 4096 queries of 32 + 8 heads of 128 over 8192 tokens took 422 us).
-struct Work {
-    uint64_t total, turn;
-    WeighRequest r;
+// A unit: the chunks of query rows that see any of its tokens, and the pages of its
+// records (-1: none).  b < 0: there is no further one.
+struct alignas(16) Unit {
     int b, h, tok0;
-    int c0, chunks;            // first chunk, how many
-    uint32_t team, teams;      // blocks that share units, and which they are
-    __device__ __forceinline__ uint64_t unit() const { return turn * teams + (turn & 1u ? teams - 1 - team : team); }
-    __device__ __forceinline__ bool any() const { return unit() < total; }
-    __device__ __forceinline__ void find(const Params& P, const uint64_t* scan, int each) {
-        const uint64_t u = unit();
-        if (u >= total) return;
-        int of_head;
-        locate<kUnit, kThreads>(P.w, scan, each, u, r, b, h, of_head);
-        // (its number among the request's units, tile by tile)
-        const uint64_t index = static_cast<uint64_t>(h) * units_of<kUnit>(r) + of_head;
-        const uint64_t tile = index / static_cast<uint64_t>(P.w.cache.heads);
-        h = static_cast<int>(index - tile * P.w.cache.heads);
-        tok0 = static_cast<int>(tile) * kUnit;
-        const WeighArgs& a = P.w.a;
-        const int i0 = max(tok0 - r.pos0, 0), last = min(tok0 + kUnit, r.len) - 1;
-        int i1 = r.n;
-        if (a.window && tok0 >= a.sinks)
-            i1 = static_cast<int>(min(static_cast<int64_t>(i1), max(static_cast<int64_t>(last) + a.window - r.pos0, static_cast<int64_t>(0))));
-        c0 = i0 / P.per;
-        chunks = i0 < i1 ? (i1 + P.per - 1) / P.per - c0 : 0;
-    }
-    __device__ __forceinline__ void next(const Params& P, const uint64_t* scan, int each) {
-        ++turn;
-        find(P, scan, each);
-    }
+    int q0, n, pos0, len;
+    int c0, chunks;
+    int page[kUnit / kKvTokens];
+    int unused[3];
 };
+static_assert(sizeof(Unit) == 80, "the list's place in shared memory");
+
+// A request's units are numbered tile by tile, all heads of a tile after each other: in
+// a prompt a tile costs no more than the one before.  Teams of blocks (of one or two)
+// take units in turns, in every second one in reverse order, so the dear ones and the
+// cheap ones of a prompt are shared out evenly (in plain turns, head by head, the
+// busiest SM had 1.5 times the average).
+__device__ __forceinline__ uint64_t unit_of_turn(uint64_t turn, uint32_t team, uint32_t teams) { return turn * teams + (turn & 1u ? teams - 1 - team : team); }
+
+__device__ __noinline__ void look_up(const Params& P, const uint64_t* scan, int each, uint64_t u, Unit* to) {
+    const WeighArgs& a = P.w.a;
+    const KvCache& cache = P.w.cache;
+    WeighRequest r;
+    Unit w{};
+    int of_head;
+    locate<kUnit, kThreads>(P.w, scan, each, u, r, w.b, w.h, of_head);
+    // (its number among the request's units, tile by tile)
+    const uint64_t index = static_cast<uint64_t>(w.h) * units_of<kUnit>(r) + of_head;
+    const uint64_t tile = index / static_cast<uint64_t>(cache.heads);
+    w.h = static_cast<int>(index - tile * cache.heads);
+    w.tok0 = static_cast<int>(tile) * kUnit;
+    w.q0 = r.q0; w.n = r.n; w.pos0 = r.pos0; w.len = r.len;
+    const int i0 = max(w.tok0 - r.pos0, 0), last = min(w.tok0 + kUnit, r.len) - 1;
+    int i1 = r.n;
+    if (a.window && w.tok0 >= a.sinks)
+        i1 = static_cast<int>(min(static_cast<int64_t>(i1), max(static_cast<int64_t>(last) + a.window - r.pos0, static_cast<int64_t>(0))));
+    w.c0 = i0 / P.per;
+    w.chunks = i0 < i1 ? (i1 + P.per - 1) / P.per - w.c0 : 0;
+#pragma unroll
+    for (int i = 0; i < kUnit / kKvTokens; ++i) {
+        const int tok = w.tok0 + i * kKvTokens;
+        const int page = tok < r.len ? a.table[w.b * a.table_stride + (tok >> cache.page_shift)] : -1;
+        w.page[i] = page >= 0 && page < cache.pages ? page : -1;
+    }
+    *to = w;
+}
 
 // A place in a ring and how often it went round.
 template <int N>
@@ -252,6 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
     auto take = [&](int n) { const uint32_t b = bar; bar += 8u * n; return b; };
     const uint32_t q_full = take(kQStages), q_empty = take(kQStages), a_full = take(kABufs), a_empty = take(kABufs), d_empty = take(kABufs);
     const uint32_t s_full = take(kPlaces), s_empty = take(kPlaces), rows_full = take(kRowStages), rows_empty = take(kRowStages), drain = take(1);
+    const uint32_t list_full = take(2), list_empty = take(2);
     const uint32_t x_full = take(2), x_empty = take(2);        // of the second block's sums: in the first block, in the second
     volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + S::kMisc);
     volatile uint32_t* abort = misc + 1;
@@ -281,6 +292,8 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
         }
         mbar_init(drain, 1);
         for (int s = 0; s < 2; ++s) {
+            mbar_init(list_full + 8 * s, 1);
+            mbar_init(list_empty + 8 * s, kSumWarps + kDecodeWarps + 4);       // of every warp but the list's
             mbar_init(x_full + 8 * s, 4);
             mbar_init(x_empty + 8 * s, 4);
         }
@@ -303,21 +316,44 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
     // nap: of the warps that work ahead, whose polling would take the others' issue slots
     auto wait = [&](uint32_t b, uint32_t parity, uint32_t nap = 0) { return mbar_try_wait(b, parity) || wait_phase(b, parity, limit, abort, nap); };
     const int split = P.split, rank = static_cast<int>(blockIdx.x) % split;    // the block's chunks: rank, rank + split, ...
-    Work w;
-    w.turn = 0;
-    w.team = blockIdx.x / split;
-    w.teams = gridDim.x / split;
-    w.total = scan[kThreads];
-    w.find(P, scan, each);
+    Unit* list = reinterpret_cast<Unit*>(smem + S::kUnits);
+    // The team's unit of a turn, from the list; false behind the last one (or where a wait gave up).
+    auto unit_at = [&](uint32_t turn, const Unit*& w, bool& ok) {
+        const uint32_t half = (turn / kList) & 1u;
+        if (turn % kList == 0) ok = ok && wait(list_full + 8 * half, (turn / (2 * kList)) & 1u);
+        w = list + half * kList + turn % kList;
+        return ok && w->b >= 0;
+    };
+    auto done_with = [&](uint32_t turn) {      // by one thread of each warp
+        if (turn % kList == kList - 1) mbar_arrive(list_empty + 8 * ((turn / kList) & 1u));
+    };
 
-    if (warp == kSumWarps + 4) {
+    if (warp == kSumWarps + 8) {
+        // ------------------------------------------------------ unit list --
+        // a lane to a unit: found one by one in every role, a unit took each of them some
+        // thousand cycles (24 requests with 64 rows of 128 over 4096 tokens: 180 us)
+        const uint64_t total = scan[kThreads];
+        const uint32_t team = blockIdx.x / split, teams = gridDim.x / split;
+        for (uint32_t first = 0;; first += kList) {
+            const uint32_t half = (first / kList) & 1u;
+            if (first >= 2 * kList && !__all_sync(0xFFFFFFFFu, wait(list_empty + 8 * half, (first / (2 * kList) - 1) & 1u, kNap))) break;
+            const uint64_t u = unit_of_turn(static_cast<uint64_t>(first) + lane, team, teams);
+            Unit* to = list + half * kList + lane;
+            if (u < total) look_up(P, scan, each, u, to);
+            else to->b = -1;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(list_full + 8 * half);
+            if (!__all_sync(0xFFFFFFFFu, u < total)) break;
+        }
+    } else if (warp == kSumWarps + 4) {
         // ------------------------------------------------------- queries --
         if (lane == 0) {
             Ring<kQStages> q;
             bool ok = true, stalled = false;
             uint32_t issued = 0;
-            for (; ok && w.any(); w.next(P, scan, each))
-                for (int c = rank; c < w.chunks; c += split) {
+            const Unit* w;
+            for (uint32_t turn = 0; unit_at(turn, w, ok); ++turn) {
+                for (int c = rank; c < w->chunks; c += split) {
                     if (q.turn > 0 && !wait(q_empty + 8 * q.at, q.emptied(), kNap)) {
                         ok = false;
                         break;
@@ -332,10 +368,13 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
                         break;
                     }
 #pragma unroll
-                    for (int j = 0; j < NG; ++j) tma_load_3d(dst + j * kCols * 128, &P.qmap, 64 * j, w.h * group, w.r.q0 + (w.c0 + c) * P.per, full);
+                    for (int j = 0; j < NG; ++j) tma_load_3d(dst + j * kCols * 128, &P.qmap, 64 * j, w->h * group, w->q0 + (w->c0 + c) * P.per, full);
                     ++issued;
                     q.step();
                 }
+                if (!ok) break;
+                done_with(turn);
+            }
             if (!ok && !stalled) *abort = 1u;
             // the last copies into the stages land before the block ends, also after an abort
             for (uint32_t s = 0; s < kQStages && s < issued; ++s) wait_phase(q_full + 8 * s, ((issued - 1 - s) / kQStages) & 1u, kAttnDrainNs, nullptr);
@@ -353,19 +392,20 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
             of_head[k] = lane + 32 * k - of_token[k] * group;
         }
         bool ok = true;
-        for (; ok && w.any(); w.next(P, scan, each)) {
+        const Unit* w;
+        for (uint32_t turn = 0; unit_at(turn, w, ok); ++turn) {
             float lse[kEach];
             auto fetch = [&](int c) {          // of the unit's chunk c; any of the request's where there is no such row
 #pragma unroll
                 for (int k = 0; k < kEach; ++k) {
-                    const int i = min((w.c0 + c) * P.per + of_token[k], w.r.n - 1);
-                    lse[k] = a.lse[(static_cast<int64_t>(w.r.q0) + i) * a.heads + w.h * group + of_head[k]];
+                    const int i = min((w->c0 + c) * P.per + of_token[k], w->n - 1);
+                    lse[k] = a.lse[(static_cast<int64_t>(w->q0) + i) * a.heads + w->h * group + of_head[k]];
                 }
             };
             // the two warps take the block's chunks in turn
             const int mine = rank + (((s.at & 1u) != 0) != (warp == kSumWarps + 7) ? split : 0);
-            if (mine < w.chunks) fetch(mine);
-            for (int c = rank; c < w.chunks; c += split) {
+            if (mine < w->chunks) fetch(mine);
+            for (int c = rank; c < w->chunks; c += split) {
                 if (((s.at & 1u) != 0) != (warp == kSumWarps + 7)) {
                     s.step();
                     continue;
@@ -373,7 +413,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
                 float now[kEach];
 #pragma unroll
                 for (int k = 0; k < kEach; ++k) now[k] = lse[k];
-                if (c + 2 * split < w.chunks) fetch(c + 2 * split);
+                if (c + 2 * split < w->chunks) fetch(c + 2 * split);
                 if (s.turn > 0 && !__all_sync(0xFFFFFFFFu, wait(rows_empty + 8 * s.at, s.emptied(), kNap))) {
                     ok = false;
                     break;
@@ -381,17 +421,20 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
                 float* to = reinterpret_cast<float*>(smem + S::kRowData) + s.at * 3 * kCols;
 #pragma unroll
                 for (int k = 0; k < kEach; ++k) {
-                    const int row = lane + 32 * k, i = (w.c0 + c) * P.per + of_token[k];
-                    const bool real = of_token[k] < P.per && i < w.r.n;
+                    const int row = lane + 32 * k, i = (w->c0 + c) * P.per + of_token[k];
+                    const bool real = of_token[k] < P.per && i < w->n;
                     const LogSum l = log_sum_of(real ? now[k] : -INFINITY, P.w.scale_rest);
                     to[row] = l.less;
                     to[kCols + row] = l.factor;
-                    reinterpret_cast<int*>(to)[2 * kCols + row] = real ? w.r.pos0 + i : INT32_MIN;
+                    reinterpret_cast<int*>(to)[2 * kCols + row] = real ? w->pos0 + i : INT32_MIN;
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(rows_full + 8 * s.at);
                 s.step();
             }
+            if (!ok) break;
+            __syncwarp();
+            if (lane == 0) done_with(turn);
         }
         if (!ok) *abort = 1u;
     } else if (warp == kSumWarps + 6) {
@@ -401,10 +444,12 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
             Ring<kABufs> k;
             Ring<kPlaces> t;
             bool ok = true;
-            for (; ok && w.any(); w.next(P, scan, each)) {
-                ok = wait(a_full + 8 * k.at, k.full());
+            const Unit* w;
+            for (uint32_t turn = 0; unit_at(turn, w, ok); ++turn) {
+                ok = wait(a_full + 8 * k.at, k.full(), 20);
                 if (!ok) break;
-                for (int c = rank; c < w.chunks; c += split) {
+                const int chunks = w->chunks;
+                for (int c = rank; c < chunks; c += split) {
                     ok = (t.turn == 0 || wait(s_empty + 8 * t.at, t.emptied(), 20)) && wait(q_full + 8 * q.at, q.full(), 20);
                     if (!ok) break;
                     tc_fence_after_sync();
@@ -422,6 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
                 if (!ok) break;
                 mma_commit(a_empty + 8 * k.at);
                 k.step();
+                done_with(turn);
             }
             if (!ok) *abort = 1u;
             mma_commit(drain);                 // every product of this block finished (also after an abort)
@@ -434,40 +480,56 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
         const int g = lane >> 2, t = lane & 3;
         Ring<kABufs> k;
         bool ok = true;
-        for (; w.any(); w.next(P, scan, each)) {
-            // the warp's records are read before the buffer is waited for
-            uint32_t kw[kRecords][2][D / 32];
+        // a unit's words are on their way while the one before is decoded, as registers allow
+        constexpr bool kAhead = D < 256;
+        struct Words {
+            uint32_t k[kRecords][2][D / 32];
             float scale[kRecords][2];          // of tokens lane % 8 and 8 more, group lane / 8
+        };
+        auto load = [&](const Unit& w, Words& to) {
 #pragma unroll
             for (int i = 0; i < kRecords; ++i) {
-                const int tok = w.tok0 + ((warp - kSumWarps) + i * kDecodeWarps) * kKvTokens;
-                const uint8_t* record = nullptr;
-                if (tok < w.r.len) {
-                    const int page = a.table[w.b * a.table_stride + (tok >> cache.page_shift)];
-                    if (page >= 0 && page < cache.pages) record = cache.record((static_cast<int64_t>(page) << cache.page_shift) + (tok & (cache.page_size - 1)), w.h);
-                }
+                const int rec = (warp - kSumWarps) + i * kDecodeWarps, page = w.page[rec];
+                const uint8_t* record = page < 0 ? nullptr :
+                    cache.record((static_cast<int64_t>(page) << cache.page_shift) + ((w.tok0 + rec * kKvTokens) & (cache.page_size - 1)), w.h);
 #pragma unroll
                 for (int hh = 0; hh < 2; ++hh) {
 #pragma unroll
-                    for (int q = 0; q < D / 32; ++q) kw[i][hh][q] = 0x88888888u;        // (zero)
-                    scale[i][hh] = 0.0f;
+                    for (int q = 0; q < D / 32; ++q) to.k[i][hh][q] = 0x88888888u;      // (zero)
+                    to.scale[i][hh] = 0.0f;
                     if (!record) continue;
 #pragma unroll
                     for (int pl = 0; pl < PL; ++pl) {
                         const uint8_t* p = record + ((hh * PL + pl) * 32 + lane) * 8 * GP;
                         if constexpr (GP == 2) {
                             const uint4 v = *reinterpret_cast<const uint4*>(p);
-                            kw[i][hh][4 * pl] = v.x; kw[i][hh][4 * pl + 1] = v.y; kw[i][hh][4 * pl + 2] = v.z; kw[i][hh][4 * pl + 3] = v.w;
+                            to.k[i][hh][4 * pl] = v.x; to.k[i][hh][4 * pl + 1] = v.y; to.k[i][hh][4 * pl + 2] = v.z; to.k[i][hh][4 * pl + 3] = v.w;
                         } else {
                             const uint2 v = *reinterpret_cast<const uint2*>(p);
-                            kw[i][hh][0] = v.x; kw[i][hh][1] = v.y;
+                            to.k[i][hh][0] = v.x; to.k[i][hh][1] = v.y;
                         }
                     }
-                    if ((lane >> 3) < NG) scale[i][hh] = __half2float(*reinterpret_cast<const __half*>(record + kv_k_scales(D) + ((hh * 8 + (lane & 7)) * NG + (lane >> 3)) * 2));
+                    if ((lane >> 3) < NG) to.scale[i][hh] = __half2float(*reinterpret_cast<const __half*>(record + kv_k_scales(D) + ((hh * 8 + (lane & 7)) * NG + (lane >> 3)) * 2));
                 }
             }
+        };
+        const Unit* w;
+        Words now, next;
+        bool more = unit_at(0, w, ok);
+        if (kAhead && more) load(*w, next);
+        for (uint32_t turn = 0; more; ++turn) {
+            if constexpr (kAhead) now = next;
+            else load(*w, now);
+            __syncwarp();
+            if (lane == 0) done_with(turn);    // its entry is not looked at again
+            more = unit_at(turn + 1, w, ok);
+            more = __all_sync(0xFFFFFFFFu, more);
+            if (kAhead && more) load(*w, next);
             if (k.turn > 0) ok = ok && wait(a_empty + 8 * k.at, k.emptied(), kNap) && wait(d_empty + 8 * k.at, k.emptied(), kNap);
-            if (!__all_sync(0xFFFFFFFFu, ok)) break;
+            if (!__all_sync(0xFFFFFFFFu, ok)) {
+                ok = false;
+                break;
+            }
             uint8_t* tile = smem + S::kA + k.at * S::kABytes;
             float* d = reinterpret_cast<float*>(smem + S::kScales) + k.at * NG * kUnit;
             auto put = [&](int token, int j, int i, uint32_t word) {   // 16-byte chunk `i` of a token's row in a group's tile
@@ -482,10 +544,10 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
                 for (int hh = 0; hh < 2; ++hh) {
 #pragma unroll
                     for (int j = 0; j < NG; ++j) {
-                        put(first + hh * 8 + g, j, 2 * t, kw[i][hh][2 * j]);
-                        put(first + hh * 8 + g, j, 2 * t + 1, kw[i][hh][2 * j + 1]);
+                        put(first + hh * 8 + g, j, 2 * t, now.k[i][hh][2 * j]);
+                        put(first + hh * 8 + g, j, 2 * t + 1, now.k[i][hh][2 * j + 1]);
                     }
-                    if ((lane >> 3) < NG) d[(lane >> 3) * kUnit + first + hh * 8 + (lane & 7)] = scale[i][hh];
+                    if ((lane >> 3) < NG) d[(lane >> 3) * kUnit + first + hh * 8 + (lane & 7)] = now.scale[i][hh];
                 }
             }
             fence_proxy_async_smem();
@@ -504,17 +566,22 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
         Ring<kABufs> k;
         Ring<kPlaces> t;
         Ring<kRowStages> rows;
-        bool ok = true;
-        for (uint32_t n = 0; w.any(); w.next(P, scan, each), ++n) {
+        bool ok = true, listed = true;         // listed: the units can be told, whatever else has given up
+        const Unit* unit;
+        uint32_t n = 0;
+        for (; __all_sync(0xFFFFFFFFu, unit_at(n, unit, listed)); ++n) {
+            const Unit w = *unit;
             const int tok = w.tok0 + token;
             // where the token's weight is, and what it was
             int64_t to = -1;
             float before = 0.0f;
-            if (tok < w.r.len) {
-                const int page = a.table[w.b * a.table_stride + (tok >> cache.page_shift)];
-                if (page >= 0 && page < cache.pages) to = ((static_cast<int64_t>(page) * cache.heads + w.h) << cache.page_shift) + (tok & (cache.page_size - 1));
+            if (tok < w.len) {
+                const int page = unit->page[token / kKvTokens];
+                if (page >= 0) to = ((static_cast<int64_t>(page) * cache.heads + w.h) << cache.page_shift) + (tok & (cache.page_size - 1));
             }
-            if (mine == 0 && to >= 0 && a.weights && tok < w.r.pos0) before = a.decay * a.weights[to];
+            __syncwarp();
+            if (lane == 0) done_with(n);
+            if (mine == 0 && to >= 0 && a.weights && tok < w.pos0) before = a.decay * a.weights[to];
             ok = ok && __all_sync(0xFFFFFFFFu, wait(a_full + 8 * k.at, k.full()));
             Two d[NG];
 #pragma unroll
@@ -532,8 +599,8 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
                     ok = __all_sync(0xFFFFFFFFu, ok);
                     tc_fence_after_sync();
                     if (ok) {
-                        const int i0 = (w.c0 + c) * P.per, pos_lo = w.r.pos0 + i0, pos_hi = pos_lo + P.per - 1;
-                        const bool plain = i0 + P.per <= w.r.n && w.tok0 + kUnit - 1 <= pos_lo && (w.tok0 > pos_hi - window || w.tok0 + kUnit <= a.sinks);
+                        const int i0 = (w.c0 + c) * P.per, pos_lo = w.pos0 + i0, pos_hi = pos_lo + P.per - 1;
+                        const bool plain = i0 + P.per <= w.n && w.tok0 + kUnit - 1 <= pos_lo && (w.tok0 > pos_hi - window || w.tok0 + kUnit <= a.sinks);
                         const float* data = reinterpret_cast<const float*>(smem + S::kRowData) + rows.at * 3 * kCols;
                         const uint32_t ts = tmem + t.at * (NG * kCols) + lanes;
                         if (plain) sum = chunk_sum<D, false>(sum, ts, d, P.w.scale_log2, data, c0, c1, tok, window, a.sinks);
@@ -577,6 +644,15 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
             }
             if (rank == 0 && to >= 0) a.out[to] = before + all;
         }
+        // where the list gave up: NaN for the units behind
+        if (!__all_sync(0xFFFFFFFFu, listed) && mine == 0 && rank == 0)
+            for (; unit_of_turn(n, blockIdx.x / split, gridDim.x / split) < scan[kThreads]; ++n) {
+                Unit w;
+                look_up(P, scan, each, unit_of_turn(n, blockIdx.x / split, gridDim.x / split), &w);
+                const int tok = w.tok0 + token, page = w.page[token / kKvTokens];
+                if (tok < w.len && page >= 0)
+                    a.out[((static_cast<int64_t>(page) * cache.heads + w.h) << cache.page_shift) + (tok & (cache.page_size - 1))] = __int_as_float(0x7FFFFFFF);
+            }
     }
     // ------------------------------------------------------------ teardown --
     tc_fence_before_sync();
