@@ -822,7 +822,7 @@ pn_status pn_kv_weigh(const uint16_t* q, int64_t q_stride, int64_t tokens, int h
     if (major < 10) return PN_EUNSUPPORTED;
     const int room = max_pages * page_size;            // as in pn_attention
     const pn::WeighArgs a{reinterpret_cast<const __half*>(q), q_stride, tokens, heads, table, table_stride, max_pages, lens, starts, batch,
-                          max_queries, lse, scale, window < room ? window : 0, sinks < room ? sinks : room, weights, decay, out};
+                          max_queries, lse, scale, window < room ? window : 0, sinks < room ? sinks : room, decay > 0.0f ? weights : nullptr, decay, out};
     const pn::KvGeometry g{static_cast<uint8_t*>(const_cast<void*>(cache)), pages, page_size, kv_heads, head_dim};
     const cudaError_t e = pn::launch_weigh(a, g, sms, g_timeout_ns.load(), g_test_stall.load(), reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PN_OK : pn::cuda_error(e);

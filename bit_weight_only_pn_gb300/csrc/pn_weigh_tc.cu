@@ -448,17 +448,18 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
             for (uint32_t turn = 0; unit_at(turn, w, ok); ++turn) {
                 ok = wait(a_full + 8 * k.at, k.full(), 20);
                 if (!ok) break;
-                const int chunks = w->chunks;
+                const int chunks = w->chunks, n = w->n, first = w->c0;
                 for (int c = rank; c < chunks; c += split) {
                     ok = (t.turn == 0 || wait(s_empty + 8 * t.at, t.emptied(), 20)) && wait(q_full + 8 * q.at, q.full(), 20);
                     if (!ok) break;
                     tc_fence_after_sync();
+                    const uint32_t desc = desc_of((min(P.per, n - (first + c) * P.per) * group + 15) / 16 * 16);
                     const uint32_t ka = base + S::kA + k.at * S::kABytes, qa = base + S::kQ + q.at * S::kQBytes, d = tmem + t.at * (NG * kCols);
 #pragma unroll
                     for (int j = 0; j < NG; ++j)
 #pragma unroll
                         for (int kk = 0; kk < 4; ++kk)
-                            mma_ss(d + kCols * j, smem_desc_sw128(ka + j * (kUnit * 128) + kk * 32), smem_desc_sw128(qa + j * (kCols * 128) + kk * 32), desc_of(kCols), kk != 0);
+                            mma_ss(d + kCols * j, smem_desc_sw128(ka + j * (kUnit * 128) + kk * 32), smem_desc_sw128(qa + j * (kCols * 128) + kk * 32), desc, kk != 0);
                     mma_commit(q_empty + 8 * q.at);
                     mma_commit(s_full + 8 * t.at);
                     q.step();
@@ -484,7 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
         constexpr bool kAhead = D < 256;
         struct Words {
             uint32_t k[kRecords][2][D / 32];
-            float scale[kRecords][2];          // of tokens lane % 8 and 8 more, group lane / 8
+            uint16_t scale[kRecords][2];       // fp16 bits, of tokens lane % 8 and 8 more, group lane / 8
         };
         auto load = [&](const Unit& w, Words& to) {
 #pragma unroll
@@ -496,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
                 for (int hh = 0; hh < 2; ++hh) {
 #pragma unroll
                     for (int q = 0; q < D / 32; ++q) to.k[i][hh][q] = 0x88888888u;      // (zero)
-                    to.scale[i][hh] = 0.0f;
+                    to.scale[i][hh] = 0;
                     if (!record) continue;
 #pragma unroll
                     for (int pl = 0; pl < PL; ++pl) {
@@ -509,7 +510,8 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
                             to.k[i][hh][0] = v.x; to.k[i][hh][1] = v.y;
                         }
                     }
-                    if ((lane >> 3) < NG) to.scale[i][hh] = __half2float(*reinterpret_cast<const __half*>(record + kv_k_scales(D) + ((hh * 8 + (lane & 7)) * NG + (lane >> 3)) * 2));
+                    // (converted later: a value made of a load under a branch waits for it there)
+                    to.scale[i][hh] = *reinterpret_cast<const uint16_t*>(record + kv_k_scales(D) + ((hh * 8 + (lane & 7)) * NG + min(lane >> 3, NG - 1)) * 2);
                 }
             }
         };
@@ -547,7 +549,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
                         put(first + hh * 8 + g, j, 2 * t, now.k[i][hh][2 * j]);
                         put(first + hh * 8 + g, j, 2 * t + 1, now.k[i][hh][2 * j + 1]);
                     }
-                    if ((lane >> 3) < NG) d[(lane >> 3) * kUnit + first + hh * 8 + (lane & 7)] = now.scale[i][hh];
+                    if ((lane >> 3) < NG) d[(lane >> 3) * kUnit + first + hh * 8 + (lane & 7)] = half_bits_to_float(now.scale[i][hh]);
                 }
             }
             fence_proxy_async_smem();
@@ -561,8 +563,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
         const int mine = warp >> 2, place = mine & 1, token = threadIdx.x & (kUnit - 1);
         const uint32_t lanes = static_cast<uint32_t>((warp & 3) * 32) << 16;
         float* parts = reinterpret_cast<float*>(smem + S::kParts);
-        const int window = a.window ? a.window : INT32_MAX, cols = (P.per * group + 15) / 16 * 16, cut = (cols / 2 + 15) / 16 * 16;
-        const int c0 = mine >> 1 ? cut : 0, c1 = mine >> 1 ? cols : cut;       // the warp's columns
+        const int window = a.window ? a.window : INT32_MAX;
         Ring<kABufs> k;
         Ring<kPlaces> t;
         Ring<kRowStages> rows;
@@ -600,7 +601,10 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
                     tc_fence_after_sync();
                     if (ok) {
                         const int i0 = (w.c0 + c) * P.per, pos_lo = w.pos0 + i0, pos_hi = pos_lo + P.per - 1;
-                        const bool plain = i0 + P.per <= w.n && w.tok0 + kUnit - 1 <= pos_lo && (w.tok0 > pos_hi - window || w.tok0 + kUnit <= a.sinks);
+                        // columns with rows; whether all of them are the request's (others may hold anything)
+                        const int real = min(P.per, w.n - i0) * group, end = (real + 15) / 16 * 16;
+                        const bool plain = (i0 + P.per <= w.n || real == end) && w.tok0 + kUnit - 1 <= pos_lo && (w.tok0 > pos_hi - window || w.tok0 + kUnit <= a.sinks);
+                        const int cut = (end / 2 + 15) / 16 * 16, c0 = mine >> 1 ? cut : 0, c1 = mine >> 1 ? end : cut;        // the warp's columns
                         const float* data = reinterpret_cast<const float*>(smem + S::kRowData) + rows.at * 3 * kCols;
                         const uint32_t ts = tmem + t.at * (NG * kCols) + lanes;
                         if (plain) sum = chunk_sum<D, false>(sum, ts, d, P.w.scale_log2, data, c0, c1, tok, window, a.sinks);
@@ -713,9 +717,18 @@ cudaError_t launch(const WeighParams& W, int num_sms, cudaStream_t s) {
 
 }  // namespace
 
+// By the rows of a call, as if every request had max_queries queries: the other kernel
+// for more than 16 rows takes its tokens' codes through the products 8 or 16 rows at a
+// time, this one needs a unit's decoding and its waits whatever the rows are.
+// Microseconds there, here; 8 heads, 24 requests of 4096 cached tokens:
+//   of 64:  32 rows 48; 64 rows 69, 61; 128 rows 115, 74
+//   of 128: 32 rows 65; 64 rows 91, 70; 128 rows 153, 85
+//   of 256: 20 rows 145, 79; 64 rows 269, 81; 128 rows 489, 111
+// One request of 8192 with 64 rows of 128: 11, 15 (it looks at no lengths).
 bool weigh_tc_takes(const WeighArgs& a, const KvGeometry& g) {
     const int group = a.heads / g.heads, cols = g.D == 256 ? Shape<256>::kCols : Shape<128>::kCols;
-    return group <= cols && static_cast<int64_t>(a.max_queries) * group >= 64;
+    const int64_t rows = static_cast<int64_t>(a.max_queries) * group;
+    return group <= cols && rows >= (g.D == 64 ? 64 : g.D == 128 ? 48 : 9);
 }
 
 cudaError_t launch_weigh_tc(const WeighParams& P, int num_sms, cudaStream_t s) {
