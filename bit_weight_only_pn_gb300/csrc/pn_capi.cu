@@ -856,10 +856,13 @@ pn_status pn_kv_evict(void* cache, int64_t pages, int page_size, int kv_heads, i
                  {free_pages, static_cast<size_t>(ring_pages) * 4}, {table_out, rows_of(out_stride)}, {lens_out, nb}, {held_out, nb}, {ring_out, 16},
                  {kept, nb * kv_heads * budget}, {refused, 4}};
     if (shared(out, in)) return PN_EINVAL;
+    int sms = 0, major = 0;
+    if (pn_status st = device_info(&sms, &major); st != PN_OK) return st;
+    if (major < 9) return PN_EUNSUPPORTED;
     const pn::EvictArgs a{weights, table, table_stride, max_pages, lens, held, batch, limit, budget, sinks, recent, free_pages, ring_pages, ring,
                           table_out, out_stride, lens_out, held_out, ring_out, kept, refused};
     const pn::KvGeometry g{static_cast<uint8_t*>(cache), pages, page_size, kv_heads, head_dim};
-    const cudaError_t e = pn::launch_evict(a, g, reinterpret_cast<cudaStream_t>(stream));
+    const cudaError_t e = pn::launch_evict(a, g, sms, reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PN_OK : pn::cuda_error(e);
 }
 

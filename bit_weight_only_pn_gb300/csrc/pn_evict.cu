@@ -7,12 +7,15 @@
 // reads is written (new pages were free, the table is written to another one), so a
 // call can be repeated and no block waits for another.
 //
-// Two launches.  select: a block to a request and head finds the kept positions.
-// Weights as whole numbers in their order, found by three histograms of 11, 11 and
-// 10 bits, from the top: each fixes a digit of the last kept weight.  Then every warp
-// counts in its share what lies above that weight and what equals it, and writes the
-// positions behind those of the warps before.  move: a warp to a record of 16 new
-// tokens gathers their codes, scales and weights.
+// Two launches.  select: a block to a request and head finds the kept positions.  It
+// holds the upper 15 bits of the weights, as whole numbers in their order, in shared
+// memory (64 steps to a power of two); a histogram over their range gives the step with
+// the last kept weight, and the few weights of that step are ranked among themselves.
+// Then every warp counts in its share what is kept, and writes the positions behind
+// those of the warps before.  Where the step holds more than a thread to a weight (all
+// weights equal, say) or a request has more tokens than fit, histograms of 2048 bins fix
+// 11 bits of the last kept weight at a time, over weights read again each time.  move:
+// a warp to a record of 16 new tokens gathers their codes, scales and weights.
 #include <cstdint>
 
 #include <cuda_fp16.h>
@@ -28,7 +31,8 @@ namespace {
 constexpr int kSelectThreads = 512;
 constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kBins = 2048;
-constexpr int kMostKeys = 48 * 1024;           // of a block, kept in shared memory
+constexpr int kMostKeys = 96 * 1024;           // of a block, whose upper bits are kept in shared memory
+constexpr int kLowBits = 17;                   // the others
 constexpr int kMoveThreads = 256;
 constexpr int kMoveRecords = kMoveThreads / 32 * 2;    // of a block
 
@@ -36,7 +40,7 @@ struct Params {
     EvictArgs a;
     KvCache cache;
     int each;                  // pages of a request that was cut back
-    int keys;                  // places for keys in shared memory
+    int keys;                  // places for keys in shared memory (even)
 };
 
 __device__ __forceinline__ int64_t wrap(int64_t i, int64_t n) {
@@ -103,12 +107,62 @@ __device__ __forceinline__ uint32_t key_of(float w) {
     return w == w ? (u & 0x80000000u ? ~u : u | 0x80000000u) : 0u;
 }
 
+// The range of the block's numbers: low, high of each thread; free again behind it.
+__device__ __forceinline__ void block_range(uint32_t& low, uint32_t& high, uint32_t* part0, uint32_t* part1) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    low = __reduce_min_sync(0xFFFFFFFFu, low);
+    high = __reduce_max_sync(0xFFFFFFFFu, high);
+    if (lane == 0) {
+        part0[warp] = low;
+        part1[warp] = high;
+    }
+    __syncthreads();
+    low = __reduce_min_sync(0xFFFFFFFFu, part0[lane % kSelectWarps]);
+    high = __reduce_max_sync(0xFFFFFFFFu, part1[lane % kSelectWarps]);
+    __syncthreads();
+}
+
+// The bin, from the largest down, with the `left`-th count; left becomes its place in
+// the bin and, returned in `in_bin`, what the bin holds.  Bins are complete and
+// synchronised before; every thread gets the answer.
+__device__ __forceinline__ uint32_t bin_of(const uint32_t* bins, uint32_t& left, uint32_t& in_bin, uint32_t* part, uint32_t* found) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    constexpr int kEach = kBins / kSelectThreads;      // of a thread
+    const int top = kBins - 1 - static_cast<int>(threadIdx.x) * kEach;
+    uint32_t n[kEach], mine = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) mine += n[i] = bins[top - i];
+    uint32_t in = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, in, d);
+        if (lane >= d) in += o;
+    }
+    if (lane == 31) part[warp] = in;
+    __syncthreads();
+    uint32_t above = in - mine + __reduce_add_sync(0xFFFFFFFFu, lane < warp ? part[lane] : 0u);
+    if (above < left && left <= above + mine) {        // one thread's
+        int i = 0;
+        while (left > above + n[i]) above += n[i++];
+        found[0] = static_cast<uint32_t>(top - i);
+        found[1] = left - above;
+        found[2] = n[i];
+    }
+    __syncthreads();
+    left = found[1];
+    in_bin = found[2];
+    const uint32_t bin = found[0];
+    __syncthreads();
+    return bin;
+}
+
 __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_constant__ Params P) {
-    extern __shared__ uint32_t keys[];         // [P.keys]
+    extern __shared__ uint16_t upper[];        // [P.keys], kMark: kept among those of the last kept weight's step
     __shared__ uint32_t bins[kBins];
     __shared__ int64_t part[kSelectWarps];
     __shared__ uint32_t warp_above[kSelectWarps], warp_equal[kSelectWarps];
-    __shared__ uint32_t found[2];              // a digit, and how many of it are to be kept
+    __shared__ uint32_t found[3], candidates;
+    constexpr uint16_t kMark = 0xFFFF;
     const EvictArgs& a = P.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, heads = P.cache.heads;
     if (blockIdx.x == static_cast<unsigned>(a.batch) * heads) {
@@ -153,79 +207,119 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
     if (need == 0) return;
     auto weight_key = [&](int i) -> uint32_t {         // of position sinks + i
         const int tok = a.sinks + i, page = row[tok >> P.cache.page_shift];
-        if (page < 0 || page >= P.cache.pages) return 0u;
-        return key_of(__ldcg(a.weights + ((static_cast<int64_t>(page) * heads + h) << P.cache.page_shift) + (tok & (P.cache.page_size - 1))));
+        const bool there = page >= 0 && page < P.cache.pages;
+        // (loaded in any case: under a branch every load waits for the one before)
+        const float w = __ldcg(a.weights + ((static_cast<int64_t>(there ? page : 0) * heads + h) << P.cache.page_shift) + (tok & (P.cache.page_size - 1)));
+        return there ? key_of(w) : 0u;
     };
-    const bool inside = count <= P.keys;
-    if (inside)
+    const uint32_t lower = (1u << lane) - 1u;
+    // a contiguous share of the positions to each warp
+    const int share = (count + kSelectWarps * 32 - 1) / (kSelectWarps * 32) * 32;
+    const int i0 = min(warp * share, count), i1 = min(i0 + share, count);
+    if (count <= P.keys) {
+        // the upper bits of all keys, and their range
+        uint32_t low = 0xFFFFFFFFu, high = 0u;
+        constexpr int kAtOnce = 8;             // loads of a thread on their way together
+        for (int first = threadIdx.x; first < count; first += kAtOnce * kSelectThreads) {
+            uint32_t k[kAtOnce];
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) k[j] = weight_key(min(first + j * kSelectThreads, count - 1)) >> kLowBits;
+#pragma unroll
+            for (int j = 0; j < kAtOnce; ++j) {
+                const int i = first + j * kSelectThreads;
+                if (i < count) upper[i] = static_cast<uint16_t>(k[j]);
+                low = min(low, k[j]);
+                high = max(high, k[j]);
+            }
+        }
+        for (int i = threadIdx.x; i < kBins; i += kSelectThreads) bins[i] = 0;
+        if (threadIdx.x == 0) candidates = 0;
+        block_range(low, high, warp_above, warp_equal);
+        // (of more than 2048 steps several share a bin)
+        const int shift = max(21 - __clz(high - low), 0);
+#pragma unroll 4
+        for (int i = threadIdx.x; i < count; i += kSelectThreads) atomicAdd(&bins[(upper[i] - low) >> shift], 1u);
+        __syncthreads();
+        uint32_t left = static_cast<uint32_t>(need), in_bin;
+        const uint32_t bin = bin_of(bins, left, in_bin, warp_above, found);
+        if (in_bin <= kBins / 2) {
+            // keys and positions of the bin's, in the histogram's place; those kept get the mark
+            uint2* list = reinterpret_cast<uint2*>(bins);
+            const uint32_t from = low + (bin << shift), range = (1u << shift) - 1u;
+#pragma unroll 4
+            for (int i = threadIdx.x; i < count; i += kSelectThreads)
+                if (upper[i] - from <= range) list[atomicAdd(&candidates, 1u)] = make_uint2(weight_key(i), static_cast<uint32_t>(i));
+            __syncthreads();
+            for (uint32_t c = threadIdx.x; c < in_bin; c += kSelectThreads) {
+                const uint2 mine = list[c];
+                uint32_t place = 0;
+                for (uint32_t o = 0; o < in_bin; ++o) place += list[o].x > mine.x || (list[o].x == mine.x && list[o].y < mine.y);
+                if (place < left) upper[mine.y] = kMark;
+            }
+            __syncthreads();
+            const uint32_t above_bin = from + range;
+            uint32_t mine = 0;
+#pragma unroll 4
+            for (int i = i0 + lane; i < i1; i += 32) mine += upper[i] > above_bin;
+            mine = __reduce_add_sync(0xFFFFFFFFu, mine);
+            if (lane == 0) warp_above[warp] = mine;
+            __syncthreads();
+            int to = a.sinks + static_cast<int>(__reduce_add_sync(0xFFFFFFFFu, lane < warp ? warp_above[lane] : 0u));
+#pragma unroll 4
+            for (int i = i0; i < i1; i += 32) {
+                const uint32_t in = __ballot_sync(0xFFFFFFFFu, i + lane < i1 && upper[min(i + lane, i1 - 1)] > above_bin);
+                if ((in >> lane) & 1u) kept[to + __popc(in & lower)] = a.sinks + i + lane;
+                to += __popc(in);
+            }
+            return;
+        }
+        __syncthreads();                       // bins are cleared again
+    }
+    // bit by bit over whole keys
+    uint32_t low = 0xFFFFFFFFu, high = 0u;
 #pragma unroll 8
-        for (int i = threadIdx.x; i < count; i += kSelectThreads) keys[i] = weight_key(i);
-    auto key = [&](int i) { return inside ? keys[i] : weight_key(i); };
-    // the smallest kept key, digit by digit, and how many of those equal to it are kept
-    uint32_t least = 0, fixed = 0, left = static_cast<uint32_t>(need);
-    for (int pass = 0; pass < 3; ++pass) {
-        const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, width = pass == 2 ? 10 : 11;
-        const uint32_t digits = (1u << width) - 1u;
+    for (int i = threadIdx.x; i < count; i += kSelectThreads) {
+        const uint32_t k = weight_key(i);
+        low = min(low, k);
+        high = max(high, k);
+    }
+    block_range(low, high, warp_above, warp_equal);
+    // the smallest kept key, from `least` on below 2^bits more, and how many of those equal to it are kept
+    uint32_t least = low, left = static_cast<uint32_t>(need), in_bin;
+    for (int bits = 32 - __clz(high - low);;) {
+        const int shift = max(bits - 11, 0);
+        const uint32_t range = bits == 32 ? 0xFFFFFFFFu : (1u << bits) - 1u;
         for (int i = threadIdx.x; i < kBins; i += kSelectThreads) bins[i] = 0;
         __syncthreads();
 #pragma unroll 4
         for (int i = threadIdx.x; i < count; i += kSelectThreads) {
-            const uint32_t k = key(i);
-            if ((k & fixed) == least) atomicAdd(&bins[(k >> shift) & digits], 1u);
+            const uint32_t k = weight_key(i) - least;  // (smaller keys: past the range)
+            if (k <= range) atomicAdd(&bins[k >> shift], 1u);
         }
         __syncthreads();
-        // from the largest digit down: a thread has four
-        constexpr int kEach = kBins / kSelectThreads;
-        const int top = kBins - 1 - static_cast<int>(threadIdx.x) * kEach;
-        uint32_t n[kEach], mine = 0;
-#pragma unroll
-        for (int i = 0; i < kEach; ++i) mine += n[i] = bins[top - i];
-        uint32_t in = mine;
-#pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const uint32_t o = __shfl_up_sync(0xFFFFFFFFu, in, d);
-            if (lane >= d) in += o;
-        }
-        if (lane == 31) warp_above[warp] = in;
-        __syncthreads();
-        uint32_t above = in - mine;
-        for (int w = 0; w < warp; ++w) above += warp_above[w];
-        if (above < left && left <= above + mine) {    // one thread's
-            int i = 0;
-            while (left > above + n[i]) above += n[i++];
-            found[0] = static_cast<uint32_t>(top - i);
-            found[1] = left - above;
-        }
-        __syncthreads();
-        least |= found[0] << shift;
-        fixed |= digits << shift;
-        left = found[1];
+        least += bin_of(bins, left, in_bin, warp_above, found) << shift;
+        if (shift == 0) break;
+        bits = shift;
     }
-    // a contiguous share to each warp
-    const int share = (count + kSelectWarps * 32 - 1) / (kSelectWarps * 32) * 32;
-    const int i0 = min(warp * share, count), i1 = min(i0 + share, count);
     uint32_t above = 0, equal = 0;
+#pragma unroll 4
     for (int i = i0 + lane; i < i1; i += 32) {
-        const uint32_t k = key(i);
+        const uint32_t k = weight_key(i);
         above += k > least;
         equal += k == least;
     }
     above = __reduce_add_sync(0xFFFFFFFFu, above);
     equal = __reduce_add_sync(0xFFFFFFFFu, equal);
-    __syncthreads();
     if (lane == 0) {
         warp_above[warp] = above;
         warp_equal[warp] = equal;
     }
     __syncthreads();
-    above = equal = 0;
-    for (int w = 0; w < warp; ++w) {
-        above += warp_above[w];
-        equal += warp_equal[w];
-    }
-    const uint32_t lower = (1u << lane) - 1u;
+    above = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? warp_above[lane] : 0u);
+    equal = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? warp_equal[lane] : 0u);
+#pragma unroll 4
     for (int i = i0; i < i1; i += 32) {
-        const uint32_t k = i + lane < i1 ? key(i + lane) : 0u;
+        const uint32_t k = weight_key(min(i + lane, i1 - 1));
         const uint32_t up = __ballot_sync(0xFFFFFFFFu, i + lane < i1 && k > least), same = __ballot_sync(0xFFFFFFFFu, i + lane < i1 && k == least);
         const uint32_t before = equal + __popc(same & lower);
         if (((up >> lane) & 1u) || (((same >> lane) & 1u) && before < left))
@@ -247,6 +341,7 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constan
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, heads = P.cache.heads;
     const int b = static_cast<int>(blockIdx.x) / heads, h = static_cast<int>(blockIdx.x) % heads;
     const int32_t* kept = a.kept + static_cast<int64_t>(blockIdx.x) * a.budget;
+    griddep_wait();                            // for select's writes
     if (kept[0] < 0) return;                   // left as it was
     const int32_t* from_row = a.table + static_cast<int64_t>(b) * a.table_stride;
     const int32_t* to_row = a.table_out + static_cast<int64_t>(b) * a.out_stride;
@@ -320,21 +415,29 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constan
 template <int D>
 cudaError_t move(const Params& P, cudaStream_t s) {
     const int records = (P.a.budget + kKvTokens - 1) / kKvTokens;
-    move_kernel<D><<<dim3(static_cast<unsigned>(P.a.batch) * P.cache.heads, (records + kMoveRecords - 1) / kMoveRecords), kMoveThreads, 0, s>>>(P);
-    return cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>(P.a.batch) * P.cache.heads, (records + kMoveRecords - 1) / kMoveRecords);
+    cfg.blockDim = dim3(kMoveThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;       // its blocks start while select's end
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, move_kernel<D>, P);
 }
 
 }  // namespace
 
-cudaError_t launch_evict(const EvictArgs& a, const KvGeometry& g, cudaStream_t s) {
+cudaError_t launch_evict(const EvictArgs& a, const KvGeometry& g, int num_sms, cudaStream_t s) {
     int shift = 0;
     while ((1 << shift) < g.page_size) ++shift;
     const int64_t room = static_cast<int64_t>(a.max_pages) * g.page_size;
-    const Params P{a, KvCache{g.data, g.pages, g.page_size, shift, g.heads, g.D}, (a.budget + g.page_size - 1) / g.page_size,
-                   static_cast<int>(room < kMostKeys ? room : kMostKeys)};
+    const int64_t keys = room < kMostKeys ? room + room % 2 : kMostKeys;
+    const Params P{a, KvCache{g.data, g.pages, g.page_size, shift, g.heads, g.D}, (a.budget + g.page_size - 1) / g.page_size, static_cast<int>(keys)};
     static std::atomic<uint64_t> smem_set{0};
-    if (cudaError_t e = set_smem_limit_once(select_kernel, kMostKeys * 4, smem_set); e != cudaSuccess) return e;
-    select_kernel<<<static_cast<unsigned>(a.batch) * g.heads + 1, kSelectThreads, P.keys * 4, s>>>(P);
+    if (cudaError_t e = set_smem_limit_once(select_kernel, kMostKeys * 2, smem_set); e != cudaSuccess) return e;
+    select_kernel<<<static_cast<unsigned>(a.batch) * g.heads + 1, kSelectThreads, P.keys * 2, s>>>(P);
     if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
     if (g.D == 64) return move<64>(P, s);
     return g.D == 128 ? move<128>(P, s) : move<256>(P, s);

@@ -364,7 +364,7 @@ struct EvictArgs {
     int32_t* kept;
     int32_t* refused;
 };
-cudaError_t launch_evict(const EvictArgs& a, const KvGeometry& g, cudaStream_t s);
+cudaError_t launch_evict(const EvictArgs& a, const KvGeometry& g, int num_sms, cudaStream_t s);
 
 // Host-side checks of a one-tensor GEMV, the same ones pn_gemv_ex makes before
 // it launches anything.  On PN_OK, *uses_workspace tells whether the call
