@@ -34,7 +34,7 @@ constexpr int kBins = 2048;
 constexpr int kMostKeys = 96 * 1024;           // of a block, whose upper bits are kept in shared memory
 constexpr int kLowBits = 17;                   // the others
 constexpr int kMoveThreads = 256;
-constexpr int kMoveRecords = kMoveThreads / 32 * 2;    // of a block
+constexpr int kMoveRecords = kMoveThreads / 32;        // of a block
 
 struct Params {
     EvictArgs a;
@@ -181,8 +181,10 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
                 ++turn;
                 behind += held_of(P, o);
             }
-        turn = block_sum<kSelectWarps>(turn, part);
-        behind = block_sum<kSelectWarps>(behind, part);
+        if (b > 0) {
+            turn = block_sum<kSelectWarps>(turn, part);
+            behind = block_sum<kSelectWarps>(behind, part);
+        }
         served = turn < most_served(P);
     }
     if (h == 0) {

@@ -599,7 +599,7 @@ pn_status pn_kv_weigh(const uint16_t* q, int64_t q_stride, int64_t tokens, int h
  * holds them: take them out of held first.  A kept token on a page outside the
  * cache becomes zeros.  No output shares memory with an input or another output.
  */
-#define PN_MAX_BUDGET (1 << 23)
+#define PN_MAX_BUDGET (1 << 22)
 pn_status pn_kv_evict(void* cache, int64_t pages, int page_size, int kv_heads, int head_dim, float* weights,
                       const int32_t* table, int64_t table_stride, int max_pages, const int32_t* lens,
                       const int32_t* held, int batch, int limit, int budget, int sinks, int recent,
