@@ -293,6 +293,10 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const __grid_constan
 // range of the call's tiles (request, head, 32 tokens) and works alone: the next
 // tile's codes, scales and weights are on their way while it multiplies, and the
 // pages of the one behind that are being looked up.
+//
+// 64 ragged requests to 16384 tokens, 32 + 8 heads of 128: bound by memory and the
+// instructions for it; with a tile's registers copied, masks worked out for every tile
+// and places in 64 bits throughout, a tile took 600 instructions and the call 101 us.
 
 template <int D>
 struct Tile {
@@ -301,20 +305,30 @@ struct Tile {
     float before;
 };
 
+// Where a tile's two records are: page * heads + head, -1 for none.
+struct Place {
+    int64_t unit[2];
+};
+
+template <int D, int NT>
+struct FewRows {
+    uint4 q[NT][D / 64][2];
+    float start[NT][D / 64][2], factor[NT][2], less[NT][2], share[NT][2];
+    int pos[NT][2];
+};
+
 template <int D>
-__device__ __forceinline__ void load_tile(const Params& P, const int64_t (&place)[2], int h, bool seen, bool kept, Tile<D>& k) {
+__device__ __forceinline__ void load_tile(const Params& P, const Place& place, int tok0, bool seen, bool kept, Tile<D>& k) {
     constexpr int NG = D / 64, GP = kv_plane_groups(D), PL = kv_planes(D);
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    const uint32_t head_bytes = static_cast<uint32_t>(P.cache.head_bytes()), in_page = P.cache.page_size - 1;
 #pragma unroll
-    for (int r = 0; r < 2; ++r)
+    for (int r = 0; r < 2; ++r) {
+        const bool there = place.unit[r] >= 0 && seen;
+        // (of a place that is none the first record is read, and not used)
+        const uint8_t* record = P.cache.data + static_cast<uint64_t>(there ? place.unit[r] : 0) * head_bytes + (((tok0 + r * kKvTokens) & in_page) >> 4) * kv_record_bytes(D);
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) k.w[r][hh][i] = 0;
-#pragma unroll
-            for (int i = 0; i < (NG + 1) / 2; ++i) k.d[r][hh][i] = 0;
-            if (place[r] < 0 || !seen) continue;
-            const uint8_t* record = P.cache.record(place[r], h);
 #pragma unroll
             for (int pl = 0; pl < PL; ++pl) {
                 const uint8_t* p = record + ((hh * PL + pl) * 32 + lane) * 8 * GP;
@@ -334,21 +348,70 @@ __device__ __forceinline__ void load_tile(const Params& P, const int64_t (&place
                 k.d[r][hh][0] = v.x; k.d[r][hh][1] = v.y;
             }
         }
+    }
     // lane (g, t) has token 8 t + g
-    const int64_t mine = t < 2 ? place[0] : place[1];
+    const int64_t mine = t < 2 ? place.unit[0] : place.unit[1];
     k.before = 0.0f;
-    if (kept && mine >= 0)
-        k.before = P.a.weights[(((mine >> P.cache.page_shift) * P.cache.heads + h) << P.cache.page_shift) + (mine & (P.cache.page_size - 1)) + ((8 * t + g) & 15)];
+    if (kept && mine >= 0) k.before = P.a.weights[(mine << P.cache.page_shift) + ((tok0 + 8 * t + g) & in_page)];
 }
 
-template <int D, int NT>
-__global__ void __launch_bounds__(kThreads, D == 256 || NT == 2 ? 2 : D == 128 ? 2 : 3) weigh_few_kernel(const __grid_constant__ Params P) {
+template <int D, int NT, bool kMasked>
+__device__ __forceinline__ void tile_sums(const Tile<D>& k, const FewRows<D, NT>& R, int tok0, int window, int sinks, float (&sum)[4]) {
     constexpr int NG = D / 64;
+    const int g = (threadIdx.x & 31) >> 2;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        float x[NT][4];
+#pragma unroll
+        for (int j = 0; j < NG; ++j) {
+            float acc[NT][4];
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                const uint32_t a = k.w[i][0][2 * j + v], c = k.w[i][1][2 * j + v], as = a >> 8, cs = c >> 8;
+                const uint32_t a0 = raw_pair<0>(a, as), a1 = raw_pair<0>(c, cs), a2 = raw_pair<1>(a, as), a3 = raw_pair<1>(c, cs);
+                const uint32_t b0 = raw_pair<2>(a, as), b1 = raw_pair<2>(c, cs), b2 = raw_pair<3>(a, as), b3 = raw_pair<3>(c, cs);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    if (v == 0) mma_from(acc[n], a0, a1, a2, a3, R.q[n][j][v].x, R.q[n][j][v].y, R.start[n][j][0], R.start[n][j][1], R.start[n][j][0], R.start[n][j][1]);
+                    else mma_16816(acc[n], a0, a1, a2, a3, R.q[n][j][v].x, R.q[n][j][v].y);
+                    mma_16816(acc[n], b0, b1, b2, b3, R.q[n][j][v].z, R.q[n][j][v].w);
+                }
+            }
+            const float d0 = half_bits_to_float(j & 1 ? k.d[i][0][j / 2] >> 16 : k.d[i][0][j / 2] & 0xFFFFu);
+            const float d1 = half_bits_to_float(j & 1 ? k.d[i][1][j / 2] >> 16 : k.d[i][1][j / 2] & 0xFFFFu);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[n][e] = j ? fmaf(e < 2 ? d0 : d1, acc[n][e], x[n][e]) : (e < 2 ? d0 : d1) * acc[n][e];
+        }
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float p = ex2(fmaf(x[n][e], R.factor[n][e & 1], R.less[n][e & 1]));
+                if constexpr (kMasked) {
+                    const int tok = tok0 + i * kKvTokens + (e >> 1) * 8 + g;
+                    p = tok <= R.pos[n][e & 1] && (tok > R.pos[n][e & 1] - window || tok < sinks) ? p : 0.0f;
+                }
+                sum[2 * i + (e >> 1)] = fmaf(p, R.share[n][e & 1], sum[2 * i + (e >> 1)]);
+            }
+    }
+}
+
+// Threads of a block and blocks to an SM: registers for a tile, the next one and the rows.
+template <int D>
+constexpr int kFewThreads = D == 256 ? 384 : 256;
+template <int D, int NT>
+constexpr int kFewBlocks = D == 256 ? 1 : D == 64 && NT == 1 ? 3 : 2;
+
+template <int D, int NT>
+__global__ void __launch_bounds__(kFewThreads<D>, kFewBlocks<D, NT>) weigh_few_kernel(const __grid_constant__ Params P) {
+    constexpr int NG = D / 64, kThreads = kFewThreads<D>, kWarps = kThreads / 32;
     __shared__ uint64_t scan[kThreads + 1];
     __shared__ uint64_t warp_sums[kWarps];
     const WeighArgs& a = P.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const int heads = P.cache.heads, window = a.window ? a.window : INT32_MAX;
+    const int heads = P.cache.heads, window = a.window ? a.window : INT32_MAX, shift = P.cache.page_shift;
     const int each = scan_units<kTile, kThreads>(P, scan, warp_sums);
     const uint64_t total = scan[kThreads], warps = static_cast<uint64_t>(gridDim.x) * kWarps, w = static_cast<uint64_t>(blockIdx.x) * kWarps + warp;
     uint64_t u = total / warps * w + min(w, total % warps);
@@ -358,37 +421,35 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NT == 2 ? 2 : D == 128 ?
     int b, h, first;
     locate<kTile, kThreads>(P, scan, each, u, r, b, h, first);
     while (u < u1) {
-        const int tiles = units_of<kTile>(r), last = static_cast<int>(min(static_cast<uint64_t>(tiles - first), u1 - u)) + first;
+        const int last = static_cast<int>(min(static_cast<uint64_t>(units_of<kTile>(r) - first), u1 - u)) + first;
         const int32_t* row = a.table + static_cast<int64_t>(b) * a.table_stride;
-        // slots of a tile's two records, -1 where there is none
-        auto look = [&](int tile, int64_t (&place)[2]) {
-            const int tok0 = tile * kTile;
+        // pages of a tile's two records; those behind the last token are its page again, and not used
+        auto look = [&](int tile, int (&page)[2]) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int tok = tok0 + i * kKvTokens;
-                place[i] = -1;
-                if (tile >= last || tok >= r.len) continue;
-                const int page = row[tok >> P.cache.page_shift];
-                if (page >= 0 && page < P.cache.pages) place[i] = (static_cast<int64_t>(page) << P.cache.page_shift) + (tok & (P.cache.page_size - 1));
-            }
+            for (int i = 0; i < 2; ++i) page[i] = row[min(tile * kTile + i * kKvTokens, r.len - 1) >> shift];
+        };
+        auto place_of = [&](int tile, const int (&page)[2]) {
+            Place p;
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+                p.unit[i] = page[i] >= 0 && page[i] < P.cache.pages && tile * kTile + i * kKvTokens < r.len ? static_cast<int64_t>(page[i]) * heads + h : -1;
+            return p;
         };
         const int pos_hi = r.pos0 + r.n - 1;
-        auto seen = [&](int tile) { return !a.window || tile * kTile < a.sinks || tile * kTile + kTile - 1 > r.pos0 - window; };
+        auto seen = [&](int tile) { return tile * kTile <= pos_hi && (!a.window || tile * kTile < a.sinks || tile * kTile + kTile - 1 > r.pos0 - window); };
         auto kept = [&](int tile) { return a.weights && tile * kTile + 8 * t + g < r.pos0; };
-        int64_t here[2], next[2];
-        look(first, here);
-        look(first + 1, next);
-        Tile<D> k;
-        load_tile<D>(P, here, h, seen(first), kept(first), k);
-        // the rows: B fragments, and for the lane's columns what the products start from and so on
-        uint4 q[NT][NG][2];
-        float start[NT][NG][2], factor[NT][2], less[NT][2], share[NT][2];
-        int pos[NT][2];
+        int page[2];
+        look(first, page);
+        Place here = place_of(first, page);
+        look(min(first + 1, last - 1), page);
+        Tile<D> even, odd;
+        load_tile<D>(P, here, first * kTile, seen(first), kept(first), even);
+        FewRows<D, NT> R;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             float sum[NG];
             const int mine = min(8 * n + g, r.rows - 1), qi = mine / P.group, head = h * P.group + mine - qi * P.group;
-            const float up = ready_fragments<D>(a.q + (r.q0 + qi) * a.q_stride + head * D, q[n], sum);
+            const float up = ready_fragments<D>(a.q + (r.q0 + qi) * a.q_stride + head * D, R.q[n], sum);
             const bool real = 8 * n + g < r.rows;
             const LogSum l = log_sum_of(real ? a.lse[static_cast<int64_t>(r.q0 + qi) * a.heads + head] : -INFINITY, P.scale_rest);
             const float f = real ? P.scale_log2 * up : 0.0f;
@@ -396,65 +457,37 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NT == 2 ? 2 : D == 128 ?
             for (int c = 0; c < 2; ++c) {
                 const int from = (2 * t + c) << 2;             // the columns' rows are those of lanes (2t + c, .)
 #pragma unroll
-                for (int j = 0; j < NG; ++j) start[n][j][c] = __shfl_sync(0xFFFFFFFFu, sum[j], from);
-                factor[n][c] = __shfl_sync(0xFFFFFFFFu, f, from);
-                less[n][c] = __shfl_sync(0xFFFFFFFFu, l.less, from);
-                share[n][c] = __shfl_sync(0xFFFFFFFFu, l.factor, from);
-                pos[n][c] = r.pos0 + __shfl_sync(0xFFFFFFFFu, qi, from);
+                for (int j = 0; j < NG; ++j) R.start[n][j][c] = __shfl_sync(0xFFFFFFFFu, sum[j], from);
+                R.factor[n][c] = __shfl_sync(0xFFFFFFFFu, f, from);
+                R.less[n][c] = __shfl_sync(0xFFFFFFFFu, l.less, from);
+                R.share[n][c] = __shfl_sync(0xFFFFFFFFu, l.factor, from);
+                R.pos[n][c] = r.pos0 + __shfl_sync(0xFFFFFFFFu, qi, from);
             }
         }
-        for (int tile = first; tile < last; ++tile) {
-            const int64_t place[2] = {here[0], here[1]};
-            const Tile<D> cur = k;
-            here[0] = next[0]; here[1] = next[1];
-            if (tile + 1 < last) load_tile<D>(P, here, h, seen(tile + 1), kept(tile + 1), k);
-            look(tile + 2, next);
+        auto step = [&](int tile, const Tile<D>& cur, Tile<D>& next) {
             const int tok0 = tile * kTile;
-            float sum[2][2] = {};
-            if (seen(tile) && tok0 <= pos_hi) {
-                const bool plain = place[0] >= 0 && place[1] >= 0 && tok0 + kTile - 1 <= r.pos0 && (tok0 > pos_hi - window || tok0 + kTile <= a.sinks);
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    float x[NT][4];
-#pragma unroll
-                    for (int j = 0; j < NG; ++j) {
-                        float acc[NT][4];
-#pragma unroll
-                        for (int v = 0; v < 2; ++v) {
-                            const uint32_t a0w = cur.w[i][0][2 * j + v], c0w = cur.w[i][1][2 * j + v], as = a0w >> 8, cs = c0w >> 8;
-                            const uint32_t a0 = raw_pair<0>(a0w, as), a1 = raw_pair<0>(c0w, cs), a2 = raw_pair<1>(a0w, as), a3 = raw_pair<1>(c0w, cs);
-                            const uint32_t b0 = raw_pair<2>(a0w, as), b1 = raw_pair<2>(c0w, cs), b2 = raw_pair<3>(a0w, as), b3 = raw_pair<3>(c0w, cs);
-#pragma unroll
-                            for (int n = 0; n < NT; ++n) {
-                                if (v == 0) mma_from(acc[n], a0, a1, a2, a3, q[n][j][v].x, q[n][j][v].y, start[n][j][0], start[n][j][1], start[n][j][0], start[n][j][1]);
-                                else mma_16816(acc[n], a0, a1, a2, a3, q[n][j][v].x, q[n][j][v].y);
-                                mma_16816(acc[n], b0, b1, b2, b3, q[n][j][v].z, q[n][j][v].w);
-                            }
-                        }
-                        const float d0 = half_bits_to_float(j & 1 ? cur.d[i][0][j / 2] >> 16 : cur.d[i][0][j / 2] & 0xFFFFu);
-                        const float d1 = half_bits_to_float(j & 1 ? cur.d[i][1][j / 2] >> 16 : cur.d[i][1][j / 2] & 0xFFFFu);
-#pragma unroll
-                        for (int n = 0; n < NT; ++n)
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const float d = e < 2 ? d0 : d1;
-                                x[n][e] = j ? fmaf(d, acc[n][e], x[n][e]) : d * acc[n][e];
-                            }
-                    }
-#pragma unroll
-                    for (int n = 0; n < NT; ++n)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            float p = ex2(fmaf(x[n][e], factor[n][e & 1], less[n][e & 1]));
-                            if (!plain) {
-                                const int tok = tok0 + i * kKvTokens + (e >> 1) * 8 + g;
-                                p = tok <= pos[n][e & 1] && (tok > pos[n][e & 1] - window || tok < a.sinks) ? p : 0.0f;
-                            }
-                            sum[i][e >> 1] = fmaf(p, share[n][e & 1], sum[i][e >> 1]);
-                        }
-                }
+            const Place behind = place_of(tile + 1, page);
+            if (tile + 1 < last) load_tile<D>(P, behind, tok0 + kTile, seen(tile + 1), kept(tile + 1), next);
+            look(min(tile + 2, last - 1), page);
+            float sum[4] = {};
+            if (seen(tile)) {
+                if (here.unit[0] >= 0 && here.unit[1] >= 0 && tok0 + kTile - 1 <= r.pos0 && (tok0 > pos_hi - window || tok0 + kTile <= a.sinks))
+                    tile_sums<D, NT, false>(cur, R, tok0, window, a.sinks, sum);
+                else tile_sums<D, NT, true>(cur, R, tok0, window, a.sinks, sum);
             }
-            write_sums(P, sum, place, h, tok0, r.len, a.decay * cur.before);
+            // over the four lanes of a token; lane (g, t) keeps that of token 8 t + g
+            const bool upper = t & 2, second = t & 1;
+            const float s0 = (upper ? sum[2] : sum[0]) + __shfl_xor_sync(0xFFFFFFFFu, upper ? sum[0] : sum[2], 2);
+            const float s1 = (upper ? sum[3] : sum[1]) + __shfl_xor_sync(0xFFFFFFFFu, upper ? sum[1] : sum[3], 2);
+            const float all = (second ? s1 : s0) + __shfl_xor_sync(0xFFFFFFFFu, second ? s0 : s1, 1);
+            const int64_t mine = upper ? here.unit[1] : here.unit[0];
+            if (mine >= 0 && tok0 + 8 * t + g < r.len)
+                a.out[(mine << shift) + ((tok0 + 8 * t + g) & (P.cache.page_size - 1))] = fmaf(a.decay, cur.before, all);
+            here = behind;
+        };
+        for (int tile = first; tile < last; tile += 2) {
+            step(tile, even, odd);
+            if (tile + 1 < last) step(tile + 1, odd, even);
         }
         u += static_cast<uint64_t>(last - first);
         first = 0;
@@ -469,8 +502,8 @@ __global__ void __launch_bounds__(kThreads, D == 256 || NT == 2 ? 2 : D == 128 ?
 template <int D>
 cudaError_t launch(const Params& P, int num_sms, cudaStream_t s) {
     const int64_t rows = static_cast<int64_t>(P.a.max_queries) * P.group;
-    if (rows <= 8) weigh_few_kernel<D, 1><<<num_sms * (D == 64 ? 3 : 2), kThreads, 0, s>>>(P);
-    else if (D < 256 && rows <= 16) weigh_few_kernel<D, D == 256 ? 1 : 2><<<num_sms * 2, kThreads, 0, s>>>(P);
+    if (rows <= 8) weigh_few_kernel<D, 1><<<num_sms * kFewBlocks<D, 1>, kFewThreads<D>, 0, s>>>(P);
+    else if (D < 256 && rows <= 16) weigh_few_kernel<D, D == 256 ? 1 : 2><<<num_sms * 2, kFewThreads<D>, 0, s>>>(P);
     else weigh_kernel<D><<<num_sms * 2, kThreads, 0, s>>>(P);
     return cudaGetLastError();
 }
