@@ -305,9 +305,16 @@ struct Tile {
     float before;
 };
 
-// Where a tile's two records are: page * heads + head, -1 for none.
+// The pages of a tile's two records, -1 for none, and where a head's keys and weights
+// of page 0 begin, from where others are so many bytes (entries) on.
 struct Place {
-    int64_t unit[2];
+    int page[2];
+};
+struct HeadBase {
+    const uint8_t* keys;
+    const float* weights;
+    float* out;
+    int64_t page_bytes, page_entries;
 };
 
 template <int D, int NT>
@@ -318,15 +325,13 @@ struct FewRows {
 };
 
 template <int D>
-__device__ __forceinline__ void load_tile(const Params& P, const Place& place, int tok0, bool seen, bool kept, Tile<D>& k) {
+__device__ __forceinline__ void load_tile(const HeadBase& base, const Place& place, int tok0, int in_page, bool kept, Tile<D>& k) {
     constexpr int NG = D / 64, GP = kv_plane_groups(D), PL = kv_planes(D);
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
-    const uint32_t head_bytes = static_cast<uint32_t>(P.cache.head_bytes()), in_page = P.cache.page_size - 1;
 #pragma unroll
     for (int r = 0; r < 2; ++r) {
-        const bool there = place.unit[r] >= 0 && seen;
-        // (of a place that is none the first record is read, and not used)
-        const uint8_t* record = P.cache.data + static_cast<uint64_t>(there ? place.unit[r] : 0) * head_bytes + (((tok0 + r * kKvTokens) & in_page) >> 4) * kv_record_bytes(D);
+        // (of a page that is none the first one is read, and not used)
+        const uint8_t* record = base.keys + max(place.page[r], 0) * base.page_bytes + (((tok0 + r * kKvTokens) & in_page) >> 4) * kv_record_bytes(D);
 #pragma unroll
         for (int hh = 0; hh < 2; ++hh) {
 #pragma unroll
@@ -350,9 +355,9 @@ __device__ __forceinline__ void load_tile(const Params& P, const Place& place, i
         }
     }
     // lane (g, t) has token 8 t + g
-    const int64_t mine = t < 2 ? place.unit[0] : place.unit[1];
+    const int mine = t < 2 ? place.page[0] : place.page[1];
     k.before = 0.0f;
-    if (kept && mine >= 0) k.before = P.a.weights[(mine << P.cache.page_shift) + ((tok0 + 8 * t + g) & in_page)];
+    if (kept && mine >= 0) k.before = base.weights[mine * base.page_entries + ((tok0 + 8 * t + g) & in_page)];
 }
 
 template <int D, int NT, bool kMasked>
@@ -411,7 +416,9 @@ __global__ void __launch_bounds__(kFewThreads<D>, kFewBlocks<D, NT>) weigh_few_k
     __shared__ uint64_t warp_sums[kWarps];
     const WeighArgs& a = P.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, g = lane >> 2, t = lane & 3;
-    const int heads = P.cache.heads, window = a.window ? a.window : INT32_MAX, shift = P.cache.page_shift;
+    const int heads = P.cache.heads, window = a.window ? a.window : INT32_MAX, shift = P.cache.page_shift, in_page = P.cache.page_size - 1;
+    const uint32_t pages = static_cast<uint32_t>(P.cache.pages);
+    const bool one_page = P.cache.page_size >= kTile;
     const int each = scan_units<kTile, kThreads>(P, scan, warp_sums);
     const uint64_t total = scan[kThreads], warps = static_cast<uint64_t>(gridDim.x) * kWarps, w = static_cast<uint64_t>(blockIdx.x) * kWarps + warp;
     uint64_t u = total / warps * w + min(w, total % warps);
@@ -423,16 +430,18 @@ __global__ void __launch_bounds__(kFewThreads<D>, kFewBlocks<D, NT>) weigh_few_k
     while (u < u1) {
         const int last = static_cast<int>(min(static_cast<uint64_t>(units_of<kTile>(r) - first), u1 - u)) + first;
         const int32_t* row = a.table + static_cast<int64_t>(b) * a.table_stride;
-        // pages of a tile's two records; those behind the last token are its page again, and not used
+        const HeadBase base{P.cache.data + h * P.cache.head_bytes(), a.weights + static_cast<int64_t>(h) * P.cache.page_size,
+                            a.out + static_cast<int64_t>(h) * P.cache.page_size, heads * P.cache.head_bytes(), static_cast<int64_t>(heads) << shift};
+        // entries of the table for a tile's two records (of one page where it holds both); behind the last token its own again
         auto look = [&](int tile, int (&page)[2]) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) page[i] = row[min(tile * kTile + i * kKvTokens, r.len - 1) >> shift];
+            page[0] = row[min(tile * kTile, r.len - 1) >> shift];
+            page[1] = one_page ? page[0] : row[min(tile * kTile + kKvTokens, r.len - 1) >> shift];
         };
         auto place_of = [&](int tile, const int (&page)[2]) {
             Place p;
 #pragma unroll
             for (int i = 0; i < 2; ++i)
-                p.unit[i] = page[i] >= 0 && page[i] < P.cache.pages && tile * kTile + i * kKvTokens < r.len ? static_cast<int64_t>(page[i]) * heads + h : -1;
+                p.page[i] = static_cast<uint32_t>(page[i]) < pages && tile * kTile + i * kKvTokens < r.len ? page[i] : -1;
             return p;
         };
         const int pos_hi = r.pos0 + r.n - 1;
@@ -443,7 +452,7 @@ __global__ void __launch_bounds__(kFewThreads<D>, kFewBlocks<D, NT>) weigh_few_k
         Place here = place_of(first, page);
         look(min(first + 1, last - 1), page);
         Tile<D> even, odd;
-        load_tile<D>(P, here, first * kTile, seen(first), kept(first), even);
+        load_tile<D>(base, here, first * kTile, in_page, kept(first), even);
         FewRows<D, NT> R;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
@@ -467,11 +476,11 @@ __global__ void __launch_bounds__(kFewThreads<D>, kFewBlocks<D, NT>) weigh_few_k
         auto step = [&](int tile, const Tile<D>& cur, Tile<D>& next) {
             const int tok0 = tile * kTile;
             const Place behind = place_of(tile + 1, page);
-            if (tile + 1 < last) load_tile<D>(P, behind, tok0 + kTile, seen(tile + 1), kept(tile + 1), next);
+            if (tile + 1 < last) load_tile<D>(base, behind, tok0 + kTile, in_page, kept(tile + 1), next);
             look(min(tile + 2, last - 1), page);
             float sum[4] = {};
             if (seen(tile)) {
-                if (here.unit[0] >= 0 && here.unit[1] >= 0 && tok0 + kTile - 1 <= r.pos0 && (tok0 > pos_hi - window || tok0 + kTile <= a.sinks))
+                if ((here.page[0] | here.page[1]) >= 0 && tok0 + kTile - 1 <= r.pos0 && (tok0 > pos_hi - window || tok0 + kTile <= a.sinks))
                     tile_sums<D, NT, false>(cur, R, tok0, window, a.sinks, sum);
                 else tile_sums<D, NT, true>(cur, R, tok0, window, a.sinks, sum);
             }
@@ -480,9 +489,8 @@ __global__ void __launch_bounds__(kFewThreads<D>, kFewBlocks<D, NT>) weigh_few_k
             const float s0 = (upper ? sum[2] : sum[0]) + __shfl_xor_sync(0xFFFFFFFFu, upper ? sum[0] : sum[2], 2);
             const float s1 = (upper ? sum[3] : sum[1]) + __shfl_xor_sync(0xFFFFFFFFu, upper ? sum[1] : sum[3], 2);
             const float all = (second ? s1 : s0) + __shfl_xor_sync(0xFFFFFFFFu, second ? s0 : s1, 1);
-            const int64_t mine = upper ? here.unit[1] : here.unit[0];
-            if (mine >= 0 && tok0 + 8 * t + g < r.len)
-                a.out[(mine << shift) + ((tok0 + 8 * t + g) & (P.cache.page_size - 1))] = fmaf(a.decay, cur.before, all);
+            const int mine = upper ? here.page[1] : here.page[0];
+            if (mine >= 0 && tok0 + 8 * t + g < r.len) base.out[mine * base.page_entries + ((tok0 + 8 * t + g) & in_page)] = fmaf(a.decay, cur.before, all);
             here = behind;
         };
         for (int tile = first; tile < last; tile += 2) {
