@@ -179,7 +179,14 @@ __device__ __forceinline__ uint32_t token_pair(uint32_t a, uint32_t b, bool odd)
     return __byte_perm(a, b, odd ? 0x7632 : 0x5410);
 }
 
-// raw_pair less 8: (n - 8) 2^-24 or (n - 8) 2^-20.
+// Pair I (0 .. 3) of four code pairs at bits 0, 4, 8, 12 of a word's halves, as
+// fp16 numbers: n 2^-24 for I even, n 2^-20 for I odd.  `shifted` = word >> 8.
+template <int I>
+__device__ __forceinline__ uint32_t raw_pair(uint32_t word, uint32_t shifted) {
+    return (I >= 2 ? shifted : word) & (I & 1 ? 0x00F000F0u : 0x000F000Fu);
+}
+
+// The same less 8: (n - 8) 2^-24 or (n - 8) 2^-20.
 template <int I>
 __device__ __forceinline__ uint32_t value_pair(uint32_t word, uint32_t shifted) {
     uint32_t d;

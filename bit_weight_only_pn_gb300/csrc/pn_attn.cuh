@@ -46,13 +46,6 @@ __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// Pair I (0 .. 3) of four code pairs at bits 0, 4, 8, 12 of a word's halves, as
-// fp16 numbers: n 2^-24 for I even, n 2^-20 for I odd.  `shifted` = word >> 8.
-template <int I>
-__device__ __forceinline__ uint32_t raw_pair(uint32_t word, uint32_t shifted) {
-    return (I >= 2 ? shifted : word) & (I & 1 ? 0x00F000F0u : 0x000F000Fu);
-}
-
 // D = C + A * B, m16n8k16, fp16 inputs, fp32 accumulate.
 __device__ __forceinline__ void mma_from(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1, float c0, float c1, float c2, float c3) {

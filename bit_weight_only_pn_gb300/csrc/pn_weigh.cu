@@ -5,9 +5,9 @@
 // lse), with each row's lse as attention gave it, and decay times what t had before
 // (nothing, for the step's own tokens).
 //
-// Only K is read.  The products are those of pn_attn.cu: codes as fp16 subnormals,
-// 16 tokens x 8 query rows to an mma.sync, 8 sum q taken off through the
-// accumulator's first value, queries scaled by powers of two.  There is no softmax
+// Only K is read.  The products run on mma.sync, 16 tokens x 8 query rows, with the
+// codes as fp16 whole numbers n - 8 and the queries as they are, so every product is
+// exact; each group's sum is multiplied by its scale in fp32.  There is no softmax
 // state, so tokens do not wait for each other: a warp has 32 of them, whose codes
 // stay in registers while the query rows go by, and each lane sums what its columns
 // give.  A token's sum is made by one warp in a fixed order; nothing is joined and
@@ -31,48 +31,21 @@ constexpr int kTile = 32;                      // tokens of a warp
 constexpr int kUnit = kWarps * kTile;          // tokens of a block's unit of work
 constexpr int kChunk = 8 * kWarps;             // query rows made ready at a time, 8 by a warp
 
-// Row g of eight as the lane's part of the products' B fragments, scaled by a power of
-// two, the sums that the products start from, and the factor back to q . k.
+// Code pair I of a word as fp16 whole numbers n - 8.  (Not as subnormals, which attention
+// takes as they are: the tensor cores align sums by the operands' exponents, and
+// products of subnormals lie some bits below theirs.  Attention's outputs are rounded
+// to fp16 and do not show it; weights are not, and erred by 1e-6 instead of 2e-7.)
+template <int I>
+__device__ __forceinline__ uint32_t codes(uint32_t word, uint32_t shifted) { return decode_pair<kPn4t, I>(word, shifted); }
+
+// Row g of eight as the lane's part of the products' B fragments.
 template <int D>
-__device__ __forceinline__ float ready_fragments(const __half* src, uint4 (&q)[D / 64][2], float (&start)[D / 64]) {
-    constexpr int NG = D / 64;
+__device__ __forceinline__ void load_fragments(const __half* src, uint4 (&q)[D / 64][2]) {
     const int t = threadIdx.x & 3;
-    uint4 f[NG][2];
-    uint32_t top = 0;                          // the row's largest |q|, as bits
 #pragma unroll
-    for (int j = 0; j < NG; ++j)
+    for (int j = 0; j < D / 64; ++j)
 #pragma unroll
-        for (int w = 0; w < 2; ++w) {
-            f[j][w] = *reinterpret_cast<const uint4*>(src + 64 * j + 16 * t + 8 * w);
-            const uint32_t v[4] = {f[j][w].x, f[j][w].y, f[j][w].z, f[j][w].w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) top = __vmaxu2(top, v[i] & 0x7FFF7FFFu);
-        }
-    top = max(top & 0xFFFFu, top >> 16);
-    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
-    top = max(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
-    const int e = 25 - static_cast<int>(max(top >> 10, 1u));                 // the largest |q| 2^e lies in [2^10, 2^11)
-    const float up = __int_as_float((127 + e) << 23);
-#pragma unroll
-    for (int j = 0; j < NG; ++j) {
-        float sum = 0.0f;
-#pragma unroll
-        for (int w = 0; w < 2; ++w) {
-            const uint32_t v[4] = {f[j][w].x, f[j][w].y, f[j][w].z, f[j][w].w};
-            uint32_t made[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float a0 = half_bits_to_float(v[i] & 0xFFFFu) * up, a1 = half_bits_to_float(v[i] >> 16) * up;
-                sum += a0 + a1;
-                made[i] = i & 1 ? pack_half2(a0, a1) : pack_half2(16.0f * a0, 16.0f * a1);
-            }
-            q[j][w] = make_uint4(made[0], made[1], made[2], made[3]);
-        }
-        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
-        sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
-        start[j] = -0x1p-17f * sum;                                          // -8 * 2^-20
-    }
-    return __int_as_float((127 + 20 - e) << 23);
+        for (int w = 0; w < 2; ++w) q[j][w] = *reinterpret_cast<const uint4*>(src + 64 * j + 16 * t + 8 * w);
 }
 
 // The sums of tokens 8 (2 i + hh) + g over a warp's columns, and what the tokens had
@@ -93,14 +66,12 @@ __device__ __forceinline__ void write_sums(const Params& P, const float (&sum)[2
         P.a.out[(((mine >> P.cache.page_shift) * P.cache.heads + h) << P.cache.page_shift) + (mine & (P.cache.page_size - 1)) + ((8 * t + g) & 15)] = before + all;
 }
 
-// Eight query rows ready for the products: B fragments by lane, and for each row
-// what the products start from, the factor to scores times log2 e, its LogSum
-// (-inf: a row that gives nothing) and its position.
+// Eight query rows ready for the products: B fragments by lane, and for each row its
+// LogSum (-inf: a row that gives nothing) and its position.
 template <int D>
 struct Rows {
     uint4 q[D / 64][2][32];
-    float start[D / 64][8];
-    float factor[8], less[8], share[8];
+    float less[8], share[8];
     int pos[8];
 };
 
@@ -110,18 +81,15 @@ __device__ __forceinline__ void make_ready(const Params& P, const Request& r, in
     const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
     const int row = min(row0 + g, r.rows - 1), qi = row / P.group, head = h * P.group + row - qi * P.group;
     uint4 q[NG][2];
-    float start[NG];
-    const float up = ready_fragments<D>(P.a.q + (r.q0 + qi) * P.a.q_stride + head * D, q, start);
+    load_fragments<D>(P.a.q + (r.q0 + qi) * P.a.q_stride + head * D, q);
 #pragma unroll
     for (int j = 0; j < NG; ++j) {
         to.q[j][0][lane] = q[j][0];
         to.q[j][1][lane] = q[j][1];
-        if (t == 0) to.start[j][g] = start[j];
     }
     if (t == 0) {
         const bool real = row0 + g < r.rows;
         const LogSum l = log_sum_of(real ? P.a.lse[static_cast<int64_t>(r.q0 + qi) * P.a.heads + head] : -INFINITY, P.scale_rest);
-        to.factor[g] = real ? P.scale_log2 * up : 0.0f;
         to.less[g] = l.less;
         to.share[g] = l.factor;
         to.pos[g] = r.pos0 + qi;
@@ -170,7 +138,7 @@ __device__ __forceinline__ void load_keys(const uint8_t* const (&record)[2], Key
 template <int D, int NT>
 __device__ __forceinline__ void products(const Keys<D>& k, const Rows<D>* rows, float (&x)[2][NT][4]) {
     constexpr int NG = D / 64;
-    const int lane = threadIdx.x & 31, t = lane & 3;
+    const int lane = threadIdx.x & 31;
 #pragma unroll
     for (int j = 0; j < NG; ++j) {
         float acc[2][NT][4];
@@ -183,16 +151,12 @@ __device__ __forceinline__ void products(const Keys<D>& k, const Rows<D>* rows, 
             for (int r = 0; r < 2; ++r) {
                 // word 2t + w of group j of tokens g (a) and g + 8 (c)
                 const uint32_t a = k.w[r][0][2 * j + w], c = k.w[r][1][2 * j + w], as = a >> 8, cs = c >> 8;
-                const uint32_t a0 = raw_pair<0>(a, as), a1 = raw_pair<0>(c, cs), a2 = raw_pair<1>(a, as), a3 = raw_pair<1>(c, cs);
-                const uint32_t b0 = raw_pair<2>(a, as), b1 = raw_pair<2>(c, cs), b2 = raw_pair<3>(a, as), b3 = raw_pair<3>(c, cs);
+                const uint32_t a0 = codes<0>(a, as), a1 = codes<0>(c, cs), a2 = codes<1>(a, as), a3 = codes<1>(c, cs);
+                const uint32_t b0 = codes<2>(a, as), b1 = codes<2>(c, cs), b2 = codes<3>(a, as), b3 = codes<3>(c, cs);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    if (w == 0) {
-                        const float2 s = *reinterpret_cast<const float2*>(rows[n].start[j] + 2 * t);
-                        mma_from(acc[r][n], a0, a1, a2, a3, b[n].x, b[n].y, s.x, s.y, s.x, s.y);
-                    } else {
-                        mma_16816(acc[r][n], a0, a1, a2, a3, b[n].x, b[n].y);
-                    }
+                    if (w == 0) mma_from(acc[r][n], a0, a1, a2, a3, b[n].x, b[n].y, 0.0f, 0.0f, 0.0f, 0.0f);
+                    else mma_16816(acc[r][n], a0, a1, a2, a3, b[n].x, b[n].y);
                     mma_16816(acc[r][n], b0, b1, b2, b3, b[n].z, b[n].w);
                 }
             }
@@ -265,14 +229,14 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const __grid_constan
                 for (int n = 0; n < NT; ++n) {
                     if (n0 + n >= groups) break;
                     const Rows<D>& rows = ready[n0 + n];
-                    const float2 f = *reinterpret_cast<const float2*>(rows.factor + 2 * t), l = *reinterpret_cast<const float2*>(rows.less + 2 * t),
+                    const float2 l = *reinterpret_cast<const float2*>(rows.less + 2 * t),
                                  e = *reinterpret_cast<const float2*>(rows.share + 2 * t);
                     const int2 pos = *reinterpret_cast<const int2*>(rows.pos + 2 * t);
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
 #pragma unroll
                         for (int hh = 0; hh < 2; ++hh) {
-                            float p0 = ex2(fmaf(x[i][n][2 * hh], f.x, l.x)), p1 = ex2(fmaf(x[i][n][2 * hh + 1], f.y, l.y));
+                            float p0 = ex2(fmaf(x[i][n][2 * hh], P.scale_log2, l.x)), p1 = ex2(fmaf(x[i][n][2 * hh + 1], P.scale_log2, l.y));
                             if (!plain) {
                                 const int k = tok0 + i * kKvTokens + hh * 8 + g;
                                 p0 = k <= pos.x && (k > pos.x - window || k < a.sinks) ? p0 : 0.0f;
@@ -320,7 +284,7 @@ struct HeadBase {
 template <int D, int NT>
 struct FewRows {
     uint4 q[NT][D / 64][2];
-    float start[NT][D / 64][2], factor[NT][2], less[NT][2], share[NT][2];
+    float less[NT][2], share[NT][2];
     int pos[NT][2];
 };
 
@@ -361,7 +325,7 @@ __device__ __forceinline__ void load_tile(const HeadBase& base, const Place& pla
 }
 
 template <int D, int NT, bool kMasked>
-__device__ __forceinline__ void tile_sums(const Tile<D>& k, const FewRows<D, NT>& R, int tok0, int window, int sinks, float (&sum)[4]) {
+__device__ __forceinline__ void tile_sums(const Tile<D>& k, const FewRows<D, NT>& R, float scale, int tok0, int window, int sinks, float (&sum)[4]) {
     constexpr int NG = D / 64;
     const int g = (threadIdx.x & 31) >> 2;
 #pragma unroll
@@ -373,11 +337,11 @@ __device__ __forceinline__ void tile_sums(const Tile<D>& k, const FewRows<D, NT>
 #pragma unroll
             for (int v = 0; v < 2; ++v) {
                 const uint32_t a = k.w[i][0][2 * j + v], c = k.w[i][1][2 * j + v], as = a >> 8, cs = c >> 8;
-                const uint32_t a0 = raw_pair<0>(a, as), a1 = raw_pair<0>(c, cs), a2 = raw_pair<1>(a, as), a3 = raw_pair<1>(c, cs);
-                const uint32_t b0 = raw_pair<2>(a, as), b1 = raw_pair<2>(c, cs), b2 = raw_pair<3>(a, as), b3 = raw_pair<3>(c, cs);
+                const uint32_t a0 = codes<0>(a, as), a1 = codes<0>(c, cs), a2 = codes<1>(a, as), a3 = codes<1>(c, cs);
+                const uint32_t b0 = codes<2>(a, as), b1 = codes<2>(c, cs), b2 = codes<3>(a, as), b3 = codes<3>(c, cs);
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    if (v == 0) mma_from(acc[n], a0, a1, a2, a3, R.q[n][j][v].x, R.q[n][j][v].y, R.start[n][j][0], R.start[n][j][1], R.start[n][j][0], R.start[n][j][1]);
+                    if (v == 0) mma_from(acc[n], a0, a1, a2, a3, R.q[n][j][v].x, R.q[n][j][v].y, 0.0f, 0.0f, 0.0f, 0.0f);
                     else mma_16816(acc[n], a0, a1, a2, a3, R.q[n][j][v].x, R.q[n][j][v].y);
                     mma_16816(acc[n], b0, b1, b2, b3, R.q[n][j][v].z, R.q[n][j][v].w);
                 }
@@ -393,7 +357,7 @@ __device__ __forceinline__ void tile_sums(const Tile<D>& k, const FewRows<D, NT>
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-                float p = ex2(fmaf(x[n][e], R.factor[n][e & 1], R.less[n][e & 1]));
+                float p = ex2(fmaf(x[n][e], scale, R.less[n][e & 1]));
                 if constexpr (kMasked) {
                     const int tok = tok0 + i * kKvTokens + (e >> 1) * 8 + g;
                     p = tok <= R.pos[n][e & 1] && (tok > R.pos[n][e & 1] - window || tok < sinks) ? p : 0.0f;
@@ -411,7 +375,7 @@ constexpr int kFewBlocks = D == 256 ? 1 : D == 64 && NT == 1 ? 3 : 2;
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kFewThreads<D>, kFewBlocks<D, NT>) weigh_few_kernel(const __grid_constant__ Params P) {
-    constexpr int NG = D / 64, kThreads = kFewThreads<D>, kWarps = kThreads / 32;
+    constexpr int kThreads = kFewThreads<D>, kWarps = kThreads / 32;
     __shared__ uint64_t scan[kThreads + 1];
     __shared__ uint64_t warp_sums[kWarps];
     const WeighArgs& a = P.a;
@@ -456,18 +420,13 @@ __global__ void __launch_bounds__(kFewThreads<D>, kFewBlocks<D, NT>) weigh_few_k
         FewRows<D, NT> R;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            float sum[NG];
             const int mine = min(8 * n + g, r.rows - 1), qi = mine / P.group, head = h * P.group + mine - qi * P.group;
-            const float up = ready_fragments<D>(a.q + (r.q0 + qi) * a.q_stride + head * D, R.q[n], sum);
+            load_fragments<D>(a.q + (r.q0 + qi) * a.q_stride + head * D, R.q[n]);
             const bool real = 8 * n + g < r.rows;
             const LogSum l = log_sum_of(real ? a.lse[static_cast<int64_t>(r.q0 + qi) * a.heads + head] : -INFINITY, P.scale_rest);
-            const float f = real ? P.scale_log2 * up : 0.0f;
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
                 const int from = (2 * t + c) << 2;             // the columns' rows are those of lanes (2t + c, .)
-#pragma unroll
-                for (int j = 0; j < NG; ++j) R.start[n][j][c] = __shfl_sync(0xFFFFFFFFu, sum[j], from);
-                R.factor[n][c] = __shfl_sync(0xFFFFFFFFu, f, from);
                 R.less[n][c] = __shfl_sync(0xFFFFFFFFu, l.less, from);
                 R.share[n][c] = __shfl_sync(0xFFFFFFFFu, l.factor, from);
                 R.pos[n][c] = r.pos0 + __shfl_sync(0xFFFFFFFFu, qi, from);
@@ -481,8 +440,8 @@ __global__ void __launch_bounds__(kFewThreads<D>, kFewBlocks<D, NT>) weigh_few_k
             float sum[4] = {};
             if (seen(tile)) {
                 if ((here.page[0] | here.page[1]) >= 0 && tok0 + kTile - 1 <= r.pos0 && (tok0 > pos_hi - window || tok0 + kTile <= a.sinks))
-                    tile_sums<D, NT, false>(cur, R, tok0, window, a.sinks, sum);
-                else tile_sums<D, NT, true>(cur, R, tok0, window, a.sinks, sum);
+                    tile_sums<D, NT, false>(cur, R, P.scale_log2, tok0, window, a.sinks, sum);
+                else tile_sums<D, NT, true>(cur, R, P.scale_log2, tok0, window, a.sinks, sum);
             }
             // over the four lanes of a token; lane (g, t) keeps that of token 8 t + g
             const bool upper = t & 2, second = t & 1;
