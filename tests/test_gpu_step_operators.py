@@ -679,3 +679,99 @@ def test_refusals(pn):
     assert ok.refused.item() == 0 and bool((ok.kept == -1).all()) and torch.equal(ok.table, table)
     with pytest.raises(pn.PnError):                           # the state of a call may not be its output
         pn.kv_evict(cache, weights, ok.table, ok.lens, ok.held, free, ok.ring, 4, 4, out=ok)
+
+
+def test_bounded_cache_steps(pn):
+    """Steps of a batch whose requests are cut back again and again, against tokens, weights and attention kept in 64 bits:
+    outputs of attention over what is kept, gathered weights, what is kept, and no page lost."""
+    heads, kv, D, page, limit, budget, sinks, recent, scale = 4, 2, 64, 16, 40, 24, 2, 8, 0.2
+    B, group = 3, 2
+    g = torch.Generator(device="cuda").manual_seed(11)
+    most = -(-64 // page) + 1
+    F = B * (most + -(-budget // page))
+    cache = pn.kv_cache(F, page, kv, D)
+    weights = pn.kv_weights(cache)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    table, free, ring = torch.zeros(B, most, **i32), torch.arange(F, **i32), torch.tensor([0, F], device="cuda")
+    lens, held, gone = (torch.zeros(B, **i32) for _ in range(3))
+    ws = pn.AttentionWorkspace()
+    # of each request and head: keys, values, weights and first positions of what is kept
+    kept = [[dict(k=np.zeros((0, D)), v=np.zeros((0, D)), w=np.zeros(0), p=np.zeros(0, np.int64)) for _ in range(kv)] for _ in range(B)]
+    total, evictions = np.zeros(B, np.int64), 0
+    angle = torch.arange(200, device="cuda")[:, None] * 10000.0 ** (-torch.arange(0, D, 2, device="cuda") / D)
+    for turn in range(50):
+        counts = [30, 5, 50] if turn == 0 else [1, 1, 1] if turn % 7 else [1, 3, 2]
+        T = sum(counts)
+        q, k, v = (torch.randn(T, n, D, generator=g, device="cuda") for n in (heads, kv, kv))
+        plan = pn.kv_plan(lens, torch.tensor(counts, **i32), held, table, free, ring, page, T)
+        positions = plan.positions + gone[plan.requests.long()]
+        assert positions.tolist() == [int(total[b]) + i for b in range(B) for i in range(counts[b])]
+        q16 = pn.kv_append(q, k, v, cache, plan.slots, positions, angle.cos(), angle.sin())
+        out, lse = pn.attention(q16, cache, table, plan.lens, plan.starts, 50, scale, workspace=ws, return_lse=True)
+        pn.kv_weigh(q16, cache, table, plan.lens, plan.starts, 50, lse, scale, weights=weights)
+        ks, vs = (x.cpu().numpy().astype(np.float64) for x in pn.kv_read(cache, plan.slots))
+        qs, out = q16.cpu().numpy().astype(np.float64), out.cpu().numpy().astype(np.float64)
+        table_host, w_host = table.cpu().numpy(), weights.cpu().numpy()
+        row = 0
+        for b in range(B):
+            rows = slice(row, row + counts[b])
+            row += counts[b]
+            for h in range(kv):
+                s = kept[b][h]
+                s["k"], s["v"] = np.concatenate([s["k"], ks[rows, h]]), np.concatenate([s["v"], vs[rows, h]])
+                s["w"], s["p"] = np.concatenate([s["w"], np.zeros(counts[b])]), np.concatenate([s["p"], total[b] + np.arange(counts[b])])
+                L = len(s["w"])
+                for i, r in enumerate(range(rows.start, rows.stop)):
+                    see = np.arange(L) <= L - counts[b] + i
+                    for j in range(group):
+                        x = np.where(see, scale * (s["k"] @ qs[r, h * group + j]), -np.inf)
+                        p = np.exp(x - x.max())
+                        p /= p.sum()
+                        s["w"] += p
+                        # (attention's own bound with room: p d is rounded once, the output once)
+                        assert np.all(np.abs(out[r, h * group + j] - p @ s["v"]) <= 2.0 ** -9 * (p @ np.abs(s["v"])) + 2.0 ** -24)
+                t = np.arange(L)
+                mine = w_host[table_host[b, t // page], h, t % page]
+                assert np.all(np.abs(mine - s["w"]) <= 2.0 ** -14 * s["w"] + 1e-6)
+            total[b] += counts[b]
+        e = pn.kv_evict(cache, weights, table, plan.lens, plan.held, free, plan.ring, limit, budget, sinks, recent)
+        assert e.refused.item() == 0
+        chosen = e.kept.cpu().numpy()
+        for b in range(B):
+            if chosen[b, 0, 0] < 0:
+                continue
+            evictions += 1
+            for h in range(kv):
+                s, c = kept[b][h], chosen[b, h]
+                L = len(s["w"])
+                assert np.all(np.diff(c) > 0) and c[:sinks].tolist() == list(range(sinks)) and c[-recent:].tolist() == list(range(L - recent, L))
+                inner, dropped = c[sinks:-recent], np.setdiff1d(np.arange(sinks, L - recent), c)
+                if len(dropped):
+                    assert s["w"][inner].min() >= s["w"][dropped].max() * (1 - 2.0 ** -13) - 2e-6
+                for name in s:
+                    s[name] = s[name][c]
+        gone = gone + plan.lens - e.lens
+        table, lens, held, ring = e.table, e.lens, e.held, e.ring
+        h_host = held.tolist()
+        mine = [p for b in range(B) for p in table.cpu()[b, :h_host[b]].tolist()]
+        head, tail = ring.tolist()
+        assert sorted(mine + [int(free[i % F]) for i in range(head, tail)]) == list(range(F))
+        assert lens.tolist() == [len(kept[b][0]["w"]) for b in range(B)]
+    assert evictions >= 8 and ws.status() == 0
+
+
+def test_bounded_cache_example(pn):
+    import os
+    import sys
+    sys.path.insert(0, os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples"))
+    import bounded_cache as e
+    model = e.Model()
+    prompts = [[7, 8, 9, 7, 8], list(range(100, 163)), [3]]
+    whole, logprobs, pages = e.generate(model, prompts, 50, 4096, 4096)
+    assert all(len(t) == 50 and all(0 <= x < e.VOCAB for x in t) for t in whole)
+    assert bool((logprobs <= 0).all()) and pages == -(-(63 + 49) // e.PAGE)
+    # a limit that nothing reaches changes nothing; one that is reached bounds the pages
+    again, same, _ = e.generate(model, prompts, 50, 200, 100)
+    assert again == whole and torch.equal(same, logprobs)
+    cut, _, pages = e.generate(model, prompts, 50, 64, 48)
+    assert all(len(t) == 50 for t in cut) and pages <= -(-65 // e.PAGE)
