@@ -145,13 +145,13 @@ at::Tensor fresh(at::IntArrayRef size, at::ScalarType type) {
     return at::detail::empty_generic(size, c10::cuda::CUDACachingAllocator::get(), c10::DispatchKeySet(c10::DispatchKey::CUDA), type, std::nullopt);
 }
 
-// `n` entries from byte `at` on of a tensor of ours: another tensor on the same
+// Entries of a shape from byte `at` on of a tensor of ours: another tensor on the same
 // memory (an allocation takes more than a microsecond).
-at::Tensor part_of(const at::Tensor& t, int64_t at, int64_t n, at::ScalarType type) {
+at::Tensor part_of(const at::Tensor& t, int64_t at, at::IntArrayRef size, at::ScalarType type) {
     const caffe2::TypeMeta meta = c10::scalarTypeToTypeMeta(type);
     auto impl = c10::make_intrusive<c10::TensorImpl>(c10::Storage(t.storage()), t.key_set(), meta);
     impl->set_storage_offset(at / static_cast<int64_t>(meta.itemsize()));
-    impl->set_sizes_contiguous({n});
+    impl->set_sizes_contiguous(size);
     return at::Tensor(std::move(impl));
 }
 
@@ -211,7 +211,7 @@ PyObject* kv_plan(PyObject* const* a) {
         const at::Tensor all = fresh({narrow_at + (2 * T + 3 * B + 2) * 4}, at::kByte);
         for (int i = 0; i < 8; ++i) {
             int64_t& from = type_of(i) == at::kLong ? wide_at : narrow_at;
-            o[i] = part_of(all, from, sizes[i], type_of(i));
+            o[i] = part_of(all, from, {sizes[i]}, type_of(i));
             from += sizes[i] * (type_of(i) == at::kLong ? 8 : 4);
         }
     }
@@ -379,11 +379,19 @@ PyObject* logprobs(PyObject* const* a) {
     if (want_entropy < 0) throw PythonError{};
     const c10::cuda::CUDAGuard guard(logits.device());
     at::Tensor given, entropy, top_tokens, top_logprobs;
-    if (tokens) given = flat ? fresh({R}, at::kFloat) : fresh({R, count}, at::kFloat);
-    if (want_entropy) entropy = fresh({R}, at::kFloat);
+    // the outputs share an allocation
+    int64_t from = 0;
+    const at::Tensor all = fresh({4 * R * ((tokens ? count : 0) + (want_entropy ? 1 : 0) + 2 * top)}, at::kByte);
+    auto part = [&](at::IntArrayRef size, at::ScalarType type) {
+        const at::Tensor t = part_of(all, from, size, type);
+        from += 4 * t.numel();
+        return t;
+    };
+    if (tokens) given = flat ? part({R}, at::kFloat) : part({R, count}, at::kFloat);
+    if (want_entropy) entropy = part({R}, at::kFloat);
     if (top) {
-        top_tokens = fresh({R, top}, at::kInt);
-        top_logprobs = fresh({R, top}, at::kFloat);
+        top_tokens = part({R, top}, at::kInt);
+        top_logprobs = part({R, top}, at::kFloat);
     }
     const pn_status st = pn_logprobs(logits.data_ptr(), matrix_stride(logits), dtype_of(logits), R, static_cast<int>(V), scale, data<int32_t>(tokens),
                                      static_cast<int>(count), tokens ? data<float>(&given) : nullptr, want_entropy ? data<float>(&entropy) : nullptr, top,
@@ -509,10 +517,10 @@ PyObject* kv_evict(PyObject* const* a) {
         o[0] = fresh({B, table.size(1)}, at::kInt);
         o[4] = fresh({B, c.heads, budget}, at::kInt);
         const at::Tensor all = fresh({16 + (2 * B + 1) * 4}, at::kByte);       // the small ones share an allocation
-        o[3] = part_of(all, 0, 2, at::kLong);
-        o[1] = part_of(all, 16, B, at::kInt);
-        o[2] = part_of(all, 16 + 4 * B, B, at::kInt);
-        o[5] = part_of(all, 16 + 8 * B, 1, at::kInt);
+        o[3] = part_of(all, 0, {2}, at::kLong);
+        o[1] = part_of(all, 16, {B}, at::kInt);
+        o[2] = part_of(all, 16 + 4 * B, {B}, at::kInt);
+        o[5] = part_of(all, 16 + 8 * B, {1}, at::kInt);
     }
     const pn_status st = pn_kv_evict(c.t.data_ptr(), c.pages, c.page_size, c.heads, c.dim, data<float>(&weights), data<int32_t>(&table), table_stride(table),
                                      static_cast<int>(table.size(1)), data<int32_t>(&lens), data<int32_t>(&held), static_cast<int>(B), limit, budget, sinks,

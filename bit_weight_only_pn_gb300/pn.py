@@ -564,7 +564,8 @@ def verify(tokens: torch.Tensor, target: torch.Tensor, draft: torch.Tensor | Non
 
 
 class LogProbs(NamedTuple):
-    """What pn.logprobs gives of rows of logits; None where it was not asked for."""
+    """What pn.logprobs gives of rows of logits; None where it was not asked for.  The
+    four share one allocation, which lasts as long as any of them."""
     logprobs: torch.Tensor      # fp32 [rows] or [rows][count]: log probabilities of the given tokens
     entropy: torch.Tensor       # fp32 [rows]
     top_tokens: torch.Tensor    # int32 [rows][top], -1 where fewer have a probability
@@ -620,7 +621,8 @@ def kv_weigh(q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, lens: to
 
 
 class KvEviction(NamedTuple):
-    """The state after pn.kv_evict."""
+    """The state after pn.kv_evict.  lens, held, ring and refused share one allocation
+    (unless given as `out`)."""
     table: torch.Tensor         # int32 [batch][pages per request]: pages of a request cut back, then -1; others as they were
     lens: torch.Tensor          # int32 [batch]
     held: torch.Tensor          # int32 [batch]
