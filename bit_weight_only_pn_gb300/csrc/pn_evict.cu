@@ -7,8 +7,9 @@
 // reads is written (new pages were free, the table is written to another one), so a
 // call can be repeated and no block waits for another.
 //
-// Two launches.  select: a block to a request and head finds the kept positions.  It
-// holds the upper 15 bits of the weights, as whole numbers in their order, in shared
+// Two launches.  select: a block to a request and head (a cluster of up to 8 with a
+// share of the positions each, where there are few heads in all) finds the kept
+// positions.  It holds the upper 15 bits of the weights, as whole numbers in their order, in shared
 // memory (64 steps to a power of two); a histogram over their range gives the step with
 // the last kept weight, and the few weights of that step are ranked among themselves.
 // Then every warp counts in its share what is kept, and writes the positions behind
@@ -16,6 +17,7 @@
 // weights equal, say) or a request has more tokens than fit, histograms of 2048 bins fix
 // 11 bits of the last kept weight at a time, over weights read again each time.  move:
 // a warp to a record of 16 new tokens gathers their codes, scales and weights.
+#include <cooperative_groups.h>
 #include <cstdint>
 
 #include <cuda_fp16.h>
@@ -25,6 +27,8 @@
 #include "pn_internal.h"
 #include "pn_kv.cuh"
 
+namespace cg = cooperative_groups;
+
 namespace pn {
 namespace {
 
@@ -33,6 +37,7 @@ constexpr int kSelectWarps = kSelectThreads / 32;
 constexpr int kBins = 2048;
 constexpr int kMostKeys = 96 * 1024;           // of a block, whose upper bits are kept in shared memory
 constexpr int kLowBits = 17;                   // the others
+constexpr int kMostParts = 8;                  // blocks to a request and head
 constexpr int kMoveThreads = 256;
 constexpr int kMoveRecords = kMoveThreads / 32;        // of a block
 
@@ -107,8 +112,27 @@ __device__ __forceinline__ uint32_t key_of(float w) {
     return w == w ? (u & 0x80000000u ? ~u : u | 0x80000000u) : 0u;
 }
 
-// The range of the block's numbers: low, high of each thread; free again behind it.
-__device__ __forceinline__ void block_range(uint32_t& low, uint32_t& high, uint32_t* part0, uint32_t* part1) {
+// What the blocks of a request and head tell each other.
+struct Shared {
+    uint32_t bins[kBins];      // a histogram, then the candidates' keys and positions
+    uint32_t low, high;        // the range of the block's keys
+    uint32_t candidates;
+    uint32_t above, equal;     // kept in the block's share (equal: of those equal to the last kept key)
+};
+
+// The blocks of a request and head, one or a cluster.
+struct Team {
+    cg::cluster_group cluster;
+    int parts, rank;
+    __device__ __forceinline__ void sync() const {
+        if (parts > 1) cluster.sync();
+        else __syncthreads();
+    }
+    __device__ __forceinline__ const Shared& of(Shared* mine, int r) const { return parts > 1 ? *cluster.map_shared_rank(mine, r) : *mine; }
+};
+
+// The range of the team's keys, from low and high of each thread.
+__device__ __forceinline__ void team_range(const Team& team, Shared* s, uint32_t& low, uint32_t& high, uint32_t* part0, uint32_t* part1) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     low = __reduce_min_sync(0xFFFFFFFFu, low);
     high = __reduce_max_sync(0xFFFFFFFFu, high);
@@ -119,19 +143,33 @@ __device__ __forceinline__ void block_range(uint32_t& low, uint32_t& high, uint3
     __syncthreads();
     low = __reduce_min_sync(0xFFFFFFFFu, part0[lane % kSelectWarps]);
     high = __reduce_max_sync(0xFFFFFFFFu, part1[lane % kSelectWarps]);
-    __syncthreads();
+    if (threadIdx.x == 0) {
+        s->low = low;
+        s->high = high;
+    }
+    team.sync();
+    if (team.parts > 1) {
+        low = __reduce_min_sync(0xFFFFFFFFu, team.of(s, lane % team.parts).low);
+        high = __reduce_max_sync(0xFFFFFFFFu, team.of(s, lane % team.parts).high);
+    }
 }
 
-// The bin, from the largest down, with the `left`-th count; left becomes its place in
-// the bin and, returned in `in_bin`, what the bin holds.  Bins are complete and
-// synchronised before; every thread gets the answer.
-__device__ __forceinline__ uint32_t bin_of(const uint32_t* bins, uint32_t& left, uint32_t& in_bin, uint32_t* part, uint32_t* found) {
+// The bin, from the largest down, with the `left`-th count of the team's histogram,
+// whose blocks' bins are complete; left becomes its place in the bin and in_bin what the
+// bin holds.  Every thread gets the answer, and the bins may be written again.
+__device__ __forceinline__ uint32_t bin_of(const Team& team, Shared* s, uint32_t& left, uint32_t& in_bin, uint32_t* part, uint32_t* found) {
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     constexpr int kEach = kBins / kSelectThreads;      // of a thread
     const int top = kBins - 1 - static_cast<int>(threadIdx.x) * kEach;
-    uint32_t n[kEach], mine = 0;
+    team.sync();
+    uint32_t n[kEach] = {}, mine = 0;
+    for (int r = 0; r < team.parts; ++r) {
+        const Shared& other = team.of(s, r);
 #pragma unroll
-    for (int i = 0; i < kEach; ++i) mine += n[i] = bins[top - i];
+        for (int i = 0; i < kEach; ++i) n[i] += other.bins[top - i];
+    }
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) mine += n[i];
     uint32_t in = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -148,30 +186,32 @@ __device__ __forceinline__ uint32_t bin_of(const uint32_t* bins, uint32_t& left,
         found[1] = left - above;
         found[2] = n[i];
     }
-    __syncthreads();
+    team.sync();
     left = found[1];
     in_bin = found[2];
-    const uint32_t bin = found[0];
-    __syncthreads();
-    return bin;
+    return found[0];
 }
 
 __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_constant__ Params P) {
     extern __shared__ uint16_t upper[];        // [P.keys], kMark: kept among those of the last kept weight's step
-    __shared__ uint32_t bins[kBins];
+    __shared__ Shared s;
     __shared__ int64_t part[kSelectWarps];
     __shared__ uint32_t warp_above[kSelectWarps], warp_equal[kSelectWarps];
-    __shared__ uint32_t found[3], candidates;
+    __shared__ uint32_t found[3];
     constexpr uint16_t kMark = 0xFFFF;
     const EvictArgs& a = P.a;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, heads = P.cache.heads;
-    if (blockIdx.x == static_cast<unsigned>(a.batch) * heads) {
-        totals(P, part);
+    Team team{cg::this_cluster(), 0, 0};
+    team.parts = static_cast<int>(team.cluster.num_blocks());
+    team.rank = static_cast<int>(team.cluster.block_rank());
+    const int64_t index = blockIdx.x / team.parts;     // of the request and head
+    if (index == static_cast<int64_t>(a.batch) * heads) {
+        if (team.rank == 0) totals(P, part);
         return;
     }
-    const int b = static_cast<int>(blockIdx.x) / heads, h = static_cast<int>(blockIdx.x) % heads;
+    const int b = static_cast<int>(index / heads), h = static_cast<int>(index % heads);
     const int len = length_of(P, b);
-    int32_t* kept = a.kept + static_cast<int64_t>(blockIdx.x) * a.budget;
+    int32_t* kept = a.kept + index * a.budget;
     const int32_t* row = a.table + static_cast<int64_t>(b) * a.table_stride;
     bool served = len > a.limit;
     int64_t turn = 0, behind = 0;              // requests past the limit before this one, and the pages that they give back
@@ -187,7 +227,7 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
         }
         served = turn < most_served(P);
     }
-    if (h == 0) {
+    if (h == 0 && team.rank == 0) {
         const int held = held_of(P, b);
         int32_t* out = a.table_out + static_cast<int64_t>(b) * a.out_stride;
         for (int i = threadIdx.x; i < a.max_pages; i += kSelectThreads)
@@ -199,29 +239,40 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
             a.held_out[b] = served ? P.each : a.held[b];
         }
     }
+    const int everyone = team.rank * kSelectThreads + threadIdx.x, all_threads = team.parts * kSelectThreads;
     if (!served) {
-        for (int i = threadIdx.x; i < a.budget; i += kSelectThreads) kept[i] = -1;
+        for (int i = everyone; i < a.budget; i += all_threads) kept[i] = -1;
         return;
     }
-    for (int i = threadIdx.x; i < a.sinks; i += kSelectThreads) kept[i] = i;
-    for (int i = threadIdx.x; i < a.recent; i += kSelectThreads) kept[a.budget - a.recent + i] = len - a.recent + i;
-    const int count = len - a.sinks - a.recent, need = a.budget - a.sinks - a.recent;      // count > need
+    for (int i = everyone; i < a.sinks; i += all_threads) kept[i] = i;
+    for (int i = everyone; i < a.recent; i += all_threads) kept[a.budget - a.recent + i] = len - a.recent + i;
+    const int all = len - a.sinks - a.recent, need = a.budget - a.sinks - a.recent;        // all > need
     if (need == 0) return;
-    auto weight_key = [&](int i) -> uint32_t {         // of position sinks + i
-        const int tok = a.sinks + i, page = row[tok >> P.cache.page_shift];
+    // the block's share of the positions between
+    const int begin = static_cast<int>(static_cast<int64_t>(all) * team.rank / team.parts), count = static_cast<int>(static_cast<int64_t>(all) * (team.rank + 1) / team.parts) - begin;
+    const int first_tok = a.sinks + begin;
+    auto weight_key = [&](int i) -> uint32_t {         // of position first_tok + i
+        const int tok = first_tok + i, page = row[tok >> P.cache.page_shift];
         const bool there = page >= 0 && page < P.cache.pages;
         // (loaded in any case: under a branch every load waits for the one before)
         const float w = __ldcg(a.weights + ((static_cast<int64_t>(there ? page : 0) * heads + h) << P.cache.page_shift) + (tok & (P.cache.page_size - 1)));
         return there ? key_of(w) : 0u;
     };
     const uint32_t lower = (1u << lane) - 1u;
-    // a contiguous share of the positions to each warp
+    // a contiguous share of them to each warp
     const int share = (count + kSelectWarps * 32 - 1) / (kSelectWarps * 32) * 32;
     const int i0 = min(warp * share, count), i1 = min(i0 + share, count);
-    if (count <= P.keys) {
+    // places of what the warps, then the blocks, before this one keep
+    auto before_of = [&](const uint32_t* warps, uint32_t Shared::*block) {
+        uint32_t n = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? warps[lane] : 0u);
+        if (team.parts > 1) n += __reduce_add_sync(0xFFFFFFFFu, lane < team.rank ? team.of(&s, min(lane, team.parts - 1)).*block : 0u);
+        return n;
+    };
+    constexpr int kAtOnce = 8;                 // loads of a thread on their way together
+    // (the last share is no smaller than the others: all blocks take the same way)
+    if ((all + team.parts - 1) / team.parts <= P.keys) {
         // the upper bits of all keys, and their range
         uint32_t low = 0xFFFFFFFFu, high = 0u;
-        constexpr int kAtOnce = 8;             // loads of a thread on their way together
         for (int first = threadIdx.x; first < count; first += kAtOnce * kSelectThreads) {
             uint32_t k[kAtOnce];
 #pragma unroll
@@ -234,29 +285,36 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
                 high = max(high, k[j]);
             }
         }
-        for (int i = threadIdx.x; i < kBins; i += kSelectThreads) bins[i] = 0;
-        if (threadIdx.x == 0) candidates = 0;
-        block_range(low, high, warp_above, warp_equal);
+        for (int i = threadIdx.x; i < kBins; i += kSelectThreads) s.bins[i] = 0;
+        if (threadIdx.x == 0) s.candidates = 0;
+        team_range(team, &s, low, high, warp_above, warp_equal);
         // (of more than 2048 steps several share a bin)
         const int shift = max(21 - __clz(high - low), 0);
 #pragma unroll 4
-        for (int i = threadIdx.x; i < count; i += kSelectThreads) atomicAdd(&bins[(upper[i] - low) >> shift], 1u);
-        __syncthreads();
+        for (int i = threadIdx.x; i < count; i += kSelectThreads) atomicAdd(&s.bins[(upper[i] - low) >> shift], 1u);
         uint32_t left = static_cast<uint32_t>(need), in_bin;
-        const uint32_t bin = bin_of(bins, left, in_bin, warp_above, found);
+        const uint32_t bin = bin_of(team, &s, left, in_bin, warp_above, found);
         if (in_bin <= kBins / 2) {
             // keys and positions of the bin's, in the histogram's place; those kept get the mark
-            uint2* list = reinterpret_cast<uint2*>(bins);
+            uint2* list = reinterpret_cast<uint2*>(s.bins);
             const uint32_t from = low + (bin << shift), range = (1u << shift) - 1u;
 #pragma unroll 4
             for (int i = threadIdx.x; i < count; i += kSelectThreads)
-                if (upper[i] - from <= range) list[atomicAdd(&candidates, 1u)] = make_uint2(weight_key(i), static_cast<uint32_t>(i));
-            __syncthreads();
-            for (uint32_t c = threadIdx.x; c < in_bin; c += kSelectThreads) {
+                if (upper[i] - from <= range) list[atomicAdd(&s.candidates, 1u)] = make_uint2(weight_key(i), static_cast<uint32_t>(begin + i));
+            team.sync();
+            for (uint32_t c = threadIdx.x; c < s.candidates; c += kSelectThreads) {
                 const uint2 mine = list[c];
                 uint32_t place = 0;
-                for (uint32_t o = 0; o < in_bin; ++o) place += list[o].x > mine.x || (list[o].x == mine.x && list[o].y < mine.y);
-                if (place < left) upper[mine.y] = kMark;
+                for (int r = 0; r < team.parts; ++r) {
+                    const Shared& other = team.of(&s, r);
+                    const uint2* theirs = reinterpret_cast<const uint2*>(other.bins);
+                    const uint32_t n = other.candidates;
+                    for (uint32_t o = 0; o < n; ++o) {
+                        const uint2 x = theirs[o];
+                        place += x.x > mine.x || (x.x == mine.x && x.y < mine.y);
+                    }
+                }
+                if (place < left) upper[mine.y - begin] = kMark;
             }
             __syncthreads();
             const uint32_t above_bin = from + range;
@@ -266,16 +324,23 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
             mine = __reduce_add_sync(0xFFFFFFFFu, mine);
             if (lane == 0) warp_above[warp] = mine;
             __syncthreads();
-            int to = a.sinks + static_cast<int>(__reduce_add_sync(0xFFFFFFFFu, lane < warp ? warp_above[lane] : 0u));
+            if (team.parts > 1) {
+                if (threadIdx.x < 32) {
+                    const uint32_t n = __reduce_add_sync(0xFFFFFFFFu, lane < kSelectWarps ? warp_above[lane] : 0u);
+                    if (lane == 0) s.above = n;
+                }
+                team.sync();
+            }
+            int to = a.sinks + static_cast<int>(before_of(warp_above, &Shared::above));
 #pragma unroll 4
             for (int i = i0; i < i1; i += 32) {
                 const uint32_t in = __ballot_sync(0xFFFFFFFFu, i + lane < i1 && upper[min(i + lane, i1 - 1)] > above_bin);
-                if ((in >> lane) & 1u) kept[to + __popc(in & lower)] = a.sinks + i + lane;
+                if ((in >> lane) & 1u) kept[to + __popc(in & lower)] = first_tok + i + lane;
                 to += __popc(in);
             }
+            if (team.parts > 1) team.sync();   // no block leaves while another may read from it
             return;
         }
-        __syncthreads();                       // bins are cleared again
     }
     // bit by bit over whole keys
     uint32_t low = 0xFFFFFFFFu, high = 0u;
@@ -285,21 +350,21 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
         low = min(low, k);
         high = max(high, k);
     }
-    block_range(low, high, warp_above, warp_equal);
+    __syncthreads();
+    team_range(team, &s, low, high, warp_above, warp_equal);
     // the smallest kept key, from `least` on below 2^bits more, and how many of those equal to it are kept
     uint32_t least = low, left = static_cast<uint32_t>(need), in_bin;
     for (int bits = 32 - __clz(high - low);;) {
         const int shift = max(bits - 11, 0);
         const uint32_t range = bits == 32 ? 0xFFFFFFFFu : (1u << bits) - 1u;
-        for (int i = threadIdx.x; i < kBins; i += kSelectThreads) bins[i] = 0;
+        for (int i = threadIdx.x; i < kBins; i += kSelectThreads) s.bins[i] = 0;
         __syncthreads();
 #pragma unroll 4
         for (int i = threadIdx.x; i < count; i += kSelectThreads) {
             const uint32_t k = weight_key(i) - least;  // (smaller keys: past the range)
-            if (k <= range) atomicAdd(&bins[k >> shift], 1u);
+            if (k <= range) atomicAdd(&s.bins[k >> shift], 1u);
         }
-        __syncthreads();
-        least += bin_of(bins, left, in_bin, warp_above, found) << shift;
+        least += bin_of(team, &s, left, in_bin, warp_above, found) << shift;
         if (shift == 0) break;
         bits = shift;
     }
@@ -312,23 +377,38 @@ __global__ void __launch_bounds__(kSelectThreads) select_kernel(const __grid_con
     }
     above = __reduce_add_sync(0xFFFFFFFFu, above);
     equal = __reduce_add_sync(0xFFFFFFFFu, equal);
+    __syncthreads();
     if (lane == 0) {
         warp_above[warp] = above;
         warp_equal[warp] = equal;
     }
     __syncthreads();
-    above = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? warp_above[lane] : 0u);
-    equal = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? warp_equal[lane] : 0u);
+    if (team.parts > 1) {
+        if (threadIdx.x < 32) {
+            const uint32_t n = __reduce_add_sync(0xFFFFFFFFu, lane < kSelectWarps ? warp_above[lane] : 0u);
+            const uint32_t m = __reduce_add_sync(0xFFFFFFFFu, lane < kSelectWarps ? warp_equal[lane] : 0u);
+            if (lane == 0) {
+                s.above = n;
+                s.equal = m;
+            }
+        }
+        team.sync();
+    }
+    above = before_of(warp_above, &Shared::above);
+    equal = before_of(warp_equal, &Shared::equal);
 #pragma unroll 4
     for (int i = i0; i < i1; i += 32) {
         const uint32_t k = weight_key(min(i + lane, i1 - 1));
         const uint32_t up = __ballot_sync(0xFFFFFFFFu, i + lane < i1 && k > least), same = __ballot_sync(0xFFFFFFFFu, i + lane < i1 && k == least);
         const uint32_t before = equal + __popc(same & lower);
-        if (((up >> lane) & 1u) || (((same >> lane) & 1u) && before < left))
-            kept[a.sinks + above + __popc(up & lower) + min(before, left)] = a.sinks + i + lane;
+        const uint32_t place = above + __popc(up & lower) + min(before, left);
+        // (place < need in any case, but for weights that another call changes meanwhile)
+        if ((((up >> lane) & 1u) || (((same >> lane) & 1u) && before < left)) && place < static_cast<uint32_t>(need))
+            kept[a.sinks + place] = first_tok + i + lane;
         above += __popc(up);
         equal += __popc(same);
     }
+    if (team.parts > 1) team.sync();           // no block leaves while another may read from it
 }
 
 // Bytes of kv_record_bytes(D) / 16 that a token has in a record lie in pieces: of K
@@ -360,7 +440,8 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const __grid_constan
         int place = 0;
         float weight = 0.0f;
         if ((lane & 15) < have) {
-            const int tok = kept[to_tok + (lane & 15)], page = from_row[tok >> P.cache.page_shift];
+            const int tok = kept[to_tok + (lane & 15)], at = tok >> P.cache.page_shift;
+            const int page = at >= 0 && at < a.max_pages ? from_row[at] : -1;
             if (page >= 0 && page < P.cache.pages) {
                 const int in_page = tok & (P.cache.page_size - 1);
                 from = P.cache.record((static_cast<int64_t>(page) << P.cache.page_shift) + in_page, h);
@@ -435,12 +516,26 @@ cudaError_t launch_evict(const EvictArgs& a, const KvGeometry& g, int num_sms, c
     int shift = 0;
     while ((1 << shift) < g.page_size) ++shift;
     const int64_t room = static_cast<int64_t>(a.max_pages) * g.page_size;
-    const int64_t keys = room < kMostKeys ? room + room % 2 : kMostKeys;
+    // blocks to a request and head: until the GPU is full, none with less than 2048 positions
+    const int64_t teams = static_cast<int64_t>(a.batch) * g.heads;
+    int parts = 1;
+    while (parts < kMostParts && teams * parts * 2 <= num_sms * 2 && room / (parts * 2) >= 2048) parts *= 2;
+    const int64_t each = (room + parts - 1) / parts, keys = each < kMostKeys ? each + each % 2 : kMostKeys;
     const Params P{a, KvCache{g.data, g.pages, g.page_size, shift, g.heads, g.D}, (a.budget + g.page_size - 1) / g.page_size, static_cast<int>(keys)};
     static std::atomic<uint64_t> smem_set{0};
     if (cudaError_t e = set_smem_limit_once(select_kernel, kMostKeys * 2, smem_set); e != cudaSuccess) return e;
-    select_kernel<<<static_cast<unsigned>(a.batch) * g.heads + 1, kSelectThreads, P.keys * 2, s>>>(P);
-    if (cudaError_t e = cudaGetLastError(); e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3(static_cast<unsigned>((teams + 1) * parts));
+    cfg.blockDim = dim3(kSelectThreads);
+    cfg.dynamicSmemBytes = P.keys * 2;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = parts;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    if (cudaError_t e = cudaLaunchKernelEx(&cfg, select_kernel, P); e != cudaSuccess) return e;
     if (g.D == 64) return move<64>(P, s);
     return g.D == 128 ? move<128>(P, s) : move<256>(P, s);
 }

@@ -585,6 +585,30 @@ def test_evict_weights(pn, kind):
     check_evict(pn, case, 200, 100, 3, 10)
 
 
+@pytest.mark.parametrize("kind", ["random", "equal", "few", "close", "zeros"])
+@pytest.mark.parametrize("lens,kv,page,limit,budget,sinks,recent", [
+    ([4100], 1, 16, 4000, 300, 2, 5),                  # shares of few positions to a block
+    ([9000, 2, 8190], 2, 64, 5000, 5000, 0, 0),
+    ([33333, 16385], 1, 128, 16000, 1000, 16, 64),
+    ([850000], 1, 1024, 800000, 2000, 4, 100),         # more than a block's keys
+])
+def test_evict_split(pn, lens, kv, page, limit, budget, sinks, recent, kind):
+    """Few and long requests: several blocks share a request and head."""
+    case = list(evict_case(lens, kv, 64, page, budget, seed=9))
+    rng = np.random.default_rng(2)
+    w = case[1]
+    if kind == "equal":
+        w[:] = 0.25
+    elif kind == "few":
+        w[:] = rng.integers(0, 5, w.shape)
+    elif kind == "close":
+        w[:] = 1 + np.float32(2.0 ** -23) * rng.integers(0, 3000, w.shape)
+    elif kind == "zeros":                              # all that counts in one block's share
+        w[:] = 0
+        w[case[2][0, :4]] = rng.random((4, kv, page))
+    check_evict(pn, case, limit, budget, sinks, recent)
+
+
 def test_evict_pages_outside(pn):
     """Old pages outside the cache: their tokens come last and become zeros; new ones outside: nothing is written there."""
     case = list(evict_case([200, 180], 1, 128, 16, 150, seed=2))
