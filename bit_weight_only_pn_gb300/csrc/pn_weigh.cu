@@ -12,6 +12,11 @@
 // stay in registers while the query rows go by, and each lane sums what its columns
 // give.  A token's sum is made by one warp in a fixed order; nothing is joined and
 // no result depends on timing.
+//
+// Three kernels, by the rows (queries of a request, at most, times heads that share a
+// key/value head): here that for few of them, and the one for more heads to a key/value
+// head than the tensor memory's kernel (pn_weigh_tc.cu) has columns for.
+#include <atomic>
 #include <cstdint>
 
 #include <cuda_fp16.h>
@@ -253,14 +258,18 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const __grid_constan
 
 // ---------------------------------------------------- few rows to a head --
 //
-// Up to 8 NT query rows, ready in a warp's registers.  Every warp takes a contiguous
-// range of the call's tiles (request, head, 32 tokens) and works alone: the next
-// tile's codes, scales and weights are on their way while it multiplies, and the
-// pages of the one behind that are being looked up.
+// Every warp takes a contiguous range of the call's tiles (request, head, 32 tokens) and
+// works alone: the next tile's codes, scales and weights are on their way while it
+// multiplies, and the pages of the one behind that are being looked up.  The rows of the
+// request and head are ready in the warp's registers, up to 8 (heads of 64: 16), or in its
+// own part of shared memory, where 8 NT of them at a time meet the tile's codes.
 //
-// 64 ragged requests to 16384 tokens, 32 + 8 heads of 128: bound by memory and the
-// instructions for it; with a tile's registers copied, masks worked out for every tile
-// and places in 64 bits throughout, a tile took 600 instructions and the call 101 us.
+// 64 ragged requests to 16384 tokens, 32 + 8 heads of 128, one query each: 71 us, 4.5 TB/s
+// of what it has to read and write.  Bound by memory and the instructions for it: with a
+// tile's registers copied, masks worked out for every tile and places in 64 bits
+// throughout, a tile took 600 instructions and the call 101 us.  With 5 queries
+// each (20 rows) it takes 121 us, with 11 (44) 211, where blocks that share rows and wait
+// for each other took 291 and 368: those waited, these are bound by instructions.
 
 template <int D>
 struct Tile {
@@ -367,15 +376,77 @@ __device__ __forceinline__ void tile_sums(const Tile<D>& k, const FewRows<D, NT>
     }
 }
 
+// The same with rows in shared memory, which are read once for both records.
+template <int D, int NT, bool kMasked>
+__device__ __forceinline__ void tile_sums(const Tile<D>& k, const Rows<D>* rows, float scale, int tok0, int window, int sinks, float (&sum)[4]) {
+    constexpr int NG = D / 64;
+    const int lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+    float x[2][NT][4];
+#pragma unroll
+    for (int j = 0; j < NG; ++j) {
+        float acc[2][NT][4];
+#pragma unroll
+        for (int v = 0; v < 2; ++v) {
+            uint4 b[NT];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) b[n] = rows[n].q[j][v][lane];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const uint32_t a = k.w[i][0][2 * j + v], c = k.w[i][1][2 * j + v], as = a >> 8, cs = c >> 8;
+                const uint32_t a0 = codes<0>(a, as), a1 = codes<0>(c, cs), a2 = codes<1>(a, as), a3 = codes<1>(c, cs);
+                const uint32_t b0 = codes<2>(a, as), b1 = codes<2>(c, cs), b2 = codes<3>(a, as), b3 = codes<3>(c, cs);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    if (v == 0) mma_from(acc[i][n], a0, a1, a2, a3, b[n].x, b[n].y, 0.0f, 0.0f, 0.0f, 0.0f);
+                    else mma_16816(acc[i][n], a0, a1, a2, a3, b[n].x, b[n].y);
+                    mma_16816(acc[i][n], b0, b1, b2, b3, b[n].z, b[n].w);
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const float d0 = half_bits_to_float(j & 1 ? k.d[i][0][j / 2] >> 16 : k.d[i][0][j / 2] & 0xFFFFu);
+            const float d1 = half_bits_to_float(j & 1 ? k.d[i][1][j / 2] >> 16 : k.d[i][1][j / 2] & 0xFFFFu);
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[i][n][e] = j ? fmaf(e < 2 ? d0 : d1, acc[i][n][e], x[i][n][e]) : (e < 2 ? d0 : d1) * acc[i][n][e];
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const float2 less = *reinterpret_cast<const float2*>(rows[n].less + 2 * t), share = *reinterpret_cast<const float2*>(rows[n].share + 2 * t);
+        int2 pos{};
+        if constexpr (kMasked) pos = *reinterpret_cast<const int2*>(rows[n].pos + 2 * t);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                float p = ex2(fmaf(x[i][n][e], scale, e & 1 ? less.y : less.x));
+                if constexpr (kMasked) {
+                    const int tok = tok0 + i * kKvTokens + (e >> 1) * 8 + g, at = e & 1 ? pos.y : pos.x;
+                    p = tok <= at && (tok > at - window || tok < sinks) ? p : 0.0f;
+                }
+                sum[2 * i + (e >> 1)] = fmaf(p, e & 1 ? share.y : share.x, sum[2 * i + (e >> 1)]);
+            }
+    }
+}
+
 // Threads of a block and blocks to an SM: registers for a tile, the next one and the rows.
-template <int D>
-constexpr int kFewThreads = D == 256 ? 384 : 256;
+// (16 rows of 128 in registers spilled: 61 us for 64 ragged requests and 4 heads, 50 from
+// shared memory; of 64, 33 and 39)
 template <int D, int NT>
-constexpr int kFewBlocks = D == 256 ? 1 : D == 64 && NT == 1 ? 3 : 2;
+constexpr bool kFewShared = NT > (D == 64 ? 2 : 1);
+template <int D, int NT>
+constexpr int kFewThreads = D == 256 || kFewShared<D, NT> ? 384 : 256;
+template <int D, int NT>
+constexpr int kFewBlocks = D == 256 || kFewShared<D, NT> ? 1 : D == 64 && NT == 1 ? 3 : 2;
 
 template <int D, int NT>
-__global__ void __launch_bounds__(kFewThreads<D>, kFewBlocks<D, NT>) weigh_few_kernel(const __grid_constant__ Params P) {
-    constexpr int kThreads = kFewThreads<D>, kWarps = kThreads / 32;
+__global__ void __launch_bounds__(kFewThreads<D, NT>, kFewBlocks<D, NT>) weigh_few_kernel(const __grid_constant__ Params P, int groups) {
+    constexpr int kThreads = kFewThreads<D, NT>, kWarps = kThreads / 32;
+    constexpr bool kShared = kFewShared<D, NT>;
+    extern __shared__ __align__(16) uint8_t few_smem[];        // kShared: Rows<D> [kWarps][groups], groups a multiple of NT
     __shared__ uint64_t scan[kThreads + 1];
     __shared__ uint64_t warp_sums[kWarps];
     const WeighArgs& a = P.a;
@@ -417,19 +488,26 @@ __global__ void __launch_bounds__(kFewThreads<D>, kFewBlocks<D, NT>) weigh_few_k
         look(min(first + 1, last - 1), page);
         Tile<D> even, odd;
         load_tile<D>(base, here, first * kTile, in_page, kept(first), even);
-        FewRows<D, NT> R;
-#pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int mine = min(8 * n + g, r.rows - 1), qi = mine / P.group, head = h * P.group + mine - qi * P.group;
-            load_fragments<D>(a.q + (r.q0 + qi) * a.q_stride + head * D, R.q[n]);
-            const bool real = 8 * n + g < r.rows;
-            const LogSum l = log_sum_of(real ? a.lse[static_cast<int64_t>(r.q0 + qi) * a.heads + head] : -INFINITY, P.scale_rest);
-#pragma unroll
-            for (int c = 0; c < 2; ++c) {
-                const int from = (2 * t + c) << 2;             // the columns' rows are those of lanes (2t + c, .)
-                R.less[n][c] = __shfl_sync(0xFFFFFFFFu, l.less, from);
-                R.share[n][c] = __shfl_sync(0xFFFFFFFFu, l.factor, from);
-                R.pos[n][c] = r.pos0 + __shfl_sync(0xFFFFFFFFu, qi, from);
+        FewRows<D, kShared ? 1 : NT> R;
+        Rows<D>* const ready = reinterpret_cast<Rows<D>*>(few_smem) + warp * groups;
+        if constexpr (kShared) {
+            __syncwarp();                      // the rows before have been read
+            for (int n = 0; n < groups; ++n) make_ready<D>(P, r, h, 8 * n, ready[n]);
+            __syncwarp();
+        } else {
+    #pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                const int mine = min(8 * n + g, r.rows - 1), qi = mine / P.group, head = h * P.group + mine - qi * P.group;
+                load_fragments<D>(a.q + (r.q0 + qi) * a.q_stride + head * D, R.q[n]);
+                const bool real = 8 * n + g < r.rows;
+                const LogSum l = log_sum_of(real ? a.lse[static_cast<int64_t>(r.q0 + qi) * a.heads + head] : -INFINITY, P.scale_rest);
+    #pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    const int from = (2 * t + c) << 2;             // the columns' rows are those of lanes (2t + c, .)
+                    R.less[n][c] = __shfl_sync(0xFFFFFFFFu, l.less, from);
+                    R.share[n][c] = __shfl_sync(0xFFFFFFFFu, l.factor, from);
+                    R.pos[n][c] = r.pos0 + __shfl_sync(0xFFFFFFFFu, qi, from);
+                }
             }
         }
         auto step = [&](int tile, const Tile<D>& cur, Tile<D>& next) {
@@ -439,8 +517,12 @@ __global__ void __launch_bounds__(kFewThreads<D>, kFewBlocks<D, NT>) weigh_few_k
             look(min(tile + 2, last - 1), page);
             float sum[4] = {};
             if (seen(tile)) {
-                if ((here.page[0] | here.page[1]) >= 0 && tok0 + kTile - 1 <= r.pos0 && (tok0 > pos_hi - window || tok0 + kTile <= a.sinks))
-                    tile_sums<D, NT, false>(cur, R, P.scale_log2, tok0, window, a.sinks, sum);
+                const bool plain = (here.page[0] | here.page[1]) >= 0 && tok0 + kTile - 1 <= r.pos0 && (tok0 > pos_hi - window || tok0 + kTile <= a.sinks);
+                if constexpr (kShared) {
+                    for (int n = 0; n < groups; n += NT)
+                        if (plain) tile_sums<D, NT, false>(cur, ready + n, P.scale_log2, tok0, window, a.sinks, sum);
+                        else tile_sums<D, NT, true>(cur, ready + n, P.scale_log2, tok0, window, a.sinks, sum);
+                } else if (plain) tile_sums<D, NT, false>(cur, R, P.scale_log2, tok0, window, a.sinks, sum);
                 else tile_sums<D, NT, true>(cur, R, P.scale_log2, tok0, window, a.sinks, sum);
             }
             // over the four lanes of a token; lane (g, t) keeps that of token 8 t + g
@@ -466,13 +548,34 @@ __global__ void __launch_bounds__(kFewThreads<D>, kFewBlocks<D, NT>) weigh_few_k
     }
 }
 
+template <int D, int NT>
+cudaError_t launch_few(const Params& P, int groups, int num_sms, cudaStream_t s) {
+    groups = (groups + NT - 1) / NT * NT;
+    size_t smem = 0;
+    if constexpr (kFewShared<D, NT>) {
+        smem = sizeof(Rows<D>) * groups * (kFewThreads<D, NT> / 32);
+        static std::atomic<uint64_t> smem_set{0};
+        if (cudaError_t e = set_smem_limit_once(weigh_few_kernel<D, NT>, static_cast<int>(sizeof(Rows<D>) * (weigh_few_rows(D) / 8) * (kFewThreads<D, NT> / 32)), smem_set); e != cudaSuccess) return e;
+    }
+    weigh_few_kernel<D, NT><<<num_sms * kFewBlocks<D, NT>, kFewThreads<D, NT>, smem, s>>>(P, groups);
+    return cudaGetLastError();
+}
+
 template <int D>
 cudaError_t launch(const Params& P, int num_sms, cudaStream_t s) {
     const int64_t rows = static_cast<int64_t>(P.a.max_queries) * P.group;
-    if (rows <= 8) weigh_few_kernel<D, 1><<<num_sms * kFewBlocks<D, 1>, kFewThreads<D>, 0, s>>>(P);
-    else if (D < 256 && rows <= 16) weigh_few_kernel<D, D == 256 ? 1 : 2><<<num_sms * 2, kFewThreads<D>, 0, s>>>(P);
-    else weigh_kernel<D><<<num_sms * 2, kThreads, 0, s>>>(P);
-    return cudaGetLastError();
+    if (rows > weigh_few_rows(D)) {
+        weigh_kernel<D><<<num_sms * 2, kThreads, 0, s>>>(P);
+        return cudaGetLastError();
+    }
+    const int groups = static_cast<int>((rows + 7) / 8);
+    if (groups == 1) return launch_few<D, 1>(P, groups, num_sms, s);
+    if (D == 256 || groups == 2) return launch_few<D, 2>(P, groups, num_sms, s);
+    if constexpr (D < 256) {
+        // three or four at a time, whichever computes fewer that are none
+        if ((groups + 3) / 4 * 4 <= (groups + 2) / 3 * 3) return launch_few<D, 4>(P, groups, num_sms, s);
+        return launch_few<D, 3>(P, groups, num_sms, s);
+    }
 }
 
 }  // namespace

@@ -103,7 +103,15 @@ __device__ __forceinline__ void locate(const WeighParams& P, const uint64_t* sca
     unit = static_cast<int>(u - h * of_head);
 }
 
-// The kernel for many query rows to a key/value head (pn_weigh_tc.cu).
+// Query rows to a key/value head up to which a warp takes its tokens through all of
+// them (weigh_few_kernel); a warp's share of shared memory holds no more.  Above, where
+// heads allow it, the kernel for many rows (pn_weigh_tc.cu).  Microseconds here, there; 64
+// ragged requests to 16384 tokens, 4 key/value heads:
+//   of 64:  64 rows 89, 153; 96 rows 125, 171
+//   of 128: 48 rows 104, 172; 64 rows 144, 176
+//   of 256: 12 rows 90, 204; 32 rows 175, 196
+// One request of 8192 and 96, 64, 32 rows of 64, 128, 256: 13.7, 12.0; 13.1, 12.2; 12.7, 12.9.
+constexpr int weigh_few_rows(int head_dim) { return head_dim == 64 ? 96 : head_dim == 128 ? 64 : 32; }
 bool weigh_tc_takes(const WeighArgs& a, const KvGeometry& g);
 cudaError_t launch_weigh_tc(const WeighParams& P, int num_sms, cudaStream_t s);
 

@@ -717,18 +717,11 @@ cudaError_t launch(const WeighParams& W, int num_sms, cudaStream_t s) {
 
 }  // namespace
 
-// By the rows of a call, as if every request had max_queries queries: the other kernel
-// for more than 16 rows takes its tokens' codes through the products 8 or 16 rows at a
-// time, this one needs a unit's decoding and its waits whatever the rows are.
-// Microseconds there, here; 8 heads, 24 requests of 4096 cached tokens:
-//   of 64:  32 rows 48; 64 rows 69, 61; 128 rows 115, 74
-//   of 128: 32 rows 65; 64 rows 91, 70; 128 rows 153, 85
-//   of 256: 20 rows 145, 79; 64 rows 269, 81; 128 rows 489, 111
-// One request of 8192 with 64 rows of 128: 11, 15 (it looks at no lengths).
+// By the rows of a call, as if every request had max_queries queries.
 bool weigh_tc_takes(const WeighArgs& a, const KvGeometry& g) {
     const int group = a.heads / g.heads, cols = g.D == 256 ? Shape<256>::kCols : Shape<128>::kCols;
     const int64_t rows = static_cast<int64_t>(a.max_queries) * group;
-    return group <= cols && rows >= (g.D == 64 ? 64 : g.D == 128 ? 48 : 9);
+    return group <= cols && rows > weigh_few_rows(g.D);
 }
 
 cudaError_t launch_weigh_tc(const WeighParams& P, int num_sms, cudaStream_t s) {

@@ -361,6 +361,13 @@ WEIGHTS = [
     ([270], [270], 2, 2, 64, 16, 64, 0), ([600], [140], 8, 1, 128, 32, 0, 0), ([300], [40], 5, 1, 128, 64, 0, 0), ([700, 0, 5, 257], [64, 0, 5, 200], 6, 2, 256, 16, 0, 0),
     ([300, 128], [90, 127], 14, 2, 64, 16, 50, 9), ([200], [3], 130, 1, 128, 16, 0, 0), ([150], [4], 65, 1, 256, 16, 0, 0), ([129], [2], 128, 1, 128, 32, 0, 0),
     ([1500, 40], [1, 33], 8, 1, 128, 64, 0, 0),
+    # rows to a key/value head: 17, 24, 28, 36, 44, 60, 64, 65, 90, 96, 97; 9, 17, 30, 32, 33; 200
+    ([100, 517], [17, 9], 2, 2, 64, 16, 0, 0), ([300, 40, 7], [6, 1, 4], 8, 2, 128, 16, 0, 0), ([400, 65, 0, 33], [7, 7, 0, 7], 8, 2, 64, 32, 64, 3),
+    ([290, 31], [9, 2], 12, 3, 128, 64, 100, 20), ([700], [11], 4, 1, 128, 16, 1, 0), ([129, 600], [15, 15], 4, 1, 64, 16, 0, 0),
+    ([1000, 64], [16, 16], 8, 2, 128, 128, 0, 0), ([200], [13], 5, 1, 128, 32, 0, 0), ([333, 90, 91], [30, 1, 30], 3, 1, 64, 64, 30, 40),
+    ([96, 500], [96, 40], 2, 2, 64, 16, 0, 0), ([97, 3], [97, 3], 1, 1, 64, 16, 0, 0), ([160, 20], [9, 2], 2, 2, 256, 16, 0, 0),
+    ([300, 17, 1], [17, 17, 1], 1, 1, 256, 32, 0, 0), ([500, 200], [6, 3], 10, 2, 256, 64, 50, 6), ([400], [8], 4, 1, 256, 16, 0, 0),
+    ([333, 32], [11, 4], 6, 2, 256, 16, 0, 0), ([77], [1], 200, 1, 64, 16, 0, 0), ([90, 300], [2, 1], 300, 2, 64, 32, 70, 2),
 ]
 
 
