@@ -510,10 +510,13 @@ pn_status pn_verify(const int32_t* tokens, const float* target, int64_t target_s
  * -inf, and they are no alternatives; so is a token outside the vocabulary.  Where
  * fewer than `top` tokens are left, -1 and -inf follow.  A row that has none gets
  * -inf and entropy 0.  A logit above 1.7e38 counts as 1.7e38.
- * Sums are fp32; a log probability is within 2^-22 (ln vocab + 1) + 2^-23 |x - max x|
- * of the exact value.  Deterministic.  logits to their element, other arrays 4-byte aligned; rows
- * whose 16-byte lines begin elsewhere than the row cost no copy.  No output shares
- * memory with an input or another output.
+ * Sums are fp32, the rest next to the largest logit, whose own 1 is added last, so a token
+ * that is nearly certain keeps its digits.  With u = 2^-24, a log probability l is within
+ *   (vocab / 8192 + 64) u + 2^-22 (2 ln vocab + 2 + |x - max x|) + 2 u |l|
+ * of the exact value.  Deterministic, a row's bits the same whatever other rows there are
+ * in calls of as many rows (the blocks to a row go by rows, vocab and the GPU).  rows 0:
+ * nothing is done.  logits to their element (at most 2^29 elements from row to row), other
+ * arrays 4-byte aligned.  No output shares memory with an input or another output.
  */
 #define PN_MAX_TOP 32
 pn_status pn_logprobs(const void* logits, int64_t stride, int dtype, int64_t rows, int vocab, float scale,
@@ -537,8 +540,9 @@ pn_status pn_logprobs(const void* logits, int64_t stride, int dtype, int64_t row
  * outputs there has to be.  Arithmetic and sums are fp32, each result is rounded
  * once, and x is made of r' as it was before that.  residual_out may be residual,
  * with its stride; else no output shares memory with an input or the other output.
- * Arrays to their element; where all rows begin at 16 bytes (fp16: 8) and hidden is
- * a multiple of 4, four values are taken at a time.
+ * A row's sums, squares of v - mean among them, are made in one order whatever other rows
+ * there are.  Arrays to their element, strides to 2^29 elements; where all rows begin at
+ * 16 bytes (fp16: 8) and hidden is a multiple of 4, four values are taken at a time.
  */
 typedef enum { PN_NORM_NONE = 0, PN_NORM_RMS = 1, PN_NORM_LAYER = 2 } pn_norm_kind;
 #define PN_MAX_HIDDEN 32768
@@ -566,9 +570,12 @@ pn_status pn_norm(const void* y, int64_t y_stride, int y_dtype, const void* resi
  * two share no memory.  No other output is written, no workspace is needed.  Tokens
  * on pages outside the cache are passed over.  Requests may share pages as long as
  * nobody reads what they leave there: each writes its own sums.  Each sum is made in
- * fp32 in one order: deterministic, and independent of what else is in the batch.
- * Scores err as pn_attention's; a sum of n probabilities by n 2^-24 of it more.
- * q and cache 16-byte aligned, q_stride a multiple of 8.
+ * fp32 in one order: deterministic.  Which kernel runs goes by head_dim, heads,
+ * kv_heads and max_queries alone: with the same of them a request's weights have the
+ * same bits whatever else is in the batch.  Scores err as pn_attention's; a sum of n
+ * probabilities by n 2^-24 of it more.  A wait on the GPU that gives up (see
+ * pn_set_wait_timeout_ns) leaves NaN in the weights of the tokens concerned.
+ * q and cache 16-byte aligned, q_stride a multiple of 8, at most 2^29.
  */
 pn_status pn_kv_weigh(const uint16_t* q, int64_t q_stride, int64_t tokens, int heads, const void* cache,
                       int64_t pages, int page_size, int kv_heads, int head_dim, const int32_t* table,
@@ -580,12 +587,13 @@ pn_status pn_kv_weigh(const uint16_t* q, int64_t q_stride, int64_t tokens, int h
  * pn_kv_evict: request b < batch (at most 16384) with lens[b] > limit keeps `budget`
  * (1 .. limit, at most PN_MAX_BUDGET) tokens of every head: the first `sinks`, the last
  * `recent` (sinks + recent <= budget), and of those between them the ones with the
- * largest weights, the earlier where they are equal (NaN counts as the lowest).
+ * largest weights, the earlier where they are equal (NaN counts as the lowest, 0 and
+ * -0 as equal).
  * Heads keep tokens of their own.  They go in their order to the places 0 .. budget -
  * 1 of pages n = ceil(budget / page_size) of which are taken from the free ring's
  * head (ring and free_pages as in pn_kv_plan), with codes, scales and weights as they
  * are; keys stay rotated by their first positions, so positions of tokens to come go
- * on from the old length.  The held[b] old pages go behind the ring's tail, in
+ * on from the old length (a window of pn_attention or pn_kv_weigh counts cached tokens).  The held[b] old pages go behind the ring's tail, in
  * request order.  Requests take pages in their order as long as there are n; the
  * others are refused and stay as they are.
  *   table_out [batch][out_stride], max_pages entries each: the table after the call
@@ -595,6 +603,7 @@ pn_status pn_kv_weigh(const uint16_t* q, int64_t q_stride, int64_t tokens, int h
  *   for a request that was left alone.
  * Inputs stay as they are but for free_pages' entries behind the tail and the cache
  * and the weights of the pages taken, so a call repeated on them gives the same.
+ * Weights have to stay as they are until the call has ended.
  * Pages that several requests share may be read, but are given back by each that
  * holds them: take them out of held first.  A kept token on a page outside the
  * cache becomes zeros.  No output shares memory with an input or another output.
@@ -620,18 +629,21 @@ pn_status pn_read_ranges(const void* const* ptrs, const size_t* bytes, int count
 
 /*
  * Testing aid: the time limit, in nanoseconds, of every device-side wait in
- * the tensor-core GEMV kernels and the prefill GEMM (default 1e9).  A wait that runs out stops its thread
- * block, which records PN_ETIMEOUT in the workspace status word and returns
- * after its outstanding copies land.  Process-wide; not for concurrent use.
+ * the tensor-core GEMV kernels, the prefill GEMM, pn_attention and pn_kv_weigh
+ * (default 1e9).  A wait that runs out stops its thread block, which records
+ * PN_ETIMEOUT in the workspace status word (pn_kv_weigh, which has none: NaN in its
+ * weights) and returns after its outstanding copies land.  Process-wide; not for
+ * concurrent use.
  */
 void pn_set_wait_timeout_ns(uint64_t ns);
 
 /*
  * Testing aid for the failure path: while on (non-zero), every thread block of
- * the tensor-core GEMV kernels and of the prefill GEMM announces the bytes of
- * its first step but never copies them, so its consumers' wait can only end
- * by timing out; the call then reports PN_ETIMEOUT through
- * pn_workspace_status and its outputs are undefined.  Off by default.
+ * the tensor-core GEMV kernels, of the prefill GEMM and of the kernels of pn_attention
+ * and pn_kv_weigh that wait for copies announces the bytes of its first step but never
+ * copies them, so its consumers' wait can only end by timing out; the call then reports
+ * PN_ETIMEOUT through pn_workspace_status (pn_kv_weigh: NaN) and its outputs are
+ * undefined.  Off by default.
  * Process-wide; not for concurrent use.
  */
 void pn_set_test_stall(int on);
