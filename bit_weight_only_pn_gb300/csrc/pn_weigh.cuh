@@ -35,6 +35,15 @@ __device__ __forceinline__ LogSum log_sum_of(float lse, float scale_rest) {
     return {-near, fabsf(u) < 1.0f ? fmaf(u, fmaf(u, fmaf(u, fmaf(u, 0.0416666667f, 0.166666667f), 0.5f), 1.0f), 1.0f) : 1.0f};
 }
 
+// The same rounded to one number (2^-24 of it off), for sums of many rows, where these
+// roundings meet: a second number for each would cost more than it gives.
+__device__ __forceinline__ float less_of(float lse, float scale_rest) {
+    if (lse == -INFINITY) return -INFINITY;
+    constexpr float kLog2e = 1.44269502f, kLog2eRest = 1.92596299e-8f;
+    const float hi = lse * kLog2e, lo = fmaf(lse, kLog2e, -hi) + lse * kLog2eRest;
+    return fmaf(hi, scale_rest, -lo) - hi;
+}
+
 struct WeighRequest {
     int n, q0, pos0, len, rows;
     __device__ __forceinline__ void read(const WeighParams& P, int b) {

@@ -12,7 +12,7 @@
 //     swizzle, once for all rows, and the scales as fp32;
 //   warp 20 brings the query rows, a chunk at a time, by TMA: a box of 64 values, the
 //     heads of the group and as many tokens as fit (64 rows of 256 values, 128 of
-//     fewer); warps 21 and 23 make their lse ready (LogSum) and their positions;
+//     fewer); warps 21 and 23 make their lse ready and their positions;
 //   warp 22 issues the products of a chunk into one of two places in tensor memory;
 //   warps 0-15 take scores, exponentials and sums: of each chunk eight, four quarters
 //     of the tokens by two halves of the columns;
@@ -21,12 +21,14 @@
 // chunks, halves, blocks) are added at the unit's end in one order and written; results
 // depend on neither timing nor what else is in the batch.
 //
-// 2048 queries of a prompt of 8192 tokens, 24 + 4 heads of 256: 251 us, 0.72
-// PFLOP/s of products; bound by the sum warps' chain (TMEM load, scales, ex2; 1590 cycles
-// for 60 rows of 128 tokens), then by shared memory, from which N = 64 products take 768.
-// Loading the next columns while these are summed, and 32 columns at a time, were slower
-// (registers); the tokens' codes converted under a branch and a unit looked up by every
-// warp for itself had cost four and two times as much.
+// 2048 queries of a prompt of 8192 tokens, 24 + 4 heads of 256: 250 us, 0.72 PFLOP/s of
+// products.  60 rows of a unit take 1600 cycles: shared memory gives the N = 64 products
+// their operands in 768, takes the next queries in 256 and gives the rows' constants in
+// 256; tensor memory gives 128 KB in 1050.  (Two constants for a row took 119 us instead
+// of 110 for 1024 queries with heads of 128; all 16 warps on one chunk, the next columns
+// loaded while these are summed, and 32 columns at a time were no faster; codes converted
+// under a branch and units looked up by every warp for itself had cost four and two times
+// as much.)
 //
 // Every wait is bounded; a unit whose wait gave up gets NaN for its weights.
 #include <atomic>
@@ -62,16 +64,16 @@ template <int D>
 struct Shape {
     static constexpr int kGroups = D / 64;
     static constexpr int kCols = D == 256 ? 64 : 128;          // rows of a chunk at most, MMA N
-    static constexpr int kABufs = D == 256 ? 1 : 2;            // decoded units
-    static constexpr int kQStages = D == 256 ? 4 : D == 128 ? 4 : 6;
+    static constexpr int kABufs = 2;           // decoded units
+    static constexpr int kQStages = D == 256 ? 2 : D == 128 ? 4 : 6;
     static constexpr int kABytes = kGroups * kUnit * 128;
     static constexpr int kQBytes = kGroups * kCols * 128;
     static constexpr uint32_t kTmemCols = kPlaces * kGroups * kCols;       // 256 or 512
     static constexpr int kA = 0;
     static constexpr int kQ = kA + kABufs * kABytes;
     static constexpr int kScales = kQ + kQStages * kQBytes;                // [buffer][group][token] floats
-    static constexpr int kRowData = kScales + kABufs * kGroups * kUnit * 4;    // [stage][less, share, pos][column]
-    static constexpr int kParts = kRowData + kRowStages * 3 * kCols * 4;    // [2][4][token] parts of the sums
+    static constexpr int kRowData = kScales + kABufs * kGroups * kUnit * 4;    // [stage][less, pos][column]
+    static constexpr int kParts = kRowData + kRowStages * 2 * kCols * 4;    // [2][4][token] parts of the sums
     static constexpr int kOther = kParts + 2 * 4 * kUnit * 4;               // [2][token] sums of the cluster's second block (in the first)
     static constexpr int kUnits = kOther + 2 * kUnit * 4;                  // [2][32] units
     static constexpr int kScan = kUnits + 2 * kList * 80;                  // [threads + 1] units before each thread's requests
@@ -149,6 +151,11 @@ __device__ __forceinline__ float2 apart(Two v) {
 __device__ __forceinline__ Two mul2(Two a, Two b) {
     Two d;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ Two add2(Two a, Two b) {
+    Two d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
     return d;
 }
 __device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
@@ -235,11 +242,11 @@ __device__ __forceinline__ Two chunk_sum(Two sum, uint32_t ts, const Two (&d)[D 
         tmem_wait_ld();
 #pragma unroll
         for (int i = 0; i < kBlock; i += 4) {
-            const ulonglong2 less = *reinterpret_cast<const ulonglong2*>(rows + c + i), share = *reinterpret_cast<const ulonglong2*>(rows + kCols + c + i);
-            const Two l2[2] = {less.x, less.y}, g2[2] = {share.x, share.y};
+            const ulonglong2 less = *reinterpret_cast<const ulonglong2*>(rows + c + i);
+            const Two l2[2] = {less.x, less.y};
             int pos[4];
             if constexpr (kMasked) {
-                const int4 v = *reinterpret_cast<const int4*>(rows + 2 * kCols + c + i);
+                const int4 v = *reinterpret_cast<const int4*>(rows + kCols + c + i);
                 pos[0] = v.x; pos[1] = v.y; pos[2] = v.z; pos[3] = v.w;
             }
 #pragma unroll
@@ -254,7 +261,7 @@ __device__ __forceinline__ Two chunk_sum(Two sum, uint32_t ts, const Two (&d)[D 
                     p0 = tok <= q0 && (tok > q0 - window || tok < sinks) ? p0 : 0.0f;
                     p1 = tok <= q1 && (tok > q1 - window || tok < sinks) ? p1 : 0.0f;
                 }
-                sum = fma2(two(p0, p1), g2[k], sum);
+                sum = add2(sum, two(p0, p1));
             }
         }
     }
@@ -428,15 +435,13 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
                     ok = false;
                     break;
                 }
-                float* to = reinterpret_cast<float*>(smem + S::kRowData) + s.at * 3 * kCols;
+                float* to = reinterpret_cast<float*>(smem + S::kRowData) + s.at * 2 * kCols;
 #pragma unroll
                 for (int k = 0; k < kEach; ++k) {
                     const int row = lane + 32 * k, i = (w->c0 + c) * P.per + of_token[k];
                     const bool real = of_token[k] < P.per && i < w->n;
-                    const LogSum l = log_sum_of(real ? now[k] : -INFINITY, P.w.scale_rest);
-                    to[row] = l.less;
-                    to[kCols + row] = l.factor;
-                    reinterpret_cast<int*>(to)[2 * kCols + row] = real ? w->pos0 + i : INT32_MIN;
+                    to[row] = less_of(real ? now[k] : -INFINITY, P.w.scale_rest);
+                    reinterpret_cast<int*>(to)[kCols + row] = real ? w->pos0 + i : INT32_MIN;
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(rows_full + 8 * s.at);
@@ -615,7 +620,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
                         const int real = min(P.per, w.n - i0) * group, end = (real + 15) / 16 * 16;
                         const bool plain = (i0 + P.per <= w.n || real == end) && w.tok0 + kUnit - 1 <= pos_lo && (w.tok0 > pos_hi - window || w.tok0 + kUnit <= a.sinks);
                         const int cut = (end / 2 + 15) / 16 * 16, c0 = mine >> 1 ? cut : 0, c1 = mine >> 1 ? end : cut;        // the warp's columns
-                        const float* data = reinterpret_cast<const float*>(smem + S::kRowData) + rows.at * 3 * kCols;
+                        const float* data = reinterpret_cast<const float*>(smem + S::kRowData) + rows.at * 2 * kCols;
                         const uint32_t ts = tmem + t.at * (NG * kCols) + lanes;
                         if (plain) sum = chunk_sum<D, false>(sum, ts, d, P.w.scale_log2, data, c0, c1, tok, window, a.sinks);
                         else sum = chunk_sum<D, true>(sum, ts, d, P.w.scale_log2, data, c0, c1, tok, window, a.sinks);
