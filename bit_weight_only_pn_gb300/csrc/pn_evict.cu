@@ -21,8 +21,9 @@
 //
 // 64 ragged requests to 16384 tokens, 8 heads of 128, cut back to 512: select 37 us (its 17
 // MB of weights are 2.5: bound by five passes with barriers between; whole keys read
-// again for each pass took about 70), move 31 us for 34 MB in and as much out (2.2 TB/s: a
-// chain of position, page and record to each load).
+// again for each pass took about 70), move 31 us for 34 MB in and as much out (a chain of
+// position, page and record to each load; and V's words of a token lie 8 bytes in every
+// 64, so the sectors read are some three times what is wanted).
 #include <cooperative_groups.h>
 #include <cstdint>
 
