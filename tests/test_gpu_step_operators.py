@@ -431,6 +431,62 @@ def test_weigh_long(pn):
         assert np.abs(got[0, h] / np.exp(x).sum(0) - 1).max() <= 2.0 ** -15
 
 
+WAYS = [(4, 2, 64, [1, 1]), (4, 2, 128, [1, 5]), (6, 2, 256, [7, 2]), (4, 2, 128, [70, 33]), (8, 1, 256, [9, 64]), (150, 1, 64, [2, 1])]
+
+
+@pytest.mark.parametrize("heads,kv,D,counts", WAYS)
+def test_weigh_strides(pn, heads, kv, D, counts):
+    """Queries inside wider rows, tables that are part of wider ones, requests that others pad: the same bits."""
+    case = weigh_case([200, 90], counts, heads, kv, D, 16, 4)
+    q, cache, table, lens, starts = (cuda(a) for a in case[:5])
+    lse = torch.randn(q.shape[0], heads, device="cuda") + 9
+    want = pn.kv_weigh(q, cache, table, lens, starts, max(counts), lse, 0.1)
+    wide_q = torch.full((q.shape[0], heads + 2 * kv, D), float("nan"), dtype=torch.float16, device="cuda")
+    wide_q[:, :heads] = q
+    wide_table = torch.full((2, table.shape[1] + 5), 1 << 30, dtype=torch.int32, device="cuda")
+    wide_table[:, 2:-3] = table
+    got = pn.kv_weigh(wide_q[:, :heads], cache, wide_table[:, 2:-3], lens, starts, max(counts), lse, 0.1)
+    assert torch.equal(got, want)
+    # before, between and behind them requests of no queries or no tokens; tokens behind the last request
+    pad = lambda t, v: torch.tensor([v[0], int(t[0]), v[1], int(t[1]), v[2]], dtype=torch.int32, device="cuda")  # noqa: E731
+    more = torch.cat([table[:1], table[:1], table[:1], table[1:], table[1:]])
+    n0, n = counts[0], sum(counts)
+    begins = torch.tensor([0, 0, n0, n0, n, n], dtype=torch.int32, device="cuda")
+    tail = torch.cat([q, torch.full_like(q[:1], float("inf"))])
+    got = pn.kv_weigh(tail, cache, more, pad(lens, [150, 0, 17]), begins, max(counts), torch.cat([lse, lse[:1]]), 0.1)
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("heads,kv,D,counts", WAYS)
+def test_weigh_two_at_once(pn, heads, kv, D, counts):
+    """Calls on two streams that overlap, and a captured one beside an eager one, do not disturb each other."""
+    states = []
+    for seed in (1, 2):
+        case = weigh_case([3000, 900], counts, heads, kv, D, 16, seed)
+        dev = [cuda(a) for a in case[:5]]
+        lse = torch.randn(dev[0].shape[0], heads, device="cuda") + 9
+        states.append((dev, lse, pn.kv_weigh(*dev, max(counts), lse, 0.1)))
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    outs = [[torch.zeros_like(states[i][2]) for _ in range(5)] for i in range(2)]
+    torch.cuda.synchronize()
+    for k in range(5):
+        for i, (dev, lse, _) in enumerate(states):
+            pn.kv_weigh(*dev, max(counts), lse, 0.1, out=outs[i][k], stream=streams[i])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, states[i][2]) for i in range(2) for o in outs[i])
+    graph = torch.cuda.CUDAGraph()
+    dev, lse, want = states[0]
+    with torch.cuda.graph(graph):
+        got = pn.kv_weigh(*dev, max(counts), lse, 0.1)
+    got.zero_()
+    outs[1][0].zero_()
+    torch.cuda.synchronize()
+    graph.replay()
+    pn.kv_weigh(*states[1][0], max(counts), states[1][1], 0.1, out=outs[1][0], stream=streams[1])
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and torch.equal(outs[1][0], states[1][2])
+
+
 def test_weigh_wait_timeout(pn):
     """A wait on the GPU that gives up leaves NaN in the weights, and the next call is right."""
     case = weigh_case([300, 200], [80, 100], 4, 2, 128, 16)
@@ -621,6 +677,29 @@ def test_evict_pages_outside(pn):
     case = list(evict_case([200, 180], 1, 128, 16, 150, seed=2))
     case[2][0, 3], case[2][0, 5], case[2][1, 0] = -1, 1 << 20, case[0].shape[0]
     check_evict(pn, case, 160, 150, 2, 4)
+
+
+def test_evict_shared_pages(pn):
+    """Requests with pages in common are cut back each for itself; what they share is only read."""
+    case = list(evict_case([300, 280, 150], 2, 128, 16, 60, seed=8))
+    case[2][1, :6] = case[2][2, :6] = case[2][0, :6]
+    check_evict(pn, case, 100, 60, 4, 9)
+
+
+def test_evict_at_once(pn):
+    """Two caches on two streams."""
+    states = []
+    for seed in (1, 2):
+        cache, weights, table, lens, held, free, ring = evict_case([9000, 300], 2, 64, 32, 200, seed=seed)
+        dev = [cuda(a) for a in (cache, weights, table, lens, held, free, ring)]
+        states.append((dev, torch.cuda.Stream()))
+    wants = [pn.kv_evict(*dev, 250, 200, 3, 20) for dev, _ in states]
+    torch.cuda.synchronize()
+    for _ in range(4):
+        gots = [pn.kv_evict(*dev, 250, 200, 3, 20, stream=stream) for dev, stream in states]
+        torch.cuda.synchronize()
+        for got, want in zip(gots, wants):
+            assert all(torch.equal(getattr(got, n), getattr(want, n)) for n in got._fields)
 
 
 def test_evict_large_batch(pn):
