@@ -15,16 +15,17 @@
 //
 // 2000 rows of 151936 fp16 logits: 122 us, 5.0 TB/s, with 72% of the issue slots in use and
 // a last wave of one block to an SM (two blocks to every row: 130 us).  64 rows of fp32:
-// 17.3 us, one wave; about 10 of them read.  One row of 32000: 6.6 us.
+// 17.1 us, one wave; about 10 of them read.  One row of 32000: 6.4 us.
 //
 // Top k (at most 32).  The k-th largest of a block's 256 thread maxima is a lower
 // bound of the k-th largest value of the row, and so is what all p blocks have (k / p)
-// of, rounded up; the best of them is taken.  Only threads whose maximum reaches the
-// bound (k, and those that tie with it) can hold one of the top k: their values are
-// looked at again, from L2, by their warp, and what reaches the bound goes to the row's
+// of, rounded up; the best of them is taken.  Only threads, and turns (a warp's 512 or
+// 1024 values at a time), whose largest value reaches the bound can hold one of the top
+// k: these are read again, and what reaches the bound goes to the row's
 // first block, which ranks it by the 64-bit number (order of the logit, ~index): there
-// are no ties in that order and the lowest index wins.  Where a block finds more than fits (a row of equal
-// values, say), each warp keeps the k first of it in a sorted list, a lane to an entry.
+// are no ties in that order and the lowest index wins.  Where a block finds more than
+// fits (a row of equal values, say), each warp keeps the k first of it in a sorted list,
+// a lane to an entry.
 #include <cooperative_groups.h>
 #include <cstdint>
 
@@ -42,6 +43,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMostCluster = 8;
+constexpr int kUnroll = 4;                     // vectors of a thread at a time
 constexpr int kMostFound = kWarps * 32;        // values of a block that may be in the top k
 constexpr int kMostEntries = kMostCluster * kMostFound;
 constexpr float kHuge = 1.7e38f;               // differences of numbers up to it are finite
@@ -264,10 +266,11 @@ __device__ __forceinline__ float float_of(int i) { return __int_as_float(i < 0 ?
 template <typename T, bool kTop>
 __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArgs a) {
     using Row = RowOf<T>;
-    constexpr int kVec = Row::kVec, kUnroll = 4;       // vectors of a thread at a time
+    constexpr int kVec = Row::kVec;
     cg::cluster_group cluster = cg::this_cluster();
     __shared__ Sums warp_sums[kWarps], block_sums;
     __shared__ int lists[kTop ? kWarps * 32 : 1];      // the warps' thread maxima in order
+    extern __shared__ float highs[];                   // [turns][kWarps]: the largest value of each warp's turns
     __shared__ float bound, share;                     // the k-th and the (k / parts)-th of them
     __shared__ uint32_t found_count, entries, entry_base;
     __shared__ Key found[kTop ? kMostFound : 1];       // the block's
@@ -285,10 +288,12 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
     const float c = a.scale * 1.4426950408889634f;
     const Two c2 = two(c, c);
 
+    const bool by_turns = kTop && parts == 1 && a.top > 1;     // how values are looked at again
     if (kTop && threadIdx.x == 0) {
         bound = share = -INFINITY;
         found_count = entries = 0;
     }
+    int turn = 0;
     float m = -kHuge, best = -INFINITY;        // the warp's reference, the thread's maximum
     Two r2 = two(0.0f, 0.0f), t2 = r2;
     uint4 raw[kUnroll];
@@ -303,8 +308,12 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
         for (int j = 0; j < kUnroll; ++j) now[j] = raw[j];
         fetch(v + kThreads * kUnroll);         // the next ones are on their way meanwhile
         const float most = Row::largest(now);
-        if (kTop) best = fmaxf(best, most);
         const float high = float_of(__reduce_max_sync(0xFFFFFFFFu, order_of(most)));
+        if constexpr (kTop) {
+            best = fmaxf(best, most);
+            if (by_turns && lane == 0) highs[turn * kWarps + warp] = high;
+            ++turn;
+        }
         if (high > m || high >= kHuge) {
             const float to = fminf(fmaxf(high, m), kHuge), by = (m - to) * c, f = exp2_fast(by);
             const float2 r1 = apart(r2), t1 = apart(t2);
@@ -408,38 +417,38 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
         if (threadIdx.x == 0 && a.entropy) a.entropy[r] = none ? 0.0f : fmaxf(fmaf(-0.693147181f, all.t / (1.0f + all.r), log_sum), 0.0f);
     }
     if constexpr (kTop) {
-        // the warp's threads that may hold some of the top k: f(16 bytes of each lane, whose vector) of their values
+        // f(16 bytes of each lane, whose vector) of the warp's values that may be some of the top k.  Of several in a row
+        // of a block's own: the turns that may hold some, 2 KB in one piece each.  Of one, or a part of a row: the threads
+        // that may, whose values, 4 KB apart, are few.  (64 rows of 151936 in eight parts, 20 wanted: 18.2 us by turns,
+        // 17.2 by threads; 600 rows of a block each: 66 and 85; 2000 rows, one wanted: 125 and 122.)
         auto look_again = [&](auto f) {
-            constexpr int kAtOnce = 4;         // threads whose loads are on their way together
-            const bool may = best >= least && best > -kHuge;
-            uint32_t who = __ballot_sync(0xFFFFFFFFu, may);
-            // in short rows, or where most threads may, each looks at its own (12 rows of 236 values, 32 wanted: 23 us
-            // thread by thread, 8 like this)
-            const int own = (v1 - v0 + kThreads - 1) / kThreads, turns = (__popc(who) + kAtOnce - 1) / kAtOnce * ((v1 - v0 + 32 * kThreads - 1) / (32 * kThreads));
-            if ((own + kAtOnce - 1) / kAtOnce <= turns) {
-                for (int j = 0; j < own; j += kAtOnce) {
-                    uint4 raw[kAtOnce][1];
-                    const int first = v0 + warp * 32 + lane + j * kThreads;
+            if (!by_turns) {
+                for (uint32_t who = __ballot_sync(0xFFFFFFFFu, best >= least && best > -kHuge); who;) {
+                    int first[kUnroll];        // of threads' vectors, whose loads are on their way together
 #pragma unroll
-                    for (int n = 0; n < kAtOnce; ++n) raw[n][0] = may && first + n * kThreads < v1 ? row.load(first + n * kThreads) : Row::nothing();
+                    for (int n = 0; n < kUnroll; ++n) {
+                        first[n] = who ? v0 + warp * 32 + __ffs(who) - 1 + lane * kThreads : v1;
+                        who &= who - 1;
+                    }
+                    for (int go = 0; go < v1 - v0; go += 32 * kThreads) {
+                        uint4 raw[kUnroll][1];
 #pragma unroll
-                    for (int n = 0; n < kAtOnce; ++n) f(raw[n], first + n * kThreads);
+                        for (int n = 0; n < kUnroll; ++n) raw[n][0] = first[n] + go < v1 ? row.load(first[n] + go) : Row::nothing();
+#pragma unroll
+                        for (int n = 0; n < kUnroll; ++n) f(raw[n], first[n] + go);
+                    }
                 }
                 return;
             }
-            while (who) {
-                int first[kAtOnce];            // of their vectors
+            for (int t0 = 0; t0 < turn; t0 += 32) {
+                const float high = t0 + lane < turn ? highs[(t0 + lane) * kWarps + warp] : -INFINITY;
+                for (uint32_t which = __ballot_sync(0xFFFFFFFFu, high >= least && high > -kHuge); which; which &= which - 1) {
+                    const int first = warp * 32 + lane + (t0 + __ffs(which) - 1) * (kThreads * kUnroll);
+                    uint4 raw[kUnroll][1];
 #pragma unroll
-                for (int n = 0; n < kAtOnce; ++n) {
-                    first[n] = who ? v0 + warp * 32 + __ffs(who) - 1 + lane * kThreads : v1;
-                    who &= who - 1;
-                }
-                for (int go = 0; go < v1 - v0; go += 32 * kThreads) {
-                    uint4 raw[kAtOnce][1];
+                    for (int j = 0; j < kUnroll; ++j) raw[j][0] = first + j * kThreads < v1 ? row.load(first + j * kThreads) : Row::nothing();
 #pragma unroll
-                    for (int n = 0; n < kAtOnce; ++n) raw[n][0] = first[n] + go < v1 ? row.load(first[n] + go) : Row::nothing();
-#pragma unroll
-                    for (int n = 0; n < kAtOnce; ++n) f(raw[n], first[n] + go);
+                    for (int j = 0; j < kUnroll; ++j) f(raw[j], first + j * kThreads);
                 }
             }
         };
@@ -515,6 +524,10 @@ cudaError_t launch(const LogprobsArgs& a, int parts, cudaStream_t s) {
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3(static_cast<unsigned>(a.rows * parts));
     cfg.blockDim = dim3(kThreads);
+    if (kTop && parts == 1 && a.top > 1) {     // (one vector more where a row begins inside one)
+        const int vectors = a.vocab / RowOf<T>::kVec + 2;
+        cfg.dynamicSmemBytes = (vectors + kThreads * kUnroll - 1) / (kThreads * kUnroll) * kWarps * sizeof(float);
+    }
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeClusterDimension;

@@ -173,6 +173,29 @@ def test_logprobs_top_in_one_place(pn, order):
     check_logprobs(pn, x, np.array([[3], [4]]), 32, 1.0)
 
 
+@pytest.mark.parametrize("rows,vocab,top", [(310, 150001, 32), (310, 150001, 1), (305, 140000, 5), (700, 9001, 20), (3, 4090, 32)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.float16])
+@pytest.mark.parametrize("steps", [0, 4, 300])
+def test_logprobs_top_of_whole_rows(pn, rows, vocab, top, dtype, steps):
+    """Rows of a block each, long ones among them: the order of a stable sort, with few different values (steps to one) too."""
+    torch.manual_seed(rows + top)
+    logits = torch.randn(rows, vocab, device="cuda") * 3
+    if steps:
+        logits = torch.round(logits * steps) / steps
+    logits = logits.to(dtype)
+    logits[1, :vocab - 3] = -math.inf                        # three tokens left
+    logits[2] = 1.5
+    got = pn.logprobs(logits, top=top)
+    for r in [0, 1, 2, *range(3, rows, 61)]:
+        x = logits[r].double()
+        order = torch.sort(x, descending=True, stable=True).indices[:top]
+        left = min(top, int(torch.isfinite(x).sum()))
+        assert torch.equal(got.top_tokens[r, :left].long(), order[:left]) and (got.top_tokens[r, left:] == -1).all(), r
+        want = x[order[:left]] - torch.logsumexp(x, 0)
+        bound = (vocab / 8192 + 64) * U + 2.0 ** -22 * (2 * math.log(vocab) + 2 + (x.max() - x[order[:left]])) + 2 * U * want.abs()
+        assert ((got.top_logprobs[r, :left].double() - want).abs() <= bound).all(), r
+
+
 # --------------------------------------------------------------------- norm --
 def ref_norm(v, kind, w, b, eps, delta):
     """v in 64 bits with errors of at most delta: the norm and its bound of error."""
