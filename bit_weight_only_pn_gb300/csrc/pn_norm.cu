@@ -102,7 +102,7 @@ template <int V>
 __device__ __forceinline__ void store_half(__half* p, int64_t at, const float* v) {
     if constexpr (V == 4) {
         const __half2 a = __floats2half2_rn(v[0], v[1]), b = __floats2half2_rn(v[2], v[3]);
-        *reinterpret_cast<uint2*>(p + at) = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+        __stcs(reinterpret_cast<uint2*>(p + at), make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b)));
     } else {
         p[at] = __float2half_rn(v[0]);
     }
@@ -112,8 +112,8 @@ template <int V>
 __device__ __forceinline__ void store(void* p, int64_t at, bool f16, const float* v) {
     if (f16) return store_half<V>(static_cast<__half*>(p), at, v);
     float* f = static_cast<float*>(p) + at;
-    if constexpr (V == 4) *reinterpret_cast<float4*>(f) = make_float4(v[0], v[1], v[2], v[3]);
-    else *f = v[0];
+    if constexpr (V == 4) __stcs(reinterpret_cast<float4*>(f), make_float4(v[0], v[1], v[2], v[3]));
+    else __stcs(f, v[0]);
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
