@@ -11,9 +11,9 @@
 // the registers), so a large mean costs no bits.  Everything is fp32 and rounded
 // where it is stored: x is made of r' before that is rounded.
 //
-// Bound by memory: 8192 rows of 5120 fp32 values (y, r in, r', x out) take 93.5 us, 6.3
+// Bound by memory: 8192 rows of 5120 fp32 values (y, r in, r', x out) take 90 us, 6.5
 // TB/s; with a gate for each token, mean and variance norms and their vectors, 4096 rows
-// of 6144, 76.5 us, 5.3 TB/s (two barriers a row, between which a block's loads wait).
+// of 6144, 76 us, 5.3 TB/s (two barriers a row, between which a block's loads wait).
 // One row of 5120: 2.7 us, launch and latency; rows that do not lie for vectors of
 // four, 5003 values each: 114 us for 8192, 4.9 TB/s.
 #include <cstdint>
@@ -268,7 +268,9 @@ cudaError_t launch_norm(const NormArgs& a, int num_sms, cudaStream_t s) {
     const bool fours = a.hidden % 4 == 0 && fits(a.y, a.y_f16 ? 8 : 16, a.y_stride) && fits(a.residual, a.residual_f16 ? 8 : 16, a.residual_stride) &&
                        fits(a.residual_out, a.residual_f16 ? 8 : 16, a.out_stride) && fits(a.gate, 16, a.gate_stride) && fits(a.post_weight, 16, 0) &&
                        fits(a.post_bias, 16, 0) && fits(a.pre_weight, 16, 0) && fits(a.pre_bias, 16, 0) && fits(a.x, 8, 0);
-    if (a.hidden <= kWarpRowHidden) return fours ? choose<4, true, 4, 8>(a, 0, s) : choose<1, true, 8, 32>(a, 0, s);
+    // (rows of 128 with four groups to a lane, three of them outside: 200000 of them 100 us instead of 47; rows of 1280
+    // and 2048 as a warp's: 57 and 60 us for 16384, as a block's 45 and 54)
+    if (a.hidden <= kWarpRowHidden) return fours ? choose<4, true, 1, 2, 4, 8>(a, 0, s) : choose<1, true, 8, 32>(a, 0, s);
     const bool many = a.tokens > num_sms;
     return fours ? choose<4, false, 1, 2, 4, 8, 16>(a, many ? 4 : 0, s) : choose<1, false, 8, 16, 32, 64>(a, many ? 16 : 0, s);
 }
