@@ -188,14 +188,15 @@ __device__ __forceinline__ void norm_row(float (&v)[N][V], const Groups<V, N>& g
     if (bias) g.with(bias, v, [](float x, float w) { return x + w; });
 }
 
-// A block's threads at most, and blocks to an SM at least, as the registers for N V values allow.
-template <int V, int N>
-constexpr int kMostThreads = N * V <= 8 ? 1024 : N * V == 16 ? (V == 4 ? 384 : 512) : 512;
-template <int V, int N>
-constexpr int kLeastBlocks = N * V <= 8 ? 1 : N * V == 16 ? (V == 4 ? 3 : 2) : N * V == 32 && V == 4 ? 2 : 1;
+// Groups of a thread, a block's threads at most, and blocks to an SM at least: what the registers allow.
+template <int kN, int kThreads, int kBlocks>
+struct Split {
+    static constexpr int N = kN, threads = kThreads, blocks = kBlocks;
+};
 
-template <int V, int N, bool kWarpRow, bool kYF16, bool kRF16>
-__global__ void __launch_bounds__(kWarpRow ? kWarpRowThreads : kMostThreads<V, N>, kWarpRow ? 1 : kLeastBlocks<V, N>) norm_kernel(const NormArgs a) {
+template <int V, typename S, bool kWarpRow, bool kYF16, bool kRF16>
+__global__ void __launch_bounds__(S::threads, S::blocks) norm_kernel(const NormArgs a) {
+    constexpr int N = S::N;
     __shared__ float parts[kWarpRow ? 1 : 2 * 96];     // a place to each of a row's norms
     const int64_t t = kWarpRow ? static_cast<int64_t>(blockIdx.x) * (kWarpRowThreads / 32) + (threadIdx.x >> 5) : blockIdx.x;
     if (t >= a.tokens) return;                         // (a whole warp, of rows that are warps')
@@ -235,32 +236,34 @@ __global__ void __launch_bounds__(kWarpRow ? kWarpRowThreads : kMostThreads<V, N
         if (g.inside(k)) store_half<V>(a.x, t * a.hidden + g.at(k), r[k]);
 }
 
-static_assert(PN_MAX_HIDDEN <= 4 * 16 * kMostThreads<4, 16> && PN_MAX_HIDDEN <= 64 * kMostThreads<1, 64>, "the longest row fits");
-
-template <int V, int N, bool kWarpRow, bool kYF16, bool kRF16>
+template <int V, typename S, bool kWarpRow, bool kYF16, bool kRF16>
 cudaError_t launch(const NormArgs& a, cudaStream_t s) {
-    const int groups = (a.hidden + V - 1) / V, threads = kWarpRow ? kWarpRowThreads : ((groups + N - 1) / N + 31) / 32 * 32;
+    const int groups = (a.hidden + V - 1) / V, threads = kWarpRow ? kWarpRowThreads : ((groups + S::N - 1) / S::N + 31) / 32 * 32;
     const int64_t blocks = kWarpRow ? (a.tokens + kWarpRowThreads / 32 - 1) / (kWarpRowThreads / 32) : a.tokens;
-    norm_kernel<V, N, kWarpRow, kYF16, kRF16><<<static_cast<unsigned>(blocks), threads, 0, s>>>(a);
+    norm_kernel<V, S, kWarpRow, kYF16, kRF16><<<static_cast<unsigned>(blocks), threads, 0, s>>>(a);
     return cudaGetLastError();
 }
-template <int V, int N, bool kWarpRow>
+template <int V, typename S, bool kWarpRow>
 cudaError_t launch(const NormArgs& a, cudaStream_t s) {
-    if (a.y_f16) return a.residual_f16 ? launch<V, N, kWarpRow, true, true>(a, s) : launch<V, N, kWarpRow, true, false>(a, s);
-    return a.residual_f16 ? launch<V, N, kWarpRow, false, true>(a, s) : launch<V, N, kWarpRow, false, false>(a, s);
+    if (a.y_f16) return a.residual_f16 ? launch<V, S, kWarpRow, true, true>(a, s) : launch<V, S, kWarpRow, true, false>(a, s);
+    return a.residual_f16 ? launch<V, S, kWarpRow, false, true>(a, s) : launch<V, S, kWarpRow, false, false>(a, s);
 }
 
-// The least N of its list with which the block (of rows that are warps': a warp) has
-// threads enough, but no less than `least`.
-template <int V, bool kWarpRow, int N, int... More>
+// The first of its list with no fewer groups to a thread than `least` with which the block
+// (of rows that are warps': a warp) has threads enough.
+template <int V, bool kWarpRow, typename S, typename... More>
 cudaError_t choose(const NormArgs& a, int least, cudaStream_t s) {
     if constexpr (sizeof...(More) > 0) {
-        if (N < least || (a.hidden + V - 1) / V > N * (kWarpRow ? 32 : kMostThreads<V, N>)) return choose<V, kWarpRow, More...>(a, least, s);
+        if (S::N < least || (a.hidden + V - 1) / V > S::N * (kWarpRow ? 32 : S::threads)) return choose<V, kWarpRow, More...>(a, least, s);
     }
-    return launch<V, N, kWarpRow>(a, s);
+    return launch<V, S, kWarpRow>(a, s);
 }
+template <int N>
+using OfWarp = Split<N, kWarpRowThreads, 1>;
 
 }  // namespace
+
+static_assert(kWarpRowHidden <= 4 * 8 * 32 && kWarpRowHidden <= 32 * 32 && PN_MAX_HIDDEN <= 4 * 16 * 512 && PN_MAX_HIDDEN <= 64 * 512, "the longest rows fit");
 
 cudaError_t launch_norm(const NormArgs& a, int num_sms, cudaStream_t s) {
     // fours where every row lies for them
@@ -270,9 +273,17 @@ cudaError_t launch_norm(const NormArgs& a, int num_sms, cudaStream_t s) {
                        fits(a.post_bias, 16, 0) && fits(a.pre_weight, 16, 0) && fits(a.pre_bias, 16, 0) && fits(a.x, 8, 0);
     // (rows of 128 with four groups to a lane, three of them outside: 200000 of them 100 us instead of 47; rows of 1280
     // and 2048 as a warp's: 57 and 60 us for 16384, as a block's 45 and 54)
-    if (a.hidden <= kWarpRowHidden) return fours ? choose<4, true, 1, 2, 4, 8>(a, 0, s) : choose<1, true, 8, 32>(a, 0, s);
+    if (a.hidden <= kWarpRowHidden) return fours ? choose<4, true, OfWarp<1>, OfWarp<2>, OfWarp<4>, OfWarp<8>>(a, 0, s) : choose<1, true, OfWarp<8>, OfWarp<32>>(a, 0, s);
     const bool many = a.tokens > num_sms;
-    return fours ? choose<4, false, 1, 2, 4, 8, 16>(a, many ? 4 : 0, s) : choose<1, false, 8, 16, 32, 64>(a, many ? 16 : 0, s);
+    // Few rows: as many threads to each as there are.  Many: four groups to a thread keep most bytes on their way; above
+    // 6144 values eight, of fp32 without spilling (102 registers, in microseconds: 4096 rows of 8192 73 against 82 with
+    // 64, of 10240 90 and 104), of fp16 with two blocks to an SM (fewer bytes to a group: 55 against 61).
+    if (!fours)
+        return choose<1, false, Split<8, 1024, 1>, Split<16, 512, 2>, Split<32, 512, 1>, Split<32, 640, 1>, Split<64, 512, 1>>(a, many ? 16 : 0, s);
+    if (!many) return choose<4, false, Split<1, 1024, 1>, Split<2, 1024, 1>, Split<4, 1024, 1>, Split<8, 640, 1>, Split<16, 512, 1>>(a, 0, s);
+    const bool halves = (!a.y || a.y_f16) && (!a.residual || a.residual_f16);
+    if (halves && a.hidden <= 4 * 8 * 512) return choose<4, false, Split<4, 384, 3>, Split<8, 512, 2>>(a, 0, s);
+    return choose<4, false, Split<4, 384, 3>, Split<8, 640, 1>, Split<16, 512, 1>>(a, 0, s);
 }
 
 }  // namespace pn

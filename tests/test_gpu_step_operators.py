@@ -227,6 +227,11 @@ NORMS = [
     (2, 16388, "f32", "f32", "channel", 1, 1, False), (2, 32768, "f16", "f16", "none", 2, 2, False), (3, 32767, "f32", "f32", "token", 1, 2, True),
     (6, 640, None, "f32", "none", 0, 1, False), (6, 641, None, "f16", "none", 0, 2, True), (4, 256, "f32", None, "channel", 1, 1, False),
     (4, 4100, "f16", None, "none", 0, 0, False), (200, 2049, "f16", "f16", "none", 0, 2, False), (1, 20000, "f32", "f32", "token", 2, 1, True),
+    (160, 6148, "f32", "f32", "none", 2, 1, True), (160, 6148, "f16", "f16", "token", 1, 2, False), (155, 16384, "f16", "f16", "none", 2, 1, False),
+    (155, 16388, "f16", "f16", "channel", 1, 1, True), (160, 20480, "f16", "f32", "none", 2, 2, False), (160, 20484, "f32", "f16", "none", 1, 0, False),
+    (155, 32768, "f32", "f32", "none", 0, 2, False), (155, 8195, "f16", "f16", "none", 1, 1, False), (155, 16385, "f32", "f32", "token", 2, 1, True),
+    (155, 20483, "f16", "f32", "none", 0, 1, False), (3, 12288, "f32", "f32", "none", 2, 2, False), (300, 128, "f16", "f16", "none", 1, 2, True),
+    (77, 132, "f32", "f32", "token", 2, 1, False), (300, 256, "f32", "f16", "none", 0, 1, False), (33, 516, "f16", "f32", "channel", 1, 1, True),
 ]
 
 
