@@ -495,13 +495,13 @@ __global__ void __launch_bounds__(kFewThreads<D, NT>, kFewBlocks<D, NT>) weigh_f
             for (int n = 0; n < groups; ++n) make_ready<D>(P, r, h, 8 * n, ready[n]);
             __syncwarp();
         } else {
-    #pragma unroll
+#pragma unroll
             for (int n = 0; n < NT; ++n) {
                 const int mine = min(8 * n + g, r.rows - 1), qi = mine / P.group, head = h * P.group + mine - qi * P.group;
                 load_fragments<D>(a.q + (r.q0 + qi) * a.q_stride + head * D, R.q[n]);
                 const bool real = 8 * n + g < r.rows;
                 const LogSum l = log_sum_of(real ? a.lse[static_cast<int64_t>(r.q0 + qi) * a.heads + head] : -INFINITY, P.scale_rest);
-    #pragma unroll
+#pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     const int from = (2 * t + c) << 2;             // the columns' rows are those of lanes (2t + c, .)
                     R.less[n][c] = __shfl_sync(0xFFFFFFFFu, l.less, from);
