@@ -164,6 +164,15 @@ __device__ __forceinline__ Two fma2(Two a, Two b, Two c) {
     return d;
 }
 
+// Of the warps that sum: a barrier, and whether v holds for all of them.
+__device__ __forceinline__ void sums_sync() { asm volatile("bar.sync 1, %0;" :: "n"(kSumWarps * 32) : "memory"); }
+__device__ __forceinline__ bool all_sums(bool v) {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %2, 0;\n\tbarrier.cta.red.and.pred q, 2, %1, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+                 : "=r"(r) : "n"(kSumWarps * 32), "r"(static_cast<uint32_t>(v)) : "memory");
+    return r != 0;
+}
+
 // A unit: the chunks of query rows that see any of its tokens, and the pages of its
 // records (-1: none).  b < 0: there is no further one.
 struct alignas(16) Unit {
@@ -341,6 +350,12 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
         w = list + half * kList + turn % kList;
         return ok && w->b >= 0;
     };
+    // The same by a whole warp, whose lanes poll each for itself: one answer for all of them.
+    auto unit_of_warp = [&](uint32_t turn, const Unit*& w, bool& ok) {
+        const bool more = unit_at(turn, w, ok);
+        ok = __all_sync(0xFFFFFFFFu, ok);
+        return __all_sync(0xFFFFFFFFu, more);
+    };
     auto done_with = [&](uint32_t turn) {      // by one thread of each warp
         if (turn % kList == kList - 1) mbar_arrive(list_empty + 8 * ((turn / kList) & 1u));
     };
@@ -410,7 +425,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
         }
         bool ok = true;
         const Unit* w;
-        for (uint32_t turn = 0; unit_at(turn, w, ok); ++turn) {
+        for (uint32_t turn = 0; unit_of_warp(turn, w, ok); ++turn) {
             float lse[kEach];
             auto fetch = [&](int c) {          // of the unit's chunk c; any of the request's where there is no such row
 #pragma unroll
@@ -532,15 +547,14 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
         };
         const Unit* w;
         Words now, next;
-        bool more = unit_at(0, w, ok);
+        bool more = unit_of_warp(0, w, ok);
         if (kAhead && more) load(*w, next);
         for (uint32_t turn = 0; more; ++turn) {
             if constexpr (kAhead) now = next;
             else load(*w, now);
             __syncwarp();
             if (lane == 0) done_with(turn);    // its entry is not looked at again
-            more = unit_at(turn + 1, w, ok);
-            more = __all_sync(0xFFFFFFFFu, more);
+            more = unit_of_warp(turn + 1, w, ok);
             if (kAhead && more) load(*w, next);
             if (k.turn > 0) ok = ok && wait(a_empty + 8 * k.at, k.emptied(), kNap) && wait(d_empty + 8 * k.at, k.emptied(), kNap);
             if (!__all_sync(0xFFFFFFFFu, ok)) {
@@ -585,7 +599,12 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
         bool ok = true, listed = true;         // listed: the units can be told, whatever else has given up
         const Unit* unit;
         uint32_t n = 0;
-        for (; __all_sync(0xFFFFFFFFu, unit_at(n, unit, listed)); ++n) {
+        for (;; ++n) {
+            const bool more = unit_of_warp(n, unit, listed);
+            // Every unit has a barrier of all these warps, so all of them go on or none does: what one
+            // has waited for in vain another may find a moment later.
+            if (n % kList == 0) listed = all_sums(listed);
+            if (!listed || !more) break;
             const Unit w = *unit;
             const int tok = w.tok0 + token;
             // where the token's weight is, and what it was
@@ -641,7 +660,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
             // order does not depend on which place of S the unit's first chunk had
             float* part = parts + (n & 1) * 4 * kUnit + token;
             part[mine * kUnit] = ok ? both.x + both.y : __int_as_float(0x7FFFFFFF);
-            asm volatile("bar.sync 1, %0;" :: "n"(kSumWarps * 32) : "memory");
+            sums_sync();
             if (mine != 0) continue;
             float all = (part[0] + part[2 * kUnit]) + (part[kUnit] + part[3 * kUnit]);
             if (split > 1) {
@@ -663,8 +682,9 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
             }
             if (rank == 0 && to >= 0) a.out[to] = before + all;
         }
+        if (!listed) *abort = 1u;
         // where the list gave up: NaN for the units behind
-        if (!__all_sync(0xFFFFFFFFu, listed) && mine == 0 && rank == 0)
+        if (!listed && mine == 0 && rank == 0)
             for (; unit_of_turn(n, blockIdx.x / split, gridDim.x / split) < scan[kThreads]; ++n) {
                 Unit w;
                 look_up(P, scan, each, unit_of_turn(n, blockIdx.x / split, gridDim.x / split), &w);
