@@ -5,13 +5,14 @@
 //   rms:   v / sqrt(mean(v^2) + eps) * w + b
 //   layer: (v - mean) / sqrt(mean((v - mean)^2) + eps) * w + b
 //
-// One pass over memory: a row's values stay in registers from its loads to its
-// stores, so y, r and a gate of every token are read once and r' and x written
-// once.  The variance is that of the differences from the mean (a second walk over
-// the registers), so a large mean costs no bits.  Everything is fp32 and rounded
-// where it is stored: x is made of r' before that is rounded.
+// One pass over memory: a row's values stay with their threads from its loads to its
+// stores, in registers but for some that the longer splits spill (at the rule), so y, r
+// and a gate of every token are read once and r' and x written once.  The variance is
+// that of the differences from the mean (a second walk over the registers), so a large
+// mean costs no bits.  Everything is fp32 and rounded where it is stored: x is made of r'
+// before that is rounded.  A row's sums do not depend on how many threads have it.
 //
-// Bound by memory: 8192 rows of 5120 fp32 values (y, r in, r', x out) take 90 us, 6.5
+// Bound by memory: 8192 rows of 5120 fp32 values (y, r in, r', x out) take 85 us, 6.9
 // TB/s; with a gate for each token, mean and variance norms and their vectors, 4096 rows
 // of 6144, 76 us, 5.3 TB/s (two barriers a row, between which a block's loads wait).
 // One row of 5120: 2.7 us, launch and latency; rows that do not lie for vectors of
@@ -31,15 +32,20 @@ constexpr int kWarpRowHidden = 1024;           // rows up to this size are a war
 constexpr int kWarpRowThreads = 128;
 constexpr unsigned kFewBlocks = 256;
 
-// A thread has N groups of V values of a row: those of group k begin at place +
-// k * step, and lie wholly inside the row or outside, where they count as 0.  Loads of
+// A segment of a row: 256 values, of which a lane has 8, in groups of V = 4 or 1 that lie
+// a warp's width apart.  (Rows that are a warp's: a warp's width.)
+template <int V, bool kWarpRow>
+constexpr int kOfSegment = kWarpRow ? 1 : 8 / V;       // groups of a lane
+
+// A thread has N groups of V values of a row, J of each of its segments, which are `step`
+// values apart.  A group lies wholly inside the row or outside, where it counts as 0.  Loads of
 // a thread's groups stand together, without a branch between them (groups outside
 // the row read its last one): loaded and used one group after the other, each waited
 // for the one before, and 13 rows of 5003 took 12 us.
-template <int V, int N>
+template <int V, int N, int J>
 struct Groups {
     int place, step, hidden;
-    __device__ __forceinline__ int at(int k) const { return place + k * step; }
+    __device__ __forceinline__ int at(int k) const { return place + k / J * step + k % J * (32 * V); }
     __device__ __forceinline__ bool inside(int k) const { return at(k) < hidden; }
     // from row element 0 at p; every element is its thread's alone, which reads it before it
     // writes it (r' may take the place of r)
@@ -133,59 +139,139 @@ __device__ __forceinline__ Moments over_lanes(const Moments& m) {
     return {n, mean, warp_sum(fmaf(m.n * off, off, m.m2))};
 }
 
-// A row's norm, with one barrier (none where the row is a warp's); `part` is its own
-// place in shared memory.
-template <int V, int N, bool kWarpRow>
-__device__ __forceinline__ void norm_row(float (&v)[N][V], const Groups<V, N>& g, int kind, const float* weight, const float* bias, float eps, float* part) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
-    float mean = 0.0f, squares;
-    if (kind == PN_NORM_LAYER) {
-        // about the thread's own mean first: a large mean costs no bits
-        float n = 0.0f, sum = 0.0f;
+// Sums over the lanes of N values (1, 2, 4 or 8) of each, that of value k in s[0] of lanes
+// k * 32 / N on.  The lanes exchange halves of what they have, so 2 values take 5 shuffles as
+// one does, and 8 take 9; the order, lanes 16, 8, 4, 2 and 1 apart, is the same for any N.
+template <int N>
+__device__ __forceinline__ void sum_each(float (&s)[N]) {
+    const int lane = threadIdx.x & 31;
+    int d = 16;
 #pragma unroll
-        for (int k = 0; k < N; ++k) {
-            n += g.inside(k) ? static_cast<float>(V) : 0.0f;
+    for (int n = N; n > 1; n /= 2, d /= 2)
 #pragma unroll
-            for (int i = 0; i < V; ++i) sum += v[k][i];
+        for (int j = 0; j < n / 2; ++j) {
+            const bool upper = lane & d;
+            const float send = upper ? s[j] : s[j + n / 2];
+            s[j] = (upper ? s[j + n / 2] : s[j]) + __shfl_xor_sync(0xFFFFFFFFu, send, d);
         }
-        Moments m{n, sum / fmaxf(n, 1.0f), 0.0f};
+#pragma unroll
+    for (; d >= 1; d /= 2) s[0] += __shfl_xor_sync(0xFFFFFFFFu, s[0], d);
+}
+
+// The sum of x(0) .. x(n - 1), n up to 128.
+template <typename F>
+__device__ __forceinline__ float sum_of(int n, F x) {
+    const int lane = threadIdx.x & 31;
+    float s = lane < n ? x(lane) : 0.0f;
+    if (n > 32) {
+        const float a = lane + 32 < n ? x(lane + 32) : 0.0f, b = lane + 64 < n ? x(lane + 64) : 0.0f, c = lane + 96 < n ? x(lane + 96) : 0.0f;
+        s = (s + a) + (b + c);
+    }
+    return warp_sum(s);
+}
+
+// A row's mean (of layer norms; else 0) and the sum of squares about it, in one order
+// however many threads have the row: its segments are summed apart, and their sums
+// together, which every warp does for itself behind the one barrier.  `part`: the row's
+// own place in shared memory, [2][segments of the block].
+template <int V, int N, int J>
+__device__ __forceinline__ void block_moments(const float (&v)[N][V], const Groups<V, N, J>& g, bool layer, float* part, float& mean, float& squares) {
+    constexpr int S = N / J;                   // segments of a warp
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+    const int segments = (g.hidden + 255) / 256, segment = lane * S / 32 * warps + warp;       // whose sums the lane will have
+    const bool mine = lane % (32 / S) == 0;
+    auto count = [&](int i) { return static_cast<float>(max(min(g.hidden - 256 * i, 256), 0)); };
+    float s[S];
+    mean = 0.0f;
+    if (!layer) {
 #pragma unroll
         for (int k = 0; k < N; ++k)
+#pragma unroll
+            for (int i = 0; i < V; ++i) s[k / J] = k % J || i ? fmaf(v[k][i], v[k][i], s[k / J]) : __fmul_rn(v[k][i], v[k][i]);
+        sum_each(s);
+        if (mine) part[segment] = s[0];
+        __syncthreads();
+        squares = sum_of(segments, [&](int i) { return part[i]; });
+        return;
+    }
+    // about the segment's own mean: a large mean costs no bits
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+#pragma unroll
+        for (int i = 0; i < V; ++i) s[k / J] = k % J || i ? s[k / J] + v[k][i] : v[k][i];
+    sum_each(s);
+    const float of_segment = s[0] / fmaxf(count(segment), 1.0f);
+#pragma unroll
+    for (int j = 0; j < S; ++j) {
+        const float m = __shfl_sync(0xFFFFFFFFu, of_segment, j * (32 / S));
+        s[j] = 0.0f;
+#pragma unroll
+        for (int k = j * J; k < j * J + J; ++k)
             if (g.inside(k))
 #pragma unroll
-                for (int i = 0; i < V; ++i) m.m2 = fmaf(v[k][i] - m.mean, v[k][i] - m.mean, m.m2);
-        m = over_lanes(m);
-        if constexpr (!kWarpRow) {
-            if (lane == 0) {
-                part[warp] = m.n;
-                part[32 + warp] = m.mean;
-                part[64 + warp] = m.m2;
-            }
-            __syncthreads();
-            m = over_lanes(lane < warps ? Moments{part[lane], part[32 + lane], part[64 + lane]} : Moments{0.0f, 0.0f, 0.0f});
-        }
-        mean = m.mean;
-        squares = m.m2;
-    } else {
+                for (int i = 0; i < V; ++i) s[j] = fmaf(v[k][i] - m, v[k][i] - m, s[j]);
+    }
+    sum_each(s);
+    float* part2 = part + S * warps;
+    if (mine) {
+        part[segment] = of_segment;
+        part2[segment] = s[0];
+    }
+    __syncthreads();
+    mean = sum_of(segments, [&](int i) { return __fmul_rn(count(i), part[i]); }) / static_cast<float>(g.hidden);
+    // what a segment's mean is off the row's adds its count times the square
+    squares = sum_of(segments, [&](int i) {
+        const float off = part[i] - mean;
+        return fmaf(__fmul_rn(count(i), off), off, part2[i]);
+    });
+}
+
+// The same of a row that is a warp's, whose split goes by the row's length alone.
+template <int V, int N, int J>
+__device__ __forceinline__ void warp_moments(const float (&v)[N][V], const Groups<V, N, J>& g, bool layer, float& mean, float& squares) {
+    mean = 0.0f;
+    if (!layer) {
         squares = 0.0f;
 #pragma unroll
         for (int k = 0; k < N; ++k)
 #pragma unroll
             for (int i = 0; i < V; ++i) squares = fmaf(v[k][i], v[k][i], squares);
         squares = warp_sum(squares);
-        if constexpr (!kWarpRow) {
-            if (lane == 0) part[warp] = squares;
-            __syncthreads();
-            squares = warp_sum(lane < warps ? part[lane] : 0.0f);
-        }
+        return;
     }
-    const float inv = 1.0f / sqrtf(squares * (1.0f / static_cast<float>(g.hidden)) + eps);
+    // about the thread's own mean first: a large mean costs no bits
+    float n = 0.0f, sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        n += g.inside(k) ? static_cast<float>(V) : 0.0f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) sum += v[k][i];
+    }
+    Moments m{n, sum / fmaxf(n, 1.0f), 0.0f};
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+        if (g.inside(k))
+#pragma unroll
+            for (int i = 0; i < V; ++i) m.m2 = fmaf(v[k][i] - m.mean, v[k][i] - m.mean, m.m2);
+    m = over_lanes(m);
+    mean = m.mean;
+    squares = m.m2;
+}
+
+// A row's norm, with one barrier (none where the row is a warp's).  (Each rounding is
+// written out: no form of the kernel may join two of them that another one does not.)
+template <int V, int N, int J, bool kWarpRow>
+__device__ __forceinline__ void norm_row(float (&v)[N][V], const Groups<V, N, J>& g, int kind, const float* weight, const float* bias, float eps, float* part) {
+    float mean, squares;
+    if constexpr (kWarpRow) warp_moments(v, g, kind == PN_NORM_LAYER, mean, squares);
+    else block_moments(v, g, kind == PN_NORM_LAYER, part, mean, squares);
+    const float inv = 1.0f / sqrtf(fmaf(squares, 1.0f / static_cast<float>(g.hidden), eps));
 #pragma unroll
     for (int k = 0; k < N; ++k)
 #pragma unroll
-        for (int i = 0; i < V; ++i) v[k][i] = (v[k][i] - mean) * inv;
-    if (weight) g.with(weight, v, [](float x, float w) { return x * w; });
-    if (bias) g.with(bias, v, [](float x, float w) { return x + w; });
+        for (int i = 0; i < V; ++i) v[k][i] = __fmul_rn(__fsub_rn(v[k][i], mean), inv);
+    if (weight) g.with(weight, v, [](float x, float w) { return __fmul_rn(x, w); });
+    if (bias) g.with(bias, v, [](float x, float w) { return __fadd_rn(x, w); });
 }
 
 // Groups of a thread, a block's threads at most, and blocks to an SM at least: what the registers allow.
@@ -197,11 +283,12 @@ struct Split {
 template <int V, typename S, bool kWarpRow, bool kYF16, bool kRF16>
 __global__ void __launch_bounds__(S::threads, S::blocks) norm_kernel(const NormArgs a) {
     constexpr int N = S::N;
-    __shared__ float parts[kWarpRow ? 1 : 2 * 96];     // a place to each of a row's norms
+    constexpr int J = kOfSegment<V, kWarpRow>, kPart = kWarpRow ? 1 : 2 * (N / J) * (S::threads / 32);
+    __shared__ float parts[2 * kPart];                 // a place to each of a row's norms
     const int64_t t = kWarpRow ? static_cast<int64_t>(blockIdx.x) * (kWarpRowThreads / 32) + (threadIdx.x >> 5) : blockIdx.x;
     if (t >= a.tokens) return;                         // (a whole warp, of rows that are warps')
-    const int threads = kWarpRow ? 32 : blockDim.x;
-    const Groups<V, N> g{static_cast<int>(kWarpRow ? threadIdx.x & 31 : threadIdx.x) * V, threads * V, a.hidden};
+    const int warp = kWarpRow ? 0 : threadIdx.x >> 5, warps = kWarpRow ? 1 : blockDim.x >> 5;
+    const Groups<V, N, J> g{(warp * (J * 32) + static_cast<int>(threadIdx.x & 31)) * V, warps * (J * 32) * V, a.hidden};
     const uint8_t* y = static_cast<const uint8_t*>(a.y) + t * a.y_stride * (kYF16 ? 2 : 4);
     const uint8_t* residual = static_cast<const uint8_t*>(a.residual) + t * a.residual_stride * (kRF16 ? 2 : 4);
     const float* gate = a.gate + t * a.gate_stride;
@@ -218,9 +305,9 @@ __global__ void __launch_bounds__(S::threads, S::blocks) norm_kernel(const NormA
         if (a.post_weight) g.prefetch(a.post_weight, 4);
         if (a.pre_weight) g.prefetch(a.pre_weight, 4);
     }
-    if (a.post != PN_NORM_NONE) norm_row<V, N, kWarpRow>(v, g, a.post, a.post_weight, a.post_bias, a.eps, parts);
+    if (a.post != PN_NORM_NONE) norm_row<V, N, J, kWarpRow>(v, g, a.post, a.post_weight, a.post_bias, a.eps, parts);
     if (kLate && a.residual) g.template load<kRF16>(residual, r);
-    if (a.gate) g.with(gate, v, [](float x, float w) { return x * w; });
+    if (a.gate) g.with(gate, v, [](float x, float w) { return __fmul_rn(x, w); });
 #pragma unroll
     for (int k = 0; k < N; ++k)
 #pragma unroll
@@ -230,7 +317,7 @@ __global__ void __launch_bounds__(S::threads, S::blocks) norm_kernel(const NormA
         for (int k = 0; k < N; ++k)
             if (g.inside(k)) store<V>(a.residual_out, t * a.out_stride + g.at(k), kRF16, r[k]);
     if (!a.x) return;
-    if (a.pre != PN_NORM_NONE) norm_row<V, N, kWarpRow>(r, g, a.pre, a.pre_weight, a.pre_bias, a.eps, kWarpRow ? parts : parts + 96);
+    if (a.pre != PN_NORM_NONE) norm_row<V, N, J, kWarpRow>(r, g, a.pre, a.pre_weight, a.pre_bias, a.eps, parts + kPart);
 #pragma unroll
     for (int k = 0; k < N; ++k)
         if (g.inside(k)) store_half<V>(a.x, t * a.hidden + g.at(k), r[k]);
@@ -275,15 +362,17 @@ cudaError_t launch_norm(const NormArgs& a, int num_sms, cudaStream_t s) {
     // and 2048 as a warp's: 57 and 60 us for 16384, as a block's 45 and 54)
     if (a.hidden <= kWarpRowHidden) return fours ? choose<4, true, OfWarp<1>, OfWarp<2>, OfWarp<4>, OfWarp<8>>(a, 0, s) : choose<1, true, OfWarp<8>, OfWarp<32>>(a, 0, s);
     const bool many = a.tokens > num_sms;
-    // Few rows: as many threads to each as there are.  Many: four groups to a thread keep most bytes on their way; above
-    // 6144 values eight, of fp32 without spilling (102 registers, in microseconds: 4096 rows of 8192 73 against 82 with
-    // 64, of 10240 90 and 104), of fp16 with two blocks to an SM (fewer bytes to a group: 55 against 61).
+    // Few rows: as many threads to each as there are.  Many: four groups to a thread keep most bytes on their way (up to 5120
+    // values without spilling: 8192 rows 85 us, 93 with the registers of 384 threads); above 6144 values eight, of fp32
+    // without spilling (96 registers, in microseconds: 4096 rows of 8192 73 against 82 with 64, of 10240 90 and 104), of fp16
+    // with two blocks to an SM (fewer bytes to a group: 55 against 61).  Spilled are 56 bytes of a thread's at 5124 to 6144
+    // fp32 values, 236 to 280 of fp16 rows above, 260 to 380 of fp32 rows above 20480, as many of odd rows.
     if (!fours)
         return choose<1, false, Split<8, 1024, 1>, Split<16, 512, 2>, Split<32, 512, 1>, Split<32, 640, 1>, Split<64, 512, 1>>(a, many ? 16 : 0, s);
-    if (!many) return choose<4, false, Split<1, 1024, 1>, Split<2, 1024, 1>, Split<4, 1024, 1>, Split<8, 640, 1>, Split<16, 512, 1>>(a, 0, s);
+    if (!many) return choose<4, false, Split<2, 1024, 1>, Split<4, 1024, 1>, Split<8, 640, 1>, Split<16, 512, 1>>(a, 0, s);
     const bool halves = (!a.y || a.y_f16) && (!a.residual || a.residual_f16);
-    if (halves && a.hidden <= 4 * 8 * 512) return choose<4, false, Split<4, 384, 3>, Split<8, 512, 2>>(a, 0, s);
-    return choose<4, false, Split<4, 384, 3>, Split<8, 640, 1>, Split<16, 512, 1>>(a, 0, s);
+    if (halves && a.hidden <= 4 * 8 * 512) return choose<4, false, Split<4, 320, 3>, Split<4, 384, 3>, Split<8, 512, 2>>(a, 0, s);
+    return choose<4, false, Split<4, 320, 3>, Split<4, 384, 3>, Split<8, 640, 1>, Split<16, 512, 1>>(a, 0, s);
 }
 
 }  // namespace pn

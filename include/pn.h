@@ -541,8 +541,9 @@ pn_status pn_logprobs(const void* logits, int64_t stride, int dtype, int64_t row
  * once, and x is made of r' as it was before that.  residual_out may be residual,
  * with its stride; else no output shares memory with an input or the other output.
  * A row's sums, squares of v - mean among them, are made in one order whatever other rows
- * there are.  Arrays to their element, strides to 2^29 elements; where all rows begin at
- * 16 bytes (fp16: 8) and hidden is a multiple of 4, four values are taken at a time.
+ * there are, so its bits do not depend on them.  Arrays to their element, strides to 2^29
+ * elements; where all rows begin at 16 bytes (fp16: 8) and hidden is a multiple of 4, four
+ * values are taken at a time, and sums have an order of their own.
  */
 typedef enum { PN_NORM_NONE = 0, PN_NORM_RMS = 1, PN_NORM_LAYER = 2 } pn_norm_kind;
 #define PN_MAX_HIDDEN 32768
