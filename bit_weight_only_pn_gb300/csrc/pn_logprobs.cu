@@ -8,6 +8,13 @@
 // token has nearly all of the probability; both terms of the entropy are positive or
 // zero, so nothing cancels.
 //
+// Roundings (u = 2^-24): a thread adds 16 (fp16: 32) values by themselves, 8 (16) to a
+// chain, and one such sum in each of a row's vocab / 4096 (8192) turns; a turn whose largest
+// logit is a new one moves the sum so far, two additions, an ex2 (4 u) and a product.
+// That makes 8 u a turn at most; then 6 additions, and 3 joins of warps and 3 of blocks
+// of 8 u each; what the arguments of ex2 err by is at most 34 u, as a term moved by more than
+// 2^24 does not count.
+//
 // One pass over memory.  A cluster of 1 to 8 thread blocks has a row, each block a
 // contiguous part of it.  A warp takes 512 (fp16: 1024) values at a time under one
 // reference m, the next ones on their way; only where one of them passes it (a few
@@ -327,7 +334,9 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
             }
             if (high >= kHuge) r2 = add2(r2, two(Row::drop_huge(now), 0.0f));      // each adds 1
         }
+        // summed by themselves first: the chain of a row's sum is as long as it has turns, not values
         const Two less = two(-m, -m);
+        Two r_turn, t_turn;
 #pragma unroll
         for (int j = 0; j < kUnroll; ++j) {
             float x[kVec];
@@ -336,11 +345,13 @@ __global__ void __launch_bounds__(kThreads, 4) logprobs_kernel(const LogprobsArg
             for (int i = 0; i < kVec; i += 2) {
                 const float2 d = apart(mul2(add2(two(x[i], x[i + 1]), less), c2));
                 const float y0 = fmaxf(d.x, kLeast), y1 = fmaxf(d.y, kLeast);          // (NaN too)
-                const Two e = two(exp2_fast(y0), exp2_fast(y1));
-                r2 = add2(r2, e);
-                t2 = fma2(e, two(y0, y1), t2);
+                const Two e = two(exp2_fast(y0), exp2_fast(y1)), y = two(y0, y1);
+                r_turn = j || i ? add2(r_turn, e) : e;
+                t_turn = j || i ? fma2(e, y, t_turn) : mul2(e, y);
             }
         }
+        r2 = add2(r2, r_turn);
+        t2 = add2(t2, t_turn);
     }
     float2 pair = apart(r2);
     Sums all{m, pair.x + pair.y, 0.0f};

@@ -512,8 +512,9 @@ pn_status pn_verify(const int32_t* tokens, const float* target, int64_t target_s
  * -inf and entropy 0.  A logit above 1.7e38 counts as 1.7e38.
  * Sums are fp32, the rest next to the largest logit, whose own 1 is added last, so a token
  * that is nearly certain keeps its digits.  With u = 2^-24, a log probability l is within
- *   (vocab / 8192 + 64) u + 2^-22 (2 ln vocab + 2 + |x - max x|) + 2 u |l|
- * of the exact value.  Deterministic, a row's bits the same whatever other rows there are
+ *   (vocab / 512 + 128) u + 2^-22 (2 ln vocab + 2 + |x - max x|) + 2 u |l|
+ * of the exact value (vocab / 4096 where logits do not rise along the row: each new largest
+ * one moves the sum so far).  Deterministic, a row's bits the same whatever other rows there are
  * in calls of as many rows (the blocks to a row go by rows, vocab and the GPU).  rows 0:
  * nothing is done.  logits to their element (at most 2^29 elements from row to row), other
  * arrays 4-byte aligned.  No output shares memory with an input or another output.
