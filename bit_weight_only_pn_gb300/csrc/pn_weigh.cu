@@ -53,6 +53,13 @@ __device__ __forceinline__ void load_fragments(const __half* src, uint4 (&q)[D /
         for (int w = 0; w < 2; ++w) q[j][w] = *reinterpret_cast<const uint4*>(src + 64 * j + 16 * t + 8 * w);
 }
 
+// Queries of a row that gives nothing become zeros: whatever they are, its products are finite, and nothing times its share.
+template <int NG>
+__device__ __forceinline__ void drop_fragments(uint4 (&q)[NG][2]) {
+#pragma unroll
+    for (int j = 0; j < NG; ++j) q[j][0] = q[j][1] = make_uint4(0, 0, 0, 0);
+}
+
 // The sums of tokens 8 (2 i + hh) + g over a warp's columns, and what the tokens had
 // before (of lane (g, t): token 8 t + g), to the weights of a tile whose records are at
 // slots `place` (-1: nowhere).
@@ -87,14 +94,15 @@ __device__ __forceinline__ void make_ready(const Params& P, const Request& r, in
     const int row = min(row0 + g, r.rows - 1), qi = row / P.group, head = h * P.group + row - qi * P.group;
     uint4 q[NG][2];
     load_fragments<D>(P.a.q + (r.q0 + qi) * P.a.q_stride + head * D, q);
+    const bool real = row0 + g < r.rows;
+    const LogSum l = log_sum_of(real ? P.a.lse[static_cast<int64_t>(r.q0 + qi) * P.a.heads + head] : -INFINITY, P.scale_rest);
+    if (l.less == -INFINITY) drop_fragments(q);
 #pragma unroll
     for (int j = 0; j < NG; ++j) {
         to.q[j][0][lane] = q[j][0];
         to.q[j][1][lane] = q[j][1];
     }
     if (t == 0) {
-        const bool real = row0 + g < r.rows;
-        const LogSum l = log_sum_of(real ? P.a.lse[static_cast<int64_t>(r.q0 + qi) * P.a.heads + head] : -INFINITY, P.scale_rest);
         to.less[g] = l.less;
         to.share[g] = l.factor;
         to.pos[g] = r.pos0 + qi;
@@ -501,6 +509,7 @@ __global__ void __launch_bounds__(kFewThreads<D, NT>, kFewBlocks<D, NT>) weigh_f
                 load_fragments<D>(a.q + (r.q0 + qi) * a.q_stride + head * D, R.q[n]);
                 const bool real = 8 * n + g < r.rows;
                 const LogSum l = log_sum_of(real ? a.lse[static_cast<int64_t>(r.q0 + qi) * a.heads + head] : -INFINITY, P.scale_rest);
+                if (l.less == -INFINITY) drop_fragments(R.q[n]);
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     const int from = (2 * t + c) << 2;             // the columns' rows are those of lanes (2t + c, .)

@@ -26,7 +26,7 @@ struct LogSum {
     float less, factor;
 };
 __device__ __forceinline__ LogSum log_sum_of(float lse, float scale_rest) {
-    if (lse == -INFINITY) return {-INFINITY, 0.0f};
+    if (fabsf(lse) == INFINITY) return {-INFINITY, 0.0f};              // a row that gives nothing
     constexpr float kLog2e = 1.44269502f, kLog2eRest = 1.92596299e-8f;       // log2 e in two parts
     const float hi = lse * kLog2e, lo = fmaf(lse, kLog2e, -hi) + lse * kLog2eRest;
     const float near = rintf(hi * 64.0f) * 0.015625f;
@@ -38,7 +38,7 @@ __device__ __forceinline__ LogSum log_sum_of(float lse, float scale_rest) {
 // The same rounded to one number (2^-24 of it off), for sums of many rows, where these
 // roundings meet: a second number for each would cost more than it gives.
 __device__ __forceinline__ float less_of(float lse, float scale_rest) {
-    if (lse == -INFINITY) return -INFINITY;
+    if (fabsf(lse) == INFINITY) return -INFINITY;
     constexpr float kLog2e = 1.44269502f, kLog2eRest = 1.92596299e-8f;
     const float hi = lse * kLog2e, lo = fmaf(lse, kLog2e, -hi) + lse * kLog2eRest;
     return fmaf(hi, scale_rest, -lo) - hi;

@@ -80,7 +80,8 @@ struct Shape {
     static constexpr int kWarpSums = kScan + (kThreads + 1) * 8;
     static constexpr int kBars = kWarpSums + kThreads / 32 * 8;
     static constexpr int kNumBars = 2 * kQStages + 3 * kABufs + 2 * kPlaces + 2 * kRowStages + 1 + 4 + 4;
-    static constexpr int kMisc = kBars + kNumBars * 8;                     // TMEM base, abort
+    static constexpr int kMisc = kBars + kNumBars * 8;                     // TMEM base, abort, [stage] some row gives nothing (bytes)
+    static_assert(kRowStages <= 8, "a byte to each behind two words");
     static constexpr int kBytes = kMisc + 16 + 1024;                       // slack to align to 1024 bytes
     static_assert(kBytes <= 227 * 1024, "fits one SM's shared memory");
     static_assert(kQ % 1024 == 0 && kQBytes % 1024 == 0 && kScales % 16 == 0 && kBars % 8 == 0, "alignment");
@@ -292,6 +293,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
     const uint32_t x_full = take(2), x_empty = take(2);        // of the second block's sums: in the first block, in the second
     volatile uint32_t* misc = reinterpret_cast<volatile uint32_t*>(smem + S::kMisc);
     volatile uint32_t* abort = misc + 1;
+    volatile uint8_t* some_none = reinterpret_cast<volatile uint8_t*>(misc + 2);
     uint64_t* scan = reinterpret_cast<uint64_t*>(smem + S::kScan);
     const WeighArgs& a = P.w.a;
     const KvCache& cache = P.w.cache;
@@ -451,13 +453,17 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
                     break;
                 }
                 float* to = reinterpret_cast<float*>(smem + S::kRowData) + s.at * 2 * kCols;
+                bool none = false;             // (a row that gives nothing sees no token: its products may be NaN)
 #pragma unroll
                 for (int k = 0; k < kEach; ++k) {
                     const int row = lane + 32 * k, i = (w->c0 + c) * P.per + of_token[k];
-                    const bool real = of_token[k] < P.per && i < w->n;
-                    to[row] = less_of(real ? now[k] : -INFINITY, P.w.scale_rest);
-                    reinterpret_cast<int*>(to)[kCols + row] = real ? w->pos0 + i : INT32_MIN;
+                    const bool real = of_token[k] < P.per && i < w->n, gives = real && fabsf(now[k]) != INFINITY;
+                    none |= real && !gives;
+                    to[row] = less_of(gives ? now[k] : -INFINITY, P.w.scale_rest);
+                    reinterpret_cast<int*>(to)[kCols + row] = gives ? w->pos0 + i : INT32_MIN;
                 }
+                none = __any_sync(0xFFFFFFFFu, none);
+                if (lane == 0) some_none[s.at] = none;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(rows_full + 8 * s.at);
                 s.step();
@@ -637,7 +643,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
                         const int i0 = (w.c0 + c) * P.per, pos_lo = w.pos0 + i0, pos_hi = pos_lo + P.per - 1;
                         // columns with rows; whether all of them are the request's (others may hold anything)
                         const int real = min(P.per, w.n - i0) * group, end = (real + 15) / 16 * 16;
-                        const bool plain = (i0 + P.per <= w.n || real == end) && w.tok0 + kUnit - 1 <= pos_lo && (w.tok0 > pos_hi - window || w.tok0 + kUnit <= a.sinks);
+                        const bool plain = !some_none[rows.at] && (i0 + P.per <= w.n || real == end) && w.tok0 + kUnit - 1 <= pos_lo && (w.tok0 > pos_hi - window || w.tok0 + kUnit <= a.sinks);
                         const int cut = (end / 2 + 15) / 16 * 16, c0 = mine >> 1 ? cut : 0, c1 = mine >> 1 ? end : cut;        // the warp's columns
                         const float* data = reinterpret_cast<const float*>(smem + S::kRowData) + rows.at * 2 * kCols;
                         const uint32_t ts = tmem + t.at * (NG * kCols) + lanes;
