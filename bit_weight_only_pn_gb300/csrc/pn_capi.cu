@@ -796,6 +796,15 @@ pn_status pn_kv_weigh(const uint16_t* q, int64_t q_stride, int64_t tokens, int h
                       int64_t table_stride, int max_pages, const int32_t* lens, const int32_t* starts, int batch,
                       int max_queries, const float* lse, float scale, int window, int sinks, const float* weights,
                       float decay, float* out, pn_stream stream) {
+    return pn_kv_weigh_ex(q, q_stride, tokens, heads, cache, pages, page_size, kv_heads, head_dim, table, table_stride, max_pages, lens, starts, batch,
+                          max_queries, lse, scale, window, sinks, weights, decay, out, nullptr, 0, stream);
+}
+
+pn_status pn_kv_weigh_ex(const uint16_t* q, int64_t q_stride, int64_t tokens, int heads, const void* cache,
+                         int64_t pages, int page_size, int kv_heads, int head_dim, const int32_t* table,
+                         int64_t table_stride, int max_pages, const int32_t* lens, const int32_t* starts, int batch,
+                         int max_queries, const float* lse, float scale, int window, int sinks, const float* weights,
+                         float decay, float* out, void* workspace, size_t workspace_bytes, pn_stream stream) {
     if (!kv_shape_ok(pages, page_size, kv_heads, head_dim)) return PN_EINVAL;
     if (tokens < 0 || tokens > INT32_MAX || heads < 1 || heads > 65536 || heads % kv_heads) return PN_EINVAL;
     if (batch < 1 || batch > pn::kKvMaxBatch || max_queries < 1 || max_pages < 1 || table_stride < max_pages || window < 0 || sinks < 0 ||
@@ -809,13 +818,14 @@ pn_status pn_kv_weigh(const uint16_t* q, int64_t q_stride, int64_t tokens, int h
     if (tokens == 0) return PN_OK;
     if (!q || !cache || !table || !lens || !starts || !lse || !out) return PN_EINVAL;
     if (!aligned(q, 16) || q_stride % 8 || !aligned(cache, 16) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(starts, 4) ||
-        !aligned(lse, 4) || !aligned(weights, 4) || !aligned(out, 4))
+        !aligned(lse, 4) || !aligned(weights, 4) || !aligned(out, 4) || !aligned(workspace, 256))
         return PN_EALIGN;
+    if (workspace && workspace_bytes < 256) return PN_EINVAL;
     const size_t nt = static_cast<size_t>(tokens), nb = static_cast<size_t>(batch) * 4, nw = static_cast<size_t>(pages) * kv_heads * page_size * 4;
     const Range ins[] = {{q, ((nt - 1) * q_stride + cols) * 2}, {cache, pn_kv_cache_bytes(pages, page_size, kv_heads, head_dim)},
                          {table, (static_cast<size_t>(batch - 1) * table_stride + max_pages) * 4}, {lens, nb}, {starts, nb + 4},
                          {lse, nt * heads * 4}, {weights == out ? nullptr : weights, nw}},
-                outs[] = {{out, nw}};
+                outs[] = {{out, nw}, {workspace, workspace_bytes}};
     if (shared(outs, ins)) return PN_EINVAL;
     int sms = 0, major = 0;
     if (pn_status st = device_info(&sms, &major); st != PN_OK) return st;
@@ -824,7 +834,7 @@ pn_status pn_kv_weigh(const uint16_t* q, int64_t q_stride, int64_t tokens, int h
     const pn::WeighArgs a{reinterpret_cast<const __half*>(q), q_stride, tokens, heads, table, table_stride, max_pages, lens, starts, batch,
                           max_queries, lse, scale, window < room ? window : 0, sinks < room ? sinks : room, decay > 0.0f ? weights : nullptr, decay, out};
     const pn::KvGeometry g{static_cast<uint8_t*>(const_cast<void*>(cache)), pages, page_size, kv_heads, head_dim};
-    const cudaError_t e = pn::launch_weigh(a, g, sms, g_timeout_ns.load(), g_test_stall.load(), reinterpret_cast<cudaStream_t>(stream));
+    const cudaError_t e = pn::launch_weigh(a, g, sms, g_timeout_ns.load(), g_test_stall.load(), static_cast<uint32_t*>(workspace), reinterpret_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? PN_OK : pn::cuda_error(e);
 }
 

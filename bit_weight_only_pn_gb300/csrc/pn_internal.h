@@ -339,7 +339,7 @@ struct WeighArgs {
     float decay;
     float* out;
 };
-cudaError_t launch_weigh(const WeighArgs& a, const KvGeometry& g, int num_sms, uint64_t timeout_ns, int stall, cudaStream_t s);
+cudaError_t launch_weigh(const WeighArgs& a, const KvGeometry& g, int num_sms, uint64_t timeout_ns, int stall, uint32_t* status, cudaStream_t s);
 
 struct EvictArgs {
     float* weights;

@@ -458,7 +458,7 @@ const at::Tensor& cache_weights(Device& on, PyObject* o, const Cache& c, const c
     return t;
 }
 
-// q, cache, table, lens, starts, max_queries, lse, scale, weights, decay, out (weights and out: one of them at least), window, sinks
+// q, cache, table, lens, starts, max_queries, lse, scale, weights, decay, out (weights and out: one of them at least), window, sinks, workspace (or None)
 PyObject* kv_weigh(PyObject* const* a) {
     Device on;
     const Cache c(on, a[1]);
@@ -476,11 +476,12 @@ PyObject* kv_weigh(PyObject* const* a) {
     const float scale = real(a[7]), decay = real(a[9]);
     const at::Tensor* weights = a[8] == Py_None ? nullptr : &cache_weights(on, a[8], c, "weights");
     const at::Tensor& out = cache_weights(on, a[10] == Py_None ? a[8] : a[10], c, "out");
+    const at::Tensor* workspace = a[13] == Py_None ? nullptr : &dense(on, a[13], at::kByte, "workspace");
     const c10::cuda::CUDAGuard guard(q.device());
-    const pn_status st = pn_kv_weigh(data<uint16_t>(&q), row_stride(q), T, static_cast<int>(heads), c.t.data_ptr(), c.pages, c.page_size, c.heads, c.dim,
-                                     data<int32_t>(&table), table_stride(table), static_cast<int>(table.size(1)), data<int32_t>(&lens), data<int32_t>(&starts),
-                                     static_cast<int>(B), max_queries, data<float>(lse), scale, window, sinks, data<float>(weights), decay,
-                                     data<float>(&out), stream_of(q));
+    const pn_status st = pn_kv_weigh_ex(data<uint16_t>(&q), row_stride(q), T, static_cast<int>(heads), c.t.data_ptr(), c.pages, c.page_size, c.heads, c.dim,
+                                        data<int32_t>(&table), table_stride(table), static_cast<int>(table.size(1)), data<int32_t>(&lens), data<int32_t>(&starts),
+                                        static_cast<int>(B), max_queries, data<float>(lse), scale, window, sinks, data<float>(weights), decay,
+                                        data<float>(&out), data<void>(workspace), workspace ? static_cast<size_t>(workspace->numel()) : 0, stream_of(q));
     return answer(st, {given_or(a[10] == Py_None ? a[8] : a[10], out)});
 }
 
@@ -567,7 +568,7 @@ PyMethodDef method(const char* name) {
 
 PyMethodDef g_methods[] = {method<kv_plan, 9>("kv_plan"), method<kv_append, 13>("kv_append"), method<kv_read, 4>("kv_read"),
                            method<attention, 13>("attention"), method<verify, 7>("verify"), method<logprobs, 5>("logprobs"),
-                           method<norm, 15>("norm"), method<kv_weigh, 13>("kv_weigh"), method<kv_evict, 12>("kv_evict"), {nullptr, nullptr, 0, nullptr}};
+                           method<norm, 15>("norm"), method<kv_weigh, 14>("kv_weigh"), method<kv_evict, 12>("kv_evict"), {nullptr, nullptr, 0, nullptr}};
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "_step", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};
 
 }  // namespace

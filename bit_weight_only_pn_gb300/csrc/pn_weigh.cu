@@ -589,12 +589,12 @@ cudaError_t launch(const Params& P, int num_sms, cudaStream_t s) {
 
 }  // namespace
 
-cudaError_t launch_weigh(const WeighArgs& a, const KvGeometry& g, int num_sms, uint64_t timeout_ns, int stall, cudaStream_t s) {
+cudaError_t launch_weigh(const WeighArgs& a, const KvGeometry& g, int num_sms, uint64_t timeout_ns, int stall, uint32_t* status, cudaStream_t s) {
     int shift = 0;
     while ((1 << shift) < g.page_size) ++shift;
     const double exact = static_cast<double>(a.scale) * 1.4426950408889634;
     const float scale_log2 = static_cast<float>(exact), rest = exact != 0.0 ? static_cast<float>((exact - scale_log2) / exact) : 0.0f;
-    const Params P{a, KvCache{g.data, g.pages, g.page_size, shift, g.heads, g.D}, a.heads / g.heads, scale_log2, rest, timeout_ns, stall};
+    const Params P{a, KvCache{g.data, g.pages, g.page_size, shift, g.heads, g.D}, a.heads / g.heads, scale_log2, rest, timeout_ns, stall, status};
     if (weigh_tc_takes(a, g)) return launch_weigh_tc(P, num_sms, s);
     if (g.D == 64) return launch<64>(P, num_sms, s);
     return g.D == 128 ? launch<128>(P, num_sms, s) : launch<256>(P, num_sms, s);

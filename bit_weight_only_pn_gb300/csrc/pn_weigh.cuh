@@ -15,6 +15,7 @@ struct WeighParams {
     float scale_rest;          // what that left of it, relative to it
     uint64_t timeout_ns;
     int stall;                 // testing aid: see pn_set_test_stall
+    uint32_t* status;          // may be null
 };
 
 // A row's lse as the exponent's argument takes it.  exp2(x f - lse log2 e), with x f

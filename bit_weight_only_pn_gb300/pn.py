@@ -119,6 +119,8 @@ def lib() -> ctypes.CDLL:
             L.pn_kv_weigh.restype = i32
             L.pn_kv_weigh.argtypes = [vp, i64, i64, i32, vp, i64, i32, i32, i32, vp, i64, i32, vp, vp, i32, i32, vp, f32, i32, i32,
                                       vp, f32, vp, vp]
+            L.pn_kv_weigh_ex.restype = i32
+            L.pn_kv_weigh_ex.argtypes = [*L.pn_kv_weigh.argtypes[:-1], vp, sz, vp]
             L.pn_kv_evict.restype = i32
             L.pn_kv_evict.argtypes = [vp, i64, i32, i32, i32, vp, vp, i64, i32, vp, vp, i32, i32, i32, i32, i32, vp, i64, vp, vp,
                                       i64, vp, vp, vp, vp, vp, vp]
@@ -608,16 +610,18 @@ def kv_weights(cache: torch.Tensor) -> torch.Tensor:
 
 def kv_weigh(q: torch.Tensor, cache: torch.Tensor, table: torch.Tensor, lens: torch.Tensor, starts: torch.Tensor, max_queries: int,
              lse: torch.Tensor, scale: float, weights: torch.Tensor | None = None, decay: float = 1.0, out: torch.Tensor | None = None,
-             window: int = 0, sinks: int = 0, stream=None) -> torch.Tensor:
+             window: int = 0, sinks: int = 0, stream=None, workspace: AttentionWorkspace | Workspace | None = None) -> torch.Tensor:
     """The attention weight that each cached token gathered from a step's queries
     (see pn_kv_weigh): arguments as of the attention call before it, and the lse
     that it returned.  Added to decay times `weights` (the step's own tokens begin
     at zero; None: all do) and written to `out` (None: into `weights`; both None:
-    new zeroed ones)."""
+    new zeroed ones).  With a workspace (the attention call's, say) its status()
+    tells of a wait on the GPU that gave up, which else shows as NaN alone."""
     if weights is None and out is None:
         with torch.cuda.stream(stream):              # zeroed in the order of the stream that runs the call
             out = kv_weights(cache)
-    return _call(stream, _step().kv_weigh, "pn_kv_weigh", q, cache, table, lens, starts, max_queries, lse, scale, weights, decay, out, window, sinks)[1]
+    return _call(stream, _step().kv_weigh, "pn_kv_weigh", q, cache, table, lens, starts, max_queries, lse, scale, weights, decay, out, window, sinks,
+                 None if workspace is None else workspace.buffer)[1]
 
 
 class KvEviction(NamedTuple):

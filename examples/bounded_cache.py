@@ -55,7 +55,7 @@ def step(model: Model, s: State, tokens: torch.Tensor, add: torch.Tensor, longes
     q = pn.kv_append(q.unflatten(1, (HEADS, DIM)), k.unflatten(1, (KV_HEADS, DIM)), v.unflatten(1, (KV_HEADS, DIM)), s.cache, plan.slots, positions,
                      model.cos, model.sin, model.q_norm, model.k_norm, EPS)
     a, lse = pn.attention(q, s.cache, s.table, plan.lens, plan.starts, longest, SCALE, workspace=model.attn_ws, return_lse=True)
-    pn.kv_weigh(q, s.cache, s.table, plan.lens, plan.starts, longest, lse, SCALE, weights=s.weights)
+    pn.kv_weigh(q, s.cache, s.table, plan.lens, plan.starts, longest, lse, SCALE, weights=s.weights, workspace=model.attn_ws)
     _, x = pn.norm(model.project((model.o,), a.flatten(1))[0], stream, eps=EPS)
     s.lens, s.held, s.ring = plan.lens, plan.held, plan.ring
     return model.project((model.head,), x)[0], plan.starts

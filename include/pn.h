@@ -576,7 +576,10 @@ pn_status pn_norm(const void* y, int64_t y_stride, int y_dtype, const void* resi
  * kv_heads and max_queries alone: with the same of them a request's weights have the
  * same bits whatever else is in the batch.  Scores err as pn_attention's; a sum of n
  * probabilities by n 2^-24 of it more.  A wait on the GPU that gives up (see
- * pn_set_wait_timeout_ns) leaves NaN in the weights of the tokens concerned.
+ * pn_set_wait_timeout_ns) leaves NaN in the weights of the tokens concerned, which
+ * pn_kv_evict drops first.  pn_kv_weigh_ex also records it, as PN_ETIMEOUT, in the
+ * status word of a workspace (any of this library's, zeroed by pn_workspace_init, 256-byte
+ * aligned; NULL: as pn_kv_weigh), which pn_workspace_status reads; it uses nothing else of it.
  * q and cache 16-byte aligned, q_stride a multiple of 8, at most 2^29.
  */
 pn_status pn_kv_weigh(const uint16_t* q, int64_t q_stride, int64_t tokens, int heads, const void* cache,
@@ -584,6 +587,11 @@ pn_status pn_kv_weigh(const uint16_t* q, int64_t q_stride, int64_t tokens, int h
                       int64_t table_stride, int max_pages, const int32_t* lens, const int32_t* starts, int batch,
                       int max_queries, const float* lse, float scale, int window, int sinks, const float* weights,
                       float decay, float* out, pn_stream stream);
+pn_status pn_kv_weigh_ex(const uint16_t* q, int64_t q_stride, int64_t tokens, int heads, const void* cache,
+                         int64_t pages, int page_size, int kv_heads, int head_dim, const int32_t* table,
+                         int64_t table_stride, int max_pages, const int32_t* lens, const int32_t* starts, int batch,
+                         int max_queries, const float* lse, float scale, int window, int sinks, const float* weights,
+                         float decay, float* out, void* workspace, size_t workspace_bytes, pn_stream stream);
 
 /*
  * pn_kv_evict: request b < batch (at most 16384) with lens[b] > limit keeps `budget`
@@ -634,7 +642,7 @@ pn_status pn_read_ranges(const void* const* ptrs, const size_t* bytes, int count
  * the tensor-core GEMV kernels, the prefill GEMM, pn_attention and pn_kv_weigh
  * (default 1e9).  A wait that runs out stops its thread block, which records
  * PN_ETIMEOUT in the workspace status word (pn_kv_weigh, which has none: NaN in its
- * weights) and returns after its outstanding copies land.  Process-wide; not for
+ * weights alone) and returns after its outstanding copies land.  Process-wide; not for
  * concurrent use.
  */
 void pn_set_wait_timeout_ns(uint64_t ns);
