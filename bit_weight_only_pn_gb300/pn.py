@@ -642,7 +642,9 @@ def kv_evict(cache: torch.Tensor, weights: torch.Tensor, table: torch.Tensor, le
     its first `sinks`, its last `recent` and those of the largest weight between, in
     pages from the free ring; their old pages are given back (see pn_kv_evict).  The
     positions of later tokens go on from the old length: add lens - result.lens to
-    those that kv_plan gives from then on.  `out` is an earlier result to write into."""
+    those that kv_plan gives from then on.  Layers that share table and ring have a
+    call each, all on the state before the first.  `out` is an earlier result to write
+    into."""
     return KvEviction(*_call(stream, _step().kv_evict, "pn_kv_evict", cache, weights, table, lens, held, free, ring, limit, budget, sinks, recent,
                              out)[1:])
 

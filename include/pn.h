@@ -603,16 +603,19 @@ pn_status pn_kv_weigh_ex(const uint16_t* q, int64_t q_stride, int64_t tokens, in
  * 1 of pages n = ceil(budget / page_size) of which are taken from the free ring's
  * head (ring and free_pages as in pn_kv_plan), with codes, scales and weights as they
  * are; keys stay rotated by their first positions, so positions of tokens to come go
- * on from the old length (a window of pn_attention or pn_kv_weigh counts cached tokens).  The held[b] old pages go behind the ring's tail, in
- * request order.  Requests take pages in their order as long as there are n; the
- * others are refused and stay as they are.
+ * on from the old length (a window of pn_attention or pn_kv_weigh counts cached tokens).
+ * The held[b] old pages go behind the ring's tail, in request order.  Requests take pages
+ * in their order as long as there are n in the ring as it is before the call (pages given
+ * back serve the next one); the others are refused and stay as they are.
  *   table_out [batch][out_stride], max_pages entries each: the table after the call
  *   (of a request cut back: its n pages, then -1); lens_out, held_out, ring_out
  *   {head, tail}: the state after it; refused[1]: how many did not fit;
  *   kept [batch][kv_heads][budget]: the positions that a head kept, -1 throughout
  *   for a request that was left alone.
  * Inputs stay as they are but for free_pages' entries behind the tail and the cache
- * and the weights of the pages taken, so a call repeated on them gives the same.
+ * and the weights of the pages taken, so a call repeated on them gives the same.  Layers
+ * that share tables and ring have a call each, with their own cache, weights and kept, all
+ * on the state before the first of them and in one order; every call gives the same state.
  * Weights have to stay as they are until the call has ended.
  * Pages that several requests share may be read, but are given back by each that
  * holds them: take them out of held first.  A kept token on a page outside the

@@ -30,7 +30,7 @@ def pn():
 class Case:
     """Requests whose tokens lie on pages of their own in any order; some pages of the cache hold nothing."""
 
-    def __init__(self, pn, lens, counts, heads, kv, D, page, window=0, sinks=0, seed=0):
+    def __init__(self, pn, lens, counts, heads, kv, D, page, window=0, sinks=0, seed=0, cancel=False):
         g = torch.Generator(device="cuda").manual_seed(seed + D + sum(lens))
         self.lens, self.counts, self.group, self.kv, self.page, self.window, self.sinks = lens, counts, heads // kv, kv, page, window, sinks
         held = [-(-n // page) for n in lens]
@@ -50,12 +50,16 @@ class Case:
         for s in slots:                                      # every group holds -8, its largest: its scale is 2^-10
             n = torch.randint(-8, 8, (len(s), kv, D), generator=g, device="cuda").float()
             n[:, :, ::64] = -8
+            if cancel:
+                n[:, :, 40::64] = n[:, :, 1::64]
             pn.kv_append(None, n * 2.0 ** -10, n * 2.0 ** -10, self.cache, s)
             self.keys.append(n.double() * 2.0 ** -10)
         if len(slots[0]):
             assert torch.equal(pn.kv_read(self.cache, slots[0])[0].double(), self.keys[0])
         self.scale = 0.5 if D <= 128 else 0.25                # scores of some units
         self.q = torch.randint(-255, 256, (sum(counts), heads, D), generator=g, device="cuda").half()
+        if cancel:
+            self.q[:, :, 1::64], self.q[:, :, 40::64] = 2.0 ** 15, -2.0 ** 15
         self.starts = torch.tensor([0, *counts], device="cuda").cumsum(0).int()
         self.device_lens = torch.tensor(lens, dtype=torch.int32, device="cuda")
         self.weights = torch.rand(pages, kv, page, generator=g, device="cuda")
@@ -182,3 +186,14 @@ def test_waits_that_give_up(pn, name):
     finally:
         pn.set_wait_timeout_ns(1_000_000_000)
     assert torch.equal(case.call(pn), right)
+
+
+@pytest.mark.parametrize("heads,kv,D,counts", [(8, 2, 64, [1, 2]), (8, 2, 64, [5, 3]), (8, 2, 128, [1, 2]), (8, 2, 128, [3, 9]), (8, 2, 256, [2, 1]),
+                                               (8, 2, 256, [6, 4]), (4, 2, 64, [90, 60]), (4, 2, 128, [70, 3]), (4, 2, 256, [60, 33]), (8, 2, 64, [300, 9]),
+                                               (8, 2, 128, [290, 5]), (8, 2, 256, [140, 130]), (130, 1, 64, [2, 1]), (132, 1, 128, [1, 2]), (70, 1, 256, [2, 1])])
+def test_no_bit_of_a_score_is_lost(pn, heads, kv, D, counts):
+    """Two of each group's products are 2^15 times a code and cancel; what is left of the score are the others, which 20 bits
+    beside them hold: products of whole numbers, as sums of 24 bits, keep them (of subnormals, which lie some 11 bits
+    below their exponent, they would not)."""
+    case = Case(pn, [500, 333], counts, heads, kv, D, 32, cancel=True)
+    case.check(case.call(pn))
