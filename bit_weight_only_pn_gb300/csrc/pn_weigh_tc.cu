@@ -342,10 +342,6 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
     if (P.split > 1) cluster_sync();           // both blocks' barriers are there
     tc_fence_after_sync();
     const uint32_t tmem = misc[0];
-    auto give_up = [&]() {
-        *abort = 1u;
-        if (P.w.status) atomicCAS(P.w.status, 0u, static_cast<uint32_t>(PN_ETIMEOUT));
-    };
     // nap: of the warps that work ahead, whose polling would take the others' issue slots
     auto wait = [&](uint32_t b, uint32_t parity, uint32_t nap = 0) { return mbar_try_wait(b, parity) || wait_phase(b, parity, limit, abort, nap); };
     const int split = P.split, rank = static_cast<int>(blockIdx.x) % split;    // the block's chunks: rank, rank + split, ...
@@ -414,7 +410,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
                 if (!ok) break;
                 done_with(turn);
             }
-            if (!ok && !stalled) give_up();
+            if (!ok && !stalled) *abort = 1u;
             // the last copies into the stages land before the block ends, also after an abort
             for (uint32_t s = 0; s < kQStages && s < issued; ++s) wait_phase(q_full + 8 * s, ((issued - 1 - s) / kQStages) & 1u, kAttnDrainNs, nullptr);
         }
@@ -477,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
             __syncwarp();
             if (lane == 0) done_with(turn);
         }
-        if (!ok) give_up();
+        if (!ok) *abort = 1u;
     } else if (warp == kSumWarps + 6) {
         // ------------------------------------------------------ MMA issue --
         if (elect_one()) {
@@ -511,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
                 k.step();
                 done_with(turn);
             }
-            if (!ok) give_up();
+            if (!ok) *abort = 1u;
             mma_commit(drain);                 // every product of this block finished (also after an abort)
             wait_phase(drain, 0u, kAttnDrainNs, nullptr);
         }
@@ -597,7 +593,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
             if (lane == 0) mbar_arrive(a_full + 8 * k.at);
             k.step();
         }
-        if (!ok) give_up();
+        if (!ok) *abort = 1u;
     } else if (warp < kSumWarps) {
         // ----------------------------------------------- scores and sums --
         const int mine = warp >> 2, place = mine & 1, token = threadIdx.x & (kUnit - 1);
@@ -665,7 +661,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
                 t.step();
                 rows.step();
             }
-            if (!ok) give_up();
+            if (!ok) *abort = 1u;
             const float2 both = apart(sum);
             // a token's four sums: two places in turn, so that one barrier a unit is enough; the
             // order does not depend on which place of S the unit's first chunk had
@@ -689,11 +685,11 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
                     __syncwarp();
                     if (lane == 0) arrive_at_block(x_empty + 8 * at, 1);
                 }
-                if (!ok) give_up();
+                if (!ok) *abort = 1u;
             }
             if (rank == 0 && to >= 0) a.out[to] = before + all;
         }
-        if (!listed) give_up();
+        if (!listed) *abort = 1u;
         // where the list gave up: NaN for the units behind
         if (!listed && mine == 0 && rank == 0)
             for (; unit_of_turn(n, blockIdx.x / split, gridDim.x / split) < scan[kThreads]; ++n) {
@@ -707,6 +703,7 @@ __global__ void __launch_bounds__(kThreads, 1) weigh_tc_kernel(const __grid_cons
     // ------------------------------------------------------------ teardown --
     tc_fence_before_sync();
     __syncthreads();
+    if (threadIdx.x == 0 && P.w.status && *abort) atomicCAS(P.w.status, 0u, static_cast<uint32_t>(PN_ETIMEOUT));
     if (warp == kThreads / 32 - 1) {
         tc_fence_after_sync();
         tmem_dealloc(tmem, S::kTmemCols);
