@@ -20,9 +20,9 @@
 // reference m, the next ones on their way; only where one of them passes it (a few
 // times in a row) are the sums moved and the new largest value left out of R.
 //
-// 2000 rows of 151936 fp16 logits: 122 us, 5.0 TB/s, with 72% of the issue slots in use and
+// 2000 rows of 151936 fp16 logits: 123 us, 4.9 TB/s, with 74% of the issue slots in use and
 // a last wave of one block to an SM (two blocks to every row: 130 us).  64 rows of fp32:
-// 17.1 us, one wave; about 10 of them read.  One row of 32000: 6.4 us.
+// 17.8 us, one wave; about 10 of them read.  One row of 32000: 7.1 us.
 //
 // Top k (at most 32).  The k-th largest of a block's 256 thread maxima is a lower
 // bound of the k-th largest value of the row, and so is what all p blocks have (k / p)

@@ -184,6 +184,9 @@ __device__ __forceinline__ void products(const Keys<D>& k, const Rows<D>* rows, 
     }
 }
 
+// More query heads to a key/value head than the kernel for many rows has columns for: a
+// block shares its rows among 256 tokens.  64 ragged requests to 16384 tokens, one query each:
+// 132 heads of 128 to one 115 us (128 heads, in that kernel: 62), 264 of 64 to two 169.
 template <int D>
 __global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const __grid_constant__ Params P) {
     constexpr int NT = D == 256 ? 1 : 2;       // row groups at a time, as registers allow
@@ -276,8 +279,9 @@ __global__ void __launch_bounds__(kThreads, 2) weigh_kernel(const __grid_constan
 // of what it has to read and write.  Bound by memory and the instructions for it: with a
 // tile's registers copied, masks worked out for every tile and places in 64 bits
 // throughout, a tile took 600 instructions and the call 101 us.  With 5 queries
-// each (20 rows) it takes 121 us, with 11 (44) 211, where blocks that share rows and wait
-// for each other took 291 and 368: those waited, these are bound by instructions.
+// each (20 rows) it takes 120 us, with 11 (44) 201, where blocks that share rows and wait
+// for each other took 291 and 368: those waited, these are bound by instructions.  Heads of
+// 64: 64 us (the forms for 8 rows spill, 80 bytes), of 256: 148 (84 bytes), with 5 queries 92, 348.
 
 template <int D>
 struct Tile {

@@ -7,7 +7,10 @@
 // in one lane of tensor memory and are summed by one thread: nothing is exchanged
 // between lanes.  S_j = K_j Q_j^T for each group j of 64 values, with K's codes as
 // fp16 whole numbers n - 8 (exact) and the queries as they are; x = sum_j d_j S_j in
-// fp32, so scores are as exact as in the kernels for few rows.  In a block of 25 warps
+// fp32, so scores are as exact as in the kernels for few rows.  A row's log sum is one
+// number here instead of two (less_of), whose rounding is in all of the row's
+// probabilities; with that and thousands of rows to a sum, 2048 queries' weights err by
+// 2.6e-7 of themselves, single queries' in the other kernel by 3e-8.  In a block of 25 warps
 //   warps 16-19 decode the unit's codes into [token][64 values] tiles with the 128-byte
 //     swizzle, once for all rows, and the scales as fp32;
 //   warp 20 brings the query rows, a chunk at a time, by TMA: a box of 64 values, the
@@ -21,7 +24,7 @@
 // chunks, halves, blocks) are added at the unit's end in one order and written; results
 // depend on neither timing nor what else is in the batch.
 //
-// 2048 queries of a prompt of 8192 tokens, 24 + 4 heads of 256: 250 us, 0.72 PFLOP/s of
+// 2048 queries of a prompt of 8192 tokens, 24 + 4 heads of 256: 253 us, 0.71 PFLOP/s of
 // products.  60 rows of a unit take 1600 cycles: shared memory gives the N = 64 products
 // their operands in 768, takes the next queries in 256 and gives the rows' constants in
 // 256; tensor memory gives 128 KB in 1050.  (Two constants for a row took 119 us instead
@@ -46,7 +49,7 @@ namespace pn {
 namespace {
 
 constexpr int kSumWarps = 16;                  // two places of S, two halves of the columns, four quarters of the tokens
-constexpr int kThreads = (kSumWarps + 9) * 32; // 80 registers each
+constexpr int kThreads = (kSumWarps + 9) * 32; // 72 registers each
 constexpr int kList = 32;                      // units looked up at a time
 constexpr int kUnit = 128;                     // tokens of a unit, MMA M
 constexpr int kPlaces = 2;                     // of S in tensor memory
