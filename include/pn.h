@@ -567,9 +567,10 @@ pn_status pn_norm(const void* y, int64_t y_stride, int y_dtype, const void* resi
  *           exp(scale * q . k_t - lse)
  *   before_t = decay * weights_t, and 0 for the step's own tokens (those of its
  *           queries' positions on) or where weights is NULL
- * (a row whose lse is an infinity gives nothing, whatever its queries are).  Other entries of out, among them those of
- * requests without queries, are not written.  out may be weights; else the
- * two share no memory.  No other output is written, no workspace is needed.  Tokens
+ * (a row whose lse is an infinity gives nothing, whatever its queries are).  Other
+ * entries of out, among them those of requests without queries, are not written.  out
+ * may be weights; else the two share no memory.  No other output is written, no
+ * workspace is needed (pn_kv_weigh_ex may be given one, for its status word).  Tokens
  * on pages outside the cache are passed over.  Requests may share pages as long as
  * nobody reads what they leave there: each writes its own sums.  Each sum is made in
  * fp32 in one order: deterministic.  Which kernel runs goes by head_dim, heads,
